@@ -33,6 +33,10 @@ __all__ = [
     "adam8bit_step",
     "adam8bit_step_multi",
     "MultiTensorArgs",
+    "MultiTensorArgs32",
+    "adam32_step_multi",
+    "GradNorm",
+    "clip_scale",
     "Adam8bit",
     "AdamW8bit",
 ]
@@ -276,4 +280,5 @@ def adam8bit_step_multi(params, grads, m_codes, m_absmax, v_codes, v_absmax, *, 
     )
 
 
+from .adam32 import GradNorm, MultiTensorArgs32, adam32_step_multi, clip_scale  # noqa: E402
 from .optim import Adam8bit, AdamW8bit  # noqa: E402

@@ -22,6 +22,9 @@ BWD_F32 = 0
 BWD_BF16 = 1
 BWD_F16 = 2
 BLOCK = 2048
+FP8_ROWS = 1
+FP8_COLS = 2
+FP8_TILES = 4
 
 
 class AdamHParams(ctypes.Structure):
@@ -72,6 +75,17 @@ _SIGNATURES = {
         _int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "bwd_embedding_backward": (
         _int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "bwd_adam32_step_multi": (
+        _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamHParams), _vp]),
+    "bwd_grad_norm_work_bytes": (_i64, [_i32]),
+    "bwd_grad_norm": (
+        _int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]),
+    "bwd_fp8_pitch": (_i64, [_i64]),
+    "bwd_fp8_scale_bytes": (_i64, [_i64, _i64]),
+    "bwd_fp8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "bwd_fp8_dequantize": (_int, [_vp, _vp, _i32, _i64, _i64, _vp, _int, _vp]),
+    "bwd_fp8_matmul": (
+        _int, [_i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _int, _vp]),
     "bwd_check_device": (_int, [_vp]),
     "bwd_selftest_bounded_wait": (_int, [_vp]),
     "bwd_status_string": (ctypes.c_char_p, [_int]),

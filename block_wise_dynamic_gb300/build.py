@@ -1,7 +1,8 @@
 """Builds the C-ABI shared library ``libbwd.so`` in-tree for sm_103a.
 
-Four translation units (the host codebook builder, the host shard planner,
-the optimizer kernels and the stable-embedding kernels) are compiled in parallel and linked with the
+Six translation units (the host codebook builder, the host shard planner,
+the 8-bit optimizer kernels, the stable-embedding kernels, the 8-bit floating
+point products and the 32-bit-state optimizer kernels) are compiled in parallel and linked with the
 static CUDA runtime, so the library depends only on the driver.  No
 fast-math: every code decision must be IEEE.
 """
@@ -29,6 +30,8 @@ SOURCES = {
     "shard.o": os.path.join(CSRC, "shard.cpp"),
     "kernels.o": os.path.join(CSRC, "kernels.cu"),
     "embedding.o": os.path.join(CSRC, "embedding.cu"),
+    "fp8.o": os.path.join(CSRC, "fp8.cu"),
+    "adam32.o": os.path.join(CSRC, "adam32.cu"),
 }
 HEADERS = [os.path.join(CSRC, h) for h in ("tables.h", "exact_div.cuh", "host_util.h")] + [os.path.join(INCLUDE, "bwd.h")]
 

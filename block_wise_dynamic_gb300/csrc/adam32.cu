@@ -1,0 +1,397 @@
+// AdamW over a list of tensors with both moments in fp32, and the 2-norm of a
+// list of gradients with the factor that clips it (sm_103a).
+//
+// The 8-bit optimizer keeps some tensors' moments in 32 bits: the embedding
+// (its gradients are uneven across rows) and vectors too small to gain from
+// 8 bits.  This step is theirs, with the same scalars as the 8-bit one:
+//   g' = s g;  m = b1 m + (1-b1) g';  v = b2 v + ((1-b2) g') g';
+//   p = p d - step m / (sqrt(v) / c + eps).
+// s is read from device memory, so a clipping factor computed on the device
+// needs no round trip through the host; where s is not finite nothing is
+// written (an overflowed gradient leaves the state as it was).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "bwd.h"
+#include "host_util.h"
+
+namespace {
+
+using bwd::host::aligned16;
+using bwd::host::aligned_to;
+using bwd::host::check_launch;
+using bwd::host::cuda_fail;
+using bwd::host::fail;
+
+constexpr int kF32 = BWD_F32, kBF16 = BWD_BF16, kF16 = BWD_F16;
+constexpr int kThreads = 256;
+constexpr int kQuads = 2;                           // quads of 4 elements per thread
+constexpr int kChunk = kThreads * kQuads * 4;       // elements a CTA works on at a time
+constexpr int kMaxTensors = 480;                    // per launch, bounded by kernel parameter space
+
+struct Tensor32 {
+  void* p;
+  const void* g;
+  float* m;
+  float* v;
+  int64_t n;
+  int64_t vec;  // every pointer aligned to four of its elements
+};
+
+struct Adam32Args {
+  int64_t chunk_start[kMaxTensors + 1];  // prefix sums of per-tensor chunk counts
+  Tensor32 t[kMaxTensors];
+  const float* grad_scale;  // or null: 1
+  int32_t num_tensors;
+  float b1, omb1, b2, omb2, eps, step_size, inv_bc2s, decay;
+};
+
+static_assert(sizeof(Adam32Args) <= 32764, "kernel parameter space");
+
+template <int kT>
+__device__ __forceinline__ float widen(unsigned short h) {
+  if (kT == kBF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
+  return __half2float(__ushort_as_half(h));
+}
+
+template <int kT>
+__device__ __forceinline__ float load1(const void* x, int64_t i) {
+  if (kT == kF32) return static_cast<const float*>(x)[i];
+  return widen<kT>(static_cast<const unsigned short*>(x)[i]);
+}
+
+template <int kT>
+__device__ __forceinline__ void store1(void* x, int64_t i, float v) {
+  if (kT == kF32) static_cast<float*>(x)[i] = v;
+  else if (kT == kBF16) static_cast<__nv_bfloat16*>(x)[i] = __float2bfloat16_rn(v);
+  else static_cast<__half*>(x)[i] = __float2half_rn(v);
+}
+
+// Four consecutive elements; each byte is read and written once.
+template <int kT>
+__device__ __forceinline__ void load4(const void* x, int64_t i, float (&o)[4]) {
+  if (kT == kF32) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(x) + i));
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+  } else {
+    const ushort4 a = __ldcs(reinterpret_cast<const ushort4*>(static_cast<const unsigned short*>(x) + i));
+    o[0] = widen<kT>(a.x); o[1] = widen<kT>(a.y); o[2] = widen<kT>(a.z); o[3] = widen<kT>(a.w);
+  }
+}
+
+template <int kT>
+__device__ __forceinline__ void store4(void* x, int64_t i, const float (&v)[4]) {
+  if (kT == kF32) {
+    __stcs(reinterpret_cast<float4*>(static_cast<float*>(x) + i), make_float4(v[0], v[1], v[2], v[3]));
+  } else {
+    ushort4 h;
+    if (kT == kBF16) {
+      h.x = __bfloat16_as_ushort(__float2bfloat16_rn(v[0])); h.y = __bfloat16_as_ushort(__float2bfloat16_rn(v[1]));
+      h.z = __bfloat16_as_ushort(__float2bfloat16_rn(v[2])); h.w = __bfloat16_as_ushort(__float2bfloat16_rn(v[3]));
+    } else {
+      h.x = __half_as_ushort(__float2half_rn(v[0])); h.y = __half_as_ushort(__float2half_rn(v[1]));
+      h.z = __half_as_ushort(__float2half_rn(v[2])); h.w = __half_as_ushort(__float2half_rn(v[3]));
+    }
+    __stcs(reinterpret_cast<ushort4*>(static_cast<unsigned short*>(x) + i), h);
+  }
+}
+
+// The last t with start[t] <= c.
+__device__ __forceinline__ int find_tensor(const int64_t* start, int num, int64_t c) {
+  int lo = 0, hi = num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+template <int kG, int kP>
+__global__ void __launch_bounds__(kThreads)
+adam32_kernel(const __grid_constant__ Adam32Args a) {
+  const float s = a.grad_scale ? *a.grad_scale : 1.0f;
+  if (!(fabsf(s) <= 3.402823466e38f)) return;
+  const int64_t total = a.chunk_start[a.num_tensors];
+  int64_t c = blockIdx.x;
+  int ti = find_tensor(a.chunk_start, a.num_tensors, c);
+  for (; c < total; c += gridDim.x) {
+    while (a.chunk_start[ti + 1] <= c) ++ti;
+    const Tensor32& T = a.t[ti];
+    const int64_t base = (c - a.chunk_start[ti]) * kChunk + 4 * threadIdx.x;
+    float p[kQuads][4], g[kQuads][4], m[kQuads][4], v[kQuads][4];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int64_t i = base + q * 4 * kThreads;
+      if (T.vec && i + 4 <= T.n) {
+        load4<kP>(T.p, i, p[q]); load4<kG>(T.g, i, g[q]);
+        load4<kF32>(T.m, i, m[q]); load4<kF32>(T.v, i, v[q]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = i + j < T.n;
+          p[q][j] = in ? load1<kP>(T.p, i + j) : 0.0f; g[q][j] = in ? load1<kG>(T.g, i + j) : 0.0f;
+          m[q][j] = in ? T.m[i + j] : 0.0f; v[q][j] = in ? T.v[i + j] : 0.0f;
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float gs = __fmul_rn(s, g[q][j]);
+        m[q][j] = __fadd_rn(__fmul_rn(a.b1, m[q][j]), __fmul_rn(a.omb1, gs));
+        v[q][j] = __fadd_rn(__fmul_rn(a.b2, v[q][j]), __fmul_rn(__fmul_rn(a.omb2, gs), gs));
+        const float den = __fmaf_rn(__fsqrt_rn(v[q][j]), a.inv_bc2s, a.eps);
+        p[q][j] = __fmaf_rn(-a.step_size, __fdiv_rn(m[q][j], den), __fmul_rn(p[q][j], a.decay));
+      }
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int64_t i = base + q * 4 * kThreads;
+      if (T.vec && i + 4 <= T.n) {
+        store4<kP>(T.p, i, p[q]); store4<kF32>(T.m, i, m[q]); store4<kF32>(T.v, i, v[q]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i + j < T.n) { store1<kP>(T.p, i + j, p[q][j]); T.m[i + j] = m[q][j]; T.v[i + j] = v[q][j]; }
+      }
+    }
+  }
+}
+
+// --------------------------------------------------------------------------
+// Norm.  Each CTA sums squares in fp32 per thread and in binary64 across
+// threads, and writes its sum to its own slot; the CTA that finishes last
+// adds the slots in order, so the result does not depend on the schedule.
+
+constexpr int kNormTensors = 1024;
+constexpr int kNormCtas = 4;  // per SM
+
+struct NormArgs {
+  int64_t chunk_start[kNormTensors + 1];
+  const void* g[kNormTensors];
+  int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where vector loads are not possible
+  double* slots;                 // one per CTA of all launches of the call
+  unsigned int* ticket;          // 0 before the call and after it
+  float* out;                    // factor, norm
+  int32_t num_tensors;
+  int32_t first_slot, total_slots;
+  float max_norm, inv_loss_scale;
+};
+
+static_assert(sizeof(NormArgs) <= 32764, "kernel parameter space");
+
+__device__ __forceinline__ double block_sum(double x, double* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
+  __syncthreads();
+  x = 0.0;
+  for (int w = 0; w < kThreads / 32; ++w) x += red[w];
+  __syncthreads();
+  return x;
+}
+
+template <int kG>
+__global__ void __launch_bounds__(kThreads)
+grad_norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ double s_red[kThreads / 32];
+  __shared__ bool s_last;
+  const int64_t total = a.chunk_start[a.num_tensors];
+  int64_t c = blockIdx.x;
+  int ti = find_tensor(a.chunk_start, a.num_tensors, c);
+  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (; c < total; c += gridDim.x) {
+    while (a.chunk_start[ti + 1] <= c) ++ti;
+    const int64_t lc = c - a.chunk_start[ti], base = lc * kChunk;
+    const bool last = c + 1 == a.chunk_start[ti + 1], vec = a.n_tail[ti] > 0;
+    const int len = last ? abs(a.n_tail[ti]) : kChunk;
+    float g[kQuads][4];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int i = 4 * threadIdx.x + q * 4 * kThreads;
+      if (vec && i + 4 <= len) {
+        load4<kG>(a.g[ti], base + i, g[q]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[q][j] = i + j < len ? load1<kG>(a.g[ti], base + i + j) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum[j] = __fmaf_rn(g[q][j], g[q][j], sum[j]);
+  }
+  const double mine = block_sum(static_cast<double>(sum[0]) + sum[1] + sum[2] + sum[3], s_red);
+  if (threadIdx.x == 0) {
+    a.slots[a.first_slot + blockIdx.x] = mine;
+    __threadfence();
+    s_last = atomicAdd(a.ticket, 1u) + 1u == static_cast<unsigned int>(a.total_slots);
+  }
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  double all = 0.0;
+  for (int i = threadIdx.x; i < a.total_slots; i += kThreads) all += __ldcg(a.slots + i);
+  all = block_sum(all, s_red);
+  if (threadIdx.x == 0) {
+    const float norm = static_cast<float>(sqrt(all) * static_cast<double>(a.inv_loss_scale));
+    const float clip = fminf(1.0f, __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f)));
+    const bool finite = norm <= 3.402823466e38f;  // false for NaN too
+    a.out[0] = finite ? __fmul_rn(clip, a.inv_loss_scale) : __uint_as_float(0x7fffffffu);
+    a.out[1] = norm;
+    *a.ticket = 0;
+  }
+}
+
+// --------------------------------------------------------------------------
+// host side
+
+bwd_status sm_count(int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev);
+  return e == cudaSuccess ? BWD_OK : cuda_fail(e, "cudaDeviceGetAttribute");
+}
+
+int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
+uintptr_t bytes_of(int t) { return t == BWD_F32 ? 4 : 2; }
+
+bwd_status launch_adam32(const Adam32Args& a, int g_type, int p_type, int sms, cudaStream_t st) {
+  const int64_t total = a.chunk_start[a.num_tensors], cap = static_cast<int64_t>(sms) * 4;
+  const int grid = static_cast<int>(total < cap ? total : cap);
+  switch (3 * p_type + g_type) {
+    case 0: adam32_kernel<kF32, kF32><<<grid, kThreads, 0, st>>>(a); break;
+    case 1: adam32_kernel<kBF16, kF32><<<grid, kThreads, 0, st>>>(a); break;
+    case 2: adam32_kernel<kF16, kF32><<<grid, kThreads, 0, st>>>(a); break;
+    case 3: adam32_kernel<kF32, kBF16><<<grid, kThreads, 0, st>>>(a); break;
+    case 4: adam32_kernel<kBF16, kBF16><<<grid, kThreads, 0, st>>>(a); break;
+    case 5: adam32_kernel<kF16, kBF16><<<grid, kThreads, 0, st>>>(a); break;
+    case 6: adam32_kernel<kF32, kF16><<<grid, kThreads, 0, st>>>(a); break;
+    case 7: adam32_kernel<kBF16, kF16><<<grid, kThreads, 0, st>>>(a); break;
+    default: adam32_kernel<kF16, kF16><<<grid, kThreads, 0, st>>>(a); break;
+  }
+  return check_launch("adam32_kernel launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g,
+                                 bwd_dtype g_dtype, float* const* m, float* const* v, const int64_t* n,
+                                 const float* grad_scale, const bwd_adam_hparams* hp, void* stream) {
+  if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
+  if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
+  if (!valid_type(p_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "parameter dtype %d", (int)p_dtype);
+  bwd_status s = bwd::host::check_hparams(hp);
+  if (s != BWD_OK) return s;
+  if (num_tensors == 0) return BWD_OK;
+  if (!p || !g || !m || !v || !n) return fail(BWD_ERR_INVALID_ARG, "NULL array");
+  if (!aligned_to(grad_scale, 4)) return fail(BWD_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
+    if (n[i] > 0 && (!p[i] || !g[i] || !m[i] || !v[i])) return fail(BWD_ERR_INVALID_ARG, "tensor %d: NULL pointer", i);
+    if (n[i] > 0 && (!aligned_to(p[i], bytes_of(p_dtype)) || !aligned_to(g[i], bytes_of(g_dtype)) ||
+                     !aligned_to(m[i], 4) || !aligned_to(v[i], 4)))
+      return fail(BWD_ERR_INVALID_ARG, "tensor %d: pointer not aligned to its element size", i);
+  }
+  int sms = 0;
+  if ((s = sm_count(&sms)) != BWD_OK) return s;
+  static thread_local Adam32Args a;  // ~27 KB: kept off the stack
+  const bwd::host::AdamScalars k = bwd::host::adam_scalars(hp);
+  a.b1 = k.b1; a.omb1 = k.omb1; a.b2 = k.b2; a.omb2 = k.omb2;
+  a.eps = k.eps; a.step_size = k.step_size; a.inv_bc2s = k.inv_bc2s; a.decay = k.decay;
+  a.grad_scale = grad_scale;
+  a.chunk_start[0] = 0;
+  int t = 0;
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    if (n[i] > 0) {
+      a.t[t] = Tensor32{p[i], g[i], m[i], v[i], n[i],
+                        aligned_to(p[i], 4 * bytes_of(p_dtype)) && aligned_to(g[i], 4 * bytes_of(g_dtype)) &&
+                            aligned16(m[i]) && aligned16(v[i])};
+      a.chunk_start[t + 1] = a.chunk_start[t] + chunks_of(n[i]);
+      ++t;
+    }
+    if (t == kMaxTensors || (t > 0 && i + 1 == num_tensors)) {
+      a.num_tensors = t;
+      if ((s = launch_adam32(a, g_dtype, p_dtype, sms, static_cast<cudaStream_t>(stream))) != BWD_OK) return s;
+      t = 0;
+    }
+  }
+  return BWD_OK;
+}
+
+int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {
+  if (num_tensors < 0) return -1;
+  // a ticket, and a slot for each CTA of each launch; 256 SMs are more than the device has
+  const int64_t launches = (num_tensors + kNormTensors - 1) / kNormTensors;
+  return 16 + 8 * launches * 256 * kNormCtas;
+}
+
+bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_dtype, const int64_t* n, float max_norm,
+                         float loss_scale, float* out, void* work, void* stream) {
+  if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
+  if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
+  if (!(max_norm > 0.0f)) return fail(BWD_ERR_INVALID_ARG, "max_norm must be > 0");
+  if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale) || !std::isfinite(1.0f / loss_scale))
+    return fail(BWD_ERR_INVALID_ARG, "loss_scale and its reciprocal must be finite and > 0");
+  if (!out || !work || (num_tensors > 0 && (!g || !n))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(out, 4) || !aligned16(work)) return fail(BWD_ERR_INVALID_ARG, "out must be 4-byte and work 16-byte aligned");
+  for (int32_t i = 0; i < num_tensors; ++i) {
+    if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
+    if (n[i] > 0 && (!g[i] || !aligned_to(g[i], bytes_of(g_dtype))))
+      return fail(BWD_ERR_INVALID_ARG, "tensor %d: NULL or unaligned pointer", i);
+  }
+  int sms = 0;
+  bwd_status s = sm_count(&sms);
+  if (s != BWD_OK) return s;
+  static thread_local NormArgs a;  // ~20 KB: kept off the stack
+  a.ticket = static_cast<unsigned int*>(work);
+  a.slots = reinterpret_cast<double*>(static_cast<char*>(work) + 16);
+  a.out = out;
+  a.max_norm = max_norm;
+  a.inv_loss_scale = 1.0f / loss_scale;
+  const int64_t cap = static_cast<int64_t>(sms < 256 ? sms : 256) * kNormCtas;
+  // two passes: how many CTAs all launches have together, then the launches
+  int64_t slots = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t first = 0;
+    int t = 0;
+    a.chunk_start[0] = 0;
+    for (int32_t i = 0; i <= num_tensors; ++i) {
+      if (i < num_tensors && n[i] > 0) {
+        a.g[t] = g[i];
+        const int32_t tail = static_cast<int32_t>(n[i] - (chunks_of(n[i]) - 1) * kChunk);
+        a.n_tail[t] = aligned_to(g[i], 4 * bytes_of(g_dtype)) ? tail : -tail;
+        a.chunk_start[t + 1] = a.chunk_start[t] + chunks_of(n[i]);
+        ++t;
+      }
+      // the last launch may have no tensors: it still forms the result
+      if (t == kNormTensors || (i == num_tensors && (t > 0 || first == 0))) {
+        const int64_t chunks = a.chunk_start[t], ctas = chunks < 1 ? 1 : chunks < cap ? chunks : cap;
+        if (pass == 1) {
+          a.num_tensors = t;
+          a.first_slot = static_cast<int32_t>(first);
+          a.total_slots = static_cast<int32_t>(slots);
+          cudaStream_t st = static_cast<cudaStream_t>(stream);
+          const int grid = static_cast<int>(ctas);
+          if (g_dtype == BWD_F32) grad_norm_kernel<kF32><<<grid, kThreads, 0, st>>>(a);
+          else if (g_dtype == BWD_BF16) grad_norm_kernel<kBF16><<<grid, kThreads, 0, st>>>(a);
+          else grad_norm_kernel<kF16><<<grid, kThreads, 0, st>>>(a);
+          if ((s = check_launch("grad_norm_kernel launch")) != BWD_OK) return s;
+        }
+        first += ctas;
+        t = 0;
+      }
+    }
+    slots = first;
+  }
+  return BWD_OK;
+}
+
+}  // extern "C"

@@ -814,9 +814,12 @@ bwd_status bwd_check_device(void* stream) {
   unsigned int fault = 0;
   if ((e = cudaMemcpyFromSymbol(&fault, g_embed_fault, sizeof fault)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyFromSymbol(fault word)");
-  if (fault == 0) return BWD_OK;
+  unsigned int fp8_fault = 0;
+  const bwd_status s = bwd::host::take_fp8_fault(&fp8_fault);
+  if (s != BWD_OK) return s;
+  if (fault == 0 && fp8_fault == 0) return BWD_OK;
   const unsigned int zero = 0;
-  if ((e = cudaMemcpyToSymbol(g_embed_fault, &zero, sizeof zero)) != cudaSuccess)
+  if (fault != 0 && (e = cudaMemcpyToSymbol(g_embed_fault, &zero, sizeof zero)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyToSymbol(fault word)");
   return fail(BWD_ERR_CUDA, "a bounded wait for a bulk copy in a library kernel gave up; the outputs of the "
                             "kernels since the last check are unspecified");

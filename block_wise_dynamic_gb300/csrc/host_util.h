@@ -23,6 +23,19 @@ bwd_status check_launch(const char* what);
 // This thread's last error message ("" if none).
 const char* last_error();
 
+// Host scalars of an Adam update: bias corrections in binary64, rounded once.
+struct AdamScalars {
+  float b1, omb1, b2, omb2, eps, step_size, inv_bc2s;
+  float decay;  // 1 - lr * weight_decay (decoupled weight decay), 1 for Adam
+};
+AdamScalars adam_scalars(const bwd_adam_hparams* hp);
+
+// BWD_OK, or BWD_ERR_INVALID_ARG where a hyper-parameter is outside its range.
+bwd_status check_hparams(const bwd_adam_hparams* hp);
+
+// Reads and clears the 8-bit products' fault word (see bwd_check_device).
+bwd_status take_fp8_fault(unsigned int* fault);
+
 // Unique id of the current CUDA context (the driver's cuCtxGetId, unique for
 // the life of the process).  Per-device state cached by the library (the
 // uploaded code tables, kernel attributes) belongs to one context: after a

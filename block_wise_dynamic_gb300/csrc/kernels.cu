@@ -917,6 +917,34 @@ bwd_status check_launch(const char* what) {
 
 const char* last_error() { return t_last_error.c_str(); }
 
+bwd_status check_hparams(const bwd_adam_hparams* hp) {
+  if (!hp) return fail(BWD_ERR_INVALID_ARG, "hparams is NULL");
+  if (hp->step < 1) return fail(BWD_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)hp->step);
+  if (!std::isfinite(hp->lr) || !std::isfinite(hp->eps) || hp->eps < 0.0f)
+    return fail(BWD_ERR_INVALID_ARG, "lr and eps must be finite, eps >= 0");
+  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+    return fail(BWD_ERR_INVALID_ARG, "betas must lie in [0, 1)");
+  if (!std::isfinite(hp->weight_decay) || hp->weight_decay < 0.0f)
+    return fail(BWD_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
+  return BWD_OK;
+}
+
+AdamScalars adam_scalars(const bwd_adam_hparams* hp) {
+  const double b1 = hp->beta1, b2 = hp->beta2, t = static_cast<double>(hp->step);
+  const double bc1 = 1.0 - std::pow(b1, t);
+  const double bc2 = 1.0 - std::pow(b2, t);
+  AdamScalars k;
+  k.b1 = hp->beta1;
+  k.b2 = hp->beta2;
+  k.omb1 = static_cast<float>(1.0 - b1);
+  k.omb2 = static_cast<float>(1.0 - b2);
+  k.eps = hp->eps;
+  k.step_size = static_cast<float>(static_cast<double>(hp->lr) / bc1);
+  k.inv_bc2s = static_cast<float>(1.0 / std::sqrt(bc2));
+  k.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * static_cast<double>(hp->weight_decay));
+  return k;
+}
+
 namespace {
 using CtxGetIdFn = int (*)(void* ctx, unsigned long long* id);  // CUresult cuCtxGetId(CUcontext, ...)
 std::once_flag g_ctx_fn_once;
@@ -949,6 +977,7 @@ namespace {
 
 using bwd::host::aligned16;
 using bwd::host::aligned_to;
+using bwd::host::check_hparams;
 using bwd::host::check_launch;
 using bwd::host::cuda_fail;
 using bwd::host::fail;
@@ -1040,31 +1069,16 @@ int grid_for(int64_t blocks, int per_cta, const DeviceState& d, int occ) {
 
 bool valid_kind(bwd_map_kind k) { return k == BWD_MAP_SIGNED || k == BWD_MAP_UNSIGNED; }
 
-bwd_status check_hparams(const bwd_adam_hparams* hp) {
-  if (!hp) return fail(BWD_ERR_INVALID_ARG, "hparams is NULL");
-  if (hp->step < 1) return fail(BWD_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)hp->step);
-  if (!std::isfinite(hp->lr) || !std::isfinite(hp->eps) || hp->eps < 0.0f)
-    return fail(BWD_ERR_INVALID_ARG, "lr and eps must be finite, eps >= 0");
-  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
-    return fail(BWD_ERR_INVALID_ARG, "betas must lie in [0, 1)");
-  if (!std::isfinite(hp->weight_decay) || hp->weight_decay < 0.0f)
-    return fail(BWD_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
-  return BWD_OK;
-}
-
-// Host scalars of the update: bias corrections in binary64, rounded once.
 void fill_scalars(const bwd_adam_hparams* hp, AdamArgs* a) {
-  const double b1 = hp->beta1, b2 = hp->beta2, t = static_cast<double>(hp->step);
-  const double bc1 = 1.0 - std::pow(b1, t);
-  const double bc2 = 1.0 - std::pow(b2, t);
-  a->b1 = hp->beta1;
-  a->b2 = hp->beta2;
-  a->omb1 = static_cast<float>(1.0 - b1);
-  a->omb2 = static_cast<float>(1.0 - b2);
-  a->eps = hp->eps;
-  a->step_size = static_cast<float>(static_cast<double>(hp->lr) / bc1);
-  a->inv_bc2s = static_cast<float>(1.0 / std::sqrt(bc2));
-  a->decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * static_cast<double>(hp->weight_decay));
+  const bwd::host::AdamScalars k = bwd::host::adam_scalars(hp);
+  a->b1 = k.b1;
+  a->b2 = k.b2;
+  a->omb1 = k.omb1;
+  a->omb2 = k.omb2;
+  a->eps = k.eps;
+  a->step_size = k.step_size;
+  a->inv_bc2s = k.inv_bc2s;
+  a->decay = k.decay;
 }
 
 template <int kG, int kP>

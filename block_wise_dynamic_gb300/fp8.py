@@ -1,0 +1,238 @@
+"""Linear layers on 8-bit floating point operands with a power-of-two scale
+for each block of 128 (e4m3 codes, sm_103a).
+
+A block's scale is 2^e with the smallest e >= -127 for which no magnitude in
+it exceeds 448 * 2^e; codes are rounded to nearest, ties to even.  Each of a
+layer's three products sums over blocks of its own operands:
+
+  y  = Q(x) Q(w)^T + bias   x in blocks of 1 x 128, w of 128 x 128
+  dx = Q(dy) Q(w)           dy in blocks of 1 x 128
+  dw = Q(dy)^T Q(x)         dy and x in blocks of 128 x 1
+
+  quantize(x, "rows" | "cols" | "both" | "tiles") -> Fp8Matrix
+  matmul(a, b, trans_a, trans_b, bias)            A B^T of two quantized matrices
+  linear(x, w, bias)                              the product with a weight kept quantized
+  forward(x, w, bias) -> (y, xq);  backward(dy, xq, w) -> (dx, dw, dbias)
+  Fp8Linear                                       torch.nn.Module with autograd through them
+
+Each function checks and marshals CUDA tensors and calls ``bwd_fp8_*`` of
+``include/bwd.h``; quantization and products run in the library's kernels.
+"""
+
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _abi
+from . import _GDT, _lib, _need, _stream_handle
+
+__all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
+
+_BLOCKS = {"rows": _abi.FP8_ROWS, "cols": _abi.FP8_COLS, "both": _abi.FP8_ROWS | _abi.FP8_COLS, "tiles": _abi.FP8_TILES}
+
+
+class Fp8Matrix:
+    """A rows x cols matrix in e4m3 codes.  ``row_codes`` / ``row_scales`` are
+    quantized in blocks along the rows, ``col_codes`` / ``col_scales`` along
+    the columns (None where ``blocks`` has no such form); with "tiles" both
+    are the same codes."""
+
+    __slots__ = ("shape", "blocks", "dtype", "row_codes", "row_scales", "col_codes", "col_scales")
+
+    def __init__(self, shape, blocks, dtype, row_codes, row_scales, col_codes, col_scales):
+        self.shape, self.blocks, self.dtype = shape, blocks, dtype
+        self.row_codes, self.row_scales = row_codes, row_scales
+        self.col_codes, self.col_scales = col_codes, col_scales
+
+    @property
+    def device(self):
+        return (self.row_codes if self.row_codes is not None else self.col_codes).device
+
+    def dequantize(self, along="rows", dtype=None, stream=None):
+        return dequantize(self, along, dtype, stream)
+
+
+def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
+    """x as a 2-d matrix with contiguous rows."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if x.dtype not in _GDT:
+        raise TypeError(f"{name} must be float32, bfloat16 or float16")
+    if x.dim() != 2:
+        if x.dim() == 0:
+            raise ValueError(f"{name} must have at least one dimension")
+        x = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.reshape(x.shape[:-1].numel(), 0)
+    if x.stride(1) != 1 and x.shape[1] > 1 or x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    return x
+
+
+def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stream=None):
+    """Quantizes a matrix (leading dimensions are flattened).  With
+    ``col_sums`` (for "cols" and "both") returns (matrix, sums of the columns
+    in x's dtype)."""
+    if blocks not in _BLOCKS:
+        raise ValueError(f"blocks must be one of {sorted(_BLOCKS)}")
+    kind = _BLOCKS[blocks]
+    if col_sums and not kind & _abi.FP8_COLS:
+        raise ValueError('column sums need blocks "cols" or "both"')
+    x = _matrix(x, "x")
+    rows, cols = x.shape
+    dev = x.device
+    pitch = _lib.bwd_fp8_pitch(cols)
+    rc = rs = cc = cs = sums = work = None
+    if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
+        rc = torch.empty((rows, pitch), dtype=torch.uint8, device=dev)
+        rs = torch.empty(_lib.bwd_fp8_scale_bytes(rows, cols), dtype=torch.uint8, device=dev)
+    if kind & (_abi.FP8_COLS | _abi.FP8_TILES):
+        cc = rc if kind == _abi.FP8_TILES else torch.empty((rows, pitch), dtype=torch.uint8, device=dev)
+        cs = torch.empty(_lib.bwd_fp8_scale_bytes(cols, rows), dtype=torch.uint8, device=dev)
+    if col_sums:
+        sums = torch.empty(cols, dtype=x.dtype, device=dev)
+        work = torch.empty(max(1, (rows + 127) // 128 * cols), dtype=torch.float32, device=dev)
+
+    def ptr(t):
+        return None if t is None else t.data_ptr()
+
+    with torch.cuda.device(dev):
+        st = _lib.bwd_fp8_quantize(x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, ptr(rc), ptr(rs),
+                                   ptr(cc), ptr(cs), ptr(sums), ptr(work), _stream_handle(dev, stream))
+    _abi.check(st, "bwd_fp8_quantize")
+    q = Fp8Matrix((rows, cols), blocks, x.dtype, rc, rs, cc, cs)
+    return (q, sums) if col_sums else q
+
+
+def _lines(a: Fp8Matrix, trans: bool, name: str):
+    """Codes, scales, number and length of a matrix's lines."""
+    if not isinstance(a, Fp8Matrix):
+        raise TypeError(f"{name} must be an Fp8Matrix")
+    rows, cols = a.shape
+    codes, scales = (a.col_codes, a.col_scales) if trans else (a.row_codes, a.row_scales)
+    if codes is None:
+        raise ValueError(f'{name} has blocks "{a.blocks}", the product sums along its {"columns" if trans else "rows"}')
+    return (codes, scales, cols, rows) if trans else (codes, scales, rows, cols)
+
+
+def dequantize(a: Fp8Matrix, along: str = "rows", dtype=None, stream=None) -> torch.Tensor:
+    """The values that the codes stand for, in ``dtype`` (the quantized
+    tensor's by default); ``along`` picks the row or the column form."""
+    if along not in ("rows", "cols"):
+        raise ValueError('along must be "rows" or "cols"')
+    codes, scales, _, _ = _lines(a, along == "cols", "a")
+    dtype = a.dtype if dtype is None else dtype
+    if dtype not in _GDT:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    rows, cols = a.shape
+    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
+    with torch.cuda.device(codes.device):
+        st = _lib.bwd_fp8_dequantize(codes.data_ptr(), scales.data_ptr(), int(along == "rows"), rows, cols, out.data_ptr(),
+                                     _GDT[dtype], _stream_handle(codes.device, stream))
+    _abi.check(st, "bwd_fp8_dequantize")
+    return out
+
+
+def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = False, bias: Optional[torch.Tensor] = None,
+           dtype=None, stream=None) -> torch.Tensor:
+    """out[i, j] = sum over the lines' elements of A's line i and B's line j,
+    plus bias[j].  A matrix's lines are its rows, or with ``trans`` its
+    columns; the blocks must run along them."""
+    ac, asc, m, k = _lines(a, trans_a, "a")
+    bc, bsc, n, kb = _lines(b, trans_b, "b")
+    if k != kb:
+        raise ValueError(f"a's lines have {k} elements, b's {kb}")
+    dev = ac.device
+    if bc.device != dev:
+        raise ValueError(f"b is on {bc.device}, the call runs on {dev}")
+    dtype = a.dtype if dtype is None else dtype
+    if dtype not in _GDT:
+        raise TypeError("dtype must be float32, bfloat16 or float16")
+    if bias is not None:
+        _need(bias, "bias", dtype, n, dev)
+    out = torch.empty((m, n), dtype=dtype, device=dev)
+    with torch.cuda.device(dev):
+        st = _lib.bwd_fp8_matmul(m, n, k, ac.data_ptr(), int(trans_a), asc.data_ptr(), bc.data_ptr(), int(trans_b),
+                                 bsc.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), n, _GDT[dtype],
+                                 _stream_handle(dev, stream))
+    _abi.check(st, "bwd_fp8_matmul")
+    return out
+
+
+def _check_width(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not isinstance(w, Fp8Matrix):
+        raise TypeError("w must be an Fp8Matrix")
+    if x.dim() < 1 or x.shape[-1] != w.shape[axis]:
+        raise ValueError(f"{name}'s last dimension must be {w.shape[axis]}")
+
+
+def linear(x: torch.Tensor, w: Fp8Matrix, bias: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """x W^T + bias in x's dtype, for a weight (outputs x inputs) quantized
+    with blocks "tiles" or "rows"; x is quantized within the call."""
+    _check_width(x, w, 1, "x")
+    y = matmul(quantize(x, "rows", stream=stream), w, bias=bias, stream=stream)
+    return y.view(*x.shape[:-1], w.shape[0])
+
+
+def forward(x: torch.Tensor, w: Fp8Matrix, bias: Optional[torch.Tensor] = None, stream=None):
+    """(y, xq): :func:`linear`, and x quantized both ways for :func:`backward`."""
+    _check_width(x, w, 1, "x")
+    xq = quantize(x, "both", stream=stream)
+    return matmul(xq, w, bias=bias, stream=stream).view(*x.shape[:-1], w.shape[0]), xq
+
+
+def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = True, need_weight: bool = True,
+             need_bias: bool = False, stream=None):
+    """(dx, dw, dbias) in dy's dtype, None for those not needed.  xq has
+    column blocks (from :func:`forward`), w blocks "tiles" or "cols"."""
+    _check_width(dy, w, 0, "dy")
+    rows = dy.shape[:-1].numel()
+    if need_weight and (not isinstance(xq, Fp8Matrix) or xq.shape != (rows, w.shape[1])):
+        raise ValueError(f"xq must be an Fp8Matrix of shape {(rows, w.shape[1])}")
+    blocks = "both" if need_input and (need_weight or need_bias) else "rows" if need_input else "cols"
+    db = None
+    if need_bias:
+        dyq, db = quantize(dy, blocks, col_sums=True, stream=stream)
+    else:
+        dyq = quantize(dy, blocks, stream=stream)
+    dx = matmul(dyq, w, trans_b=True, stream=stream).view(*dy.shape[:-1], w.shape[1]) if need_input else None
+    dw = matmul(dyq, xq, trans_a=True, trans_b=True, stream=stream) if need_weight else None
+    return dx, dw, db
+
+
+class _Fp8LinearFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, wq):
+        y, xq = forward(x, wq, bias)
+        ctx.xq, ctx.wq = xq, wq
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        dx, dw, db = backward(dy, ctx.xq, ctx.wq, *ctx.needs_input_grad[:3])
+        return dx, dw, db, None
+
+
+class Fp8Linear(torch.nn.Module):
+    """Linear layer whose three products take 8-bit operands.  ``weight``
+    (outputs x inputs, Xavier-uniform) and ``bias`` (zeros) are ordinary
+    parameters of ``dtype`` for any optimizer; each call quantizes the weight
+    as it is then.  :func:`linear` takes a weight quantized once."""
+
+    def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None, dtype=torch.bfloat16):
+        super().__init__()
+        device = torch.device(device if device is not None else "cuda")
+        self.in_features, self.out_features = int(in_features), int(out_features)
+        self.weight = torch.nn.Parameter(torch.empty(out_features, in_features, dtype=dtype, device=device))
+        self.bias = torch.nn.Parameter(torch.zeros(out_features, dtype=dtype, device=device)) if bias else None
+        bound = (6.0 / (in_features + out_features)) ** 0.5
+        with torch.no_grad():
+            self.weight.uniform_(-bound, bound)
+
+    def forward(self, x: torch.Tensor) -> torch.Tensor:
+        wq = quantize(self.weight.detach(), "tiles")
+        return _Fp8LinearFn.apply(x, self.weight, self.bias, wq)

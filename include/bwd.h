@@ -260,10 +260,126 @@ bwd_status bwd_embedding_backward(const int64_t* ids, int64_t num_tokens,
                                   const float* dy, float* dweight,
                                   float* dgamma, float* dbeta, void* stream);
 
+/* ------------------------------------------------------------------------
+ * AdamW with both moments in fp32, for the tensors of a run whose moments
+ * stay in 32 bits (an embedding, norms, biases), and the gradients' norm.
+ *
+ * One step over a list of tensors (480 per launch), in place:
+ *     g' = s g;  m = b1 m + (1-b1) g';  v = b2 v + ((1-b2) g') g';
+ *     p = p d - step m / (sqrt(v) / c + eps)
+ * with the scalars of bwd_adam8bit_step and s = *grad_scale.  m and v take
+ * one binary32 rounding per operation in that order.  Arrays are HOST arrays
+ * of length num_tensors.
+ *   p          : device pointers to n[i] values of p_dtype, updated in place
+ *                (16-bit ones are widened and rounded back to nearest even).
+ *   g          : device pointers to n[i] values of g_dtype, read only.
+ *   m, v       : device pointers to float[n[i]], updated in place.
+ *   grad_scale : device float[1], read by the kernel, or NULL for 1.  Where
+ *                it is infinite or NaN the call writes nothing.
+ * A NaN or infinite gradient makes its own element's state and parameter
+ * NaN or infinite and no other. */
+bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p,
+                                 bwd_dtype p_dtype, const void* const* g,
+                                 bwd_dtype g_dtype, float* const* m,
+                                 float* const* v, const int64_t* n,
+                                 const float* grad_scale,
+                                 const bwd_adam_hparams* hp, void* stream);
+
+/* Bytes of the workspace of bwd_grad_norm (-1 for num_tensors < 0). */
+int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
+
+/* 2-norm of all elements of a list of gradients, and the factor that brings
+ * it to max_norm at most:
+ *     norm = sqrt(sum (g / loss_scale)^2),
+ *     factor = min(1, max_norm / (norm + 1e-6)) / loss_scale,
+ * NaN where the norm is not finite, so that a step that reads it as its
+ * grad_scale writes nothing.  Sums are fp32 within a thread and binary64
+ * across threads, in a fixed order: results are deterministic.
+ *   out  : device float[2], written: factor, norm.
+ *   work : device, 16-byte aligned, bwd_grad_norm_work_bytes(num_tensors)
+ *          bytes, whose first 16 are zero before the first call; each call
+ *          leaves them zero.  Calls that may run at the same time need one
+ *          each.
+ *   max_norm > 0 (infinity: no clipping), loss_scale > 0 and finite, as is
+ *   1 / loss_scale.  num_tensors == 0 gives norm 0. */
+bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g,
+                         bwd_dtype g_dtype, const int64_t* n, float max_norm,
+                         float loss_scale, float* out, void* work,
+                         void* stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit floating point (e4m3) with a power-of-two scale for each block of
+ * 128: section 二 / 逐块量化's block-wise scaling applied to the operands of a
+ * linear layer's products.
+ *
+ * A block's scale is 2^e, e the smallest integer >= -127 for which no
+ * magnitude in the block exceeds 448 * 2^e; a value's code is the e4m3 number
+ * nearest to x * 2^-e, ties to even.  A block with an infinity or a NaN has
+ * the NaN scale (byte 255) and NaN codes: every product with it is NaN.
+ *
+ * Code array of a rows x cols matrix: uint8[rows][pitch], 16-byte aligned,
+ * pitch = bwd_fp8_pitch(cols) (cols rounded up to 16); the bytes past cols
+ * may hold anything.
+ *
+ * Scale array for `count` lines of `length` elements, each line in blocks of
+ * 128: bwd_fp8_scale_bytes(count, length) bytes, 16-byte aligned; the byte
+ * e + 127 of line r, block k is at
+ *     ((r / 128) * G + k / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + k % 4
+ * with G = ceil(ceil(length / 128) / 4), the order in which the matrix
+ * instruction's scale memory is filled. */
+#define BWD_FP8_ROWS 1  /* blocks of 1 x 128: lines are the rows           */
+#define BWD_FP8_COLS 2  /* blocks of 128 x 1: lines are the columns        */
+#define BWD_FP8_TILES 4 /* blocks of 128 x 128, with scales for both lines */
+
+/* Both -1 for a negative size or one above 2^30. */
+int64_t bwd_fp8_pitch(int64_t cols);
+int64_t bwd_fp8_scale_bytes(int64_t count, int64_t length);
+
+/* Quantizes x (device, rows x cols, `ld` elements between rows).
+ *   blocks : BWD_FP8_ROWS, BWD_FP8_COLS, both of them together, or
+ *            BWD_FP8_TILES.
+ *   row_codes, row_scales : written for BWD_FP8_ROWS and BWD_FP8_TILES;
+ *            scales of `rows` lines of `cols` elements.
+ *   col_codes : written for BWD_FP8_COLS.
+ *   col_scales: written for BWD_FP8_COLS and BWD_FP8_TILES; scales of `cols`
+ *            lines of `rows` elements.
+ *   col_sums : with BWD_FP8_COLS, or NULL: cols values of x's type, written:
+ *            the columns' sums (summed in fp32; a bias's gradient).
+ *   col_sums_work : device float[ceil(rows / 128) * cols] if col_sums is
+ *            given.
+ * At most 65535 * 128 rows. */
+bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows,
+                            int64_t cols, int64_t ld, int32_t blocks,
+                            uint8_t* row_codes, uint8_t* row_scales,
+                            uint8_t* col_codes, uint8_t* col_scales,
+                            void* col_sums, float* col_sums_work,
+                            void* stream);
+
+/* code * 2^e as out[rows][cols] (contiguous) of the given type, rounded to
+ * nearest once; along_rows says which lines the scales belong to (1: rows). */
+bwd_status bwd_fp8_dequantize(const uint8_t* codes, const uint8_t* scales,
+                              int32_t along_rows, int64_t rows, int64_t cols,
+                              void* out, bwd_dtype dtype, void* stream);
+
+/* out[i, j] = sum_l A(i, l) B(j, l) + bias[j], i < m, j < n, l < k.
+ *   a, a_scales : codes and scales of m lines of k elements.  a_trans 0: the
+ *            lines are the rows of an m x k matrix; 1: they are the columns
+ *            of a k x m matrix.  b the same with n for m.
+ *   bias : device, n values of the output's type, or NULL.
+ *   out  : device, m x n values of `dtype`, `ldo` elements between rows.
+ * Products are exact, sums are held in fp32, and the result is rounded once;
+ * the order of the sums is fixed. */
+bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
+                          int32_t a_trans, const uint8_t* a_scales,
+                          const uint8_t* b, int32_t b_trans,
+                          const uint8_t* b_scales, const void* bias, void* out,
+                          int64_t ldo, bwd_dtype dtype, void* stream);
+
 /* Waits for `stream` and reports whether a bounded wait inside one of the
  * library's kernels gave up since the last check (the staged embedding
- * backward waits for its own bulk copies; each wait gives up after about a
- * second, flags the device and lets the kernel return).  BWD_OK, or
+ * backward and the 8-bit product wait for their own copies and products; each
+ * wait gives up after about a second, flags the device and lets the kernel
+ * return).  BWD_OK, or
  * BWD_ERR_CUDA with bwd_last_error() describing it; the flag is cleared.
  * Blocking; not callable during stream capture. */
 bwd_status bwd_check_device(void* stream);
