@@ -223,7 +223,6 @@ fp8_quantize_kernel(const QuantArgs a) {
   }
 }
 
-// Column sums from the quantizer's partial sums, in the order of the rows.
 template <int kT>
 __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
   if (kT == kF32) static_cast<float*>(out)[i] = v;
@@ -231,6 +230,16 @@ __device__ __forceinline__ void store1(void* out, int64_t i, float v) {
   else static_cast<__half*>(out)[i] = __float2half_rn(v);
 }
 
+// Two values as a packed pair of 16-bit ones, rounded to nearest even.
+template <int kT>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if (kT == kBF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Column sums from the quantizer's partial sums, in the order of the rows.
 template <int kT>
 __global__ void __launch_bounds__(256)
 col_sums_kernel(const float* __restrict__ partial, int64_t tiles, int64_t cols, void* __restrict__ out) {
@@ -274,14 +283,17 @@ __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
+}
+
+// Arrival on the same barrier of the pair's first CTA.
+__device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
+  asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}"
+               ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Every wait is bounded: after about a second (or 2^24 polls) it sets the
@@ -304,173 +316,343 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, fail_flag);
 }
 
-// x is the innermost coordinate: a multiple of 128 bytes everywhere here.
-__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
-               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+// Address of a barrier of this CTA in the shared memory of the pair's first
+// CTA, which issues the products for both.
+__device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
+  return r;
 }
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
-               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Tensor copy into this CTA's shared memory that completes on a barrier of
+// the pair's first CTA.  x is the innermost coordinate: a multiple of 64
+// bytes everywhere here.
+__device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+               ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(src)) : "memory");
 }
 
 // Shared-memory matrix descriptor: address, leading and stride byte offsets
-// in units of 16 bytes, version 1, swizzle mode (0 none, 2 128-byte).
+// in units of 16 bytes, version 1, swizzle mode (0 none, 2 128-byte, 4
+// 64-byte).
 __device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead, uint32_t stride, uint32_t swizzle) {
   return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(lead >> 4) << 16) |
          (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (static_cast<uint64_t>(swizzle) << 61);
 }
 
-constexpr int kBM = 128;          // rows of a tile
-constexpr int kBN = 128;          // columns of a tile
+// Arrival on a barrier of both CTAs when the pair's products and scale
+// copies issued so far have finished.
+__device__ __forceinline__ void commit_pair(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+               "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+               "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                 "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                 "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+
+// A pair of CTAs (a cluster of two, one per SM) works on a tile of 256 rows
+// and kBN columns: each holds its 128 rows of A and its half of B's lines,
+// the first CTA issues products that read both halves (cta_group::2) and
+// each CTA's tensor memory holds its own rows' sums.  Against one CTA with
+// 128 x 128 this halves the operand bytes that an SM reads per product.
+// Pairs are persistent and walk the tiles with a grid stride; warp 0 copies,
+// warp 1 issues, warps 2 to 5 store the tile before, all meeting at
+// mbarriers only.
+constexpr int kBM = 256;
 constexpr int kBK = 128;          // bytes of the summed axis in one stage: one scale block
-constexpr int kStages = 5;
-constexpr int kMmThreads = 192;   // warp 0 copies, warp 1 issues products, warps 2 to 5 store
-constexpr int kStageBytes = (kBM + kBN) * kBK;
-constexpr int kStageSf = 2 * kSfTile;
-constexpr int kMmSmem = 1024 + kStages * (kStageBytes + kStageSf);
+constexpr int kMmThreads = 192;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemSf = 2 * kBN;  // scales after the two accumulators
+constexpr uint32_t kTmemSf = 480; // scales after the accumulators: two sets of 4 + 8 columns
+constexpr int kStoreBytes = 4096; // staging of one storing warp: 32 rows of 128 bytes
 
 // The matrix instruction adds into its fp32 accumulator with truncation, an
 // error with a sign that grows with the number of additions (measured
 // relative to 64 bits: 1.9e-7 after 1024 products, 7.6e-7 after 4096,
-// 2.0e-5 after 65536).  Sums therefore leave the accumulator every
-// kChunk blocks and are added up in registers, rounded to nearest.
+// 2.0e-5 after 65536).  That is far below a 16-bit output's rounding.  For
+// fp32 outputs (kSum) the sums leave the accumulator every kChunk blocks and
+// are added up in registers, rounded to nearest.
 constexpr int kChunk = 8;
 
+template <int kBN> __host__ __device__ constexpr int mm_stages() { return kBN == 256 ? 6 : 7; }
+template <int kBN> __host__ __device__ constexpr int mm_a_bytes() { return kBM / 2 * kBK; }
+template <int kBN> __host__ __device__ constexpr int mm_b_bytes() { return kBN / 2 * kBK; }
+template <int kBN> __host__ __device__ constexpr int mm_sf_bytes() { return kSfTile + kBN / 128 * kSfTile; }
+template <int kBN> __host__ __device__ constexpr int mm_smem() {
+  return 1024 + mm_stages<kBN>() * (mm_a_bytes<kBN>() + mm_b_bytes<kBN>() + mm_sf_bytes<kBN>()) + 4 * kStoreBytes;
+}
+
 struct MmArgs {
-  const uint8_t* sfa;
-  const uint8_t* sfb;
   const void* bias;  // [n] or null, of the output's type
   void* out;
   int64_t ldo;
   int m, n, k;
   int a_trans, b_trans;  // operand stored with its own index contiguous
-  int tiles_n;
+  int tiles_m, tiles_n;
+  int sf_rows_b;         // row tiles of B's scales
+  int store;             // the output's rows allow tensor stores
 };
 
-template <int kT>
-__global__ void __launch_bounds__(kMmThreads, 1)
-fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MmArgs p) {
+// The two accumulators.  With 256 columns each they overlap by 32 columns,
+// which leaves room for the scales: the storing warps read the shared
+// columns first and the next tile's products start when they have.
+template <int kBN> __device__ __forceinline__ uint32_t acc_col(int buf) { return buf ? (kBN == 256 ? 224u : 128u) : 0u; }
+
+template <int kT, int kBN, bool kSum>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+                  const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
+                  const __grid_constant__ CUtensorMap map_out, const MmArgs p) {
+  static_assert(!kSum || kBN == 128, "the sums of 256 columns do not fit a thread's registers");
+  constexpr int kStages = mm_stages<kBN>(), kA = mm_a_bytes<kBN>(), kB = mm_b_bytes<kBN>(), kSf = mm_sf_bytes<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* const sf = sm + kStages * kStageBytes;
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2];
+  uint8_t* const store = sm + kStages * (kA + kB);
+  uint8_t* const sf = store + 4 * kStoreBytes;
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_overlap;
+  __shared__ __align__(16) float s_bias[4][128];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t rank;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 4); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 8); }
+    mbar_init(&s_overlap, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols) : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
+  __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
+  cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
   const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
-  const int m0 = static_cast<int>(blockIdx.x) / p.tiles_n * kBM, n0 = static_cast<int>(blockIdx.x) % p.tiles_n * kBN;
+  const int tiles = p.tiles_m * p.tiles_n, pairs = static_cast<int>(gridDim.x) / 2;
+  const int first = static_cast<int>(blockIdx.x) / 2;
+  const int chunk = kSum ? kChunk : kblocks;
 
-  if (warp == 0 && lane == 0) {
-    int kb = 0;
-    for (; kb < kblocks; ++kb) {
-      const int s = kb % kStages;
-      if (!mbar_wait(&s_empty[s], ((kb / kStages) & 1) ^ 1, &s_fail)) break;
-      const bool scales = (kb & 3) == 0;  // four blocks' scales come with the first of them
-      mbar_expect_tx(&s_full[s], kStageBytes + (scales ? kStageSf : 0));
-      uint8_t* const a = sm + s * kStageBytes;
-      uint8_t* const b = a + kBM * kBK;
-      if (p.a_trans) tma_load(a, &map_a, m0, kb * kBK, &s_full[s]); else tma_load(a, &map_a, kb * kBK, m0, &s_full[s]);
-      if (p.b_trans) tma_load(b, &map_b, n0, kb * kBK, &s_full[s]); else tma_load(b, &map_b, kb * kBK, n0, &s_full[s]);
-      if (scales) {
-        bulk_load(sf + s * kStageSf, p.sfa + (static_cast<int64_t>(m0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[s]);
-        bulk_load(sf + s * kStageSf + kSfTile, p.sfb + (static_cast<int64_t>(n0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[s]);
-      }
-    }
-    // After a failure, let the copies issued so far land (bounded) before the
-    // shared memory goes away.
-    if (kb < kblocks)
-      for (int q = kb > kStages ? kb - kStages : 0; q < kb; ++q) mbar_wait(&s_full[q % kStages], (q / kStages) & 1, nullptr);
-  } else if (warp == 1 && lane == 0) {
-    // e4m3 x e4m3, E8M0 scales, 128 x 128, fp32 accumulators; bits 15 and 16: transposed operands
-    const uint32_t idesc = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) |
-                           ((kBN / 8) << 17) | (1u << 23) | ((kBM / 16) << 24);
-    int chunk = 0;
-    bool ok = true;
-    for (int k0 = 0; ok && k0 < kblocks; k0 += kChunk, ++chunk) {
-      const int buf = chunk & 1;
-      ok = mbar_wait(&s_acc_empty[buf], ((chunk >> 1) & 1) ^ 1, &s_fail);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int kb = k0; ok && kb < kblocks && kb < k0 + kChunk; ++kb) {
-        const int s = kb % kStages;
-        if (!(ok = mbar_wait(&s_full[s], (kb / kStages) & 1, &s_fail))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t a = smem_u32(sm + s * kStageBytes), b = a + kBM * kBK;
-        const uint32_t tsf = tmem + kTmemSf + 8 * ((kb >> 2) & 1);
-        if ((kb & 3) == 0) {
-          const uint32_t d = smem_u32(sf + s * kStageSf);
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf), "l"(smem_desc(d, 16, 128, 0)) : "memory");
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4), "l"(smem_desc(d + kSfTile, 16, 128, 0)) : "memory");
-        }
-        const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2), nt = t % p.tiles_n * kBN;
+        const int n0 = nt + static_cast<int>(rank) * (kBN / 2);
+        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!(ok = mbar_wait(&s_empty[s], ((it / kStages) & 1) ^ 1, &s_fail))) break;
+          const bool scales = (kb & 3) == 0;  // four blocks' scales come with the first of them
+          const uint32_t bar = leader_addr(&s_full[s]);
+          if (rank == 0) mbar_expect_tx(&s_full[s], 2 * (kA + kB + (scales ? kSf : 0)));
+          uint8_t* const a = sm + s * (kA + kB);
+          uint8_t* const b = a + kA;
+          if (p.a_trans) tma_load(a, &map_a, m0, kb * kBK, bar); else tma_load(a, &map_a, kb * kBK, m0, bar);
+          if (p.b_trans) tma_load(b, &map_b, n0, kb * kBK, bar); else tma_load(b, &map_b, kb * kBK, n0, bar);
+          if (scales) {
+            // A's for this CTA's rows, B's for the whole tile
+            tma_load(sf + s * kSf, &map_sfa, 0, m0 / 128 * groups + kb / 4, bar);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint64_t da = p.a_trans ? smem_desc(a + q * 4096, 16384, 1024, 2) : smem_desc(a + q * 32, 16, 1024, 2);
-          const uint64_t db = p.b_trans ? smem_desc(b + q * 4096, 16384, 1024, 2) : smem_desc(b + q * 32, 16, 1024, 2);
-          asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                       ::"r"(tmem + buf * kBN), "l"(da), "l"(db), "r"(id), "r"(tsf), "r"(tsf + 4),
-                       "r"(static_cast<uint32_t>(kb != k0 || q != 0)) : "memory");
+            for (int h = 0; h < kBN / 128; ++h) {
+              const int rt = nt / 128 + h;  // past the last row tile: columns past n, whatever they hold
+              tma_load(sf + s * kSf + (1 + h) * kSfTile, &map_sfb, 0, (rt < p.sf_rows_b ? rt : p.sf_rows_b - 1) * groups + kb / 4, bar);
+            }
+          }
         }
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_empty[s])) : "memory");
       }
-      asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(&s_acc_full[buf])) : "memory");
     }
-  } else if (warp >= 2) {
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
+      const uint32_t idesc = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) |
+                             ((kBN / 8) << 17) | (1u << 23) | ((kBM / 16) << 24);
+      // descriptors without their addresses, and the step of 32 along the summed axis
+      const uint64_t da0 = smem_desc(0, 16, 1024, 2);
+      const uint64_t db0 = p.b_trans && kBN == 128 ? smem_desc(0, 16, 512, 4) : smem_desc(0, 16, 1024, 2);
+      const uint32_t sa = p.a_trans ? 4096 / 16 : 32 / 16, sb = p.b_trans ? kBN / 2 * 32 / 16 : 32 / 16;
+      int it = 0, use = 0;  // stages and accumulators used so far
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += pairs) {
+        for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
+          const int buf = use & 1;
+          ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
+          if (kBN == 256 && ok && use > 0) ok = mbar_wait(&s_overlap, (use - 1) & 1, &s_fail);
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const int k1 = kblocks < k0 + chunk ? kblocks : k0 + chunk;
+          for (int kb = k0; ok && kb < k1; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!(ok = mbar_wait(&s_full[s], (it / kStages) & 1, &s_fail))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t a = smem_u32(sm + s * (kA + kB)), b = a + kA;
+            const uint32_t tsf = tmem + kTmemSf + 16 * ((kb >> 2) & 1);
+            if ((kb & 3) == 0) {
+              const uint32_t d = smem_u32(sf + s * kSf);
+#pragma unroll
+              for (int h = 0; h < 1 + kBN / 128; ++h)
+                asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4 * h), "l"(smem_desc(d + h * kSfTile, 16, 128, 0)) : "memory");
+            }
+            const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+#pragma unroll
+            for (uint32_t q = 0; q < 4; ++q)
+              asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+                           "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                           ::"r"(tmem + acc_col<kBN>(buf)), "l"(da0 + (a >> 4) + q * sa), "l"(db0 + (b >> 4) + q * sb), "r"(id), "r"(tsf), "r"(tsf + 4),
+                           "r"(static_cast<uint32_t>(kb != k0 || q != 0)) : "memory");
+            commit_pair(&s_empty[s]);
+          }
+          commit_pair(&s_acc_full[buf]);
+        }
+      }
+    }
+  } else {
     const int quarter = warp & 3;  // the lanes of tensor memory that this warp may read
-    const int m = m0 + quarter * 32 + lane;
-    float sum[kBN];
-#pragma unroll
-    for (int j = 0; j < kBN; ++j) sum[j] = 0.0f;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint8_t* const stage = store + quarter * kStoreBytes;
+    float* const bias_s = s_bias[quarter];
+    constexpr int kCols = kT == kF32 ? 32 : 64;  // columns of one staged group: 128 bytes
+    constexpr int kGroups = kBN / kCols;
+    int use = 0;
     bool ok = true;
-    int chunk = 0;
-    for (int k0 = 0; ok && k0 < kblocks; k0 += kChunk, ++chunk) {
-      const int buf = chunk & 1;
-      ok = mbar_wait(&s_acc_full[buf], (chunk >> 1) & 1, &s_fail);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    for (int t = first; ok && t < tiles; t += pairs) {
+      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = t % p.tiles_n * kBN;
+      float sum[kSum ? kBN : 1];
+      if constexpr (kSum) {
 #pragma unroll
-      for (int c = 0; c < kBN; c += 16) {
-        uint32_t r[16];
-        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                     : "r"(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + buf * kBN + c));
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        for (int j = 0; j < kBN; ++j) sum[j] = 0.0f;
+        for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
+          const int buf = use & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[buf], (use >> 1) & 1, &s_fail));
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-        for (int u = 0; u < 16; ++u) sum[c + u] = __fadd_rn(sum[c + u], __uint_as_float(r[u]));
+          for (int c = 0; c < kBN; c += 32) {
+            uint32_t r[32];
+            tmem_load32(lanes + acc_col<kBN>(buf) + c, r);
+            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+            for (int u = 0; u < 32; ++u) sum[c + u] = __fadd_rn(sum[c + u], __uint_as_float(r[u]));
+          }
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
+        }
+        if (!ok) break;
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_acc_empty[buf]);
-    }
-    if (ok && m < p.m) {
+      const int buf = use & 1;
+      if constexpr (!kSum) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[buf], (use >> 1) & 1, &s_fail));
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      }
 #pragma unroll
-      for (int j = 0; j < kBN; ++j)
-        if (n0 + j < p.n)
-          store1<kT>(p.out, m * p.ldo + n0 + j, p.bias ? __fadd_rn(sum[j], load1<kT>(p.bias, n0 + j)) : sum[j]);
+      for (int i = 0; i < kGroups; ++i) {
+        // the group that holds the accumulators' shared columns goes first
+        const int gr = (!kSum && kBN == 256 && buf == 0) ? (i + kGroups - 1) % kGroups : i;
+        const int c = gr * kCols;
+        float v[kCols];
+        if constexpr (kSum) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = sum[i * kCols + j];
+        } else {
+          uint32_t r[kCols / 32][32];
+#pragma unroll
+          for (int h = 0; h < kCols / 32; ++h) tmem_load32(lanes + acc_col<kBN>(buf) + c + 32 * h, r[h]);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (i == 0 || i == kGroups - 1) {
+            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+            __syncwarp();
+            if (lane == 0 && i == 0 && kBN == 256) mbar_arrive_leader(&s_overlap);
+            if (lane == 0 && i == kGroups - 1) mbar_arrive_leader(&s_acc_empty[buf]);
+          }
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
+        }
+        if (p.bias) {
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < kCols; h += 32) bias_s[h + lane] = n0 + c + h + lane < p.n ? load1<kT>(p.bias, n0 + c + h + lane) : 0.0f;
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < kCols; j += 4) {
+            const float4 b = *reinterpret_cast<const float4*>(bias_s + j);
+            v[j] = __fadd_rn(v[j], b.x); v[j + 1] = __fadd_rn(v[j + 1], b.y);
+            v[j + 2] = __fadd_rn(v[j + 2], b.z); v[j + 3] = __fadd_rn(v[j + 3], b.w);
+          }
+        }
+        if (p.store) {
+          // a row of 128 bytes per lane, its 16-byte pieces swizzled as the tensor map says
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            uint4 w;
+            if constexpr (kT == kF32) {
+              w = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+            } else {
+              w = make_uint4(pack16<kT>(v[8 * q], v[8 * q + 1]), pack16<kT>(v[8 * q + 2], v[8 * q + 3]),
+                             pack16<kT>(v[8 * q + 4], v[8 * q + 5]), pack16<kT>(v[8 * q + 6], v[8 * q + 7]));
+            }
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0 && m0 < p.m && n0 + c < p.n) {
+            tma_store(&map_out, n0 + c, m0, stage);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else if (m0 + lane < p.m) {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            if (n0 + c + j < p.n) store1<kT>(p.out, (m0 + lane) * p.ldo + n0 + c + j, v[j]);
+        }
+      }
+      if (!kSum) ++use;
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  // After a failed wait, copies and products may still be under way: leave
+  // them two milliseconds before the memory they use goes away.
+  if (s_fail && lane == 0 && warp < 2) {
+    uint64_t t0, t1;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+    for (int i = 0; i < (1 << 20); ++i) {
+      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
+      if (t1 - t0 > 2000000ull) break;
     }
   }
+  __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  cluster_sync();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// A product over nothing: the bias, or zero.
+template <int kT>
+__global__ void __launch_bounds__(256)
+fill_rows_kernel(const void* __restrict__ bias, void* __restrict__ out, int64_t ldo, int64_t m, int64_t n) {
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < m * n; i += stride)
+    store1<kT>(out, i / n * ldo + i % n, bias ? load1<kT>(bias, i % n) : 0.0f);
 }
 
 // --------------------------------------------------------------------------
@@ -496,19 +678,32 @@ bwd_status encode_fn(EncodeFn* out) {
   return BWD_OK;
 }
 
-// Map of a row-major byte matrix for boxes of 128 bytes x box_rows rows.
-bwd_status code_map(CUtensorMap* map, const uint8_t* codes, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
+// Map of a row-major matrix for boxes of box_cols x box_rows elements.
+bwd_status matrix_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows, int64_t cols,
+                      int64_t pitch_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
   EncodeFn encode = nullptr;
   bwd_status s = encode_fn(&encode);
   if (s != BWD_OK) return s;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch)};
-  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(codes), dims, strides, box, step,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch_bytes)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+  const CUresult r = encode(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BWD_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
   return BWD_OK;
+}
+
+// Map of one operand's codes: `lines` lines of k codes, box of box_lines lines.
+bwd_status code_map(CUtensorMap* map, const uint8_t* codes, int64_t lines, int64_t k, int trans, int box_lines) {
+  if (trans)
+    return matrix_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, k, lines, bwd_fp8_pitch(lines), box_lines, kBK,
+                      box_lines == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  return matrix_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, lines, k, bwd_fp8_pitch(k), kBK, box_lines, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Map of a scale array: one row of 512 bytes for each of its tiles.
+bwd_status scale_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles) {
+  return matrix_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, tiles, kSfTile / 4, kSfTile, kSfTile / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 constexpr int64_t kMaxDim = int64_t{1} << 30;
@@ -527,12 +722,75 @@ bwd_status launch_quantize(int mode, const QuantArgs& a, cudaStream_t st) {
   return check_launch("fp8_quantize_kernel launch");
 }
 
-template <int kT>
-bwd_status launch_matmul(const CUtensorMap& ma, const CUtensorMap& mb, const MmArgs& p, int tiles, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(fp8_matmul_kernel<kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmSmem);
+// What a launch needs to know of the device, found once for each.
+constexpr int kMaxDevices = 64;
+struct DeviceState {
+  bool ready = false;
+  unsigned long long ctx = 0;
+  int pairs = 0;  // CTA pairs that are resident at a time
+};
+std::mutex g_mu;
+DeviceState g_dev[kMaxDevices];
+
+template <int kT, int kBN, bool kSum>
+cudaError_t opt_in() {
+  return cudaFuncSetAttribute(fp8_matmul_kernel<kT, kBN, kSum>, cudaFuncAttributeMaxDynamicSharedMemorySize, mm_smem<kBN>());
+}
+
+bwd_status ensure_device(const DeviceState** out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (dev < 0 || dev >= kMaxDevices) return fail(BWD_ERR_CUDA, "device ordinal %d unsupported", dev);
+  unsigned long long ctx = 0;
+  const bwd_status s = bwd::host::current_context_id(&ctx);
+  if (s != BWD_OK) return s;
+  std::lock_guard<std::mutex> lock(g_mu);
+  DeviceState& d = g_dev[dev];
+  *out = &d;
+  if (d.ready && d.ctx == ctx) return BWD_OK;
+  int sms = 0;
+  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = opt_in<kF32, 128, true>();
+  if (e == cudaSuccess) e = opt_in<kBF16, 256, false>();
+  if (e == cudaSuccess) e = opt_in<kF16, 256, false>();
+  if (e == cudaSuccess) e = opt_in<kBF16, 128, false>();
+  if (e == cudaSuccess) e = opt_in<kF16, 128, false>();
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
-  fp8_matmul_kernel<kT><<<tiles, kMmThreads, kMmSmem, st>>>(ma, mb, p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = mm_smem<256>();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {2, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false>, &cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+  if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
+  d.ctx = ctx;
+  d.ready = true;
+  return BWD_OK;
+}
+
+struct MmMaps {
+  CUtensorMap a, b, sfa, sfb, out;
+};
+
+template <int kT, int kBN, bool kSum>
+bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
+  const int tiles = p.tiles_m * p.tiles_n;
+  fp8_matmul_kernel<kT, kBN, kSum><<<2 * (tiles < pairs ? tiles : pairs), kMmThreads, mm_smem<kBN>(), st>>>(
+      maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
   return check_launch("fp8_matmul_kernel launch");
+}
+
+template <int kT>
+bwd_status launch_fill(const MmArgs& p, cudaStream_t st) {
+  const int64_t need = (static_cast<int64_t>(p.m) * p.n + 255) / 256;
+  fill_rows_kernel<kT><<<static_cast<unsigned>(need < 1216 ? need : 1216), 256, 0, st>>>(p.bias, p.out, p.ldo, p.m, p.n);
+  return check_launch("fill_rows_kernel launch");
 }
 
 }  // namespace
@@ -638,22 +896,38 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
   if (!aligned_to(out, eb) || (bias && !aligned_to(bias, eb))) return fail(BWD_ERR_INVALID_ARG, "out and bias must be aligned to their element size");
   if (k > 0 && (!aligned16(a) || !aligned16(b) || !aligned16(a_scales) || !aligned16(b_scales)))
     return fail(BWD_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
-  CUtensorMap ma{}, mb{};
-  bwd_status s;
-  if (k > 0) {
-    s = a_trans ? code_map(&ma, a, k, m, bwd_fp8_pitch(m), kBK) : code_map(&ma, a, m, k, bwd_fp8_pitch(k), kBM);
-    if (s != BWD_OK) return s;
-    s = b_trans ? code_map(&mb, b, k, n, bwd_fp8_pitch(n), kBK) : code_map(&mb, b, n, k, bwd_fp8_pitch(k), kBN);
-    if (s != BWD_OK) return s;
-  }
-  const int64_t tiles_n = tiles_of(n), tiles = tiles_of(m) * tiles_n;
-  if (tiles > 0x7fffffff) return fail(BWD_ERR_INVALID_ARG, "too many output tiles");
-  MmArgs p{a_scales, b_scales, bias, out, ldo, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k),
-           a_trans ? 1 : 0, b_trans ? 1 : 0, static_cast<int>(tiles_n)};
+  MmArgs p{};
+  p.bias = bias; p.out = out; p.ldo = ldo;
+  p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
+  p.a_trans = a_trans ? 1 : 0; p.b_trans = b_trans ? 1 : 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (dtype == BWD_F32) return launch_matmul<kF32>(ma, mb, p, static_cast<int>(tiles), st);
-  if (dtype == BWD_BF16) return launch_matmul<kBF16>(ma, mb, p, static_cast<int>(tiles), st);
-  return launch_matmul<kF16>(ma, mb, p, static_cast<int>(tiles), st);
+  if (k == 0) return dtype == BWD_F32 ? launch_fill<kF32>(p, st) : dtype == BWD_BF16 ? launch_fill<kBF16>(p, st) : launch_fill<kF16>(p, st);
+  const DeviceState* d = nullptr;
+  bwd_status s = ensure_device(&d);
+  if (s != BWD_OK) return s;
+  const int64_t tiles_m = (m + kBM - 1) / kBM;
+  // 256 columns unless tiles of 128 are needed to give every pair one
+  const int bn = dtype == BWD_F32 || tiles_m * ((n + 255) / 256) < d->pairs ? 128 : 256;
+  const int64_t tiles_n = (n + bn - 1) / bn;
+  if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
+    return fail(BWD_ERR_INVALID_ARG, "too many tiles");
+  p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
+  p.sf_rows_b = static_cast<int>(tiles_of(n));
+  p.store = aligned16(out) && ldo * eb % 16 == 0;
+  MmMaps maps{};
+  if ((s = code_map(&maps.a, a, m, k, p.a_trans, kBM / 2)) != BWD_OK) return s;
+  if ((s = code_map(&maps.b, b, n, k, p.b_trans, bn / 2)) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfa, a_scales, tiles_of(m) * groups_of(k))) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfb, b_scales, tiles_of(n) * groups_of(k))) != BWD_OK) return s;
+  if (p.store) {
+    const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
+  }
+  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
+  if (dtype == BWD_BF16)
+    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, st);
+  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, st);
 }
 
 }  // extern "C"
