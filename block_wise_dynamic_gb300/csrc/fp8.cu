@@ -28,6 +28,7 @@
 
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "bwd.h"
 #include "host_util.h"
@@ -67,19 +68,17 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits) {
   return static_cast<uint32_t>(b < 0 ? 0 : b);
 }
 
-// 2^-e for a scale byte (finite: bytes of finite maxima are at most 248).
-__device__ __forceinline__ float inv_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+// 2^-e for a scale byte (bytes of finite maxima are at most 248); NaN for a
+// block that is not finite, which makes all its codes NaN.
+__device__ __forceinline__ float inv_scale(uint32_t byte) {
+  return __uint_as_float(byte == 255u ? 0x7fffffffu : (254u - byte) << 23);
+}
 
-// Four codes, packed.  255 marks a block with non-finite values.
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], const uint32_t (&byte)[4]) {
-  float y[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    y[j] = byte[j] == 255u ? __uint_as_float(0x7fffffffu) : __fmul_rn(x[j], inv_scale(byte[j]));
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
-  return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
+// Two codes: cvt rounds to nearest even, and no finite value here exceeds 448.
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <int kT>
@@ -90,24 +89,29 @@ __device__ __forceinline__ float load1(const void* x, int64_t i) {
   return __half2float(__ushort_as_half(h));
 }
 
-// Four consecutive elements; the address is aligned to their size.
+// The quantizer keeps what it has read as it was stored: words of one fp32
+// value or two 16-bit ones.  Magnitudes of any of the types order like their
+// bits (infinities and NaN above all numbers), so maxima are integer ones.
 template <int kT>
-__device__ __forceinline__ void load4(const void* x, int64_t i, float (&o)[4]) {
-  if (kT == kF32) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(x) + i));
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-  } else {
-    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + i));
-    if (kT == kBF16) {
-      o[0] = __uint_as_float(a.x << 16); o[1] = __uint_as_float(a.x & 0xffff0000u);
-      o[2] = __uint_as_float(a.y << 16); o[3] = __uint_as_float(a.y & 0xffff0000u);
-    } else {
-      o[0] = __half2float(__ushort_as_half(static_cast<unsigned short>(a.x & 0xffffu)));
-      o[1] = __half2float(__ushort_as_half(static_cast<unsigned short>(a.x >> 16)));
-      o[2] = __half2float(__ushort_as_half(static_cast<unsigned short>(a.y & 0xffffu)));
-      o[3] = __half2float(__ushort_as_half(static_cast<unsigned short>(a.y >> 16)));
-    }
-  }
+__device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) { return kT == kF32 ? max(a, b) : __vmaxu2(a, b); }
+template <int kT>
+__device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & (kT == kF32 ? 0x7fffffffu : 0x7fff7fffu); }
+
+// fp32 bits of a magnitude given by its own type's bits.
+template <int kT>
+__device__ __forceinline__ uint32_t widen_bits(uint32_t b) {
+  if (kT == kF32) return b;
+  if (kT == kBF16) return b << 16;
+  return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(b))));
+}
+
+// Value j (0 .. 16 / size - 1) of a 16-byte piece.
+template <int kT>
+__device__ __forceinline__ float piece(const uint4& w, int j) {
+  const uint32_t q = (&w.x)[kT == kF32 ? j : j / 2];
+  if (kT == kF32) return __uint_as_float(q);
+  if (kT == kBF16) return __uint_as_float(j % 2 ? q & 0xffff0000u : q << 16);
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(j % 2 ? q >> 16 : q & 0xffffu)));
 }
 
 struct QuantArgs {
@@ -121,104 +125,187 @@ struct QuantArgs {
   uint8_t* codes_c;        // 128 x 1 blocks
   uint8_t* scales_c;
   float* col_sums;         // [row tiles][cols] partial column sums, or null
-  int vec;                 // rows start on 4-element boundaries
+  int vec;                 // rows start on 16-byte boundaries and hold whole pieces
 };
 
-// One CTA for a tile of 128 x 128 elements: warp w holds rows w, w + 8, ...,
-// lane l the columns 4 l to 4 l + 3, so a warp's load covers a row's 128
-// elements.  kMode is a set of BWD_FP8_ROWS, BWD_FP8_COLS, BWD_FP8_TILES.
-constexpr int kQThreads = 256, kQWarps = kQThreads / 32, kQRows = kTile / kQWarps;
+// One CTA for a tile of 128 x 128 elements.  A thread holds eight pieces of
+// 16 bytes in registers, one from every eighth part of the tile's rows, as
+// they were stored; a warp's load covers whole rows.  Both maxima and all
+// codes come from that one read.  kMode is a set of BWD_FP8_ROWS,
+// BWD_FP8_COLS, BWD_FP8_TILES.
+template <int kT> __host__ __device__ constexpr int q_vals() { return 16 / elem_bytes<kT>(); }  // values of a piece
+template <int kT> __host__ __device__ constexpr int q_lanes() { return kTile / q_vals<kT>(); }  // lanes to a row
+template <int kT> __host__ __device__ constexpr int q_rows() { return 32 / q_lanes<kT>(); }     // rows to a warp's load
+constexpr int kQPieces = 8;
+template <int kT> __host__ __device__ constexpr int q_warps() { return kTile / kQPieces / q_rows<kT>(); }
 
-template <int kT, int kMode>
-__global__ void __launch_bounds__(kQThreads)
+template <int kT, int kMode, bool kSums, bool kVec>
+__global__ void __launch_bounds__(32 * q_warps<kT>(), 32 / q_warps<kT>())
 fp8_quantize_kernel(const QuantArgs a) {
   constexpr bool kRows = kMode & BWD_FP8_ROWS, kCols = kMode & BWD_FP8_COLS, kTiles = kMode & BWD_FP8_TILES;
-  __shared__ uint32_t s_col[kQWarps][kTile];
-  __shared__ float s_sum[kQWarps][kTile];
-  __shared__ uint32_t s_tile[kQWarps];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  constexpr int kVals = q_vals<kT>(), kLanes = q_lanes<kT>(), kPerLoad = q_rows<kT>(), kWarps = q_warps<kT>();
+  __shared__ __align__(16) uint4 s_col[kCols ? kWarps : 1][kLanes];
+  __shared__ __align__(16) float s_sum[kSums ? kWarps : 1][kTile];
+  __shared__ uint32_t s_tile[kWarps];
+  __shared__ uint8_t s_byte[kTile];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % kLanes;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile, c0 = static_cast<int64_t>(blockIdx.x) * kTile;
-  const int64_t c = c0 + 4 * lane;
-  float x[kQRows][4];
-  const bool vec = a.vec && c + 4 <= a.cols;
-#pragma unroll
-  for (int i = 0; i < kQRows; ++i) {
-    const int64_t r = r0 + warp + kQWarps * i;
-    if (vec && r < a.rows) {
-      load4<kT>(a.x, r * a.ld + c, x[i]);
+  const int64_t c = c0 + kVals * part;
+  const int row = warp * kPerLoad + lane / kLanes;  // piece i: row + i * kTile / kQPieces
+  const int rows_here = a.rows - r0 < kTile ? static_cast<int>(a.rows - r0) : kTile;
+  const char* const src0 = static_cast<const char*>(a.x) + ((r0 + row) * a.ld + c) * elem_bytes<kT>();
+  const int64_t src_step = a.ld * (kTile / kQPieces) * elem_bytes<kT>();
+  const auto load = [&](int i) {
+    const char* const src = src0 + i * src_step;
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    const bool in = row + i * (kTile / kQPieces) < rows_here;
+    if constexpr (kVec) {
+      if (in && c < a.cols) w = *reinterpret_cast<const uint4*>(src);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[i][j] = (r < a.rows && c + j < a.cols) ? load1<kT>(a.x, r * a.ld + c + j) : 0.0f;
+      for (int j = 0; j < kVals; ++j)
+        if (in && c + j < a.cols) {
+          if (kT == kF32) (&w.x)[j] = reinterpret_cast<const uint32_t*>(src)[j];
+          else (&w.x)[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[j]) << (16 * (j % 2));
+        }
     }
-  }
+    return w;
+  };
+  uint4 x[kQPieces];
+#pragma unroll
+  for (int i = 0; i < kQPieces; ++i) x[i] = load(i);
 
-  if (kRows) {
+  // Codes of piece i; the pitch is a multiple of 16, so a piece's codes lie
+  // before it or past it.
+  const int64_t at = (r0 + row) * a.pitch + c, step = a.pitch * (kTile / kQPieces);
+  const bool in_pitch = c < a.pitch;
+  const auto put = [&](uint8_t* codes, int i, const uint4& w16, const float (&inv)[kVals]) {
+    uint32_t w[kVals / 4];
 #pragma unroll
-    for (int i = 0; i < kQRows; ++i) {
-      const int64_t r = r0 + warp + kQWarps * i;
-      uint32_t top = 0;
+    for (int j = 0; j < kVals; j += 4)
+      w[j / 4] = codes2(__fmul_rn(piece<kT>(w16, j), inv[j]), __fmul_rn(piece<kT>(w16, j + 1), inv[j + 1])) |
+                 codes2(__fmul_rn(piece<kT>(w16, j + 2), inv[j + 2]), __fmul_rn(piece<kT>(w16, j + 3), inv[j + 3])) << 16;
+    if (in_pitch && row + i * (kTile / kQPieces) < rows_here) {
+      uint32_t* const dst = reinterpret_cast<uint32_t*>(codes + i * step);
+      if constexpr (kVals == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else *dst = w[0];
+    }
+  };
+
+  if constexpr (kCols) {
+    uint4 top = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7fffffffu);
-      const uint32_t b = scale_byte(__reduce_max_sync(0xffffffffu, top));
-      const uint32_t bytes[4] = {b, b, b, b};
-      if (r < a.rows && c < a.pitch) *reinterpret_cast<uint32_t*>(a.codes_r + r * a.pitch + c) = codes4(x[i], bytes);
-      if (lane == 0) a.scales_r[scale_offset(r, blockIdx.x, a.groups_r)] = static_cast<uint8_t>(b);
+    for (int i = 0; i < kQPieces; ++i) {
+      top.x = max_words<kT>(top.x, magnitude<kT>(x[i].x)); top.y = max_words<kT>(top.y, magnitude<kT>(x[i].y));
+      top.z = max_words<kT>(top.z, magnitude<kT>(x[i].z)); top.w = max_words<kT>(top.w, magnitude<kT>(x[i].w));
+    }
+    if (kPerLoad == 2) {
+      top.x = max_words<kT>(top.x, __shfl_xor_sync(0xffffffffu, top.x, 16)); top.y = max_words<kT>(top.y, __shfl_xor_sync(0xffffffffu, top.y, 16));
+      top.z = max_words<kT>(top.z, __shfl_xor_sync(0xffffffffu, top.z, 16)); top.w = max_words<kT>(top.w, __shfl_xor_sync(0xffffffffu, top.w, 16));
+    }
+    if (lane < kLanes) s_col[warp][lane] = top;
+  } else if constexpr (kTiles) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i)
+      top = max_words<kT>(top, max_words<kT>(max_words<kT>(magnitude<kT>(x[i].x), magnitude<kT>(x[i].y)),
+                                             max_words<kT>(magnitude<kT>(x[i].z), magnitude<kT>(x[i].w))));
+    if (kT != kF32) top = max(top & 0xffffu, top >> 16);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_tile[warp] = top;
+  }
+  if constexpr (kRows) {
+    uint32_t top[kQPieces];
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i)
+      top[i] = max_words<kT>(max_words<kT>(magnitude<kT>(x[i].x), magnitude<kT>(x[i].y)),
+                             max_words<kT>(magnitude<kT>(x[i].z), magnitude<kT>(x[i].w)));
+    if constexpr (kT == kF32) {
+#pragma unroll
+      for (int i = 0; i < kQPieces; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
+    } else {
+      // two rows to a word, reduced over the row's sixteen lanes
+#pragma unroll
+      for (int i = 0; i < kQPieces; i += 2) {
+        uint32_t both = __vmaxu2(__byte_perm(top[i], top[i + 1], 0x5410), __byte_perm(top[i], top[i + 1], 0x7632));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+        top[i] = both & 0xffffu;
+        top[i + 1] = both >> 16;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i) {
+      const uint32_t b = scale_byte(widen_bits<kT>(top[i]));
+      if (part == 0) s_byte[row + i * (kTile / kQPieces)] = static_cast<uint8_t>(b);
+      float inv[kVals];
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) inv[j] = inv_scale(b);
+      put(a.codes_r + at, i, x[i], inv);
     }
   }
-  if (kCols || kTiles) {
-    uint32_t top[4] = {0, 0, 0, 0};
-    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+  if (kRows && threadIdx.x < kTile)
+    a.scales_r[scale_offset(r0 + threadIdx.x, blockIdx.x, a.groups_r)] = s_byte[threadIdx.x];
+  if constexpr (kCols) {
+    uint4 top = s_col[0][part];
 #pragma unroll
-    for (int i = 0; i < kQRows; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        top[j] = max(top[j], __float_as_uint(x[i][j]) & 0x7fffffffu);
-        if (kCols) sum[j] += x[i][j];
-      }
-    if (kCols) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) { s_col[warp][4 * lane + j] = top[j]; s_sum[warp][4 * lane + j] = sum[j]; }
-    } else {
-      const uint32_t t = __reduce_max_sync(0xffffffffu, max(max(top[0], top[1]), max(top[2], top[3])));
-      if (lane == 0) s_tile[warp] = t;
+    for (int w = 1; w < kWarps; ++w) {
+      const uint4 t = s_col[w][part];
+      top.x = max_words<kT>(top.x, t.x); top.y = max_words<kT>(top.y, t.y);
+      top.z = max_words<kT>(top.z, t.z); top.w = max_words<kT>(top.w, t.w);
     }
-    __syncthreads();
-    uint32_t bytes[4];
-    if (kCols) {
+    float inv[kVals];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t t = 0;
-#pragma unroll
-        for (int w = 0; w < kQWarps; ++w) t = max(t, s_col[w][4 * lane + j]);
-        bytes[j] = scale_byte(t);
-      }
-      if (warp == 0) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a.scales_c[scale_offset(c + j, blockIdx.y, a.groups_c)] = static_cast<uint8_t>(bytes[j]);
-      }
-      if (a.col_sums && threadIdx.x < kTile && c0 + threadIdx.x < a.cols) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kQWarps; ++w) s += s_sum[w][threadIdx.x];
-        a.col_sums[blockIdx.y * a.cols + c0 + threadIdx.x] = s;
-      }
-    } else {
-      uint32_t t = 0;
-#pragma unroll
-      for (int w = 0; w < kQWarps; ++w) t = max(t, s_tile[w]);
-      const uint32_t b = scale_byte(t);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) bytes[j] = b;
-      // the tile's scale, once for each of its rows and once for each of its columns
-      if (threadIdx.x < kTile) a.scales_r[scale_offset(r0 + threadIdx.x, blockIdx.x, a.groups_r)] = static_cast<uint8_t>(b);
-      else a.scales_c[scale_offset(c0 + threadIdx.x - kTile, blockIdx.y, a.groups_c)] = static_cast<uint8_t>(b);
+    for (int j = 0; j < kVals; ++j) {
+      const uint32_t q = (&top.x)[kT == kF32 ? j : j / 2];
+      const uint32_t b = scale_byte(widen_bits<kT>(kT == kF32 ? q : j % 2 ? q >> 16 : q & 0xffffu));
+      inv[j] = inv_scale(b);
+      if (warp == 0 && lane < kLanes) a.scales_c[scale_offset(c + j, blockIdx.y, a.groups_c)] = static_cast<uint8_t>(b);
     }
-    uint8_t* const codes = kCols ? a.codes_c : a.codes_r;
+    // With both forms of 16-bit values the tile is read again, from L1: held
+    // in registers over the first form's codes it spilled (8192 x 11008: 82 us
+    // against 75).  fp32 pieces hold half as many values and stay (101 us
+    // against 138).
+    constexpr bool kAgain = kRows && kT != kF32;
+    float sum[kVals] = {};
 #pragma unroll
-    for (int i = 0; i < kQRows; ++i) {
-      const int64_t r = r0 + warp + kQWarps * i;
-      if (r < a.rows && c < a.pitch) *reinterpret_cast<uint32_t*>(codes + r * a.pitch + c) = codes4(x[i], bytes);
+    for (int i = 0; i < kQPieces; ++i) {
+      const uint4 w = kAgain ? load(i) : x[i];
+      put(a.codes_c + at, i, w, inv);
+      if constexpr (kSums) {
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) sum[j] += piece<kT>(w, j);
+      }
+    }
+    if constexpr (kSums) {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        if (kPerLoad == 2) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 16);
+        if (lane < kLanes) s_sum[warp][kVals * part + j] = sum[j];
+      }
+      __syncthreads();
+    }
+  } else if constexpr (kTiles) {
+    uint32_t top = s_tile[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) top = max(top, s_tile[w]);
+    const uint32_t b = scale_byte(widen_bits<kT>(top));
+    // the tile's scale, once for each of its rows and once for each of its columns
+    if (threadIdx.x < kTile) a.scales_r[scale_offset(r0 + threadIdx.x, blockIdx.x, a.groups_r)] = static_cast<uint8_t>(b);
+    else if (threadIdx.x < 2 * kTile) a.scales_c[scale_offset(c0 + threadIdx.x - kTile, blockIdx.y, a.groups_c)] = static_cast<uint8_t>(b);
+    float inv[kVals];
+#pragma unroll
+    for (int j = 0; j < kVals; ++j) inv[j] = inv_scale(b);
+#pragma unroll
+    for (int i = 0; i < kQPieces; ++i) put(a.codes_r + at, i, x[i], inv);
+  }
+  if constexpr (kSums) {
+    if (threadIdx.x < kTile && c0 + threadIdx.x < a.cols) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += s_sum[w][threadIdx.x];
+      a.col_sums[blockIdx.y * a.cols + c0 + threadIdx.x] = s;
     }
   }
 }
@@ -714,11 +801,20 @@ int64_t groups_of(int64_t n) { return (tiles_of(n) + 3) / 4; }
 
 template <int kT>
 bwd_status launch_quantize(int mode, const QuantArgs& a, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(tiles_of(a.cols)), static_cast<unsigned>(tiles_of(a.rows)));
-  if (mode == BWD_FP8_ROWS) fp8_quantize_kernel<kT, BWD_FP8_ROWS><<<grid, kQThreads, 0, st>>>(a);
-  else if (mode == BWD_FP8_COLS) fp8_quantize_kernel<kT, BWD_FP8_COLS><<<grid, kQThreads, 0, st>>>(a);
-  else if (mode == BWD_FP8_TILES) fp8_quantize_kernel<kT, BWD_FP8_TILES><<<grid, kQThreads, 0, st>>>(a);
-  else fp8_quantize_kernel<kT, BWD_FP8_ROWS | BWD_FP8_COLS><<<grid, kQThreads, 0, st>>>(a);
+  const auto launch = [&](auto m, auto sums) {
+    constexpr int kMode = decltype(m)::value;
+    constexpr bool kSums = decltype(sums)::value;
+    const dim3 grid(static_cast<unsigned>(tiles_of(a.cols)), static_cast<unsigned>(tiles_of(a.rows)));
+    if (a.vec) fp8_quantize_kernel<kT, kMode, kSums, true><<<grid, 32 * q_warps<kT>(), 0, st>>>(a);
+    else fp8_quantize_kernel<kT, kMode, kSums, false><<<grid, 32 * q_warps<kT>(), 0, st>>>(a);
+  };
+  using Rows = std::integral_constant<int, BWD_FP8_ROWS>;
+  using Cols = std::integral_constant<int, BWD_FP8_COLS>;
+  using Both = std::integral_constant<int, BWD_FP8_ROWS | BWD_FP8_COLS>;
+  if (mode == BWD_FP8_ROWS) launch(Rows{}, std::false_type{});
+  else if (mode == BWD_FP8_TILES) launch(std::integral_constant<int, BWD_FP8_TILES>{}, std::false_type{});
+  else if (mode == BWD_FP8_COLS) a.col_sums ? launch(Cols{}, std::true_type{}) : launch(Cols{}, std::false_type{});
+  else a.col_sums ? launch(Both{}, std::true_type{}) : launch(Both{}, std::false_type{});
   return check_launch("fp8_quantize_kernel launch");
 }
 
@@ -851,7 +947,7 @@ bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_
     a.groups_r = groups_of(cols); a.groups_c = groups_of(rows);
     a.codes_r = row_codes; a.scales_r = row_scales; a.codes_c = col_codes; a.scales_c = col_scales;
     a.col_sums = col_sums ? col_sums_work : nullptr;
-    a.vec = ld % 4 == 0 && aligned_to(x, 4 * eb);
+    a.vec = ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x);
     s = dtype == BWD_F32 ? launch_quantize<kF32>(blocks, a, st) : dtype == BWD_BF16 ? launch_quantize<kBF16>(blocks, a, st)
                                                                                    : launch_quantize<kF16>(blocks, a, st);
   }
