@@ -48,6 +48,8 @@ constexpr int kF32 = BWD_F32, kBF16 = BWD_BF16, kF16 = BWD_F16;
 template <int kT>
 __host__ __device__ constexpr int elem_bytes() { return kT == kF32 ? 4 : 2; }
 
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
 // Byte of (row r, block kb) in a scale array whose rows have `groups` groups
 // of four blocks.
 __device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t kb, int64_t groups) {
@@ -97,6 +99,11 @@ __device__ __forceinline__ uint32_t max_words(uint32_t a, uint32_t b) { return k
 template <int kT>
 __device__ __forceinline__ uint32_t magnitude(uint32_t w) { return w & (kT == kF32 ? 0x7fffffffu : 0x7fff7fffu); }
 
+template <int kT>
+__device__ __forceinline__ uint32_t max_piece(const uint4& w) {
+  return max_words<kT>(max_words<kT>(magnitude<kT>(w.x), magnitude<kT>(w.y)), max_words<kT>(magnitude<kT>(w.z), magnitude<kT>(w.w)));
+}
+
 // fp32 bits of a magnitude given by its own type's bits.
 template <int kT>
 __device__ __forceinline__ uint32_t widen_bits(uint32_t b) {
@@ -140,7 +147,7 @@ constexpr int kQPieces = 8;
 template <int kT> __host__ __device__ constexpr int q_warps() { return kTile / kQPieces / q_rows<kT>(); }
 
 template <int kT, int kMode, bool kSums, bool kVec>
-__global__ void __launch_bounds__(32 * q_warps<kT>(), 32 / q_warps<kT>())
+__global__ void __launch_bounds__(32 * q_warps<kT>(), kT == kF32 ? 2 : 5)
 fp8_quantize_kernel(const QuantArgs a) {
   constexpr bool kRows = kMode & BWD_FP8_ROWS, kCols = kMode & BWD_FP8_COLS, kTiles = kMode & BWD_FP8_TILES;
   constexpr int kVals = q_vals<kT>(), kLanes = q_lanes<kT>(), kPerLoad = q_rows<kT>(), kWarps = q_warps<kT>();
@@ -155,7 +162,7 @@ fp8_quantize_kernel(const QuantArgs a) {
   const int rows_here = a.rows - r0 < kTile ? static_cast<int>(a.rows - r0) : kTile;
   const char* const src0 = static_cast<const char*>(a.x) + ((r0 + row) * a.ld + c) * elem_bytes<kT>();
   const int64_t src_step = a.ld * (kTile / kQPieces) * elem_bytes<kT>();
-  const auto load = [&](int i) {
+  const auto fetch = [&](int i) {
     const char* const src = src0 + i * src_step;
     uint4 w = make_uint4(0u, 0u, 0u, 0u);
     const bool in = row + i * (kTile / kQPieces) < rows_here;
@@ -171,9 +178,27 @@ fp8_quantize_kernel(const QuantArgs a) {
     }
     return w;
   };
-  uint4 x[kQPieces];
+  // 16-bit pieces wait in shared memory, each thread's own; fp32 ones, which
+  // hold half as many values, in registers.
+  constexpr bool kStaged = kT != kF32;
+  __shared__ __align__(16) uint4 s_x[kStaged ? kQPieces : 1][kStaged ? 32 * kWarps : 1];
+  uint4 x[kStaged ? 1 : kQPieces];
 #pragma unroll
-  for (int i = 0; i < kQPieces; ++i) x[i] = load(i);
+  for (int i = 0; i < kQPieces; ++i) {
+    if constexpr (!kStaged) x[i] = fetch(i);
+    else if constexpr (!kVec) s_x[i][threadIdx.x] = fetch(i);
+    else {
+      const bool in = row + i * (kTile / kQPieces) < rows_here && c < a.cols;
+      // copies nothing and fills with zeros past the edge
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   ::"r"(smem_u32(&s_x[i][threadIdx.x])), "l"(in ? src0 + i * src_step : src0), "r"(in ? 16u : 0u) : "memory");
+    }
+  }
+  if constexpr (kStaged && kVec) asm volatile("cp.async.wait_all;" ::: "memory");
+  const auto load = [&](int i) {
+    if constexpr (kStaged) return s_x[i][threadIdx.x];
+    else return x[i];
+  };
 
   // Codes of piece i; the pitch is a multiple of 16, so a piece's codes lie
   // before it or past it.
@@ -196,8 +221,9 @@ fp8_quantize_kernel(const QuantArgs a) {
     uint4 top = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int i = 0; i < kQPieces; ++i) {
-      top.x = max_words<kT>(top.x, magnitude<kT>(x[i].x)); top.y = max_words<kT>(top.y, magnitude<kT>(x[i].y));
-      top.z = max_words<kT>(top.z, magnitude<kT>(x[i].z)); top.w = max_words<kT>(top.w, magnitude<kT>(x[i].w));
+      const uint4 w = load(i);
+      top.x = max_words<kT>(top.x, magnitude<kT>(w.x)); top.y = max_words<kT>(top.y, magnitude<kT>(w.y));
+      top.z = max_words<kT>(top.z, magnitude<kT>(w.z)); top.w = max_words<kT>(top.w, magnitude<kT>(w.w));
     }
     if (kPerLoad == 2) {
       top.x = max_words<kT>(top.x, __shfl_xor_sync(0xffffffffu, top.x, 16)); top.y = max_words<kT>(top.y, __shfl_xor_sync(0xffffffffu, top.y, 16));
@@ -207,41 +233,46 @@ fp8_quantize_kernel(const QuantArgs a) {
   } else if constexpr (kTiles) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kQPieces; ++i)
-      top = max_words<kT>(top, max_words<kT>(max_words<kT>(magnitude<kT>(x[i].x), magnitude<kT>(x[i].y)),
-                                             max_words<kT>(magnitude<kT>(x[i].z), magnitude<kT>(x[i].w))));
+    for (int i = 0; i < kQPieces; ++i) top = max_words<kT>(top, max_piece<kT>(load(i)));
     if (kT != kF32) top = max(top & 0xffffu, top >> 16);
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) s_tile[warp] = top;
   }
   if constexpr (kRows) {
-    uint32_t top[kQPieces];
+    // two rows at a time, whose 16-bit maxima share a word; fp32 pieces, in
+    // registers anyway, all at once where no other form needs some
+    constexpr int kStep = kT == kF32 && !kCols ? kQPieces : 2;
+#pragma unroll (kStaged ? 1 : kQPieces / kStep)
+    for (int i = 0; i < kQPieces; i += kStep) {
+      uint4 w[kStep];
+      uint32_t top[kStep];
 #pragma unroll
-    for (int i = 0; i < kQPieces; ++i)
-      top[i] = max_words<kT>(max_words<kT>(magnitude<kT>(x[i].x), magnitude<kT>(x[i].y)),
-                             max_words<kT>(magnitude<kT>(x[i].z), magnitude<kT>(x[i].w)));
-    if constexpr (kT == kF32) {
-#pragma unroll
-      for (int i = 0; i < kQPieces; ++i) top[i] = __reduce_max_sync(0xffffffffu, top[i]);
-    } else {
-      // two rows to a word, reduced over the row's sixteen lanes
-#pragma unroll
-      for (int i = 0; i < kQPieces; i += 2) {
-        uint32_t both = __vmaxu2(__byte_perm(top[i], top[i + 1], 0x5410), __byte_perm(top[i], top[i + 1], 0x7632));
-#pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
-        top[i] = both & 0xffffu;
-        top[i + 1] = both >> 16;
+      for (int h = 0; h < kStep; ++h) {
+        w[h] = load(i + h);
+        top[h] = max_piece<kT>(w[h]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kQPieces; ++i) {
-      const uint32_t b = scale_byte(widen_bits<kT>(top[i]));
-      if (part == 0) s_byte[row + i * (kTile / kQPieces)] = static_cast<uint8_t>(b);
-      float inv[kVals];
+      for (int h = 0; h < kStep; h += 2) {
+        if constexpr (kT == kF32) {
+          top[h] = __reduce_max_sync(0xffffffffu, top[h]);
+          top[h + 1] = __reduce_max_sync(0xffffffffu, top[h + 1]);
+        } else {
+          uint32_t both = __vmaxu2(__byte_perm(top[h], top[h + 1], 0x5410), __byte_perm(top[h], top[h + 1], 0x7632));
 #pragma unroll
-      for (int j = 0; j < kVals; ++j) inv[j] = inv_scale(b);
-      put(a.codes_r + at, i, x[i], inv);
+          for (int o = kLanes / 2; o > 0; o >>= 1) both = __vmaxu2(both, __shfl_xor_sync(0xffffffffu, both, o));
+          top[h] = both & 0xffffu;
+          top[h + 1] = both >> 16;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < kStep; ++h) {
+        const uint32_t b = scale_byte(widen_bits<kT>(top[h]));
+        if (part == 0) s_byte[row + (i + h) * (kTile / kQPieces)] = static_cast<uint8_t>(b);
+        float inv[kVals];
+#pragma unroll
+        for (int j = 0; j < kVals; ++j) inv[j] = inv_scale(b);
+        put(a.codes_r + at, i + h, w[h], inv);
+      }
     }
   }
   __syncthreads();
@@ -263,15 +294,10 @@ fp8_quantize_kernel(const QuantArgs a) {
       inv[j] = inv_scale(b);
       if (warp == 0 && lane < kLanes) a.scales_c[scale_offset(c + j, blockIdx.y, a.groups_c)] = static_cast<uint8_t>(b);
     }
-    // With both forms of 16-bit values the tile is read again, from L1: held
-    // in registers over the first form's codes it spilled (8192 x 11008: 82 us
-    // against 75).  fp32 pieces hold half as many values and stay (101 us
-    // against 138).
-    constexpr bool kAgain = kRows && kT != kF32;
     float sum[kVals] = {};
-#pragma unroll
+#pragma unroll (kStaged ? 2 : kQPieces)
     for (int i = 0; i < kQPieces; ++i) {
-      const uint4 w = kAgain ? load(i) : x[i];
+      const uint4 w = load(i);
       put(a.codes_c + at, i, w, inv);
       if constexpr (kSums) {
 #pragma unroll
@@ -298,7 +324,7 @@ fp8_quantize_kernel(const QuantArgs a) {
 #pragma unroll
     for (int j = 0; j < kVals; ++j) inv[j] = inv_scale(b);
 #pragma unroll
-    for (int i = 0; i < kQPieces; ++i) put(a.codes_r + at, i, x[i], inv);
+    for (int i = 0; i < kQPieces; ++i) put(a.codes_r + at, i, load(i), inv);
   }
   if constexpr (kSums) {
     if (threadIdx.x < kTile && c0 + threadIdx.x < a.cols) {
@@ -326,14 +352,27 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// Column sums from the quantizer's partial sums, in the order of the rows.
+// Column sums from the quantizer's partial sums, one for each tile of rows:
+// eight warps of a CTA each add every eighth of a column's, in order, and the
+// first then adds the eight.
+constexpr int kSumWarps = 8;
+
 template <int kT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kSumWarps)
 col_sums_kernel(const float* __restrict__ partial, int64_t tiles, int64_t cols, void* __restrict__ out) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (c >= cols) return;
+  __shared__ float s_part[kSumWarps][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
-  for (int64_t t = 0; t < tiles; ++t) s += partial[t * cols + c];
+  if (c < cols) {
+#pragma unroll 8
+    for (int64_t t = warp; t < tiles; t += kSumWarps) s += partial[t * cols + c];
+  }
+  s_part[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || c >= cols) return;
+#pragma unroll
+  for (int w = 1; w < kSumWarps; ++w) s += s_part[w][lane];
   store1<kT>(out, c, s);
 }
 
@@ -361,8 +400,6 @@ fp8_dequantize_kernel(const uint8_t* __restrict__ codes, int64_t pitch, const ui
 // matrix product
 
 __device__ unsigned int g_fp8_fault;  // set when a bounded wait gives up
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
@@ -952,11 +989,11 @@ bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_
                                                                                    : launch_quantize<kF16>(blocks, a, st);
   }
   if (s == BWD_OK && col_sums) {
-    const unsigned grid = static_cast<unsigned>((cols + 255) / 256);
+    const unsigned grid = static_cast<unsigned>((cols + 31) / 32);
     const int64_t tiles = tiles_of(rows);
-    if (dtype == BWD_F32) col_sums_kernel<kF32><<<grid, 256, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else if (dtype == BWD_BF16) col_sums_kernel<kBF16><<<grid, 256, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else col_sums_kernel<kF16><<<grid, 256, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    if (dtype == BWD_F32) col_sums_kernel<kF32><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    else if (dtype == BWD_BF16) col_sums_kernel<kBF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    else col_sums_kernel<kF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
     s = check_launch("col_sums_kernel launch");
   }
   return s;
