@@ -86,6 +86,12 @@ _SIGNATURES = {
     "bwd_fp8_dequantize": (_int, [_vp, _vp, _i32, _i64, _i64, _vp, _int, _vp]),
     "bwd_fp8_matmul": (
         _int, [_i64, _i64, _i64, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _i64, _int, _vp]),
+    "bwd_fp8_linear_work_bytes": (_i64, [_i64, _i64]),
+    "bwd_fp8_linear": (
+        _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp]),
+    "bwd_fp8_linear_backward_work_bytes": (_i64, [_i64, _i64]),
+    "bwd_fp8_linear_backward": (
+        _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
     "bwd_check_device": (_int, [_vp]),
     "bwd_selftest_bounded_wait": (_int, [_vp]),
     "bwd_status_string": (ctypes.c_char_p, [_int]),

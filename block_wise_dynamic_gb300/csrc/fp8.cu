@@ -155,6 +155,8 @@ fp8_quantize_kernel(const QuantArgs a) {
   __shared__ __align__(16) float s_sum[kSums ? kWarps : 1][kTile];
   __shared__ uint32_t s_tile[kWarps];
   __shared__ uint8_t s_byte[kTile];
+  // a product launched to follow may set itself up meanwhile
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % kLanes;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile, c0 = static_cast<int64_t>(blockIdx.x) * kTile;
   const int64_t c = c0 + kVals * part;
@@ -440,6 +442,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   return mbar_try(bar, parity) || mbar_wait_slow(bar, parity, fail_flag);
 }
 
+// After a failed wait, copies and products may still be under way: leaves
+// them two milliseconds before the memory they use goes away.
+__device__ __noinline__ void let_copies_land() {
+  uint64_t t0, t1;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+  for (int i = 0; i < (1 << 20); ++i) {
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
+    if (t1 - t0 > 2000000ull) break;
+  }
+}
+
 // Address of a barrier of this CTA in the shared memory of the pair's first
 // CTA, which issues the products for both.
 __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
@@ -447,6 +460,9 @@ __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
   return r;
 }
+// Where the launch was allowed to begin before the kernel ahead of it (the
+// quantizer of its operand) has ended: waits for that kernel's results.
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -578,6 +594,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
   if (warp == 0) {
     if (lane == 0) {
+      wait_for_inputs();
       int it = 0;
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs) {
@@ -754,20 +771,204 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
-  // After a failed wait, copies and products may still be under way: leave
-  // them two milliseconds before the memory they use goes away.
-  if (s_fail && lane == 0 && warp < 2) {
-    uint64_t t0, t1;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-    for (int i = 0; i < (1 << 20); ++i) {
-      asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
-      if (t1 - t0 > 2000000ull) break;
-    }
-  }
+  if (s_fail && lane == 0 && warp < 2) let_copies_land();
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   cluster_sync();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// --------------------------------------------------------------------------
+// product with few rows
+//
+// For few lines of A (tokens) the roles change: the 128 rows of the matrix
+// instruction are lines of B (the weight's outputs) and its columns the few
+// lines of A, so no product is wasted on rows that are not there.  Such a
+// product is bound by reading B once, and a cluster of `split` CTAs divides
+// the summed axis, so that all SMs read.  Each CTA keeps its part's sums in
+// its tensor memory; at the end CTA r gathers, from all of the cluster over
+// distributed shared memory, the r-th share of the columns and adds the parts
+// in the order of the ranks.
+
+template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 64 ? 3 : kBN == 16 ? 5 : 4; }
+template <int kBN> __host__ __device__ constexpr int few_stage_bytes() { return kTile * kBK + kBN * kBK; }
+// stages, their scales, and the gathered parts: kBN columns of 128 fp32 sums
+template <int kBN> __host__ __device__ constexpr int few_smem() {
+  return 1024 + few_stages<kBN>() * (few_stage_bytes<kBN>() + 2 * kSfTile) + (kBN + 8) * kTile * 4;
+}
+// Up to 64 columns two CTAs share an SM and its tensor memory.  Accumulators
+// that fit beside the scales: sums move on to the next after kChunk blocks,
+// or later where that would take more of them.
+template <int kBN> __host__ __device__ constexpr int few_ctas() { return kBN == 128 ? 1 : 2; }
+template <int kBN> __host__ __device__ constexpr uint32_t few_tmem() { return kTmemCols / few_ctas<kBN>(); }
+template <int kBN> __host__ __device__ constexpr int few_accs() { return static_cast<int>(few_tmem<kBN>() - 16) / kBN; }
+
+__device__ __forceinline__ void tma_load_one(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void commit_one(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+struct FewArgs {
+  const void* bias;
+  void* out;
+  int64_t ldo;
+  int m, n, k;           // lines of A (columns here), lines of B (rows here), summed axis
+  int a_trans, b_trans;
+  int split;             // CTAs of a cluster, along the summed axis
+};
+
+// map_w: lines of B in boxes of 128; map_x: lines of A in boxes of kBN.  A
+// grid with several tiles of A's lines, or A transposed, needs kBN 128 (the
+// scales' tiles hold 128 lines).
+template <int kT, int kBN>
+__global__ void __launch_bounds__(kMmThreads, 1)
+fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_sfw, const __grid_constant__ CUtensorMap map_sfx, const FewArgs p) {
+  constexpr int kStages = few_stages<kBN>(), kW = kTile * kBK, kStage = few_stage_bytes<kBN>();
+  constexpr uint32_t kCols = few_tmem<kBN>(), kSfCol = kCols - 16;
+  constexpr int kAccs = few_accs<kBN>();
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* const sf = sm + kStages * kStage;
+  float* const parts = reinterpret_cast<float*>(sf + kStages * 2 * kSfTile);  // [rank][column of the share][128]
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t rank;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+  if (threadIdx.x == 0) {
+    s_fail = 0;
+    for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+    mbar_init(&s_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  cluster_sync();  // every CTA of the cluster runs before another writes to it
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
+  const int n0 = static_cast<int>(blockIdx.x) / p.split * kTile, m0 = static_cast<int>(blockIdx.y) * kBN;
+  // this CTA's blocks of the summed axis, and its accumulators' share of them
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / p.split);
+  const int least = (kb1 - kb0 + kAccs - 1) / kAccs, chunk = least > kChunk ? least : kChunk;
+  const int accs = (kb1 - kb0 + chunk - 1) / chunk;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const auto weight = [&](int kb, int s) {
+        uint8_t* const w = sm + s * kStage;
+        if (p.b_trans) tma_load_one(w, &map_w, n0, kb * kBK, &s_full[s]); else tma_load_one(w, &map_w, kb * kBK, n0, &s_full[s]);
+      };
+      // the first stages' weights do not depend on the kernel ahead
+      const int ahead = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
+      for (int i = 0; i < ahead; ++i) {
+        mbar_expect_tx(&s_full[i], kStage + (i == 0 || ((kb0 + i) & 3) == 0 ? 2 * kSfTile : 0));
+        weight(kb0 + i, i);
+      }
+      wait_for_inputs();
+      for (int i = 0; i < kb1 - kb0; ++i) {
+        const int s = i % kStages, kb = kb0 + i;
+        const bool scales = i == 0 || (kb & 3) == 0;
+        if (i >= ahead) {
+          if (!mbar_wait(&s_empty[s], ((i / kStages) & 1) ^ 1, &s_fail)) break;
+          mbar_expect_tx(&s_full[s], kStage + (scales ? 2 * kSfTile : 0));
+          weight(kb, s);
+        }
+        uint8_t* const x = sm + s * kStage + kW;
+        if (p.a_trans) tma_load_one(x, &map_x, m0, kb * kBK, &s_full[s]); else tma_load_one(x, &map_x, kb * kBK, m0, &s_full[s]);
+        if (scales) {
+          tma_load_one(sf + s * 2 * kSfTile, &map_sfw, 0, n0 / 128 * groups + kb / 4, &s_full[s]);
+          tma_load_one(sf + s * 2 * kSfTile + kSfTile, &map_sfx, 0, m0 / 128 * groups + kb / 4, &s_full[s]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = (static_cast<uint32_t>(p.b_trans) << 15) | (static_cast<uint32_t>(p.a_trans) << 16) |
+                             ((kBN / 8) << 17) | (1u << 23) | ((kTile / 16) << 24);
+      const uint64_t desc = smem_desc(0, 16, 1024, 2);
+      const uint32_t sw = p.b_trans ? 4096 / 16 : 32 / 16, sx = p.a_trans ? 4096 / 16 : 32 / 16;
+      bool ok = true;
+      for (int i = 0; ok && i < kb1 - kb0; ++i) {
+        const int s = i % kStages, kb = kb0 + i;
+        if (!(ok = mbar_wait(&s_full[s], (i / kStages) & 1, &s_fail))) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t w = smem_u32(sm + s * kStage), x = w + kW;
+        const uint32_t tsf = tmem + kSfCol + 8 * ((kb >> 2) & 1);
+        if (i == 0 || (kb & 3) == 0) {
+          const uint32_t d = smem_u32(sf + s * 2 * kSfTile);
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf), "l"(smem_desc(d, 16, 128, 0)) : "memory");
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4), "l"(smem_desc(d + kSfTile, 16, 128, 0)) : "memory");
+        }
+        const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+#pragma unroll
+        for (uint32_t q = 0; q < 4; ++q)
+          asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+                       "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                       ::"r"(tmem + (i / chunk) * kBN), "l"(desc + (w >> 4) + q * sw), "l"(desc + (x >> 4) + q * sx), "r"(id), "r"(tsf), "r"(tsf + 4),
+                       "r"(static_cast<uint32_t>(i % chunk != 0 || q != 0)) : "memory");
+        commit_one(&s_empty[s]);
+      }
+      commit_one(&s_done);
+    }
+  }
+  __syncwarp();
+  const int quarter = warp & 3, share = (kBN + p.split - 1) / p.split;  // columns that a CTA gathers
+  bool ok = true;
+  if (warp >= 2) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&s_done, 0, &s_fail));
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    const int row = quarter * 32 + lane;
+#pragma unroll
+    for (int c = 0; c < kBN; c += 16) {
+      float sum[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) sum[u] = 0.0f;
+      for (int a = 0; a < accs; ++a) {
+        uint32_t r[16];
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                       "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                     : "r"(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + a * kBN + c));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < 16; ++u) sum[u] = __fadd_rn(sum[u], __uint_as_float(r[u]));
+      }
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        const int to = (c + u) / share, at = (static_cast<int>(rank) * share + (c + u) % share) * kTile + row;
+        uint32_t dst;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + at)), "r"(to));
+        if (m0 + c + u < p.m) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(sum[u]) : "memory");
+      }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  if (s_fail && lane == 0 && warp < 2) let_copies_land();
+  __syncwarp();
+  cluster_sync();
+  if (warp >= 2) {
+    const int row = quarter * 32 + lane;
+    const float bias = p.bias && n0 + row < p.n ? load1<kT>(p.bias, n0 + row) : 0.0f;
+    for (int c = 0; c < share; ++c) {
+      const int m = m0 + static_cast<int>(rank) * share + c;
+      if (static_cast<int>(rank) * share + c >= kBN || m >= p.m || n0 + row >= p.n || !ok) break;
+      float sum = parts[c * kTile + row];
+      for (int r = 1; r < p.split; ++r) sum = __fadd_rn(sum, parts[(r * share + c) * kTile + row]);
+      store1<kT>(p.out, m * p.ldo + n0 + row, p.bias ? __fadd_rn(sum, bias) : sum);
+    }
+  }
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
 }
 
 // A product over nothing: the bias, or zero.
@@ -860,14 +1061,24 @@ constexpr int kMaxDevices = 64;
 struct DeviceState {
   bool ready = false;
   unsigned long long ctx = 0;
+  int sms = 0;
   int pairs = 0;  // CTA pairs that are resident at a time
 };
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 
-template <int kT, int kBN, bool kSum>
-cudaError_t opt_in() {
-  return cudaFuncSetAttribute(fp8_matmul_kernel<kT, kBN, kSum>, cudaFuncAttributeMaxDynamicSharedMemorySize, mm_smem<kBN>());
+template <typename F>
+cudaError_t opt_in(F* kernel, int smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+template <int kT>
+cudaError_t opt_in_few() {
+  cudaError_t e = opt_in(fp8_matmul_few_kernel<kT, 16>, few_smem<16>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 32>, few_smem<32>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 64>, few_smem<64>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 128>, few_smem<128>());
+  return e;
 }
 
 bwd_status ensure_device(const DeviceState** out) {
@@ -882,16 +1093,18 @@ bwd_status ensure_device(const DeviceState** out) {
   DeviceState& d = g_dev[dev];
   *out = &d;
   if (d.ready && d.ctx == ctx) return BWD_OK;
-  int sms = 0;
-  e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = opt_in<kF32, 128, true>();
-  if (e == cudaSuccess) e = opt_in<kBF16, 256, false>();
-  if (e == cudaSuccess) e = opt_in<kF16, 256, false>();
-  if (e == cudaSuccess) e = opt_in<kBF16, 128, false>();
-  if (e == cudaSuccess) e = opt_in<kF16, 128, false>();
+  e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 128, true>, mm_smem<128>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false>, mm_smem<256>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false>, mm_smem<256>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 128, false>, mm_smem<128>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 128, false>, mm_smem<128>());
+  if (e == cudaSuccess) e = opt_in_few<kF32>();
+  if (e == cudaSuccess) e = opt_in_few<kBF16>();
+  if (e == cudaSuccess) e = opt_in_few<kF16>();
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
+  cfg.gridDim = dim3(static_cast<unsigned>(d.sms / 2 * 2));
   cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = mm_smem<256>();
   cudaLaunchAttribute attr[1];
@@ -911,20 +1124,187 @@ struct MmMaps {
   CUtensorMap a, b, sfa, sfb, out;
 };
 
+// One product's operands: codes and scales of `lines` lines of k elements.
+struct Lines {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t lines;
+  int trans;
+};
+
+// `early`: the launch may begin before the kernel ahead of it has ended.
+template <typename... Params, typename... Args>
+bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int cluster, int smem, bool early, cudaStream_t st, const char* what,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kMmThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n++].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  }
+  if (early) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = static_cast<unsigned>(n);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? BWD_OK : cuda_fail(e, what);
+}
+
 template <int kT, int kBN, bool kSum>
-bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
+bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, bool early, cudaStream_t st) {
   const int tiles = p.tiles_m * p.tiles_n;
-  fp8_matmul_kernel<kT, kBN, kSum><<<2 * (tiles < pairs ? tiles : pairs), kMmThreads, mm_smem<kBN>(), st>>>(
-      maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
-  return check_launch("fp8_matmul_kernel launch");
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), 0, mm_smem<kBN>(), early, st,
+                   "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
+}
+
+template <int kT, int kBN>
+bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool early, cudaStream_t st) {
+  MmMaps maps;
+  bwd_status s;
+  if ((s = code_map(&maps.b, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
+  if ((s = code_map(&maps.a, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfb, w.scales, tiles_of(w.lines) * groups_of(p.k))) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfa, x.scales, tiles_of(x.lines) * groups_of(p.k))) != BWD_OK) return s;
+  const int64_t tiles_n = tiles_of(p.n), tiles_m = (p.m + kBN - 1) / kBN, blocks = tiles_of(p.k);
+  // as many parts of the summed axis as the device has room for at once, of two blocks each at least
+  int64_t split = sms * few_ctas<kBN>() / (tiles_n * tiles_m);
+  split = split > 8 ? 8 : split;
+  split = split > blocks / 2 ? blocks / 2 : split;
+  p.split = static_cast<int>(split < 1 ? 1 : split);
+  return launch_ex(fp8_matmul_few_kernel<kT, kBN>, dim3(static_cast<unsigned>(tiles_n * p.split), static_cast<unsigned>(tiles_m)), p.split,
+                   few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", maps.b, maps.a, maps.sfb, maps.sfa, p);
 }
 
 template <int kT>
-bwd_status launch_fill(const MmArgs& p, cudaStream_t st) {
-  const int64_t need = (static_cast<int64_t>(p.m) * p.n + 255) / 256;
-  fill_rows_kernel<kT><<<static_cast<unsigned>(need < 1216 ? need : 1216), 256, 0, st>>>(p.bias, p.out, p.ldo, p.m, p.n);
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, int sms, bool early, cudaStream_t st) {
+  if (x.trans || p.m > 64) return launch_few<kT, 128>(x, w, p, sms, early, st);
+  if (p.m > 32) return launch_few<kT, 64>(x, w, p, sms, early, st);
+  if (p.m > 16) return launch_few<kT, 32>(x, w, p, sms, early, st);
+  return launch_few<kT, 16>(x, w, p, sms, early, st);
+}
+
+// Whether a product goes to the kernel for few lines of A.
+bool use_few(int64_t m, int64_t n, int64_t k, int pairs) {
+  (void)n; (void)k; (void)pairs;
+  return m <= 128;
+}
+
+// out = A B^T + bias, k > 0.
+bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, bool early,
+                  cudaStream_t st) {
+  const int64_t m = a.lines, n = b.lines;
+  const int eb = dtype == BWD_F32 ? 4 : 2;
+  const DeviceState* d = nullptr;
+  bwd_status s = ensure_device(&d);
+  if (s != BWD_OK) return s;
+  if (use_few(m, n, k, d->pairs)) {
+    const FewArgs p{bias, out, ldo, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
+    if (dtype == BWD_F32) return few<kF32>(a, b, p, d->sms, early, st);
+    if (dtype == BWD_BF16) return few<kBF16>(a, b, p, d->sms, early, st);
+    return few<kF16>(a, b, p, d->sms, early, st);
+  }
+  const int64_t tiles_m = (m + kBM - 1) / kBM;
+  // 256 columns unless tiles of 128 are needed to give every pair one
+  const int bn = dtype == BWD_F32 || tiles_m * ((n + 255) / 256) < d->pairs ? 128 : 256;
+  const int64_t tiles_n = (n + bn - 1) / bn;
+  if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
+    return fail(BWD_ERR_INVALID_ARG, "too many tiles");
+  MmArgs p{};
+  p.bias = bias; p.out = out; p.ldo = ldo;
+  p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
+  p.a_trans = a.trans; p.b_trans = b.trans;
+  p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
+  p.sf_rows_b = static_cast<int>(tiles_of(n));
+  p.store = aligned16(out) && ldo * eb % 16 == 0;
+  MmMaps maps{};
+  if ((s = code_map(&maps.a, a.codes, m, k, a.trans, kBM / 2)) != BWD_OK) return s;
+  if ((s = code_map(&maps.b, b.codes, n, k, b.trans, bn / 2)) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfa, a.scales, tiles_of(m) * groups_of(k))) != BWD_OK) return s;
+  if ((s = scale_map(&maps.sfb, b.scales, tiles_of(n) * groups_of(k))) != BWD_OK) return s;
+  if (p.store) {
+    const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
+  }
+  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, early, st);
+  if (dtype == BWD_BF16)
+    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, early, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, early, st);
+  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, early, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, early, st);
+}
+
+// The bias, or zero: a product over nothing.
+bwd_status fill(int64_t m, int64_t n, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, cudaStream_t st) {
+  const int64_t need = (m * n + 255) / 256;
+  const unsigned grid = static_cast<unsigned>(need < 1216 ? need : 1216);
+  if (dtype == BWD_F32) fill_rows_kernel<kF32><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
+  else if (dtype == BWD_BF16) fill_rows_kernel<kBF16><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
+  else fill_rows_kernel<kF16><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
   return check_launch("fill_rows_kernel launch");
 }
+
+bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, bool early,
+                   cudaStream_t st) {
+  if (a.lines == 0 || b.lines == 0) return BWD_OK;
+  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, early, st);
+}
+
+// Checks of a matrix that is quantized.
+bwd_status check_matrix(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld) {
+  if (!valid_type(dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return fail(BWD_ERR_INVALID_ARG, "bad size");
+  if (tiles_of(rows) > 65535) return fail(BWD_ERR_INVALID_ARG, "more than 65535 * 128 rows");
+  if (ld < cols) return fail(BWD_ERR_INVALID_ARG, "ld is less than cols");
+  if (rows > 0 && cols > 0) {
+    if (!x) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+    if (!aligned_to(x, dtype == BWD_F32 ? 4 : 2)) return fail(BWD_ERR_INVALID_ARG, "x is not aligned to its element size");
+  }
+  return BWD_OK;
+}
+
+// Quantizes, and finishes the column sums where they are asked for.
+bwd_status quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld, int blocks, uint8_t* row_codes,
+                    uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales, void* col_sums, float* col_sums_work, cudaStream_t st) {
+  const int eb = dtype == BWD_F32 ? 4 : 2;
+  bwd_status s = BWD_OK;
+  if (rows > 0 && cols > 0) {
+    QuantArgs a{};
+    a.x = x; a.rows = rows; a.cols = cols; a.ld = ld;
+    a.pitch = bwd_fp8_pitch(cols);
+    a.groups_r = groups_of(cols); a.groups_c = groups_of(rows);
+    a.codes_r = row_codes; a.scales_r = row_scales; a.codes_c = col_codes; a.scales_c = col_scales;
+    a.col_sums = col_sums ? col_sums_work : nullptr;
+    a.vec = ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x);
+    s = dtype == BWD_F32 ? launch_quantize<kF32>(blocks, a, st) : dtype == BWD_BF16 ? launch_quantize<kBF16>(blocks, a, st)
+                                                                                   : launch_quantize<kF16>(blocks, a, st);
+  }
+  if (s == BWD_OK && col_sums && cols > 0) {
+    const unsigned grid = static_cast<unsigned>((cols + 31) / 32);
+    const int64_t tiles = tiles_of(rows);
+    if (dtype == BWD_F32) col_sums_kernel<kF32><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    else if (dtype == BWD_BF16) col_sums_kernel<kBF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    else col_sums_kernel<kF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
+    s = check_launch("col_sums_kernel launch");
+  }
+  return s;
+}
+
+// Divides a workspace into 256-byte aligned pieces.
+struct Pieces {
+  uint8_t* at;
+  int64_t used = 0;
+  uint8_t* take(int64_t bytes) {
+    uint8_t* const p = at ? at + used : nullptr;
+    used += (bytes + 255) / 256 * 256;
+    return p;
+  }
+};
 
 }  // namespace
 
@@ -955,48 +1335,23 @@ int64_t bwd_fp8_pitch(int64_t cols) { return cols < 0 || cols > kMaxDim ? -1 : (
 bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld, int32_t blocks,
                             uint8_t* row_codes, uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales,
                             void* col_sums, float* col_sums_work, void* stream) {
-  if (!valid_type(dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "dtype %d", (int)dtype);
+  const bwd_status s = check_matrix(x, dtype, rows, cols, ld);
+  if (s != BWD_OK) return s;
   if (blocks != BWD_FP8_ROWS && blocks != BWD_FP8_COLS && blocks != BWD_FP8_TILES && blocks != (BWD_FP8_ROWS | BWD_FP8_COLS))
     return fail(BWD_ERR_INVALID_ARG, "bad block set %d", blocks);
-  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return fail(BWD_ERR_INVALID_ARG, "bad size");
-  if (tiles_of(rows) > 65535) return fail(BWD_ERR_INVALID_ARG, "more than 65535 * 128 rows");
-  if (ld < cols) return fail(BWD_ERR_INVALID_ARG, "ld is less than cols");
   if (col_sums && !(blocks & BWD_FP8_COLS)) return fail(BWD_ERR_INVALID_ARG, "column sums need blocks along the columns");
   if (cols == 0 || (rows == 0 && !col_sums)) return BWD_OK;
-  const int eb = dtype == BWD_F32 ? 4 : 2;
   if (rows > 0) {
-    if (!x) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
-    if (!aligned_to(x, eb)) return fail(BWD_ERR_INVALID_ARG, "x is not aligned to its element size");
     const bool r = blocks & (BWD_FP8_ROWS | BWD_FP8_TILES), c = blocks & BWD_FP8_COLS;
     if ((r && (!row_codes || !row_scales)) || (c && !col_codes) || ((c || blocks == BWD_FP8_TILES) && !col_scales))
       return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
     if ((r && !aligned16(row_codes)) || (c && !aligned16(col_codes)))
       return fail(BWD_ERR_INVALID_ARG, "codes must be 16-byte aligned");
   }
-  if (col_sums && (!col_sums_work || !aligned_to(col_sums, eb) || !aligned_to(col_sums_work, 4)))
+  if (col_sums && (!col_sums_work || !aligned_to(col_sums, dtype == BWD_F32 ? 4 : 2) || !aligned_to(col_sums_work, 4)))
     return fail(BWD_ERR_INVALID_ARG, "column sums need a workspace, both aligned to their element size");
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  bwd_status s = BWD_OK;
-  if (rows > 0) {
-    QuantArgs a{};
-    a.x = x; a.rows = rows; a.cols = cols; a.ld = ld;
-    a.pitch = bwd_fp8_pitch(cols);
-    a.groups_r = groups_of(cols); a.groups_c = groups_of(rows);
-    a.codes_r = row_codes; a.scales_r = row_scales; a.codes_c = col_codes; a.scales_c = col_scales;
-    a.col_sums = col_sums ? col_sums_work : nullptr;
-    a.vec = ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x);
-    s = dtype == BWD_F32 ? launch_quantize<kF32>(blocks, a, st) : dtype == BWD_BF16 ? launch_quantize<kBF16>(blocks, a, st)
-                                                                                   : launch_quantize<kF16>(blocks, a, st);
-  }
-  if (s == BWD_OK && col_sums) {
-    const unsigned grid = static_cast<unsigned>((cols + 31) / 32);
-    const int64_t tiles = tiles_of(rows);
-    if (dtype == BWD_F32) col_sums_kernel<kF32><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else if (dtype == BWD_BF16) col_sums_kernel<kBF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else col_sums_kernel<kF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    s = check_launch("col_sums_kernel launch");
-  }
-  return s;
+  return quantize(x, dtype, rows, cols, ld, blocks, row_codes, row_scales, col_codes, col_scales, col_sums, col_sums_work,
+                  static_cast<cudaStream_t>(stream));
 }
 
 bwd_status bwd_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t along_rows, int64_t rows, int64_t cols,
@@ -1029,38 +1384,84 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
   if (!aligned_to(out, eb) || (bias && !aligned_to(bias, eb))) return fail(BWD_ERR_INVALID_ARG, "out and bias must be aligned to their element size");
   if (k > 0 && (!aligned16(a) || !aligned16(b) || !aligned16(a_scales) || !aligned16(b_scales)))
     return fail(BWD_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
-  MmArgs p{};
-  p.bias = bias; p.out = out; p.ldo = ldo;
-  p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
-  p.a_trans = a_trans ? 1 : 0; p.b_trans = b_trans ? 1 : 0;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (k == 0) return dtype == BWD_F32 ? launch_fill<kF32>(p, st) : dtype == BWD_BF16 ? launch_fill<kBF16>(p, st) : launch_fill<kF16>(p, st);
-  const DeviceState* d = nullptr;
-  bwd_status s = ensure_device(&d);
+  return product(Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo, dtype, false,
+                 static_cast<cudaStream_t>(stream));
+}
+
+int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return -1;
+  Pieces w{nullptr};
+  w.take(rows * bwd_fp8_pitch(cols));
+  w.take(bwd_fp8_scale_bytes(rows, cols));
+  return w.used;
+}
+
+bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld, const uint8_t* w,
+                          const uint8_t* w_scales, int64_t n, const void* bias, void* y, int64_t ldy, uint8_t* x_col_codes,
+                          uint8_t* x_col_scales, void* work, void* stream) {
+  bwd_status s = check_matrix(x, dtype, rows, cols, ld);
   if (s != BWD_OK) return s;
-  const int64_t tiles_m = (m + kBM - 1) / kBM;
-  // 256 columns unless tiles of 128 are needed to give every pair one
-  const int bn = dtype == BWD_F32 || tiles_m * ((n + 255) / 256) < d->pairs ? 128 : 256;
-  const int64_t tiles_n = (n + bn - 1) / bn;
-  if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
-    return fail(BWD_ERR_INVALID_ARG, "too many tiles");
-  p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
-  p.sf_rows_b = static_cast<int>(tiles_of(n));
-  p.store = aligned16(out) && ldo * eb % 16 == 0;
-  MmMaps maps{};
-  if ((s = code_map(&maps.a, a, m, k, p.a_trans, kBM / 2)) != BWD_OK) return s;
-  if ((s = code_map(&maps.b, b, n, k, p.b_trans, bn / 2)) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfa, a_scales, tiles_of(m) * groups_of(k))) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfb, b_scales, tiles_of(n) * groups_of(k))) != BWD_OK) return s;
-  if (p.store) {
-    const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
-  }
-  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
-  if (dtype == BWD_BF16)
-    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, st);
-  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, st);
+  if (n < 0 || n > kMaxDim) return fail(BWD_ERR_INVALID_ARG, "bad size");
+  if (ldy < n) return fail(BWD_ERR_INVALID_ARG, "ldy is less than n");
+  if (!x_col_codes != !x_col_scales) return fail(BWD_ERR_INVALID_ARG, "column codes and scales go together");
+  const int eb = dtype == BWD_F32 ? 4 : 2;
+  const bool some = rows > 0 && cols > 0;
+  if ((rows > 0 && n > 0 && !y) || (some && !work) || (some && n > 0 && (!w || !w_scales))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(y, eb) || !aligned_to(bias, eb)) return fail(BWD_ERR_INVALID_ARG, "y and bias must be aligned to their element size");
+  if (!aligned16(w) || !aligned16(w_scales) || !aligned16(x_col_codes) || !aligned16(work))
+    return fail(BWD_ERR_INVALID_ARG, "codes, scales and work must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Pieces pieces{static_cast<uint8_t*>(work)};
+  uint8_t* const codes = pieces.take(rows * bwd_fp8_pitch(cols));
+  uint8_t* const scales = pieces.take(bwd_fp8_scale_bytes(rows, cols));
+  s = quantize(x, dtype, rows, cols, ld, x_col_codes ? BWD_FP8_ROWS | BWD_FP8_COLS : BWD_FP8_ROWS, codes, scales, x_col_codes, x_col_scales,
+               nullptr, nullptr, st);
+  if (s != BWD_OK) return s;
+  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, true, st);
+}
+
+int64_t bwd_fp8_linear_backward_work_bytes(int64_t rows, int64_t n) {
+  if (rows < 0 || n < 0 || rows > kMaxDim || n > kMaxDim) return -1;
+  Pieces w{nullptr};
+  w.take(rows * bwd_fp8_pitch(n));
+  w.take(bwd_fp8_scale_bytes(rows, n));
+  w.take(rows * bwd_fp8_pitch(n));
+  w.take(bwd_fp8_scale_bytes(n, rows));
+  w.take(tiles_of(rows) * n * 4);
+  return w.used;
+}
+
+bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype, int64_t rows, int64_t n, int64_t ld, const uint8_t* w,
+                                   const uint8_t* w_col_scales, const uint8_t* x_col_codes, const uint8_t* x_col_scales, int64_t k,
+                                   void* dx, int64_t lddx, void* dw, int64_t lddw, void* dbias, void* work, void* stream) {
+  bwd_status s = check_matrix(dy, dtype, rows, n, ld);
+  if (s != BWD_OK) return s;
+  if (k < 0 || k > kMaxDim) return fail(BWD_ERR_INVALID_ARG, "bad size");
+  if ((dx && lddx < k) || (dw && lddw < k)) return fail(BWD_ERR_INVALID_ARG, "lddx or lddw is less than k");
+  const int eb = dtype == BWD_F32 ? 4 : 2;
+  const bool some = rows > 0 && n > 0 && k > 0;
+  if ((some && dx && (!w || !w_col_scales)) || (some && dw && (!x_col_codes || !x_col_scales)) || (rows > 0 && n > 0 && !work))
+    return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(dx, eb) || !aligned_to(dw, eb) || !aligned_to(dbias, eb))
+    return fail(BWD_ERR_INVALID_ARG, "dx, dw and dbias must be aligned to their element size");
+  if (!aligned16(w) || !aligned16(w_col_scales) || !aligned16(x_col_codes) || !aligned16(x_col_scales) || !aligned16(work))
+    return fail(BWD_ERR_INVALID_ARG, "codes, scales and work must be 16-byte aligned");
+  if (!dx && !dw && !dbias) return BWD_OK;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  Pieces pieces{static_cast<uint8_t*>(work)};
+  uint8_t* const row_codes = pieces.take(rows * bwd_fp8_pitch(n));
+  uint8_t* const row_scales = pieces.take(bwd_fp8_scale_bytes(rows, n));
+  uint8_t* const col_codes = pieces.take(rows * bwd_fp8_pitch(n));
+  uint8_t* const col_scales = pieces.take(bwd_fp8_scale_bytes(n, rows));
+  float* const sums = reinterpret_cast<float*>(pieces.take(tiles_of(rows) * n * 4));
+  const int blocks = (dx ? BWD_FP8_ROWS : 0) | (dw || dbias ? BWD_FP8_COLS : 0);
+  s = quantize(dy, dtype, rows, n, ld, blocks, row_codes, row_scales, col_codes, col_scales, dbias, sums, st);
+  // only the quantizer itself lets the next kernel begin early
+  if (s == BWD_OK && dx)
+    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, !dbias, st);
+  if (s == BWD_OK && dw)
+    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, !dx && !dbias, st);
+  return s;
 }
 
 }  // extern "C"

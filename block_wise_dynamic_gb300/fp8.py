@@ -65,10 +65,42 @@ def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
     if x.dim() != 2:
         if x.dim() == 0:
             raise ValueError(f"{name} must have at least one dimension")
-        x = x.reshape(-1, x.shape[-1]) if x.shape[-1] else x.reshape(x.shape[:-1].numel(), 0)
-    if x.stride(1) != 1 and x.shape[1] > 1 or x.stride(0) < x.shape[1]:
+        x = x.reshape(x.shape[:-1].numel(), x.shape[-1])
+    if not x.is_contiguous() and (x.stride(1) != 1 or x.stride(0) < x.shape[1]):
         x = x.contiguous()
     return x
+
+
+def _pitch(cols: int) -> int:
+    return (cols + 15) // 16 * 16
+
+
+def _scale_bytes(count: int, length: int) -> int:
+    return (count + 127) // 128 * ((length + 511) // 512) * 512
+
+
+def _round256(n: int) -> int:
+    return (n + 255) // 256 * 256
+
+
+def _launch(entry: str, device: torch.device, stream, *args) -> None:
+    """Calls a library entry point on ``device`` and the given or current stream."""
+    fn = getattr(_lib, entry)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream_handle(device, stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(device, stream))
+    if st:
+        _abi.check(st, entry)
+
+
+def _bytes(n: int, device: torch.device) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stream=None):
@@ -83,25 +115,18 @@ def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stre
     x = _matrix(x, "x")
     rows, cols = x.shape
     dev = x.device
-    pitch = _lib.bwd_fp8_pitch(cols)
     rc = rs = cc = cs = sums = work = None
     if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
-        rc = torch.empty((rows, pitch), dtype=torch.uint8, device=dev)
-        rs = torch.empty(_lib.bwd_fp8_scale_bytes(rows, cols), dtype=torch.uint8, device=dev)
+        rc = _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols))
+        rs = _bytes(_scale_bytes(rows, cols), dev)
     if kind & (_abi.FP8_COLS | _abi.FP8_TILES):
-        cc = rc if kind == _abi.FP8_TILES else torch.empty((rows, pitch), dtype=torch.uint8, device=dev)
-        cs = torch.empty(_lib.bwd_fp8_scale_bytes(cols, rows), dtype=torch.uint8, device=dev)
+        cc = rc if kind == _abi.FP8_TILES else _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols))
+        cs = _bytes(_scale_bytes(cols, rows), dev)
     if col_sums:
         sums = torch.empty(cols, dtype=x.dtype, device=dev)
         work = torch.empty(max(1, (rows + 127) // 128 * cols), dtype=torch.float32, device=dev)
-
-    def ptr(t):
-        return None if t is None else t.data_ptr()
-
-    with torch.cuda.device(dev):
-        st = _lib.bwd_fp8_quantize(x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, ptr(rc), ptr(rs),
-                                   ptr(cc), ptr(cs), ptr(sums), ptr(work), _stream_handle(dev, stream))
-    _abi.check(st, "bwd_fp8_quantize")
+    _launch("bwd_fp8_quantize", dev, stream, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, _ptr(rc), _ptr(rs),
+            _ptr(cc), _ptr(cs), _ptr(sums), _ptr(work))
     q = Fp8Matrix((rows, cols), blocks, x.dtype, rc, rs, cc, cs)
     return (q, sums) if col_sums else q
 
@@ -128,10 +153,8 @@ def dequantize(a: Fp8Matrix, along: str = "rows", dtype=None, stream=None) -> to
         raise TypeError("dtype must be float32, bfloat16 or float16")
     rows, cols = a.shape
     out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
-    with torch.cuda.device(codes.device):
-        st = _lib.bwd_fp8_dequantize(codes.data_ptr(), scales.data_ptr(), int(along == "rows"), rows, cols, out.data_ptr(),
-                                     _GDT[dtype], _stream_handle(codes.device, stream))
-    _abi.check(st, "bwd_fp8_dequantize")
+    _launch("bwd_fp8_dequantize", codes.device, stream, codes.data_ptr(), scales.data_ptr(), int(along == "rows"), rows, cols,
+            out.data_ptr(), _GDT[dtype])
     return out
 
 
@@ -153,54 +176,78 @@ def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = Fa
     if bias is not None:
         _need(bias, "bias", dtype, n, dev)
     out = torch.empty((m, n), dtype=dtype, device=dev)
-    with torch.cuda.device(dev):
-        st = _lib.bwd_fp8_matmul(m, n, k, ac.data_ptr(), int(trans_a), asc.data_ptr(), bc.data_ptr(), int(trans_b),
-                                 bsc.data_ptr(), None if bias is None else bias.data_ptr(), out.data_ptr(), n, _GDT[dtype],
-                                 _stream_handle(dev, stream))
-    _abi.check(st, "bwd_fp8_matmul")
+    _launch("bwd_fp8_matmul", dev, stream, m, n, k, ac.data_ptr(), int(trans_a), asc.data_ptr(), bc.data_ptr(), int(trans_b),
+            bsc.data_ptr(), _ptr(bias), out.data_ptr(), n, _GDT[dtype])
     return out
 
 
-def _check_width(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
+def _operands(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
+    """x as a matrix whose width is w's ``axis``, and w's codes and scales for
+    lines along it (the row form for axis 1, the column form for axis 0)."""
     if not isinstance(w, Fp8Matrix):
         raise TypeError("w must be an Fp8Matrix")
-    if x.dim() < 1 or x.shape[-1] != w.shape[axis]:
+    m = _matrix(x, name)
+    if m.shape[1] != w.shape[axis]:
         raise ValueError(f"{name}'s last dimension must be {w.shape[axis]}")
+    codes, scales, _, _ = _lines(w, axis == 0, "w")
+    if codes.device != m.device:
+        raise ValueError(f"w is on {codes.device}, the call runs on {m.device}")
+    return m, codes, scales
+
+
+def _forward(x, w, bias, both, stream):
+    m, codes, scales = _operands(x, w, 1, "x")
+    rows, cols = m.shape
+    n, dev, dt = w.shape[0], m.device, m.dtype
+    if bias is not None:
+        _need(bias, "bias", dt, n, dev)
+    y = torch.empty((*x.shape[:-1], n), dtype=dt, device=dev)
+    work = _bytes(_round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols)), dev)
+    cc = cs = xq = None
+    if both:
+        cc, cs = _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols)), _bytes(_scale_bytes(cols, rows), dev)
+        xq = Fp8Matrix((rows, cols), "cols", dt, None, None, cc, cs)
+    _launch("bwd_fp8_linear", dev, stream, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes.data_ptr(), scales.data_ptr(), n,
+            _ptr(bias), y.data_ptr(), n, _ptr(cc), _ptr(cs), work.data_ptr())
+    return y, xq
 
 
 def linear(x: torch.Tensor, w: Fp8Matrix, bias: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """x W^T + bias in x's dtype, for a weight (outputs x inputs) quantized
     with blocks "tiles" or "rows"; x is quantized within the call."""
-    _check_width(x, w, 1, "x")
-    y = matmul(quantize(x, "rows", stream=stream), w, bias=bias, stream=stream)
-    return y.view(*x.shape[:-1], w.shape[0])
+    return _forward(x, w, bias, False, stream)[0]
 
 
 def forward(x: torch.Tensor, w: Fp8Matrix, bias: Optional[torch.Tensor] = None, stream=None):
-    """(y, xq): :func:`linear`, and x quantized both ways for :func:`backward`."""
-    _check_width(x, w, 1, "x")
-    xq = quantize(x, "both", stream=stream)
-    return matmul(xq, w, bias=bias, stream=stream).view(*x.shape[:-1], w.shape[0]), xq
+    """(y, xq): :func:`linear`, and x quantized in column blocks, which
+    :func:`backward` reads."""
+    return _forward(x, w, bias, True, stream)
 
 
 def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = True, need_weight: bool = True,
              need_bias: bool = False, stream=None):
     """(dx, dw, dbias) in dy's dtype, None for those not needed.  xq has
     column blocks (from :func:`forward`), w blocks "tiles" or "cols"."""
-    _check_width(dy, w, 0, "dy")
-    rows = dy.shape[:-1].numel()
-    if need_weight and (not isinstance(xq, Fp8Matrix) or xq.shape != (rows, w.shape[1])):
-        raise ValueError(f"xq must be an Fp8Matrix of shape {(rows, w.shape[1])}")
-    blocks = "both" if need_input and (need_weight or need_bias) else "rows" if need_input else "cols"
-    db = None
+    m, codes, scales = _operands(dy, w, 0, "dy")
+    rows, n = m.shape
+    k, dev, dt = w.shape[1], m.device, m.dtype
+    xc = xs = dx = dw = db = None
+    if need_weight:
+        if not isinstance(xq, Fp8Matrix) or tuple(xq.shape) != (rows, k):
+            raise ValueError(f"xq must be an Fp8Matrix of shape {(rows, k)}")
+        xc, xs, _, _ = _lines(xq, True, "xq")
+        if xc.device != dev:
+            raise ValueError(f"xq is on {xc.device}, the call runs on {dev}")
+        dw = torch.empty((n, k), dtype=dt, device=dev)
+    if need_input:
+        dx = torch.empty((*dy.shape[:-1], k), dtype=dt, device=dev)
     if need_bias:
-        dyq, db = quantize(dy, blocks, col_sums=True, stream=stream)
-    else:
-        dyq = quantize(dy, blocks, stream=stream)
-    dx = matmul(dyq, w, trans_b=True, stream=stream).view(*dy.shape[:-1], w.shape[1]) if need_input else None
-    dw = matmul(dyq, xq, trans_a=True, trans_b=True, stream=stream) if need_weight else None
+        db = torch.empty(n, dtype=dt, device=dev)
+    codes_bytes = _round256(rows * _pitch(n))
+    work = _bytes(2 * codes_bytes + _round256(_scale_bytes(rows, n)) + _round256(_scale_bytes(n, rows)) +
+                  _round256((rows + 127) // 128 * n * 4), dev)
+    _launch("bwd_fp8_linear_backward", dev, stream, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes.data_ptr(), scales.data_ptr(),
+            _ptr(xc), _ptr(xs), k, _ptr(dx), k, _ptr(dw), k, _ptr(db), work.data_ptr())
     return dx, dw, db
 
 

@@ -375,6 +375,42 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
                           const uint8_t* b_scales, const void* bias, void* out,
                           int64_t ldo, bwd_dtype dtype, void* stream);
 
+/* A linear layer's forward pass in one call: y = Q(x) W^T + bias, x
+ * (rows x cols) quantized in blocks of 1 x 128 in the workspace.
+ *   w, w_scales : codes and scales of n lines of cols elements (BWD_FP8_ROWS
+ *            or BWD_FP8_TILES of an n x cols weight).
+ *   bias : n values of x's type, or NULL.   y : rows x n of x's type.
+ *   x_col_codes, x_col_scales : both NULL, or written as for BWD_FP8_COLS
+ *            (the backward pass reads them).
+ *   work : device, 16-byte aligned, bwd_fp8_linear_work_bytes(rows, cols). */
+int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols);
+bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows,
+                          int64_t cols, int64_t ld, const uint8_t* w,
+                          const uint8_t* w_scales, int64_t n, const void* bias,
+                          void* y, int64_t ldy, uint8_t* x_col_codes,
+                          uint8_t* x_col_scales, void* work, void* stream);
+
+/* Its backward pass: dy (rows x n) is quantized once in both forms, then
+ *     dx = Q(dy) W           rows x k, `lddx` between rows, or NULL
+ *     dw = Q(dy)^T Q(x)      n x k, `lddw` between rows, or NULL
+ *     dbias = sum of dy's rows   n values, or NULL
+ * all of dy's type.
+ *   w, w_col_scales : codes and scales of the k columns of the n x k weight
+ *            (BWD_FP8_TILES or BWD_FP8_COLS); read for dx.
+ *   x_col_codes, x_col_scales : of x's k columns; read for dw.
+ *   work : device, 16-byte aligned,
+ *            bwd_fp8_linear_backward_work_bytes(rows, n). */
+int64_t bwd_fp8_linear_backward_work_bytes(int64_t rows, int64_t n);
+bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype,
+                                   int64_t rows, int64_t n, int64_t ld,
+                                   const uint8_t* w,
+                                   const uint8_t* w_col_scales,
+                                   const uint8_t* x_col_codes,
+                                   const uint8_t* x_col_scales, int64_t k,
+                                   void* dx, int64_t lddx, void* dw,
+                                   int64_t lddw, void* dbias, void* work,
+                                   void* stream);
+
 /* Waits for `stream` and reports whether a bounded wait inside one of the
  * library's kernels gave up since the last check (the staged embedding
  * backward and the 8-bit product wait for their own copies and products; each
