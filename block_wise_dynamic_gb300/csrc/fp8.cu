@@ -411,27 +411,30 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
                : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
   return ok != 0;
 }
 
 // Arrival on the same barrier of the pair's first CTA.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
-  asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n}"
+  asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [r];\n}"
                ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Every wait is bounded: after about a second (or 2^24 polls) it sets the
 // CTA's fail flag and the device's fault word, and from then on every other
 // wait of the CTA gives up at once.
+// (The timer is read after 64 polls for the first time: reading it takes
+// longer than a stage's products.)
 __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* fail_flag) {
-  uint64_t t0, t1;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-  for (int i = 0; i < (1 << 24); ++i) {
+  uint64_t t0 = 0, t1;
+  for (int i = 1; i < (1 << 24); ++i) {
     if (mbar_try(bar, parity)) return true;
     if (fail_flag && *fail_flag) return false;
+    if (i % 64 != 0) continue;
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
+    if (t0 == 0) t0 = t1;
     if (t1 - t0 > 1000000000ull) break;
   }
   if (fail_flag) *fail_flag = 1;
@@ -452,6 +455,26 @@ __device__ __noinline__ void let_copies_land() {
     if (t1 - t0 > 2000000ull) break;
   }
 }
+
+// One lane of a converged warp.  The copying and issuing warps run their loops
+// with all lanes and elect the one that issues, so that the compiler keeps
+// addresses and descriptors in uniform registers (with a loop of one lane,
+// 0.36 us per stage of a 256 x 128 tile against 0.18).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(ok));
+  return ok != 0;
+}
+
+// A stage of a ring of kStages barriers and the parity of its phase.
+template <int kStages>
+struct Ring {
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == kStages) { s = 0; phase ^= 1u; }
+  }
+};
 
 // Address of a barrier of this CTA in the shared memory of the pair's first
 // CTA, which issues the products for both.
@@ -593,45 +616,49 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   const int chunk = kSum ? kChunk : kblocks;
 
   if (warp == 0) {
-    if (lane == 0) {
-      wait_for_inputs();
-      int it = 0;
-      bool ok = true;
-      for (int t = first; ok && t < tiles; t += pairs) {
-        const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2), nt = t % p.tiles_n * kBN;
-        const int n0 = nt + static_cast<int>(rank) * (kBN / 2);
-        for (int kb = 0; kb < kblocks; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!(ok = mbar_wait(&s_empty[s], ((it / kStages) & 1) ^ 1, &s_fail))) break;
+    wait_for_inputs();
+    const bool one = elect_one();
+    Ring<kStages> ring;
+    bool ok = true;
+    for (int t = first; ok && t < tiles; t += pairs) {
+      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2), nt = t % p.tiles_n * kBN;
+      const int n0 = nt + static_cast<int>(rank) * (kBN / 2);
+      for (int kb = 0; kb < kblocks; ++kb, ring.next()) {
+        if (!(ok = mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail))) break;
+        if (one) {
           const bool scales = (kb & 3) == 0;  // four blocks' scales come with the first of them
-          const uint32_t bar = leader_addr(&s_full[s]);
-          if (rank == 0) mbar_expect_tx(&s_full[s], 2 * (kA + kB + (scales ? kSf : 0)));
-          uint8_t* const a = sm + s * (kA + kB);
+          const uint32_t bar = leader_addr(&s_full[ring.s]);
+          if (rank == 0) mbar_expect_tx(&s_full[ring.s], 2 * (kA + kB + (scales ? kSf : 0)));
+          uint8_t* const a = sm + ring.s * (kA + kB);
           uint8_t* const b = a + kA;
-          if (p.a_trans) tma_load(a, &map_a, m0, kb * kBK, bar); else tma_load(a, &map_a, kb * kBK, m0, bar);
-          if (p.b_trans) tma_load(b, &map_b, n0, kb * kBK, bar); else tma_load(b, &map_b, kb * kBK, n0, bar);
+          tma_load(a, &map_a, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, bar);
+          tma_load(b, &map_b, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, bar);
           if (scales) {
             // A's for this CTA's rows, B's for the whole tile
-            tma_load(sf + s * kSf, &map_sfa, 0, m0 / 128 * groups + kb / 4, bar);
+            tma_load(sf + ring.s * kSf, &map_sfa, 0, m0 / 128 * groups + kb / 4, bar);
 #pragma unroll
             for (int h = 0; h < kBN / 128; ++h) {
               const int rt = nt / 128 + h;  // past the last row tile: columns past n, whatever they hold
-              tma_load(sf + s * kSf + (1 + h) * kSfTile, &map_sfb, 0, (rt < p.sf_rows_b ? rt : p.sf_rows_b - 1) * groups + kb / 4, bar);
+              tma_load(sf + ring.s * kSf + (1 + h) * kSfTile, &map_sfb, 0, (rt < p.sf_rows_b ? rt : p.sf_rows_b - 1) * groups + kb / 4, bar);
             }
           }
         }
+        __syncwarp();
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
+      const bool one = elect_one();
       // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
       const uint32_t idesc = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) |
                              ((kBN / 8) << 17) | (1u << 23) | ((kBM / 16) << 24);
-      // descriptors without their addresses, and the step of 32 along the summed axis
-      const uint64_t da0 = smem_desc(0, 16, 1024, 2);
-      const uint64_t db0 = p.b_trans && kBN == 128 ? smem_desc(0, 16, 512, 4) : smem_desc(0, 16, 1024, 2);
+      // descriptors of stage 0, and the step of 32 along the summed axis
+      const uint64_t da0 = smem_desc(smem_u32(sm), 16, 1024, 2);
+      const uint64_t db0 = p.b_trans && kBN == 128 ? smem_desc(smem_u32(sm + kA), 16, 512, 4) : smem_desc(smem_u32(sm + kA), 16, 1024, 2);
+      const uint64_t dsf0 = smem_desc(smem_u32(sf), 16, 128, 0);
       const uint32_t sa = p.a_trans ? 4096 / 16 : 32 / 16, sb = p.b_trans ? kBN / 2 * 32 / 16 : 32 / 16;
-      int it = 0, use = 0;  // stages and accumulators used so far
+      Ring<kStages> ring;
+      int use = 0;  // accumulators used so far
       bool ok = true;
       for (int t = first; ok && t < tiles; t += pairs) {
         for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
@@ -640,28 +667,33 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           if (kBN == 256 && ok && use > 0) ok = mbar_wait(&s_overlap, (use - 1) & 1, &s_fail);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const int k1 = kblocks < k0 + chunk ? kblocks : k0 + chunk;
-          for (int kb = k0; ok && kb < k1; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!(ok = mbar_wait(&s_full[s], (it / kStages) & 1, &s_fail))) break;
+          const uint32_t acc = tmem + acc_col<kBN>(buf);
+          for (int kb = k0; ok && kb < k1; ++kb, ring.next()) {
+            if (!(ok = mbar_wait(&s_full[ring.s], ring.phase, &s_fail))) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-            const uint32_t a = smem_u32(sm + s * (kA + kB)), b = a + kA;
-            const uint32_t tsf = tmem + kTmemSf + 16 * ((kb >> 2) & 1);
-            if ((kb & 3) == 0) {
-              const uint32_t d = smem_u32(sf + s * kSf);
+            if (one) {
+              const uint64_t da = da0 + static_cast<uint32_t>(ring.s * ((kA + kB) / 16)), db = db0 + static_cast<uint32_t>(ring.s * ((kA + kB) / 16));
+              const uint32_t tsf = tmem + kTmemSf + 16 * ((kb >> 2) & 1);
+              if ((kb & 3) == 0) {
 #pragma unroll
-              for (int h = 0; h < 1 + kBN / 128; ++h)
-                asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4 * h), "l"(smem_desc(d + h * kSfTile, 16, 128, 0)) : "memory");
+                for (int h = 0; h < 1 + kBN / 128; ++h)
+                  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4 * h),
+                               "l"(dsf0 + static_cast<uint32_t>(ring.s * (kSf / 16) + h * (kSfTile / 16))) : "memory");
+              }
+              // which of the four bytes: bits 4 and 29
+              const uint32_t id = idesc + static_cast<uint32_t>(kb & 3) * ((1u << 4) | (1u << 29));
+#pragma unroll
+              for (uint32_t q = 0; q < 4; ++q)
+                asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+                             "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
+                             ::"r"(acc), "l"(da + q * sa), "l"(db + q * sb), "r"(id), "r"(tsf), "r"(tsf + 4),
+                             "r"(static_cast<uint32_t>(kb != k0 || q != 0)) : "memory");
+              commit_pair(&s_empty[ring.s]);
             }
-            const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
-#pragma unroll
-            for (uint32_t q = 0; q < 4; ++q)
-              asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-                           "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                           ::"r"(tmem + acc_col<kBN>(buf)), "l"(da0 + (a >> 4) + q * sa), "l"(db0 + (b >> 4) + q * sb), "r"(id), "r"(tsf), "r"(tsf + 4),
-                           "r"(static_cast<uint32_t>(kb != k0 || q != 0)) : "memory");
-            commit_pair(&s_empty[s]);
+            __syncwarp();
           }
-          commit_pair(&s_acc_full[buf]);
+          if (one) commit_pair(&s_acc_full[buf]);
+          __syncwarp();
         }
       }
     }
@@ -864,63 +896,73 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   const int accs = (kb1 - kb0 + chunk - 1) / chunk;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const auto weight = [&](int kb, int s) {
-        uint8_t* const w = sm + s * kStage;
-        if (p.b_trans) tma_load_one(w, &map_w, n0, kb * kBK, &s_full[s]); else tma_load_one(w, &map_w, kb * kBK, n0, &s_full[s]);
-      };
-      // the first stages' weights do not depend on the kernel ahead
-      const int ahead = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
+    const bool one = elect_one();
+    const auto weight = [&](int kb, int s) {
+      tma_load_one(sm + s * kStage, &map_w, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, &s_full[s]);
+    };
+    // the first stages' weights do not depend on the kernel ahead
+    const int ahead = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
+    if (one) {
       for (int i = 0; i < ahead; ++i) {
         mbar_expect_tx(&s_full[i], kStage + (i == 0 || ((kb0 + i) & 3) == 0 ? 2 * kSfTile : 0));
         weight(kb0 + i, i);
       }
-      wait_for_inputs();
-      for (int i = 0; i < kb1 - kb0; ++i) {
-        const int s = i % kStages, kb = kb0 + i;
-        const bool scales = i == 0 || (kb & 3) == 0;
+    }
+    __syncwarp();
+    wait_for_inputs();
+    Ring<kStages> ring;
+    for (int i = 0; i < kb1 - kb0; ++i, ring.next()) {
+      const int kb = kb0 + i;
+      const bool scales = i == 0 || (kb & 3) == 0;
+      if (i >= ahead && !mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail)) break;
+      if (one) {
         if (i >= ahead) {
-          if (!mbar_wait(&s_empty[s], ((i / kStages) & 1) ^ 1, &s_fail)) break;
-          mbar_expect_tx(&s_full[s], kStage + (scales ? 2 * kSfTile : 0));
-          weight(kb, s);
+          mbar_expect_tx(&s_full[ring.s], kStage + (scales ? 2 * kSfTile : 0));
+          weight(kb, ring.s);
         }
-        uint8_t* const x = sm + s * kStage + kW;
-        if (p.a_trans) tma_load_one(x, &map_x, m0, kb * kBK, &s_full[s]); else tma_load_one(x, &map_x, kb * kBK, m0, &s_full[s]);
+        tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, &s_full[ring.s]);
         if (scales) {
-          tma_load_one(sf + s * 2 * kSfTile, &map_sfw, 0, n0 / 128 * groups + kb / 4, &s_full[s]);
-          tma_load_one(sf + s * 2 * kSfTile + kSfTile, &map_sfx, 0, m0 / 128 * groups + kb / 4, &s_full[s]);
+          tma_load_one(sf + ring.s * 2 * kSfTile, &map_sfw, 0, n0 / 128 * groups + kb / 4, &s_full[ring.s]);
+          tma_load_one(sf + ring.s * 2 * kSfTile + kSfTile, &map_sfx, 0, m0 / 128 * groups + kb / 4, &s_full[ring.s]);
         }
       }
+      __syncwarp();
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = (static_cast<uint32_t>(p.b_trans) << 15) | (static_cast<uint32_t>(p.a_trans) << 16) |
-                             ((kBN / 8) << 17) | (1u << 23) | ((kTile / 16) << 24);
-      const uint64_t desc = smem_desc(0, 16, 1024, 2);
-      const uint32_t sw = p.b_trans ? 4096 / 16 : 32 / 16, sx = p.a_trans ? 4096 / 16 : 32 / 16;
-      bool ok = true;
-      for (int i = 0; ok && i < kb1 - kb0; ++i) {
-        const int s = i % kStages, kb = kb0 + i;
-        if (!(ok = mbar_wait(&s_full[s], (i / kStages) & 1, &s_fail))) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t w = smem_u32(sm + s * kStage), x = w + kW;
+    const bool one = elect_one();
+    const uint32_t idesc = (static_cast<uint32_t>(p.b_trans) << 15) | (static_cast<uint32_t>(p.a_trans) << 16) |
+                           ((kBN / 8) << 17) | (1u << 23) | ((kTile / 16) << 24);
+    const uint64_t dw0 = smem_desc(smem_u32(sm), 16, 1024, 2), dx0 = smem_desc(smem_u32(sm + kW), 16, 1024, 2);
+    const uint64_t dsf0 = smem_desc(smem_u32(sf), 16, 128, 0);
+    const uint32_t sw = p.b_trans ? 4096 / 16 : 32 / 16, sx = p.a_trans ? 4096 / 16 : 32 / 16;
+    Ring<kStages> ring;
+    uint32_t acc = tmem;
+    int left = chunk;  // blocks that this accumulator still takes
+    for (int i = 0; i < kb1 - kb0; ++i, ring.next()) {
+      const int kb = kb0 + i;
+      if (!mbar_wait(&s_full[ring.s], ring.phase, &s_fail)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (one) {
+        const uint64_t dw = dw0 + static_cast<uint32_t>(ring.s * (kStage / 16)), dx = dx0 + static_cast<uint32_t>(ring.s * (kStage / 16));
         const uint32_t tsf = tmem + kSfCol + 8 * ((kb >> 2) & 1);
         if (i == 0 || (kb & 3) == 0) {
-          const uint32_t d = smem_u32(sf + s * 2 * kSfTile);
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf), "l"(smem_desc(d, 16, 128, 0)) : "memory");
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4), "l"(smem_desc(d + kSfTile, 16, 128, 0)) : "memory");
+          const uint64_t d = dsf0 + static_cast<uint32_t>(ring.s * (2 * kSfTile / 16));
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf), "l"(d) : "memory");
+          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4), "l"(d + kSfTile / 16) : "memory");
         }
-        const uint32_t id = idesc | (static_cast<uint32_t>(kb & 3) << 4) | (static_cast<uint32_t>(kb & 3) << 29);
+        const uint32_t id = idesc + static_cast<uint32_t>(kb & 3) * ((1u << 4) | (1u << 29));
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q)
           asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
                        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                       ::"r"(tmem + (i / chunk) * kBN), "l"(desc + (w >> 4) + q * sw), "l"(desc + (x >> 4) + q * sx), "r"(id), "r"(tsf), "r"(tsf + 4),
-                       "r"(static_cast<uint32_t>(i % chunk != 0 || q != 0)) : "memory");
-        commit_one(&s_empty[s]);
+                       ::"r"(acc), "l"(dw + q * sw), "l"(dx + q * sx), "r"(id), "r"(tsf), "r"(tsf + 4),
+                       "r"(static_cast<uint32_t>(left != chunk || q != 0)) : "memory");
+        commit_one(&s_empty[ring.s]);
       }
-      commit_one(&s_done);
+      __syncwarp();
+      if (--left == 0) { left = chunk; acc += kBN; }
     }
+    if (one) commit_one(&s_done);
   }
   __syncwarp();
   const int quarter = warp & 3, share = (kBN + p.split - 1) / p.split;  // columns that a CTA gathers
