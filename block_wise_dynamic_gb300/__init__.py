@@ -70,10 +70,23 @@ def _kind(kind) -> int:
 
 def _stream_handle(device: torch.device, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device.index is None else device.index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _launch(entry: str, device: torch.device, stream, *args) -> None:
+    """Calls a library entry point whose last argument is the stream, with
+    ``device`` current."""
+    fn = getattr(_abi.load(), entry)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream_handle(device, stream))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream_handle(device, stream))
+    if st:
+        _abi.check(st, entry)
 
 
 def _need(t: torch.Tensor, name: str, dtype, numel: Optional[int] = None,

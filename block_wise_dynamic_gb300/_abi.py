@@ -40,6 +40,19 @@ class AdamHParams(ctypes.Structure):
     ]
 
 
+class AdamWHParams(ctypes.Structure):
+    """Mirror of ``bwd_adamw_hparams``."""
+
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("step", ctypes.c_int64),
+    ]
+
+
 class BwdError(RuntimeError):
     def __init__(self, status: int, where: str, detail: str):
         self.status = status
@@ -76,10 +89,10 @@ _SIGNATURES = {
     "bwd_embedding_backward": (
         _int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "bwd_adam32_step_multi": (
-        _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamHParams), _vp]),
+        _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamWHParams), _vp]),
     "bwd_grad_norm_work_bytes": (_i64, [_i32]),
     "bwd_grad_norm": (
-        _int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]),
+        _int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "bwd_fp8_pitch": (_i64, [_i64]),
     "bwd_fp8_scale_bytes": (_i64, [_i64, _i64]),
     "bwd_fp8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),

@@ -19,7 +19,7 @@ from typing import Sequence
 import torch
 
 from . import _abi
-from . import _GDT, _hparams, _lib, _need, _stream_handle
+from . import _GDT, _launch, _lib, _need
 
 __all__ = ["MultiTensorArgs32", "adam32_step_multi", "GradNorm", "clip_scale"]
 
@@ -102,11 +102,9 @@ class MultiTensorArgs32(_GradList):
         if self.T == 0:
             return
         scale = _check_scale(grad_scale, self.device)
-        hp = _hparams(lr, beta1, beta2, eps, step, weight_decay)
-        with torch.cuda.device(self.device):
-            st = _lib.bwd_adam32_step_multi(self.T, self.p, self.p_dtype, self.g, self.g_dtype, self.m, self.v, self.n,
-                                            scale, ctypes.byref(hp), _stream_handle(self.device, stream))
-        _abi.check(st, "bwd_adam32_step_multi")
+        hp = _abi.AdamWHParams(lr, beta1, beta2, eps, weight_decay, int(step))
+        _launch("bwd_adam32_step_multi", self.device, stream, self.T, self.p, self.p_dtype, self.g, self.g_dtype, self.m, self.v, self.n,
+                scale, ctypes.byref(hp))
 
 
 def adam32_step_multi(params, grads, m, v, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step,
@@ -131,12 +129,11 @@ class GradNorm(_GradList):
         gradients divided by ``loss_scale``, and the factor that divides by
         ``loss_scale`` and clips to ``max_norm``: min(1, max_norm / (norm +
         1e-6)) / loss_scale, NaN where the norm is not finite."""
-        out = torch.empty(2, dtype=torch.float32, device=self.device)
-        with torch.cuda.device(self.device):
-            st = _lib.bwd_grad_norm(self.T, self.g, self.g_dtype, self.n, float(max_norm), float(loss_scale),
-                                    out.data_ptr(), self._work.data_ptr(), _stream_handle(self.device, stream))
-        _abi.check(st, "bwd_grad_norm")
-        return out[:1], out[1:]
+        factor = torch.empty(1, dtype=torch.float32, device=self.device)
+        norm = torch.empty(1, dtype=torch.float32, device=self.device)
+        _launch("bwd_grad_norm", self.device, stream, self.T, self.g, self.g_dtype, self.n, float(max_norm), float(loss_scale),
+                factor.data_ptr(), norm.data_ptr(), self._work.data_ptr())
+        return factor, norm
 
 
 def clip_scale(grads: Sequence[torch.Tensor], max_norm: float, loss_scale: float = 1.0, stream=None):

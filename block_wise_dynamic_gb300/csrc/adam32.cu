@@ -176,7 +176,8 @@ struct NormArgs {
   int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where vector loads are not possible
   double* slots;                 // one per CTA of all launches of the call
   unsigned int* ticket;          // 0 before the call and after it
-  float* out;                    // factor, norm
+  float* factor;
+  float* norm;
   int32_t num_tensors;
   int32_t first_slot, total_slots;
   float max_norm, inv_loss_scale;
@@ -241,8 +242,8 @@ grad_norm_kernel(const __grid_constant__ NormArgs a) {
     const float norm = static_cast<float>(sqrt(all) * static_cast<double>(a.inv_loss_scale));
     const float clip = fminf(1.0f, __fdiv_rn(a.max_norm, __fadd_rn(norm, 1e-6f)));
     const bool finite = norm <= 3.402823466e38f;  // false for NaN too
-    a.out[0] = finite ? __fmul_rn(clip, a.inv_loss_scale) : __uint_as_float(0x7fffffffu);
-    a.out[1] = norm;
+    *a.factor = finite ? __fmul_rn(clip, a.inv_loss_scale) : __uint_as_float(0x7fffffffu);
+    *a.norm = norm;
     *a.ticket = 0;
   }
 }
@@ -284,7 +285,7 @@ extern "C" {
 
 bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g,
                                  bwd_dtype g_dtype, float* const* m, float* const* v, const int64_t* n,
-                                 const float* grad_scale, const bwd_adam_hparams* hp, void* stream) {
+                                 const float* grad_scale, const bwd_adamw_hparams* hp, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
   if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
   if (!valid_type(p_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "parameter dtype %d", (int)p_dtype);
@@ -303,7 +304,7 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
   int sms = 0;
   if ((s = sm_count(&sms)) != BWD_OK) return s;
   static thread_local Adam32Args a;  // ~27 KB: kept off the stack
-  const bwd::host::AdamScalars k = bwd::host::adam_scalars(hp);
+  const bwd::host::AdamScalars k = bwd::host::adam_scalars(*hp);
   a.b1 = k.b1; a.omb1 = k.omb1; a.b2 = k.b2; a.omb2 = k.omb2;
   a.eps = k.eps; a.step_size = k.step_size; a.inv_bc2s = k.inv_bc2s; a.decay = k.decay;
   a.grad_scale = grad_scale;
@@ -334,14 +335,15 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {
 }
 
 bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_dtype, const int64_t* n, float max_norm,
-                         float loss_scale, float* out, void* work, void* stream) {
+                         float loss_scale, float* factor, float* norm, void* work, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
   if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
   if (!(max_norm > 0.0f)) return fail(BWD_ERR_INVALID_ARG, "max_norm must be > 0");
   if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale) || !std::isfinite(1.0f / loss_scale))
     return fail(BWD_ERR_INVALID_ARG, "loss_scale and its reciprocal must be finite and > 0");
-  if (!out || !work || (num_tensors > 0 && (!g || !n))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
-  if (!aligned_to(out, 4) || !aligned16(work)) return fail(BWD_ERR_INVALID_ARG, "out must be 4-byte and work 16-byte aligned");
+  if (!factor || !norm || !work || (num_tensors > 0 && (!g || !n))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  if (!aligned_to(factor, 4) || !aligned_to(norm, 4) || !aligned16(work))
+    return fail(BWD_ERR_INVALID_ARG, "factor and norm must be 4-byte and work 16-byte aligned");
   for (int32_t i = 0; i < num_tensors; ++i) {
     if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
     if (n[i] > 0 && (!g[i] || !aligned_to(g[i], bytes_of(g_dtype))))
@@ -353,7 +355,8 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
   static thread_local NormArgs a;  // ~20 KB: kept off the stack
   a.ticket = static_cast<unsigned int*>(work);
   a.slots = reinterpret_cast<double*>(static_cast<char*>(work) + 16);
-  a.out = out;
+  a.factor = factor;
+  a.norm = norm;
   a.max_norm = max_norm;
   a.inv_loss_scale = 1.0f / loss_scale;
   const int64_t cap = static_cast<int64_t>(sms < 256 ? sms : 256) * kNormCtas;

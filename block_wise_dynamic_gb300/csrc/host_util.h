@@ -28,10 +28,11 @@ struct AdamScalars {
   float b1, omb1, b2, omb2, eps, step_size, inv_bc2s;
   float decay;  // 1 - lr * weight_decay (decoupled weight decay), 1 for Adam
 };
-AdamScalars adam_scalars(const bwd_adam_hparams* hp);
+AdamScalars adam_scalars(const bwd_adamw_hparams& hp);
 
 // BWD_OK, or BWD_ERR_INVALID_ARG where a hyper-parameter is outside its range.
 bwd_status check_hparams(const bwd_adam_hparams* hp);
+bwd_status check_hparams(const bwd_adamw_hparams* hp);
 
 // Reads and clears the 8-bit products' fault word (see bwd_check_device).
 bwd_status take_fp8_fault(unsigned int* fault);

@@ -917,31 +917,37 @@ bwd_status check_launch(const char* what) {
 
 const char* last_error() { return t_last_error.c_str(); }
 
-bwd_status check_hparams(const bwd_adam_hparams* hp) {
+namespace {
+template <typename HP>
+bwd_status check_hparams_of(const HP* hp) {
   if (!hp) return fail(BWD_ERR_INVALID_ARG, "hparams is NULL");
   if (hp->step < 1) return fail(BWD_ERR_INVALID_ARG, "step must be >= 1 (got %lld)", (long long)hp->step);
-  if (!std::isfinite(hp->lr) || !std::isfinite(hp->eps) || hp->eps < 0.0f)
+  if (!std::isfinite(hp->lr) || !std::isfinite(hp->eps) || hp->eps < 0)
     return fail(BWD_ERR_INVALID_ARG, "lr and eps must be finite, eps >= 0");
-  if (!(hp->beta1 >= 0.0f && hp->beta1 < 1.0f) || !(hp->beta2 >= 0.0f && hp->beta2 < 1.0f))
+  if (!(hp->beta1 >= 0 && hp->beta1 < 1) || !(hp->beta2 >= 0 && hp->beta2 < 1))
     return fail(BWD_ERR_INVALID_ARG, "betas must lie in [0, 1)");
-  if (!std::isfinite(hp->weight_decay) || hp->weight_decay < 0.0f)
+  if (!std::isfinite(hp->weight_decay) || hp->weight_decay < 0)
     return fail(BWD_ERR_INVALID_ARG, "weight_decay must be finite and >= 0");
   return BWD_OK;
 }
+}  // namespace
 
-AdamScalars adam_scalars(const bwd_adam_hparams* hp) {
-  const double b1 = hp->beta1, b2 = hp->beta2, t = static_cast<double>(hp->step);
-  const double bc1 = 1.0 - std::pow(b1, t);
-  const double bc2 = 1.0 - std::pow(b2, t);
+bwd_status check_hparams(const bwd_adam_hparams* hp) { return check_hparams_of(hp); }
+bwd_status check_hparams(const bwd_adamw_hparams* hp) { return check_hparams_of(hp); }
+
+AdamScalars adam_scalars(const bwd_adamw_hparams& hp) {
+  const double t = static_cast<double>(hp.step);
+  const double bc1 = 1.0 - std::pow(hp.beta1, t);
+  const double bc2 = 1.0 - std::pow(hp.beta2, t);
   AdamScalars k;
-  k.b1 = hp->beta1;
-  k.b2 = hp->beta2;
-  k.omb1 = static_cast<float>(1.0 - b1);
-  k.omb2 = static_cast<float>(1.0 - b2);
-  k.eps = hp->eps;
-  k.step_size = static_cast<float>(static_cast<double>(hp->lr) / bc1);
+  k.b1 = static_cast<float>(hp.beta1);
+  k.b2 = static_cast<float>(hp.beta2);
+  k.omb1 = static_cast<float>(1.0 - hp.beta1);
+  k.omb2 = static_cast<float>(1.0 - hp.beta2);
+  k.eps = static_cast<float>(hp.eps);
+  k.step_size = static_cast<float>(hp.lr / bc1);
   k.inv_bc2s = static_cast<float>(1.0 / std::sqrt(bc2));
-  k.decay = static_cast<float>(1.0 - static_cast<double>(hp->lr) * static_cast<double>(hp->weight_decay));
+  k.decay = static_cast<float>(1.0 - hp.lr * hp.weight_decay);
   return k;
 }
 
@@ -1070,7 +1076,8 @@ int grid_for(int64_t blocks, int per_cta, const DeviceState& d, int occ) {
 bool valid_kind(bwd_map_kind k) { return k == BWD_MAP_SIGNED || k == BWD_MAP_UNSIGNED; }
 
 void fill_scalars(const bwd_adam_hparams* hp, AdamArgs* a) {
-  const bwd::host::AdamScalars k = bwd::host::adam_scalars(hp);
+  const bwd::host::AdamScalars k = bwd::host::adam_scalars(
+      bwd_adamw_hparams{hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, hp->step});
   a->b1 = k.b1;
   a->b2 = k.b2;
   a->omb1 = k.omb1;

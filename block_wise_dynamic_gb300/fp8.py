@@ -26,7 +26,7 @@ from typing import Optional
 import torch
 
 from . import _abi
-from . import _GDT, _lib, _need, _stream_handle
+from . import _GDT, _launch, _need
 
 __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
 
@@ -81,18 +81,6 @@ def _scale_bytes(count: int, length: int) -> int:
 
 def _round256(n: int) -> int:
     return (n + 255) // 256 * 256
-
-
-def _launch(entry: str, device: torch.device, stream, *args) -> None:
-    """Calls a library entry point on ``device`` and the given or current stream."""
-    fn = getattr(_lib, entry)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream_handle(device, stream))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream_handle(device, stream))
-    if st:
-        _abi.check(st, entry)
 
 
 def _bytes(n: int, device: torch.device) -> torch.Tensor:
@@ -184,12 +172,10 @@ def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = Fa
 def _operands(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
     """x as a matrix whose width is w's ``axis``, and w's codes and scales for
     lines along it (the row form for axis 1, the column form for axis 0)."""
-    if not isinstance(w, Fp8Matrix):
-        raise TypeError("w must be an Fp8Matrix")
     m = _matrix(x, name)
-    if m.shape[1] != w.shape[axis]:
-        raise ValueError(f"{name}'s last dimension must be {w.shape[axis]}")
-    codes, scales, _, _ = _lines(w, axis == 0, "w")
+    codes, scales, _, width = _lines(w, axis == 0, "w")
+    if m.shape[1] != width:
+        raise ValueError(f"{name}'s last dimension must be {width}")
     if codes.device != m.device:
         raise ValueError(f"w is on {codes.device}, the call runs on {m.device}")
     return m, codes, scales
@@ -201,7 +187,7 @@ def _forward(x, w, bias, both, stream):
     n, dev, dt = w.shape[0], m.device, m.dtype
     if bias is not None:
         _need(bias, "bias", dt, n, dev)
-    y = torch.empty((*x.shape[:-1], n), dtype=dt, device=dev)
+    y = torch.empty((rows, n) if m is x else (*x.shape[:-1], n), dtype=dt, device=dev)
     work = _bytes(_round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols)), dev)
     cc = cs = xq = None
     if both:
@@ -240,7 +226,7 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
             raise ValueError(f"xq is on {xc.device}, the call runs on {dev}")
         dw = torch.empty((n, k), dtype=dt, device=dev)
     if need_input:
-        dx = torch.empty((*dy.shape[:-1], k), dtype=dt, device=dev)
+        dx = torch.empty((rows, k) if m is dy else (*dy.shape[:-1], k), dtype=dt, device=dev)
     if need_bias:
         db = torch.empty(n, dtype=dt, device=dev)
     codes_bytes = _round256(rows * _pitch(n))

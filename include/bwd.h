@@ -260,6 +260,18 @@ bwd_status bwd_embedding_backward(const int64_t* ids, int64_t num_tokens,
                                   const float* dy, float* dweight,
                                   float* dgamma, float* dbeta, void* stream);
 
+/* Hyper-parameters of the step below: bwd_adam_hparams with its numbers in
+ * binary64, so that 1 - beta and the bias corrections are those of the beta
+ * meant (a binary32 0.999 is off by 1.3e-8, its 1 - beta by 1.3e-5 of it). */
+typedef struct {
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int64_t step;
+} bwd_adamw_hparams;
+
 /* ------------------------------------------------------------------------
  * AdamW with both moments in fp32, for the tensors of a run whose moments
  * stay in 32 bits (an embedding, norms, biases), and the gradients' norm.
@@ -267,8 +279,9 @@ bwd_status bwd_embedding_backward(const int64_t* ids, int64_t num_tokens,
  * One step over a list of tensors (480 per launch), in place:
  *     g' = s g;  m = b1 m + (1-b1) g';  v = b2 v + ((1-b2) g') g';
  *     p = p d - step m / (sqrt(v) / c + eps)
- * with the scalars of bwd_adam8bit_step and s = *grad_scale.  m and v take
- * one binary32 rounding per operation in that order.  Arrays are HOST arrays
+ * with step, c and d formed in binary64 on the host as for
+ * bwd_adam8bit_step (each scalar rounded once) and s = *grad_scale.  m and v
+ * take one binary32 rounding per operation in that order.  Arrays are HOST arrays
  * of length num_tensors.
  *   p          : device pointers to n[i] values of p_dtype, updated in place
  *                (16-bit ones are widened and rounded back to nearest even).
@@ -283,7 +296,7 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p,
                                  bwd_dtype g_dtype, float* const* m,
                                  float* const* v, const int64_t* n,
                                  const float* grad_scale,
-                                 const bwd_adam_hparams* hp, void* stream);
+                                 const bwd_adamw_hparams* hp, void* stream);
 
 /* Bytes of the workspace of bwd_grad_norm (-1 for num_tensors < 0). */
 int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
@@ -295,7 +308,7 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
  * NaN where the norm is not finite, so that a step that reads it as its
  * grad_scale writes nothing.  Sums are fp32 within a thread and binary64
  * across threads, in a fixed order: results are deterministic.
- *   out  : device float[2], written: factor, norm.
+ *   factor, norm : device float[1] each, written.
  *   work : device, 16-byte aligned, bwd_grad_norm_work_bytes(num_tensors)
  *          bytes, whose first 16 are zero before the first call; each call
  *          leaves them zero.  Calls that may run at the same time need one
@@ -304,8 +317,8 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
  *   1 / loss_scale.  num_tensors == 0 gives norm 0. */
 bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g,
                          bwd_dtype g_dtype, const int64_t* n, float max_norm,
-                         float loss_scale, float* out, void* work,
-                         void* stream);
+                         float loss_scale, float* factor, float* norm,
+                         void* work, void* stream);
 
 /* ------------------------------------------------------------------------
  * 8-bit floating point (e4m3) with a power-of-two scale for each block of

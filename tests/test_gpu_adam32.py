@@ -49,12 +49,10 @@ def state(sizes, pk, gk, seed, offset=0):
 def check(old, new, pk, step, scale=1.0):
     for i in range(len(new[0])):
         p, g, m, v = (np64(t) for t in (old[0][i], old[1][i], old[2][i], old[3][i]))
-        b1, b2 = float(np.float32(HP["beta1"])), float(np.float32(HP["beta2"]))
-        rp, rm, rv = ref.step(p, g, m, v, **{**HP, "beta1": b1, "beta2": b2, "lr": float(np.float32(HP["lr"])),
-                                              "eps": float(np.float32(HP["eps"])), "weight_decay": float(np.float32(HP["weight_decay"]))},
-                              step=step, scale=scale)
+        b1, b2 = HP["beta1"], HP["beta2"]
+        rp, rm, rv = ref.step(p, g, m, v, **HP, step=step, scale=scale)
         gs = np.abs(g * scale)
-        # m: three products and a sum, each half a unit (1 - b1 rounded once more); v: four products and a sum
+        # m: a coefficient, a product and a sum (and g'), half a unit each; v: one product more
         assert np.all(np.abs(np64(new[2][i]) - rm) <= 4 * 2.0 ** -24 * (b1 * np.abs(m) + (1 - b1) * gs) + 1e-44)
         assert np.all(np.abs(np64(new[3][i]) - rv) <= 6 * 2.0 ** -24 * (b2 * np.abs(v) + (1 - b2) * gs * gs) + 1e-44)
         # the update: m's error (of the size of its terms), and ten roundings of the quotient; then p's own
