@@ -29,8 +29,7 @@ using bwd::host::fail;
 
 constexpr int kF32 = BWD_F32, kBF16 = BWD_BF16, kF16 = BWD_F16;
 constexpr int kThreads = 256;
-constexpr int kQuads = 2;                           // quads of 4 elements per thread
-constexpr int kChunk = kThreads * kQuads * 4;       // elements a CTA works on at a time
+constexpr int kChunk = kThreads * 4;                // elements of a CTA: a quad of 4 per thread
 constexpr int kMaxTensors = 480;                    // per launch, bounded by kernel parameter space
 
 struct Tensor32 {
@@ -49,6 +48,8 @@ struct Adam32Args {
   int32_t num_tensors;
   float b1, omb1, b2, omb2, eps, step_size, inv_bc2s, decay;
 };
+
+constexpr int64_t kMaxChunks = 0x7fffffff;  // CTAs of one launch
 
 static_assert(sizeof(Adam32Args) <= 32764, "kernel parameter space");
 
@@ -100,80 +101,76 @@ __device__ __forceinline__ void store4(void* x, int64_t i, const float (&v)[4]) 
   }
 }
 
-// The last t with start[t] <= c.
+// The last t with start[t] <= c, found by a warp in two reads of the table
+// (num <= 1024): which of 32 stretches, and where in it.
 __device__ __forceinline__ int find_tensor(const int64_t* start, int num, int64_t c) {
-  int lo = 0, hi = num - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (start[mid] <= c) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  const int lane = threadIdx.x % 32, step = (num + 31) / 32;
+  const int i = lane * step;
+  const int base = (__popc(__ballot_sync(0xffffffffu, i < num && start[i] <= c)) - 1) * step;
+  const int j = base + 1 + lane;
+  return base + __popc(__ballot_sync(0xffffffffu, lane < step - 1 && j < num && start[j] <= c));
 }
 
+// One CTA for each chunk of 1,024 elements.  Bound by DRAM (26 bytes a
+// parameter with fp32 parameters and bf16 gradients).  Against CTAs that walk
+// the chunks, four to an SM with twice the elements each, 32000 x 4096 bf16
+// parameters take 408 us instead of 431 (7.1 TB/s), and all of a 355M set
+// 1.31 ms instead of 1.43; prefetches of the next chunk into L2 made those
+// slower still (497 us).
 template <int kG, int kP>
 __global__ void __launch_bounds__(kThreads)
 adam32_kernel(const __grid_constant__ Adam32Args a) {
+  const int ti = find_tensor(a.chunk_start, a.num_tensors, blockIdx.x);
+  const Tensor32& T = a.t[ti];
+  const int64_t i = (blockIdx.x - a.chunk_start[ti]) * kChunk + 4 * threadIdx.x;
+  const bool vec = T.vec && i + 4 <= T.n;
+  float p[4], g[4], m[4], v[4];
+  if (vec) {
+    load4<kP>(T.p, i, p); load4<kG>(T.g, i, g);
+    load4<kF32>(T.m, i, m); load4<kF32>(T.v, i, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool in = i + j < T.n;
+      p[j] = in ? load1<kP>(T.p, i + j) : 0.0f; g[j] = in ? load1<kG>(T.g, i + j) : 0.0f;
+      m[j] = in ? T.m[i + j] : 0.0f; v[j] = in ? T.v[i + j] : 0.0f;
+    }
+  }
   const float s = a.grad_scale ? *a.grad_scale : 1.0f;
   if (!(fabsf(s) <= 3.402823466e38f)) return;
-  const int64_t total = a.chunk_start[a.num_tensors];
-  int64_t c = blockIdx.x;
-  int ti = find_tensor(a.chunk_start, a.num_tensors, c);
-  for (; c < total; c += gridDim.x) {
-    while (a.chunk_start[ti + 1] <= c) ++ti;
-    const Tensor32& T = a.t[ti];
-    const int64_t base = (c - a.chunk_start[ti]) * kChunk + 4 * threadIdx.x;
-    float p[kQuads][4], g[kQuads][4], m[kQuads][4], v[kQuads][4];
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int64_t i = base + q * 4 * kThreads;
-      if (T.vec && i + 4 <= T.n) {
-        load4<kP>(T.p, i, p[q]); load4<kG>(T.g, i, g[q]);
-        load4<kF32>(T.m, i, m[q]); load4<kF32>(T.v, i, v[q]);
-      } else {
+  for (int j = 0; j < 4; ++j) {
+    const float gs = __fmul_rn(s, g[j]);
+    m[j] = __fadd_rn(__fmul_rn(a.b1, m[j]), __fmul_rn(a.omb1, gs));
+    v[j] = __fadd_rn(__fmul_rn(a.b2, v[j]), __fmul_rn(__fmul_rn(a.omb2, gs), gs));
+    const float den = __fmaf_rn(__fsqrt_rn(v[j]), a.inv_bc2s, a.eps);
+    p[j] = __fmaf_rn(-a.step_size, __fdiv_rn(m[j], den), __fmul_rn(p[j], a.decay));
+  }
+  if (vec) {
+    store4<kP>(T.p, i, p); store4<kF32>(T.m, i, m); store4<kF32>(T.v, i, v);
+  } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = i + j < T.n;
-          p[q][j] = in ? load1<kP>(T.p, i + j) : 0.0f; g[q][j] = in ? load1<kG>(T.g, i + j) : 0.0f;
-          m[q][j] = in ? T.m[i + j] : 0.0f; v[q][j] = in ? T.v[i + j] : 0.0f;
-        }
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float gs = __fmul_rn(s, g[q][j]);
-        m[q][j] = __fadd_rn(__fmul_rn(a.b1, m[q][j]), __fmul_rn(a.omb1, gs));
-        v[q][j] = __fadd_rn(__fmul_rn(a.b2, v[q][j]), __fmul_rn(__fmul_rn(a.omb2, gs), gs));
-        const float den = __fmaf_rn(__fsqrt_rn(v[q][j]), a.inv_bc2s, a.eps);
-        p[q][j] = __fmaf_rn(-a.step_size, __fdiv_rn(m[q][j], den), __fmul_rn(p[q][j], a.decay));
-      }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int64_t i = base + q * 4 * kThreads;
-      if (T.vec && i + 4 <= T.n) {
-        store4<kP>(T.p, i, p[q]); store4<kF32>(T.m, i, m[q]); store4<kF32>(T.v, i, v[q]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (i + j < T.n) { store1<kP>(T.p, i + j, p[q][j]); T.m[i + j] = m[q][j]; T.v[i + j] = v[q][j]; }
-      }
-    }
+    for (int j = 0; j < 4; ++j)
+      if (i + j < T.n) { store1<kP>(T.p, i + j, p[j]); T.m[i + j] = m[j]; T.v[i + j] = v[j]; }
   }
 }
 
 // --------------------------------------------------------------------------
-// Norm.  Each CTA sums squares in fp32 per thread and in binary64 across
-// threads, and writes its sum to its own slot; the CTA that finishes last
-// adds the slots in order, so the result does not depend on the schedule.
+// Norm.  A thread sums the squares of four 16-byte pieces in fp32, and such
+// sums, and those of the threads, in binary64; each CTA writes its sum to its
+// own slot, and the CTA that finishes last adds the slots in order, so the
+// result does not depend on the schedule.
 
 constexpr int kNormTensors = 1024;
-constexpr int kNormCtas = 4;  // per SM
+constexpr int kNormCtas = 8;   // per SM
+constexpr int kNormPieces = 4;
+template <int kT> __host__ __device__ constexpr int norm_vals() { return kT == kF32 ? 4 : 8; }  // values of a piece
+__host__ __device__ constexpr int norm_chunk(int type) { return kThreads * kNormPieces * (type == BWD_F32 ? 4 : 8); }
 
 struct NormArgs {
   int64_t chunk_start[kNormTensors + 1];
   const void* g[kNormTensors];
-  int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where vector loads are not possible
+  int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where 16-byte loads are not possible
   double* slots;                 // one per CTA of all launches of the call
   unsigned int* ticket;          // 0 before the call and after it
   float* factor;
@@ -197,36 +194,50 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
 }
 
 template <int kG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kNormCtas)
 grad_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ double s_red[kThreads / 32];
   __shared__ bool s_last;
+  constexpr int kVals = norm_vals<kG>();
   const int64_t total = a.chunk_start[a.num_tensors];
   int64_t c = blockIdx.x;
-  int ti = find_tensor(a.chunk_start, a.num_tensors, c);
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (; c < total; c += gridDim.x) {
-    while (a.chunk_start[ti + 1] <= c) ++ti;
-    const int64_t lc = c - a.chunk_start[ti], base = lc * kChunk;
-    const bool last = c + 1 == a.chunk_start[ti + 1], vec = a.n_tail[ti] > 0;
-    const int len = last ? abs(a.n_tail[ti]) : kChunk;
-    float g[kQuads][4];
+  double part = 0.0;
+  if (c < total) {
+    int ti = find_tensor(a.chunk_start, a.num_tensors, c);
+    for (; c < total; c += gridDim.x) {
+      while (a.chunk_start[ti + 1] <= c) ++ti;
+      const bool last = c + 1 == a.chunk_start[ti + 1], vec = a.n_tail[ti] > 0;
+      const int len = last ? abs(a.n_tail[ti]) : norm_chunk(kG);
+      const char* const g = static_cast<const char*>(a.g[ti]) + (c - a.chunk_start[ti]) * norm_chunk(kG) * (16 / kVals);
+      uint4 w[kNormPieces];
 #pragma unroll
-    for (int q = 0; q < kQuads; ++q) {
-      const int i = 4 * threadIdx.x + q * 4 * kThreads;
-      if (vec && i + 4 <= len) {
-        load4<kG>(a.g[ti], base + i, g[q]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) g[q][j] = i + j < len ? load1<kG>(a.g[ti], base + i + j) : 0.0f;
+      for (int q = 0; q < kNormPieces; ++q) {
+        const int i = (q * kThreads + threadIdx.x) * kVals;
+        w[q] = make_uint4(0u, 0u, 0u, 0u);
+        if (vec && i + kVals <= len) w[q] = __ldcs(reinterpret_cast<const uint4*>(g) + q * kThreads + threadIdx.x);
       }
+      float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+      for (int q = 0; q < kNormPieces; ++q) {
+        const int i = (q * kThreads + threadIdx.x) * kVals;
+        if (vec && i + kVals <= len) {
+#pragma unroll
+          for (int j = 0; j < kVals; ++j) {
+            const uint32_t u = (&w[q].x)[kG == kF32 ? j : j / 2];
+            const float x = kG == kF32 ? __uint_as_float(u) : widen<kG>(static_cast<unsigned short>(j % 2 ? u >> 16 : u & 0xffffu));
+            sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
+          }
+        } else {
+          for (int j = 0; j < kVals && i + j < len; ++j) {
+            const float x = load1<kG>(g, i + j);
+            sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
+          }
+        }
+      }
+      part += static_cast<double>(__fadd_rn(sum[0], sum[1]));
     }
-#pragma unroll
-    for (int q = 0; q < kQuads; ++q)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum[j] = __fmaf_rn(g[q][j], g[q][j], sum[j]);
   }
-  const double mine = block_sum(static_cast<double>(sum[0]) + sum[1] + sum[2] + sum[3], s_red);
+  const double mine = block_sum(part, s_red);
   if (threadIdx.x == 0) {
     a.slots[a.first_slot + blockIdx.x] = mine;
     __threadfence();
@@ -258,13 +269,12 @@ bwd_status sm_count(int* out) {
   return e == cudaSuccess ? BWD_OK : cuda_fail(e, "cudaDeviceGetAttribute");
 }
 
-int64_t chunks_of(int64_t n) { return (n + kChunk - 1) / kChunk; }
+int64_t chunks_of(int64_t n, int64_t chunk) { return (n + chunk - 1) / chunk; }
 bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
 uintptr_t bytes_of(int t) { return t == BWD_F32 ? 4 : 2; }
 
-bwd_status launch_adam32(const Adam32Args& a, int g_type, int p_type, int sms, cudaStream_t st) {
-  const int64_t total = a.chunk_start[a.num_tensors], cap = static_cast<int64_t>(sms) * 4;
-  const int grid = static_cast<int>(total < cap ? total : cap);
+bwd_status launch_adam32(const Adam32Args& a, int g_type, int p_type, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>(a.chunk_start[a.num_tensors]);
   switch (3 * p_type + g_type) {
     case 0: adam32_kernel<kF32, kF32><<<grid, kThreads, 0, st>>>(a); break;
     case 1: adam32_kernel<kBF16, kF32><<<grid, kThreads, 0, st>>>(a); break;
@@ -295,14 +305,12 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
   if (!p || !g || !m || !v || !n) return fail(BWD_ERR_INVALID_ARG, "NULL array");
   if (!aligned_to(grad_scale, 4)) return fail(BWD_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
   for (int32_t i = 0; i < num_tensors; ++i) {
-    if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
+    if (n[i] < 0 || n[i] > kMaxChunks * kChunk) return fail(BWD_ERR_INVALID_ARG, "tensor %d: bad size", i);
     if (n[i] > 0 && (!p[i] || !g[i] || !m[i] || !v[i])) return fail(BWD_ERR_INVALID_ARG, "tensor %d: NULL pointer", i);
     if (n[i] > 0 && (!aligned_to(p[i], bytes_of(p_dtype)) || !aligned_to(g[i], bytes_of(g_dtype)) ||
                      !aligned_to(m[i], 4) || !aligned_to(v[i], 4)))
       return fail(BWD_ERR_INVALID_ARG, "tensor %d: pointer not aligned to its element size", i);
   }
-  int sms = 0;
-  if ((s = sm_count(&sms)) != BWD_OK) return s;
   static thread_local Adam32Args a;  // ~27 KB: kept off the stack
   const bwd::host::AdamScalars k = bwd::host::adam_scalars(*hp);
   a.b1 = k.b1; a.omb1 = k.omb1; a.b2 = k.b2; a.omb2 = k.omb2;
@@ -310,21 +318,24 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
   a.grad_scale = grad_scale;
   a.chunk_start[0] = 0;
   int t = 0;
+  const auto flush = [&] {
+    if (t == 0) return BWD_OK;
+    a.num_tensors = t;
+    t = 0;
+    return launch_adam32(a, g_dtype, p_dtype, static_cast<cudaStream_t>(stream));
+  };
   for (int32_t i = 0; i < num_tensors; ++i) {
-    if (n[i] > 0) {
-      a.t[t] = Tensor32{p[i], g[i], m[i], v[i], n[i],
-                        aligned_to(p[i], 4 * bytes_of(p_dtype)) && aligned_to(g[i], 4 * bytes_of(g_dtype)) &&
-                            aligned16(m[i]) && aligned16(v[i])};
-      a.chunk_start[t + 1] = a.chunk_start[t] + chunks_of(n[i]);
-      ++t;
-    }
-    if (t == kMaxTensors || (t > 0 && i + 1 == num_tensors)) {
-      a.num_tensors = t;
-      if ((s = launch_adam32(a, g_dtype, p_dtype, sms, static_cast<cudaStream_t>(stream))) != BWD_OK) return s;
-      t = 0;
-    }
+    if (n[i] == 0) continue;
+    const int64_t chunks = chunks_of(n[i], kChunk);
+    if (t == kMaxTensors || a.chunk_start[t] + chunks > kMaxChunks)
+      if ((s = flush()) != BWD_OK) return s;
+    a.t[t] = Tensor32{p[i], g[i], m[i], v[i], n[i],
+                      aligned_to(p[i], 4 * bytes_of(p_dtype)) && aligned_to(g[i], 4 * bytes_of(g_dtype)) &&
+                          aligned16(m[i]) && aligned16(v[i])};
+    a.chunk_start[t + 1] = a.chunk_start[t] + chunks;
+    ++t;
   }
-  return BWD_OK;
+  return flush();
 }
 
 int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {
@@ -360,18 +371,21 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
   a.max_norm = max_norm;
   a.inv_loss_scale = 1.0f / loss_scale;
   const int64_t cap = static_cast<int64_t>(sms < 256 ? sms : 256) * kNormCtas;
-  // two passes: how many CTAs all launches have together, then the launches
+  const int64_t chunk = norm_chunk(g_dtype);
+  // two passes: how many CTAs all launches have together, then the launches;
+  // one pass where there is one launch
   int64_t slots = 0;
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = num_tensors > kNormTensors ? 0 : 1; pass < 2; ++pass) {
     int64_t first = 0;
     int t = 0;
     a.chunk_start[0] = 0;
     for (int32_t i = 0; i <= num_tensors; ++i) {
       if (i < num_tensors && n[i] > 0) {
         a.g[t] = g[i];
-        const int32_t tail = static_cast<int32_t>(n[i] - (chunks_of(n[i]) - 1) * kChunk);
-        a.n_tail[t] = aligned_to(g[i], 4 * bytes_of(g_dtype)) ? tail : -tail;
-        a.chunk_start[t + 1] = a.chunk_start[t] + chunks_of(n[i]);
+        const int64_t chunks = chunks_of(n[i], chunk);
+        const int32_t tail = static_cast<int32_t>(n[i] - (chunks - 1) * chunk);
+        a.n_tail[t] = aligned16(g[i]) ? tail : -tail;
+        a.chunk_start[t + 1] = a.chunk_start[t] + chunks;
         ++t;
       }
       // the last launch may have no tensors: it still forms the result
@@ -380,7 +394,7 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
         if (pass == 1) {
           a.num_tensors = t;
           a.first_slot = static_cast<int32_t>(first);
-          a.total_slots = static_cast<int32_t>(slots);
+          a.total_slots = static_cast<int32_t>(slots ? slots : ctas);
           cudaStream_t st = static_cast<cudaStream_t>(stream);
           const int grid = static_cast<int>(ctas);
           if (g_dtype == BWD_F32) grad_norm_kernel<kF32><<<grid, kThreads, 0, st>>>(a);
