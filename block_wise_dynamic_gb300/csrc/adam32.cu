@@ -101,21 +101,23 @@ __device__ __forceinline__ void store4(void* x, int64_t i, const float (&v)[4]) 
   }
 }
 
-// The last t with start[t] <= c, found by a warp in two reads of the table
-// (num <= 1024): which of 32 stretches, and where in it.
+// The last t with start[t] <= c: uniform reads of the table in parameter
+// space (a warp's ballot over 32 entries at a time reads lanes' own entries,
+// which that space serves one by one: 292 tensors 1.39 ms against 1.29).
 __device__ __forceinline__ int find_tensor(const int64_t* start, int num, int64_t c) {
-  const int lane = threadIdx.x % 32, step = (num + 31) / 32;
-  const int i = lane * step;
-  const int base = (__popc(__ballot_sync(0xffffffffu, i < num && start[i] <= c)) - 1) * step;
-  const int j = base + 1 + lane;
-  return base + __popc(__ballot_sync(0xffffffffu, lane < step - 1 && j < num && start[j] <= c));
+  int lo = 0, hi = num - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (start[mid] <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
 }
 
 // One CTA for each chunk of 1,024 elements.  Bound by DRAM (26 bytes a
 // parameter with fp32 parameters and bf16 gradients).  Against CTAs that walk
 // the chunks, four to an SM with twice the elements each, 32000 x 4096 bf16
 // parameters take 408 us instead of 431 (7.1 TB/s), and all of a 355M set
-// 1.31 ms instead of 1.43; prefetches of the next chunk into L2 made those
+// 1.29 ms instead of 1.43; prefetches of the next chunk into L2 made those
 // slower still (497 us).
 template <int kG, int kP>
 __global__ void __launch_bounds__(kThreads)

@@ -772,31 +772,44 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             v[j + 2] = __fadd_rn(v[j + 2], b.z); v[j + 3] = __fadd_rn(v[j + 3], b.w);
           }
         }
-        if (p.store) {
-          // a row of 128 bytes per lane, its 16-byte pieces swizzled as the tensor map says
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          __syncwarp();
+        // a row of 128 bytes per lane, its 16-byte pieces swizzled as the tensor map says
+        if (p.store && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint4 w;
-            if constexpr (kT == kF32) {
-              w = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
-            } else {
-              w = make_uint4(pack16<kT>(v[8 * q], v[8 * q + 1]), pack16<kT>(v[8 * q + 2], v[8 * q + 3]),
-                             pack16<kT>(v[8 * q + 4], v[8 * q + 5]), pack16<kT>(v[8 * q + 6], v[8 * q + 7]));
-            }
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+        for (int q = 0; q < 8; ++q) {
+          uint4 w;
+          if constexpr (kT == kF32) {
+            w = make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3]));
+          } else {
+            w = make_uint4(pack16<kT>(v[8 * q], v[8 * q + 1]), pack16<kT>(v[8 * q + 2], v[8 * q + 3]),
+                           pack16<kT>(v[8 * q + 4], v[8 * q + 5]), pack16<kT>(v[8 * q + 6], v[8 * q + 7]));
           }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
+        }
+        if (p.store) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0 && m0 < p.m && n0 + c < p.n) {
             tma_store(&map_out, n0 + c, m0, stage);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
-        } else if (m0 + lane < p.m) {
+        } else {
+          // rows of no 16-byte multiple: row by row, a lane to an element
+          __syncwarp();
+          constexpr int kEb = elem_bytes<kT>();
+          const int rows = p.m - m0 < 32 ? p.m - m0 : 32;
+#pragma unroll 8
+          for (int r = 0; r < rows; ++r)
 #pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            if (n0 + c + j < p.n) store1<kT>(p.out, (m0 + lane) * p.ldo + n0 + c + j, v[j]);
+            for (int h = 0; h < kCols; h += 32) {
+              const int j = h + lane, byte = j * kEb;
+              const uint8_t* const src = stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
+              if (n0 + c + j < p.n) {
+                if (kT == kF32) static_cast<float*>(p.out)[(m0 + r) * p.ldo + n0 + c + j] = *reinterpret_cast<const float*>(src);
+                else static_cast<uint16_t*>(p.out)[(m0 + r) * p.ldo + n0 + c + j] = *reinterpret_cast<const uint16_t*>(src);
+              }
+            }
+          __syncwarp();
         }
       }
       if (!kSum) ++use;
@@ -843,7 +856,14 @@ __device__ __forceinline__ void commit_one(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
 struct FewArgs {
+  const uint8_t* sfw;
+  const uint8_t* sfx;
   const void* bias;
   void* out;
   int64_t ldo;
@@ -858,7 +878,7 @@ struct FewArgs {
 template <int kT, int kBN>
 __global__ void __launch_bounds__(kMmThreads, 1)
 fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                      const __grid_constant__ CUtensorMap map_sfw, const __grid_constant__ CUtensorMap map_sfx, const FewArgs p) {
+                      const FewArgs p) {
   constexpr int kStages = few_stages<kBN>(), kW = kTile * kBK, kStage = few_stage_bytes<kBN>();
   constexpr uint32_t kCols = few_tmem<kBN>(), kSfCol = kCols - 16;
   constexpr int kAccs = few_accs<kBN>();
@@ -922,8 +942,8 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         }
         tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, &s_full[ring.s]);
         if (scales) {
-          tma_load_one(sf + ring.s * 2 * kSfTile, &map_sfw, 0, n0 / 128 * groups + kb / 4, &s_full[ring.s]);
-          tma_load_one(sf + ring.s * 2 * kSfTile + kSfTile, &map_sfx, 0, m0 / 128 * groups + kb / 4, &s_full[ring.s]);
+          bulk_load(sf + ring.s * 2 * kSfTile, p.sfw + (static_cast<int64_t>(n0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[ring.s]);
+          bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + (static_cast<int64_t>(m0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[ring.s]);
         }
       }
       __syncwarp();
@@ -1208,12 +1228,10 @@ bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, bool ea
 
 template <int kT, int kBN>
 bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool early, cudaStream_t st) {
-  MmMaps maps;
+  CUtensorMap map_w, map_x;
   bwd_status s;
-  if ((s = code_map(&maps.b, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
-  if ((s = code_map(&maps.a, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfb, w.scales, tiles_of(w.lines) * groups_of(p.k))) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfa, x.scales, tiles_of(x.lines) * groups_of(p.k))) != BWD_OK) return s;
+  if ((s = code_map(&map_w, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
+  if ((s = code_map(&map_x, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
   const int64_t tiles_n = tiles_of(p.n), tiles_m = (p.m + kBN - 1) / kBN, blocks = tiles_of(p.k);
   // as many parts of the summed axis as the device has room for at once, of two blocks each at least
   int64_t split = sms * few_ctas<kBN>() / (tiles_n * tiles_m);
@@ -1221,7 +1239,7 @@ bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool e
   split = split > blocks / 2 ? blocks / 2 : split;
   p.split = static_cast<int>(split < 1 ? 1 : split);
   return launch_ex(fp8_matmul_few_kernel<kT, kBN>, dim3(static_cast<unsigned>(tiles_n * p.split), static_cast<unsigned>(tiles_m)), p.split,
-                   few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", maps.b, maps.a, maps.sfb, maps.sfa, p);
+                   few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
 }
 
 template <int kT>
@@ -1247,7 +1265,7 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
   if (use_few(m, n, k, d->pairs)) {
-    const FewArgs p{bias, out, ldo, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
+    const FewArgs p{b.scales, a.scales, bias, out, ldo, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
     if (dtype == BWD_F32) return few<kF32>(a, b, p, d->sms, early, st);
     if (dtype == BWD_BF16) return few<kBF16>(a, b, p, d->sms, early, st);
     return few<kF16>(a, b, p, d->sms, early, st);
