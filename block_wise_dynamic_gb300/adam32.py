@@ -115,25 +115,26 @@ def adam32_step_multi(params, grads, m, v, *, lr=1e-3, beta1=0.9, beta2=0.999, e
 
 
 class GradNorm(_GradList):
-    """Norm of a fixed list of gradients.  Its workspace belongs to it: calls
-    of one object are made on one stream, or ordered by the caller."""
+    """Norm of a fixed list of gradients.  Its workspace and results belong to
+    it: calls of one object are made on one stream, or ordered by the caller,
+    and each writes the same two tensors again."""
 
     def __init__(self, grads: Sequence[torch.Tensor], device=None):
         if not grads and device is None:
             raise ValueError("an empty list needs a device")
         self._init_grads(grads, grads[0].device if grads else torch.device(device))
+        self.factor = torch.empty(1, dtype=torch.float32, device=self.device)
+        self.norm = torch.empty(1, dtype=torch.float32, device=self.device)
         self._work = torch.zeros(_lib.bwd_grad_norm_work_bytes(self.T), dtype=torch.uint8, device=self.device)
 
     def clip_scale(self, max_norm: float, loss_scale: float = 1.0, stream=None):
-        """(factor, norm) as float32 CUDA tensors of one element: norm of the
+        """(factor, norm), the object's float32 CUDA tensors of one element: norm of the
         gradients divided by ``loss_scale``, and the factor that divides by
         ``loss_scale`` and clips to ``max_norm``: min(1, max_norm / (norm +
         1e-6)) / loss_scale, NaN where the norm is not finite."""
-        factor = torch.empty(1, dtype=torch.float32, device=self.device)
-        norm = torch.empty(1, dtype=torch.float32, device=self.device)
-        _launch("bwd_grad_norm", self.device, stream, self.T, self.g, self.g_dtype, self.n, float(max_norm), float(loss_scale),
-                factor.data_ptr(), norm.data_ptr(), self._work.data_ptr())
-        return factor, norm
+        _launch("bwd_grad_norm", self.device, stream, self.T, self.g, self.g_dtype, self.n, max_norm, loss_scale,
+                self.factor.data_ptr(), self.norm.data_ptr(), self._work.data_ptr())
+        return self.factor, self.norm
 
 
 def clip_scale(grads: Sequence[torch.Tensor], max_norm: float, loss_scale: float = 1.0, stream=None):

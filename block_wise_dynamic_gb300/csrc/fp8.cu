@@ -416,6 +416,9 @@ __device__ __forceinline__ bool mbar_try(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 // Arrival on the same barrier of the pair's first CTA.
 __device__ __forceinline__ void mbar_arrive_leader(uint64_t* bar) {
   asm volatile("{\n .reg .b32 r;\n mapa.shared::cluster.u32 r, %0, 0;\n mbarrier.arrive.shared::cluster.b64 _, [r];\n}"
@@ -834,19 +837,30 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // its tensor memory; at the end CTA r gathers, from all of the cluster over
 // distributed shared memory, the r-th share of the columns and adds the parts
 // in the order of the ranks.
+//
+// Up to kFuse lines, A may also come unquantized: the warps that store in the
+// end then quantize each stage's 128 columns on the way into shared memory
+// while the weight's copies are under way, which saves the quantizer's launch
+// and its results' way through memory.  Every CTA of a rank quantizes the
+// same part of A again, so this pays for few lines only (33 x 4096 x 11008,
+// timed with a version of it for 64 lines: 18.9 us against 12.7).
 
-template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 64 ? 3 : kBN == 16 ? 5 : 4; }
+constexpr int kFuse = 16;
+constexpr int kFewThreads = 320;  // warp 0 copies, warp 1 issues, warps 2 to 9 quantize and store
+constexpr int kFewWarps = 8;
+template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 128 ? 3 : kBN >= 48 ? 4 : 5; }
 template <int kBN> __host__ __device__ constexpr int few_stage_bytes() { return kTile * kBK + kBN * kBK; }
-// stages, their scales, and the gathered parts: kBN columns of 128 fp32 sums
+// Stages and their scales; the gathered parts, at most kBN + 7 columns of 128
+// fp32 sums, take the stages' place.
 template <int kBN> __host__ __device__ constexpr int few_smem() {
-  return 1024 + few_stages<kBN>() * (few_stage_bytes<kBN>() + 2 * kSfTile) + (kBN + 8) * kTile * 4;
+  static_assert((kBN + 8) * kTile * 4 <= few_stages<kBN>() * few_stage_bytes<kBN>(), "the parts fit the stages");
+  return 1024 + few_stages<kBN>() * (few_stage_bytes<kBN>() + 2 * kSfTile);
 }
-// Up to 64 columns two CTAs share an SM and its tensor memory.  Accumulators
-// that fit beside the scales: sums move on to the next after kChunk blocks,
-// or later where that would take more of them.
-template <int kBN> __host__ __device__ constexpr int few_ctas() { return kBN == 128 ? 1 : 2; }
-template <int kBN> __host__ __device__ constexpr uint32_t few_tmem() { return kTmemCols / few_ctas<kBN>(); }
-template <int kBN> __host__ __device__ constexpr int few_accs() { return static_cast<int>(few_tmem<kBN>() - 16) / kBN; }
+// Two CTAs share an SM and its tensor memory.  Accumulators that fit beside
+// the scales: sums move on to the next after kChunk blocks, or later where
+// that would take more of them.
+constexpr uint32_t kFewCols = kTmemCols / 2, kFewSfCol = kFewCols - 16;
+template <int kBN> __host__ __device__ constexpr int few_accs() { return static_cast<int>(kFewSfCol) / kBN; }
 
 __device__ __forceinline__ void tma_load_one(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -867,83 +881,105 @@ struct FewArgs {
   const void* bias;
   void* out;
   int64_t ldo;
+  const void* x;         // A itself, `ldx` elements between lines, where the kernel quantizes it
+  int64_t ldx;
+  int vec;               // its lines start on 16-byte boundaries and hold whole 16-byte pieces
   int m, n, k;           // lines of A (columns here), lines of B (rows here), summed axis
   int a_trans, b_trans;
   int split;             // CTAs of a cluster, along the summed axis
 };
 
-// map_w: lines of B in boxes of 128; map_x: lines of A in boxes of kBN.  A
-// grid with several tiles of A's lines, or A transposed, needs kBN 128 (the
-// scales' tiles hold 128 lines).
-template <int kT, int kBN>
-__global__ void __launch_bounds__(kMmThreads, 1)
-fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-                      const FewArgs p) {
-  constexpr int kStages = few_stages<kBN>(), kW = kTile * kBK, kStage = few_stage_bytes<kBN>();
-  constexpr uint32_t kCols = few_tmem<kBN>(), kSfCol = kCols - 16;
-  constexpr int kAccs = few_accs<kBN>();
+// Eight consecutive values of a line of A from element e on, zero past k.
+template <int kT>
+__device__ __forceinline__ void few_load(const FewArgs& p, int line, int e, uint4 (&w)[kT == kF32 ? 2 : 1]) {
+  constexpr int kPieces = kT == kF32 ? 2 : 1, kVals = 16 / elem_bytes<kT>();
+  const char* const src = static_cast<const char*>(p.x) + (line * p.ldx + e) * elem_bytes<kT>();
+#pragma unroll
+  for (int q = 0; q < kPieces; ++q) {
+    w[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (line >= p.m) continue;
+    if (p.vec) {
+      if (e + q * kVals < p.k) w[q] = __ldg(reinterpret_cast<const uint4*>(src) + q);
+    } else {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j)
+        if (e + q * kVals + j < p.k) {
+          if (kT == kF32) (&w[q].x)[j] = reinterpret_cast<const uint32_t*>(src)[q * kVals + j];
+          else (&w[q].x)[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[q * kVals + j]) << (16 * (j % 2));
+        }
+    }
+  }
+}
+
+// map_w: lines of B in boxes of 128; map_x: all lines of A in one box of kBN
+// (128 where A is transposed: a swizzled row of its box).
+template <int kT, int kBN, bool kFused>
+__global__ void __launch_bounds__(kFewThreads, 2)
+fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const FewArgs p) {
+  static_assert(!kFused || kBN == kFuse, "scales of up to 32 lines lie in one column");
+  constexpr int kStages = few_stages<kBN>(), kW = kTile * kBK, kStage = few_stage_bytes<kBN>(), kAccs = few_accs<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sf = sm + kStages * kStage;
-  float* const parts = reinterpret_cast<float*>(sf + kStages * 2 * kSfTile);  // [rank][column of the share][128]
+  float* const parts = reinterpret_cast<float*>(sm);  // [rank][column of the share][128], once the stages are done with
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
-  if (threadIdx.x == 0) {
-    s_fail = 0;
-    for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
-    mbar_init(&s_done, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
+  const int n0 = static_cast<int>(blockIdx.x) / p.split * kTile;
+  // this CTA's blocks of the summed axis, and its accumulators' share of them
+  const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / p.split);
+  const int count = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / p.split) - kb0;
+  const int least = (count + kAccs - 1) / kAccs, chunk = least > kChunk ? least : kChunk;
+  const int accs = (count + chunk - 1) / chunk;
+
+  const auto weight = [&](int i, int s) {  // block i of this CTA's, into stage s
+    const int kb = kb0 + i;
+    const bool scales = i == 0 || (kb & 3) == 0;
+    mbar_expect_tx(&s_full[s], (kFused ? kW : kStage) + (scales ? (kFused ? 1 : 2) * kSfTile : 0));
+    tma_load_one(sm + s * kStage, &map_w, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, &s_full[s]);
+    if (scales)
+      bulk_load(sf + s * 2 * kSfTile, p.sfw + (static_cast<int64_t>(n0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[s]);
+  };
+  const int ahead = count < kStages ? count : kStages;
+  if (warp == 0) {
+    if (elect_one()) {
+      s_fail = 0;
+      for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], kFused ? 2 : 1); mbar_init(&s_empty[i], 1); }
+      mbar_init(&s_done, 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      // the first stages' weights do not depend on the kernel ahead
+      for (int i = 0; i < ahead; ++i) weight(i, i);
+    }
+    __syncwarp();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kCols) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kFewCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  cluster_sync();  // every CTA of the cluster runs before another writes to it
+  __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
-  const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
-  const int n0 = static_cast<int>(blockIdx.x) / p.split * kTile, m0 = static_cast<int>(blockIdx.y) * kBN;
-  // this CTA's blocks of the summed axis, and its accumulators' share of them
-  const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / p.split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / p.split);
-  const int least = (kb1 - kb0 + kAccs - 1) / kAccs, chunk = least > kChunk ? least : kChunk;
-  const int accs = (kb1 - kb0 + chunk - 1) / chunk;
 
   if (warp == 0) {
     const bool one = elect_one();
-    const auto weight = [&](int kb, int s) {
-      tma_load_one(sm + s * kStage, &map_w, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, &s_full[s]);
-    };
-    // the first stages' weights do not depend on the kernel ahead
-    const int ahead = kb1 - kb0 < kStages ? kb1 - kb0 : kStages;
-    if (one) {
-      for (int i = 0; i < ahead; ++i) {
-        mbar_expect_tx(&s_full[i], kStage + (i == 0 || ((kb0 + i) & 3) == 0 ? 2 * kSfTile : 0));
-        weight(kb0 + i, i);
-      }
-    }
-    __syncwarp();
     wait_for_inputs();
     Ring<kStages> ring;
-    for (int i = 0; i < kb1 - kb0; ++i, ring.next()) {
-      const int kb = kb0 + i;
-      const bool scales = i == 0 || (kb & 3) == 0;
+    for (int i = 0; i < count; ++i, ring.next()) {
       if (i >= ahead && !mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail)) break;
       if (one) {
-        if (i >= ahead) {
-          mbar_expect_tx(&s_full[ring.s], kStage + (scales ? 2 * kSfTile : 0));
-          weight(kb, ring.s);
-        }
-        tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, &s_full[ring.s]);
-        if (scales) {
-          bulk_load(sf + ring.s * 2 * kSfTile, p.sfw + (static_cast<int64_t>(n0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[ring.s]);
-          bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + (static_cast<int64_t>(m0 / 128) * groups + kb / 4) * kSfTile, kSfTile, &s_full[ring.s]);
+        if (i >= ahead) weight(i, ring.s);
+        if constexpr (!kFused) {
+          const int kb = kb0 + i;
+          tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? 0 : kb * kBK, p.a_trans ? kb * kBK : 0, &s_full[ring.s]);
+          if (i == 0 || (kb & 3) == 0)
+            bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + static_cast<int64_t>(kb / 4) * kSfTile, kSfTile,
+                      &s_full[ring.s]);
         }
       }
       __syncwarp();
@@ -958,24 +994,24 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     Ring<kStages> ring;
     uint32_t acc = tmem;
     int left = chunk;  // blocks that this accumulator still takes
-    for (int i = 0; i < kb1 - kb0; ++i, ring.next()) {
+    for (int i = 0; i < count; ++i, ring.next()) {
       const int kb = kb0 + i;
       if (!mbar_wait(&s_full[ring.s], ring.phase, &s_fail)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (one) {
         const uint64_t dw = dw0 + static_cast<uint32_t>(ring.s * (kStage / 16)), dx = dx0 + static_cast<uint32_t>(ring.s * (kStage / 16));
-        const uint32_t tsf = tmem + kSfCol + 8 * ((kb >> 2) & 1);
-        if (i == 0 || (kb & 3) == 0) {
-          const uint64_t d = dsf0 + static_cast<uint32_t>(ring.s * (2 * kSfTile / 16));
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf), "l"(d) : "memory");
-          asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tsf + 4), "l"(d + kSfTile / 16) : "memory");
-        }
-        const uint32_t id = idesc + static_cast<uint32_t>(kb & 3) * ((1u << 4) | (1u << 29));
+        const uint64_t d = dsf0 + static_cast<uint32_t>(ring.s * (2 * kSfTile / 16));
+        // two sets of scales of either operand; where A is quantized here, its stage holds that one block's
+        const uint32_t tw = tmem + kFewSfCol + 4 * ((kb >> 2) & 1), tx = tmem + kFewSfCol + 8 + 4 * ((kFused ? kb : kb >> 2) & 1);
+        const bool scales = i == 0 || (kb & 3) == 0;
+        if (scales) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tw), "l"(d) : "memory");
+        if (scales || kFused) asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tx), "l"(d + kSfTile / 16) : "memory");
+        const uint32_t id = idesc + static_cast<uint32_t>(kb & 3) * (kFused ? 1u << 29 : (1u << 4) | (1u << 29));
 #pragma unroll
         for (uint32_t q = 0; q < 4; ++q)
           asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
                        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-                       ::"r"(acc), "l"(dw + q * sw), "l"(dx + q * sx), "r"(id), "r"(tsf), "r"(tsf + 4),
+                       ::"r"(acc), "l"(dw + q * sw), "l"(dx + q * sx), "r"(id), "r"(tw), "r"(tx),
                        "r"(static_cast<uint32_t>(left != chunk || q != 0)) : "memory");
         commit_one(&s_empty[ring.s]);
       }
@@ -983,16 +1019,64 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
       if (--left == 0) { left = chunk; acc += kBN; }
     }
     if (one) commit_one(&s_done);
+  } else if constexpr (kFused) {
+    // A warp to each stage, sixteen lanes to a line, eight columns to a lane:
+    // the blocks' latencies overlap across the warps.  (All warps on each
+    // block, two lines to a warp: 1 x 4096 x 11008 10.7 us.)  A warp sees
+    // every phase of its own stage's barrier: it never runs two ahead, where
+    // a wait on the parity alone would let it pass.
+    static_assert(kStages <= kFewWarps, "a warp to each stage");
+    constexpr int kHalves = kBN / 2, kPieces = kT == kF32 ? 2 : 1;
+    const int part = lane % 16, first = lane / 16;
+    const int s = warp - 2;
+    uint32_t phase = 1;
+    for (int i = s < kStages ? s : count; i < count; i += kStages, phase ^= 1u) {
+      uint4 w[kHalves][kPieces];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        if (2 * h < p.m) few_load<kT>(p, first + 2 * h, (kb0 + i) * kBK + 8 * part, w[h]);
+      if (i >= kStages && !__all_sync(0xffffffffu, mbar_wait(&s_empty[s], phase, &s_fail))) break;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (2 * h >= p.m) break;
+        const int line = first + 2 * h;
+        uint32_t top = max_piece<kT>(w[h][0]);
+        if (kPieces == 2) top = max(top, max_piece<kT>(w[h][kPieces - 1]));
+        if (kT != kF32) top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t b = scale_byte(widen_bits<kT>(top));
+        const float inv = inv_scale(b);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(kT == kF32 ? piece<kT>(w[h][j / 4 % kPieces], j % 4) : piece<kT>(w[h][0], j), inv);
+        const uint2 codes = make_uint2(codes2(v[0], v[1]) | codes2(v[2], v[3]) << 16, codes2(v[4], v[5]) | codes2(v[6], v[7]) << 16);
+        // the 128-byte swizzle: 16-byte piece c of line l at c ^ (l mod 8)
+        *reinterpret_cast<uint2*>(sm + s * kStage + kW + line * kBK + (((part / 2) ^ (line & 7)) << 4) + (part & 1) * 8) = codes;
+        if (part == 0) *reinterpret_cast<uint32_t*>(sf + s * 2 * kSfTile + kSfTile + line * 16) = b;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_full[s]);
+    }
   }
   __syncwarp();
-  const int quarter = warp & 3, share = (kBN + p.split - 1) / p.split;  // columns that a CTA gathers
+  // warps w and w + 4 share a quarter of the rows and take turns at the columns
+  const int quarter = warp & 3, half = (warp - 2) / 4, share = (kBN + p.split - 1) / p.split;  // columns that a CTA gathers
+  const int row = quarter * 32 + lane;
   bool ok = true;
   if (warp >= 2) {
     ok = __all_sync(0xffffffffu, mbar_wait(&s_done, 0, &s_fail));
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    const int row = quarter * 32 + lane;
+  }
+  if (s_fail && lane == 0 && warp < 2) let_copies_land();
+  __syncwarp();
+  cluster_sync();  // every CTA is done with its stages: the parts may take their place
+  if (warp >= 2) {
 #pragma unroll
-    for (int c = 0; c < kBN; c += 16) {
+    for (int c0 = 0; c0 < kBN; c0 += 32) {
+      const int c = c0 + 16 * half;
+      if (c >= kBN || c >= p.m) break;
       float sum[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u) sum[u] = 0.0f;
@@ -1008,29 +1092,28 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
       }
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
+        if (c + u >= p.m) break;
         const int to = (c + u) / share, at = (static_cast<int>(rank) * share + (c + u) % share) * kTile + row;
         uint32_t dst;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + at)), "r"(to));
-        if (m0 + c + u < p.m) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(sum[u]) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(sum[u]) : "memory");
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
-  if (s_fail && lane == 0 && warp < 2) let_copies_land();
   __syncwarp();
   cluster_sync();
-  if (warp >= 2) {
-    const int row = quarter * 32 + lane;
-    const float bias = p.bias && n0 + row < p.n ? load1<kT>(p.bias, n0 + row) : 0.0f;
-    for (int c = 0; c < share; ++c) {
-      const int m = m0 + static_cast<int>(rank) * share + c;
-      if (static_cast<int>(rank) * share + c >= kBN || m >= p.m || n0 + row >= p.n || !ok) break;
+  if (warp >= 2 && ok && n0 + row < p.n) {
+    const float bias = p.bias ? load1<kT>(p.bias, n0 + row) : 0.0f;
+    for (int c = half; c < share; c += 2) {
+      const int m = static_cast<int>(rank) * share + c;
+      if (m >= p.m) break;
       float sum = parts[c * kTile + row];
       for (int r = 1; r < p.split; ++r) sum = __fadd_rn(sum, parts[(r * share + c) * kTile + row]);
       store1<kT>(p.out, m * p.ldo + n0 + row, p.bias ? __fadd_rn(sum, bias) : sum);
     }
   }
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kCols));
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewCols));
 }
 
 // A product over nothing: the bias, or zero.
@@ -1134,13 +1217,18 @@ cudaError_t opt_in(F* kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int kT>
+template <int kT, int kBN, bool kFused = false>
 cudaError_t opt_in_few() {
-  cudaError_t e = opt_in(fp8_matmul_few_kernel<kT, 16>, few_smem<16>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 32>, few_smem<32>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 64>, few_smem<64>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_few_kernel<kT, 128>, few_smem<128>());
-  return e;
+  return opt_in(fp8_matmul_few_kernel<kT, kBN, kFused>, few_smem<kBN>());
+}
+
+template <int kT>
+cudaError_t opt_in_all_few() {
+  const cudaError_t e[] = {opt_in_few<kT, 16>(), opt_in_few<kT, 32>(), opt_in_few<kT, 48>(), opt_in_few<kT, 64>(), opt_in_few<kT, 128>(),
+                           opt_in_few<kT, kFuse, true>()};
+  for (const cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 bwd_status ensure_device(const DeviceState** out) {
@@ -1161,9 +1249,9 @@ bwd_status ensure_device(const DeviceState** out) {
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false>, mm_smem<256>());
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 128, false>, mm_smem<128>());
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 128, false>, mm_smem<128>());
-  if (e == cudaSuccess) e = opt_in_few<kF32>();
-  if (e == cudaSuccess) e = opt_in_few<kBF16>();
-  if (e == cudaSuccess) e = opt_in_few<kF16>();
+  if (e == cudaSuccess) e = opt_in_all_few<kF32>();
+  if (e == cudaSuccess) e = opt_in_all_few<kBF16>();
+  if (e == cudaSuccess) e = opt_in_all_few<kF16>();
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(d.sms / 2 * 2));
@@ -1196,11 +1284,11 @@ struct Lines {
 
 // `early`: the launch may begin before the kernel ahead of it has ended.
 template <typename... Params, typename... Args>
-bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int cluster, int smem, bool early, cudaStream_t st, const char* what,
+bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int threads, int cluster, int smem, bool early, cudaStream_t st, const char* what,
                      const Args&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kMmThreads);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1222,38 +1310,55 @@ bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int cluster, int smem
 template <int kT, int kBN, bool kSum>
 bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, bool early, cudaStream_t st) {
   const int tiles = p.tiles_m * p.tiles_n;
-  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), 0, mm_smem<kBN>(), early, st,
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), kMmThreads, 0, mm_smem<kBN>(), early, st,
                    "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
 }
 
-template <int kT, int kBN>
-bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool early, cudaStream_t st) {
-  CUtensorMap map_w, map_x;
-  bwd_status s;
-  if ((s = code_map(&map_w, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
-  if ((s = code_map(&map_x, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
-  const int64_t tiles_n = tiles_of(p.n), tiles_m = (p.m + kBN - 1) / kBN, blocks = tiles_of(p.k);
-  // as many parts of the summed axis as the device has room for at once, of two blocks each at least
-  int64_t split = sms * few_ctas<kBN>() / (tiles_n * tiles_m);
+// As many parts of the summed axis as the device has room for at once, of two
+// blocks each at least.
+int64_t few_split(int64_t tiles_n, int64_t blocks, int sms) {
+  int64_t split = 2 * sms / tiles_n;
   split = split > 8 ? 8 : split;
   split = split > blocks / 2 ? blocks / 2 : split;
-  p.split = static_cast<int>(split < 1 ? 1 : split);
-  return launch_ex(fp8_matmul_few_kernel<kT, kBN>, dim3(static_cast<unsigned>(tiles_n * p.split), static_cast<unsigned>(tiles_m)), p.split,
-                   few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
+  return split < 1 ? 1 : split;
+}
+
+// x.codes null: A is p.x, quantized by the kernel.
+template <int kT, int kBN, bool kFused>
+bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool early, cudaStream_t st) {
+  CUtensorMap map_w, map_x{};
+  bwd_status s;
+  if ((s = code_map(&map_w, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
+  if (!kFused && (s = code_map(&map_x, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
+  const int64_t tiles_n = tiles_of(p.n);
+  p.split = static_cast<int>(few_split(tiles_n, tiles_of(p.k), sms));
+  return launch_ex(fp8_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles_n * p.split)),
+                   kFewThreads, p.split, few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
 }
 
 template <int kT>
 bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, int sms, bool early, cudaStream_t st) {
-  if (x.trans || p.m > 64) return launch_few<kT, 128>(x, w, p, sms, early, st);
-  if (p.m > 32) return launch_few<kT, 64>(x, w, p, sms, early, st);
-  if (p.m > 16) return launch_few<kT, 32>(x, w, p, sms, early, st);
-  return launch_few<kT, 16>(x, w, p, sms, early, st);
+  if (!x.codes) return launch_few<kT, kFuse, true>(x, w, p, sms, early, st);
+  if (x.trans) return launch_few<kT, 128, false>(x, w, p, sms, early, st);
+  if (p.m > 48) return launch_few<kT, 64, false>(x, w, p, sms, early, st);
+  if (p.m > 32) return launch_few<kT, 48, false>(x, w, p, sms, early, st);
+  if (p.m > 16) return launch_few<kT, 32, false>(x, w, p, sms, early, st);
+  return launch_few<kT, 16, false>(x, w, p, sms, early, st);
+}
+
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype, int sms, bool early, cudaStream_t st) {
+  if (dtype == BWD_F32) return few<kF32>(x, w, p, sms, early, st);
+  if (dtype == BWD_BF16) return few<kBF16>(x, w, p, sms, early, st);
+  return few<kF16>(x, w, p, sms, early, st);
 }
 
 // Whether a product goes to the kernel for few lines of A.
-bool use_few(int64_t m, int64_t n, int64_t k, int pairs) {
-  (void)n; (void)k; (void)pairs;
-  return m <= 128;
+bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, int sms) {
+  if (a.lines > 64) return false;
+  if (dtype != BWD_F32) return true;
+  // fp32 results: no accumulator may take much more than kChunk blocks
+  const int64_t part = (tiles_of(k) + few_split(tiles_of(n), tiles_of(k), sms) - 1) / few_split(tiles_of(n), tiles_of(k), sms);
+  return part <= 2 * kChunk * (a.trans ? few_accs<128>() : few_accs<64>());
 }
 
 // out = A B^T + bias, k > 0.
@@ -1264,15 +1369,18 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   const DeviceState* d = nullptr;
   bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
-  if (use_few(m, n, k, d->pairs)) {
-    const FewArgs p{b.scales, a.scales, bias, out, ldo, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
-    if (dtype == BWD_F32) return few<kF32>(a, b, p, d->sms, early, st);
-    if (dtype == BWD_BF16) return few<kBF16>(a, b, p, d->sms, early, st);
-    return few<kF16>(a, b, p, d->sms, early, st);
+  if (use_few(a, n, k, dtype, d->sms)) {
+    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
+    return few(a, b, p, dtype, d->sms, early, st);
   }
   const int64_t tiles_m = (m + kBM - 1) / kBM;
-  // 256 columns unless tiles of 128 are needed to give every pair one
-  const int bn = dtype == BWD_F32 || tiles_m * ((n + 255) / 256) < d->pairs ? 128 : 256;
+  // A tile of 256 columns takes up to one and a half times as long as one of
+  // 128 (per stage 0.24 us against 0.17 where few pairs work, 0.36 against
+  // 0.30 where all do): the wider one where it saves more waves than that.
+  // 256 x 4096 x 11008 15.1 us against 17.7, 512 x 4096 x 4096 11.3 against
+  // 14.9 the other way.
+  const auto waves = [&](int64_t width) { return (tiles_m * ((n + width - 1) / width) + d->pairs - 1) / d->pairs; };
+  const int bn = dtype != BWD_F32 && 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   const int64_t tiles_n = (n + bn - 1) / bn;
   if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
     return fail(BWD_ERR_INVALID_ARG, "too many tiles");
@@ -1450,6 +1558,7 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
 
 int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return -1;
+  if (rows <= kFuse) return 0;
   Pieces w{nullptr};
   w.take(rows * bwd_fp8_pitch(cols));
   w.take(bwd_fp8_scale_bytes(rows, cols));
@@ -1465,12 +1574,22 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   if (ldy < n) return fail(BWD_ERR_INVALID_ARG, "ldy is less than n");
   if (!x_col_codes != !x_col_scales) return fail(BWD_ERR_INVALID_ARG, "column codes and scales go together");
   const int eb = dtype == BWD_F32 ? 4 : 2;
-  const bool some = rows > 0 && cols > 0;
-  if ((rows > 0 && n > 0 && !y) || (some && !work) || (some && n > 0 && (!w || !w_scales))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  const bool some = rows > 0 && cols > 0, fused = rows <= kFuse;
+  if ((rows > 0 && n > 0 && !y) || (some && !fused && !work) || (some && n > 0 && (!w || !w_scales))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned_to(y, eb) || !aligned_to(bias, eb)) return fail(BWD_ERR_INVALID_ARG, "y and bias must be aligned to their element size");
   if (!aligned16(w) || !aligned16(w_scales) || !aligned16(x_col_codes) || !aligned16(work))
     return fail(BWD_ERR_INVALID_ARG, "codes, scales and work must be 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fused && some) {
+    if (x_col_codes && (s = quantize(x, dtype, rows, cols, ld, BWD_FP8_COLS, nullptr, nullptr, x_col_codes, x_col_scales, nullptr, nullptr, st)) != BWD_OK)
+      return s;
+    if (n == 0) return BWD_OK;
+    const DeviceState* d = nullptr;
+    if ((s = ensure_device(&d)) != BWD_OK) return s;
+    const FewArgs p{w_scales, nullptr, bias, y, ldy, x, ld, ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x),
+                    static_cast<int>(rows), static_cast<int>(n), static_cast<int>(cols), 0, 0, 1};
+    return few(Lines{nullptr, nullptr, rows, 0}, Lines{w, w_scales, n, 0}, p, dtype, d->sms, false, st);
+  }
   Pieces pieces{static_cast<uint8_t*>(work)};
   uint8_t* const codes = pieces.take(rows * bwd_fp8_pitch(cols));
   uint8_t* const scales = pieces.take(bwd_fp8_scale_bytes(rows, cols));

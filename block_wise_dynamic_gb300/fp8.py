@@ -31,27 +31,77 @@ from . import _GDT, _launch, _need
 __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
 
 _BLOCKS = {"rows": _abi.FP8_ROWS, "cols": _abi.FP8_COLS, "both": _abi.FP8_ROWS | _abi.FP8_COLS, "tiles": _abi.FP8_TILES}
+_FUSED_ROWS = 16  # rows that the library's product quantizes itself, without a workspace
 
 
 class Fp8Matrix:
     """A rows x cols matrix in e4m3 codes.  ``row_codes`` / ``row_scales`` are
     quantized in blocks along the rows, ``col_codes`` / ``col_scales`` along
     the columns (None where ``blocks`` has no such form); with "tiles" both
-    are the same codes."""
+    are the same codes.  All lie in one buffer."""
 
-    __slots__ = ("shape", "blocks", "dtype", "row_codes", "row_scales", "col_codes", "col_scales")
+    __slots__ = ("shape", "blocks", "dtype", "device", "buffer", "_places", "_pointers")
 
-    def __init__(self, shape, blocks, dtype, row_codes, row_scales, col_codes, col_scales):
-        self.shape, self.blocks, self.dtype = shape, blocks, dtype
-        self.row_codes, self.row_scales = row_codes, row_scales
-        self.col_codes, self.col_scales = col_codes, col_scales
+    def __init__(self, rows: int, cols: int, blocks: str, dtype, device):
+        kind = _BLOCKS[blocks]
+        self.shape, self.blocks, self.dtype, self.device = (rows, cols), blocks, dtype, device
+        codes = _round256(rows * _pitch(cols))
+        rc = rs = cc = cs = None
+        end = 0
+        if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
+            rc, rs = 0, codes
+            end = codes + _round256(_scale_bytes(rows, cols))
+        if kind & _abi.FP8_COLS:
+            cc, cs = end, end + codes
+            end += codes + _scale_bytes(cols, rows)
+        elif kind & _abi.FP8_TILES:
+            cc, cs = 0, end
+            end += _scale_bytes(cols, rows)
+        self.buffer = torch.empty(end, dtype=torch.uint8, device=device)
+        # of row codes, row scales, column codes, column scales: offsets in the buffer, addresses
+        base = self.buffer.data_ptr()
+        self._places = (rc, rs, cc, cs)
+        self._pointers = tuple(None if at is None else base + at for at in self._places)
+
+    def _view(self, which, size):
+        at = self._places[which]
+        return None if at is None else self.buffer[at:at + size]
+
+    def _codes(self, which):
+        rows, cols = self.shape
+        v = self._view(which, rows * _pitch(cols))
+        return None if v is None else v.view(rows, _pitch(cols))
 
     @property
-    def device(self):
-        return (self.row_codes if self.row_codes is not None else self.col_codes).device
+    def row_codes(self):
+        return self._codes(0)
+
+    @property
+    def row_scales(self):
+        return self._view(1, _scale_bytes(*self.shape))
+
+    @property
+    def col_codes(self):
+        return self._codes(2)
+
+    @property
+    def col_scales(self):
+        return self._view(3, _scale_bytes(self.shape[1], self.shape[0]))
 
     def dequantize(self, along="rows", dtype=None, stream=None):
         return dequantize(self, along, dtype, stream)
+
+
+def _pitch(cols: int) -> int:
+    return (cols + 15) // 16 * 16
+
+
+def _scale_bytes(count: int, length: int) -> int:
+    return (count + 127) // 128 * ((length + 511) // 512) * 512
+
+
+def _round256(n: int) -> int:
+    return (n + 255) // 256 * 256
 
 
 def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
@@ -69,18 +119,6 @@ def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
     if not x.is_contiguous() and (x.stride(1) != 1 or x.stride(0) < x.shape[1]):
         x = x.contiguous()
     return x
-
-
-def _pitch(cols: int) -> int:
-    return (cols + 15) // 16 * 16
-
-
-def _scale_bytes(count: int, length: int) -> int:
-    return (count + 127) // 128 * ((length + 511) // 512) * 512
-
-
-def _round256(n: int) -> int:
-    return (n + 255) // 256 * 256
 
 
 def _bytes(n: int, device: torch.device) -> torch.Tensor:
@@ -103,28 +141,23 @@ def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stre
     x = _matrix(x, "x")
     rows, cols = x.shape
     dev = x.device
-    rc = rs = cc = cs = sums = work = None
-    if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
-        rc = _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols))
-        rs = _bytes(_scale_bytes(rows, cols), dev)
-    if kind & (_abi.FP8_COLS | _abi.FP8_TILES):
-        cc = rc if kind == _abi.FP8_TILES else _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols))
-        cs = _bytes(_scale_bytes(cols, rows), dev)
+    q = Fp8Matrix(rows, cols, blocks, x.dtype, dev)
+    rc, rs, cc, cs = q._pointers
+    sums = work = None
     if col_sums:
         sums = torch.empty(cols, dtype=x.dtype, device=dev)
         work = torch.empty(max(1, (rows + 127) // 128 * cols), dtype=torch.float32, device=dev)
-    _launch("bwd_fp8_quantize", dev, stream, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, _ptr(rc), _ptr(rs),
-            _ptr(cc), _ptr(cs), _ptr(sums), _ptr(work))
-    q = Fp8Matrix((rows, cols), blocks, x.dtype, rc, rs, cc, cs)
+    _launch("bwd_fp8_quantize", dev, stream, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, rc, rs, cc, cs,
+            _ptr(sums), _ptr(work))
     return (q, sums) if col_sums else q
 
 
 def _lines(a: Fp8Matrix, trans: bool, name: str):
-    """Codes, scales, number and length of a matrix's lines."""
+    """Addresses of codes and scales, number and length of a matrix's lines."""
     if not isinstance(a, Fp8Matrix):
         raise TypeError(f"{name} must be an Fp8Matrix")
     rows, cols = a.shape
-    codes, scales = (a.col_codes, a.col_scales) if trans else (a.row_codes, a.row_scales)
+    codes, scales = a._pointers[2:] if trans else a._pointers[:2]
     if codes is None:
         raise ValueError(f'{name} has blocks "{a.blocks}", the product sums along its {"columns" if trans else "rows"}')
     return (codes, scales, cols, rows) if trans else (codes, scales, rows, cols)
@@ -140,9 +173,8 @@ def dequantize(a: Fp8Matrix, along: str = "rows", dtype=None, stream=None) -> to
     if dtype not in _GDT:
         raise TypeError("dtype must be float32, bfloat16 or float16")
     rows, cols = a.shape
-    out = torch.empty((rows, cols), dtype=dtype, device=codes.device)
-    _launch("bwd_fp8_dequantize", codes.device, stream, codes.data_ptr(), scales.data_ptr(), int(along == "rows"), rows, cols,
-            out.data_ptr(), _GDT[dtype])
+    out = torch.empty((rows, cols), dtype=dtype, device=a.device)
+    _launch("bwd_fp8_dequantize", a.device, stream, codes, scales, int(along == "rows"), rows, cols, out.data_ptr(), _GDT[dtype])
     return out
 
 
@@ -155,29 +187,30 @@ def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = Fa
     bc, bsc, n, kb = _lines(b, trans_b, "b")
     if k != kb:
         raise ValueError(f"a's lines have {k} elements, b's {kb}")
-    dev = ac.device
-    if bc.device != dev:
-        raise ValueError(f"b is on {bc.device}, the call runs on {dev}")
+    dev = a.device
+    if b.device != dev:
+        raise ValueError(f"b is on {b.device}, the call runs on {dev}")
     dtype = a.dtype if dtype is None else dtype
     if dtype not in _GDT:
         raise TypeError("dtype must be float32, bfloat16 or float16")
     if bias is not None:
         _need(bias, "bias", dtype, n, dev)
     out = torch.empty((m, n), dtype=dtype, device=dev)
-    _launch("bwd_fp8_matmul", dev, stream, m, n, k, ac.data_ptr(), int(trans_a), asc.data_ptr(), bc.data_ptr(), int(trans_b),
-            bsc.data_ptr(), _ptr(bias), out.data_ptr(), n, _GDT[dtype])
+    _launch("bwd_fp8_matmul", dev, stream, m, n, k, ac, int(trans_a), asc, bc, int(trans_b), bsc, _ptr(bias), out.data_ptr(), n,
+            _GDT[dtype])
     return out
 
 
 def _operands(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
-    """x as a matrix whose width is w's ``axis``, and w's codes and scales for
-    lines along it (the row form for axis 1, the column form for axis 0)."""
+    """x as a matrix whose width is w's ``axis``, and the addresses of w's codes
+    and scales for lines along it (the row form for axis 1, the column form
+    for axis 0)."""
     m = _matrix(x, name)
     codes, scales, _, width = _lines(w, axis == 0, "w")
     if m.shape[1] != width:
         raise ValueError(f"{name}'s last dimension must be {width}")
-    if codes.device != m.device:
-        raise ValueError(f"w is on {codes.device}, the call runs on {m.device}")
+    if w.device != m.device:
+        raise ValueError(f"w is on {w.device}, the call runs on {m.device}")
     return m, codes, scales
 
 
@@ -188,13 +221,14 @@ def _forward(x, w, bias, both, stream):
     if bias is not None:
         _need(bias, "bias", dt, n, dev)
     y = torch.empty((rows, n) if m is x else (*x.shape[:-1], n), dtype=dt, device=dev)
-    work = _bytes(_round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols)), dev)
-    cc = cs = xq = None
+    work = cc = cs = xq = None
+    if rows > _FUSED_ROWS:
+        work = _bytes(_round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols)), dev)
     if both:
-        cc, cs = _bytes(rows * _pitch(cols), dev).view(rows, _pitch(cols)), _bytes(_scale_bytes(cols, rows), dev)
-        xq = Fp8Matrix((rows, cols), "cols", dt, None, None, cc, cs)
-    _launch("bwd_fp8_linear", dev, stream, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes.data_ptr(), scales.data_ptr(), n,
-            _ptr(bias), y.data_ptr(), n, _ptr(cc), _ptr(cs), work.data_ptr())
+        xq = Fp8Matrix(rows, cols, "cols", dt, dev)
+        _, _, cc, cs = xq._pointers
+    _launch("bwd_fp8_linear", dev, stream, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes, scales, n, _ptr(bias),
+            y.data_ptr(), n, cc, cs, _ptr(work))
     return y, xq
 
 
@@ -222,8 +256,8 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
         if not isinstance(xq, Fp8Matrix) or tuple(xq.shape) != (rows, k):
             raise ValueError(f"xq must be an Fp8Matrix of shape {(rows, k)}")
         xc, xs, _, _ = _lines(xq, True, "xq")
-        if xc.device != dev:
-            raise ValueError(f"xq is on {xc.device}, the call runs on {dev}")
+        if xq.device != dev:
+            raise ValueError(f"xq is on {xq.device}, the call runs on {dev}")
         dw = torch.empty((n, k), dtype=dt, device=dev)
     if need_input:
         dx = torch.empty((rows, k) if m is dy else (*dy.shape[:-1], k), dtype=dt, device=dev)
@@ -232,8 +266,8 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
     codes_bytes = _round256(rows * _pitch(n))
     work = _bytes(2 * codes_bytes + _round256(_scale_bytes(rows, n)) + _round256(_scale_bytes(n, rows)) +
                   _round256((rows + 127) // 128 * n * 4), dev)
-    _launch("bwd_fp8_linear_backward", dev, stream, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes.data_ptr(), scales.data_ptr(),
-            _ptr(xc), _ptr(xs), k, _ptr(dx), k, _ptr(dw), k, _ptr(db), work.data_ptr())
+    _launch("bwd_fp8_linear_backward", dev, stream, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes, scales, xc, xs, k,
+            _ptr(dx), k, _ptr(dw), k, _ptr(db), work.data_ptr())
     return dx, dw, db
 
 

@@ -395,7 +395,9 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
  *   bias : n values of x's type, or NULL.   y : rows x n of x's type.
  *   x_col_codes, x_col_scales : both NULL, or written as for BWD_FP8_COLS
  *            (the backward pass reads them).
- *   work : device, 16-byte aligned, bwd_fp8_linear_work_bytes(rows, cols). */
+ *   work : device, 16-byte aligned, bwd_fp8_linear_work_bytes(rows, cols)
+ *            bytes; none, and NULL will do, for up to 16 rows, which the
+ *            product's kernel quantizes itself. */
 int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols);
 bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows,
                           int64_t cols, int64_t ld, const uint8_t* w,

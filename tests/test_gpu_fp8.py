@@ -154,6 +154,19 @@ def test_linear(fp8, m, n, k, bias, kind):
     near(got, want, size + (0 if b is None else np.abs(np64(b))), k, kind)
 
 
+# few rows over a long summed axis: every part of a cluster goes round its
+# stages several times
+LONG = [(1, 200, 20000), (3, 11008, 4096), (16, 300, 33000), (2, 40000, 2300), (33, 129, 20000), (64, 2000, 9000), (128, 130, 30011)]
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k", LONG)
+def test_few_rows_long_sums(fp8, m, n, k, kind):
+    x, w = draw((m, k), 21, kind), draw((n, k), 22, kind, 0.02, loud=False)
+    got = fp8.linear(x, fp8.quantize(w, "tiles"))
+    near(got, *ref.linear(np64(x), np64(w)), k, kind)
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("m,n,k", SIZES)
 def test_backward(fp8, m, n, k, kind):
