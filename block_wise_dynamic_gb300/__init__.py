@@ -272,10 +272,18 @@ class MultiTensorArgs:
         self.g[:] = [g.data_ptr() for g in grads]
 
     def step(self, *, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step,
-             stream=None) -> None:
+             stream=None, grad_scale=None) -> None:
+        """One step in place.  ``grad_scale``: a float32 CUDA tensor of one
+        element that multiplies every gradient, or None for 1; where it is not
+        finite the step writes nothing."""
         if self.T == 0:
             return
         hp = _hparams(lr, beta1, beta2, eps, step, weight_decay)
+        if grad_scale is not None:
+            _need(grad_scale, "grad_scale", torch.float32, 1, self.device)
+            return _launch("bwd_adam8bit_step_multi_scaled", self.device, stream, self.T, self.p, self.p_dtype, self.g,
+                           self.g_dtype, self.mc, self.ma, self.vc, self.va, self.n, grad_scale.data_ptr(),
+                           ctypes.byref(hp))
         with torch.cuda.device(self.device):
             st = _lib.bwd_adam8bit_step_multi_ex(
                 self.T, self.p, self.p_dtype, self.g, self.g_dtype, self.mc, self.ma, self.vc, self.va,

@@ -81,6 +81,10 @@ _SIGNATURES = {
         _int,
         [_i32, _pp, _int, _pp, _int, _pp, _pp, _pp, _pp, ctypes.POINTER(_i64), ctypes.POINTER(AdamHParams), _vp],
     ),
+    "bwd_adam8bit_step_multi_scaled": (
+        _int,
+        [_i32, _pp, _int, _pp, _int, _pp, _pp, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamHParams), _vp],
+    ),
     "bwd_zero_shard": (_int, [_i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "bwd_embedding_init": (_int, [_vp, _i64, _i64, _vp, _vp]),
     "bwd_embedding_xavier_bound": (ctypes.c_float, [_i64, _i64]),
@@ -92,7 +96,7 @@ _SIGNATURES = {
         _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamWHParams), _vp]),
     "bwd_grad_norm_work_bytes": (_i64, [_i32]),
     "bwd_grad_norm": (
-        _int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp]),
+        _int, [_i32, _pp, ctypes.POINTER(_i32), ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "bwd_fp8_pitch": (_i64, [_i64]),
     "bwd_fp8_scale_bytes": (_i64, [_i64, _i64]),
     "bwd_fp8_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),

@@ -50,24 +50,25 @@ class _GradList:
 
     def _init_grads(self, grads, device):
         self.T = len(grads)
-        self.g_dtype = _one_dtype(grads, "gradients")
         self.device = device
-        self._gdtype = grads[0].dtype if grads else None
         for i, g in enumerate(grads):
             _need(g, f"grads[{i}]", g.dtype, None, device)
+            if g.dtype not in _GDT:
+                raise TypeError("gradients must be float32, bfloat16 or float16")
         self._grads = list(grads)
+        self._dtypes = [g.dtype for g in grads]
         self.g = _pointers(grads)
         self._sizes = [g.numel() for g in grads]
         self.n = (ctypes.c_int64 * self.T)(*self._sizes)
 
     def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
-        """Points the table at new gradient tensors of the same sizes, dtype
+        """Points the table at new gradient tensors of the same sizes, dtypes
         and device (non-contiguous ones are copied)."""
         if len(grads) != self.T:
             raise ValueError(f"expected {self.T} gradients, got {len(grads)}")
-        dev, gdt = self.device, self._gdtype
-        if not all(isinstance(g, torch.Tensor) and g.dtype == gdt for g in grads):
-            raise TypeError(f"every gradient must be a {gdt} tensor, as when the table was built")
+        dev = self.device
+        if not all(isinstance(g, torch.Tensor) for g in grads) or [g.dtype for g in grads] != self._dtypes:
+            raise TypeError("every gradient must be a tensor of the dtype that the table was built for")
         if [g.numel() for g in grads] != self._sizes:
             raise ValueError("gradient sizes differ from those the table was built for")
         if not all(g.device == dev for g in grads):
@@ -86,6 +87,7 @@ class MultiTensorArgs32(_GradList):
         if not (len(grads) == len(m) == len(v) == len(params)):
             raise ValueError("all lists must have the same length")
         self.p_dtype = _one_dtype(params, "parameters")
+        self.g_dtype = _one_dtype(grads, "gradients")
         self._init_grads(grads, params[0].device if params else None)
         for i, p in enumerate(params):
             _need(p, f"params[{i}]", p.dtype, self._sizes[i], self.device)
@@ -115,7 +117,7 @@ def adam32_step_multi(params, grads, m, v, *, lr=1e-3, beta1=0.9, beta2=0.999, e
 
 
 class GradNorm(_GradList):
-    """Norm of a fixed list of gradients.  Its workspace and results belong to
+    """Norm of a fixed list of gradients, of any of the types.  Its workspace and results belong to
     it: calls of one object are made on one stream, or ordered by the caller,
     and each writes the same two tensors again."""
 
@@ -123,6 +125,7 @@ class GradNorm(_GradList):
         if not grads and device is None:
             raise ValueError("an empty list needs a device")
         self._init_grads(grads, grads[0].device if grads else torch.device(device))
+        self._types = (ctypes.c_int32 * self.T)(*[_GDT[d] for d in self._dtypes])
         self.factor = torch.empty(1, dtype=torch.float32, device=self.device)
         self.norm = torch.empty(1, dtype=torch.float32, device=self.device)
         self._work = torch.zeros(_lib.bwd_grad_norm_work_bytes(self.T), dtype=torch.uint8, device=self.device)
@@ -132,7 +135,7 @@ class GradNorm(_GradList):
         gradients divided by ``loss_scale``, and the factor that divides by
         ``loss_scale`` and clips to ``max_norm``: min(1, max_norm / (norm +
         1e-6)) / loss_scale, NaN where the norm is not finite."""
-        _launch("bwd_grad_norm", self.device, stream, self.T, self.g, self.g_dtype, self.n, max_norm, loss_scale,
+        _launch("bwd_grad_norm", self.device, stream, self.T, self.g, self._types, self.n, max_norm, loss_scale,
                 self.factor.data_ptr(), self.norm.data_ptr(), self._work.data_ptr())
         return self.factor, self.norm
 

@@ -37,25 +37,36 @@ def decompress_moments(m_codes, m_absmax, v_codes, v_absmax) -> Tuple[torch.Tens
 
 def load_from_fp32_adam(opt8, fp32_opt: torch.optim.Optimizer) -> None:
     """Fill an ``Adam8bit``/``AdamW8bit`` over the same parameters with the
-    compressed state of an fp32 ``torch.optim.Adam``/``AdamW``.  Parameters
-    without fp32 state are left untouched."""
+    compressed state of an fp32 ``torch.optim.Adam``/``AdamW`` (in fp32 as it
+    is, for groups with ``state_bits=32``).  Parameters without fp32 state are
+    left untouched."""
+    bits = {q: g.get("state_bits", 8) for g in opt8.param_groups for q in g["params"]}
     for p, st in fp32_opt.state.items():
         if "exp_avg" not in st:
             continue
-        if p not in {q for g in opt8.param_groups for q in g["params"]}:
+        if p not in bits:
             raise ValueError("the two optimizers must hold the same parameters")
-        mc, ma, vc, va = compress_moments(st["exp_avg"], st["exp_avg_sq"])
         step = st.get("step", 0)
         step = int(step.item()) if torch.is_tensor(step) else int(step)
+        if bits[p] == 32:
+            opt8.state[p] = {"step": step, **{k: st[k].detach().reshape(-1).to(torch.float32, copy=True)
+                                              for k in ("exp_avg", "exp_avg_sq")}}
+            continue
+        mc, ma, vc, va = compress_moments(st["exp_avg"], st["exp_avg_sq"])
         opt8.state[p] = {"step": step, "m_codes": mc, "m_absmax": ma, "v_codes": vc, "v_absmax": va}
     opt8._reset_plans()
 
 
 def export_fp32_adam_state(opt8) -> Dict[torch.Tensor, dict]:
-    """Per parameter: {"step", "exp_avg", "exp_avg_sq"} decompressed to fp32,
-    shaped like the parameter (the keys ``torch.optim.Adam`` uses)."""
+    """Per parameter: {"step", "exp_avg", "exp_avg_sq"} decompressed to fp32
+    (or as they are, where the state is fp32), shaped like the parameter (the
+    keys ``torch.optim.Adam`` uses)."""
     out = {}
     for p, st in opt8.state.items():
+        if "exp_avg" in st:
+            out[p] = {"step": torch.tensor(float(st["step"])), "exp_avg": st["exp_avg"].clone().view_as(p),
+                      "exp_avg_sq": st["exp_avg_sq"].clone().view_as(p)}
+            continue
         if "m_codes" not in st:
             continue
         m, v = decompress_moments(st["m_codes"], st["m_absmax"], st["v_codes"], st["v_absmax"])

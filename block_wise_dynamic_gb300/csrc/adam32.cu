@@ -166,13 +166,13 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
 constexpr int kNormTensors = 1024;
 constexpr int kNormCtas = 8;   // per SM
 constexpr int kNormPieces = 4;
-template <int kT> __host__ __device__ constexpr int norm_vals() { return kT == kF32 ? 4 : 8; }  // values of a piece
 __host__ __device__ constexpr int norm_chunk(int type) { return kThreads * kNormPieces * (type == BWD_F32 ? 4 : 8); }
 
 struct NormArgs {
   int64_t chunk_start[kNormTensors + 1];
   const void* g[kNormTensors];
   int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where 16-byte loads are not possible
+  uint8_t type[kNormTensors];
   double* slots;                 // one per CTA of all launches of the call
   unsigned int* ticket;          // 0 before the call and after it
   float* factor;
@@ -195,12 +195,42 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   return x;
 }
 
+// Sum of squares of this thread's share of one chunk of `len` elements.
 template <int kG>
+__device__ __forceinline__ float chunk_squares(const void* g, int len, bool vec) {
+  constexpr int kVals = kG == kF32 ? 4 : 8;  // values of a piece
+  uint4 w[kNormPieces];
+#pragma unroll
+  for (int q = 0; q < kNormPieces; ++q) {
+    const int i = (q * kThreads + threadIdx.x) * kVals;
+    w[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (vec && i + kVals <= len) w[q] = __ldcs(static_cast<const uint4*>(g) + q * kThreads + threadIdx.x);
+  }
+  float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+  for (int q = 0; q < kNormPieces; ++q) {
+    const int i = (q * kThreads + threadIdx.x) * kVals;
+    if (vec && i + kVals <= len) {
+#pragma unroll
+      for (int j = 0; j < kVals; ++j) {
+        const uint32_t u = (&w[q].x)[kG == kF32 ? j : j / 2];
+        const float x = kG == kF32 ? __uint_as_float(u) : widen<kG>(static_cast<unsigned short>(j % 2 ? u >> 16 : u & 0xffffu));
+        sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
+      }
+    } else {
+      for (int j = 0; j < kVals && i + j < len; ++j) {
+        const float x = load1<kG>(g, i + j);
+        sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
+      }
+    }
+  }
+  return __fadd_rn(sum[0], sum[1]);
+}
+
 __global__ void __launch_bounds__(kThreads, kNormCtas)
 grad_norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ double s_red[kThreads / 32];
   __shared__ bool s_last;
-  constexpr int kVals = norm_vals<kG>();
   const int64_t total = a.chunk_start[a.num_tensors];
   int64_t c = blockIdx.x;
   double part = 0.0;
@@ -208,35 +238,14 @@ grad_norm_kernel(const __grid_constant__ NormArgs a) {
     int ti = find_tensor(a.chunk_start, a.num_tensors, c);
     for (; c < total; c += gridDim.x) {
       while (a.chunk_start[ti + 1] <= c) ++ti;
+      const int type = a.type[ti];
       const bool last = c + 1 == a.chunk_start[ti + 1], vec = a.n_tail[ti] > 0;
-      const int len = last ? abs(a.n_tail[ti]) : norm_chunk(kG);
-      const char* const g = static_cast<const char*>(a.g[ti]) + (c - a.chunk_start[ti]) * norm_chunk(kG) * (16 / kVals);
-      uint4 w[kNormPieces];
-#pragma unroll
-      for (int q = 0; q < kNormPieces; ++q) {
-        const int i = (q * kThreads + threadIdx.x) * kVals;
-        w[q] = make_uint4(0u, 0u, 0u, 0u);
-        if (vec && i + kVals <= len) w[q] = __ldcs(reinterpret_cast<const uint4*>(g) + q * kThreads + threadIdx.x);
-      }
-      float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int q = 0; q < kNormPieces; ++q) {
-        const int i = (q * kThreads + threadIdx.x) * kVals;
-        if (vec && i + kVals <= len) {
-#pragma unroll
-          for (int j = 0; j < kVals; ++j) {
-            const uint32_t u = (&w[q].x)[kG == kF32 ? j : j / 2];
-            const float x = kG == kF32 ? __uint_as_float(u) : widen<kG>(static_cast<unsigned short>(j % 2 ? u >> 16 : u & 0xffffu));
-            sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
-          }
-        } else {
-          for (int j = 0; j < kVals && i + j < len; ++j) {
-            const float x = load1<kG>(g, i + j);
-            sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
-          }
-        }
-      }
-      part += static_cast<double>(__fadd_rn(sum[0], sum[1]));
+      const int len = last ? abs(a.n_tail[ti]) : norm_chunk(type);
+      // a chunk is 64 bytes to a thread, whatever the type
+      const char* const g = static_cast<const char*>(a.g[ti]) + (c - a.chunk_start[ti]) * (kThreads * kNormPieces * 16);
+      const float sum = type == kF32 ? chunk_squares<kF32>(g, len, vec)
+                        : type == kBF16 ? chunk_squares<kBF16>(g, len, vec) : chunk_squares<kF16>(g, len, vec);
+      part += static_cast<double>(sum);
     }
   }
   const double mine = block_sum(part, s_red);
@@ -347,19 +356,19 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {
   return 16 + 8 * launches * 256 * kNormCtas;
 }
 
-bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_dtype, const int64_t* n, float max_norm,
+bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, const int32_t* g_dtype, const int64_t* n, float max_norm,
                          float loss_scale, float* factor, float* norm, void* work, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
-  if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
   if (!(max_norm > 0.0f)) return fail(BWD_ERR_INVALID_ARG, "max_norm must be > 0");
   if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale) || !std::isfinite(1.0f / loss_scale))
     return fail(BWD_ERR_INVALID_ARG, "loss_scale and its reciprocal must be finite and > 0");
-  if (!factor || !norm || !work || (num_tensors > 0 && (!g || !n))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  if (!factor || !norm || !work || (num_tensors > 0 && (!g || !g_dtype || !n))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned_to(factor, 4) || !aligned_to(norm, 4) || !aligned16(work))
     return fail(BWD_ERR_INVALID_ARG, "factor and norm must be 4-byte and work 16-byte aligned");
   for (int32_t i = 0; i < num_tensors; ++i) {
     if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
-    if (n[i] > 0 && (!g[i] || !aligned_to(g[i], bytes_of(g_dtype))))
+    if (!valid_type(g_dtype[i])) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "tensor %d: gradient dtype %d", i, (int)g_dtype[i]);
+    if (n[i] > 0 && (!g[i] || !aligned_to(g[i], bytes_of(g_dtype[i]))))
       return fail(BWD_ERR_INVALID_ARG, "tensor %d: NULL or unaligned pointer", i);
   }
   int sms = 0;
@@ -373,7 +382,6 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
   a.max_norm = max_norm;
   a.inv_loss_scale = 1.0f / loss_scale;
   const int64_t cap = static_cast<int64_t>(sms < 256 ? sms : 256) * kNormCtas;
-  const int64_t chunk = norm_chunk(g_dtype);
   // two passes: how many CTAs all launches have together, then the launches;
   // one pass where there is one launch
   int64_t slots = 0;
@@ -384,7 +392,8 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
     for (int32_t i = 0; i <= num_tensors; ++i) {
       if (i < num_tensors && n[i] > 0) {
         a.g[t] = g[i];
-        const int64_t chunks = chunks_of(n[i], chunk);
+        const int64_t chunk = norm_chunk(g_dtype[i]), chunks = chunks_of(n[i], chunk);
+        a.type[t] = static_cast<uint8_t>(g_dtype[i]);
         const int32_t tail = static_cast<int32_t>(n[i] - (chunks - 1) * chunk);
         a.n_tail[t] = aligned16(g[i]) ? tail : -tail;
         a.chunk_start[t + 1] = a.chunk_start[t] + chunks;
@@ -399,9 +408,7 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, bwd_dtype g_
           a.total_slots = static_cast<int32_t>(slots ? slots : ctas);
           cudaStream_t st = static_cast<cudaStream_t>(stream);
           const int grid = static_cast<int>(ctas);
-          if (g_dtype == BWD_F32) grad_norm_kernel<kF32><<<grid, kThreads, 0, st>>>(a);
-          else if (g_dtype == BWD_BF16) grad_norm_kernel<kBF16><<<grid, kThreads, 0, st>>>(a);
-          else grad_norm_kernel<kF16><<<grid, kThreads, 0, st>>>(a);
+          grad_norm_kernel<<<grid, kThreads, 0, st>>>(a);
           if ((s = check_launch("grad_norm_kernel launch")) != BWD_OK) return s;
         }
         first += ctas;

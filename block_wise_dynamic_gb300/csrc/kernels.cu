@@ -543,6 +543,7 @@ struct AdamArgs {
   int32_t num_tensors;
   float b1, omb1, b2, omb2, eps, step_size, inv_bc2s;
   float decay;  // 1 - lr * weight_decay (decoupled weight decay), 1 for Adam
+  const float* grad_scale;  // device factor of every gradient (kScale)
 };
 
 static_assert(sizeof(AdamArgs) <= 32764, "kernel parameter space");
@@ -653,8 +654,10 @@ int adam_smem_of(int p_type) {
 }
 
 // kG: gradient type; kP: parameter type (kF32, kBF16 or kF16; 16-bit
-// parameters are widened for the update and rounded back on store).
-template <int kG, int kP>
+// parameters are widened for the update and rounded back on store).  kScale:
+// gradients are multiplied by a factor read from device memory first; where
+// it is not finite nothing is written.
+template <int kG, int kP, bool kScale = false>
 __global__ void __launch_bounds__(kGroup * adam_groups<kG, kP>(), 1)
 adam8bit_kernel(const __grid_constant__ AdamArgs args) {
   constexpr int kGroups = adam_groups<kG, kP>();
@@ -691,6 +694,8 @@ adam8bit_kernel(const __grid_constant__ AdamArgs args) {
 
   const float b1 = args.b1, omb1 = args.omb1, b2 = args.b2, omb2 = args.omb2;
   const float eps = args.eps, step_size = args.step_size, inv_bc2s = args.inv_bc2s, decay = args.decay;
+  const float scale = kScale ? *args.grad_scale : 1.0f;
+  if (kScale && !(fabsf(scale) <= 3.402823466e38f)) return;
   const float* map_s = tab.map[0];
   const float* map_u = tab.map[1];
   const unsigned char* const rep_b = reinterpret_cast<const unsigned char*>(rep4);
@@ -816,7 +821,7 @@ adam8bit_kernel(const __grid_constant__ AdamArgs args) {
           mo = bwd::mul2(make_float2(map_s[im0], map_s[im1]), ma2);
           vo = bwd::mul2(make_float2(map_u[iv0], map_u[iv1]), va2);
         }
-        const float2 g2 = make_float2(g[j], g[j + 1]);
+        const float2 g2 = kScale ? bwd::mul2(make_float2(g[j], g[j + 1]), bwd::dup2(scale)) : make_float2(g[j], g[j + 1]);
         // products packed, sums scalar: a packed multiply feeding a packed add
         // may be contracted into one fused operation, which would change the
         // rounding
@@ -994,7 +999,7 @@ struct DeviceState {
   int num_sms = 0;
   int occ_quant[2] = {0, 0};
   int occ_dequant[2] = {0, 0};
-  int occ_adam[9] = {};  // [3 * parameter type + gradient type]
+  int occ_adam[18] = {};  // [9 * scaled + 3 * parameter type + gradient type]
 };
 
 std::mutex g_mu;
@@ -1044,18 +1049,19 @@ bwd_status ensure_device(DeviceState** out) {
                        reinterpret_cast<const void*>(quantize_kernel<false>)};
   const void* kd[2] = {reinterpret_cast<const void*>(dequantize_kernel<true>),
                        reinterpret_cast<const void*>(dequantize_kernel<false>)};
-  const void* ka[9] = {
-      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF32>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF32>),
-      reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF32>), reinterpret_cast<const void*>(adam8bit_kernel<kF32, kBF16>),
-      reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kBF16>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kBF16>),
-      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF16>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF16>),
-      reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF16>)};
+  const void* ka[18] = {
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF32, false>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF32, false>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF32, false>),
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kBF16, false>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kBF16, false>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kBF16, false>),
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF16, false>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF16, false>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF16, false>),
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF32, true>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF32, true>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF32, true>),
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kBF16, true>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kBF16, true>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kBF16, true>),
+      reinterpret_cast<const void*>(adam8bit_kernel<kF32, kF16, true>), reinterpret_cast<const void*>(adam8bit_kernel<kBF16, kF16, true>), reinterpret_cast<const void*>(adam8bit_kernel<kF16, kF16, true>)};
   for (int k = 0; k < 2; ++k) {
     if ((s = occupancy(kq[k], kQCta, k == 0 ? kQSmemBytes : kTablesBytes, &d.occ_quant[k])) != BWD_OK) return s;
     if ((s = occupancy(kd[k], kDeqThreads, 0, &d.occ_dequant[k])) != BWD_OK) return s;
   }
-  for (int k = 0; k < 9; ++k)
-    if ((s = occupancy(ka[k], kGroup * adam_groups_of(k / 3, k % 3), adam_smem_of(k / 3), &d.occ_adam[k])) != BWD_OK)
+  for (int k = 0; k < 18; ++k)
+    if ((s = occupancy(ka[k], kGroup * adam_groups_of(k % 9 / 3, k % 3), adam_smem_of(k % 9 / 3), &d.occ_adam[k])) != BWD_OK)
       return s;
   d.ctx = ctx;
   d.ready = true;
@@ -1090,13 +1096,14 @@ void fill_scalars(const bwd_adam_hparams* hp, AdamArgs* a) {
 
 template <int kG, int kP>
 void launch_typed(const AdamArgs& a, int grid, cudaStream_t st) {
-  adam8bit_kernel<kG, kP><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
+  if (a.grad_scale) adam8bit_kernel<kG, kP, true><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
+  else adam8bit_kernel<kG, kP><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
 }
 
 bwd_status launch_adam_chunk(const AdamArgs& a, int g_type, int p_type, const DeviceState& d, cudaStream_t st) {
   const int64_t total = a.block_start[a.num_tensors];
   if (total == 0) return BWD_OK;
-  const int grid = grid_for(total, adam_groups_of(p_type, g_type), d, d.occ_adam[3 * p_type + g_type]);
+  const int grid = grid_for(total, adam_groups_of(p_type, g_type), d, d.occ_adam[(a.grad_scale ? 9 : 0) + 3 * p_type + g_type]);
   switch (3 * p_type + g_type) {
     case 0: launch_typed<kF32, kF32>(a, grid, st); break;
     case 1: launch_typed<kBF16, kF32>(a, grid, st); break;
@@ -1205,7 +1212,7 @@ namespace {
 template <typename PP>
 bwd_status step_multi(int32_t num_tensors, PP p, bwd_dtype p_dtype, const void* const* g, bwd_dtype g_dtype,
                       uint8_t* const* m_codes, float* const* m_absmax, uint8_t* const* v_codes,
-                      float* const* v_absmax, const int64_t* n, const bwd_adam_hparams* hp, void* stream) {
+                      float* const* v_absmax, const int64_t* n, const float* grad_scale, const bwd_adam_hparams* hp, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
   if (g_dtype != BWD_F32 && g_dtype != BWD_BF16 && g_dtype != BWD_F16)
     return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
@@ -1216,6 +1223,7 @@ bwd_status step_multi(int32_t num_tensors, PP p, bwd_dtype p_dtype, const void* 
   if (num_tensors == 0) return BWD_OK;
   if (!p || !g || !m_codes || !m_absmax || !v_codes || !v_absmax || !n)
     return fail(BWD_ERR_INVALID_ARG, "NULL array");
+  if (!aligned_to(grad_scale, 4)) return fail(BWD_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
   bool any_work = false;
   for (int32_t i = 0; i < num_tensors; ++i) {
     if (n[i] < 0) return fail(BWD_ERR_INVALID_ARG, "tensor %d: n < 0", i);
@@ -1232,6 +1240,7 @@ bwd_status step_multi(int32_t num_tensors, PP p, bwd_dtype p_dtype, const void* 
 
   static thread_local AdamArgs a;  // ~32 KB: kept off the stack
   fill_scalars(hp, &a);
+  a.grad_scale = grad_scale;
   const int g_type = static_cast<int>(g_dtype), p_type = static_cast<int>(p_dtype);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int k = 0;
@@ -1271,7 +1280,7 @@ bwd_status bwd_adam8bit_step_multi(int32_t num_tensors, float* const* p, const v
                                    bwd_dtype g_dtype, uint8_t* const* m_codes, float* const* m_absmax,
                                    uint8_t* const* v_codes, float* const* v_absmax, const int64_t* n,
                                    const bwd_adam_hparams* hp, void* stream) {
-  return step_multi(num_tensors, p, BWD_F32, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, hp, stream);
+  return step_multi(num_tensors, p, BWD_F32, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, hp, stream);
 }
 
 bwd_status bwd_adam8bit_step_multi_ex(int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
@@ -1279,7 +1288,15 @@ bwd_status bwd_adam8bit_step_multi_ex(int32_t num_tensors, void* const* p, bwd_d
                                       float* const* m_absmax, uint8_t* const* v_codes,
                                       float* const* v_absmax, const int64_t* n,
                                       const bwd_adam_hparams* hp, void* stream) {
-  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, hp, stream);
+  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, hp, stream);
+}
+
+bwd_status bwd_adam8bit_step_multi_scaled(int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
+                                          const void* const* g, bwd_dtype g_dtype, uint8_t* const* m_codes,
+                                          float* const* m_absmax, uint8_t* const* v_codes,
+                                          float* const* v_absmax, const int64_t* n, const float* grad_scale,
+                                          const bwd_adam_hparams* hp, void* stream) {
+  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, grad_scale, hp, stream);
 }
 
 bwd_status bwd_adam8bit_step(float* p, const void* g, bwd_dtype g_dtype, uint8_t* m_codes,

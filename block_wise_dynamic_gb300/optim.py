@@ -14,7 +14,16 @@ the update, stored back rounded to nearest even); gradients fp32, bf16 or
 fp16.  Per parameter the state holds ``step`` and the codes and absmax of
 both moments; ``state_dict()`` / ``load_state_dict()`` round-trip them
 exactly.  Each ``step()`` issues one multi-tensor launch per (device,
-gradient dtype, step count) group.  The launch tables are built once per
+gradient dtype, step count) group.  A parameter group with ``state_bits=32``
+(an embedding, norms, biases) keeps its moments in fp32 (``exp_avg``,
+``exp_avg_sq``) and takes the 32-bit step.  ``clip_scale`` computes the norm
+of all gradients and the clipping factor on the device, and ``step`` takes
+that factor:
+
+    factor, norm = opt.clip_scale(1.0)
+    opt.step(grad_scale=factor)
+
+The launch tables are built once per
 parameter group and reused: when gradients are fresh tensors each step (the
 default ``zero_grad(set_to_none=True)``), a step only re-reads the gradient
 pointers.
@@ -26,7 +35,7 @@ from collections import defaultdict
 
 import torch
 
-from . import MultiTensorArgs, num_blocks, state_init
+from . import GradNorm, MultiTensorArgs, MultiTensorArgs32, num_blocks, state_init
 
 
 class Adam8bit(torch.optim.Optimizer):
@@ -35,7 +44,7 @@ class Adam8bit(torch.optim.Optimizer):
 
     _decoupled = False
 
-    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0):
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8):
         if lr < 0.0:
             raise ValueError(f"invalid learning rate {lr}")
         if not (0.0 <= betas[0] < 1.0 and 0.0 <= betas[1] < 1.0):
@@ -44,18 +53,25 @@ class Adam8bit(torch.optim.Optimizer):
             raise ValueError(f"invalid eps {eps}")
         if weight_decay < 0.0 or (weight_decay != 0.0 and not self._decoupled):
             raise ValueError("Adam8bit takes no weight decay; AdamW8bit applies it decoupled")
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
+        if any(g["state_bits"] not in (8, 32) for g in self.param_groups):
+            raise ValueError("state_bits must be 8 or 32")
         self._args_cache = {}
+        self._norm = None
 
-    def _state_for(self, p: torch.Tensor):
+    def _state_for(self, p: torch.Tensor, bits: int):
         st = self.state[p]
-        if len(st) == 0:
+        if len(st) == 0 and bits == 32:
+            st["step"] = 0
+            st["exp_avg"] = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
+            st["exp_avg_sq"] = torch.zeros(p.numel(), dtype=torch.float32, device=p.device)
+        elif len(st) == 0:
             mc, ma, vc, va = state_init(p.numel(), p.device)
             st["step"] = 0
             st["m_codes"], st["m_absmax"], st["v_codes"], st["v_absmax"] = mc, ma, vc, va
         return st
 
-    def _plan(self, params, grads):
+    def _plan(self, params, grads, bits):
         """Launch plan of one parameter group: its parameters with a gradient,
         bucketed by (device, parameter dtype, gradient dtype, step count), each
         bucket with its argument table (parameter and state pointers fixed)."""
@@ -67,24 +83,49 @@ class Adam8bit(torch.optim.Optimizer):
                 raise TypeError("Adam8bit needs fp32, bf16 or fp16 CUDA parameters")
             if g.is_sparse:
                 raise TypeError("sparse gradients are not supported")
-            st = self._state_for(p)
-            if st["m_absmax"].numel() != num_blocks(p.numel()):
+            st = self._state_for(p, bits)
+            if ("exp_avg" in st) != (bits == 32):
+                raise ValueError(f"the state of a parameter is not the one of state_bits={bits}")
+            if bits == 8 and st["m_absmax"].numel() != num_blocks(p.numel()):
                 raise ValueError("state does not match the parameter size")
             buckets[(p.device, p.dtype, g.dtype, st["step"])].append(i)
         plan = []
         for (_, _, _, t), idx in buckets.items():
             sts = [self.state[params[i]] for i in idx]
             gs = [grads[i] if grads[i].is_contiguous() else grads[i].contiguous() for i in idx]
-            args = MultiTensorArgs(
-                [params[i].view(-1) for i in idx], [g.view(-1) for g in gs],
-                [s["m_codes"] for s in sts], [s["m_absmax"] for s in sts],
-                [s["v_codes"] for s in sts], [s["v_absmax"] for s in sts],
-            )
+            lists = [params[i].view(-1) for i in idx], [g.view(-1) for g in gs]
+            if bits == 32:
+                args = MultiTensorArgs32(*lists, [s["exp_avg"].view(-1) for s in sts], [s["exp_avg_sq"].view(-1) for s in sts])
+            else:
+                args = MultiTensorArgs(*lists, [s["m_codes"] for s in sts], [s["m_absmax"] for s in sts],
+                                       [s["v_codes"] for s in sts], [s["v_absmax"] for s in sts])
             plan.append([idx, sts, args, t])
         return {"params": list(params), "has_grad": [g is not None for g in grads], "buckets": plan}
 
     @torch.no_grad()
-    def step(self, closure=None):
+    def clip_scale(self, max_norm: float, loss_scale: float = 1.0):
+        """(factor, norm) of all gradients as one-element CUDA tensors (see
+        :meth:`GradNorm.clip_scale`); pass the factor to :meth:`step`.  Where
+        the norm is not finite the factor is NaN and that step writes no
+        parameter and no moment (its step counts still advance)."""
+        grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
+        if not grads:
+            raise ValueError("no parameter has a gradient")
+        if any(g.is_sparse for g in grads):
+            raise TypeError("sparse gradients are not supported")
+        grads = [g if g.is_contiguous() else g.contiguous() for g in grads]
+        try:
+            if self._norm is None:
+                raise ValueError
+            self._norm.set_grads(grads)
+        except (TypeError, ValueError):  # the first call, or other gradients than before
+            self._norm = GradNorm(grads)
+        return self._norm.clip_scale(max_norm, loss_scale)
+
+    @torch.no_grad()
+    def step(self, closure=None, grad_scale=None):
+        """One step.  ``grad_scale``: a one-element float32 CUDA tensor that
+        multiplies every gradient, or None."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -97,7 +138,7 @@ class Adam8bit(torch.optim.Optimizer):
                      or not all(a is b for a, b in zip(plan["params"], params))
                      or plan["has_grad"] != [g is not None for g in grads])
             if fresh:
-                plan = self._args_cache[gi] = self._plan(params, grads)
+                plan = self._args_cache[gi] = self._plan(params, grads, group.get("state_bits", 8))
             b1, b2 = group["betas"]
             for bucket in plan["buckets"]:
                 idx, sts, args, t = bucket
@@ -109,7 +150,7 @@ class Adam8bit(torch.optim.Optimizer):
                         self._args_cache.pop(gi, None)
                         raise
                 args.step(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
-                          weight_decay=group["weight_decay"], step=t + 1)
+                          weight_decay=group["weight_decay"], step=t + 1, grad_scale=grad_scale)
                 # the step count advances only once its launch went through
                 bucket[3] = t + 1
                 for s in sts:
@@ -124,11 +165,21 @@ class Adam8bit(torch.optim.Optimizer):
         self._reset_plans()
         super().load_state_dict(state_dict)
         # torch casts every floating parameter's state tensors to the
-        # parameter dtype; codes are integers 0..255, so casting back is exact
-        for st in self.state.values():
+        # parameter dtype: codes are integers 0..255, so casting back is
+        # exact, and fp32 tensors are taken again from the saved ones
+        saved = state_dict["state"]
+        order = [p for g in self.param_groups for p in g["params"]]
+        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
+        for i, p in zip(ids, order):
+            if i not in saved or p not in self.state:
+                continue
+            st = self.state[p]
             for k in ("m_codes", "v_codes"):
                 if k in st and st[k].dtype != torch.uint8:
                     st[k] = st[k].to(torch.uint8)
+            for k in ("m_absmax", "v_absmax", "exp_avg", "exp_avg_sq"):
+                if k in st and st[k].dtype != torch.float32:
+                    st[k] = saved[i][k].to(device=p.device, dtype=torch.float32, copy=True)
 
 
 class AdamW8bit(Adam8bit):
@@ -137,5 +188,5 @@ class AdamW8bit(Adam8bit):
 
     _decoupled = True
 
-    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2):
-        super().__init__(params, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay)
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=8):
+        super().__init__(params, lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits)

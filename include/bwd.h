@@ -172,6 +172,18 @@ bwd_status bwd_adam8bit_step_multi_ex(int32_t num_tensors, void* const* p,
                                       float* const* v_absmax, const int64_t* n,
                                       const bwd_adam_hparams* hp, void* stream);
 
+/* The same with every gradient multiplied by s = *grad_scale first (one
+ * binary32 product), a factor in device memory such as bwd_grad_norm's.
+ *   grad_scale : device float[1], read by the kernel, or NULL for
+ *                bwd_adam8bit_step_multi_ex.  Where it is infinite or NaN the
+ *                call writes nothing. */
+bwd_status bwd_adam8bit_step_multi_scaled(
+    int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
+    const void* const* g, bwd_dtype g_dtype, uint8_t* const* m_codes,
+    float* const* m_absmax, uint8_t* const* v_codes, float* const* v_absmax,
+    const int64_t* n, const float* grad_scale, const bwd_adam_hparams* hp,
+    void* stream);
+
 /* ------------------------------------------------------------------------
  * ZeRO-style sharding of the step over P processes ("Яндекс Публикует ЯЛМ
  * 100Б", section "ZeRO" under "Случай с несколькими графическими
@@ -308,6 +320,7 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
  * NaN where the norm is not finite, so that a step that reads it as its
  * grad_scale writes nothing.  Sums are fp32 within a thread and binary64
  * across threads, in a fixed order: results are deterministic.
+ *   g_dtype : HOST array, the bwd_dtype of each tensor.
  *   factor, norm : device float[1] each, written.
  *   work : device, 16-byte aligned, bwd_grad_norm_work_bytes(num_tensors)
  *          bytes, whose first 16 are zero before the first call; each call
@@ -316,7 +329,7 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
  *   max_norm > 0 (infinity: no clipping), loss_scale > 0 and finite, as is
  *   1 / loss_scale.  num_tensors == 0 gives norm 0. */
 bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g,
-                         bwd_dtype g_dtype, const int64_t* n, float max_norm,
+                         const int32_t* g_dtype, const int64_t* n, float max_norm,
                          float loss_scale, float* factor, float* norm,
                          void* work, void* stream);
 
