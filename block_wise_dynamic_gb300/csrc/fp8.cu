@@ -50,6 +50,13 @@ __host__ __device__ constexpr int elem_bytes() { return kT == kF32 ? 4 : 2; }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 
+// Every kernel here is launched so that it may begin before the kernel ahead
+// of it in the stream has ended, and waits for that kernel's results before
+// it uses any; and it lets the next one begin once it has waited itself, so
+// that what came before the kernel ahead has ended too.
+__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_begin() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Byte of (row r, block kb) in a scale array whose rows have `groups` groups
 // of four blocks.
 __device__ __forceinline__ int64_t scale_offset(int64_t r, int64_t kb, int64_t groups) {
@@ -155,8 +162,8 @@ fp8_quantize_kernel(const QuantArgs a) {
   __shared__ __align__(16) float s_sum[kSums ? kWarps : 1][kTile];
   __shared__ uint32_t s_tile[kWarps];
   __shared__ uint8_t s_byte[kTile];
-  // a product launched to follow may set itself up meanwhile
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_inputs();
+  let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = lane % kLanes;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile, c0 = static_cast<int64_t>(blockIdx.x) * kTile;
   const int64_t c = c0 + kVals * part;
@@ -173,10 +180,7 @@ fp8_quantize_kernel(const QuantArgs a) {
     } else {
 #pragma unroll
       for (int j = 0; j < kVals; ++j)
-        if (in && c + j < a.cols) {
-          if (kT == kF32) (&w.x)[j] = reinterpret_cast<const uint32_t*>(src)[j];
-          else (&w.x)[j / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(src)[j]) << (16 * (j % 2));
-        }
+        if (in && c + j < a.cols) (&w.x)[j] = reinterpret_cast<const uint32_t*>(src)[j];
     }
     return w;
   };
@@ -187,9 +191,22 @@ fp8_quantize_kernel(const QuantArgs a) {
   uint4 x[kStaged ? 1 : kQPieces];
 #pragma unroll
   for (int i = 0; i < kQPieces; ++i) {
-    if constexpr (!kStaged) x[i] = fetch(i);
-    else if constexpr (!kVec) s_x[i][threadIdx.x] = fetch(i);
-    else {
+    if constexpr (!kStaged) {
+      x[i] = fetch(i);
+    } else if constexpr (!kVec) {
+      // rows of no 16-byte alignment: a lane to an element, 64 bytes a load
+#pragma unroll
+      for (int h = 0; h < kPerLoad; ++h) {
+        const int64_t r = r0 + warp * kPerLoad + h + i * (kTile / kQPieces);
+        const uint16_t* const src = static_cast<const uint16_t*>(a.x) + r * a.ld + c0;
+        uint16_t* const dst = reinterpret_cast<uint16_t*>(&s_x[i][32 * warp + kLanes * h]);
+        uint16_t v[kTile / 32];
+#pragma unroll
+        for (int q = 0; q < kTile / 32; ++q) v[q] = r < a.rows && c0 + lane + 32 * q < a.cols ? __ldcs(src + lane + 32 * q) : uint16_t{0};
+#pragma unroll
+        for (int q = 0; q < kTile / 32; ++q) dst[lane + 32 * q] = v[q];
+      }
+    } else {
       const bool in = row + i * (kTile / kQPieces) < rows_here && c < a.cols;
       // copies nothing and fills with zeros past the edge
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
@@ -197,6 +214,7 @@ fp8_quantize_kernel(const QuantArgs a) {
     }
   }
   if constexpr (kStaged && kVec) asm volatile("cp.async.wait_all;" ::: "memory");
+  if constexpr (kStaged && !kVec) __syncwarp();  // a warp's rows are its own
   const auto load = [&](int i) {
     if constexpr (kStaged) return s_x[i][threadIdx.x];
     else return x[i];
@@ -363,6 +381,8 @@ template <int kT>
 __global__ void __launch_bounds__(32 * kSumWarps)
 col_sums_kernel(const float* __restrict__ partial, int64_t tiles, int64_t cols, void* __restrict__ out) {
   __shared__ float s_part[kSumWarps][32];
+  wait_for_inputs();
+  let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
@@ -486,9 +506,6 @@ __device__ __forceinline__ uint32_t leader_addr(const uint64_t* bar) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(bar)));
   return r;
 }
-// Where the launch was allowed to begin before the kernel ahead of it (the
-// quantizer of its operand) has ended: waits for that kernel's results.
-__device__ __forceinline__ void wait_for_inputs() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -499,6 +516,9 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void tma_load(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, int x, int y, const void* src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
@@ -598,6 +618,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    prefetch_map(&map_sfa);
+    prefetch_map(&map_sfb);
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 8); }
@@ -620,6 +644,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 
   if (warp == 0) {
     wait_for_inputs();
+    let_next_begin();
     const bool one = elect_one();
     Ring<kStages> ring;
     bool ok = true;
@@ -887,6 +912,7 @@ struct FewArgs {
   int m, n, k;           // lines of A (columns here), lines of B (rows here), summed axis
   int a_trans, b_trans;
   int split;             // CTAs of a cluster, along the summed axis
+  int b_ready;           // B is no result of the kernel ahead
 };
 
 // Eight consecutive values of a line of A from element e on, zero past k.
@@ -951,7 +977,8 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
       for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], kFused ? 2 : 1); mbar_init(&s_empty[i], 1); }
       mbar_init(&s_done, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      // the first stages' weights do not depend on the kernel ahead
+      // the first stages' weights, at once where they do not depend on the kernel ahead
+      if (!p.b_ready) wait_for_inputs();
       for (int i = 0; i < ahead; ++i) weight(i, i);
     }
     __syncwarp();
@@ -969,6 +996,7 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   if (warp == 0) {
     const bool one = elect_one();
     wait_for_inputs();
+    let_next_begin();
     Ring<kStages> ring;
     for (int i = 0; i < count; ++i, ring.next()) {
       if (i >= ahead && !mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail)) break;
@@ -1028,6 +1056,7 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     static_assert(kStages <= kFewWarps, "a warp to each stage");
     constexpr int kHalves = kBN / 2, kPieces = kT == kF32 ? 2 : 1;
     const int part = lane % 16, first = lane / 16;
+    wait_for_inputs();
     const int s = warp - 2;
     uint32_t phase = 1;
     for (int i = s < kStages ? s : count; i < count; i += kStages, phase ^= 1u) {
@@ -1120,6 +1149,8 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 template <int kT>
 __global__ void __launch_bounds__(256)
 fill_rows_kernel(const void* __restrict__ bias, void* __restrict__ out, int64_t ldo, int64_t m, int64_t n) {
+  wait_for_inputs();
+  let_next_begin();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < m * n; i += stride)
     store1<kT>(out, i / n * ldo + i % n, bias ? load1<kT>(bias, i % n) : 0.0f);
@@ -1182,23 +1213,43 @@ bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 int64_t groups_of(int64_t n) { return (tiles_of(n) + 3) / 4; }
 
+template <typename... Params, typename... Args>
+bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int threads, int cluster, int smem, cudaStream_t st, const char* what,
+                     const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  if (cluster > 0) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e == cudaSuccess ? BWD_OK : cuda_fail(e, what);
+}
+
 template <int kT>
 bwd_status launch_quantize(int mode, const QuantArgs& a, cudaStream_t st) {
   const auto launch = [&](auto m, auto sums) {
     constexpr int kMode = decltype(m)::value;
     constexpr bool kSums = decltype(sums)::value;
     const dim3 grid(static_cast<unsigned>(tiles_of(a.cols)), static_cast<unsigned>(tiles_of(a.rows)));
-    if (a.vec) fp8_quantize_kernel<kT, kMode, kSums, true><<<grid, 32 * q_warps<kT>(), 0, st>>>(a);
-    else fp8_quantize_kernel<kT, kMode, kSums, false><<<grid, 32 * q_warps<kT>(), 0, st>>>(a);
+    return launch_ex(a.vec ? fp8_quantize_kernel<kT, kMode, kSums, true> : fp8_quantize_kernel<kT, kMode, kSums, false>, grid,
+                     32 * q_warps<kT>(), 0, 0, st, "fp8_quantize_kernel launch", a);
   };
   using Rows = std::integral_constant<int, BWD_FP8_ROWS>;
   using Cols = std::integral_constant<int, BWD_FP8_COLS>;
   using Both = std::integral_constant<int, BWD_FP8_ROWS | BWD_FP8_COLS>;
-  if (mode == BWD_FP8_ROWS) launch(Rows{}, std::false_type{});
-  else if (mode == BWD_FP8_TILES) launch(std::integral_constant<int, BWD_FP8_TILES>{}, std::false_type{});
-  else if (mode == BWD_FP8_COLS) a.col_sums ? launch(Cols{}, std::true_type{}) : launch(Cols{}, std::false_type{});
-  else a.col_sums ? launch(Both{}, std::true_type{}) : launch(Both{}, std::false_type{});
-  return check_launch("fp8_quantize_kernel launch");
+  if (mode == BWD_FP8_ROWS) return launch(Rows{}, std::false_type{});
+  if (mode == BWD_FP8_TILES) return launch(std::integral_constant<int, BWD_FP8_TILES>{}, std::false_type{});
+  if (mode == BWD_FP8_COLS) return a.col_sums ? launch(Cols{}, std::true_type{}) : launch(Cols{}, std::false_type{});
+  return a.col_sums ? launch(Both{}, std::true_type{}) : launch(Both{}, std::false_type{});
 }
 
 // What a launch needs to know of the device, found once for each.
@@ -1282,35 +1333,10 @@ struct Lines {
   int trans;
 };
 
-// `early`: the launch may begin before the kernel ahead of it has ended.
-template <typename... Params, typename... Args>
-bwd_status launch_ex(void (*kernel)(Params...), dim3 grid, int threads, int cluster, int smem, bool early, cudaStream_t st, const char* what,
-                     const Args&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (cluster > 0) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n++].val.clusterDim = {static_cast<unsigned>(cluster), 1, 1};
-  }
-  if (early) {
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = static_cast<unsigned>(n);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return e == cudaSuccess ? BWD_OK : cuda_fail(e, what);
-}
-
 template <int kT, int kBN, bool kSum>
-bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, bool early, cudaStream_t st) {
+bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
   const int tiles = p.tiles_m * p.tiles_n;
-  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), kMmThreads, 0, mm_smem<kBN>(), early, st,
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), kMmThreads, 0, mm_smem<kBN>(), st,
                    "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
 }
 
@@ -1325,7 +1351,7 @@ int64_t few_split(int64_t tiles_n, int64_t blocks, int sms) {
 
 // x.codes null: A is p.x, quantized by the kernel.
 template <int kT, int kBN, bool kFused>
-bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool early, cudaStream_t st) {
+bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, cudaStream_t st) {
   CUtensorMap map_w, map_x{};
   bwd_status s;
   if ((s = code_map(&map_w, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
@@ -1333,23 +1359,23 @@ bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, bool e
   const int64_t tiles_n = tiles_of(p.n);
   p.split = static_cast<int>(few_split(tiles_n, tiles_of(p.k), sms));
   return launch_ex(fp8_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles_n * p.split)),
-                   kFewThreads, p.split, few_smem<kBN>(), early, st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
+                   kFewThreads, p.split, few_smem<kBN>(), st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
 }
 
 template <int kT>
-bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, int sms, bool early, cudaStream_t st) {
-  if (!x.codes) return launch_few<kT, kFuse, true>(x, w, p, sms, early, st);
-  if (x.trans) return launch_few<kT, 128, false>(x, w, p, sms, early, st);
-  if (p.m > 48) return launch_few<kT, 64, false>(x, w, p, sms, early, st);
-  if (p.m > 32) return launch_few<kT, 48, false>(x, w, p, sms, early, st);
-  if (p.m > 16) return launch_few<kT, 32, false>(x, w, p, sms, early, st);
-  return launch_few<kT, 16, false>(x, w, p, sms, early, st);
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, int sms, cudaStream_t st) {
+  if (!x.codes) return launch_few<kT, kFuse, true>(x, w, p, sms, st);
+  if (x.trans) return launch_few<kT, 128, false>(x, w, p, sms, st);
+  if (p.m > 48) return launch_few<kT, 64, false>(x, w, p, sms, st);
+  if (p.m > 32) return launch_few<kT, 48, false>(x, w, p, sms, st);
+  if (p.m > 16) return launch_few<kT, 32, false>(x, w, p, sms, st);
+  return launch_few<kT, 16, false>(x, w, p, sms, st);
 }
 
-bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype, int sms, bool early, cudaStream_t st) {
-  if (dtype == BWD_F32) return few<kF32>(x, w, p, sms, early, st);
-  if (dtype == BWD_BF16) return few<kBF16>(x, w, p, sms, early, st);
-  return few<kF16>(x, w, p, sms, early, st);
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype, int sms, cudaStream_t st) {
+  if (dtype == BWD_F32) return few<kF32>(x, w, p, sms, st);
+  if (dtype == BWD_BF16) return few<kBF16>(x, w, p, sms, st);
+  return few<kF16>(x, w, p, sms, st);
 }
 
 // Whether a product goes to the kernel for few lines of A.
@@ -1361,8 +1387,9 @@ bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, int sms) {
   return part <= 2 * kChunk * (a.trans ? few_accs<128>() : few_accs<64>());
 }
 
-// out = A B^T + bias, k > 0.
-bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, bool early,
+// out = A B^T + bias, k > 0.  b_ready: a kernel that this call launched lies
+// between whatever wrote B and this product.
+bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready,
                   cudaStream_t st) {
   const int64_t m = a.lines, n = b.lines;
   const int eb = dtype == BWD_F32 ? 4 : 2;
@@ -1370,8 +1397,8 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
   if (use_few(a, n, k, dtype, d->sms)) {
-    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1};
-    return few(a, b, p, dtype, d->sms, early, st);
+    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1, b_ready};
+    return few(a, b, p, dtype, d->sms, st);
   }
   const int64_t tiles_m = (m + kBM - 1) / kBM;
   // A tile of 256 columns takes up to one and a half times as long as one of
@@ -1401,26 +1428,24 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
                                      : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
   }
-  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, early, st);
+  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
   if (dtype == BWD_BF16)
-    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, early, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, early, st);
-  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, early, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, early, st);
+    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, st);
+  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, st);
 }
 
 // The bias, or zero: a product over nothing.
 bwd_status fill(int64_t m, int64_t n, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, cudaStream_t st) {
   const int64_t need = (m * n + 255) / 256;
   const unsigned grid = static_cast<unsigned>(need < 1216 ? need : 1216);
-  if (dtype == BWD_F32) fill_rows_kernel<kF32><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
-  else if (dtype == BWD_BF16) fill_rows_kernel<kBF16><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
-  else fill_rows_kernel<kF16><<<grid, 256, 0, st>>>(bias, out, ldo, m, n);
-  return check_launch("fill_rows_kernel launch");
+  return launch_ex(dtype == BWD_F32 ? fill_rows_kernel<kF32> : dtype == BWD_BF16 ? fill_rows_kernel<kBF16> : fill_rows_kernel<kF16>,
+                   dim3(grid), 256, 0, 0, st, "fill_rows_kernel launch", bias, out, ldo, m, n);
 }
 
-bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, bool early,
+bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready,
                    cudaStream_t st) {
   if (a.lines == 0 || b.lines == 0) return BWD_OK;
-  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, early, st);
+  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, b_ready, st);
 }
 
 // Checks of a matrix that is quantized.
@@ -1455,10 +1480,8 @@ bwd_status quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, 
   if (s == BWD_OK && col_sums && cols > 0) {
     const unsigned grid = static_cast<unsigned>((cols + 31) / 32);
     const int64_t tiles = tiles_of(rows);
-    if (dtype == BWD_F32) col_sums_kernel<kF32><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else if (dtype == BWD_BF16) col_sums_kernel<kBF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    else col_sums_kernel<kF16><<<grid, 32 * kSumWarps, 0, st>>>(col_sums_work, tiles, cols, col_sums);
-    s = check_launch("col_sums_kernel launch");
+    s = launch_ex(dtype == BWD_F32 ? col_sums_kernel<kF32> : dtype == BWD_BF16 ? col_sums_kernel<kBF16> : col_sums_kernel<kF16>, dim3(grid),
+                  32 * kSumWarps, 0, 0, st, "col_sums_kernel launch", const_cast<const float*>(col_sums_work), tiles, cols, col_sums);
   }
   return s;
 }
@@ -1552,7 +1575,7 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
   if (!aligned_to(out, eb) || (bias && !aligned_to(bias, eb))) return fail(BWD_ERR_INVALID_ARG, "out and bias must be aligned to their element size");
   if (k > 0 && (!aligned16(a) || !aligned16(b) || !aligned16(a_scales) || !aligned16(b_scales)))
     return fail(BWD_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
-  return product(Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo, dtype, false,
+  return product(Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo, dtype, 0,
                  static_cast<cudaStream_t>(stream));
 }
 
@@ -1587,8 +1610,8 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
     const DeviceState* d = nullptr;
     if ((s = ensure_device(&d)) != BWD_OK) return s;
     const FewArgs p{w_scales, nullptr, bias, y, ldy, x, ld, ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x),
-                    static_cast<int>(rows), static_cast<int>(n), static_cast<int>(cols), 0, 0, 1};
-    return few(Lines{nullptr, nullptr, rows, 0}, Lines{w, w_scales, n, 0}, p, dtype, d->sms, false, st);
+                    static_cast<int>(rows), static_cast<int>(n), static_cast<int>(cols), 0, 0, 1, x_col_codes != nullptr};
+    return few(Lines{nullptr, nullptr, rows, 0}, Lines{w, w_scales, n, 0}, p, dtype, d->sms, st);
   }
   Pieces pieces{static_cast<uint8_t*>(work)};
   uint8_t* const codes = pieces.take(rows * bwd_fp8_pitch(cols));
@@ -1596,7 +1619,7 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   s = quantize(x, dtype, rows, cols, ld, x_col_codes ? BWD_FP8_ROWS | BWD_FP8_COLS : BWD_FP8_ROWS, codes, scales, x_col_codes, x_col_scales,
                nullptr, nullptr, st);
   if (s != BWD_OK) return s;
-  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, true, st);
+  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, 1, st);
 }
 
 int64_t bwd_fp8_linear_backward_work_bytes(int64_t rows, int64_t n) {
@@ -1635,11 +1658,10 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype, int64_t rows
   float* const sums = reinterpret_cast<float*>(pieces.take(tiles_of(rows) * n * 4));
   const int blocks = (dx ? BWD_FP8_ROWS : 0) | (dw || dbias ? BWD_FP8_COLS : 0);
   s = quantize(dy, dtype, rows, n, ld, blocks, row_codes, row_scales, col_codes, col_scales, dbias, sums, st);
-  // only the quantizer itself lets the next kernel begin early
   if (s == BWD_OK && dx)
-    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, !dbias, st);
+    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, 1, st);
   if (s == BWD_OK && dw)
-    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, !dx && !dbias, st);
+    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, 1, st);
   return s;
 }
 

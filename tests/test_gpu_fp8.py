@@ -338,3 +338,34 @@ def test_offsets_past_2_to_31(fp8):
     gv = ref.quantize(np64(got[-40:]), 128, 1)[0]
     xv = ref.quantize(np64(tail), 128, 1)[0]
     near(dw, gv.T @ xv, np.abs(gv).T @ np.abs(xv), rows, "bf16")
+
+
+@pytest.mark.parametrize("m", [1, 16, 40, 64, 300])
+def test_calls_in_a_row_see_each_others_results(fp8, m):
+    """Kernels may begin before the one ahead has ended: what one call writes
+    and the next reads, with nothing waited for in between."""
+    n, k = 1024, 4096
+    g = torch.Generator(DEV).manual_seed(23)
+    ws = [torch.randn(n, k, generator=g, device=DEV).to(torch.bfloat16) for _ in range(8)]
+    xs = [torch.randn(m, k, generator=g, device=DEV).to(torch.bfloat16) for _ in range(8)]
+    want = []
+    for w, x in zip(ws, xs):
+        y, xq = fp8.forward(x, fp8.quantize(w, "tiles"))
+        torch.cuda.synchronize()
+        dx, dw, db = fp8.backward(y, xq, fp8.quantize(w, "tiles"), need_bias=True)
+        torch.cuda.synchronize()
+        want.append((y, dx, dw, db, fp8.linear(x, fp8.quantize(w, "rows"))))
+        torch.cuda.synchronize()
+    w, x = torch.empty_like(ws[0]), torch.empty_like(xs[0])
+    got = []
+    for i in range(8):
+        w.copy_(ws[i])
+        x.copy_(xs[i])
+        wq = fp8.quantize(w, "tiles")
+        y, xq = fp8.forward(x, wq)
+        dx, dw, db = fp8.backward(y, xq, wq, need_bias=True)
+        w.mul_(1.0)
+        got.append((y, dx, dw, db, fp8.linear(x, fp8.quantize(w, "rows"))))
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
