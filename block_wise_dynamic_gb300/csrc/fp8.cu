@@ -197,14 +197,15 @@ fp8_quantize_kernel(const QuantArgs a) {
       // rows of no 16-byte alignment: a lane to an element, 64 bytes a load
 #pragma unroll
       for (int h = 0; h < kPerLoad; ++h) {
-        const int64_t r = r0 + warp * kPerLoad + h + i * (kTile / kQPieces);
-        const uint16_t* const src = static_cast<const uint16_t*>(a.x) + r * a.ld + c0;
-        uint16_t* const dst = reinterpret_cast<uint16_t*>(&s_x[i][32 * warp + kLanes * h]);
+        const int r = warp * kPerLoad + h + i * (kTile / kQPieces);
+        const uint16_t* const src = static_cast<const uint16_t*>(a.x) + (r0 + r) * a.ld + c0 + lane;
+        uint16_t* const dst = reinterpret_cast<uint16_t*>(&s_x[i][32 * warp + kLanes * h]) + lane;
+        const int cols_here = r < rows_here ? static_cast<int>(a.cols - c0 < kTile ? a.cols - c0 : kTile) - lane : 0;
         uint16_t v[kTile / 32];
 #pragma unroll
-        for (int q = 0; q < kTile / 32; ++q) v[q] = r < a.rows && c0 + lane + 32 * q < a.cols ? __ldcs(src + lane + 32 * q) : uint16_t{0};
+        for (int q = 0; q < kTile / 32; ++q) v[q] = 32 * q < cols_here ? __ldcs(src + 32 * q) : uint16_t{0};
 #pragma unroll
-        for (int q = 0; q < kTile / 32; ++q) dst[lane + 32 * q] = v[q];
+        for (int q = 0; q < kTile / 32; ++q) dst[32 * q] = v[q];
       }
     } else {
       const bool in = row + i * (kTile / kQPieces) < rows_here && c < a.cols;
@@ -825,18 +826,22 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           // rows of no 16-byte multiple: row by row, a lane to an element
           __syncwarp();
           constexpr int kEb = elem_bytes<kT>();
-          const int rows = p.m - m0 < 32 ? p.m - m0 : 32;
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r)
+          using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
+          Elem* dst = static_cast<Elem*>(p.out) + m0 * p.ldo + n0 + c + lane;
+          // the element's 16-byte piece of a row, swizzled by the row below
+          const int piece0 = lane * kEb >> 4, in_piece = lane * kEb & 15;
+          const auto put_rows = [&](auto tag) {
+            constexpr bool whole = decltype(tag)::value;
+            const int rows = whole ? 32 : p.m - m0 < 32 ? p.m - m0 : 32;
+#pragma unroll 16
+            for (int r = 0; r < (whole ? 32 : rows); ++r, dst += p.ldo)
 #pragma unroll
-            for (int h = 0; h < kCols; h += 32) {
-              const int j = h + lane, byte = j * kEb;
-              const uint8_t* const src = stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15);
-              if (n0 + c + j < p.n) {
-                if (kT == kF32) static_cast<float*>(p.out)[(m0 + r) * p.ldo + n0 + c + j] = *reinterpret_cast<const float*>(src);
-                else static_cast<uint16_t*>(p.out)[(m0 + r) * p.ldo + n0 + c + j] = *reinterpret_cast<const uint16_t*>(src);
-              }
-            }
+              for (int h = 0; h < kCols; h += 32)
+                if (whole || n0 + c + h + lane < p.n)
+                  dst[h] = *reinterpret_cast<const Elem*>(stage + r * 128 + (((piece0 + h * kEb / 16) ^ (r & 7)) << 4) + in_piece);
+          };
+          if (m0 + 32 <= p.m && n0 + c + kCols <= p.n) put_rows(std::true_type{});
+          else put_rows(std::false_type{});
           __syncwarp();
         }
       }
@@ -1521,7 +1526,13 @@ int64_t bwd_fp8_scale_bytes(int64_t count, int64_t length) {
   return tiles_of(count) * groups_of(length) * kSfTile;
 }
 
-int64_t bwd_fp8_pitch(int64_t cols) { return cols < 0 || cols > kMaxDim ? -1 : (cols + 15) / 16 * 16; }
+int64_t bwd_fp8_pitch(int64_t cols) {
+  if (cols < 0 || cols > kMaxDim) return -1;
+  // On 128-byte boundaries a stage's row of 128 bytes is one line of L2 and
+  // not parts of two: 8192 x 4097 x 11007 228 us against 300 at a pitch of
+  // 4,112.  Short rows are padded to 16 bytes only, which the tensor maps need.
+  return cols > 512 ? (cols + 127) / 128 * 128 : (cols + 15) / 16 * 16;
+}
 
 bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld, int32_t blocks,
                             uint8_t* row_codes, uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales,
