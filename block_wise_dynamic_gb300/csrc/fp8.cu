@@ -139,7 +139,8 @@ struct QuantArgs {
   uint8_t* codes_c;        // 128 x 1 blocks
   uint8_t* scales_c;
   float* col_sums;         // [row tiles][cols] partial column sums, or null
-  int vec;                 // rows start on 16-byte boundaries and hold whole pieces
+  int vec;                 // rows start on 16-byte boundaries and hold whole pieces,
+  int unit;                // or on boundaries of so many bytes and hold whole units
 };
 
 // One CTA for a tile of 128 x 128 elements.  A thread holds eight pieces of
@@ -189,30 +190,44 @@ fp8_quantize_kernel(const QuantArgs a) {
   constexpr bool kStaged = kT != kF32;
   __shared__ __align__(16) uint4 s_x[kStaged ? kQPieces : 1][kStaged ? 32 * kWarps : 1];
   uint4 x[kStaged ? 1 : kQPieces];
+  if constexpr (!kStaged) {
 #pragma unroll
-  for (int i = 0; i < kQPieces; ++i) {
-    if constexpr (!kStaged) {
-      x[i] = fetch(i);
-    } else if constexpr (!kVec) {
-      // rows of no 16-byte alignment: a lane to an element, 64 bytes a load
+    for (int i = 0; i < kQPieces; ++i) x[i] = fetch(i);
+  } else if constexpr (kVec) {
 #pragma unroll
-      for (int h = 0; h < kPerLoad; ++h) {
-        const int r = warp * kPerLoad + h + i * (kTile / kQPieces);
-        const uint16_t* const src = static_cast<const uint16_t*>(a.x) + (r0 + r) * a.ld + c0 + lane;
-        uint16_t* const dst = reinterpret_cast<uint16_t*>(&s_x[i][32 * warp + kLanes * h]) + lane;
-        const int cols_here = r < rows_here ? static_cast<int>(a.cols - c0 < kTile ? a.cols - c0 : kTile) - lane : 0;
-        uint16_t v[kTile / 32];
-#pragma unroll
-        for (int q = 0; q < kTile / 32; ++q) v[q] = 32 * q < cols_here ? __ldcs(src + 32 * q) : uint16_t{0};
-#pragma unroll
-        for (int q = 0; q < kTile / 32; ++q) dst[32 * q] = v[q];
-      }
-    } else {
+    for (int i = 0; i < kQPieces; ++i) {
       const bool in = row + i * (kTile / kQPieces) < rows_here && c < a.cols;
       // copies nothing and fills with zeros past the edge
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                    ::"r"(smem_u32(&s_x[i][threadIdx.x])), "l"(in ? src0 + i * src_step : src0), "r"(in ? 16u : 0u) : "memory");
     }
+  } else {
+    // rows of no 16-byte alignment: as many bytes to a lane as their
+    // alignment allows, consecutive lanes along a row
+    const int bytes_here = static_cast<int>(a.cols - c0 < kTile ? a.cols - c0 : kTile) * 2;
+    const auto get_rows = [&](auto unit) {
+      using Unit = decltype(unit);
+      constexpr int kBytes = sizeof(Unit), kLoads = 2 * kTile / (32 * kBytes);
+#pragma unroll
+      for (int i = 0; i < kQPieces; ++i)
+#pragma unroll
+        for (int h = 0; h < kPerLoad; ++h) {
+          const int r = warp * kPerLoad + h + i * (kTile / kQPieces), here = r < rows_here ? bytes_here : 0;
+          const char* const src = static_cast<const char*>(a.x) + ((r0 + r) * a.ld + c0) * 2;
+          char* const dst = reinterpret_cast<char*>(&s_x[i][32 * warp + kLanes * h]);
+          Unit v[kLoads];
+#pragma unroll
+          for (int q = 0; q < kLoads; ++q) {
+            const int at = (32 * q + lane) * kBytes;
+            v[q] = at < here ? __ldcs(reinterpret_cast<const Unit*>(src + at)) : Unit{};
+          }
+#pragma unroll
+          for (int q = 0; q < kLoads; ++q) *reinterpret_cast<Unit*>(dst + (32 * q + lane) * kBytes) = v[q];
+        }
+    };
+    if (a.unit == 8) get_rows(uint2{});
+    else if (a.unit == 4) get_rows(uint32_t{});
+    else get_rows(uint16_t{});
   }
   if constexpr (kStaged && kVec) asm volatile("cp.async.wait_all;" ::: "memory");
   if constexpr (kStaged && !kVec) __syncwarp();  // a warp's rows are its own
@@ -592,7 +607,8 @@ struct MmArgs {
   int a_trans, b_trans;  // operand stored with its own index contiguous
   int tiles_m, tiles_n;
   int sf_rows_b;         // row tiles of B's scales
-  int store;             // the output's rows allow tensor stores
+  int store;             // the output's rows allow tensor stores,
+  int unit;              // or stores of so many bytes
 };
 
 // The two accumulators.  With 256 columns each they overlap by 32 columns,
@@ -823,25 +839,39 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
-          // rows of no 16-byte multiple: row by row, a lane to an element
+          // rows of no 16-byte multiple: as many bytes to a lane as their
+          // alignment allows, consecutive lanes along a row
           __syncwarp();
           constexpr int kEb = elem_bytes<kT>();
-          using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
-          Elem* dst = static_cast<Elem*>(p.out) + m0 * p.ldo + n0 + c + lane;
-          // the element's 16-byte piece of a row, swizzled by the row below
-          const int piece0 = lane * kEb >> 4, in_piece = lane * kEb & 15;
-          const auto put_rows = [&](auto tag) {
-            constexpr bool whole = decltype(tag)::value;
-            const int rows = whole ? 32 : p.m - m0 < 32 ? p.m - m0 : 32;
+          char* const dst = static_cast<char*>(p.out) + (m0 * p.ldo + n0 + c) * kEb;
+          const int64_t row_bytes = p.ldo * kEb;
+          const auto put_rows = [&](auto unit) {
+            using Unit = decltype(unit);
+            constexpr int kBytes = sizeof(Unit), kLanes = 128 / kBytes, kRows = kLanes < 32 ? 32 / kLanes : 1;
+            const int byte = lane * kBytes % 128, row = lane / kLanes;
+            char* at = dst + row * row_bytes + byte;
 #pragma unroll 16
-            for (int r = 0; r < (whole ? 32 : rows); ++r, dst += p.ldo)
+            for (int r = row; r < 32; r += kRows, at += kRows * row_bytes)
 #pragma unroll
-              for (int h = 0; h < kCols; h += 32)
-                if (whole || n0 + c + h + lane < p.n)
-                  dst[h] = *reinterpret_cast<const Elem*>(stage + r * 128 + (((piece0 + h * kEb / 16) ^ (r & 7)) << 4) + in_piece);
+              for (int h = 0; h < 128; h += 32 * kBytes)  // 2-byte units: two to a lane
+                *reinterpret_cast<Unit*>(at + h) =
+                    *reinterpret_cast<const Unit*>(stage + r * 128 + ((((byte + h) >> 4) ^ (r & 7)) << 4) + (byte & 15));
           };
-          if (m0 + 32 <= p.m && n0 + c + kCols <= p.n) put_rows(std::true_type{});
-          else put_rows(std::false_type{});
+          if (m0 + 32 <= p.m && n0 + c + kCols <= p.n) {
+            if (p.unit == 8) put_rows(uint2{});
+            else if (kT == kF32 || p.unit == 4) put_rows(uint32_t{});
+            else put_rows(uint16_t{});
+          } else {
+            using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
+            for (int r = 0; r < 32 && m0 + r < p.m; ++r)
+#pragma unroll
+              for (int h = 0; h < kCols; h += 32) {
+                const int byte = (h + lane) * kEb;
+                if (n0 + c + h + lane < p.n)
+                  *reinterpret_cast<Elem*>(dst + r * row_bytes + byte) =
+                      *reinterpret_cast<const Elem*>(stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
+              }
+          }
           __syncwarp();
         }
       }
@@ -1212,6 +1242,11 @@ bwd_status scale_map(CUtensorMap* map, const uint8_t* scales, int64_t tiles) {
   return matrix_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, tiles, kSfTile / 4, kSfTile, kSfTile / 4, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+// The largest of 8, 4 and 2 bytes that divides a matrix's address and row.
+int unit_of(const void* base, int64_t row_bytes) {
+  return aligned_to(base, 8) && row_bytes % 8 == 0 ? 8 : aligned_to(base, 4) && row_bytes % 4 == 0 ? 4 : 2;
+}
+
 constexpr int64_t kMaxDim = int64_t{1} << 30;
 
 bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
@@ -1423,6 +1458,7 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
   p.sf_rows_b = static_cast<int>(tiles_of(n));
   p.store = aligned16(out) && ldo * eb % 16 == 0;
+  p.unit = unit_of(out, ldo * eb);
   MmMaps maps{};
   if ((s = code_map(&maps.a, a.codes, m, k, a.trans, kBM / 2)) != BWD_OK) return s;
   if ((s = code_map(&maps.b, b.codes, n, k, b.trans, bn / 2)) != BWD_OK) return s;
@@ -1479,6 +1515,7 @@ bwd_status quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, 
     a.codes_r = row_codes; a.scales_r = row_scales; a.codes_c = col_codes; a.scales_c = col_scales;
     a.col_sums = col_sums ? col_sums_work : nullptr;
     a.vec = ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x);
+    a.unit = unit_of(x, (ld | cols) * eb);
     s = dtype == BWD_F32 ? launch_quantize<kF32>(blocks, a, st) : dtype == BWD_BF16 ? launch_quantize<kBF16>(blocks, a, st)
                                                                                    : launch_quantize<kF16>(blocks, a, st);
   }

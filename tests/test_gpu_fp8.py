@@ -167,6 +167,25 @@ def test_few_rows_long_sums(fp8, m, n, k, kind):
     near(got, *ref.linear(np64(x), np64(w)), k, kind)
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(300, 516, 260), (300, 518, 262), (300, 517, 261), (290, 514, 132), (70, 12, 20)])
+def test_rows_of_other_alignments(fp8, m, n, k, kind):
+    """Rows of 8, 4 and 2 bytes' alignment, read by the quantizers and written
+    by the products, also from inside a larger matrix."""
+    x, w, dy = draw((m, k), 24, kind), draw((n, k), 25, kind, 0.02, loud=False), draw((m, n), 26, kind, 0.01)
+    for blocks in ("rows", "both", "tiles"):
+        check_quantized(fp8.quantize(x, blocks), x, blocks)
+        check_quantized(fp8.quantize(x[3:, 1:], blocks), x[3:, 1:], blocks)
+        check_quantized(fp8.quantize(x[:, 2:k - 1], blocks), x[:, 2:k - 1], blocks)
+    wq = fp8.quantize(w, "tiles")
+    y, xq = fp8.forward(x, wq)
+    dx, dw, _ = fp8.backward(dy, xq, wq)
+    near(y, *ref.linear(np64(x), np64(w)), k, kind)
+    (rx, rw, _), (sx, sw) = ref.linear_backward(np64(dy), np64(x), np64(w))
+    near(dx, rx, sx, n, kind)
+    near(dw, rw, sw, m, kind)
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("m,n,k", SIZES)
 def test_backward(fp8, m, n, k, kind):
