@@ -574,11 +574,12 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
 // each CTA's tensor memory holds its own rows' sums.  Against one CTA with
 // 128 x 128 this halves the operand bytes that an SM reads per product.
 // Pairs are persistent and walk the tiles with a grid stride; warp 0 copies,
-// warp 1 issues, warps 2 to 5 store the tile before, all meeting at
-// mbarriers only.
+// warp 1 issues, warps 2 to 9 store the tile before (each a quarter of its
+// rows and half of its columns), all meeting at mbarriers only.
 constexpr int kBM = 256;
 constexpr int kBK = 128;          // bytes of the summed axis in one stage: one scale block
-constexpr int kMmThreads = 192;
+constexpr int kMmThreads = 320;
+constexpr int kStoreWarps = 8;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSf = 480; // scales after the accumulators: two sets of 4 + 8 columns
 constexpr int kStoreBytes = 4096; // staging of one storing warp: 32 rows of 128 bytes
@@ -587,16 +588,20 @@ constexpr int kStoreBytes = 4096; // staging of one storing warp: 32 rows of 128
 // error with a sign that grows with the number of additions (measured
 // relative to 64 bits: 1.9e-7 after 1024 products, 7.6e-7 after 4096,
 // 2.0e-5 after 65536).  That is far below a 16-bit output's rounding.  For
-// fp32 outputs (kSum) the sums leave the accumulator every kChunk blocks and
-// are added up in registers, rounded to nearest.
-constexpr int kChunk = 8;
+// fp32 outputs (kSum) the sums leave the accumulator every kChunk blocks,
+// 2,048 products, and are added up in registers, rounded to nearest.  Each
+// time the next products wait for the columns that the accumulators share:
+// 8192 x 4096 x 11008 takes 264 us with eight blocks, 257 with sixteen and
+// 254 without (with 128 columns, whose accumulators share none but which
+// read more bytes per product, 306, 296 and 295).
+constexpr int kChunk = 16;
 
-template <int kBN> __host__ __device__ constexpr int mm_stages() { return kBN == 256 ? 6 : 7; }
+template <int kBN> __host__ __device__ constexpr int mm_stages() { return kBN == 256 ? 5 : 7; }
 template <int kBN> __host__ __device__ constexpr int mm_a_bytes() { return kBM / 2 * kBK; }
 template <int kBN> __host__ __device__ constexpr int mm_b_bytes() { return kBN / 2 * kBK; }
 template <int kBN> __host__ __device__ constexpr int mm_sf_bytes() { return kSfTile + kBN / 128 * kSfTile; }
 template <int kBN> __host__ __device__ constexpr int mm_smem() {
-  return 1024 + mm_stages<kBN>() * (mm_a_bytes<kBN>() + mm_b_bytes<kBN>() + mm_sf_bytes<kBN>()) + 4 * kStoreBytes;
+  return 1024 + mm_stages<kBN>() * (mm_a_bytes<kBN>() + mm_b_bytes<kBN>() + mm_sf_bytes<kBN>()) + kStoreWarps * kStoreBytes;
 }
 
 struct MmArgs {
@@ -621,14 +626,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
                   const __grid_constant__ CUtensorMap map_out, const MmArgs p) {
-  static_assert(!kSum || kBN == 128, "the sums of 256 columns do not fit a thread's registers");
   constexpr int kStages = mm_stages<kBN>(), kA = mm_a_bytes<kBN>(), kB = mm_b_bytes<kBN>(), kSf = mm_sf_bytes<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const store = sm + kStages * (kA + kB);
-  uint8_t* const sf = store + 4 * kStoreBytes;
+  uint8_t* const sf = store + kStoreWarps * kStoreBytes;
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_overlap;
-  __shared__ __align__(16) float s_bias[4][128];
+  __shared__ __align__(16) float s_bias[kStoreWarps][64];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -641,8 +645,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     prefetch_map(&map_sfb);
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 8); }
-    mbar_init(&s_overlap, 8);
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 2 * kStoreWarps); }
+    mbar_init(&s_overlap, kStoreWarps);  // half of either CTA's storing warps read the shared columns
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -743,36 +747,60 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
   } else {
-    const int quarter = warp & 3;  // the lanes of tensor memory that this warp may read
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    uint8_t* const stage = store + quarter * kStoreBytes;
-    float* const bias_s = s_bias[quarter];
+    const int quarter = warp & 3;      // the lanes of tensor memory that this warp may read
+    const int half = (warp - 2) / 4;   // which half of the columns is its own
+    constexpr int kHalf = kBN / 2;
+    const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
+    uint8_t* const stage = store + (warp - 2) * kStoreBytes;
+    float* const bias_s = s_bias[warp - 2];
     constexpr int kCols = kT == kF32 ? 32 : 64;  // columns of one staged group: 128 bytes
-    constexpr int kGroups = kBN / kCols;
+    constexpr int kGroups = kHalf / kCols;
     int use = 0;
     bool ok = true;
+    // Done with the accumulators' shared columns, or with all of its own: the
+    // first accumulator's last columns and the second one's first are shared.
+    const auto done_shared = [&](int buf) {
+      if (kBN != 256 || buf == half) return;
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(&s_overlap);
+    };
+    const auto done_all = [&](int buf) {
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
+    };
     for (int t = first; ok && t < tiles; t += pairs) {
-      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = t % p.tiles_n * kBN;
-      float sum[kSum ? kBN : 1];
+      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = t % p.tiles_n * kBN + half * kHalf;
+      float sum[kSum ? kHalf : 1];
       if constexpr (kSum) {
 #pragma unroll
-        for (int j = 0; j < kBN; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
         for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
           const int buf = use & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[buf], (use >> 1) & 1, &s_fail));
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-#pragma unroll
-          for (int c = 0; c < kBN; c += 32) {
+          const auto add = [&](auto at) {
+            constexpr int c = decltype(at)::value;
             uint32_t r[32];
-            tmem_load32(lanes + acc_col<kBN>(buf) + c, r);
+            tmem_load32(own + acc_col<kBN>(buf) + c, r);
             asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
             for (int u = 0; u < 32; ++u) sum[c + u] = __fadd_rn(sum[c + u], __uint_as_float(r[u]));
+          };
+          using C0 = std::integral_constant<int, 0>;
+          using C1 = std::integral_constant<int, 32 % kHalf>;
+          using C2 = std::integral_constant<int, 64 % kHalf>;
+          using C3 = std::integral_constant<int, 96 % kHalf>;
+          if (half == 0) {  // shared columns first
+            add(C0{}); done_shared(buf); add(C1{});
+            if constexpr (kHalf == 128) { add(C2{}); add(C3{}); }
+          } else {
+            if constexpr (kHalf == 128) { add(C3{}); done_shared(buf); add(C2{}); }
+            add(C1{}); add(C0{});
           }
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
+          done_all(buf);
         }
         if (!ok) break;
       }
@@ -784,8 +812,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
-        // the group that holds the accumulators' shared columns goes first
-        const int gr = (!kSum && kBN == 256 && buf == 0) ? (i + kGroups - 1) % kGroups : i;
+        // shared columns first
+        const int gr = kSum || half == 0 ? i : kGroups - 1 - i;
         const int c = gr * kCols;
         float v[kCols];
         if constexpr (kSum) {
@@ -794,14 +822,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         } else {
           uint32_t r[kCols / 32][32];
 #pragma unroll
-          for (int h = 0; h < kCols / 32; ++h) tmem_load32(lanes + acc_col<kBN>(buf) + c + 32 * h, r[h]);
+          for (int h = 0; h < kCols / 32; ++h) tmem_load32(own + acc_col<kBN>(buf) + c + 32 * h, r[h]);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          if (i == 0 || i == kGroups - 1) {
-            asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-            __syncwarp();
-            if (lane == 0 && i == 0 && kBN == 256) mbar_arrive_leader(&s_overlap);
-            if (lane == 0 && i == kGroups - 1) mbar_arrive_leader(&s_acc_empty[buf]);
-          }
+          if (i == 0) done_shared(buf);
+          if (i == kGroups - 1) done_all(buf);
 #pragma unroll
           for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
         }
@@ -1335,6 +1359,7 @@ bwd_status ensure_device(const DeviceState** out) {
   *out = &d;
   if (d.ready && d.ctx == ctx) return BWD_OK;
   e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 256, true>, mm_smem<256>());
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 128, true>, mm_smem<128>());
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false>, mm_smem<256>());
   if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false>, mm_smem<256>());
@@ -1422,9 +1447,9 @@ bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype
 bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, int sms) {
   if (a.lines > 64) return false;
   if (dtype != BWD_F32) return true;
-  // fp32 results: no accumulator may take much more than kChunk blocks
+  // fp32 results: no accumulator may take more than kChunk blocks
   const int64_t part = (tiles_of(k) + few_split(tiles_of(n), tiles_of(k), sms) - 1) / few_split(tiles_of(n), tiles_of(k), sms);
-  return part <= 2 * kChunk * (a.trans ? few_accs<128>() : few_accs<64>());
+  return part <= kChunk * (a.trans ? few_accs<128>() : few_accs<64>());
 }
 
 // out = A B^T + bias, k > 0.  b_ready: a kernel that this call launched lies
@@ -1447,7 +1472,7 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   // 256 x 4096 x 11008 15.1 us against 17.7, 512 x 4096 x 4096 11.3 against
   // 14.9 the other way.
   const auto waves = [&](int64_t width) { return (tiles_m * ((n + width - 1) / width) + d->pairs - 1) / d->pairs; };
-  const int bn = dtype != BWD_F32 && 3 * waves(256) < 2 * waves(128) ? 256 : 128;
+  const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   const int64_t tiles_n = (n + bn - 1) / bn;
   if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
     return fail(BWD_ERR_INVALID_ARG, "too many tiles");
@@ -1469,7 +1494,8 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
                                      : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
   }
-  if (dtype == BWD_F32) return launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
+  if (dtype == BWD_F32)
+    return bn == 256 ? launch_matmul<kF32, 256, true>(maps, p, d->pairs, st) : launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
   if (dtype == BWD_BF16)
     return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, st);
   return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, st);

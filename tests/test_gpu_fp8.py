@@ -116,9 +116,9 @@ def near(got, want, size, k, kind):
     """Within the sums' and the result's rounding.  The matrix instruction adds
     32 products at a time into an fp32 sum and truncates: a unit of the last
     place of a running sum that never exceeds `size` for each addition.  For
-    fp32 results there are 32 of them to a stretch of 1,024 products, and the
+    fp32 results there are 64 of them to a stretch of 2,048 products, and the
     stretches are added up to nearest; 16-bit results take all in one."""
-    steps = 32 + -(-k // 1024) if kind == "fp32" else -(-k // 32) + 1
+    steps = 64 + -(-k // 2048) if kind == "fp32" else -(-k // 32) + 1
     bound = steps * 2.0 ** -23 * size + ROUND[kind] * np.abs(want) + TINY[kind]
     bad = np.abs(np64(got) - want) > bound
     assert not bad.any(), (np.argwhere(bad)[:4], np64(got)[bad][:4], want[bad][:4])
