@@ -38,7 +38,7 @@ struct Tensor32 {
   float* m;
   float* v;
   int64_t n;
-  int64_t vec;  // every pointer aligned to four of its elements
+  int64_t shift;  // elements that every pointer lies past four of its elements' boundary, or -1 where they differ
 };
 
 struct Adam32Args {
@@ -124,8 +124,15 @@ __global__ void __launch_bounds__(kThreads)
 adam32_kernel(const __grid_constant__ Adam32Args a) {
   const int ti = find_tensor(a.chunk_start, a.num_tensors, blockIdx.x);
   const Tensor32& T = a.t[ti];
-  const int64_t i = (blockIdx.x - a.chunk_start[ti]) * kChunk + 4 * threadIdx.x;
-  const bool vec = T.vec && i + 4 <= T.n;
+  // Quads lie on boundaries in memory: of a tensor that starts between two,
+  // the first quad holds fewer elements.  Where the four arrays start
+  // differently, a thread's elements are a CTA apart, so that a warp's still
+  // follow one another.
+  const int64_t base = (blockIdx.x - a.chunk_start[ti]) * kChunk;
+  const bool together = T.shift >= 0;
+  const int64_t i = together ? base - T.shift + 4 * threadIdx.x : base + threadIdx.x;
+  const int step = together ? 1 : kThreads;
+  const bool vec = together && i >= 0 && i + 4 <= T.n;
   float p[4], g[4], m[4], v[4];
   if (vec) {
     load4<kP>(T.p, i, p); load4<kG>(T.g, i, g);
@@ -133,9 +140,10 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const bool in = i + j < T.n;
-      p[j] = in ? load1<kP>(T.p, i + j) : 0.0f; g[j] = in ? load1<kG>(T.g, i + j) : 0.0f;
-      m[j] = in ? T.m[i + j] : 0.0f; v[j] = in ? T.v[i + j] : 0.0f;
+      const int64_t e = i + j * step;
+      const bool in = e >= 0 && e < T.n;
+      p[j] = in ? load1<kP>(T.p, e) : 0.0f; g[j] = in ? load1<kG>(T.g, e) : 0.0f;
+      m[j] = in ? T.m[e] : 0.0f; v[j] = in ? T.v[e] : 0.0f;
     }
   }
   const float s = a.grad_scale ? *a.grad_scale : 1.0f;
@@ -152,8 +160,10 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
     store4<kP>(T.p, i, p); store4<kF32>(T.m, i, m); store4<kF32>(T.v, i, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (i + j < T.n) { store1<kP>(T.p, i + j, p[j]); T.m[i + j] = m[j]; T.v[i + j] = v[j]; }
+    for (int j = 0; j < 4; ++j) {
+      const int64_t e = i + j * step;
+      if (e >= 0 && e < T.n) { store1<kP>(T.p, e, p[j]); T.m[e] = m[j]; T.v[e] = v[j]; }
+    }
   }
 }
 
@@ -171,8 +181,9 @@ __host__ __device__ constexpr int norm_chunk(int type) { return kThreads * kNorm
 struct NormArgs {
   int64_t chunk_start[kNormTensors + 1];
   const void* g[kNormTensors];
-  int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, negative where 16-byte loads are not possible
+  int32_t n_tail[kNormTensors];  // elements of the tensor's last chunk, counted from the 16-byte boundary before it
   uint8_t type[kNormTensors];
+  uint8_t shift[kNormTensors];   // elements between that boundary and the tensor's start
   double* slots;                 // one per CTA of all launches of the call
   unsigned int* ticket;          // 0 before the call and after it
   float* factor;
@@ -195,22 +206,23 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   return x;
 }
 
-// Sum of squares of this thread's share of one chunk of `len` elements.
+// Sum of squares of this thread's share of elements first .. len - 1 of one
+// chunk; g is on a 16-byte boundary.
 template <int kG>
-__device__ __forceinline__ float chunk_squares(const void* g, int len, bool vec) {
+__device__ __forceinline__ float chunk_squares(const void* g, int first, int len) {
   constexpr int kVals = kG == kF32 ? 4 : 8;  // values of a piece
   uint4 w[kNormPieces];
 #pragma unroll
   for (int q = 0; q < kNormPieces; ++q) {
     const int i = (q * kThreads + threadIdx.x) * kVals;
     w[q] = make_uint4(0u, 0u, 0u, 0u);
-    if (vec && i + kVals <= len) w[q] = __ldcs(static_cast<const uint4*>(g) + q * kThreads + threadIdx.x);
+    if (i >= first && i + kVals <= len) w[q] = __ldcs(static_cast<const uint4*>(g) + q * kThreads + threadIdx.x);
   }
   float sum[2] = {0.0f, 0.0f};
 #pragma unroll
   for (int q = 0; q < kNormPieces; ++q) {
     const int i = (q * kThreads + threadIdx.x) * kVals;
-    if (vec && i + kVals <= len) {
+    if (i >= first && i + kVals <= len) {
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
         const uint32_t u = (&w[q].x)[kG == kF32 ? j : j / 2];
@@ -218,10 +230,11 @@ __device__ __forceinline__ float chunk_squares(const void* g, int len, bool vec)
         sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
       }
     } else {
-      for (int j = 0; j < kVals && i + j < len; ++j) {
-        const float x = load1<kG>(g, i + j);
-        sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
-      }
+      for (int j = 0; j < kVals; ++j)
+        if (i + j >= first && i + j < len) {
+          const float x = load1<kG>(g, i + j);
+          sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
+        }
     }
   }
   return __fadd_rn(sum[0], sum[1]);
@@ -239,12 +252,12 @@ grad_norm_kernel(const __grid_constant__ NormArgs a) {
     for (; c < total; c += gridDim.x) {
       while (a.chunk_start[ti + 1] <= c) ++ti;
       const int type = a.type[ti];
-      const bool last = c + 1 == a.chunk_start[ti + 1], vec = a.n_tail[ti] > 0;
-      const int len = last ? abs(a.n_tail[ti]) : norm_chunk(type);
+      const int len = c + 1 == a.chunk_start[ti + 1] ? a.n_tail[ti] : norm_chunk(type);
+      const int first = c == a.chunk_start[ti] ? a.shift[ti] : 0;
       // a chunk is 64 bytes to a thread, whatever the type
       const char* const g = static_cast<const char*>(a.g[ti]) + (c - a.chunk_start[ti]) * (kThreads * kNormPieces * 16);
-      const float sum = type == kF32 ? chunk_squares<kF32>(g, len, vec)
-                        : type == kBF16 ? chunk_squares<kBF16>(g, len, vec) : chunk_squares<kF16>(g, len, vec);
+      const float sum = type == kF32 ? chunk_squares<kF32>(g, first, len)
+                        : type == kBF16 ? chunk_squares<kBF16>(g, first, len) : chunk_squares<kF16>(g, first, len);
       part += static_cast<double>(sum);
     }
   }
@@ -284,6 +297,9 @@ int64_t chunks_of(int64_t n, int64_t chunk) { return (n + chunk - 1) / chunk; }
 bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
 uintptr_t bytes_of(int t) { return t == BWD_F32 ? 4 : 2; }
 
+// Elements between a pointer and the boundary of four of them before it.
+int64_t past_quad(const void* x, int type) { return static_cast<int64_t>(reinterpret_cast<uintptr_t>(x) / bytes_of(type) % 4); }
+
 bwd_status launch_adam32(const Adam32Args& a, int g_type, int p_type, cudaStream_t st) {
   const unsigned grid = static_cast<unsigned>(a.chunk_start[a.num_tensors]);
   switch (3 * p_type + g_type) {
@@ -316,7 +332,7 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
   if (!p || !g || !m || !v || !n) return fail(BWD_ERR_INVALID_ARG, "NULL array");
   if (!aligned_to(grad_scale, 4)) return fail(BWD_ERR_INVALID_ARG, "grad_scale is not 4-byte aligned");
   for (int32_t i = 0; i < num_tensors; ++i) {
-    if (n[i] < 0 || n[i] > kMaxChunks * kChunk) return fail(BWD_ERR_INVALID_ARG, "tensor %d: bad size", i);
+    if (n[i] < 0 || n[i] > (kMaxChunks - 1) * kChunk) return fail(BWD_ERR_INVALID_ARG, "tensor %d: bad size", i);
     if (n[i] > 0 && (!p[i] || !g[i] || !m[i] || !v[i])) return fail(BWD_ERR_INVALID_ARG, "tensor %d: NULL pointer", i);
     if (n[i] > 0 && (!aligned_to(p[i], bytes_of(p_dtype)) || !aligned_to(g[i], bytes_of(g_dtype)) ||
                      !aligned_to(m[i], 4) || !aligned_to(v[i], 4)))
@@ -337,12 +353,12 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
   };
   for (int32_t i = 0; i < num_tensors; ++i) {
     if (n[i] == 0) continue;
-    const int64_t chunks = chunks_of(n[i], kChunk);
+    const int64_t at[4] = {past_quad(p[i], p_dtype), past_quad(g[i], g_dtype), past_quad(m[i], BWD_F32), past_quad(v[i], BWD_F32)};
+    const int64_t shift = at[0] == at[1] && at[0] == at[2] && at[0] == at[3] ? at[0] : -1;
+    const int64_t chunks = chunks_of(n[i] + (shift > 0 ? shift : 0), kChunk);
     if (t == kMaxTensors || a.chunk_start[t] + chunks > kMaxChunks)
       if ((s = flush()) != BWD_OK) return s;
-    a.t[t] = Tensor32{p[i], g[i], m[i], v[i], n[i],
-                      aligned_to(p[i], 4 * bytes_of(p_dtype)) && aligned_to(g[i], 4 * bytes_of(g_dtype)) &&
-                          aligned16(m[i]) && aligned16(v[i])};
+    a.t[t] = Tensor32{p[i], g[i], m[i], v[i], n[i], shift};
     a.chunk_start[t + 1] = a.chunk_start[t] + chunks;
     ++t;
   }
@@ -391,11 +407,13 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g, const int32_
     a.chunk_start[0] = 0;
     for (int32_t i = 0; i <= num_tensors; ++i) {
       if (i < num_tensors && n[i] > 0) {
-        a.g[t] = g[i];
-        const int64_t chunk = norm_chunk(g_dtype[i]), chunks = chunks_of(n[i], chunk);
+        const uintptr_t over = reinterpret_cast<uintptr_t>(g[i]) % 16;
+        const int64_t shift = static_cast<int64_t>(over / bytes_of(g_dtype[i]));
+        const int64_t chunk = norm_chunk(g_dtype[i]), chunks = chunks_of(n[i] + shift, chunk);
+        a.g[t] = static_cast<const char*>(g[i]) - over;
         a.type[t] = static_cast<uint8_t>(g_dtype[i]);
-        const int32_t tail = static_cast<int32_t>(n[i] - (chunks - 1) * chunk);
-        a.n_tail[t] = aligned16(g[i]) ? tail : -tail;
+        a.shift[t] = static_cast<uint8_t>(shift);
+        a.n_tail[t] = static_cast<int32_t>(n[i] + shift - (chunks - 1) * chunk);
         a.chunk_start[t + 1] = a.chunk_start[t] + chunks;
         ++t;
       }

@@ -87,6 +87,22 @@ def test_step_unaligned(bwd, offset, pk, gk):
     check(old, new, pk, 1)
 
 
+@pytest.mark.parametrize("offsets", [(1, 2, 3, 0), (0, 0, 0, 1), (3, 3, 3, 7), (5, 1, 9, 13)])
+@pytest.mark.parametrize("pk,gk", [("fp32", "fp32"), ("bf16", "fp16")])
+def test_step_arrays_that_start_differently(bwd, offsets, pk, gk):
+    sizes = [1, 2, 3, 1023, 1024, 1025, 5000]
+    new = [tensors(sizes, pk, 31, 0.02, offsets[0]), tensors(sizes, gk, 32, 1e-3, offsets[1]),
+           tensors(sizes, "fp32", 33, 3e-4, offsets[2]), [t.square_() for t in tensors(sizes, "fp32", 34, 1e-3, offsets[3])]]
+    whole = [[t._base.clone() for t in ts] for ts in new]
+    old = [[t.clone() for t in ts] for ts in new]
+    bwd.adam32_step_multi(*new, **HP, step=2)
+    check(old, new, pk, 2)
+    for k, ts in enumerate(new):  # nothing beside the tensors is written
+        for t, w in zip(ts, whole[k]):
+            w[offsets[k]:offsets[k] + t.numel()] = t
+            assert torch.equal(t._base, w)
+
+
 def test_step_reads_the_factor_on_the_device(bwd):
     old = state([3000, 17], "fp32", "bf16", 3)
     new = [[t.clone() for t in ts] for ts in old]
@@ -123,7 +139,7 @@ def test_new_gradients_in_an_old_table(bwd):
 
 @pytest.mark.parametrize("gk", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("sizes", LISTS + [[3] * 2500, [2048 * 4000 + 1]], ids=lambda s: f"{len(s)}x{max(s)}")
-@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("offset", [0, 1, 3, 6])
 def test_norm(bwd, sizes, gk, offset):
     g = tensors(sizes, gk, 6, 1e-2, offset)
     for max_norm, loss_scale in ((0.01, 1.0), (1e9, 1.0), (0.5, 1024.0), (float("inf"), 3.0)):
