@@ -142,4 +142,9 @@ class GradNorm(_GradList):
 
 def clip_scale(grads: Sequence[torch.Tensor], max_norm: float, loss_scale: float = 1.0, stream=None):
     """:meth:`GradNorm.clip_scale` of a list used once."""
-    return GradNorm(grads).clip_scale(max_norm, loss_scale, stream)
+    if stream is not None:  # its workspace belongs to the stream that it is used on
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream, grads[0].device)
+        with torch.cuda.stream(stream):
+            return GradNorm(grads).clip_scale(max_norm, loss_scale)
+    return GradNorm(grads).clip_scale(max_norm, loss_scale)

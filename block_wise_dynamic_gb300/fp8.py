@@ -121,6 +121,13 @@ def _matrix(x: torch.Tensor, name: str) -> torch.Tensor:
     return x
 
 
+def _on(stream, device):
+    """Context in which ``stream`` (a torch stream or a handle) is current: a
+    call's temporaries, copies and results belong to the stream they are used
+    on."""
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, device))
+
+
 def _bytes(n: int, device: torch.device) -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
@@ -138,6 +145,9 @@ def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stre
     kind = _BLOCKS[blocks]
     if col_sums and not kind & _abi.FP8_COLS:
         raise ValueError('column sums need blocks "cols" or "both"')
+    if stream is not None:
+        with _on(stream, x.device):
+            return quantize(x, blocks, col_sums)
     x = _matrix(x, "x")
     rows, cols = x.shape
     dev = x.device
@@ -147,7 +157,7 @@ def quantize(x: torch.Tensor, blocks: str = "rows", col_sums: bool = False, stre
     if col_sums:
         sums = torch.empty(cols, dtype=x.dtype, device=dev)
         work = torch.empty(max(1, (rows + 127) // 128 * cols), dtype=torch.float32, device=dev)
-    _launch("bwd_fp8_quantize", dev, stream, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, rc, rs, cc, cs,
+    _launch("bwd_fp8_quantize", dev, None, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), kind, rc, rs, cc, cs,
             _ptr(sums), _ptr(work))
     return (q, sums) if col_sums else q
 
@@ -169,12 +179,15 @@ def dequantize(a: Fp8Matrix, along: str = "rows", dtype=None, stream=None) -> to
     if along not in ("rows", "cols"):
         raise ValueError('along must be "rows" or "cols"')
     codes, scales, _, _ = _lines(a, along == "cols", "a")
+    if stream is not None:
+        with _on(stream, a.device):
+            return dequantize(a, along, dtype)
     dtype = a.dtype if dtype is None else dtype
     if dtype not in _GDT:
         raise TypeError("dtype must be float32, bfloat16 or float16")
     rows, cols = a.shape
     out = torch.empty((rows, cols), dtype=dtype, device=a.device)
-    _launch("bwd_fp8_dequantize", a.device, stream, codes, scales, int(along == "rows"), rows, cols, out.data_ptr(), _GDT[dtype])
+    _launch("bwd_fp8_dequantize", a.device, None, codes, scales, int(along == "rows"), rows, cols, out.data_ptr(), _GDT[dtype])
     return out
 
 
@@ -187,6 +200,9 @@ def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = Fa
     bc, bsc, n, kb = _lines(b, trans_b, "b")
     if k != kb:
         raise ValueError(f"a's lines have {k} elements, b's {kb}")
+    if stream is not None:
+        with _on(stream, a.device):
+            return matmul(a, b, trans_a, trans_b, bias, dtype)
     dev = a.device
     if b.device != dev:
         raise ValueError(f"b is on {b.device}, the call runs on {dev}")
@@ -196,7 +212,7 @@ def matmul(a: Fp8Matrix, b: Fp8Matrix, trans_a: bool = False, trans_b: bool = Fa
     if bias is not None:
         _need(bias, "bias", dtype, n, dev)
     out = torch.empty((m, n), dtype=dtype, device=dev)
-    _launch("bwd_fp8_matmul", dev, stream, m, n, k, ac, int(trans_a), asc, bc, int(trans_b), bsc, _ptr(bias), out.data_ptr(), n,
+    _launch("bwd_fp8_matmul", dev, None, m, n, k, ac, int(trans_a), asc, bc, int(trans_b), bsc, _ptr(bias), out.data_ptr(), n,
             _GDT[dtype])
     return out
 
@@ -215,6 +231,9 @@ def _operands(x: torch.Tensor, w: Fp8Matrix, axis: int, name: str):
 
 
 def _forward(x, w, bias, both, stream):
+    if stream is not None:
+        with _on(stream, x.device):
+            return _forward(x, w, bias, both, None)
     m, codes, scales = _operands(x, w, 1, "x")
     rows, cols = m.shape
     n, dev, dt = w.shape[0], m.device, m.dtype
@@ -227,7 +246,7 @@ def _forward(x, w, bias, both, stream):
     if both:
         xq = Fp8Matrix(rows, cols, "cols", dt, dev)
         _, _, cc, cs = xq._pointers
-    _launch("bwd_fp8_linear", dev, stream, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes, scales, n, _ptr(bias),
+    _launch("bwd_fp8_linear", dev, None, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes, scales, n, _ptr(bias),
             y.data_ptr(), n, cc, cs, _ptr(work))
     return y, xq
 
@@ -248,6 +267,9 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
              need_bias: bool = False, stream=None):
     """(dx, dw, dbias) in dy's dtype, None for those not needed.  xq has
     column blocks (from :func:`forward`), w blocks "tiles" or "cols"."""
+    if stream is not None:
+        with _on(stream, dy.device):
+            return backward(dy, xq, w, need_input, need_weight, need_bias)
     m, codes, scales = _operands(dy, w, 0, "dy")
     rows, n = m.shape
     k, dev, dt = w.shape[1], m.device, m.dtype
@@ -266,7 +288,7 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
     codes_bytes = _round256(rows * _pitch(n))
     work = _bytes(2 * codes_bytes + _round256(_scale_bytes(rows, n)) + _round256(_scale_bytes(n, rows)) +
                   _round256((rows + 127) // 128 * n * 4), dev)
-    _launch("bwd_fp8_linear_backward", dev, stream, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes, scales, xc, xs, k,
+    _launch("bwd_fp8_linear_backward", dev, None, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes, scales, xc, xs, k,
             _ptr(dx), k, _ptr(dw), k, _ptr(db), work.data_ptr())
     return dx, dw, db
 

@@ -291,6 +291,25 @@ def test_same_result_every_time_and_on_another_stream(fp8):
     bwd.check_device(0)
 
 
+@pytest.mark.parametrize("handle", [False, True])
+def test_stream_argument(fp8, handle):
+    """A given stream is used for everything, copies of strided inputs and
+    temporaries among it."""
+    s = torch.cuda.Stream()
+    x, w = draw((40, 300), 27, "bf16").t(), draw((500, 40), 28, "bf16", 0.02)
+    want_w = fp8.quantize(w, "tiles")
+    y, xq = fp8.forward(x, want_w)
+    want = [y, *fp8.backward(y, xq, want_w, need_bias=True), fp8.linear(x, want_w), xq.dequantize("cols")]
+    torch.cuda.synchronize()
+    at = s.cuda_stream if handle else s
+    for _ in range(3):
+        wq = fp8.quantize(w, "tiles", stream=at)
+        y, xq = fp8.forward(x, wq, stream=at)
+        got = [y, *fp8.backward(y, xq, wq, need_bias=True, stream=at), fp8.linear(x, wq, stream=at), xq.dequantize("cols", stream=at)]
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_graph_capture(fp8):
     x, w = draw((48, 512), 17, "bf16"), draw((640, 512), 18, "bf16", 0.02)
     wq = fp8.quantize(w, "tiles")
