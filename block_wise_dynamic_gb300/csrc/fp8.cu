@@ -611,10 +611,24 @@ struct MmArgs {
   int m, n, k;
   int a_trans, b_trans;  // operand stored with its own index contiguous
   int tiles_m, tiles_n;
+  int whole;             // the first tiles; the rest are worked on as two halves of 128 columns each
   int sf_rows_b;         // row tiles of B's scales
   int store;             // the output's rows allow tensor stores,
   int unit;              // or stores of so many bytes
 };
+
+// What a pair works on: a tile, or half of one (its columns from n0 on).  A
+// last wave that less than half fills the device is cut into halves, which
+// take half as long.
+struct Item {
+  int m0, n0, cols;
+};
+template <int kBN>
+__device__ __forceinline__ Item item_of(const MmArgs& p, int i) {
+  if (kBN == 128 || i < p.whole) return Item{i / p.tiles_n * kBM, i % p.tiles_n * kBN, kBN};
+  const int t = p.whole + (i - p.whole) / 2;
+  return Item{t / p.tiles_n * kBM, t % p.tiles_n * kBN + (i - p.whole) % 2 * 128, 128};
+}
 
 // The two accumulators.  With 256 columns each they overlap by 32 columns,
 // which leaves room for the scales: the storing warps read the shared
@@ -659,7 +673,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
   const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
-  const int tiles = p.tiles_m * p.tiles_n, pairs = static_cast<int>(gridDim.x) / 2;
+  const int items = 2 * p.tiles_m * p.tiles_n - p.whole, pairs = static_cast<int>(gridDim.x) / 2;
   const int first = static_cast<int>(blockIdx.x) / 2;
   const int chunk = kSum ? kChunk : kblocks;
 
@@ -669,9 +683,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const bool one = elect_one();
     Ring<kStages> ring;
     bool ok = true;
-    for (int t = first; ok && t < tiles; t += pairs) {
-      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2), nt = t % p.tiles_n * kBN;
-      const int n0 = nt + static_cast<int>(rank) * (kBN / 2);
+    for (int t = first; ok && t < items; t += pairs) {
+      const Item item = item_of<kBN>(p, t);
+      // of a half, the copies of B bring as many lines as of a whole
+      const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2), nt = item.n0, n0 = nt + static_cast<int>(rank) * (item.cols / 2);
       for (int kb = 0; kb < kblocks; ++kb, ring.next()) {
         if (!(ok = mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail))) break;
         if (one) {
@@ -699,8 +714,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     if (rank == 0) {
       const bool one = elect_one();
       // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
-      const uint32_t idesc = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) |
-                             ((kBN / 8) << 17) | (1u << 23) | ((kBM / 16) << 24);
+      const uint32_t idesc0 = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) | (1u << 23) | ((kBM / 16) << 24);
       // descriptors of stage 0, and the step of 32 along the summed axis
       const uint64_t da0 = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint64_t db0 = p.b_trans && kBN == 128 ? smem_desc(smem_u32(sm + kA), 16, 512, 4) : smem_desc(smem_u32(sm + kA), 16, 1024, 2);
@@ -709,7 +723,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       Ring<kStages> ring;
       int use = 0;  // accumulators used so far
       bool ok = true;
-      for (int t = first; ok && t < tiles; t += pairs) {
+      for (int t = first; ok && t < items; t += pairs) {
+        const uint32_t idesc = idesc0 | static_cast<uint32_t>(item_of<kBN>(p, t).cols / 8) << 17;
         for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
           const int buf = use & 1;
           ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
@@ -770,8 +785,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
     };
-    for (int t = first; ok && t < tiles; t += pairs) {
-      const int m0 = t / p.tiles_n * kBM + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = t % p.tiles_n * kBN + half * kHalf;
+    for (int t = first; ok && t < items; t += pairs) {
+      const Item item = item_of<kBN>(p, t);
+      const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = item.n0 + half * kHalf;
+      const bool mine = half == 0 || item.cols == kBN;  // of a half tile, the second warps have nothing to store
       float sum[kSum ? kHalf : 1];
       if constexpr (kSum) {
 #pragma unroll
@@ -829,6 +846,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
           for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
         }
+        if (!mine) continue;
         if (p.bias) {
           __syncwarp();
 #pragma unroll
@@ -1400,8 +1418,8 @@ struct Lines {
 
 template <int kT, int kBN, bool kSum>
 bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
-  const int tiles = p.tiles_m * p.tiles_n;
-  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), kMmThreads, 0, mm_smem<kBN>(), st,
+  const int items = 2 * p.tiles_m * p.tiles_n - p.whole;
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))), kMmThreads, 0, mm_smem<kBN>(), st,
                    "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
 }
 
@@ -1474,13 +1492,15 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   const auto waves = [&](int64_t width) { return (tiles_m * ((n + width - 1) / width) + d->pairs - 1) / d->pairs; };
   const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   const int64_t tiles_n = (n + bn - 1) / bn;
-  if (tiles_m * tiles_n > 0x7fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
+  const int64_t tiles = tiles_m * tiles_n, last = tiles % d->pairs;
+  if (tiles > 0x3fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
     return fail(BWD_ERR_INVALID_ARG, "too many tiles");
   MmArgs p{};
   p.bias = bias; p.out = out; p.ldo = ldo;
   p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
   p.a_trans = a.trans; p.b_trans = b.trans;
   p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
+  p.whole = static_cast<int>(bn == 256 && 2 * last <= d->pairs ? tiles - last : tiles);
   p.sf_rows_b = static_cast<int>(tiles_of(n));
   p.store = aligned16(out) && ldo * eb % 16 == 0;
   p.unit = unit_of(out, ldo * eb);

@@ -143,6 +143,21 @@ def test_matmul_orders(fp8, m, n, k, trans_a, trans_b):
         near(got, av @ bv.T, np.abs(av) @ np.abs(bv).T, k, kind)
 
 
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("trans_a,trans_b", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("m,n,k", [(4096, 4900, 200), (4000, 5001, 1300), (9000, 2300, 2100)])
+def test_matmul_of_several_waves(fp8, m, n, k, trans_a, trans_b, kind):
+    """More tiles than the device works on at a time, and a last wave of few."""
+    a = draw((k, m) if trans_a else (m, k), 31, "bf16")
+    b = draw((k, n) if trans_b else (n, k), 32, "bf16")
+    aq, bq = fp8.quantize(a, "cols" if trans_a else "rows"), fp8.quantize(b, "cols" if trans_b else "rows")
+    bias = draw((1, n), 33, kind, loud=False).view(-1)
+    av, bv = (q.dequantize("cols" if t else "rows", torch.float32).double() for q, t in ((aq, trans_a), (bq, trans_b)))
+    av, bv = av.t() if trans_a else av, bv.t() if trans_b else bv
+    got = fp8.matmul(aq, bq, trans_a, trans_b, bias=bias, dtype=TYPES[kind])
+    near(got, np64(av @ bv.t() + bias.double()), np64(av.abs() @ bv.abs().t() + bias.double().abs()), k, kind)
+
+
 @pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("m,n,k", SIZES)
