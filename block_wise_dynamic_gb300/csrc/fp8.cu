@@ -582,20 +582,23 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32]) {
 // each CTA's tensor memory holds its own rows' sums.  Against one CTA with
 // 128 x 128 this halves the operand bytes that an SM reads per product.
 // Pairs are persistent and walk the tiles with a grid stride; warp 0 copies,
-// warp 1 issues, warps 2 to 9 store the tile before (each a quarter of its
-// rows and half of its columns), all meeting at mbarriers only.
+// warp 1 issues, the other kWarps store the tile before (each a quarter of its
+// rows; four warps all of its columns, eight half of them), all meeting at
+// mbarriers only.  Eight are faster where a tile is stored in less time than
+// the next one takes (8192 x 128 x 9728 28 us against 35); four draw less
+// power where it is not (16384 x 4096 x 11008 474 us against 484 with the
+// quantizer), and have a sixth stage in the other four's staging.
 //
 // Bound by the matrix instruction at the clock that its power leaves: 16384 x
 // 4096 x 11008 takes 330 us with the copies left out (0.28 us for a stage of
 // 512 cycles, the instruction's rate at 1.86 GHz), 351 on zeros, and 395 to
 // 410 (3.6 to 3.7 PFLOP/s, 1.9 times the bf16 library product) on random
-// values, with the clock at 1.6 GHz.  Five stages: six ran as fast, four 7%
+// values, with the clock at 1.6 GHz.  Five stages run as fast as six, four 7%
 // slower.  Order of the tiles and cache hints for loads and stores changed
 // it by 1% at most.
 constexpr int kBM = 256;
 constexpr int kBK = 128;          // bytes of the summed axis in one stage: one scale block
-constexpr int kMmThreads = 320;
-constexpr int kStoreWarps = 8;
+__host__ __device__ constexpr int mm_threads(int store_warps) { return 64 + 32 * store_warps; }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemSf = 480; // scales after the accumulators: two sets of 4 + 8 columns
 constexpr int kStoreBytes = 4096; // staging of one storing warp: 32 rows of 128 bytes
@@ -612,12 +615,12 @@ constexpr int kStoreBytes = 4096; // staging of one storing warp: 32 rows of 128
 // read more bytes per product, 306, 296 and 295).
 constexpr int kChunk = 16;
 
-template <int kBN> __host__ __device__ constexpr int mm_stages() { return kBN == 256 ? 5 : 7; }
+template <int kBN, int kWarps> __host__ __device__ constexpr int mm_stages() { return kBN == 128 ? 7 : kWarps == 4 ? 6 : 5; }
 template <int kBN> __host__ __device__ constexpr int mm_a_bytes() { return kBM / 2 * kBK; }
 template <int kBN> __host__ __device__ constexpr int mm_b_bytes() { return kBN / 2 * kBK; }
 template <int kBN> __host__ __device__ constexpr int mm_sf_bytes() { return kSfTile + kBN / 128 * kSfTile; }
-template <int kBN> __host__ __device__ constexpr int mm_smem() {
-  return 1024 + mm_stages<kBN>() * (mm_a_bytes<kBN>() + mm_b_bytes<kBN>() + mm_sf_bytes<kBN>()) + kStoreWarps * kStoreBytes;
+template <int kBN, int kWarps> __host__ __device__ constexpr int mm_smem() {
+  return 1024 + mm_stages<kBN, kWarps>() * (mm_a_bytes<kBN>() + mm_b_bytes<kBN>() + mm_sf_bytes<kBN>()) + kWarps * kStoreBytes;
 }
 
 struct MmArgs {
@@ -651,18 +654,19 @@ __device__ __forceinline__ Item item_of(const MmArgs& p, int i) {
 // columns first and the next tile's products start when they have.
 template <int kBN> __device__ __forceinline__ uint32_t acc_col(int buf) { return buf ? (kBN == 256 ? 224u : 128u) : 0u; }
 
-template <int kT, int kBN, bool kSum>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
+template <int kT, int kBN, bool kSum, int kWarps>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mm_threads(kWarps), 1)
 fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                   const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
                   const __grid_constant__ CUtensorMap map_out, const MmArgs p) {
-  constexpr int kStages = mm_stages<kBN>(), kA = mm_a_bytes<kBN>(), kB = mm_b_bytes<kBN>(), kSf = mm_sf_bytes<kBN>();
+  static_assert(kWarps == 8 || (kWarps == 4 && !kSum), "a thread's registers hold the sums of 128 columns at most");
+  constexpr int kStages = mm_stages<kBN, kWarps>(), kA = mm_a_bytes<kBN>(), kB = mm_b_bytes<kBN>(), kSf = mm_sf_bytes<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const store = sm + kStages * (kA + kB);
-  uint8_t* const sf = store + kStoreWarps * kStoreBytes;
+  uint8_t* const sf = store + kWarps * kStoreBytes;
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_overlap;
-  __shared__ __align__(16) float s_bias[kStoreWarps][64];
+  __shared__ __align__(16) float s_bias[kWarps][64];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -675,8 +679,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     prefetch_map(&map_sfb);
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 2 * kStoreWarps); }
-    mbar_init(&s_overlap, kStoreWarps);  // half of either CTA's storing warps read the shared columns
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 2 * kWarps); }
+    mbar_init(&s_overlap, 8);  // four warps of either CTA read the shared columns
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -779,8 +783,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     }
   } else {
     const int quarter = warp & 3;      // the lanes of tensor memory that this warp may read
-    const int half = (warp - 2) / 4;   // which half of the columns is its own
-    constexpr int kHalf = kBN / 2;
+    const int half = (warp - 2) / 4;   // with eight warps, which half of the columns is its own
+    constexpr int kHalf = kWarps == 8 ? kBN / 2 : kBN;  // columns of one warp
     const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
     uint8_t* const stage = store + (warp - 2) * kStoreBytes;
     float* const bias_s = s_bias[warp - 2];
@@ -791,7 +795,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     // Done with the accumulators' shared columns, or with all of its own: the
     // first accumulator's last columns and the second one's first are shared.
     const auto done_shared = [&](int buf) {
-      if (kBN != 256 || buf == half) return;
+      if (kBN != 256 || (kWarps == 8 && buf == half)) return;
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(&s_overlap);
@@ -804,7 +808,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     for (int t = first; ok && t < items; t += pairs) {
       const Item item = item_of<kBN>(p, t);
       const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = item.n0 + half * kHalf;
-      const bool mine = half == 0 || item.cols == kBN;  // of a half tile, the second warps have nothing to store
+      const int cols = item.cols - half * kHalf;  // of a half tile, some columns are not there
       float sum[kSum ? kHalf : 1];
       if constexpr (kSum) {
 #pragma unroll
@@ -846,7 +850,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
       for (int i = 0; i < kGroups; ++i) {
         // shared columns first
-        const int gr = kSum || half == 0 ? i : kGroups - 1 - i;
+        const int gr = kSum ? i : kWarps == 4 ? (buf == 0 ? (i + kGroups - 1) % kGroups : i) : half == 0 ? i : kGroups - 1 - i;
         const int c = gr * kCols;
         float v[kCols];
         if constexpr (kSum) {
@@ -862,7 +866,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
           for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
         }
-        if (!mine) continue;
+        if (c >= cols) continue;
         if (p.bias) {
           __syncwarp();
 #pragma unroll
@@ -1398,26 +1402,28 @@ bwd_status ensure_device(const DeviceState** out) {
   *out = &d;
   if (d.ready && d.ctx == ctx) return BWD_OK;
   e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 256, true>, mm_smem<256>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 128, true>, mm_smem<128>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false>, mm_smem<256>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false>, mm_smem<256>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 128, false>, mm_smem<128>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 128, false>, mm_smem<128>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 256, true, 8>, mm_smem<256, 8>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 128, true, 8>, mm_smem<128, 8>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false, 8>, mm_smem<256, 8>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false, 8>, mm_smem<256, 8>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false, 4>, mm_smem<256, 4>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false, 4>, mm_smem<256, 4>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 128, false, 8>, mm_smem<128, 8>());
+  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 128, false, 8>, mm_smem<128, 8>());
   if (e == cudaSuccess) e = opt_in_all_few<kF32>();
   if (e == cudaSuccess) e = opt_in_all_few<kBF16>();
   if (e == cudaSuccess) e = opt_in_all_few<kF16>();
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(d.sms / 2 * 2));
-  cfg.blockDim = dim3(kMmThreads);
-  cfg.dynamicSmemBytes = mm_smem<256>();
+  cfg.blockDim = dim3(mm_threads(4));
+  cfg.dynamicSmemBytes = mm_smem<256, 4>();
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false, 4>, &cfg);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
   if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
   d.ctx = ctx;
@@ -1437,11 +1443,21 @@ struct Lines {
   int trans;
 };
 
-template <int kT, int kBN, bool kSum>
+template <int kT, int kBN, bool kSum, int kWarps>
 bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
   const int items = 2 * p.tiles_m * p.tiles_n - p.whole;
-  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum>, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))), kMmThreads, 0, mm_smem<kBN>(), st,
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum, kWarps>, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))),
+                   mm_threads(kWarps), 0, mm_smem<kBN, kWarps>(), st,
                    "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
+}
+
+// 16-bit results.  Four storing warps where a tile's products (sixteen stages
+// or more, some 6 us) outlast its tensor stores.
+template <int kT>
+bwd_status launch_matmul16(const MmMaps& maps, const MmArgs& p, int bn, int pairs, cudaStream_t st) {
+  if (bn == 128) return launch_matmul<kT, 128, false, 8>(maps, p, pairs, st);
+  if (p.store && p.k > 15 * kBK) return launch_matmul<kT, 256, false, 4>(maps, p, pairs, st);
+  return launch_matmul<kT, 256, false, 8>(maps, p, pairs, st);
 }
 
 // As many parts of the summed axis as the device has room for at once, of two
@@ -1536,10 +1552,8 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
     if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
   }
   if (dtype == BWD_F32)
-    return bn == 256 ? launch_matmul<kF32, 256, true>(maps, p, d->pairs, st) : launch_matmul<kF32, 128, true>(maps, p, d->pairs, st);
-  if (dtype == BWD_BF16)
-    return bn == 256 ? launch_matmul<kBF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kBF16, 128, false>(maps, p, d->pairs, st);
-  return bn == 256 ? launch_matmul<kF16, 256, false>(maps, p, d->pairs, st) : launch_matmul<kF16, 128, false>(maps, p, d->pairs, st);
+    return bn == 256 ? launch_matmul<kF32, 256, true, 8>(maps, p, d->pairs, st) : launch_matmul<kF32, 128, true, 8>(maps, p, d->pairs, st);
+  return dtype == BWD_BF16 ? launch_matmul16<kBF16>(maps, p, bn, d->pairs, st) : launch_matmul16<kF16>(maps, p, bn, d->pairs, st);
 }
 
 // The bias, or zero: a product over nothing.
