@@ -395,30 +395,47 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// Column sums from the quantizer's partial sums, one for each tile of rows:
-// eight warps of a CTA each add every eighth of a column's, in order, and the
-// first then adds the eight.
+// Column sums from the quantizer's partial sums, one for each tile of rows.
+struct ColSums {
+  const float* partial;  // [tiles][cols]
+  int64_t tiles, cols;
+  void* out;             // or null: none
+};
+
+// As a kernel of its own: eight warps of a CTA each add every eighth of a
+// column's partial sums, in order, and the first then adds the eight.
 constexpr int kSumWarps = 8;
 
 template <int kT>
 __global__ void __launch_bounds__(32 * kSumWarps)
-col_sums_kernel(const float* __restrict__ partial, int64_t tiles, int64_t cols, void* __restrict__ out) {
+col_sums_kernel(const ColSums a) {
   __shared__ float s_part[kSumWarps][32];
   wait_for_inputs();
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float s = 0.0f;
-  if (c < cols) {
+  if (c < a.cols) {
 #pragma unroll 8
-    for (int64_t t = warp; t < tiles; t += kSumWarps) s += partial[t * cols + c];
+    for (int64_t t = warp; t < a.tiles; t += kSumWarps) s += a.partial[t * a.cols + c];
   }
   s_part[warp][lane] = s;
   __syncthreads();
-  if (warp != 0 || c >= cols) return;
+  if (warp != 0 || c >= a.cols) return;
 #pragma unroll
   for (int w = 1; w < kSumWarps; ++w) s += s_part[w][lane];
-  store1<kT>(out, c, s);
+  store1<kT>(a.out, c, s);
+}
+
+// Beside a product: every `step`-th group of 32 columns to a warp.
+template <int kT>
+__device__ __forceinline__ void col_sums_of_warp(const ColSums& a, int64_t first, int64_t step) {
+  for (int64_t c = 32 * first + threadIdx.x % 32; c < a.cols; c += 32 * step) {
+    float s = 0.0f;
+#pragma unroll 8
+    for (int64_t t = 0; t < a.tiles; ++t) s += a.partial[t * a.cols + c];
+    store1<kT>(a.out, c, s);
+  }
 }
 
 // --------------------------------------------------------------------------
@@ -632,6 +649,7 @@ struct MmArgs {
   int tiles_m, tiles_n;
   int whole;             // the first tiles; the rest are worked on as two halves of 128 columns each
   int sf_rows_b;         // row tiles of B's scales
+  ColSums sums;          // column sums to finish beside the product
   int store;             // the output's rows allow tensor stores,
   int unit;              // or stores of so many bytes
 };
@@ -731,7 +749,13 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       }
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank != 0) {
+      // the issuing warp of the second CTA has nothing to issue
+      if (p.sums.out) {
+        wait_for_inputs();
+        col_sums_of_warp<kT>(p.sums, first, pairs);
+      }
+    } else {
       const bool one = elect_one();
       // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
       const uint32_t idesc0 = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) | (1u << 23) | ((kBM / 16) << 24);
@@ -1509,7 +1533,9 @@ bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, int sms) {
 
 // out = A B^T + bias, k > 0.  b_ready: a kernel that this call launched lies
 // between whatever wrote B and this product.
-bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready,
+// *sums, where given, are column sums that the product finishes on the way;
+// it clears them when it does.
+bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready, ColSums* sums,
                   cudaStream_t st) {
   const int64_t m = a.lines, n = b.lines;
   const int eb = dtype == BWD_F32 ? 4 : 2;
@@ -1539,6 +1565,10 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
   p.whole = static_cast<int>(bn == 256 && 2 * last <= d->pairs ? tiles - last : tiles);
   p.sf_rows_b = static_cast<int>(tiles_of(n));
+  if (sums) {
+    p.sums = *sums;
+    sums->out = nullptr;
+  }
   p.store = aligned16(out) && ldo * eb % 16 == 0;
   p.unit = unit_of(out, ldo * eb);
   MmMaps maps{};
@@ -1564,10 +1594,16 @@ bwd_status fill(int64_t m, int64_t n, const void* bias, void* out, int64_t ldo, 
                    dim3(grid), 256, 0, 0, st, "fill_rows_kernel launch", bias, out, ldo, m, n);
 }
 
-bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready,
+bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready, ColSums* sums,
                    cudaStream_t st) {
   if (a.lines == 0 || b.lines == 0) return BWD_OK;
-  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, b_ready, st);
+  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, b_ready, sums, st);
+}
+
+bwd_status finish_col_sums(const ColSums& a, bwd_dtype dtype, cudaStream_t st) {
+  if (!a.out || a.cols == 0) return BWD_OK;
+  return launch_ex(dtype == BWD_F32 ? col_sums_kernel<kF32> : dtype == BWD_BF16 ? col_sums_kernel<kBF16> : col_sums_kernel<kF16>,
+                   dim3(static_cast<unsigned>((a.cols + 31) / 32)), 32 * kSumWarps, 0, 0, st, "col_sums_kernel launch", a);
 }
 
 // Checks of a matrix that is quantized.
@@ -1583,9 +1619,9 @@ bwd_status check_matrix(const void* x, bwd_dtype dtype, int64_t rows, int64_t co
   return BWD_OK;
 }
 
-// Quantizes, and finishes the column sums where they are asked for.
+// Quantizes; with col_sums_work, leaves the column sums' parts there.
 bwd_status quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld, int blocks, uint8_t* row_codes,
-                    uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales, void* col_sums, float* col_sums_work, cudaStream_t st) {
+                    uint8_t* row_scales, uint8_t* col_codes, uint8_t* col_scales, float* col_sums_work, cudaStream_t st) {
   const int eb = dtype == BWD_F32 ? 4 : 2;
   bwd_status s = BWD_OK;
   if (rows > 0 && cols > 0) {
@@ -1594,17 +1630,11 @@ bwd_status quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, 
     a.pitch = bwd_fp8_pitch(cols);
     a.groups_r = groups_of(cols); a.groups_c = groups_of(rows);
     a.codes_r = row_codes; a.scales_r = row_scales; a.codes_c = col_codes; a.scales_c = col_scales;
-    a.col_sums = col_sums ? col_sums_work : nullptr;
+    a.col_sums = col_sums_work;
     a.vec = ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x);
     a.unit = unit_of(x, (ld | cols) * eb);
     s = dtype == BWD_F32 ? launch_quantize<kF32>(blocks, a, st) : dtype == BWD_BF16 ? launch_quantize<kBF16>(blocks, a, st)
                                                                                    : launch_quantize<kF16>(blocks, a, st);
-  }
-  if (s == BWD_OK && col_sums && cols > 0) {
-    const unsigned grid = static_cast<unsigned>((cols + 31) / 32);
-    const int64_t tiles = tiles_of(rows);
-    s = launch_ex(dtype == BWD_F32 ? col_sums_kernel<kF32> : dtype == BWD_BF16 ? col_sums_kernel<kBF16> : col_sums_kernel<kF16>, dim3(grid),
-                  32 * kSumWarps, 0, 0, st, "col_sums_kernel launch", const_cast<const float*>(col_sums_work), tiles, cols, col_sums);
   }
   return s;
 }
@@ -1670,8 +1700,10 @@ bwd_status bwd_fp8_quantize(const void* x, bwd_dtype dtype, int64_t rows, int64_
   }
   if (col_sums && (!col_sums_work || !aligned_to(col_sums, dtype == BWD_F32 ? 4 : 2) || !aligned_to(col_sums_work, 4)))
     return fail(BWD_ERR_INVALID_ARG, "column sums need a workspace, both aligned to their element size");
-  return quantize(x, dtype, rows, cols, ld, blocks, row_codes, row_scales, col_codes, col_scales, col_sums, col_sums_work,
-                  static_cast<cudaStream_t>(stream));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bwd_status q = quantize(x, dtype, rows, cols, ld, blocks, row_codes, row_scales, col_codes, col_scales,
+                                col_sums ? col_sums_work : nullptr, st);
+  return q == BWD_OK && col_sums ? finish_col_sums(ColSums{col_sums_work, tiles_of(rows), cols, col_sums}, dtype, st) : q;
 }
 
 bwd_status bwd_fp8_dequantize(const uint8_t* codes, const uint8_t* scales, int32_t along_rows, int64_t rows, int64_t cols,
@@ -1705,7 +1737,7 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
   if (k > 0 && (!aligned16(a) || !aligned16(b) || !aligned16(a_scales) || !aligned16(b_scales)))
     return fail(BWD_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
   return product(Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo, dtype, 0,
-                 static_cast<cudaStream_t>(stream));
+                 nullptr, static_cast<cudaStream_t>(stream));
 }
 
 int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols) {
@@ -1733,7 +1765,7 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
     return fail(BWD_ERR_INVALID_ARG, "codes, scales and work must be 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (fused && some) {
-    if (x_col_codes && (s = quantize(x, dtype, rows, cols, ld, BWD_FP8_COLS, nullptr, nullptr, x_col_codes, x_col_scales, nullptr, nullptr, st)) != BWD_OK)
+    if (x_col_codes && (s = quantize(x, dtype, rows, cols, ld, BWD_FP8_COLS, nullptr, nullptr, x_col_codes, x_col_scales, nullptr, st)) != BWD_OK)
       return s;
     if (n == 0) return BWD_OK;
     const DeviceState* d = nullptr;
@@ -1746,9 +1778,9 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   uint8_t* const codes = pieces.take(rows * bwd_fp8_pitch(cols));
   uint8_t* const scales = pieces.take(bwd_fp8_scale_bytes(rows, cols));
   s = quantize(x, dtype, rows, cols, ld, x_col_codes ? BWD_FP8_ROWS | BWD_FP8_COLS : BWD_FP8_ROWS, codes, scales, x_col_codes, x_col_scales,
-               nullptr, nullptr, st);
+               nullptr, st);
   if (s != BWD_OK) return s;
-  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, 1, st);
+  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, 1, nullptr, st);
 }
 
 int64_t bwd_fp8_linear_backward_work_bytes(int64_t rows, int64_t n) {
@@ -1786,11 +1818,14 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype, int64_t rows
   uint8_t* const col_scales = pieces.take(bwd_fp8_scale_bytes(n, rows));
   float* const sums = reinterpret_cast<float*>(pieces.take(tiles_of(rows) * n * 4));
   const int blocks = (dx ? BWD_FP8_ROWS : 0) | (dw || dbias ? BWD_FP8_COLS : 0);
-  s = quantize(dy, dtype, rows, n, ld, blocks, row_codes, row_scales, col_codes, col_scales, dbias, sums, st);
+  s = quantize(dy, dtype, rows, n, ld, blocks, row_codes, row_scales, col_codes, col_scales, dbias ? sums : nullptr, st);
+  ColSums left{sums, tiles_of(rows), n, dbias};  // until a product has taken them along
   if (s == BWD_OK && dx)
-    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, 1, st);
+    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, 1, &left, st);
   if (s == BWD_OK && dw)
-    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, 1, st);
+    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, 1,
+                &left, st);
+  if (s == BWD_OK) s = finish_col_sums(left, dtype, st);
   return s;
 }
 
