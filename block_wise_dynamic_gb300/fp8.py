@@ -93,7 +93,7 @@ class Fp8Matrix:
 
 
 def _pitch(cols: int) -> int:
-    return (cols + 127) // 128 * 128 if cols > 512 else (cols + 15) // 16 * 16
+    return (cols + 127) // 128 * 128 if cols > 64 else (cols + 15) // 16 * 16
 
 
 def _scale_bytes(count: int, length: int) -> int:

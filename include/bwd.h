@@ -344,8 +344,9 @@ bwd_status bwd_grad_norm(int32_t num_tensors, const void* const* g,
  * the NaN scale (byte 255) and NaN codes: every product with it is NaN.
  *
  * Code array of a rows x cols matrix: uint8[rows][pitch], 16-byte aligned,
- * pitch = bwd_fp8_pitch(cols) (cols rounded up to 16); the bytes past cols
- * may hold anything.
+ * pitch = bwd_fp8_pitch(cols): cols rounded up to 128, or to 16 for up to 64
+ * of them.  A product reads whole rows: the bytes past cols are zero (NaN
+ * codes beside NaN codes will do), as bwd_fp8_quantize writes them.
  *
  * Scale array for `count` lines of `length` elements, each line in blocks of
  * 128: bwd_fp8_scale_bytes(count, length) bytes, 16-byte aligned; the byte

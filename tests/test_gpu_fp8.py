@@ -74,6 +74,22 @@ def test_quantize(fp8, shape, kind, blocks):
     check_quantized(fp8.quantize(x, blocks), x, blocks)
 
 
+@pytest.mark.parametrize("blocks", ["rows", "cols", "both", "tiles"])
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("cols", [1, 17, 63, 65, 100, 129, 300, 513, 1003])
+def test_rows_are_padded_with_zeros(fp8, cols, kind, blocks):
+    """A product reads whole rows: what lies past a matrix must not count."""
+    x = draw((150, cols), cols, kind)
+    size = fp8.quantize(x, blocks).buffer.numel()
+    for _ in range(4):  # memory that held something else
+        torch.full((size,), 0x7F, dtype=torch.uint8, device=DEV)
+    q = fp8.quantize(x, blocks)
+    for codes in (q.row_codes, q.col_codes):
+        if codes is not None:
+            assert codes.shape == (150, fp8._pitch(cols))
+            assert not codes[:, cols:].any()
+
+
 @pytest.mark.parametrize("blocks", ["both", "tiles"])
 def test_quantize_special_values(fp8, blocks):
     x = torch.randn(300, 700, device=DEV)
