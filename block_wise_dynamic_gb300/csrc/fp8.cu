@@ -973,7 +973,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 }
 
 // --------------------------------------------------------------------------
-// product with few rows
+// product with few rows, or few tiles
 //
 // For few lines of A (tokens) the roles change: the 128 rows of the matrix
 // instruction are lines of B (the weight's outputs) and its columns the few
@@ -982,7 +982,11 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // the summed axis, so that all SMs read.  Each CTA keeps its part's sums in
 // its tensor memory; at the end CTA r gathers, from all of the cluster over
 // distributed shared memory, the r-th share of the columns and adds the parts
-// in the order of the ranks.
+// in the order of the ranks.  (Four columns to a store: 33 x 4096 x 11008 8.0
+// us against 9.7 a column at a time, 500 x 1024 x 1000 in four parts 6.8
+// against 12.4.)  Products of more lines that have few tiles and a long sum
+// are split here too, 128 lines to a tile: 353 x 9883 x 135 8.4 us against
+// 21.3 in pairs.
 //
 // Up to kFuse lines, A may also come unquantized: the warps that store in the
 // end then quantize each stage's 128 columns on the way into shared memory
@@ -991,8 +995,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 // same part of A again, so this pays for few lines only (33 x 4096 x 11008,
 // timed with a version of it for 64 lines: 19.2 us against 13.3).
 //
-// Measured, call after call: 1 x 4096 x 4096 5.3 us (its 16.8 MB take 2.5),
-// 1 x 4096 x 11008 6.7 (6.7), 33 x 4096 x 11008 9.7 without the quantizer.
+// Measured, call after call: 1 x 4096 x 4096 5.0 us (its 16.8 MB take 2.5),
+// 1 x 4096 x 11008 6.7 (6.7), 33 x 4096 x 11008 8.0 without the quantizer.
 // What it takes beyond the reading is a launch, the first copies' latency and
 // the gathering, 1 us or so each.
 
@@ -1001,10 +1005,12 @@ constexpr int kFewThreads = 320;  // warp 0 copies, warp 1 issues, warps 2 to 9 
 constexpr int kFewWarps = 8;
 template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 128 ? 3 : kBN >= 48 ? 4 : 5; }
 template <int kBN> __host__ __device__ constexpr int few_stage_bytes() { return kTile * kBK + kBN * kBK; }
-// Stages and their scales; the gathered parts, at most kBN + 7 columns of 128
-// fp32 sums, take the stages' place.
+// Columns of sums that go to the CTA that gathers them in one store.
+template <int kBN> __host__ __device__ constexpr int few_unit() { return kBN >= 32 ? 4 : 2; }
+// Stages and their scales; the gathered parts, at most seven units more than
+// kBN columns of 128 fp32 sums, take the stages' place.
 template <int kBN> __host__ __device__ constexpr int few_smem() {
-  static_assert((kBN + 8) * kTile * 4 <= few_stages<kBN>() * few_stage_bytes<kBN>(), "the parts fit the stages");
+  static_assert((kBN + 7 * few_unit<kBN>()) * kTile * 4 <= few_stages<kBN>() * few_stage_bytes<kBN>(), "the parts fit the stages");
   return 1024 + few_stages<kBN>() * (few_stage_bytes<kBN>() + 2 * kSfTile);
 }
 // Two CTAs share an SM and its tensor memory.  Accumulators that fit beside
@@ -1038,6 +1044,7 @@ struct FewArgs {
   int m, n, k;           // lines of A (columns here), lines of B (rows here), summed axis
   int a_trans, b_trans;
   int split;             // CTAs of a cluster, along the summed axis
+  int tiles_n;           // tiles of 128 lines of B
   int b_ready;           // B is no result of the kernel ahead
 };
 
@@ -1063,8 +1070,9 @@ __device__ __forceinline__ void few_load(const FewArgs& p, int line, int e, uint
   }
 }
 
-// map_w: lines of B in boxes of 128; map_x: all lines of A in one box of kBN
-// (128 where A is transposed: a swizzled row of its box).
+// map_w: lines of B in boxes of 128; map_x: lines of A in boxes of kBN, all of
+// them in one where it is less than 128 (a transposed A's box has 128: a
+// swizzled row of it).
 template <int kT, int kBN, bool kFused>
 __global__ void __launch_bounds__(kFewThreads, 2)
 fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const FewArgs p) {
@@ -1073,7 +1081,7 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const sf = sm + kStages * kStage;
-  float* const parts = reinterpret_cast<float*>(sm);  // [rank][column of the share][128], once the stages are done with
+  float* const parts = reinterpret_cast<float*>(sm);  // [rank][unit of the share][128][kQ], once the stages are done with
   __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
@@ -1081,7 +1089,8 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
-  const int n0 = static_cast<int>(blockIdx.x) / p.split * kTile;
+  const int tile = static_cast<int>(blockIdx.x) / p.split, n0 = tile % p.tiles_n * kTile, m0 = kBN == 128 ? tile / p.tiles_n * kBN : 0;
+  const int lines = p.m - m0 < kBN ? p.m - m0 : kBN;
   // this CTA's blocks of the summed axis, and its accumulators' share of them
   const int kb0 = static_cast<int>(static_cast<int64_t>(kblocks) * rank / p.split);
   const int count = static_cast<int>(static_cast<int64_t>(kblocks) * (rank + 1) / p.split) - kb0;
@@ -1130,9 +1139,9 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         if (i >= ahead) weight(i, ring.s);
         if constexpr (!kFused) {
           const int kb = kb0 + i;
-          tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? 0 : kb * kBK, p.a_trans ? kb * kBK : 0, &s_full[ring.s]);
+          tma_load_one(sm + ring.s * kStage + kW, &map_x, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, &s_full[ring.s]);
           if (i == 0 || (kb & 3) == 0)
-            bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + static_cast<int64_t>(kb / 4) * kSfTile, kSfTile,
+            bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + (static_cast<int64_t>(m0 / 128) * groups + kb / 4) * kSfTile, kSfTile,
                       &s_full[ring.s]);
         }
       }
@@ -1217,7 +1226,11 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   }
   __syncwarp();
   // warps w and w + 4 share a quarter of the rows and take turns at the columns
-  const int quarter = warp & 3, half = (warp - 2) / 4, share = (kBN + p.split - 1) / p.split;  // columns that a CTA gathers
+  const int quarter = warp & 3, half = (warp - 2) / 4;
+  // columns that a CTA gathers, in units of kQ that move as one; u / share is
+  // (u * magic) >> 16 for the few units there are
+  constexpr int kQ = few_unit<kBN>();
+  const uint32_t share = (kBN / kQ + p.split - 1) / p.split, magic = (65536 + share - 1) / share;
   const int row = quarter * 32 + lane;
   bool ok = true;
   if (warp >= 2) {
@@ -1231,7 +1244,7 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
     for (int c0 = 0; c0 < kBN; c0 += 32) {
       const int c = c0 + 16 * half;
-      if (c >= kBN || c >= p.m) break;
+      if (c >= kBN || c >= lines) break;
       float sum[16];
 #pragma unroll
       for (int u = 0; u < 16; ++u) sum[u] = 0.0f;
@@ -1246,12 +1259,16 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         for (int u = 0; u < 16; ++u) sum[u] = __fadd_rn(sum[u], __uint_as_float(r[u]));
       }
 #pragma unroll
-      for (int u = 0; u < 16; ++u) {
-        if (c + u >= p.m) break;
-        const int to = (c + u) / share, at = (static_cast<int>(rank) * share + (c + u) % share) * kTile + row;
+      for (int u = 0; u < 16; u += kQ) {
+        if (c + u >= lines) break;
+        const uint32_t unit = (c + u) / kQ, to = unit * magic >> 16, at = (rank * share + unit - to * share) * kTile + row;
         uint32_t dst;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + at)), "r"(to));
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(sum[u]) : "memory");
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + kQ * at)), "r"(to));
+        if constexpr (kQ == 4)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
+                       ::"r"(dst), "f"(sum[u]), "f"(sum[u + 1]), "f"(sum[u + 2]), "f"(sum[u + 3]) : "memory");
+        else
+          asm volatile("st.shared::cluster.v2.f32 [%0], {%1,%2};" ::"r"(dst), "f"(sum[u]), "f"(sum[u + 1]) : "memory");
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -1260,12 +1277,23 @@ fp8_matmul_few_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
   cluster_sync();
   if (warp >= 2 && ok && n0 + row < p.n) {
     const float bias = p.bias ? load1<kT>(p.bias, n0 + row) : 0.0f;
-    for (int c = half; c < share; c += 2) {
-      const int m = static_cast<int>(rank) * share + c;
-      if (m >= p.m) break;
-      float sum = parts[c * kTile + row];
-      for (int r = 1; r < p.split; ++r) sum = __fadd_rn(sum, parts[(r * share + c) * kTile + row]);
-      store1<kT>(p.out, m * p.ldo + n0 + row, p.bias ? __fadd_rn(sum, bias) : sum);
+    for (uint32_t u = half; u < share; u += 2) {
+      const int m = static_cast<int>((rank * share + u) * kQ);
+      if (m >= lines) break;
+      float sum[kQ];
+      const auto add = [&](uint32_t r, bool first) {
+        const float* const from = parts + kQ * ((r * share + u) * kTile + row);
+        float v[kQ];
+        if constexpr (kQ == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(from);
+        else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(from);
+#pragma unroll
+        for (int j = 0; j < kQ; ++j) sum[j] = first ? v[j] : __fadd_rn(sum[j], v[j]);
+      };
+      add(0, true);
+      for (int r = 1; r < p.split; ++r) add(r, false);
+#pragma unroll
+      for (int j = 0; j < kQ; ++j)
+        if (m + j < lines) store1<kT>(p.out, (m0 + m + j) * p.ldo + n0 + row, p.bias ? __fadd_rn(sum[j], bias) : sum[j]);
     }
   }
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kFewCols));
@@ -1387,6 +1415,8 @@ bwd_status launch_quantize(int mode, const QuantArgs& a, cudaStream_t st) {
   return a.col_sums ? launch(Both{}, std::true_type{}) : launch(Both{}, std::false_type{});
 }
 
+constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
+
 // What a launch needs to know of the device, found once for each.
 constexpr int kMaxDevices = 64;
 struct DeviceState {
@@ -1394,6 +1424,7 @@ struct DeviceState {
   unsigned long long ctx = 0;
   int sms = 0;
   int pairs = 0;  // CTA pairs that are resident at a time
+  int clusters[kMaxSplit + 1] = {};  // clusters of so many CTAs that find an SM for each CTA
 };
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -1454,6 +1485,22 @@ bwd_status ensure_device(const DeviceState** out) {
   e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false, 4>, &cfg);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
   if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
+  // so much shared memory that no SM takes two
+  int smem = 0;
+  e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceGetAttribute");
+  smem = smem / 2 > few_smem<128>() ? smem / 2 : few_smem<128>();
+  e = opt_in(fp8_matmul_few_kernel<kBF16, 128, false>, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
+  cfg.blockDim = dim3(kFewThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  d.clusters[1] = d.sms;
+  for (int c = 2; c <= kMaxSplit; ++c) {
+    cfg.gridDim = dim3(static_cast<unsigned>(d.sms / c * c));
+    attr[0].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
+    e = cudaOccupancyMaxActiveClusters(&d.clusters[c], fp8_matmul_few_kernel<kBF16, 128, false>, &cfg);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+  }
   d.ctx = ctx;
   d.ready = true;
   return BWD_OK;
@@ -1488,51 +1535,62 @@ bwd_status launch_matmul16(const MmMaps& maps, const MmArgs& p, int bn, int pair
   return launch_matmul<kT, 256, false, 8>(maps, p, pairs, st);
 }
 
-// As many parts of the summed axis as the device has room for at once, of two
-// blocks each at least.
-int64_t few_split(int64_t tiles_n, int64_t blocks, int sms) {
-  int64_t split = 2 * sms / tiles_n;
-  split = split > 8 ? 8 : split;
-  split = split > blocks / 2 ? blocks / 2 : split;
-  return split < 1 ? 1 : split;
+// Parts of the summed axis, of two blocks each at least: as many as find an SM
+// for each CTA, so that the kernel behind finds room to begin (33 x 4096 x
+// 4096 5.6 us with four parts, 6.9 with eight; 500 x 4096 x 1000 8.4 and
+// 11.5).  Where up to 64 lines of A leave parts of sixteen blocks or more,
+// reading B is what takes the time, and two CTAs on an SM read faster (1 x
+// 11008 x 4096 7.9 us with four, 7.0 with eight).
+int64_t few_split(int64_t tiles, int64_t blocks, int64_t lines, const DeviceState& d) {
+  const int64_t most = blocks / 2 < kMaxSplit ? blocks / 2 : kMaxSplit;
+  int64_t split = most < 1 ? 1 : most;
+  while (split > 1 && tiles > d.clusters[split]) --split;
+  if (lines > 64 || (blocks + split - 1) / split < 16) return split;
+  const int64_t two = 2 * d.sms / tiles < most ? 2 * d.sms / tiles : most;
+  return two > split ? two : split;
 }
 
 // x.codes null: A is p.x, quantized by the kernel.
 template <int kT, int kBN, bool kFused>
-bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, int sms, cudaStream_t st) {
+bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, const DeviceState& d, cudaStream_t st) {
   CUtensorMap map_w, map_x{};
   bwd_status s;
   if ((s = code_map(&map_w, w.codes, w.lines, p.k, w.trans, kTile)) != BWD_OK) return s;
   if (!kFused && (s = code_map(&map_x, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
-  const int64_t tiles_n = tiles_of(p.n);
-  p.split = static_cast<int>(few_split(tiles_n, tiles_of(p.k), sms));
-  return launch_ex(fp8_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles_n * p.split)),
+  const int64_t tiles = tiles_of(p.n) * ((p.m + kBN - 1) / kBN);
+  p.tiles_n = static_cast<int>(tiles_of(p.n));
+  p.split = static_cast<int>(few_split(tiles, tiles_of(p.k), p.m, d));
+  return launch_ex(fp8_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles * p.split)),
                    kFewThreads, p.split, few_smem<kBN>(), st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
 }
 
 template <int kT>
-bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, int sms, cudaStream_t st) {
-  if (!x.codes) return launch_few<kT, kFuse, true>(x, w, p, sms, st);
-  if (x.trans) return launch_few<kT, 128, false>(x, w, p, sms, st);
-  if (p.m > 48) return launch_few<kT, 64, false>(x, w, p, sms, st);
-  if (p.m > 32) return launch_few<kT, 48, false>(x, w, p, sms, st);
-  if (p.m > 16) return launch_few<kT, 32, false>(x, w, p, sms, st);
-  return launch_few<kT, 16, false>(x, w, p, sms, st);
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, const DeviceState& d, cudaStream_t st) {
+  if (!x.codes) return launch_few<kT, kFuse, true>(x, w, p, d, st);
+  if (x.trans || p.m > 64) return launch_few<kT, 128, false>(x, w, p, d, st);
+  if (p.m > 48) return launch_few<kT, 64, false>(x, w, p, d, st);
+  if (p.m > 32) return launch_few<kT, 48, false>(x, w, p, d, st);
+  if (p.m > 16) return launch_few<kT, 32, false>(x, w, p, d, st);
+  return launch_few<kT, 16, false>(x, w, p, d, st);
 }
 
-bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype, int sms, cudaStream_t st) {
-  if (dtype == BWD_F32) return few<kF32>(x, w, p, sms, st);
-  if (dtype == BWD_BF16) return few<kBF16>(x, w, p, sms, st);
-  return few<kF16>(x, w, p, sms, st);
+bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype, const DeviceState& d, cudaStream_t st) {
+  if (dtype == BWD_F32) return few<kF32>(x, w, p, d, st);
+  if (dtype == BWD_BF16) return few<kBF16>(x, w, p, d, st);
+  return few<kF16>(x, w, p, d, st);
 }
 
-// Whether a product goes to the kernel for few lines of A.
-bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, int sms) {
-  if (a.lines > 64) return false;
-  if (dtype != BWD_F32) return true;
+// Whether a product goes to the kernel for few lines of A, or few tiles.  For
+// more than 64 lines it takes some 6.0 us and 0.27 for each block of a part,
+// a pair 3.3 and 0.185 for each block of all (100 x 4096 x 300 6.1 us against
+// 10.4, 500 x 4096 x 1000 8.4 against 9.3, x 8192 10.5 against 15.2; 1000 x
+// 4096 x 1000 10.5 against 9.4 and 128 x 1024 x 1000 6.2 against 5.0).
+bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, const DeviceState& d) {
+  const int64_t blocks = tiles_of(k), tiles = tiles_of(n) * tiles_of(a.lines);
+  const int64_t split = few_split(tiles, blocks, a.lines, d), part = (blocks + split - 1) / split;
   // fp32 results: no accumulator may take more than kChunk blocks
-  const int64_t part = (tiles_of(k) + few_split(tiles_of(n), tiles_of(k), sms) - 1) / few_split(tiles_of(n), tiles_of(k), sms);
-  return part <= kChunk * (a.trans ? few_accs<128>() : few_accs<64>());
+  if (dtype == BWD_F32 && part > kChunk * (a.trans || a.lines > 64 ? few_accs<128>() : few_accs<64>())) return false;
+  return a.lines <= 64 || 3 * part + 24 < 2 * blocks;
 }
 
 // out = A B^T + bias, k > 0.  b_ready: a kernel that this call launched lies
@@ -1546,9 +1604,9 @@ bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, v
   const DeviceState* d = nullptr;
   bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
-  if (use_few(a, n, k, dtype, d->sms)) {
-    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1, b_ready};
-    return few(a, b, p, dtype, d->sms, st);
+  if (use_few(a, n, k, dtype, *d)) {
+    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1, 1, b_ready};
+    return few(a, b, p, dtype, *d, st);
   }
   const int64_t tiles_m = (m + kBM - 1) / kBM;
   // A tile of 256 columns takes up to one and a half times as long as one of
@@ -1778,8 +1836,8 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
     const DeviceState* d = nullptr;
     if ((s = ensure_device(&d)) != BWD_OK) return s;
     const FewArgs p{w_scales, nullptr, bias, y, ldy, x, ld, ld * eb % 16 == 0 && cols * eb % 16 == 0 && aligned16(x),
-                    static_cast<int>(rows), static_cast<int>(n), static_cast<int>(cols), 0, 0, 1, x_col_codes != nullptr};
-    return few(Lines{nullptr, nullptr, rows, 0}, Lines{w, w_scales, n, 0}, p, dtype, d->sms, st);
+                    static_cast<int>(rows), static_cast<int>(n), static_cast<int>(cols), 0, 0, 1, 1, x_col_codes != nullptr};
+    return few(Lines{nullptr, nullptr, rows, 0}, Lines{w, w_scales, n, 0}, p, dtype, *d, st);
   }
   Pieces pieces{static_cast<uint8_t*>(work)};
   uint8_t* const codes = pieces.take(rows * bwd_fp8_pitch(cols));

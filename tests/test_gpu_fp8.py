@@ -438,3 +438,20 @@ def test_calls_in_a_row_see_each_others_results(fp8, m):
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("trans_a,trans_b", [(False, False), (False, True), (True, False), (True, True)])
+@pytest.mark.parametrize("m,n,k", [(65, 1, 4000), (128, 129, 4097), (353, 135, 9883), (130, 2049, 5000), (500, 1000, 8192), (1300, 70, 6143),
+                                   (640, 900, 11000), (50, 1000, 9000)])
+def test_few_tiles_and_long_sums(fp8, m, n, k, trans_a, trans_b, kind):
+    """The summed axis in as many parts as there is room for."""
+    a = draw((k, m) if trans_a else (m, k), 41, "bf16")
+    b = draw((k, n) if trans_b else (n, k), 42, "bf16")
+    aq, bq = fp8.quantize(a, "cols" if trans_a else "rows"), fp8.quantize(b, "cols" if trans_b else "rows")
+    bias = draw((1, n), 43, kind, loud=False).view(-1)
+    av, bv = (q.dequantize("cols" if t else "rows", torch.float32).double() for q, t in ((aq, trans_a), (bq, trans_b)))
+    av, bv = av.t() if trans_a else av, bv.t() if trans_b else bv
+    got = fp8.matmul(aq, bq, trans_a, trans_b, bias=bias, dtype=TYPES[kind])
+    near(got, np64(av @ bv.t() + bias.double()), np64(av.abs() @ bv.abs().t() + bias.double().abs()), k, kind)
+    assert torch.equal(got, fp8.matmul(aq, bq, trans_a, trans_b, bias=bias, dtype=TYPES[kind]))
