@@ -80,8 +80,8 @@ def _launch(entry: str, device: torch.device, stream, *args) -> None:
     """Calls a library entry point whose last argument is the stream, with
     ``device`` current."""
     fn = getattr(_abi.load(), entry)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream_handle(device, stream))
+    if torch._C._cuda_getDevice() == device.index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream_handle(device, stream))
     else:
         with torch.cuda.device(device):
             st = fn(*args, _stream_handle(device, stream))

@@ -21,6 +21,7 @@ Each function checks and marshals CUDA tensors and calls ``bwd_fp8_*`` of
 
 from __future__ import annotations
 
+from functools import lru_cache
 from typing import Optional
 
 import torch
@@ -32,6 +33,10 @@ __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward",
 
 _BLOCKS = {"rows": _abi.FP8_ROWS, "cols": _abi.FP8_COLS, "both": _abi.FP8_ROWS | _abi.FP8_COLS, "tiles": _abi.FP8_TILES}
 _FUSED_ROWS = 16  # rows that the library's product quantizes itself, without a workspace
+# Up to this many bytes of workspace lie behind the matrix that forward() returns
+# and live as long: such calls take less time than an allocation costs (2.5 of
+# some 58 us for a training pass of 300 x 704 x 304).
+_ROOM = 1 << 20
 
 
 class Fp8Matrix:
@@ -42,26 +47,15 @@ class Fp8Matrix:
 
     __slots__ = ("shape", "blocks", "dtype", "device", "buffer", "_places", "_pointers")
 
-    def __init__(self, rows: int, cols: int, blocks: str, dtype, device):
-        kind = _BLOCKS[blocks]
+    def __init__(self, rows: int, cols: int, blocks: str, dtype, device, room: int = 0):
+        """``room``: bytes that the buffer has beyond the matrix, from a multiple of 256 on."""
         self.shape, self.blocks, self.dtype, self.device = (rows, cols), blocks, dtype, device
-        codes = _round256(rows * _pitch(cols))
-        rc = rs = cc = cs = None
-        end = 0
-        if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
-            rc, rs = 0, codes
-            end = codes + _round256(_scale_bytes(rows, cols))
-        if kind & _abi.FP8_COLS:
-            cc, cs = end, end + codes
-            end += codes + _scale_bytes(cols, rows)
-        elif kind & _abi.FP8_TILES:
-            cc, cs = 0, end
-            end += _scale_bytes(cols, rows)
-        self.buffer = torch.empty(end, dtype=torch.uint8, device=device)
-        # of row codes, row scales, column codes, column scales: offsets in the buffer, addresses
+        rc, rs, cc, cs, end = self._places = _layout(rows, cols, _BLOCKS[blocks])
+        self.buffer = torch.empty(_round256(end) + room if room else end, dtype=torch.uint8, device=device)
+        # addresses of row codes, row scales, column codes, column scales
         base = self.buffer.data_ptr()
-        self._places = (rc, rs, cc, cs)
-        self._pointers = tuple(None if at is None else base + at for at in self._places)
+        self._pointers = (None if rc is None else base + rc, None if rs is None else base + rs,
+                          None if cc is None else base + cc, None if cs is None else base + cs)
 
     def _view(self, which, size):
         at = self._places[which]
@@ -90,6 +84,38 @@ class Fp8Matrix:
 
     def dequantize(self, along="rows", dtype=None, stream=None):
         return dequantize(self, along, dtype, stream)
+
+
+@lru_cache(maxsize=1024)
+def _layout(rows: int, cols: int, kind: int):
+    """Offsets in a matrix's buffer of row codes, row scales, column codes and
+    column scales, and the buffer's size."""
+    codes = _round256(rows * _pitch(cols))
+    rc = rs = cc = cs = None
+    end = 0
+    if kind & (_abi.FP8_ROWS | _abi.FP8_TILES):
+        rc, rs = 0, codes
+        end = codes + _round256(_scale_bytes(rows, cols))
+    if kind & _abi.FP8_COLS:
+        cc, cs = end, end + codes
+        end += codes + _scale_bytes(cols, rows)
+    elif kind & _abi.FP8_TILES:
+        cc, cs = 0, end
+        end += _scale_bytes(cols, rows)
+    return rc, rs, cc, cs, end
+
+
+@lru_cache(maxsize=1024)
+def _forward_work(rows: int, cols: int) -> int:
+    """bwd_fp8_linear_work_bytes."""
+    return 0 if rows <= _FUSED_ROWS else _round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols))
+
+
+@lru_cache(maxsize=1024)
+def _backward_work(rows: int, n: int) -> int:
+    """bwd_fp8_linear_backward_work_bytes."""
+    return (2 * _round256(rows * _pitch(n)) + _round256(_scale_bytes(rows, n)) + _round256(_scale_bytes(n, rows)) +
+            _round256((rows + 127) // 128 * n * 4))
 
 
 def _pitch(cols: int) -> int:
@@ -241,13 +267,18 @@ def _forward(x, w, bias, both, stream):
         _need(bias, "bias", dt, n, dev)
     y = torch.empty((rows, n) if m is x else (*x.shape[:-1], n), dtype=dt, device=dev)
     work = cc = cs = xq = None
-    if rows > _FUSED_ROWS:
-        work = _bytes(_round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols)), dev)
+    size = _forward_work(rows, cols)
     if both:
-        xq = Fp8Matrix(rows, cols, "cols", dt, dev)
+        room = size if size <= _ROOM else 0
+        xq = Fp8Matrix(rows, cols, "cols", dt, dev, room)
         _, _, cc, cs = xq._pointers
+        if room:
+            work = xq.buffer.data_ptr() + xq.buffer.numel() - room
+    if size and work is None:
+        scratch = _bytes(size, dev)
+        work = scratch.data_ptr()
     _launch("bwd_fp8_linear", dev, None, m.data_ptr(), _GDT[dt], rows, cols, max(m.stride(0), cols), codes, scales, n, _ptr(bias),
-            y.data_ptr(), n, cc, cs, _ptr(work))
+            y.data_ptr(), n, cc, cs, work)
     return y, xq
 
 
@@ -285,9 +316,7 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
         dx = torch.empty((rows, k) if m is dy else (*dy.shape[:-1], k), dtype=dt, device=dev)
     if need_bias:
         db = torch.empty(n, dtype=dt, device=dev)
-    codes_bytes = _round256(rows * _pitch(n))
-    work = _bytes(2 * codes_bytes + _round256(_scale_bytes(rows, n)) + _round256(_scale_bytes(n, rows)) +
-                  _round256((rows + 127) // 128 * n * 4), dev)
+    work = _bytes(_backward_work(rows, n), dev)
     _launch("bwd_fp8_linear_backward", dev, None, m.data_ptr(), _GDT[dt], rows, n, max(m.stride(0), n), codes, scales, xc, xs, k,
             _ptr(dx), k, _ptr(dw), k, _ptr(db), work.data_ptr())
     return dx, dw, db
