@@ -440,14 +440,19 @@ col_sums_kernel(const ColSums a) {
   store1<kT>(a.out, c, s);
 }
 
-// Beside a product: every `step`-th group of 32 columns to a warp.
+// Beside a product: every `step`-th group of 32 columns to a warp, in the same
+// order of additions.
 template <int kT>
 __device__ __forceinline__ void col_sums_of_warp(const ColSums& a, int64_t first, int64_t step) {
   for (int64_t c = 32 * first + threadIdx.x % 32; c < a.cols; c += 32 * step) {
-    float s = 0.0f;
-#pragma unroll 8
-    for (int64_t t = 0; t < a.tiles; ++t) s += a.partial[t * a.cols + c];
-    store1<kT>(a.out, c, s);
+    float s[kSumWarps] = {};
+    for (int64_t t = 0; t < a.tiles; t += kSumWarps)
+#pragma unroll
+      for (int w = 0; w < kSumWarps; ++w)
+        if (t + w < a.tiles) s[w] += a.partial[(t + w) * a.cols + c];
+#pragma unroll
+    for (int w = 1; w < kSumWarps; ++w) s[0] += s[w];
+    store1<kT>(a.out, c, s[0]);
   }
 }
 
@@ -662,22 +667,39 @@ struct MmArgs {
   int tiles_m, tiles_n;
   int whole;             // the first tiles; the rest are worked on as two halves of 128 columns each
   int sf_rows_b;         // row tiles of B's scales
-  ColSums sums;          // column sums to finish beside the product
   int store;             // the output's rows allow tensor stores,
   int unit;              // or stores of so many bytes
+};
+
+struct MmMaps {
+  CUtensorMap a, b, sfa, sfb, out;
+};
+
+// One product, or two of one call in one launch: the pairs go on from the
+// first one's tiles to the second one's, with no kernel's end and start
+// between them.
+template <int kCount>
+struct MmCall {
+  MmMaps maps[kCount];
+  MmArgs p[kCount];
+  int items[2];   // of the first, of both
+  ColSums sums;   // column sums to finish beside the products
 };
 
 // What a pair works on: a tile, or half of one (its columns from n0 on).  A
 // last wave that less than half fills the device is cut into halves, which
 // take half as long.
 struct Item {
-  int m0, n0, cols;
+  int m0, n0, cols, call;
 };
-template <int kBN>
-__device__ __forceinline__ Item item_of(const MmArgs& p, int i) {
-  if (kBN == 128 || i < p.whole) return Item{i / p.tiles_n * kBM, i % p.tiles_n * kBN, kBN};
+template <int kBN, bool kTwo>
+__device__ __forceinline__ Item item_of(const MmCall<kTwo ? 2 : 1>& c, int i) {
+  const int call = kTwo && i >= c.items[0] ? 1 : 0;
+  if (call) i -= c.items[0];
+  const MmArgs& p = c.p[call];
+  if (kBN == 128 || i < p.whole) return Item{i / p.tiles_n * kBM, i % p.tiles_n * kBN, kBN, call};
   const int t = p.whole + (i - p.whole) / 2;
-  return Item{t / p.tiles_n * kBM, t % p.tiles_n * kBN + (i - p.whole) % 2 * 128, 128};
+  return Item{t / p.tiles_n * kBM, t % p.tiles_n * kBN + (i - p.whole) % 2 * 128, 128, call};
 }
 
 // The two accumulators.  With 256 columns each they overlap by 32 columns,
@@ -685,11 +707,11 @@ __device__ __forceinline__ Item item_of(const MmArgs& p, int i) {
 // columns first and the next tile's products start when they have.
 template <int kBN> __device__ __forceinline__ uint32_t acc_col(int buf) { return buf ? (kBN == 256 ? 224u : 128u) : 0u; }
 
-template <int kT, int kBN, bool kSum, int kWarps>
+// kTwo: the call may have two products.  (Its arguments are then read through
+// an index: 4096 x 7 x 4096 13.5 us with it, 11.8 without.)
+template <int kT, int kBN, bool kSum, int kWarps, bool kTwo>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(mm_threads(kWarps), 1)
-fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                  const __grid_constant__ CUtensorMap map_sfa, const __grid_constant__ CUtensorMap map_sfb,
-                  const __grid_constant__ CUtensorMap map_out, const MmArgs p) {
+fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
   static_assert(kWarps == 8 || (kWarps == 4 && !kSum), "a thread's registers hold the sums of 128 columns at most");
   constexpr int kStages = mm_stages<kBN, kWarps>(), kA = mm_a_bytes<kBN>(), kB = mm_b_bytes<kBN>(), kSf = mm_sf_bytes<kBN>();
   extern __shared__ uint8_t smem_raw[];
@@ -704,10 +726,10 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
   if (threadIdx.x == 0) {
-    prefetch_map(&map_a);
-    prefetch_map(&map_b);
-    prefetch_map(&map_sfa);
-    prefetch_map(&map_sfb);
+    prefetch_map(&c.maps[0].a);
+    prefetch_map(&c.maps[0].b);
+    prefetch_map(&c.maps[0].sfa);
+    prefetch_map(&c.maps[0].sfb);
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 2 * kWarps); }
@@ -723,10 +745,11 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
-  const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
-  const int items = 2 * p.tiles_m * p.tiles_n - p.whole, pairs = static_cast<int>(gridDim.x) / 2;
-  const int first = static_cast<int>(blockIdx.x) / 2;
-  const int chunk = kSum ? kChunk : kblocks;
+  const int items = c.items[1], pairs = static_cast<int>(gridDim.x) / 2;
+  // two products' tiles forth and back: whoever has one of the longer sums
+  // first has none of the wave behind that is not full (2048 x 1024 x 1024's
+  // backward pass 18.0 us against 21.5)
+  const int first = static_cast<int>(blockIdx.x) / 2, turn = kTwo ? 2 * (pairs - first) - 1 : pairs;
 
   if (warp == 0) {
     wait_for_inputs();
@@ -734,8 +757,11 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
     const bool one = elect_one();
     Ring<kStages> ring;
     bool ok = true;
-    for (int t = first; ok && t < items; t += pairs) {
-      const Item item = item_of<kBN>(p, t);
+    for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+      const Item item = item_of<kBN, kTwo>(c, t);
+      const MmArgs& p = c.p[kTwo ? item.call : 0];
+      const MmMaps& maps = c.maps[kTwo ? item.call : 0];
+      const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
       // of a half, the copies of B bring as many lines as of a whole
       const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2), nt = item.n0, n0 = nt + static_cast<int>(rank) * (item.cols / 2);
       for (int kb = 0; kb < kblocks; ++kb, ring.next()) {
@@ -746,15 +772,15 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           if (rank == 0) mbar_expect_tx(&s_full[ring.s], 2 * (kA + kB + (scales ? kSf : 0)));
           uint8_t* const a = sm + ring.s * (kA + kB);
           uint8_t* const b = a + kA;
-          tma_load(a, &map_a, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, bar);
-          tma_load(b, &map_b, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, bar);
+          tma_load(a, &maps.a, p.a_trans ? m0 : kb * kBK, p.a_trans ? kb * kBK : m0, bar);
+          tma_load(b, &maps.b, p.b_trans ? n0 : kb * kBK, p.b_trans ? kb * kBK : n0, bar);
           if (scales) {
             // A's for this CTA's rows, B's for the whole tile
-            tma_load(sf + ring.s * kSf, &map_sfa, 0, m0 / 128 * groups + kb / 4, bar);
+            tma_load(sf + ring.s * kSf, &maps.sfa, 0, m0 / 128 * groups + kb / 4, bar);
 #pragma unroll
             for (int h = 0; h < kBN / 128; ++h) {
               const int rt = nt / 128 + h;  // past the last row tile: columns past n, whatever they hold
-              tma_load(sf + ring.s * kSf + (1 + h) * kSfTile, &map_sfb, 0, (rt < p.sf_rows_b ? rt : p.sf_rows_b - 1) * groups + kb / 4, bar);
+              tma_load(sf + ring.s * kSf + (1 + h) * kSfTile, &maps.sfb, 0, (rt < p.sf_rows_b ? rt : p.sf_rows_b - 1) * groups + kb / 4, bar);
             }
           }
         }
@@ -764,24 +790,27 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
   } else if (warp == 1) {
     if (rank != 0) {
       // the issuing warp of the second CTA has nothing to issue
-      if (p.sums.out) {
+      if (c.sums.out) {
         wait_for_inputs();
-        col_sums_of_warp<kT>(p.sums, first, pairs);
+        col_sums_of_warp<kT>(c.sums, first, pairs);
       }
     } else {
       const bool one = elect_one();
-      // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
-      const uint32_t idesc0 = (static_cast<uint32_t>(p.a_trans) << 15) | (static_cast<uint32_t>(p.b_trans) << 16) | (1u << 23) | ((kBM / 16) << 24);
       // descriptors of stage 0, and the step of 32 along the summed axis
-      const uint64_t da0 = smem_desc(smem_u32(sm), 16, 1024, 2);
-      const uint64_t db0 = p.b_trans && kBN == 128 ? smem_desc(smem_u32(sm + kA), 16, 512, 4) : smem_desc(smem_u32(sm + kA), 16, 1024, 2);
-      const uint64_t dsf0 = smem_desc(smem_u32(sf), 16, 128, 0);
-      const uint32_t sa = p.a_trans ? 4096 / 16 : 32 / 16, sb = p.b_trans ? kBN / 2 * 32 / 16 : 32 / 16;
+      const uint64_t da0 = smem_desc(smem_u32(sm), 16, 1024, 2), dsf0 = smem_desc(smem_u32(sf), 16, 128, 0);
       Ring<kStages> ring;
       int use = 0;  // accumulators used so far
       bool ok = true;
-      for (int t = first; ok && t < items; t += pairs) {
-        const uint32_t idesc = idesc0 | static_cast<uint32_t>(item_of<kBN>(p, t).cols / 8) << 17;
+      for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+        const Item item = item_of<kBN, kTwo>(c, t);
+        const MmArgs& p = c.p[kTwo ? item.call : 0];
+        const int kblocks = (p.k + kBK - 1) / kBK, chunk = kSum ? kChunk : kblocks;
+        const int a_trans = p.a_trans, b_trans = p.b_trans;
+        // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
+        const uint32_t idesc = (static_cast<uint32_t>(a_trans) << 15) | (static_cast<uint32_t>(b_trans) << 16) |
+                               (static_cast<uint32_t>(item.cols / 8) << 17) | (1u << 23) | ((kBM / 16) << 24);
+        const uint64_t db0 = b_trans && kBN == 128 ? smem_desc(smem_u32(sm + kA), 16, 512, 4) : smem_desc(smem_u32(sm + kA), 16, 1024, 2);
+        const uint32_t sa = a_trans ? 4096 / 16 : 32 / 16, sb = b_trans ? kBN / 2 * 32 / 16 : 32 / 16;
         for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
           const int buf = use & 1;
           ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
@@ -842,15 +871,16 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
     };
-    for (int t = first; ok && t < items; t += pairs) {
-      const Item item = item_of<kBN>(p, t);
+    for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+      const Item item = item_of<kBN, kTwo>(c, t);
+      const MmArgs& p = c.p[kTwo ? item.call : 0];
       const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = item.n0 + half * kHalf;
       const int cols = item.cols - half * kHalf;  // of a half tile, some columns are not there
       float sum[kSum ? kHalf : 1];
       if constexpr (kSum) {
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) sum[j] = 0.0f;
-        for (int k0 = 0; ok && k0 < kblocks; k0 += chunk, ++use) {
+        for (int k0 = 0; ok && k0 < p.k; k0 += kChunk * kBK, ++use) {
           const int buf = use & 1;
           ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[buf], (use >> 1) & 1, &s_fail));
           if (!ok) break;
@@ -888,7 +918,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
       for (int i = 0; i < kGroups; ++i) {
         // shared columns first
         const int gr = kSum ? i : kWarps == 4 ? (buf == 0 ? (i + kGroups - 1) % kGroups : i) : half == 0 ? i : kGroups - 1 - i;
-        const int c = gr * kCols;
+        const int col = gr * kCols;
         float v[kCols];
         if constexpr (kSum) {
 #pragma unroll
@@ -896,18 +926,18 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         } else {
           uint32_t r[kCols / 32][32];
 #pragma unroll
-          for (int h = 0; h < kCols / 32; ++h) tmem_load32(own + acc_col<kBN>(buf) + c + 32 * h, r[h]);
+          for (int h = 0; h < kCols / 32; ++h) tmem_load32(own + acc_col<kBN>(buf) + col + 32 * h, r[h]);
           asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
           if (i == 0) done_shared(buf);
           if (i == kGroups - 1) done_all(buf);
 #pragma unroll
           for (int j = 0; j < kCols; ++j) v[j] = __uint_as_float(r[j / 32][j % 32]);
         }
-        if (c >= cols) continue;
+        if (col >= cols) continue;
         if (p.bias) {
           __syncwarp();
 #pragma unroll
-          for (int h = 0; h < kCols; h += 32) bias_s[h + lane] = n0 + c + h + lane < p.n ? load1<kT>(p.bias, n0 + c + h + lane) : 0.0f;
+          for (int h = 0; h < kCols; h += 32) bias_s[h + lane] = n0 + col + h + lane < p.n ? load1<kT>(p.bias, n0 + col + h + lane) : 0.0f;
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < kCols; j += 4) {
@@ -917,7 +947,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           }
         }
         // a row of 128 bytes per lane, its 16-byte pieces swizzled as the tensor map says
-        if (p.store && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -933,8 +963,8 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
         if (p.store) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0 && m0 < p.m && n0 + c < p.n) {
-            tma_store(&map_out, n0 + c, m0, stage);
+          if (lane == 0 && m0 < p.m && n0 + col < p.n) {
+            tma_store(&c.maps[kTwo ? item.call : 0].out, n0 + col, m0, stage);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
@@ -942,7 +972,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
           // alignment allows, consecutive lanes along a row
           __syncwarp();
           constexpr int kEb = elem_bytes<kT>();
-          char* const dst = static_cast<char*>(p.out) + (m0 * p.ldo + n0 + c) * kEb;
+          char* const dst = static_cast<char*>(p.out) + (m0 * p.ldo + n0 + col) * kEb;
           const int64_t row_bytes = p.ldo * kEb;
           const auto put_rows = [&](auto unit) {
             using Unit = decltype(unit);
@@ -956,7 +986,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
                 *reinterpret_cast<Unit*>(at + h) =
                     *reinterpret_cast<const Unit*>(stage + r * 128 + ((((byte + h) >> 4) ^ (r & 7)) << 4) + (byte & 15));
           };
-          if (m0 + 32 <= p.m && n0 + c + kCols <= p.n) {
+          if (m0 + 32 <= p.m && n0 + col + kCols <= p.n) {
             if (p.unit == 8) put_rows(uint2{});
             else if (kT == kF32 || p.unit == 4) put_rows(uint32_t{});
             else put_rows(uint16_t{});
@@ -966,7 +996,7 @@ fp8_matmul_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_consta
 #pragma unroll
               for (int h = 0; h < kCols; h += 32) {
                 const int byte = (h + lane) * kEb;
-                if (n0 + c + h + lane < p.n)
+                if (n0 + col + h + lane < p.n)
                   *reinterpret_cast<Elem*>(dst + r * row_bytes + byte) =
                       *reinterpret_cast<const Elem*>(stage + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 15));
               }
@@ -1447,6 +1477,12 @@ cudaError_t opt_in(F* kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
+template <int kT, int kBN, int kWarps>
+cudaError_t opt_in_pairs() {
+  const cudaError_t e = opt_in(fp8_matmul_kernel<kT, kBN, kT == kF32, kWarps, false>, mm_smem<kBN, kWarps>());
+  return e == cudaSuccess ? opt_in(fp8_matmul_kernel<kT, kBN, kT == kF32, kWarps, true>, mm_smem<kBN, kWarps>()) : e;
+}
+
 template <int kT, int kBN, bool kFused = false>
 cudaError_t opt_in_few() {
   return opt_in(fp8_matmul_few_kernel<kT, kBN, kFused>, few_smem<kBN>());
@@ -1474,14 +1510,14 @@ bwd_status ensure_device(const DeviceState** out) {
   *out = &d;
   if (d.ready && d.ctx == ctx) return BWD_OK;
   e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 256, true, 8>, mm_smem<256, 8>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF32, 128, true, 8>, mm_smem<128, 8>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false, 8>, mm_smem<256, 8>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false, 8>, mm_smem<256, 8>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 256, false, 4>, mm_smem<256, 4>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 256, false, 4>, mm_smem<256, 4>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kBF16, 128, false, 8>, mm_smem<128, 8>());
-  if (e == cudaSuccess) e = opt_in(fp8_matmul_kernel<kF16, 128, false, 8>, mm_smem<128, 8>());
+  if (e == cudaSuccess) e = opt_in_pairs<kF32, 256, 8>();
+  if (e == cudaSuccess) e = opt_in_pairs<kF32, 128, 8>();
+  if (e == cudaSuccess) e = opt_in_pairs<kBF16, 256, 8>();
+  if (e == cudaSuccess) e = opt_in_pairs<kF16, 256, 8>();
+  if (e == cudaSuccess) e = opt_in_pairs<kBF16, 256, 4>();
+  if (e == cudaSuccess) e = opt_in_pairs<kF16, 256, 4>();
+  if (e == cudaSuccess) e = opt_in_pairs<kBF16, 128, 8>();
+  if (e == cudaSuccess) e = opt_in_pairs<kF16, 128, 8>();
   if (e == cudaSuccess) e = opt_in_all_few<kF32>();
   if (e == cudaSuccess) e = opt_in_all_few<kBF16>();
   if (e == cudaSuccess) e = opt_in_all_few<kF16>();
@@ -1495,7 +1531,7 @@ bwd_status ensure_device(const DeviceState** out) {
   attr[0].val.clusterDim = {2, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false, 4>, &cfg);
+  e = cudaOccupancyMaxActiveClusters(&d.pairs, fp8_matmul_kernel<kBF16, 256, false, 4, false>, &cfg);
   if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
   if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
   // so much shared memory that no SM takes two
@@ -1519,10 +1555,6 @@ bwd_status ensure_device(const DeviceState** out) {
   return BWD_OK;
 }
 
-struct MmMaps {
-  CUtensorMap a, b, sfa, sfb, out;
-};
-
 // One product's operands: codes and scales of `lines` lines of k elements.
 struct Lines {
   const uint8_t* codes;
@@ -1531,21 +1563,94 @@ struct Lines {
   int trans;
 };
 
-template <int kT, int kBN, bool kSum, int kWarps>
-bwd_status launch_matmul(const MmMaps& maps, const MmArgs& p, int pairs, cudaStream_t st) {
-  const int items = 2 * p.tiles_m * p.tiles_n - p.whole;
-  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum, kWarps>, dim3(static_cast<unsigned>(2 * (items < pairs ? items : pairs))),
-                   mm_threads(kWarps), 0, mm_smem<kBN, kWarps>(), st,
-                   "fp8_matmul_kernel launch", maps.a, maps.b, maps.sfa, maps.sfb, maps.out, p);
+// out = A B^T + bias, k > 0.
+struct Product {
+  Lines a, b;
+  int64_t k;
+  const void* bias;
+  void* out;
+  int64_t ldo;
+};
+
+template <int kT, int kBN, int kWarps>
+bwd_status launch_matmul(const MmCall<2>& c, int pairs, cudaStream_t st) {
+  constexpr bool kSum = kT == kF32;
+  constexpr int kThreads = mm_threads(kWarps), kSmem = mm_smem<kBN, kWarps>();
+  const dim3 grid(static_cast<unsigned>(2 * (c.items[1] < pairs ? c.items[1] : pairs)));
+  if (c.items[0] < c.items[1])
+    return launch_ex(fp8_matmul_kernel<kT, kBN, kSum, kWarps, true>, grid, kThreads, 0, kSmem, st, "fp8_matmul_kernel launch", c);
+  const MmCall<1> one{{c.maps[0]}, {c.p[0]}, {c.items[0], c.items[1]}, c.sums};
+  return launch_ex(fp8_matmul_kernel<kT, kBN, kSum, kWarps, false>, grid, kThreads, 0, kSmem, st, "fp8_matmul_kernel launch", one);
 }
 
 // 16-bit results.  Four storing warps where a tile's products (sixteen stages
 // or more, some 6 us) outlast its tensor stores.
 template <int kT>
-bwd_status launch_matmul16(const MmMaps& maps, const MmArgs& p, int bn, int pairs, cudaStream_t st) {
-  if (bn == 128) return launch_matmul<kT, 128, false, 8>(maps, p, pairs, st);
-  if (p.store && p.k > 15 * kBK) return launch_matmul<kT, 256, false, 4>(maps, p, pairs, st);
-  return launch_matmul<kT, 256, false, 8>(maps, p, pairs, st);
+bwd_status launch_matmul16(const MmCall<2>& c, bool long_sums, int bn, int pairs, cudaStream_t st) {
+  if (bn == 128) return launch_matmul<kT, 128, 8>(c, pairs, st);
+  if (long_sums) return launch_matmul<kT, 256, 4>(c, pairs, st);
+  return launch_matmul<kT, 256, 8>(c, pairs, st);
+}
+
+int64_t tiles_of(const Product& q, int bn) { return (q.a.lines + kBM - 1) / kBM * ((q.b.lines + bn - 1) / bn); }
+
+// Columns of a product's tiles.  A tile of 256 columns takes up to one and a
+// half times as long as one of 128 (per stage 0.24 us against 0.17 where few
+// pairs work, 0.36 against 0.30 where all do): the wider one where it saves
+// more waves than that.  256 x 4096 x 11008 15.1 us against 17.7, 512 x 4096 x
+// 4096 11.3 against 14.9 the other way.
+int columns_of(const Product& q, int pairs) {
+  const auto waves = [&](int bn) { return (tiles_of(q, bn) + pairs - 1) / pairs; };
+  return 3 * waves(256) < 2 * waves(128) ? 256 : 128;
+}
+
+// One product, or two with tiles of as many columns, by CTA pairs.
+// *sums, where given, are column sums that the kernel finishes on the way;
+// they are cleared when it does.
+bwd_status by_pairs(const Product* q, int count, bwd_dtype dtype, const DeviceState& d, ColSums* sums, cudaStream_t st) {
+  const int eb = dtype == BWD_F32 ? 4 : 2, bn = columns_of(q[0], d.pairs);
+  MmCall<2> c{};
+  bool long_sums = true;
+  int64_t total = 0;
+  for (int i = 0; i < count; ++i) {
+    const Product& o = q[i];
+    const int64_t m = o.a.lines, n = o.b.lines, k = o.k, tiles = tiles_of(o, bn);
+    total += tiles;
+    if (total > 0x3fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
+      return fail(BWD_ERR_INVALID_ARG, "too many tiles");
+    const int64_t last = total % d.pairs;
+    const bool halves = i + 1 == count && bn == 256 && 2 * last <= d.pairs && last <= tiles;
+    MmArgs& p = c.p[i];
+    p.bias = o.bias; p.out = o.out; p.ldo = o.ldo;
+    p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
+    p.a_trans = o.a.trans; p.b_trans = o.b.trans;
+    p.tiles_m = static_cast<int>((m + kBM - 1) / kBM); p.tiles_n = static_cast<int>((n + bn - 1) / bn);
+    p.whole = static_cast<int>(halves ? tiles - last : tiles);
+    p.sf_rows_b = static_cast<int>(tiles_of(n));
+    p.store = aligned16(o.out) && o.ldo * eb % 16 == 0;
+    p.unit = unit_of(o.out, o.ldo * eb);
+    long_sums = long_sums && p.store && k > 15 * kBK;
+    c.items[1] = static_cast<int>(c.items[1] + 2 * tiles - p.whole);
+    if (i == 0) c.items[0] = c.items[1];
+    MmMaps& maps = c.maps[i];
+    bwd_status s;
+    if ((s = code_map(&maps.a, o.a.codes, m, k, o.a.trans, kBM / 2)) != BWD_OK) return s;
+    if ((s = code_map(&maps.b, o.b.codes, n, k, o.b.trans, bn / 2)) != BWD_OK) return s;
+    if ((s = scale_map(&maps.sfa, o.a.scales, tiles_of(m) * groups_of(k))) != BWD_OK) return s;
+    if ((s = scale_map(&maps.sfb, o.b.scales, tiles_of(n) * groups_of(k))) != BWD_OK) return s;
+    if (p.store) {
+      const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+      if ((s = matrix_map(&maps.out, type, o.out, m, n, o.ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
+    }
+  }
+  if (sums) {
+    c.sums = *sums;
+    sums->out = nullptr;
+  }
+  if (dtype == BWD_F32)
+    return bn == 256 ? launch_matmul<kF32, 256, 8>(c, d.pairs, st) : launch_matmul<kF32, 128, 8>(c, d.pairs, st);
+  return dtype == BWD_BF16 ? launch_matmul16<kBF16>(c, long_sums, bn, d.pairs, st) : launch_matmul16<kF16>(c, long_sums, bn, d.pairs, st);
 }
 
 // Parts of the summed axis, of two blocks each at least: as many as find an SM
@@ -1606,59 +1711,31 @@ bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, const Device
   return a.lines <= 64 || 3 * part + 24 < 2 * blocks;
 }
 
-// out = A B^T + bias, k > 0.  b_ready: a kernel that this call launched lies
-// between whatever wrote B and this product.
-// *sums, where given, are column sums that the product finishes on the way;
-// it clears them when it does.
-bwd_status matmul(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready, ColSums* sums,
-                  cudaStream_t st) {
-  const int64_t m = a.lines, n = b.lines;
-  const int eb = dtype == BWD_F32 ? 4 : 2;
+// b_ready: a kernel that this call launched lies between whatever wrote B and
+// this product.
+bwd_status matmul(const Product& q, bwd_dtype dtype, int b_ready, ColSums* sums, cudaStream_t st) {
+  const DeviceState* d = nullptr;
+  const bwd_status s = ensure_device(&d);
+  if (s != BWD_OK) return s;
+  if (!use_few(q.a, q.b.lines, q.k, dtype, *d)) return by_pairs(&q, 1, dtype, *d, sums, st);
+  const FewArgs p{q.b.scales, q.a.scales, q.bias, q.out, q.ldo, nullptr, 0, 0, static_cast<int>(q.a.lines), static_cast<int>(q.b.lines),
+                  static_cast<int>(q.k), q.a.trans, q.b.trans, 1, 1, b_ready};
+  return few(q.a, q.b, p, dtype, *d, st);
+}
+
+// Two products of one call.  In one launch where both are for pairs and want
+// the same tiles, the longer sum first (4096 x 1024 x 4096's backward pass 39.4 us
+// against 43.7, 700 x 600 x 500's 8.7 against 12.7).
+bwd_status both(const Product& q, const Product& r, bwd_dtype dtype, ColSums* sums, cudaStream_t st) {
   const DeviceState* d = nullptr;
   bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
-  if (use_few(a, n, k, dtype, *d)) {
-    const FewArgs p{b.scales, a.scales, bias, out, ldo, nullptr, 0, 0, static_cast<int>(m), static_cast<int>(n), static_cast<int>(k), a.trans, b.trans, 1, 1, b_ready};
-    return few(a, b, p, dtype, *d, st);
+  if (!use_few(q.a, q.b.lines, q.k, dtype, *d) && !use_few(r.a, r.b.lines, r.k, dtype, *d) && columns_of(q, d->pairs) == columns_of(r, d->pairs)) {
+    const Product two[2] = {q.k < r.k ? r : q, q.k < r.k ? q : r};
+    return by_pairs(two, 2, dtype, *d, sums, st);
   }
-  const int64_t tiles_m = (m + kBM - 1) / kBM;
-  // A tile of 256 columns takes up to one and a half times as long as one of
-  // 128 (per stage 0.24 us against 0.17 where few pairs work, 0.36 against
-  // 0.30 where all do): the wider one where it saves more waves than that.
-  // 256 x 4096 x 11008 15.1 us against 17.7, 512 x 4096 x 4096 11.3 against
-  // 14.9 the other way.
-  const auto waves = [&](int64_t width) { return (tiles_m * ((n + width - 1) / width) + d->pairs - 1) / d->pairs; };
-  const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
-  const int64_t tiles_n = (n + bn - 1) / bn;
-  const int64_t tiles = tiles_m * tiles_n, last = tiles % d->pairs;
-  if (tiles > 0x3fffffff || tiles_of(m) * groups_of(k) > 0x7fffffff || tiles_of(n) * groups_of(k) > 0x7fffffff)
-    return fail(BWD_ERR_INVALID_ARG, "too many tiles");
-  MmArgs p{};
-  p.bias = bias; p.out = out; p.ldo = ldo;
-  p.m = static_cast<int>(m); p.n = static_cast<int>(n); p.k = static_cast<int>(k);
-  p.a_trans = a.trans; p.b_trans = b.trans;
-  p.tiles_m = static_cast<int>(tiles_m); p.tiles_n = static_cast<int>(tiles_n);
-  p.whole = static_cast<int>(bn == 256 && 2 * last <= d->pairs ? tiles - last : tiles);
-  p.sf_rows_b = static_cast<int>(tiles_of(n));
-  if (sums) {
-    p.sums = *sums;
-    sums->out = nullptr;
-  }
-  p.store = aligned16(out) && ldo * eb % 16 == 0;
-  p.unit = unit_of(out, ldo * eb);
-  MmMaps maps{};
-  if ((s = code_map(&maps.a, a.codes, m, k, a.trans, kBM / 2)) != BWD_OK) return s;
-  if ((s = code_map(&maps.b, b.codes, n, k, b.trans, bn / 2)) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfa, a.scales, tiles_of(m) * groups_of(k))) != BWD_OK) return s;
-  if ((s = scale_map(&maps.sfb, b.scales, tiles_of(n) * groups_of(k))) != BWD_OK) return s;
-  if (p.store) {
-    const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                                     : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    if ((s = matrix_map(&maps.out, type, out, m, n, ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
-  }
-  if (dtype == BWD_F32)
-    return bn == 256 ? launch_matmul<kF32, 256, true, 8>(maps, p, d->pairs, st) : launch_matmul<kF32, 128, true, 8>(maps, p, d->pairs, st);
-  return dtype == BWD_BF16 ? launch_matmul16<kBF16>(maps, p, bn, d->pairs, st) : launch_matmul16<kF16>(maps, p, bn, d->pairs, st);
+  s = matmul(q, dtype, 1, sums, st);
+  return s == BWD_OK ? matmul(r, dtype, 1, sums->out ? sums : nullptr, st) : s;
 }
 
 // The bias, or zero: a product over nothing.
@@ -1669,10 +1746,9 @@ bwd_status fill(int64_t m, int64_t n, const void* bias, void* out, int64_t ldo, 
                    dim3(grid), 256, 0, 0, st, "fill_rows_kernel launch", bias, out, ldo, m, n);
 }
 
-bwd_status product(const Lines& a, const Lines& b, int64_t k, const void* bias, void* out, int64_t ldo, bwd_dtype dtype, int b_ready, ColSums* sums,
-                   cudaStream_t st) {
-  if (a.lines == 0 || b.lines == 0) return BWD_OK;
-  return k == 0 ? fill(a.lines, b.lines, bias, out, ldo, dtype, st) : matmul(a, b, k, bias, out, ldo, dtype, b_ready, sums, st);
+bwd_status product(const Product& q, bwd_dtype dtype, int b_ready, ColSums* sums, cudaStream_t st) {
+  if (q.a.lines == 0 || q.b.lines == 0) return BWD_OK;
+  return q.k == 0 ? fill(q.a.lines, q.b.lines, q.bias, q.out, q.ldo, dtype, st) : matmul(q, dtype, b_ready, sums, st);
 }
 
 bwd_status finish_col_sums(const ColSums& a, bwd_dtype dtype, cudaStream_t st) {
@@ -1814,7 +1890,7 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
   if (!aligned_to(out, eb) || (bias && !aligned_to(bias, eb))) return fail(BWD_ERR_INVALID_ARG, "out and bias must be aligned to their element size");
   if (k > 0 && (!aligned16(a) || !aligned16(b) || !aligned16(a_scales) || !aligned16(b_scales)))
     return fail(BWD_ERR_INVALID_ARG, "codes and scales must be 16-byte aligned");
-  return product(Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo, dtype, 0,
+  return product(Product{Lines{a, a_scales, m, a_trans ? 1 : 0}, Lines{b, b_scales, n, b_trans ? 1 : 0}, k, bias, out, ldo}, dtype, 0,
                  nullptr, static_cast<cudaStream_t>(stream));
 }
 
@@ -1858,7 +1934,7 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   s = quantize(x, dtype, rows, cols, ld, x_col_codes ? BWD_FP8_ROWS | BWD_FP8_COLS : BWD_FP8_ROWS, codes, scales, x_col_codes, x_col_scales,
                nullptr, st);
   if (s != BWD_OK) return s;
-  return product(Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy, dtype, 1, nullptr, st);
+  return product(Product{Lines{codes, scales, rows, 0}, Lines{w, w_scales, n, 0}, cols, bias, y, ldy}, dtype, 1, nullptr, st);
 }
 
 int64_t bwd_fp8_linear_backward_work_bytes(int64_t rows, int64_t n) {
@@ -1898,11 +1974,14 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype, int64_t rows
   const int blocks = (dx ? BWD_FP8_ROWS : 0) | (dw || dbias ? BWD_FP8_COLS : 0);
   s = quantize(dy, dtype, rows, n, ld, blocks, row_codes, row_scales, col_codes, col_scales, dbias ? sums : nullptr, st);
   ColSums left{sums, tiles_of(rows), n, dbias};  // until a product has taken them along
-  if (s == BWD_OK && dx)
-    s = product(Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx, dtype, 1, &left, st);
-  if (s == BWD_OK && dw)
-    s = product(Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw, dtype, 1,
-                &left, st);
+  const Product for_x{Lines{row_codes, row_scales, rows, 0}, Lines{w, w_col_scales, k, 1}, n, nullptr, dx, lddx};
+  const Product for_w{Lines{col_codes, col_scales, n, 1}, Lines{x_col_codes, x_col_scales, k, 1}, rows, nullptr, dw, lddw};
+  if (s == BWD_OK && dx && dw && some) {
+    s = both(for_x, for_w, dtype, &left, st);
+  } else {
+    if (s == BWD_OK && dx) s = product(for_x, dtype, 1, &left, st);
+    if (s == BWD_OK && dw) s = product(for_w, dtype, 1, &left, st);
+  }
   if (s == BWD_OK) s = finish_col_sums(left, dtype, st);
   return s;
 }

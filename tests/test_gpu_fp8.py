@@ -455,3 +455,21 @@ def test_few_tiles_and_long_sums(fp8, m, n, k, trans_a, trans_b, kind):
     got = fp8.matmul(aq, bq, trans_a, trans_b, bias=bias, dtype=TYPES[kind])
     near(got, np64(av @ bv.t() + bias.double()), np64(av.abs() @ bv.abs().t() + bias.double().abs()), k, kind)
     assert torch.equal(got, fp8.matmul(aq, bq, trans_a, trans_b, bias=bias, dtype=TYPES[kind]))
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("m,n,k", [(700, 600, 500), (2048, 1024, 1024), (4096, 1024, 640), (333, 3000, 1111), (5000, 2200, 2100), (300, 2176, 300)])
+def test_backward_of_two_products_in_one_launch(fp8, m, n, k, kind):
+    """The two products' tiles follow one another: each on its own, bit for
+    bit, whatever its neighbour's sizes and row alignment."""
+    x, w, dy = draw((m, k), 51, kind), draw((n, k), 52, kind, 0.02, loud=False), draw((m, n), 53, kind, 1e-3)
+    wq = fp8.quantize(w, "tiles")
+    xq, dyq = fp8.quantize(x, "cols"), fp8.quantize(dy, "both")
+    dx, dw, db = fp8.backward(dy, xq, wq, need_bias=True)
+    assert torch.equal(dx, fp8.matmul(dyq, wq, trans_b=True))
+    assert torch.equal(dw, fp8.matmul(dyq, xq, True, True))
+    assert torch.equal(db, fp8.quantize(dy, "cols", col_sums=True)[1])
+    wv, xv = wq.dequantize("cols", torch.float32).double(), xq.dequantize("cols", torch.float32).double()
+    rows, cols = dyq.dequantize("rows", torch.float32).double(), dyq.dequantize("cols", torch.float32).double()
+    near(dx, np64(rows @ wv), np64(rows.abs() @ wv.abs()), n, kind)
+    near(dw, np64(cols.t() @ xv), np64(cols.abs().t() @ xv.abs()), m, kind)
