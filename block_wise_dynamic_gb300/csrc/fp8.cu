@@ -745,11 +745,13 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = s_tmem;
+  // one product's arguments stay where the launch left them
+  using Args = std::conditional_t<kTwo, const MmArgs&, const MmArgs>;
   const int items = c.items[1], pairs = static_cast<int>(gridDim.x) / 2;
   // two products' tiles forth and back: whoever has one of the longer sums
   // first has none of the wave behind that is not full (2048 x 1024 x 1024's
   // backward pass 18.0 us against 21.5)
-  const int first = static_cast<int>(blockIdx.x) / 2, turn = kTwo ? 2 * (pairs - first) - 1 : pairs;
+  const int first = static_cast<int>(blockIdx.x) / 2, turn = 2 * (pairs - first) - 1;
 
   if (warp == 0) {
     wait_for_inputs();
@@ -757,9 +759,9 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
     const bool one = elect_one();
     Ring<kStages> ring;
     bool ok = true;
-    for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+    for (int t = first, step = turn; ok && t < items; t += kTwo ? step : pairs, step = 2 * pairs - step) {
       const Item item = item_of<kBN, kTwo>(c, t);
-      const MmArgs& p = c.p[kTwo ? item.call : 0];
+      const Args p = c.p[kTwo ? item.call : 0];
       const MmMaps& maps = c.maps[kTwo ? item.call : 0];
       const int kblocks = (p.k + kBK - 1) / kBK, groups = (kblocks + 3) / 4;
       // of a half, the copies of B bring as many lines as of a whole
@@ -801,9 +803,9 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
       Ring<kStages> ring;
       int use = 0;  // accumulators used so far
       bool ok = true;
-      for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+      for (int t = first, step = turn; ok && t < items; t += kTwo ? step : pairs, step = 2 * pairs - step) {
         const Item item = item_of<kBN, kTwo>(c, t);
-        const MmArgs& p = c.p[kTwo ? item.call : 0];
+        const Args p = c.p[kTwo ? item.call : 0];
         const int kblocks = (p.k + kBK - 1) / kBK, chunk = kSum ? kChunk : kblocks;
         const int a_trans = p.a_trans, b_trans = p.b_trans;
         // e4m3 x e4m3, E8M0 scales, fp32 accumulators; bits 15 and 16: transposed operands
@@ -871,9 +873,9 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
       __syncwarp();
       if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
     };
-    for (int t = first, step = turn; ok && t < items; t += step, step = 2 * pairs - step) {
+    for (int t = first, step = turn; ok && t < items; t += kTwo ? step : pairs, step = 2 * pairs - step) {
       const Item item = item_of<kBN, kTwo>(c, t);
-      const MmArgs& p = c.p[kTwo ? item.call : 0];
+      const Args p = c.p[kTwo ? item.call : 0];
       const int m0 = item.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, n0 = item.n0 + half * kHalf;
       const int cols = item.cols - half * kHalf;  // of a half tile, some columns are not there
       float sum[kSum ? kHalf : 1];
@@ -947,7 +949,7 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
           }
         }
         // a row of 128 bytes per lane, its 16-byte pieces swizzled as the tensor map says
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if ((kTwo || p.store) && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
