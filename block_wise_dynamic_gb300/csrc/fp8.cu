@@ -1701,16 +1701,18 @@ bwd_status few(const Lines& x, const Lines& w, const FewArgs& p, bwd_dtype dtype
 }
 
 // Whether a product goes to the kernel for few lines of A, or few tiles.  For
-// more than 64 lines it takes some 6.0 us and 0.27 for each block of a part,
-// a pair 3.3 and 0.185 for each block of all (100 x 4096 x 300 6.1 us against
-// 10.4, 500 x 4096 x 1000 8.4 against 9.3, x 8192 10.5 against 15.2; 1000 x
-// 4096 x 1000 10.5 against 9.4 and 128 x 1024 x 1000 6.2 against 5.0).
+// more than 64 lines, between kernels of other kinds, it takes some 6 us and
+// 0.27 for each block of a part, a pair 3.3 and 0.185 for each block of all;
+// with CTAs on more than half of the SMs some 2 us more, because they begin
+// later (quantizer and product together, in pairs and here: 128 x 4096 x 1000
+// 11.9 and 9.1 us, 606 x 4096 x 270 13.7 and 11.8, 500 x 8192 x 1000 19.3 and
+// 16.1; 500 x 2970 x 1000 10.9 and 13.8, 384 x 4096 x 1600 12.0 and 13.2).
 bool use_few(const Lines& a, int64_t n, int64_t k, bwd_dtype dtype, const DeviceState& d) {
   const int64_t blocks = tiles_of(k), tiles = tiles_of(n) * tiles_of(a.lines);
   const int64_t split = few_split(tiles, blocks, a.lines, d), part = (blocks + split - 1) / split;
   // fp32 results: no accumulator may take more than kChunk blocks
   if (dtype == BWD_F32 && part > kChunk * (a.trans || a.lines > 64 ? few_accs<128>() : few_accs<64>())) return false;
-  return a.lines <= 64 || 3 * part + 24 < 2 * blocks;
+  return a.lines <= 64 || 3 * part + (2 * tiles * split <= d.sms ? 24 : 48) < 2 * blocks;
 }
 
 // b_ready: a kernel that this call launched lies between whatever wrote B and
