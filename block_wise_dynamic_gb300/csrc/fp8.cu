@@ -667,8 +667,8 @@ struct MmArgs {
   int tiles_m, tiles_n;
   int whole;             // the first tiles; the rest are worked on as two halves of 128 columns each
   int sf_rows_b;         // row tiles of B's scales
-  int store;             // the output's rows allow tensor stores,
-  int unit;              // or stores of so many bytes
+  int store;             // columns that tensor stores take: all, whole groups only, or none;
+  int unit;              // the others go in stores of so many bytes
 };
 
 struct MmMaps {
@@ -962,16 +962,17 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = w;
         }
-        if (p.store) {
+        if (n0 + col < p.store) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0 && m0 < p.m && n0 + col < p.n) {
+          if (lane == 0 && m0 < p.m) {
             tma_store(&c.maps[kTwo ? item.call : 0].out, n0 + col, m0, stage);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
-          // rows of no 16-byte multiple: as many bytes to a lane as their
-          // alignment allows, consecutive lanes along a row
+          // rows of no 16-byte multiple, or a group that they end in: as many
+          // bytes to a lane as their alignment allows, consecutive lanes along
+          // a row
           __syncwarp();
           constexpr int kEb = elem_bytes<kT>();
           char* const dst = static_cast<char*>(p.out) + (m0 * p.ldo + n0 + col) * kEb;
@@ -992,7 +993,7 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
             if (p.unit == 8) put_rows(uint2{});
             else if (kT == kF32 || p.unit == 4) put_rows(uint32_t{});
             else put_rows(uint16_t{});
-          } else {
+          } else if (n0 + col < p.n) {
             using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
             for (int r = 0; r < 32 && m0 + r < p.m; ++r)
 #pragma unroll
@@ -1629,9 +1630,13 @@ bwd_status by_pairs(const Product* q, int count, bwd_dtype dtype, const DeviceSt
     p.tiles_m = static_cast<int>((m + kBM - 1) / kBM); p.tiles_n = static_cast<int>((n + bn - 1) / bn);
     p.whole = static_cast<int>(halves ? tiles - last : tiles);
     p.sf_rows_b = static_cast<int>(tiles_of(n));
-    p.store = aligned16(o.out) && o.ldo * eb % 16 == 0;
+    // A tensor store writes whole pieces of 16 bytes: where a row ends inside
+    // one, it would write up to 14 bytes past the end, so the map then covers
+    // whole groups of 128 bytes and the rest is stored element by element.
+    const int64_t mapped = n * eb % 16 == 0 ? n : n - n % (128 / eb);
+    p.store = aligned16(o.out) && o.ldo * eb % 16 == 0 ? static_cast<int>(mapped) : 0;
     p.unit = unit_of(o.out, o.ldo * eb);
-    long_sums = long_sums && p.store && k > 15 * kBK;
+    long_sums = long_sums && p.store > 0 && k > 15 * kBK;
     c.items[1] = static_cast<int>(c.items[1] + 2 * tiles - p.whole);
     if (i == 0) c.items[0] = c.items[1];
     MmMaps& maps = c.maps[i];
@@ -1643,7 +1648,7 @@ bwd_status by_pairs(const Product* q, int count, bwd_dtype dtype, const DeviceSt
     if (p.store) {
       const CUtensorMapDataType type = dtype == BWD_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                        : dtype == BWD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-      if ((s = matrix_map(&maps.out, type, o.out, m, n, o.ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
+      if ((s = matrix_map(&maps.out, type, o.out, m, mapped, o.ldo * eb, 128 / eb, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != BWD_OK) return s;
     }
   }
   if (sums) {
