@@ -367,8 +367,9 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
 
 int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {
   if (num_tensors < 0) return -1;
-  // a ticket, and a slot for each CTA of each launch; 256 SMs are more than the device has
-  const int64_t launches = (num_tensors + kNormTensors - 1) / kNormTensors;
+  // a ticket, and a slot for each CTA of each launch, of which a call over no
+  // tensor has one too; 256 SMs are more than the device has
+  const int64_t launches = num_tensors > kNormTensors ? (static_cast<int64_t>(num_tensors) + kNormTensors - 1) / kNormTensors : 1;
   return 16 + 8 * launches * 256 * kNormCtas;
 }
 
