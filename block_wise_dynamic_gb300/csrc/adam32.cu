@@ -171,7 +171,9 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
 // Norm.  A thread sums the squares of four 16-byte pieces in fp32, and such
 // sums, and those of the threads, in binary64; each CTA writes its sum to its
 // own slot, and the CTA that finishes last adds the slots in order, so the
-// result does not depend on the schedule.
+// result does not depend on the schedule.  Where the pieces' sum leaves the
+// range in which fp32 holds it in full (elements above some 1e19 or all below
+// 1e-18), they are read again and squared in binary64.
 
 constexpr int kNormTensors = 1024;
 constexpr int kNormCtas = 8;   // per SM
@@ -206,11 +208,29 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   return x;
 }
 
+// The same sum as chunk_squares's in binary64, for the few pieces that need
+// it: the square of any fp32 value is an ordinary binary64 number.
+template <int kG>
+__device__ __noinline__ double chunk_squares_wide(const void* g, int first, int len) {
+  constexpr int kVals = kG == kF32 ? 4 : 8;
+  double sum = 0.0;
+  for (int q = 0; q < kNormPieces; ++q) {
+    const int i = (q * kThreads + threadIdx.x) * kVals;
+    for (int j = 0; j < kVals; ++j)
+      if (i + j >= first && i + j < len) {
+        const double x = static_cast<double>(load1<kG>(g, i + j));
+        sum = __fma_rn(x, x, sum);
+      }
+  }
+  return sum;
+}
+
 // Sum of squares of this thread's share of elements first .. len - 1 of one
 // chunk; g is on a 16-byte boundary.
 template <int kG>
-__device__ __forceinline__ float chunk_squares(const void* g, int first, int len) {
+__device__ __forceinline__ double chunk_squares(const void* g, int first, int len) {
   constexpr int kVals = kG == kF32 ? 4 : 8;  // values of a piece
+  uint32_t any = 0;  // bits that are set in any value
   uint4 w[kNormPieces];
 #pragma unroll
   for (int q = 0; q < kNormPieces; ++q) {
@@ -226,6 +246,7 @@ __device__ __forceinline__ float chunk_squares(const void* g, int first, int len
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
         const uint32_t u = (&w[q].x)[kG == kF32 ? j : j / 2];
+        any |= u;
         const float x = kG == kF32 ? __uint_as_float(u) : widen<kG>(static_cast<unsigned short>(j % 2 ? u >> 16 : u & 0xffffu));
         sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
       }
@@ -233,11 +254,17 @@ __device__ __forceinline__ float chunk_squares(const void* g, int first, int len
       for (int j = 0; j < kVals; ++j)
         if (i + j >= first && i + j < len) {
           const float x = load1<kG>(g, i + j);
+          any |= __float_as_uint(x);
           sum[j % 2] = __fmaf_rn(x, x, sum[j % 2]);
         }
     }
   }
-  return __fadd_rn(sum[0], sum[1]);
+  const float all = __fadd_rn(sum[0], sum[1]);
+  // Below 2^-120 the roundings of up to 16 subnormal squares, 2^-150 each, may
+  // count.  Squares of fp16 values lie between 2^-48 and 2^32.
+  if (kG != kF16 && !(all >= 0x1p-120f && all <= 3.402823466e38f) && (any & (kG == kF32 ? 0x7fffffffu : 0x7fff7fffu)) != 0)
+    return chunk_squares_wide<kG>(g, first, len);
+  return static_cast<double>(all);
 }
 
 __global__ void __launch_bounds__(kThreads, kNormCtas)
@@ -256,9 +283,9 @@ grad_norm_kernel(const __grid_constant__ NormArgs a) {
       const int first = c == a.chunk_start[ti] ? a.shift[ti] : 0;
       // a chunk is 64 bytes to a thread, whatever the type
       const char* const g = static_cast<const char*>(a.g[ti]) + (c - a.chunk_start[ti]) * (kThreads * kNormPieces * 16);
-      const float sum = type == kF32 ? chunk_squares<kF32>(g, first, len)
+      const double sum = type == kF32 ? chunk_squares<kF32>(g, first, len)
                         : type == kBF16 ? chunk_squares<kBF16>(g, first, len) : chunk_squares<kF16>(g, first, len);
-      part += static_cast<double>(sum);
+      part += sum;
     }
   }
   const double mine = block_sum(part, s_red);

@@ -318,8 +318,10 @@ int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
  *     norm = sqrt(sum (g / loss_scale)^2),
  *     factor = min(1, max_norm / (norm + 1e-6)) / loss_scale,
  * NaN where the norm is not finite, so that a step that reads it as its
- * grad_scale writes nothing.  Sums are fp32 within a thread and binary64
- * across threads, in a fixed order: results are deterministic.
+ * grad_scale writes nothing.  Sums are fp32 within 64 bytes of a thread, or
+ * binary64 where those squares leave fp32's range, and binary64 above, in a
+ * fixed order: results are deterministic, and elements of any finite
+ * magnitude count.
  *   g_dtype : HOST array, the bwd_dtype of each tensor.
  *   factor, norm : device float[1] each, written.
  *   work : device, 16-byte aligned, bwd_grad_norm_work_bytes(num_tensors)
