@@ -28,6 +28,7 @@ import torch
 
 from . import _abi
 from . import _GDT, _launch, _need
+from ._once import first_order
 
 __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
 
@@ -330,6 +331,7 @@ class _Fp8LinearFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_order("Fp8Linear")
     def backward(ctx, dy):
         dx, dw, db = backward(dy, ctx.xq, ctx.wq, *ctx.needs_input_grad[:3])
         return dx, dw, db, None
@@ -339,7 +341,8 @@ class Fp8Linear(torch.nn.Module):
     """Linear layer whose three products take 8-bit operands.  ``weight``
     (outputs x inputs, Xavier-uniform) and ``bias`` (zeros) are ordinary
     parameters of ``dtype`` for any optimizer; each call quantizes the weight
-    as it is then.  :func:`linear` takes a weight quantized once."""
+    as it is then.  It has first derivatives only: differentiating through
+    gradients made with ``create_graph`` raises.  :func:`linear` takes a weight quantized once."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None, dtype=torch.bfloat16):
         super().__init__()
