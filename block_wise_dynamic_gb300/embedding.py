@@ -22,6 +22,7 @@ import torch
 
 from . import _abi
 from . import _lib, _need, _stream_handle
+from ._once import first_order
 
 EPS = 1e-5
 
@@ -119,6 +120,7 @@ class _StableEmbeddingFn(torch.autograd.Function):
         return y
 
     @staticmethod
+    @first_order("StableEmbedding")
     def backward(ctx, dy):
         ids, weight, gamma, mean, rstd = ctx.saved_tensors
         dweight = torch.zeros_like(weight)
@@ -132,7 +134,8 @@ class StableEmbedding(torch.nn.Module):
     """Embedding lookup followed by LayerNorm, Xavier-uniform initialised
     (fp32 weight, CUDA only).  ``weight`` is (num_embeddings, dim); the
     normalisation's scale and shift are ``norm_weight`` (ones) and
-    ``norm_bias`` (zeros)."""
+    ``norm_bias`` (zeros).  It has first derivatives only: differentiating
+    through gradients made with ``create_graph`` raises."""
 
     def __init__(self, num_embeddings: int, dim: int, eps: float = EPS, device=None, generator=None):
         super().__init__()
