@@ -50,13 +50,28 @@ class Fp8Matrix:
 
     def __init__(self, rows: int, cols: int, blocks: str, dtype, device, room: int = 0):
         """``room``: bytes that the buffer has beyond the matrix, from a multiple of 256 on."""
-        self.shape, self.blocks, self.dtype, self.device = (rows, cols), blocks, dtype, device
-        rc, rs, cc, cs, end = self._places = _layout(rows, cols, _BLOCKS[blocks])
-        self.buffer = torch.empty(_round256(end) + room if room else end, dtype=torch.uint8, device=device)
+        end = _layout(rows, cols, _BLOCKS[blocks])[4]
+        self._place(rows, cols, blocks, dtype, _bytes(_round256(end) + room if room else end, device))
+
+    def _place(self, rows, cols, blocks, dtype, buffer):
+        self.shape, self.blocks, self.dtype, self.device, self.buffer = (rows, cols), blocks, dtype, buffer.device, buffer
+        rc, rs, cc, cs, _ = self._places = _layout(rows, cols, _BLOCKS[blocks])
         # addresses of row codes, row scales, column codes, column scales
         base = self.buffer.data_ptr()
         self._pointers = (None if rc is None else base + rc, None if rs is None else base + rs,
                           None if cc is None else base + cc, None if cs is None else base + cs)
+
+    @classmethod
+    def _over(cls, like, buffer: torch.Tensor):
+        """The matrix whose ``_like()`` that was, in a buffer with the same bytes."""
+        if not buffer.is_contiguous() or buffer.data_ptr() % 16:
+            buffer = buffer.clone(memory_format=torch.contiguous_format)
+        q = cls.__new__(cls)
+        q._place(*like, buffer)
+        return q
+
+    def _like(self):
+        return (*self.shape, self.blocks, self.dtype)
 
     def _view(self, which, size):
         at = self._places[which]
@@ -327,13 +342,15 @@ class _Fp8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, wq):
         y, xq = forward(x, wq, bias)
-        ctx.xq, ctx.wq = xq, wq
+        ctx.save_for_backward(xq.buffer, wq.buffer)
+        ctx.like = xq._like(), wq._like()
         return y
 
     @staticmethod
     @first_order("Fp8Linear")
     def backward(ctx, dy):
-        dx, dw, db = backward(dy, ctx.xq, ctx.wq, *ctx.needs_input_grad[:3])
+        xq, wq = map(Fp8Matrix._over, ctx.like, ctx.saved_tensors)
+        dx, dw, db = backward(dy, xq, wq, *ctx.needs_input_grad[:3])
         return dx, dw, db, None
 
 

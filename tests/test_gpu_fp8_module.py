@@ -59,3 +59,60 @@ def test_the_mark_of_gradients_names_the_layer(fp8):
     loss.backward(create_graph=True)  # some optimizers ask for it and use first derivatives only
     with pytest.raises(RuntimeError, match="Fp8Linear has no second derivatives"):
         x.grad.float().sum().backward()
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_saved_tensor_hooks_see_the_codes(fp8, rows):
+    """What a hook gives back, at another address, is what backward reads."""
+    layer, x = make(fp8, rows)
+    dy = torch.randn(rows, 200, device=DEV, dtype=torch.bfloat16)
+    want = gradients(layer, x, dy)
+    sizes = []
+
+    def pack(t):
+        sizes.append(t.numel() * t.element_size())
+        return t.cpu()
+
+    with torch.autograd.graph.saved_tensors_hooks(pack, lambda t: t.to(DEV)):
+        got = gradients(layer, x, dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sum(sizes) >= rows * 300 + 200 * 300
+
+
+def test_checkpointing(fp8):
+    from torch.utils.checkpoint import checkpoint
+
+    layer, x = make(fp8, 700)
+    dy = torch.randn(700, 200, device=DEV, dtype=torch.bfloat16)
+    want = gradients(layer, x, dy)
+    layer.zero_grad()
+    x.grad = None
+    checkpoint(layer, x, use_reentrant=False).backward(dy)
+    assert all(torch.equal(a, b) for a, b in zip([x.grad, layer.weight.grad, layer.bias.grad], want))
+
+
+def test_backward_frees_what_forward_saved(fp8):
+    rows, n, k = 2048, 1024, 4096
+    layer, x = make(fp8, rows, n=n, k=k)
+    x.grad, layer.weight.grad, layer.bias.grad = torch.zeros_like(x), torch.zeros_like(layer.weight), torch.zeros_like(layer.bias)
+    y = layer(x)
+    held = torch.cuda.memory_allocated()
+    y.backward(torch.zeros_like(y))
+    assert held - torch.cuda.memory_allocated() >= rows * k + n * k  # y and its graph are still there
+    with pytest.raises(RuntimeError):
+        y.backward(torch.zeros_like(y))
+
+
+@pytest.mark.parametrize("rows", [5, 300])
+def test_hooks_may_give_back_any_place(fp8, rows):
+    layer, x = make(fp8, rows)
+    dy = torch.randn(rows, 200, device=DEV, dtype=torch.bfloat16)
+    want = gradients(layer, x, dy)
+
+    def unpack(t):
+        other = torch.zeros(t.numel() + 5, dtype=t.dtype, device=DEV)[5:]
+        return other.copy_(t)
+
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), unpack):
+        got = gradients(layer, x, dy)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
