@@ -341,15 +341,16 @@ def backward(dy: torch.Tensor, xq: Fp8Matrix, w: Fp8Matrix, need_input: bool = T
 class _Fp8LinearFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, wq):
-        y, xq = forward(x, wq, bias)
-        ctx.save_for_backward(xq.buffer, wq.buffer)
-        ctx.like = xq._like(), wq._like()
+        # x's column form is read for the weight's gradient alone
+        y, xq = forward(x, wq, bias) if ctx.needs_input_grad[1] else (linear(x, wq, bias), None)
+        ctx.save_for_backward(wq.buffer, None if xq is None else xq.buffer)
+        ctx.like = wq._like(), None if xq is None else xq._like()
         return y
 
     @staticmethod
     @first_order("Fp8Linear")
     def backward(ctx, dy):
-        xq, wq = map(Fp8Matrix._over, ctx.like, ctx.saved_tensors)
+        wq, xq = (None if t is None else Fp8Matrix._over(like, t) for like, t in zip(ctx.like, ctx.saved_tensors))
         dx, dw, db = backward(dy, xq, wq, *ctx.needs_input_grad[:3])
         return dx, dw, db, None
 
@@ -373,4 +374,6 @@ class Fp8Linear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         wq = quantize(self.weight.detach(), "tiles")
+        if not torch.is_grad_enabled():
+            return linear(x, wq, self.bias)
         return _Fp8LinearFn.apply(x, self.weight, self.bias, wq)

@@ -116,3 +116,44 @@ def test_hooks_may_give_back_any_place(fp8, rows):
     with torch.autograd.graph.saved_tensors_hooks(lambda t: t.clone(), unpack):
         got = gradients(layer, x, dy)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.fixture
+def calls(fp8, monkeypatch):
+    seen = []
+    launch = fp8._launch
+
+    def spy(entry, device, stream, *args):
+        seen.append((entry, args))
+        return launch(entry, device, stream, *args)
+
+    monkeypatch.setattr(fp8, "_launch", spy)
+    return seen
+
+
+def column_codes(calls):
+    """The column codes that bwd_fp8_linear was asked for, one for each call of it."""
+    return [args[11] for entry, args in calls if entry == "bwd_fp8_linear"]
+
+
+@pytest.mark.parametrize("rows", [1, 16, 300])
+def test_only_a_weight_gradient_needs_column_codes(fp8, calls, rows):
+    layer, x = make(fp8, rows)
+    want = layer(x)
+    assert column_codes(calls)[-1] is not None
+    with torch.no_grad():
+        y = layer(x)
+    assert column_codes(calls)[-1] is None and torch.equal(y, want) and not y.requires_grad
+    with torch.inference_mode():
+        assert torch.equal(layer(x), want) and column_codes(calls)[-1] is None
+    dy = torch.randn_like(want)
+    dx = gradients(layer, x, dy)[0]
+    layer.weight.requires_grad_(False)
+    layer.weight.grad = layer.bias.grad = x.grad = None
+    y = layer(x)
+    assert column_codes(calls)[-1] is None and torch.equal(y, want)
+    y.backward(dy)
+    assert torch.equal(x.grad, dx) and layer.weight.grad is None and layer.bias.grad is not None
+    layer.bias.requires_grad_(False)
+    y = layer(x.detach())
+    assert column_codes(calls)[-1] is None and torch.equal(y, want) and not y.requires_grad
