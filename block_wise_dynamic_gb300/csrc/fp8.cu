@@ -1064,6 +1064,10 @@ template <int kBN> __host__ __device__ constexpr int few_smem() {
 // that would take more of them.
 constexpr uint32_t kFewCols = kTmemCols / 2, kFewSfCol = kFewCols - 16;
 template <int kBN> __host__ __device__ constexpr int few_accs() { return static_cast<int>(kFewSfCol) / kBN; }
+constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
+// Longest line of A that the kernel quantizes for fp32 results: longer ones
+// leave the accumulators of a cluster's CTAs more than kChunk blocks each.
+constexpr int64_t kFuseCols = int64_t{kMaxSplit} * few_accs<kFuse>() * kChunk * kBK;
 
 __device__ __forceinline__ void tma_load_one(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
@@ -1461,8 +1465,6 @@ bwd_status launch_quantize(int mode, const QuantArgs& a, cudaStream_t st) {
   return a.col_sums ? launch(Both{}, std::true_type{}) : launch(Both{}, std::false_type{});
 }
 
-constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
-
 // What a launch needs to know of the device, found once for each.
 constexpr int kMaxDevices = 64;
 struct DeviceState {
@@ -1684,7 +1686,10 @@ bwd_status launch_few(const Lines& x, const Lines& w, FewArgs p, const DeviceSta
   if (!kFused && (s = code_map(&map_x, x.codes, x.lines, p.k, x.trans, kBN)) != BWD_OK) return s;
   const int64_t tiles = tiles_of(p.n) * ((p.m + kBN - 1) / kBN);
   p.tiles_n = static_cast<int>(tiles_of(p.n));
-  p.split = static_cast<int>(few_split(tiles, tiles_of(p.k), p.m, d));
+  const int64_t blocks = tiles_of(p.k), part = few_accs<kBN>() * kChunk;
+  const int64_t split = few_split(tiles, blocks, p.m, d);
+  // fp32 results: no accumulator may take more than kChunk blocks
+  p.split = static_cast<int>(kT == kF32 && split * part < blocks ? (blocks + part - 1) / part : split);
   return launch_ex(fp8_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles * p.split)),
                    kFewThreads, p.split, few_smem<kBN>(), st, "fp8_matmul_few_kernel launch", map_w, map_x, p);
 }
@@ -1905,7 +1910,7 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, int
 
 int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return -1;
-  if (rows <= kFuse) return 0;
+  if (rows <= kFuse && cols <= kFuseCols) return 0;
   Pieces w{nullptr};
   w.take(rows * bwd_fp8_pitch(cols));
   w.take(bwd_fp8_scale_bytes(rows, cols));
@@ -1921,7 +1926,7 @@ bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   if (ldy < n) return fail(BWD_ERR_INVALID_ARG, "ldy is less than n");
   if (!x_col_codes != !x_col_scales) return fail(BWD_ERR_INVALID_ARG, "column codes and scales go together");
   const int eb = dtype == BWD_F32 ? 4 : 2;
-  const bool some = rows > 0 && cols > 0, fused = rows <= kFuse;
+  const bool some = rows > 0 && cols > 0, fused = rows <= kFuse && (dtype != BWD_F32 || cols <= kFuseCols);
   if ((rows > 0 && n > 0 && !y) || (some && !fused && !work) || (some && n > 0 && (!w || !w_scales))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned_to(y, eb) || !aligned_to(bias, eb)) return fail(BWD_ERR_INVALID_ARG, "y and bias must be aligned to their element size");
   if (!aligned16(w) || !aligned16(w_scales) || !aligned16(x_col_codes) || !aligned16(work))

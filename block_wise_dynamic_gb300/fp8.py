@@ -33,7 +33,7 @@ from ._once import first_order
 __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
 
 _BLOCKS = {"rows": _abi.FP8_ROWS, "cols": _abi.FP8_COLS, "both": _abi.FP8_ROWS | _abi.FP8_COLS, "tiles": _abi.FP8_TILES}
-_FUSED_ROWS = 16  # rows that the library's product quantizes itself, without a workspace
+_FUSED_ROWS, _FUSED_COLS = 16, 245_760  # what the library's product quantizes itself, without a workspace
 # Up to this many bytes of workspace lie behind the matrix that forward() returns
 # and live as long: such calls take less time than an allocation costs (2.5 of
 # some 58 us for a training pass of 300 x 704 x 304).
@@ -124,7 +124,9 @@ def _layout(rows: int, cols: int, kind: int):
 @lru_cache(maxsize=1024)
 def _forward_work(rows: int, cols: int) -> int:
     """bwd_fp8_linear_work_bytes."""
-    return 0 if rows <= _FUSED_ROWS else _round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols))
+    if rows <= _FUSED_ROWS and cols <= _FUSED_COLS:
+        return 0
+    return _round256(rows * _pitch(cols)) + _round256(_scale_bytes(rows, cols))
 
 
 @lru_cache(maxsize=1024)

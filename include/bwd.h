@@ -412,8 +412,8 @@ bwd_status bwd_fp8_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
  *   x_col_codes, x_col_scales : both NULL, or written as for BWD_FP8_COLS
  *            (the backward pass reads them).
  *   work : device, 16-byte aligned, bwd_fp8_linear_work_bytes(rows, cols)
- *            bytes; none, and NULL will do, for up to 16 rows, which the
- *            product's kernel quantizes itself. */
+ *            bytes; none, and NULL will do, for up to 16 rows of up to
+ *            245,760 elements, which the product's kernel quantizes itself. */
 int64_t bwd_fp8_linear_work_bytes(int64_t rows, int64_t cols);
 bwd_status bwd_fp8_linear(const void* x, bwd_dtype dtype, int64_t rows,
                           int64_t cols, int64_t ld, const uint8_t* w,
