@@ -54,10 +54,13 @@ class Adam8bit(torch.optim.Optimizer):
         if weight_decay < 0.0 or (weight_decay != 0.0 and not self._decoupled):
             raise ValueError("Adam8bit takes no weight decay; AdamW8bit applies it decoupled")
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits))
-        if any(g["state_bits"] not in (8, 32) for g in self.param_groups):
-            raise ValueError("state_bits must be 8 or 32")
         self._args_cache = {}
         self._norm = None
+
+    def add_param_group(self, param_group):
+        if isinstance(param_group, dict) and param_group.get("state_bits", self.defaults["state_bits"]) not in (8, 32):
+            raise ValueError("state_bits must be 8 or 32")
+        super().add_param_group(param_group)
 
     def _state_for(self, p: torch.Tensor, bits: int):
         st = self.state[p]
