@@ -107,7 +107,7 @@ class Adam8bit(torch.optim.Optimizer):
 
     @torch.no_grad()
     def clip_scale(self, max_norm: float, loss_scale: float = 1.0):
-        """(factor, norm) of all gradients as one-element CUDA tensors (see
+        """(factor, norm) of all gradients as new one-element CUDA tensors (see
         :meth:`GradNorm.clip_scale`); pass the factor to :meth:`step`.  Where
         the norm is not finite the factor is NaN and that step writes no
         parameter and no moment (its step counts still advance)."""
@@ -123,6 +123,8 @@ class Adam8bit(torch.optim.Optimizer):
             self._norm.set_grads(grads)
         except (TypeError, ValueError):  # the first call, or other gradients than before
             self._norm = GradNorm(grads)
+        # results of this call's own: the object would write an earlier call's again
+        self._norm.factor, self._norm.norm = torch.empty((2, 1), dtype=torch.float32, device=self._norm.device).unbind()
         return self._norm.clip_scale(max_norm, loss_scale)
 
     @torch.no_grad()
