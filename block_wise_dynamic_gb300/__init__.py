@@ -35,6 +35,7 @@ __all__ = [
     "MultiTensorArgs",
     "MultiTensorArgs32",
     "adam32_step_multi",
+    "StepCount",
     "GradNorm",
     "clip_scale",
     "Adam8bit",
@@ -275,9 +276,15 @@ class MultiTensorArgs:
              stream=None, grad_scale=None) -> None:
         """One step in place.  ``grad_scale``: a float32 CUDA tensor of one
         element that multiplies every gradient, or None for 1; where it is not
-        finite the step writes nothing."""
+        finite the step writes nothing.  ``step``: which one it is, from 1 on,
+        or a :class:`StepCount`, which the call advances if it writes."""
         if self.T == 0:
             return
+        if isinstance(step, StepCount):
+            scale, count = _check_scale(grad_scale, self.device), _count_on(step, self.device)
+            hp = _hparams(lr, beta1, beta2, eps, 1, weight_decay)
+            return _launch("bwd_adam8bit_step_multi_counted", self.device, stream, self.T, self.p, self.p_dtype, self.g,
+                           self.g_dtype, self.mc, self.ma, self.vc, self.va, self.n, scale, count, ctypes.byref(hp))
         hp = _hparams(lr, beta1, beta2, eps, step, weight_decay)
         if grad_scale is not None:
             _need(grad_scale, "grad_scale", torch.float32, 1, self.device)
@@ -301,5 +308,6 @@ def adam8bit_step_multi(params, grads, m_codes, m_absmax, v_codes, v_absmax, *, 
     )
 
 
-from .adam32 import GradNorm, MultiTensorArgs32, adam32_step_multi, clip_scale  # noqa: E402
+from .adam32 import GradNorm, MultiTensorArgs32, StepCount, adam32_step_multi, clip_scale  # noqa: E402
+from .adam32 import _check_scale, _count_on  # noqa: E402
 from .optim import Adam8bit, AdamW8bit  # noqa: E402

@@ -85,6 +85,10 @@ _SIGNATURES = {
         _int,
         [_i32, _pp, _int, _pp, _int, _pp, _pp, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamHParams), _vp],
     ),
+    "bwd_adam8bit_step_multi_counted": (
+        _int,
+        [_i32, _pp, _int, _pp, _int, _pp, _pp, _pp, _pp, ctypes.POINTER(_i64), _vp, _vp, ctypes.POINTER(AdamHParams), _vp],
+    ),
     "bwd_zero_shard": (_int, [_i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _vp]),
     "bwd_embedding_init": (_int, [_vp, _i64, _i64, _vp, _vp]),
     "bwd_embedding_xavier_bound": (ctypes.c_float, [_i64, _i64]),
@@ -94,6 +98,8 @@ _SIGNATURES = {
         _int, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "bwd_adam32_step_multi": (
         _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(AdamWHParams), _vp]),
+    "bwd_adam32_step_multi_counted": (
+        _int, [_i32, _pp, _int, _pp, _int, _pp, _pp, ctypes.POINTER(_i64), _vp, _vp, ctypes.POINTER(AdamWHParams), _vp]),
     "bwd_grad_norm_work_bytes": (_i64, [_i32]),
     "bwd_grad_norm": (
         _int, [_i32, _pp, ctypes.POINTER(_i32), ctypes.POINTER(_i64), ctypes.c_float, ctypes.c_float, _vp, _vp, _vp, _vp]),

@@ -21,7 +21,7 @@ import torch
 from . import _abi
 from . import _GDT, _launch, _lib, _need
 
-__all__ = ["MultiTensorArgs32", "adam32_step_multi", "GradNorm", "clip_scale"]
+__all__ = ["StepCount", "MultiTensorArgs32", "adam32_step_multi", "GradNorm", "clip_scale"]
 
 
 def _one_dtype(tensors, what):
@@ -43,6 +43,22 @@ def _check_scale(grad_scale, device):
         return None
     _need(grad_scale, "grad_scale", torch.float32, 1, device)
     return grad_scale.data_ptr()
+
+
+class StepCount:
+    """A number of steps taken, held on the device: steps whose factor is not
+    finite write nothing and are not counted, which the host does not know.
+    ``taken`` is an int64 CUDA tensor of no dimension, the number itself."""
+
+    def __init__(self, device, taken: int = 0):
+        self.buffer = torch.full((2,), int(taken), dtype=torch.int64, device=device)
+        self.taken = self.buffer[0]
+
+
+def _count_on(count: StepCount, device) -> int:
+    if count.buffer.device != device:
+        raise ValueError(f"the step count is on {count.buffer.device}, the call runs on {device}")
+    return count.buffer.data_ptr()
 
 
 class _GradList:
@@ -100,10 +116,16 @@ class MultiTensorArgs32(_GradList):
              stream=None) -> None:
         """One AdamW step in place.  ``grad_scale``: a float32 CUDA tensor of
         one element that multiplies every gradient, or None for 1; where it is
-        not finite the step writes nothing."""
+        not finite the step writes nothing.  ``step``: which one it is, from 1
+        on, or a :class:`StepCount`, which the call advances if it writes."""
         if self.T == 0:
             return
         scale = _check_scale(grad_scale, self.device)
+        if isinstance(step, StepCount):
+            count = _count_on(step, self.device)
+            hp = _abi.AdamWHParams(lr, beta1, beta2, eps, weight_decay, 1)
+            return _launch("bwd_adam32_step_multi_counted", self.device, stream, self.T, self.p, self.p_dtype, self.g, self.g_dtype,
+                           self.m, self.v, self.n, scale, count, ctypes.byref(hp))
         hp = _abi.AdamWHParams(lr, beta1, beta2, eps, weight_decay, int(step))
         _launch("bwd_adam32_step_multi", self.device, stream, self.T, self.p, self.p_dtype, self.g, self.g_dtype, self.m, self.v, self.n,
                 scale, ctypes.byref(hp))

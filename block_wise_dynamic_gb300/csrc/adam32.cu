@@ -8,7 +8,9 @@
 //   p = p d - step m / (sqrt(v) / c + eps).
 // s is read from device memory, so a clipping factor computed on the device
 // needs no round trip through the host; where s is not finite nothing is
-// written (an overflowed gradient leaves the state as it was).
+// written (an overflowed gradient leaves the state as it was).  Whether it is
+// the host does not know, so the count of steps, which the bias corrections
+// step and c come from, may be held on the device too.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,6 +28,7 @@ using bwd::host::aligned_to;
 using bwd::host::check_launch;
 using bwd::host::cuda_fail;
 using bwd::host::fail;
+using bwd::host::StepCount;
 
 constexpr int kF32 = BWD_F32, kBF16 = BWD_BF16, kF16 = BWD_F16;
 constexpr int kThreads = 256;
@@ -45,6 +48,7 @@ struct Adam32Args {
   int64_t chunk_start[kMaxTensors + 1];  // prefix sums of per-tensor chunk counts
   Tensor32 t[kMaxTensors];
   const float* grad_scale;  // or null: 1
+  const StepCount* count;   // where step_size and inv_bc2s are, or null: here
   int32_t num_tensors;
   float b1, omb1, b2, omb2, eps, step_size, inv_bc2s, decay;
 };
@@ -148,13 +152,15 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
   }
   const float s = a.grad_scale ? *a.grad_scale : 1.0f;
   if (!(fabsf(s) <= 3.402823466e38f)) return;
+  const float step_size = a.count ? a.count->step_size : a.step_size;
+  const float inv_bc2s = a.count ? a.count->inv_bc2s : a.inv_bc2s;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float gs = __fmul_rn(s, g[j]);
     m[j] = __fadd_rn(__fmul_rn(a.b1, m[j]), __fmul_rn(a.omb1, gs));
     v[j] = __fadd_rn(__fmul_rn(a.b2, v[j]), __fmul_rn(__fmul_rn(a.omb2, gs), gs));
-    const float den = __fmaf_rn(__fsqrt_rn(v[j]), a.inv_bc2s, a.eps);
-    p[j] = __fmaf_rn(-a.step_size, __fdiv_rn(m[j], den), __fmul_rn(p[j], a.decay));
+    const float den = __fmaf_rn(__fsqrt_rn(v[j]), inv_bc2s, a.eps);
+    p[j] = __fmaf_rn(-step_size, __fdiv_rn(m[j], den), __fmul_rn(p[j], a.decay));
   }
   if (vec) {
     store4<kP>(T.p, i, p); store4<kF32>(T.m, i, m); store4<kF32>(T.v, i, v);
@@ -165,6 +171,23 @@ adam32_kernel(const __grid_constant__ Adam32Args a) {
       if (e >= 0 && e < T.n) { store1<kP>(T.p, e, p[j]); T.m[e] = m[j]; T.v[e] = v[j]; }
     }
   }
+}
+
+// Two threads, ahead of the step that they count: a bias correction each, in
+// binary64 and rounded once, as the host forms them.
+__global__ void advance_kernel(StepCount* count, const float* grad_scale, double lr, double b1, double b2) {
+  const int64_t taken = count->taken + 1;
+  const float s = grad_scale ? *grad_scale : 1.0f;
+  if (!(fabsf(s) <= 3.402823466e38f)) return;
+  const bool first = threadIdx.x == 0;
+  const double bc = 1.0 - pow(first ? b1 : b2, static_cast<double>(taken));
+  if (first) {
+    count->step_size = static_cast<float>(lr / bc);
+  } else {
+    count->inv_bc2s = static_cast<float>(1.0 / sqrt(bc));
+  }
+  __syncwarp(3u);
+  if (first) count->taken = taken;
 }
 
 // --------------------------------------------------------------------------
@@ -343,13 +366,10 @@ bwd_status launch_adam32(const Adam32Args& a, int g_type, int p_type, cudaStream
   return check_launch("adam32_kernel launch");
 }
 
-}  // namespace
-
-extern "C" {
-
-bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g,
-                                 bwd_dtype g_dtype, float* const* m, float* const* v, const int64_t* n,
-                                 const float* grad_scale, const bwd_adamw_hparams* hp, void* stream) {
+// The step of either entry point; with `count`, hp's step is not read.
+bwd_status adam32_step(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g, bwd_dtype g_dtype,
+                       float* const* m, float* const* v, const int64_t* n, const float* grad_scale, StepCount* count,
+                       const bwd_adamw_hparams* hp, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
   if (!valid_type(g_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
   if (!valid_type(p_dtype)) return fail(BWD_ERR_UNSUPPORTED_DTYPE, "parameter dtype %d", (int)p_dtype);
@@ -365,11 +385,13 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
                      !aligned_to(m[i], 4) || !aligned_to(v[i], 4)))
       return fail(BWD_ERR_INVALID_ARG, "tensor %d: pointer not aligned to its element size", i);
   }
+  if (count && (s = bwd::host::advance(count, grad_scale, *hp, stream)) != BWD_OK) return s;
   static thread_local Adam32Args a;  // ~27 KB: kept off the stack
   const bwd::host::AdamScalars k = bwd::host::adam_scalars(*hp);
   a.b1 = k.b1; a.omb1 = k.omb1; a.b2 = k.b2; a.omb2 = k.omb2;
   a.eps = k.eps; a.step_size = k.step_size; a.inv_bc2s = k.inv_bc2s; a.decay = k.decay;
   a.grad_scale = grad_scale;
+  a.count = count;
   a.chunk_start[0] = 0;
   int t = 0;
   const auto flush = [&] {
@@ -390,6 +412,37 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype 
     ++t;
   }
   return flush();
+}
+
+}  // namespace
+
+namespace bwd {
+namespace host {
+
+bwd_status advance(StepCount* count, const float* grad_scale, const bwd_adamw_hparams& hp, void* stream) {
+  advance_kernel<<<1, 2, 0, static_cast<cudaStream_t>(stream)>>>(count, grad_scale, hp.lr, hp.beta1, hp.beta2);
+  return check_launch("advance_kernel launch");
+}
+
+}  // namespace host
+}  // namespace bwd
+
+extern "C" {
+
+bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g,
+                                 bwd_dtype g_dtype, float* const* m, float* const* v, const int64_t* n,
+                                 const float* grad_scale, const bwd_adamw_hparams* hp, void* stream) {
+  return adam32_step(num_tensors, p, p_dtype, g, g_dtype, m, v, n, grad_scale, nullptr, hp, stream);
+}
+
+bwd_status bwd_adam32_step_multi_counted(int32_t num_tensors, void* const* p, bwd_dtype p_dtype, const void* const* g,
+                                         bwd_dtype g_dtype, float* const* m, float* const* v, const int64_t* n,
+                                         const float* grad_scale, void* count, const bwd_adamw_hparams* hp, void* stream) {
+  if (!count || !aligned_to(count, 8)) return fail(BWD_ERR_INVALID_ARG, "count is NULL or not 8-byte aligned");
+  if (!hp) return fail(BWD_ERR_INVALID_ARG, "hparams is NULL");
+  bwd_adamw_hparams h = *hp;
+  h.step = 1;
+  return adam32_step(num_tensors, p, p_dtype, g, g_dtype, m, v, n, grad_scale, static_cast<StepCount*>(count), &h, stream);
 }
 
 int64_t bwd_grad_norm_work_bytes(int32_t num_tensors) {

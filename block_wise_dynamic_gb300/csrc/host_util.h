@@ -30,6 +30,15 @@ struct AdamScalars {
 };
 AdamScalars adam_scalars(const bwd_adamw_hparams& hp);
 
+// A count of steps in device memory, and the scalars of the step that it last
+// counted.
+struct StepCount {
+  int64_t taken;
+  float step_size, inv_bc2s;
+};
+// Counts a step, unless *grad_scale is not finite, and forms its scalars.
+bwd_status advance(StepCount* count, const float* grad_scale, const bwd_adamw_hparams& hp, void* stream);
+
 // BWD_OK, or BWD_ERR_INVALID_ARG where a hyper-parameter is outside its range.
 bwd_status check_hparams(const bwd_adam_hparams* hp);
 bwd_status check_hparams(const bwd_adamw_hparams* hp);

@@ -543,7 +543,8 @@ struct AdamArgs {
   int32_t num_tensors;
   float b1, omb1, b2, omb2, eps, step_size, inv_bc2s;
   float decay;  // 1 - lr * weight_decay (decoupled weight decay), 1 for Adam
-  const float* grad_scale;  // device factor of every gradient (kScale)
+  const float* grad_scale;  // device factor of every gradient (kScale), or null: 1
+  const bwd::host::StepCount* count;  // where step_size and inv_bc2s are (kScale), or null: here
 };
 
 static_assert(sizeof(AdamArgs) <= 32764, "kernel parameter space");
@@ -693,9 +694,11 @@ adam8bit_kernel(const __grid_constant__ AdamArgs args) {
   int tn = lo;  // tensor of the block prefetched one iteration ahead (the prefetching threads)
 
   const float b1 = args.b1, omb1 = args.omb1, b2 = args.b2, omb2 = args.omb2;
-  const float eps = args.eps, step_size = args.step_size, inv_bc2s = args.inv_bc2s, decay = args.decay;
-  const float scale = kScale ? *args.grad_scale : 1.0f;
+  const float eps = args.eps, decay = args.decay;
+  const float scale = kScale && args.grad_scale ? *args.grad_scale : 1.0f;
   if (kScale && !(fabsf(scale) <= 3.402823466e38f)) return;
+  const float step_size = kScale && args.count ? args.count->step_size : args.step_size;
+  const float inv_bc2s = kScale && args.count ? args.count->inv_bc2s : args.inv_bc2s;
   const float* map_s = tab.map[0];
   const float* map_u = tab.map[1];
   const unsigned char* const rep_b = reinterpret_cast<const unsigned char*>(rep4);
@@ -1081,9 +1084,12 @@ int grid_for(int64_t blocks, int per_cta, const DeviceState& d, int occ) {
 
 bool valid_kind(bwd_map_kind k) { return k == BWD_MAP_SIGNED || k == BWD_MAP_UNSIGNED; }
 
+bwd_adamw_hparams widen(const bwd_adam_hparams& hp) {
+  return bwd_adamw_hparams{hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, hp.step};
+}
+
 void fill_scalars(const bwd_adam_hparams* hp, AdamArgs* a) {
-  const bwd::host::AdamScalars k = bwd::host::adam_scalars(
-      bwd_adamw_hparams{hp->lr, hp->beta1, hp->beta2, hp->eps, hp->weight_decay, hp->step});
+  const bwd::host::AdamScalars k = bwd::host::adam_scalars(widen(*hp));
   a->b1 = k.b1;
   a->b2 = k.b2;
   a->omb1 = k.omb1;
@@ -1096,14 +1102,14 @@ void fill_scalars(const bwd_adam_hparams* hp, AdamArgs* a) {
 
 template <int kG, int kP>
 void launch_typed(const AdamArgs& a, int grid, cudaStream_t st) {
-  if (a.grad_scale) adam8bit_kernel<kG, kP, true><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
+  if (a.grad_scale || a.count) adam8bit_kernel<kG, kP, true><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
   else adam8bit_kernel<kG, kP><<<grid, kGroup * adam_groups<kG, kP>(), adam_smem<kP>(), st>>>(a);
 }
 
 bwd_status launch_adam_chunk(const AdamArgs& a, int g_type, int p_type, const DeviceState& d, cudaStream_t st) {
   const int64_t total = a.block_start[a.num_tensors];
   if (total == 0) return BWD_OK;
-  const int grid = grid_for(total, adam_groups_of(p_type, g_type), d, d.occ_adam[(a.grad_scale ? 9 : 0) + 3 * p_type + g_type]);
+  const int grid = grid_for(total, adam_groups_of(p_type, g_type), d, d.occ_adam[(a.grad_scale || a.count ? 9 : 0) + 3 * p_type + g_type]);
   switch (3 * p_type + g_type) {
     case 0: launch_typed<kF32, kF32>(a, grid, st); break;
     case 1: launch_typed<kBF16, kF32>(a, grid, st); break;
@@ -1212,7 +1218,8 @@ namespace {
 template <typename PP>
 bwd_status step_multi(int32_t num_tensors, PP p, bwd_dtype p_dtype, const void* const* g, bwd_dtype g_dtype,
                       uint8_t* const* m_codes, float* const* m_absmax, uint8_t* const* v_codes,
-                      float* const* v_absmax, const int64_t* n, const float* grad_scale, const bwd_adam_hparams* hp, void* stream) {
+                      float* const* v_absmax, const int64_t* n, const float* grad_scale, bwd::host::StepCount* count,
+                      const bwd_adam_hparams* hp, void* stream) {
   if (num_tensors < 0) return fail(BWD_ERR_INVALID_ARG, "num_tensors < 0");
   if (g_dtype != BWD_F32 && g_dtype != BWD_BF16 && g_dtype != BWD_F16)
     return fail(BWD_ERR_UNSUPPORTED_DTYPE, "gradient dtype %d", (int)g_dtype);
@@ -1234,13 +1241,15 @@ bwd_status step_multi(int32_t num_tensors, PP p, bwd_dtype p_dtype, const void* 
       return fail(BWD_ERR_INVALID_ARG, "tensor %d: pointer not aligned to its element size", i);
     any_work = any_work || n[i] > 0;
   }
-  if (!any_work) return BWD_OK;
+  if (!any_work && !count) return BWD_OK;
   DeviceState* d = nullptr;
   if ((s = ensure_device(&d)) != BWD_OK) return s;
+  if (count && (s = bwd::host::advance(count, grad_scale, widen(*hp), stream)) != BWD_OK) return s;
 
   static thread_local AdamArgs a;  // ~32 KB: kept off the stack
   fill_scalars(hp, &a);
   a.grad_scale = grad_scale;
+  a.count = count;
   const int g_type = static_cast<int>(g_dtype), p_type = static_cast<int>(p_dtype);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int k = 0;
@@ -1280,7 +1289,7 @@ bwd_status bwd_adam8bit_step_multi(int32_t num_tensors, float* const* p, const v
                                    bwd_dtype g_dtype, uint8_t* const* m_codes, float* const* m_absmax,
                                    uint8_t* const* v_codes, float* const* v_absmax, const int64_t* n,
                                    const bwd_adam_hparams* hp, void* stream) {
-  return step_multi(num_tensors, p, BWD_F32, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, hp, stream);
+  return step_multi(num_tensors, p, BWD_F32, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, nullptr, hp, stream);
 }
 
 bwd_status bwd_adam8bit_step_multi_ex(int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
@@ -1288,7 +1297,7 @@ bwd_status bwd_adam8bit_step_multi_ex(int32_t num_tensors, void* const* p, bwd_d
                                       float* const* m_absmax, uint8_t* const* v_codes,
                                       float* const* v_absmax, const int64_t* n,
                                       const bwd_adam_hparams* hp, void* stream) {
-  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, hp, stream);
+  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, nullptr, nullptr, hp, stream);
 }
 
 bwd_status bwd_adam8bit_step_multi_scaled(int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
@@ -1296,7 +1305,20 @@ bwd_status bwd_adam8bit_step_multi_scaled(int32_t num_tensors, void* const* p, b
                                           float* const* m_absmax, uint8_t* const* v_codes,
                                           float* const* v_absmax, const int64_t* n, const float* grad_scale,
                                           const bwd_adam_hparams* hp, void* stream) {
-  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, grad_scale, hp, stream);
+  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, grad_scale, nullptr, hp, stream);
+}
+
+bwd_status bwd_adam8bit_step_multi_counted(int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
+                                           const void* const* g, bwd_dtype g_dtype, uint8_t* const* m_codes,
+                                           float* const* m_absmax, uint8_t* const* v_codes,
+                                           float* const* v_absmax, const int64_t* n, const float* grad_scale,
+                                           void* count, const bwd_adam_hparams* hp, void* stream) {
+  if (!count || !aligned_to(count, 8)) return fail(BWD_ERR_INVALID_ARG, "count is NULL or not 8-byte aligned");
+  if (!hp) return fail(BWD_ERR_INVALID_ARG, "hparams is NULL");
+  bwd_adam_hparams h = *hp;
+  h.step = 1;
+  return step_multi(num_tensors, p, p_dtype, g, g_dtype, m_codes, m_absmax, v_codes, v_absmax, n, grad_scale,
+                    static_cast<bwd::host::StepCount*>(count), &h, stream);
 }
 
 bwd_status bwd_adam8bit_step(float* p, const void* g, bwd_dtype g_dtype, uint8_t* m_codes,

@@ -35,7 +35,23 @@ from collections import defaultdict
 
 import torch
 
-from . import GradNorm, MultiTensorArgs, MultiTensorArgs32, num_blocks, state_init
+from . import GradNorm, MultiTensorArgs, MultiTensorArgs32, StepCount, num_blocks, state_init
+
+
+class _Counts:
+    """Step counts of states as numbers; one that lies on the device, which
+    many states share, is read once."""
+
+    def __init__(self):
+        self._read = {}
+
+    def __call__(self, state) -> int:
+        step = state["step"]
+        if not torch.is_tensor(step):
+            return step
+        if id(step) not in self._read:
+            self._read[id(step)] = step, int(step)
+        return self._read[id(step)][1]
 
 
 class Adam8bit(torch.optim.Optimizer):
@@ -79,6 +95,7 @@ class Adam8bit(torch.optim.Optimizer):
         bucketed by (device, parameter dtype, gradient dtype, step count), each
         bucket with its argument table (parameter and state pointers fixed)."""
         buckets = defaultdict(list)
+        count = _Counts()
         for i, (p, g) in enumerate(zip(params, grads)):
             if g is None:
                 continue
@@ -91,7 +108,7 @@ class Adam8bit(torch.optim.Optimizer):
                 raise ValueError(f"the state of a parameter is not the one of state_bits={bits}")
             if bits == 8 and st["m_absmax"].numel() != num_blocks(p.numel()):
                 raise ValueError("state does not match the parameter size")
-            buckets[(p.device, p.dtype, g.dtype, st["step"])].append(i)
+            buckets[(p.device, p.dtype, g.dtype, count(st))].append(i)
         plan = []
         for (_, _, _, t), idx in buckets.items():
             sts = [self.state[params[i]] for i in idx]
@@ -103,6 +120,9 @@ class Adam8bit(torch.optim.Optimizer):
                 args = MultiTensorArgs(*lists, [s["m_codes"] for s in sts], [s["m_absmax"] for s in sts],
                                        [s["v_codes"] for s in sts], [s["v_absmax"] for s in sts])
             plan.append([idx, sts, args, t])
+        for _, sts, _, t in plan:
+            for s in sts:
+                s["step"] = t
         return {"params": list(params), "has_grad": [g is not None for g in grads], "buckets": plan}
 
     @torch.no_grad()
@@ -110,7 +130,7 @@ class Adam8bit(torch.optim.Optimizer):
         """(factor, norm) of all gradients as new one-element CUDA tensors (see
         :meth:`GradNorm.clip_scale`); pass the factor to :meth:`step`.  Where
         the norm is not finite the factor is NaN and that step writes no
-        parameter and no moment (its step counts still advance)."""
+        parameter and no moment and is not counted."""
         grads = [p.grad for group in self.param_groups for p in group["params"] if p.grad is not None]
         if not grads:
             raise ValueError("no parameter has a gradient")
@@ -130,7 +150,11 @@ class Adam8bit(torch.optim.Optimizer):
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
         """One step.  ``grad_scale``: a one-element float32 CUDA tensor that
-        multiplies every gradient, or None."""
+        multiplies every gradient, or None.  Where it is not finite the step
+        writes nothing and is not counted; from the first call with one on,
+        the states' ``step`` is therefore an int64 CUDA tensor (a number again
+        in ``state_dict()``), and a step captured in a graph after that is
+        replayed as the next one."""
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -154,17 +178,29 @@ class Adam8bit(torch.optim.Optimizer):
                         # a gradient changed dtype or shape: rebuild this group's plan next step
                         self._args_cache.pop(gi, None)
                         raise
-                args.step(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"],
-                          weight_decay=group["weight_decay"], step=t + 1, grad_scale=grad_scale)
+                counted = isinstance(t, StepCount)
+                if grad_scale is not None and not counted:
+                    t, counted = StepCount(args.device, t), True
+                args.step(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], weight_decay=group["weight_decay"],
+                          step=t if counted else t + 1, grad_scale=grad_scale)
                 # the step count advances only once its launch went through
-                bucket[3] = t + 1
-                for s in sts:
-                    s["step"] = t + 1
+                if not counted:
+                    t += 1
+                if t is not bucket[3]:
+                    bucket[3] = t
+                    for s in sts:
+                        s["step"] = t.taken if counted else t
         return loss
 
     def _reset_plans(self):
         """Forget the cached launch plans (after the state was replaced)."""
         self._args_cache = {}
+
+    def state_dict(self):
+        sd = super().state_dict()
+        count = _Counts()
+        sd["state"] = {k: {**st, "step": count(st)} if "step" in st else st for k, st in sd["state"].items()}
+        return sd
 
     def load_state_dict(self, state_dict):
         self._reset_plans()

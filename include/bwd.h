@@ -184,6 +184,22 @@ bwd_status bwd_adam8bit_step_multi_scaled(
     const int64_t* n, const float* grad_scale, const bwd_adam_hparams* hp,
     void* stream);
 
+/* The same with the number of steps taken held in device memory, because where
+ * *grad_scale is not finite nothing is written and the step is not counted,
+ * which the host does not know; and so that a captured call can be replayed
+ * as the next step.
+ *   grad_scale : as above; NULL for 1.
+ *   count      : device, 16 bytes, 8-byte aligned: an int64_t, the steps taken
+ *                so far, and eight bytes that the call writes.  The call takes
+ *                step *count + 1 and leaves *count that, or as it was.
+ *                hp->step is not read. */
+bwd_status bwd_adam8bit_step_multi_counted(
+    int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
+    const void* const* g, bwd_dtype g_dtype, uint8_t* const* m_codes,
+    float* const* m_absmax, uint8_t* const* v_codes, float* const* v_absmax,
+    const int64_t* n, const float* grad_scale, void* count,
+    const bwd_adam_hparams* hp, void* stream);
+
 /* ------------------------------------------------------------------------
  * ZeRO-style sharding of the step over P processes ("Яндекс Публикует ЯЛМ
  * 100Б", section "ZeRO" under "Случай с несколькими графическими
@@ -309,6 +325,14 @@ bwd_status bwd_adam32_step_multi(int32_t num_tensors, void* const* p,
                                  float* const* v, const int64_t* n,
                                  const float* grad_scale,
                                  const bwd_adamw_hparams* hp, void* stream);
+
+/* The same with the number of steps taken in device memory, as for
+ * bwd_adam8bit_step_multi_counted. */
+bwd_status bwd_adam32_step_multi_counted(
+    int32_t num_tensors, void* const* p, bwd_dtype p_dtype,
+    const void* const* g, bwd_dtype g_dtype, float* const* m, float* const* v,
+    const int64_t* n, const float* grad_scale, void* count,
+    const bwd_adamw_hparams* hp, void* stream);
 
 /* Bytes of the workspace of bwd_grad_norm (-1 for num_tensors < 0). */
 int64_t bwd_grad_norm_work_bytes(int32_t num_tensors);
