@@ -1041,10 +1041,13 @@ fp8_matmul_kernel(const __grid_constant__ MmCall<kTwo ? 2 : 1> c) {
 // same part of A again, so this pays for few lines only (33 x 4096 x 11008,
 // timed with a version of it for 64 lines: 19.2 us; in two kernels 11.3).
 //
-// Measured, call after call: 1 x 4096 x 4096 5.0 us (its 16.8 MB take 2.5),
-// 1 x 4096 x 11008 6.7 (6.7), 33 x 4096 x 11008 8.0 without the quantizer.
-// What it takes beyond the reading is a launch, the first copies' latency and
-// the gathering, 1 us or so each.
+// Measured, call after call in a captured graph, through weights of over 500
+// MB, so that each is read from DRAM: 1 x 4096 x 4096 6.0 us (its 16.8 MB take
+// 2.5 at the copy rate), 1 x 4096 x 11008 10.2 (6.7), 33 x 4096 x 11008 11.4
+// (6.9) without the quantizer and 14.1 with it.  With one weight again and
+// again, then in L2, 4.8, 6.8, 8.0 and 11.6; the other times here are of that
+// kind.  What it takes beyond the reading is a launch, the first copies'
+// latency and the gathering, 1 us or so each.
 
 constexpr int kFuse = 16;
 constexpr int kFewThreads = 320;  // warp 0 copies, warp 1 issues, warps 2 to 9 quantize and store
