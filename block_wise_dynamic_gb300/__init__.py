@@ -185,13 +185,16 @@ def _hparams(lr, beta1, beta2, eps, step, weight_decay=0.0) -> _abi.AdamHParams:
 
 
 def adam8bit_step(p, g, m_codes, m_absmax, v_codes, v_absmax, *, lr=1e-3, beta1=0.9, beta2=0.999,
-                  eps=1e-8, weight_decay=0.0, step, stream=None) -> None:
+                  eps=1e-8, weight_decay=0.0, step, stream=None, grad_scale=None) -> None:
     """One 8-bit Adam step on one flat tensor, in place (``bwd_adam8bit_step``);
     ``weight_decay`` > 0 makes it AdamW (decoupled).  bf16 and fp16
-    parameters go through ``bwd_adam8bit_step_multi_ex``."""
-    if isinstance(p, torch.Tensor) and p.dtype in (torch.bfloat16, torch.float16):
-        return adam8bit_step_multi([p], [g], [m_codes], [m_absmax], [v_codes], [v_absmax], lr=lr, beta1=beta1,
-                                   beta2=beta2, eps=eps, weight_decay=weight_decay, step=step, stream=stream)
+    parameters go through ``bwd_adam8bit_step_multi_ex``, and what
+    ``MultiTensorArgs.step`` takes as ``grad_scale`` and ``step`` besides
+    through its entry points."""
+    if isinstance(p, torch.Tensor) and (p.dtype in (torch.bfloat16, torch.float16) or grad_scale is not None
+                                        or isinstance(step, StepCount)):
+        return adam8bit_step_multi([p], [g], [m_codes], [m_absmax], [v_codes], [v_absmax], lr=lr, beta1=beta1, beta2=beta2,
+                                   eps=eps, weight_decay=weight_decay, step=step, stream=stream, grad_scale=grad_scale)
     n = p.numel()
     _need(p, "p", torch.float32)
     if g.dtype not in _GDT:
@@ -300,11 +303,11 @@ class MultiTensorArgs:
 
 
 def adam8bit_step_multi(params, grads, m_codes, m_absmax, v_codes, v_absmax, *, lr=1e-3, beta1=0.9,
-                        beta2=0.999, eps=1e-8, weight_decay=0.0, step, stream=None) -> None:
-    """One 8-bit Adam(W) step over a list of tensors (``bwd_adam8bit_step_multi_ex``);
-    parameters fp32 or bf16, gradients fp32 or bf16."""
+                        beta2=0.999, eps=1e-8, weight_decay=0.0, step, stream=None, grad_scale=None) -> None:
+    """One 8-bit Adam(W) step over a list of tensors, fp32, bf16 or fp16 ones
+    (``bwd_adam8bit_step_multi_ex``; see :meth:`MultiTensorArgs.step`)."""
     MultiTensorArgs(params, grads, m_codes, m_absmax, v_codes, v_absmax).step(
-        lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, step=step, stream=stream
+        lr=lr, beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, step=step, stream=stream, grad_scale=grad_scale
     )
 
 
