@@ -166,3 +166,29 @@ def test_a_captured_step_replays_as_the_next_one(bwd, dtype):
     torch.cuda.synchronize()
     same(opt, eager, ps, qs)
     assert all(int(opt.state[p]["step"]) == 4 for p in ps)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_captured_clipping_and_step(bwd, dtype):
+    ps, qs = make(dtype), make(dtype)
+    opt, eager = build(bwd, ps), build(bwd, qs)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        opt.step(grad_scale=opt.clip_scale(0.1)[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        factor, norm = opt.clip_scale(0.1)
+        opt.step(grad_scale=factor)
+    eager.step(grad_scale=eager.clip_scale(0.1)[0])
+    for t in (1, 2, 3):
+        for p, q in zip(ps, qs):
+            g = torch.randn(p.shape, generator=torch.Generator(DEV).manual_seed(t), device=DEV) * (float("nan") if t == 2 else 1e-2)
+            p.grad.copy_(g)
+            q.grad.copy_(g)
+        graph.replay()
+        eager.step(grad_scale=eager.clip_scale(0.1)[0])
+    torch.cuda.synchronize()
+    same(opt, eager, ps, qs)
+    assert all(int(opt.state[p]["step"]) == 3 for p in ps)
