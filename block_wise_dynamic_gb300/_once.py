@@ -15,7 +15,7 @@ class _NoSecondDerivative(torch.autograd.Function):
     @staticmethod
     def forward(ctx, name, anything, *gradients):
         ctx.name = name
-        return tuple(g.view_as(g) for g in gradients)
+        return tuple(g.detach() for g in gradients)  # not views, which could not be changed in place
 
     @staticmethod
     def backward(ctx, *_):

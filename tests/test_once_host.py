@@ -40,3 +40,28 @@ def test_second_derivatives_raise(cube, dy_takes_a_gradient, loss_depends_on_x_o
     loss = dx.square().sum() + (x.sum() if loss_depends_on_x_otherwise else 0.0)
     with pytest.raises(RuntimeError, match="Cube has no second derivatives"):
         loss.backward()
+
+
+def test_gradients_may_be_changed_in_place():
+    """As optimizers and clipping do with gradients made with create_graph."""
+    from block_wise_dynamic_gb300._once import first_order
+
+    class Scale(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, y):
+            return 2 * x + 3 * y
+
+        @staticmethod
+        @first_order("Scale")
+        def backward(ctx, dy):
+            return 2 * dy, 3 * dy
+
+    x, y = (torch.ones(2, requires_grad=True) for _ in range(2))
+    dx, dy = torch.autograd.grad(Scale.apply(x, y).sum(), [x, y], create_graph=True)
+    dx.mul_(2)
+    with torch.no_grad():
+        dy.add_(1)
+    assert dx.tolist() == [4.0, 4.0] and dy.tolist() == [4.0, 4.0]
+    for g in (dx, dy):
+        with pytest.raises(RuntimeError, match="Scale has no second derivatives"):
+            g.sum().backward()
