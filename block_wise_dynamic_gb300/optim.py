@@ -73,6 +73,12 @@ class Adam8bit(torch.optim.Optimizer):
         self._args_cache = {}
         self._norm = None
 
+    def __setstate__(self, state):
+        # a copied or unpickled optimizer has none of the launch tables; their addresses were the original's
+        super().__setstate__(state)
+        self._args_cache = {}
+        self._norm = None
+
     def add_param_group(self, param_group):
         if isinstance(param_group, dict) and param_group.get("state_bits", self.defaults["state_bits"]) not in (8, 32):
             raise ValueError("state_bits must be 8 or 32")
