@@ -115,6 +115,11 @@ _SIGNATURES = {
     "bwd_fp8_linear_backward_work_bytes": (_i64, [_i64, _i64]),
     "bwd_fp8_linear_backward": (
         _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "bwd_norm_forward": (
+        _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "bwd_norm_backward_work_bytes": (_i64, [_i64, _i64]),
+    "bwd_norm_backward": (
+        _int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "bwd_check_device": (_int, [_vp]),
     "bwd_selftest_bounded_wait": (_int, [_vp]),
     "bwd_status_string": (ctypes.c_char_p, [_int]),

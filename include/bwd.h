@@ -470,9 +470,41 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype,
                                    int64_t lddw, void* dbias, void* work,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * Layer normalisation over the rows of a matrix:
+ *     mean = sum x / D;  var = sum (x - mean)^2 / D;  rstd = (var + eps)^-1/2
+ *     xh = (x - mean) rstd;  y = xh gamma + beta
+ *   x    : device, rows x width values of `dtype`, `ldx` elements between
+ *          rows; width at most 16384.
+ *   gamma, beta : device, width values of `vector_dtype`, which is BWD_F32 or
+ *          x's; NULL for 1 and 0.
+ *   y    : device, rows x width values of `dtype`, written.
+ *   mean, rstd : device float[rows], written, or NULL.
+ * Statistics are held in fp32, the variance is of the centred values. */
+bwd_status bwd_norm_forward(const void* x, bwd_dtype dtype, int64_t rows,
+                            int64_t width, int64_t ldx, const void* gamma,
+                            const void* beta, bwd_dtype vector_dtype, float eps,
+                            void* y, float* mean, float* rstd, void* stream);
+
+/* Its gradients for the given statistics:
+ *     h = dy gamma
+ *     dx = rstd (h - sum h / D - xh sum(h xh) / D)   rows x width, or NULL
+ *     dgamma = sum over rows of dy xh    width values of `vector_dtype`, or NULL
+ *     dbeta = sum over rows of dy        the same
+ * all written, in a fixed order of sums.
+ *   work : device, 4-byte aligned, bwd_norm_backward_work_bytes(rows, width);
+ *          read and written where dgamma or dbeta is. */
+int64_t bwd_norm_backward_work_bytes(int64_t rows, int64_t width);
+bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype,
+                             int64_t rows, int64_t width, int64_t lddy,
+                             int64_t ldx, const void* gamma,
+                             bwd_dtype vector_dtype, const float* mean,
+                             const float* rstd, void* dx, void* dgamma,
+                             void* dbeta, void* work, void* stream);
+
 /* Waits for `stream` and reports whether a bounded wait inside one of the
  * library's kernels gave up since the last check (the staged embedding
- * backward and the 8-bit product wait for their own copies and products; each
+ * backward and the matrix products wait for their own copies and products; each
  * wait gives up after about a second, flags the device and lets the kernel
  * return).  BWD_OK, or
  * BWD_ERR_CUDA with bwd_last_error() describing it; the flag is cleared.
