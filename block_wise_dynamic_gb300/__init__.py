@@ -40,6 +40,9 @@ __all__ = [
     "clip_scale",
     "Adam8bit",
     "AdamW8bit",
+    "Muon",
+    "MuonArgs",
+    "orthogonalize",
 ]
 
 _KINDS = {"signed": _abi.BWD_MAP_SIGNED, "unsigned": _abi.BWD_MAP_UNSIGNED}
@@ -314,3 +317,4 @@ def adam8bit_step_multi(params, grads, m_codes, m_absmax, v_codes, v_absmax, *, 
 from .adam32 import GradNorm, MultiTensorArgs32, StepCount, adam32_step_multi, clip_scale  # noqa: E402
 from .adam32 import _check_scale, _count_on  # noqa: E402
 from .optim import Adam8bit, AdamW8bit  # noqa: E402
+from .muon import Muon, MuonArgs, orthogonalize  # noqa: E402

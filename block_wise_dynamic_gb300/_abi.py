@@ -59,6 +59,19 @@ class BwdError(RuntimeError):
         super().__init__(f"{where}: {detail}")
 
 
+class MuonHParams(ctypes.Structure):
+    """Mirror of ``bwd_muon_hparams``."""
+
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("momentum", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("rms", ctypes.c_double),
+        ("nesterov", ctypes.c_int32),
+        ("steps", ctypes.c_int32),
+    ]
+
+
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
@@ -120,6 +133,10 @@ _SIGNATURES = {
     "bwd_norm_backward_work_bytes": (_i64, [_i64, _i64]),
     "bwd_norm_backward": (
         _int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "bwd_orthogonalize_work_bytes": (_i64, [_i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
+    "bwd_orthogonalize": (_int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.POINTER(_i64), _i32, _pp, _vp, _vp]),
+    "bwd_muon_step": (
+        _int, [_i32, _pp, _int, _pp, _int, _pp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), _vp, ctypes.POINTER(MuonHParams), _vp, _vp]),
     "bwd_check_device": (_int, [_vp]),
     "bwd_selftest_bounded_wait": (_int, [_vp]),
     "bwd_status_string": (ctypes.c_char_p, [_int]),

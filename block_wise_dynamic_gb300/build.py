@@ -2,7 +2,8 @@
 
 The translation units (the host codebook builder, the host shard planner, the
 8-bit optimizer kernels, the stable-embedding kernels, the 8-bit
-floating point products, the 32-bit-state optimizer kernels and the layer norm) are compiled in parallel and linked with the static CUDA runtime, so the library depends only on the driver.  No
+floating point products, the 32-bit-state optimizer kernels, the layer norm and the
+orthogonalised updates) are compiled in parallel and linked with the static CUDA runtime, so the library depends only on the driver.  No
 fast-math: every code decision must be IEEE.
 """
 
@@ -31,6 +32,7 @@ SOURCES = {
     "embedding.o": os.path.join(CSRC, "embedding.cu"),
     "fp8.o": os.path.join(CSRC, "fp8.cu"),
     "norm.o": os.path.join(CSRC, "norm.cu"),
+    "muon.o": os.path.join(CSRC, "muon.cu"),
     "adam32.o": os.path.join(CSRC, "adam32.cu"),
 }
 HEADERS = [os.path.join(CSRC, h) for h in ("tables.h", "exact_div.cuh", "host_util.h", "tensor.cuh")] + [os.path.join(INCLUDE, "bwd.h")]

@@ -37,6 +37,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "bwd.h"
@@ -814,10 +815,14 @@ bwd_status bwd_check_device(void* stream) {
   unsigned int fault = 0;
   if ((e = cudaMemcpyFromSymbol(&fault, g_embed_fault, sizeof fault)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyFromSymbol(fault word)");
-  unsigned int fp8_fault = 0;
-  const bwd_status s = bwd::host::take_fp8_fault(&fp8_fault);
-  if (s != BWD_OK) return s;
-  if (fault == 0 && fp8_fault == 0) return BWD_OK;
+  unsigned int product_fault = 0;
+  for (const auto take : {bwd::host::take_fp8_fault, bwd::host::take_muon_fault}) {
+    unsigned int one = 0;
+    const bwd_status s = take(&one);
+    if (s != BWD_OK) return s;
+    product_fault |= one;
+  }
+  if (fault == 0 && product_fault == 0) return BWD_OK;
   const unsigned int zero = 0;
   if (fault != 0 && (e = cudaMemcpyToSymbol(g_embed_fault, &zero, sizeof zero)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyToSymbol(fault word)");

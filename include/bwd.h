@@ -502,6 +502,56 @@ bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype,
                              const float* rstd, void* dx, void* dgamma,
                              void* dbeta, void* work, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates.  For each matrix G (rows x cols, contiguous):
+ *     X = G / (|G| + 1e-7)   Frobenius norm; G^T where rows > cols
+ *     `steps` times:  A = X X^T;  X = a X + (b A + c A A) X
+ * with (a, b, c) = (3.4445, -4.7750, 2.0315), and the result X (or X^T).
+ * Five steps bring singular values above 1e-3 of the norm to 0.7 ... 1.2.
+ *   g, out : HOST arrays of device pointers to rows[i] x cols[i] values of
+ *            `dtype`; out[i] may be g[i].  Matrices of one shape, or of its
+ *            transpose, are worked on together, up to 64 of them.
+ *   rows, cols : HOST arrays, at most 65536 each; an empty matrix is left out.
+ *   work : device, 256-byte aligned, bwd_orthogonalize_work_bytes(...) bytes
+ *          (-1 for a bad argument); calls that share it are ordered by the
+ *          caller.
+ * Products are of pairs of fp16 values (22 bits), added in fp32 by the matrix
+ * instruction, which truncates; for bf16 results the last step takes the
+ * values' 11 leading bits.  A matrix with a NaN or an infinity comes out NaN,
+ * the others are not touched by it. */
+int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows,
+                                     const int64_t* cols);
+bwd_status bwd_orthogonalize(int32_t count, const void* const* g,
+                             bwd_dtype dtype, const int64_t* rows,
+                             const int64_t* cols, int32_t steps,
+                             void* const* out, void* work, void* stream);
+
+/* Hyper-parameters of the step below.  `rms` is the root mean square that an
+ * update of full rank is scaled to, before lr (0.2: that of AdamW's). */
+typedef struct {
+  double lr;
+  double momentum;
+  double weight_decay;
+  double rms;
+  int32_t nesterov;
+  int32_t steps;
+} bwd_muon_hparams;
+
+/* One step over a list of matrices, in place:
+ *     m = mu m + s g;   u = s g + mu m (nesterov), or m
+ *     p = p (1 - lr weight_decay) - lr rms sqrt(max(rows, cols)) O(u)
+ * with O as above, formed to the precision that p_dtype asks for.
+ *   p, g, m : HOST arrays of device pointers to rows[i] x cols[i] contiguous
+ *             values of p_dtype, g_dtype and float; p and m are updated.
+ *   grad_scale : device float[1], s, read by the kernels, or NULL for 1.
+ *             Where it is infinite or NaN the call writes nothing but work.
+ *   work : as for bwd_orthogonalize. */
+bwd_status bwd_muon_step(int32_t count, void* const* p, bwd_dtype p_dtype,
+                         const void* const* g, bwd_dtype g_dtype,
+                         float* const* m, const int64_t* rows,
+                         const int64_t* cols, const float* grad_scale,
+                         const bwd_muon_hparams* hp, void* work, void* stream);
+
 /* Waits for `stream` and reports whether a bounded wait inside one of the
  * library's kernels gave up since the last check (the staged embedding
  * backward and the matrix products wait for their own copies and products; each
