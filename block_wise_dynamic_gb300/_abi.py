@@ -128,6 +128,13 @@ _SIGNATURES = {
     "bwd_fp8_linear_backward_work_bytes": (_i64, [_i64, _i64]),
     "bwd_fp8_linear_backward": (
         _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "bwd_fp4_pitch": (_i64, [_i64]),
+    "bwd_fp4_scale_bytes": (_i64, [_i64, _i64]),
+    "bwd_fp4_quantize": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "bwd_fp4_dequantize": (_int, [_vp, _vp, _i64, _i64, _vp, _int, _vp]),
+    "bwd_fp4_matmul": (_int, [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _int, _vp]),
+    "bwd_fp4_linear_work_bytes": (_i64, [_i64, _i64]),
+    "bwd_fp4_linear": (_int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp]),
     "bwd_norm_forward": (
         _int, [_vp, _int, _i64, _i64, _i64, _vp, _vp, _int, ctypes.c_float, _vp, _vp, _vp, _vp]),
     "bwd_norm_backward_work_bytes": (_i64, [_i64, _i64]),

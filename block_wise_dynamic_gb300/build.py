@@ -1,7 +1,7 @@
 """Builds the C-ABI shared library ``libbwd.so`` in-tree for sm_103a.
 
 The translation units (the host codebook builder, the host shard planner, the
-8-bit optimizer kernels, the stable-embedding kernels, the 8-bit
+8-bit optimizer kernels, the stable-embedding kernels, the 8-bit and 4-bit
 floating point products, the 32-bit-state optimizer kernels, the layer norm and the
 orthogonalised updates) are compiled in parallel and linked with the static CUDA runtime, so the library depends only on the driver.  No
 fast-math: every code decision must be IEEE.
@@ -31,6 +31,7 @@ SOURCES = {
     "kernels.o": os.path.join(CSRC, "kernels.cu"),
     "embedding.o": os.path.join(CSRC, "embedding.cu"),
     "fp8.o": os.path.join(CSRC, "fp8.cu"),
+    "fp4.o": os.path.join(CSRC, "fp4.cu"),
     "norm.o": os.path.join(CSRC, "norm.cu"),
     "muon.o": os.path.join(CSRC, "muon.cu"),
     "adam32.o": os.path.join(CSRC, "adam32.cu"),

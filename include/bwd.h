@@ -471,6 +471,54 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype,
                                    void* stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point.  A block of 1 x 32 elements of a row has
+ * the scale 2^e, e >= -127 the smallest for which no magnitude of the block
+ * exceeds 6 * 2^e, and each element the e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6
+ * and their negatives) nearest to x 2^-e, ties to the even code.  A block with
+ * an infinity or a NaN stands for NaN throughout.
+ *   codes  : two to a byte, the earlier column in the low half; rows start
+ *            bwd_fp4_pitch(cols) bytes apart (16-byte aligned), the rest of a
+ *            row's bytes are zero.
+ *   scales : e + 127 of row r's block k (columns 32 k and on) at byte
+ *            ((r / 128) G + k / 4) 512 + (r % 32) 16 + (r / 32 % 4) 4 + k % 4,
+ *            G = 2 ceil(cols / 256); bwd_fp4_scale_bytes(rows, cols) in all.
+ *            Of existing rows, blocks past the last column have the byte 0;
+ *            the bytes of rows that do not exist are not written. */
+int64_t bwd_fp4_pitch(int64_t cols);
+int64_t bwd_fp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* x: device, rows x cols values of `dtype`, `ld` elements between rows. */
+bwd_status bwd_fp4_quantize(const void* x, bwd_dtype dtype, int64_t rows,
+                            int64_t cols, int64_t ld, uint8_t* codes,
+                            uint8_t* scales, void* stream);
+
+/* out: device, rows x cols values of `dtype`, contiguous. */
+bwd_status bwd_fp4_dequantize(const uint8_t* codes, const uint8_t* scales,
+                              int64_t rows, int64_t cols, void* out,
+                              bwd_dtype dtype, void* stream);
+
+/* out[i, j] = sum_l A(i, l) B(j, l) + bias[j], i < m, j < n, l < k, for
+ * quantized A (m x k) and B (n x k).
+ *   bias : device, n values of `dtype`, or NULL.
+ *   out  : device, m x n values of `dtype`, `ldo` elements between rows.
+ * Products are exact, sums are held in fp32 (the matrix instruction truncates
+ * its additions; fp32 results leave it every 2,048 products and are then added
+ * up to nearest), and the result is rounded once; the order is fixed. */
+bwd_status bwd_fp4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
+                          const uint8_t* a_scales, const uint8_t* b,
+                          const uint8_t* b_scales, const void* bias, void* out,
+                          int64_t ldo, bwd_dtype dtype, void* stream);
+
+/* y = Q(x) W^T + bias in one call, x (rows x cols) quantized in the workspace.
+ *   w, w_scales : of the n x cols weight.   y : rows x n of x's type.
+ *   work : device, 16-byte aligned, bwd_fp4_linear_work_bytes(rows, cols). */
+int64_t bwd_fp4_linear_work_bytes(int64_t rows, int64_t cols);
+bwd_status bwd_fp4_linear(const void* x, bwd_dtype dtype, int64_t rows,
+                          int64_t cols, int64_t ld, const uint8_t* w,
+                          const uint8_t* w_scales, int64_t n, const void* bias,
+                          void* y, int64_t ldy, void* work, void* stream);
+
+/* ------------------------------------------------------------------------
  * Layer normalisation over the rows of a matrix:
  *     mean = sum x / D;  var = sum (x - mean)^2 / D;  rstd = (var + eps)^-1/2
  *     xh = (x - mean) rstd;  y = xh gamma + beta

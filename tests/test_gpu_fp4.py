@@ -1,0 +1,249 @@
+"""Microscaled 4-bit quantization and the product of quantized matrices,
+against the 64-bit statement."""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp4 as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = {"fp32": torch.float32, "bf16": torch.bfloat16, "fp16": torch.float16}
+U = 2.0 ** -24
+ROUND = {"fp32": 2.0 ** -24, "bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+TINY = {"fp32": 2.0 ** -149, "bf16": 2.0 ** -134, "fp16": 2.0 ** -25}
+
+
+@pytest.fixture(scope="module")
+def fp4():
+    from block_wise_dynamic_gb300 import build
+
+    build.build()
+    from block_wise_dynamic_gb300 import fp4 as m
+
+    return m
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def name_of(dtype):
+    return next(k for k, v in TYPES.items() if v == dtype)
+
+
+def draw(shape, seed, kind, std=1.0):
+    rng = np.random.default_rng(seed)
+    x = rng.standard_normal(shape) * std * np.exp(rng.standard_normal((shape[0], 1)))
+    x[:, rng.random(shape[1]) < 0.02] *= 30
+    return torch.from_numpy(x).to(DEV).to(TYPES[kind])
+
+
+def scale_bytes(q):
+    """The documented place of each block's byte."""
+    rows, cols = q.shape
+    s = q.scales.cpu().numpy()
+    r, k = np.meshgrid(np.arange(rows), np.arange(8 * -(-cols // 256)), indexing="ij")
+    return s[((r // 128) * 2 * -(-cols // 256) + k // 4) * 512 + (r % 32) * 16 + (r // 32 % 4) * 4 + k % 4].astype(np.int64)
+
+
+def check_quantized(q, x):
+    rows, cols = x.shape
+    want, e = ref.quantize(np64(x))
+    got = scale_bytes(q)
+    assert np.array_equal(got[:, :e.shape[1]], e + 127)
+    assert not got[:, e.shape[1]:].any()
+    codes = q.codes.cpu().numpy()
+    both = np.stack([codes & 15, codes >> 4], -1).reshape(rows, -1)
+    assert not both[:, cols:].any()
+    grid = np.concatenate([ref.GRID, -ref.GRID])
+    values = grid[both[:, :cols]] * np.exp2(np.repeat(e, 32, 1)[:, :cols].astype(np.float64))
+    finite = np.isfinite(want)
+    assert np.array_equal(values[finite], want[finite])
+    for dtype in TYPES.values():
+        back = np64(q.dequantize(dtype))
+        if dtype == torch.float16:
+            continue  # its range is less than a scale's; rounded below
+        assert np.array_equal(back, torch.from_numpy(want).to(dtype).double().numpy(), equal_nan=True)
+
+
+SIZES = [(1, 1), (1, 31), (3, 32), (2, 33), (1, 4096), (5, 128), (31, 129), (33, 255), (128, 256), (129, 257), (200, 1003), (64, 1000), (300, 64)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("rows,cols", SIZES)
+def test_quantize(fp4, rows, cols, kind):
+    x = draw((rows, cols), 1, kind)
+    q = fp4.quantize(x)
+    check_quantized(q, x)
+    back = q.dequantize()
+    assert back.dtype == x.dtype and np.array_equal(np64(back), ref.quantize(np64(x))[0])
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("off,pitch", [(0, 8), (1, 0), (1, 3), (2, 2), (4, 4), (8, 1)])
+def test_quantize_strides_and_alignment(fp4, off, pitch, kind):
+    rows, cols = 70, 520
+    flat = torch.full((off + rows * (cols + pitch),), 1e4, dtype=TYPES[kind], device=DEV)
+    x = flat[off:].view(rows, cols + pitch)[:, :cols]
+    x.copy_(draw((rows, cols), 2, kind))
+    check_quantized(fp4.quantize(x), x)
+    assert torch.equal(fp4.quantize(x).dequantize(), fp4.quantize(x.contiguous()).dequantize())
+    t = draw((cols, rows), 3, kind).t()
+    check_quantized(fp4.quantize(t), t)
+
+
+def test_quantize_special_values(fp4):
+    x = torch.zeros((9, 96), device=DEV)
+    x[0, 3] = float("inf")
+    x[1, 40] = float("nan")
+    x[2] = torch.linspace(-6, 6, 96, device=DEV)
+    x[3, :32] = 2.0 ** -149
+    x[4, :32] = torch.finfo(torch.float32).max
+    x[5] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 12, device=DEV) * 2.0 ** 20
+    x[6] = -x[5] * 2.0 ** -140
+    x[7, 0], x[7, 33] = 6.0, float(np.nextafter(np.float32(6), np.float32(7)))
+    x[8] = -0.0
+    check_quantized(fp4.quantize(x), x)
+    big = torch.tensor([[65504.0, 60000.0, 1.0, -65504.0]], dtype=torch.float16, device=DEV)
+    check_quantized(fp4.quantize(big), big)
+
+
+def check_product(y, x, w, bias):
+    """Terms are exact.  The matrix instruction aligns and truncates what it
+    adds, 32 products at a time, to some 2^-22 of the largest sum so far; fp32
+    results leave it after 2,048 products and are added up with the parts of a
+    cluster and the bias, to nearest."""
+    kind, k = name_of(y.dtype), x.shape[1]
+    want, size = ref.linear(np64(x), np64(w), None if bias is None else np64(bias))
+    steps = -(-min(k, 2048) // 32) if kind == "fp32" else -(-k // 32)
+    off = size * (2.0 ** -22 * steps + U * (k / 2048 + 12))
+    got = np64(y)
+    assert got.shape == want.shape
+    over = np.abs(got - want) - off - ROUND[kind] * (np.abs(want) + off) - TINY[kind]
+    assert over.max(initial=-1) <= 0, (over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+PRODUCTS = [(1, 16, 32), (1, 1, 1), (1, 130, 700), (3, 300, 256), (16, 128, 300), (17, 200, 512), (32, 257, 64), (33, 140, 1500), (64, 128, 1024),
+            (65, 128, 256), (100, 130, 40), (128, 128, 2600), (129, 260, 300), (257, 300, 520), (300, 515, 1003), (513, 258, 100)]
+
+
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("m,n,k", PRODUCTS)
+def test_linear(fp4, m, n, k, kind):
+    x, w = draw((m, k), 1, kind), draw((n, k), 2, kind, 0.02)
+    bias = draw((1, n), 3, kind)[0]
+    wq = fp4.quantize(w)
+    for b in (None, bias):
+        y = fp4.linear(x, wq, b)
+        assert y.dtype == x.dtype
+        check_product(y, x, w, b)
+        assert torch.equal(fp4.linear(x, wq, b), y)
+    assert torch.equal(fp4.matmul(fp4.quantize(x), wq, bias), y)
+
+
+@pytest.mark.parametrize("kind", ["fp32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(2, 200, 9000), (20, 130, 30000), (70, 260, 17000), (400, 300, 5000), (2300, 1100, 300)])
+def test_long_sums_and_many_tiles(fp4, m, n, k, kind):
+    x, w = draw((m, k), 1, kind), draw((n, k), 2, kind, 0.02)
+    x[:, ::3] = x[:, ::3].abs()  # sums of like signs, where truncation shows
+    y = fp4.linear(x, fp4.quantize(w))
+    rows = np.r_[0:min(m, 3), max(0, m - 3):m]
+    check_product(y[rows], x[rows], w, None)
+
+
+def test_every_tile_of_a_large_product(fp4):
+    """Small whole numbers: every sum is exact."""
+    g = torch.Generator(DEV).manual_seed(0)
+    for m, n, k in [(5000, 3000, 512), (1000, 9000, 768), (700, 20000, 256)]:
+        x = torch.randint(-2, 3, (m, k), generator=g, device=DEV).to(torch.bfloat16)
+        w = torch.randint(-2, 3, (n, k), generator=g, device=DEV).to(torch.bfloat16)
+        y = fp4.linear(x.float(), fp4.quantize(w))
+        assert torch.equal(y, x.float() @ w.float().t())
+
+
+def test_outputs_end_where_they_should(fp4):
+    from block_wise_dynamic_gb300 import _abi
+
+    lib = _abi.load()
+    for m, n, k, ldo in [(130, 70, 300, 71), (260, 300, 300, 304), (5, 70, 300, 80), (300, 130, 64, 257), (300, 65, 64, 72)]:
+        x, w = draw((m, k), 1, "bf16"), draw((n, k), 2, "bf16")
+        xq, wq = fp4.quantize(x), fp4.quantize(w)
+        for dtype, code in ((torch.bfloat16, 1), (torch.float32, 0)):
+            out = torch.full((m + 2, ldo), 7.0, dtype=dtype, device=DEV)
+            assert lib.bwd_fp4_matmul(m, n, k, *xq._pointers(), *wq._pointers(), None, out[1].data_ptr(), ldo, code, None) == 0
+            torch.cuda.synchronize()
+            assert (out[0] == 7).all() and (out[m + 1] == 7).all() and (out[1:m + 1, n:] == 7).all()
+            check_product(out[1:m + 1, :n].contiguous(), x, w, None)
+
+
+def test_not_finite_rows(fp4):
+    x, w = draw((300, 400), 1, "bf16"), draw((200, 400), 2, "bf16")
+    x[7, 350] = float("inf")
+    w[150, 3] = float("nan")
+    for rows in (300, 10):
+        y = fp4.linear(x[:rows], fp4.quantize(w))
+        assert y[7].isnan().all() and y[:, 150].isnan().all()
+        keep = [i for i in range(rows) if i != 7]
+        cols = [i for i in range(200) if i != 150]
+        assert y[keep][:, cols].isfinite().all()
+
+
+def test_nothing(fp4):
+    bias = torch.arange(4.0, device=DEV)
+    w = fp4.quantize(torch.empty((4, 0), device=DEV))
+    assert torch.equal(fp4.linear(torch.empty((3, 0), device=DEV), w, bias), bias.expand(3, 4))
+    w = fp4.quantize(torch.ones((4, 8), device=DEV))
+    assert fp4.linear(torch.empty((0, 8), device=DEV), w).shape == (0, 4)
+    assert fp4.linear(torch.empty((2, 8), device=DEV), fp4.quantize(torch.empty((0, 8), device=DEV))).shape == (2, 0)
+    assert fp4.quantize(torch.empty((0, 8), device=DEV)).dequantize().shape == (0, 8)
+
+
+def test_leading_dimensions_streams_and_graphs(fp4):
+    x, w = draw((6, 300), 1, "bf16").view(2, 3, 300), draw((50, 300), 2, "bf16")
+    wq = fp4.quantize(w)
+    y = fp4.linear(x, wq)
+    assert y.shape == (2, 3, 50)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = fp4.linear(x, fp4.quantize(w, stream=side), stream=side)
+    side.synchronize()
+    assert torch.equal(got, y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fp4.linear(x, wq)
+        back = fp4.quantize(x).dequantize()
+    x.copy_(draw((6, 300), 5, "bf16").view(2, 3, 300))
+    graph.replay()
+    torch.cuda.synchronize()
+    check_product(out.view(6, 50), x.view(6, 300), w, None)
+    assert np.array_equal(np64(back), ref.quantize(np64(x.view(6, 300)))[0])
+
+
+def test_a_weight_written_by_the_kernel_ahead(fp4):
+    """Quantizer, product and again, one right behind the other."""
+    x = draw((8, 2048), 1, "bf16")
+    ws = [draw((512, 2048), 10 + i, "bf16") for i in range(4)]
+    want = [fp4.linear(x, fp4.quantize(w)) for w in ws]
+    torch.cuda.synchronize()
+    xq = fp4.quantize(x)
+    for _ in range(20):
+        for w, y in zip(ws, want):
+            assert torch.equal(fp4.matmul(xq, fp4.quantize(w)), y)
+
+
+def test_module(fp4):
+    layer = torch.nn.Linear(300, 70, device=DEV, dtype=torch.bfloat16)
+    m = fp4.Fp4Linear(layer)
+    x = draw((5, 300), 1, "bf16")
+    with torch.no_grad():
+        y = m(x)
+    check_product(y, x, layer.weight, layer.bias)
+    assert torch.equal(m(x), y)
+    with pytest.raises(RuntimeError, match="no gradients"):
+        m(x.clone().requires_grad_())
+    other = fp4.Fp4Linear(torch.nn.Linear(300, 70, device=DEV, dtype=torch.bfloat16))
+    other.load_state_dict(m.state_dict())
+    assert torch.equal(other(x), y)
+    assert fp4.Fp4Linear(torch.nn.Linear(8, 4, bias=False, device=DEV))(torch.ones(2, 8, device=DEV)).shape == (2, 4)
