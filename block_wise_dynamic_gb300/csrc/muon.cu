@@ -64,11 +64,61 @@ struct PrepareArgs {
 __device__ __forceinline__ bool finite(float s) { return fabsf(s) <= 3.402823466e38f; }
 
 // mom = mu mom + s g; the update u is s g + mu mom, or mom.
-__device__ __forceinline__ float new_momentum(const PrepareArgs& a, float s, float g, float mom) {
-  return __fmaf_rn(a.momentum, mom, __fmul_rn(s, g));
+
+// Eight consecutive values.
+template <int kT>
+__device__ __forceinline__ void load8(const void* x, int64_t i, float (&v)[8]) {
+  if constexpr (kT == kF32) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const float4 f = __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(x) + i) + q);
+      v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+    }
+  } else {
+    const uint4 w = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + i));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t h = j % 2 ? (&w.x)[j / 2] >> 16 : (&w.x)[j / 2] & 0xffffu;
+      v[j] = kT == kBF16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(h)));
+    }
+  }
 }
-__device__ __forceinline__ float update_of(const PrepareArgs& a, float s, float g, float mom) {
-  return a.nesterov ? __fmaf_rn(a.momentum, mom, __fmul_rn(s, g)) : mom;
+__device__ __forceinline__ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The update's values i .. i + 7, zeros from `end` on; with kStep the new
+// momentum is formed and written, else it is read.
+template <int kT, bool kMomentum, bool kStep>
+__device__ __forceinline__ void update8(const PrepareArgs& a, const void* g, float* mom, float s, bool vec, int64_t i, int64_t end, float (&u)[8]) {
+  float m[8] = {};
+  const bool whole = vec && i + 8 <= end;
+  if (whole) {
+    load8<kT>(g, i, u);
+    if constexpr (kMomentum) load8<kF32>(mom, i, m);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      u[j] = i + j < end ? load1<kT>(g, i + j) : 0.0f;
+      if constexpr (kMomentum) m[j] = i + j < end ? mom[i + j] : 0.0f;
+    }
+  }
+  if constexpr (kMomentum && kStep) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m[j] = __fmaf_rn(a.momentum, m[j], __fmul_rn(s, u[j]));
+    if (!finite(s)) {
+      // nothing is written
+    } else if (whole) {
+      reinterpret_cast<float4*>(mom + i)[0] = make_float4(m[0], m[1], m[2], m[3]);
+      reinterpret_cast<float4*>(mom + i)[1] = make_float4(m[4], m[5], m[6], m[7]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + j < end) mom[i + j] = m[j];
+    }
+  }
+  if constexpr (kMomentum) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) u[j] = a.nesterov ? __fmaf_rn(a.momentum, m[j], __fmul_rn(s, u[j])) : m[j];
+  }
 }
 
 // One chunk of one matrix: the new momentum, and the update's sum of squares
@@ -77,7 +127,6 @@ __device__ __forceinline__ float update_of(const PrepareArgs& a, float s, float 
 template <int kT, bool kMomentum>
 __global__ void __launch_bounds__(kThreads)
 ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
-  constexpr int kEach = 8;
   __shared__ double s_red[kThreads / 32];
   wait_for_inputs();
   let_next_begin();
@@ -85,32 +134,23 @@ ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
   const void* const g = a.x.g[z];
   float* const mom = a.x.mom[z];
   const float s = kMomentum && a.grad_scale ? *a.grad_scale : 1.0f;
+  const bool vec = on16(g) && on16(mom);
   double sum = 0.0;
   const int64_t end = min(a.size, (blockIdx.x + 1) * a.chunk);
-  for (int64_t i0 = blockIdx.x * a.chunk + threadIdx.x; i0 < end; i0 += kEach * kThreads) {
-    float u[kEach], old[kEach];
-#pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int64_t i = i0 + j * kThreads;
-      u[j] = i < end ? load1<kT>(g, i) : 0.0f;
-      if constexpr (kMomentum) old[j] = i < end ? mom[i] : 0.0f;
-    }
+#pragma unroll 2
+  for (int64_t i = blockIdx.x * a.chunk + 8 * threadIdx.x; i < end; i += 8 * kThreads) {
+    float u[8];
+    update8<kT, kMomentum, true>(a, g, mom, s, vec, i, end, u);
     float part = 0.0f;
     uint32_t any = 0;
 #pragma unroll
-    for (int j = 0; j < kEach; ++j) {
-      const int64_t i = i0 + j * kThreads;
-      if constexpr (kMomentum) {
-        const float next = new_momentum(a, s, u[j], old[j]);
-        if (i < end && finite(s)) mom[i] = next;
-        u[j] = update_of(a, s, u[j], next);
-      }
+    for (int j = 0; j < 8; ++j) {
       any |= __float_as_uint(u[j]);
       part = __fmaf_rn(u[j], u[j], part);
     }
     if ((any & 0x7fffffffu) != 0 && !(part >= 0x1p-120f && part <= 3.402823466e38f)) {
 #pragma unroll
-      for (int j = 0; j < kEach; ++j) sum = __fma_rn(static_cast<double>(u[j]), static_cast<double>(u[j]), sum);
+      for (int j = 0; j < 8; ++j) sum = __fma_rn(static_cast<double>(u[j]), static_cast<double>(u[j]), sum);
     } else {
       sum += static_cast<double>(part);
     }
@@ -133,9 +173,12 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& high, uint3
   low = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// X's pair from the update, 64 x 64 elements of the wide form to a CTA, which
-// go through shared memory so that both sides' rows are contiguous for either
-// orientation.  Columns up to the pitch are written, as zeros.
+// X's pair from the update, 64 rows and 256 columns of the wide form to a CTA.
+// A tall matrix goes through shared memory, 64 x 64 elements at a time, so
+// that both sides' rows are contiguous.  Columns up to the pitch are written,
+// as zeros.
+constexpr int kSplitRows = 64, kSplitCols = 256;
+
 template <int kT, bool kMomentum>
 __global__ void __launch_bounds__(kThreads)
 ns_split_kernel(const __grid_constant__ PrepareArgs a) {
@@ -162,37 +205,53 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
   __syncthreads();
   const float first = s_inv[0], inv = s_inv[1];
   const void* const g = a.x.g[z];
-  const float* const mom = a.x.mom[z];
+  float* const mom = a.x.mom[z];
   const float s = kMomentum && a.grad_scale ? *a.grad_scale : 1.0f;
   const bool tall = a.x.tall[z];
-  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
-  // as stored: rows of the wide form, or its columns
-  const int rows = tall ? a.n : a.m, cols = tall ? a.m : a.n, sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0;
-#pragma unroll 4
-  for (int e = threadIdx.x; e < 64 * 64; e += kThreads) {
-    const int r = e / 64, c = e % 64;
-    float x = 0.0f;
-    if (sr0 + r < rows && sc0 + c < cols) {
-      const int64_t i = static_cast<int64_t>(sr0 + r) * cols + sc0 + c;
-      x = load1<kT>(g, i);
-      if constexpr (kMomentum) x = update_of(a, s, x, mom[i]);
-      x = __fmul_rn(__fmul_rn(x, first), inv);
-    }
-    if (tall) s_x[c][r] = x;
-    else s_x[r][c] = x;
-  }
-  __syncthreads();
+  const int cols = tall ? a.m : a.n;  // as stored
+  const bool vec = on16(g) && on16(mom) && cols % 8 == 0;
   __half* const high = a.planes + static_cast<int64_t>(z) * 2 * a.m * a.pitch;
   __half* const low = high + static_cast<int64_t>(a.m) * a.pitch;
-  for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
-    const int r = e / 8, c = e % 8 * 8;
-    if (r0 + r >= a.m || c0 + c >= a.pitch) continue;
+  const int r0 = blockIdx.y * kSplitRows;
+  const auto put = [&](int row, int col, const float (&x)[8]) {
+    if (row >= a.m || col >= a.pitch) return;
     uint4 h, l;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) split2(s_x[r][c + 2 * j], s_x[r][c + 2 * j + 1], (&h.x)[j], (&l.x)[j]);
-    const int64_t at = static_cast<int64_t>(r0 + r) * a.pitch + c0 + c;
+    for (int j = 0; j < 4; ++j) split2(x[2 * j], x[2 * j + 1], (&h.x)[j], (&l.x)[j]);
+    const int64_t at = static_cast<int64_t>(row) * a.pitch + col;
     *reinterpret_cast<uint4*>(high + at) = h;
     *reinterpret_cast<uint4*>(low + at) = l;
+  };
+  for (int c0 = blockIdx.x * kSplitCols, c1 = c0 + kSplitCols; c0 < c1; c0 += 64) {
+    const int sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0, rows = tall ? a.n : a.m;
+#pragma unroll
+    for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
+      const int r = e / 8, c = e % 8 * 8;
+      float x[8] = {};
+      if (sr0 + r < rows && sc0 + c < cols) {
+        const int64_t at = static_cast<int64_t>(sr0 + r) * cols;
+        update8<kT, kMomentum, false>(a, g, mom, s, vec, at + sc0 + c, at + cols, x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fmul_rn(__fmul_rn(x[j], first), inv);
+      }
+      if (tall) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s_x[c + j][r] = x[j];
+      } else {
+        put(r0 + r, c0 + c, x);
+      }
+    }
+    if (!tall) continue;
+    __syncthreads();
+#pragma unroll
+    for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
+      const int r = e / 8, c = e % 8 * 8;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = s_x[r][c + j];
+      put(r0 + r, c0 + c, x);
+    }
+    __syncthreads();
   }
 }
 
@@ -201,27 +260,31 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
 //
 // A pair of CTAs (a cluster of two) works on a tile of 256 rows and kBN
 // columns; pairs walk the tiles of all matrices with a grid stride.  Warp 0
-// copies, warp 1 of the first CTA issues for both, and eight warps store the
-// tile before from the other accumulator.
+// copies, warp 1 of the first CTA issues for both, and sixteen warps store the
+// tile before from the other accumulator: each 32 rows of a quarter of the
+// columns, whose sums its registers hold, 32 columns at a time through 4 KB of
+// its own.  There the matrix that is added arrives by a tensor copy and the
+// result replaces it, high and low parts in rows of 64 bytes.
 constexpr int kBM = 256;
 constexpr int kBK = 64;  // fp16 values of the summed axis in a stage: 128 bytes
-constexpr int kMmThreads = 320;
+constexpr int kStoreWarps = 16;
+constexpr int kStoreWarp = 2;  // the first of them
+constexpr int kMmThreads = 32 * (kStoreWarp + kStoreWarps);
 constexpr uint32_t kTmemCols = 512;
-constexpr int kPad = 33;  // words of a staged row of 32
+constexpr int kPlaneBytes = 32 * 64;  // of a warp's 32 x 32 values, one plane
 
 template <int kBN> __host__ __device__ constexpr int ns_stages() { return kBN == 256 ? 5 : 6; }
 constexpr int kABytes = kBM / 2 * kBK * 2;
 template <int kBN> __host__ __device__ constexpr int ns_b_bytes() { return kBN / 2 * kBK * 2; }
 template <int kBN> __host__ __device__ constexpr int ns_smem() {
-  return 1024 + ns_stages<kBN>() * (kABytes + ns_b_bytes<kBN>()) + 8 * 32 * kPad * 4;
+  return 1024 + ns_stages<kBN>() * (kABytes + ns_b_bytes<kBN>()) + kStoreWarps * 2 * kPlaneBytes;
 }
 
 enum Mode { kGram, kPoly, kApply, kFinal };
 
 struct ProductArgs {
   CUtensorMap p, q;      // planes of the two operands
-  const __half* add;     // planes that alpha multiplies, of the result's shape
-  __half* out;           // the result's planes
+  CUtensorMap add, out;  // planes that alpha multiplies, and the result's, in boxes of 32 x 32
   int m, n, pitch;       // the result's
   int kblocks;
   int passes;            // 3, or 1: the high parts alone
@@ -238,6 +301,36 @@ struct FinalArgs {
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                 "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+               : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_load3_one(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               ::"r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void tma_store3(const CUtensorMap* map, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+               ::"l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src)) : "memory");
+}
+
+__device__ __forceinline__ uint4 shared_load16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void shared_store16(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void shared_store2(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(v)) : "memory");
 }
 
 struct Tile {
@@ -264,9 +357,26 @@ __device__ __forceinline__ float half_at(const uint4& w, int j) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(j % 2 ? q >> 16 : q & 0xffffu)));
 }
 
+// The matrix instruction adds into its fp32 accumulator with truncation, an
+// error with a sign, which A's diagonal shows in full.  For fp32 results (kSum)
+// the sums leave it every kChunk stages of high x high, 256 products, and are
+// added up in registers, rounded to nearest; what low parts add is 2^-11 of
+// that and stays for all of their products.  (777 x 301: error 5.2e-6 without,
+// and fp32 arithmetic has 1.8e-6.)
+constexpr int kChunk = 4;
+
+// Stages of a tile whose sums leave the accumulator together, from stage k on.
+template <bool kSum>
+__device__ __forceinline__ int chunk_end(const ProductArgs& a, int k) {
+  const int all = a.passes * a.kblocks, small = all - a.kblocks;
+  if (!kSum) return all;
+  if (k < small) return small;
+  return k + kChunk < all ? k + kChunk : all;
+}
+
 // kT and kUpdate: of the last product, whose result has type kT, or updates a
 // parameter of that type.
-template <int kBN, int kMode, int kT, bool kUpdate>
+template <int kBN, int kMode, int kT, bool kUpdate, bool kSum>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
@@ -274,7 +384,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
   constexpr int kStages = ns_stages<kBN>(), kB_ = ns_b_bytes<kBN>(), kStage = kABytes + kB_;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2];
+  __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages], s_acc_full[2], s_acc_empty[2], s_add[kStoreWarps];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -285,7 +395,8 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     prefetch_map(&a.q);
     s_fail = 0;
     for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 16); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], 2 * kStoreWarps); }
+    for (int i = 0; i < kStoreWarps; ++i) mbar_init(&s_add[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -341,126 +452,206 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       int use = 0;
       bool ok = true;
       const int blocks = a.passes * a.kblocks;
-      for (int t = first; ok && t < a.items; t += pairs, ++use) {
-        const int buf = use & 1;
-        ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t acc = tmem + buf * 256;
-        for (int kb = 0; ok && kb < blocks; ++kb, ring.next()) {
-          if (!(ok = mbar_wait(&s_full[ring.s], ring.phase, &s_fail))) break;
+      for (int t = first; ok && t < a.items; t += pairs)
+        for (int k0 = 0, k1; ok && k0 < blocks; k0 = k1, ++use) {
+          k1 = chunk_end<kSum>(a, k0);
+          const int buf = use & 1;
+          ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          if (one) {
-            const uint64_t dp = dp0 + static_cast<uint32_t>(ring.s * (kStage / 16)), dq = dq0 + static_cast<uint32_t>(ring.s * (kStage / 16));
+          const uint32_t acc = tmem + buf * 256;
+          for (int kb = k0; ok && kb < k1; ++kb, ring.next()) {
+            if (!(ok = mbar_wait(&s_full[ring.s], ring.phase, &s_fail))) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            if (one) {
+              const uint64_t dp = dp0 + static_cast<uint32_t>(ring.s * (kStage / 16)), dq = dq0 + static_cast<uint32_t>(ring.s * (kStage / 16));
 #pragma unroll
-            for (uint32_t q = 0; q < 4; ++q)
-              asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-                           "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
-                           ::"r"(acc), "l"(dp + q * kStepP), "l"(dq + q * kStepQ), "r"(idesc),
-                           "r"(static_cast<uint32_t>(kb != 0 || q != 0)) : "memory");
-            commit_pair(&s_empty[ring.s]);
+              for (uint32_t q = 0; q < 4; ++q)
+                asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                             "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+                             ::"r"(acc), "l"(dp + q * kStepP), "l"(dq + q * kStepQ), "r"(idesc),
+                             "r"(static_cast<uint32_t>(kb != k0 || q != 0)) : "memory");
+              commit_pair(&s_empty[ring.s]);
+            }
+            __syncwarp();
           }
+          if (one) commit_pair(&s_acc_full[buf]);
           __syncwarp();
         }
-        if (one) commit_pair(&s_acc_full[buf]);
-        __syncwarp();
-      }
     }
   } else {
     wait_for_inputs();
-    const int quarter = warp & 3, half = (warp - 2) / 4;
-    constexpr int kHalf = kBN / 2;  // columns of one warp
-    float* const stage = reinterpret_cast<float*>(sm + kStages * kStage) + (warp - 2) * 32 * kPad;
-    const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * kHalf;
+    const int w = warp - kStoreWarp, quarter = warp & 3;
+    constexpr int kOwn = kBN / 4, kGroups = kOwn / 32;  // columns of one warp
+    const int own_col = w / 4 * kOwn;
+    uint8_t* const buf = sm + kStages * kStage + w * 2 * kPlaneBytes;
+    const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + own_col;
     int use = 0;
+    uint32_t adds = 0;  // parity of the next tensor copy
     bool ok = true, writes = true;
     if constexpr (kMode == kFinal && kUpdate) writes = finite(f.grad_scale ? *f.grad_scale : 1.0f);
-    for (int t = first; ok && t < a.items; t += pairs, ++use) {
-      const Tile tile = tile_of<kBN, kSymmetric>(a, t);
-      const int buf = use & 1, row0 = tile.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, row = row0 + lane;
-      const bool in = row < a.m;
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[buf], (use >> 1) & 1, &s_fail));
-      if (!ok) break;
+    const int blocks = a.passes * a.kblocks;
+    const auto wait_full = [&] {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[use & 1], (use >> 1) & 1, &s_fail));
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const int64_t plane = static_cast<int64_t>(a.m) * a.pitch, at_row = 2 * tile.z * plane + static_cast<int64_t>(in ? row : 0) * a.pitch;
+      return ok;
+    };
+    const auto done = [&] {
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_leader(&s_acc_empty[use & 1]);
+      ++use;
+    };
+    // 16-byte piece q of this lane's row; the tensor maps swizzle rows of 64 bytes
+    const uint32_t buf_at = smem_u32(buf), my_row = buf_at + lane * 64, swizzle = ((lane >> 1) & 3) << 4;
+    const auto store_planes = [&](int x, int y, int z) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        tma_store3(&a.out, x, y, 2 * z, buf);
+        tma_store3(&a.out, x, y, 2 * z + 1, buf + kPlaneBytes);
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    };
+    const auto wait_stored = [&] {
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    };
+    for (int t = first; ok && t < a.items; t += pairs) {
+      const Tile tile = tile_of<kBN, kSymmetric>(a, t);
+      const int row0 = tile.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, row = row0 + lane, col0 = tile.n0 + own_col;
+      // (what lies past the matrix is not there to copy or to store)
+      const bool some = row0 < a.m;
+      const auto fetch = [&](int col) {
+        if (!kAdd || !some || col >= a.pitch) return;
+        wait_stored();
+        if (lane == 0) {
+          mbar_expect_tx(&s_add[w], 2 * kPlaneBytes);
+          tma_load3_one(buf, &a.add, col, row0, 2 * tile.z, &s_add[w]);
+          tma_load3_one(buf + kPlaneBytes, &a.add, col, row0, 2 * tile.z + 1, &s_add[w]);
+        }
+      };
+      fetch(col0);
+      float sum[kSum ? kOwn : 1];
+#pragma unroll
+      for (int j = 0; j < (kSum ? kOwn : 1); ++j) sum[j] = 0.0f;
+      if constexpr (kSum) {
 #pragma unroll 1
-      for (int g = 0; g < kHalf / 32; ++g) {
-        const int col = tile.n0 + half * kHalf + 32 * g;
-        uint4 ch[4], cl[4];
-        if constexpr (kAdd) {
-          if (col < a.pitch) {
-            const uint4* const from = reinterpret_cast<const uint4*>(a.add + at_row + col);
+        for (int k0 = 0; k0 < blocks; k0 = chunk_end<kSum>(a, k0)) {
+          if (!wait_full()) break;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              ch[q] = __ldg(from + q);
-              cl[q] = __ldg(from + plane / 8 + q);
-            }
+          for (int c = 0; c < kOwn; c += 16) {
+            float r[16];
+            tmem_load16(own + (use & 1) * 256 + c, r);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], r[j]);
           }
+          done();
         }
-        uint32_t r[32];
-        tmem_load32(own + buf * 256 + 32 * g, r);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (g == kHalf / 32 - 1) {
-          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive_leader(&s_acc_empty[buf]);
-        }
-        if (col >= a.pitch) continue;
-        float v[32];
+      } else {
+        wait_full();
+      }
+      if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          v[j] = __fmul_rn(a.beta, __uint_as_float(r[j]));
-          if constexpr (kAdd) v[j] = __fmaf_rn(a.alpha, __fadd_rn(half_at(ch[j / 8], j % 8), half_at(cl[j / 8], j % 8)), v[j]);
-          if constexpr (kSymmetric) v[j] = in ? v[j] : 0.0f;
+      for (int g = 0; g < kGroups; ++g) {
+        const int col = col0 + 32 * g;
+        if (g > 0) fetch(col);
+        float v[32];
+        if constexpr (kSum) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = sum[32 * g + j];
+        } else {
+          uint32_t r[32];
+          tmem_load32(own + (use & 1) * 256 + 32 * g, r);
+          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+          if (g == kGroups - 1) done();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+        }
+        if (!some || col >= a.pitch) continue;
+        if constexpr (kAdd) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&s_add[w], adds, &s_fail));
+          adds ^= 1u;
+          if (!ok) break;
+        } else {
+          wait_stored();
+        }
+        uint32_t h[16], l[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 ch, cl;
+          if constexpr (kAdd) {
+            ch = shared_load16(my_row + (swizzle ^ (q << 4)));
+            cl = shared_load16(my_row + (swizzle ^ (q << 4)) + kPlaneBytes);
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float& x = v[8 * q + j];
+            x = __fmul_rn(a.beta, x);
+            if constexpr (kAdd) x = __fmaf_rn(a.alpha, __fadd_rn(half_at(ch, j), half_at(cl, j)), x);
+          }
+          if constexpr (kMode != kFinal) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) split2(v[8 * q + 2 * j], v[8 * q + 2 * j + 1], h[4 * q + j], l[4 * q + j]);
+            shared_store16(my_row + (swizzle ^ (q << 4)), make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]));
+            shared_store16(my_row + (swizzle ^ (q << 4)) + kPlaneBytes, make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]));
+          }
         }
         if constexpr (kMode != kFinal) {
-          uint32_t h[16], l[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) split2(v[2 * j], v[2 * j + 1], h[j], l[j]);
-          if (in) {
-            uint4* const to = reinterpret_cast<uint4*>(a.out + at_row + col);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              to[q] = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-              to[plane / 8 + q] = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
-            }
-          }
+          store_planes(col, row0, tile.z);
           // Columns left of the diagonal's tiles are all rows of the matrix.
-          // As rows they have their zeros up to the pitch from here.
-          if (kSymmetric && tile.mirror && row < a.pitch) {
-            uint16_t* const to = reinterpret_cast<uint16_t*>(a.out) + 2 * tile.z * plane + static_cast<int64_t>(col) * a.pitch + row;
+          if (kSymmetric && tile.mirror) {
+            wait_stored();
+            // column j becomes a row: this lane's 2 bytes in piece lane / 8 of it
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              to[static_cast<int64_t>(j) * a.pitch] = static_cast<uint16_t>(j % 2 ? h[j / 2] >> 16 : h[j / 2] & 0xffffu);
-              to[plane + static_cast<int64_t>(j) * a.pitch] = static_cast<uint16_t>(j % 2 ? l[j / 2] >> 16 : l[j / 2] & 0xffffu);
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t to = buf_at + ((((lane >> 3) ^ x) << 4) | (lane & 7) * 2);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int j = i / 2 * 8 + 2 * x + i % 2;
+                shared_store2(to + j * 64, j % 2 ? h[j / 2] >> 16 : h[j / 2]);
+                shared_store2(to + j * 64 + kPlaneBytes, j % 2 ? l[j / 2] >> 16 : l[j / 2]);
+              }
             }
+            store_planes(row0, col, tile.z);
           }
         } else {
-          void* const out = f.x.out[tile.z];
-          const auto emit = [&](int64_t i, float o) {
-            if constexpr (kUpdate) store1<kT>(out, i, __fmaf_rn(-f.step, o, __fmul_rn(load1<kT>(out, i), f.decay)));
-            else store1<kT>(out, i, o);
-          };
           if (!writes) continue;
-          if (f.x.tall[tile.z]) {
-            if (in) {
+          // 32 values of a line of the result that are far apart, neighbouring
+          // lanes' side by side; several old parameters are read before any of
+          // them is written
+          const bool tall = f.x.tall[tile.z];
+          float* const stage = reinterpret_cast<float*>(buf);
+          __syncwarp();
+          if (!tall) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (col + j < a.n) emit(static_cast<int64_t>(col + j) * a.m + row, v[j]);
-            }
-          } else {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) stage[lane * kPad + j] = v[j];
-            __syncwarp();
-            if (col + lane < a.n) {
-              const int rows = a.m - row0 < 32 ? a.m - row0 : 32;
-#pragma unroll 8
-              for (int q = 0; q < rows; ++q) emit(static_cast<int64_t>(row0 + q) * a.n + col + lane, stage[q * kPad + lane]);
-            }
+            for (int j = 0; j < 32; ++j) stage[lane * 32 + (j ^ lane)] = v[j];
           }
+          __syncwarp();
+          const int64_t ld = tall ? a.m : a.n;
+          int64_t at = tall ? static_cast<int64_t>(col) * ld + row : static_cast<int64_t>(row0) * ld + col + lane;
+          const int count = tall ? (row < a.m ? a.n - col : 0) : col + lane < a.n ? a.m - row0 : 0;
+          void* const out = f.x.out[tile.z];
+#pragma unroll
+          for (int j0 = 0; j0 < 32; j0 += 8, at += 8 * ld) {
+            float o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = tall ? v[j0 + j] : stage[(j0 + j) * 32 + (lane ^ (j0 + j))];
+            if constexpr (kUpdate) {
+              float p[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) p[j] = j0 + j < count ? load1<kT>(out, at + j * ld) : 0.0f;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(-f.step, o[j], __fmul_rn(p[j], f.decay));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j0 + j < count) store1<kT>(out, at + j * ld, o[j]);
+          }
+          __syncwarp();
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   if (s_fail && lane == 0 && warp < 2) let_copies_land();
   __syncwarp();
@@ -506,12 +697,17 @@ struct DeviceState {
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 
+// The products of a call whose results have type kT.
 template <int kBN, int kMode, int kT, bool kUpdate>
-cudaError_t opt_in_one() { return opt_in(ns_product_kernel<kBN, kMode, kT, kUpdate>, ns_smem<kBN>()); }
+constexpr auto kernel_of() { return ns_product_kernel<kBN, kMode, kMode == kFinal ? kT : kF32, kUpdate, kT == kF32>; }
+
+template <int kBN, int kMode, int kT, bool kUpdate>
+cudaError_t opt_in_one() { return opt_in(kernel_of<kBN, kMode, kT, kUpdate>(), ns_smem<kBN>()); }
 
 template <int kBN>
 cudaError_t opt_in_all() {
   const cudaError_t e[] = {opt_in_one<kBN, kGram, kF32, false>(), opt_in_one<kBN, kPoly, kF32, false>(), opt_in_one<kBN, kApply, kF32, false>(),
+                           opt_in_one<kBN, kGram, kF16, false>(), opt_in_one<kBN, kPoly, kF16, false>(), opt_in_one<kBN, kApply, kF16, false>(),
                            opt_in_one<kBN, kFinal, kF32, false>(), opt_in_one<kBN, kFinal, kBF16, false>(), opt_in_one<kBN, kFinal, kF16, false>(),
                            opt_in_one<kBN, kFinal, kF32, true>(), opt_in_one<kBN, kFinal, kBF16, true>(), opt_in_one<kBN, kFinal, kF16, true>()};
   for (const cudaError_t x : e)
@@ -544,7 +740,7 @@ bwd_status ensure_device(int* pairs) {
     attr[0].val.clusterDim = {2, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&d.pairs, ns_product_kernel<256, kApply, kF32, false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of<256, kApply, kF16, false>(), &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
     if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
     d.ctx = ctx;
@@ -556,6 +752,7 @@ bwd_status ensure_device(int* pairs) {
 
 // Map of `planes` planes of m rows and `pitch` columns.
 bwd_status plane_map(CUtensorMap* map, const __half* base, int64_t m, int64_t pitch, int64_t planes, int box_cols, int box_rows) {
+  const CUtensorMapSwizzle swizzle = box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;  // a box's whole row
   EncodeFn encode = nullptr;
   const bwd_status s = encode_fn(&encode);
   if (s != BWD_OK) return s;
@@ -563,8 +760,7 @@ bwd_status plane_map(CUtensorMap* map, const __half* base, int64_t m, int64_t pi
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch * 2), static_cast<cuuint64_t>(m * pitch * 2)};
   const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1}, step[3] = {1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(base), dims, strides, box, step,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BWD_ERR_CUDA, "cuTensorMapEncodeTiled: error %d", static_cast<int>(r));
   return BWD_OK;
 }
@@ -591,13 +787,13 @@ bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& 
     return launch_ex(kernel, grid, kMmThreads, 0, ns_smem<kBN>(), stream, "ns_product_kernel launch", a, last);
   };
   if constexpr (kMode != kFinal) {
-    return go(ns_product_kernel<kBN, kMode, kF32, false>, 0);
+    return st.out_type == BWD_F32 ? go(kernel_of<kBN, kMode, kF32, false>(), 0) : go(kernel_of<kBN, kMode, kF16, false>(), 0);
   } else if (st.update) {
-    if (st.out_type == BWD_F32) return go(ns_product_kernel<kBN, kMode, kF32, true>, *f);
-    return st.out_type == BWD_BF16 ? go(ns_product_kernel<kBN, kMode, kBF16, true>, *f) : go(ns_product_kernel<kBN, kMode, kF16, true>, *f);
+    if (st.out_type == BWD_F32) return go(kernel_of<kBN, kMode, kF32, true>(), *f);
+    return st.out_type == BWD_BF16 ? go(kernel_of<kBN, kMode, kBF16, true>(), *f) : go(kernel_of<kBN, kMode, kF16, true>(), *f);
   } else {
-    if (st.out_type == BWD_F32) return go(ns_product_kernel<kBN, kMode, kF32, false>, *f);
-    return st.out_type == BWD_BF16 ? go(ns_product_kernel<kBN, kMode, kBF16, false>, *f) : go(ns_product_kernel<kBN, kMode, kF16, false>, *f);
+    if (st.out_type == BWD_F32) return go(kernel_of<kBN, kMode, kF32, false>(), *f);
+    return st.out_type == BWD_BF16 ? go(kernel_of<kBN, kMode, kBF16, false>(), *f) : go(kernel_of<kBN, kMode, kF16, false>(), *f);
   }
 }
 
@@ -610,7 +806,6 @@ bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* 
   // a tile of 256 columns takes up to one and a half times as long as one of 128
   const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   ProductArgs a{};
-  a.add = add; a.out = out;
   a.m = static_cast<int>(result.m); a.n = static_cast<int>(result.n); a.pitch = static_cast<int>(up(result.n, 64));
   a.kblocks = static_cast<int>((k + kBK - 1) / kBK);
   a.passes = passes;
@@ -623,6 +818,8 @@ bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* 
   bwd_status s = plane_map(&a.p, p, result.m, up(k, 64), 2 * count, kBK, kBM / 2);
   if (s != BWD_OK) return s;
   s = kSymmetric ? plane_map(&a.q, q, result.m, up(k, 64), 2 * count, kBK, bn / 2) : plane_map(&a.q, q, k, up(result.n, 64), 2 * count, 64, kBK);
+  if (s == BWD_OK && add) s = plane_map(&a.add, add, result.m, a.pitch, 2 * count, 32, 32);
+  if (s == BWD_OK && out) s = plane_map(&a.out, out, result.m, a.pitch, 2 * count, 32, 32);
   if (s != BWD_OK) return s;
   return bn == 256 ? launch_product<256, kMode>(a, f, st, pairs, stream) : launch_product<128, kMode>(a, f, st, pairs, stream);
 }
@@ -630,7 +827,8 @@ bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* 
 template <bool kMomentum>
 bwd_status prepare(const PrepareArgs& a, int64_t count, int type, cudaStream_t st) {
   const dim3 by_chunk(static_cast<unsigned>(a.chunks), static_cast<unsigned>(count));
-  const dim3 by_tile(static_cast<unsigned>((a.pitch + 63) / 64), static_cast<unsigned>((a.m + 63) / 64), static_cast<unsigned>(count));
+  const dim3 by_tile(static_cast<unsigned>((a.pitch + kSplitCols - 1) / kSplitCols),
+                     static_cast<unsigned>((a.m + kSplitRows - 1) / kSplitRows), static_cast<unsigned>(count));
   const auto go = [&](auto norm, auto split) {
     const bwd_status s = launch_ex(norm, by_chunk, kThreads, 0, 0, st, "ns_norm_kernel launch", a);
     return s == BWD_OK ? launch_ex(split, by_tile, kThreads, 0, 0, st, "ns_split_kernel launch", a) : s;
