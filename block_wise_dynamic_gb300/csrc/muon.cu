@@ -57,6 +57,7 @@ struct PrepareArgs {
   int64_t chunk;            // of one CTA of the first kernel
   int chunks;
   int m, n, pitch;          // of the wide form
+  int split_cols;           // columns of one CTA of the second kernel, a multiple of 64
   float momentum;
   int nesterov;
 };
@@ -173,11 +174,11 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& high, uint3
   low = *reinterpret_cast<const uint32_t*>(&l);
 }
 
-// X's pair from the update, 64 rows and 256 columns of the wide form to a CTA.
+// X's pair from the update, 64 rows and split_cols columns of the wide form to a CTA.
 // A tall matrix goes through shared memory, 64 x 64 elements at a time, so
 // that both sides' rows are contiguous.  Columns up to the pitch are written,
 // as zeros.
-constexpr int kSplitRows = 64, kSplitCols = 256;
+constexpr int kSplitRows = 64;
 
 template <int kT, bool kMomentum>
 __global__ void __launch_bounds__(kThreads)
@@ -222,7 +223,7 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
     *reinterpret_cast<uint4*>(high + at) = h;
     *reinterpret_cast<uint4*>(low + at) = l;
   };
-  for (int c0 = blockIdx.x * kSplitCols, c1 = c0 + kSplitCols; c0 < c1; c0 += 64) {
+  for (int c0 = blockIdx.x * a.split_cols, c1 = c0 + a.split_cols; c0 < c1; c0 += 64) {
     const int sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0, rows = tall ? a.n : a.m;
 #pragma unroll
     for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
@@ -285,10 +286,14 @@ enum Mode { kGram, kPoly, kApply, kFinal };
 struct ProductArgs {
   CUtensorMap p, q;      // planes of the two operands
   CUtensorMap add, out;  // planes that alpha multiplies, and the result's, in boxes of 32 x 32
+  const __half* add_at;  // the same planes' addresses
+  __half* out_at;
   int m, n, pitch;       // the result's
   int kblocks;
   int passes;            // 3, or 1: the high parts alone
   int tiles_m, tiles_n, tiles, items;
+  int whole;             // the first items; the others are halves of a tile
+  int split;             // CTAs that divide the summed axis, of small products
   float alpha, beta;     // result = alpha add + beta product
 };
 
@@ -338,18 +343,25 @@ struct Tile {
   bool mirror;  // also stored transposed
 };
 // Symmetric results: the tiles that reach the diagonal or lie below it, row
-// by row, kBM / kBN more in each row of tiles than in the one before.
-template <int kBN, bool kSymmetric>
+// by row, kRows / kCols more in each row of tiles than in the one before.
+template <int kRows, int kCols, bool kSymmetric>
 __device__ __forceinline__ Tile tile_of(const ProductArgs& a, int item) {
   const int z = item / a.tiles, t = item - z * a.tiles;
-  if constexpr (!kSymmetric) return Tile{z, t / a.tiles_n * kBM, t % a.tiles_n * kBN, false};
-  constexpr int kPer = kBM / kBN;
+  if constexpr (!kSymmetric) {
+    // eight rows of tiles at a time, down their columns: what the device works
+    // on together has few rows and columns
+    constexpr int kTogether = 8;
+    const int strip = t / (kTogether * a.tiles_n), i0 = strip * kTogether, in = a.tiles_m - i0 < kTogether ? a.tiles_m - i0 : kTogether;
+    const int u = t - i0 * a.tiles_n;
+    return Tile{z, (i0 + u % in) * kRows, u / in * kCols, false};
+  }
+  constexpr int kPer = kRows / kCols;
   // rows of tiles before row i hold kPer i (i + 1) / 2
   int i = static_cast<int>((sqrtf(8.0f * (t / kPer) + 1.0f) - 1.0f) * 0.5f);
   while (kPer * (i + 1) * (i + 2) / 2 <= t) ++i;
   while (kPer * i * (i + 1) / 2 > t) --i;
   const int j = t - kPer * i * (i + 1) / 2;
-  return Tile{z, i * kBM, j * kBN, j < kPer * i};
+  return Tile{z, i * kRows, j * kCols, j < kPer * i};
 }
 
 __device__ __forceinline__ float half_at(const uint4& w, int j) {
@@ -372,6 +384,18 @@ __device__ __forceinline__ int chunk_end(const ProductArgs& a, int k) {
   if (!kSum) return all;
   if (k < small) return small;
   return k + kChunk < all ? k + kChunk : all;
+}
+
+// What a pair works on: a tile, or half of its columns.  A last wave that less
+// than half fills the device is cut into halves, which take half as long.
+template <int kBN, bool kSymmetric>
+__device__ __forceinline__ Tile item_of(const ProductArgs& a, int i, int* cols) {
+  *cols = kBN;
+  if (kBN == 128 || i < a.whole) return tile_of<kBM, kBN, kSymmetric>(a, i);
+  Tile t = tile_of<kBM, kBN, kSymmetric>(a, a.whole + (i - a.whole) / 2);
+  t.n0 += (i - a.whole) % 2 * 128;
+  *cols = 128;
+  return t;
 }
 
 // kT and kUpdate: of the last product, whose result has type kT, or updates a
@@ -417,8 +441,10 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     Ring<kStages> ring;
     bool ok = true;
     for (int t = first; ok && t < a.items; t += pairs) {
-      const Tile tile = tile_of<kBN, kSymmetric>(a, t);
-      const int m0 = tile.m0 + static_cast<int>(rank) * (kBM / 2), n0 = tile.n0 + static_cast<int>(rank) * (kBN / 2);
+      int cols;
+      const Tile tile = item_of<kBN, kSymmetric>(a, t, &cols);
+      // of a half, the copies of Q bring as many lines as of a whole
+      const int m0 = tile.m0 + static_cast<int>(rank) * (kBM / 2), n0 = tile.n0 + static_cast<int>(rank) * (cols / 2);
       for (int pass = 3 - a.passes; ok && pass < 3; ++pass) {
         const int zp = 2 * tile.z + (pass == 1), zq = 2 * tile.z + (pass == 0);
         for (int kb = 0; kb < a.kblocks; ++kb, ring.next()) {
@@ -444,7 +470,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     if (rank == 0) {
       const bool one = elect_one();
       // f16 x f16, fp32 accumulators; bit 16: q's lines are contiguous
-      const uint32_t idesc = (1u << 4) | (kTrans ? 1u << 16 : 0u) | ((kBN / 8) << 17) | ((kBM / 16) << 24);
+      const uint32_t idesc_of = (1u << 4) | (kTrans ? 1u << 16 : 0u) | ((kBM / 16) << 24);
       const uint64_t dp0 = smem_desc(smem_u32(sm), 16, 1024, 2);
       const uint64_t dq0 = kTrans ? smem_desc(smem_u32(sm + kABytes), kBK * 128, 1024, 2) : smem_desc(smem_u32(sm + kABytes), 16, 1024, 2);
       constexpr uint32_t kStepP = 32 / 16, kStepQ = kTrans ? 2048 / 16 : 32 / 16;  // 16 of the summed axis
@@ -452,7 +478,8 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       int use = 0;
       bool ok = true;
       const int blocks = a.passes * a.kblocks;
-      for (int t = first; ok && t < a.items; t += pairs)
+      for (int t = first; ok && t < a.items; t += pairs) {
+        const uint32_t idesc = idesc_of | ((kBN == 128 || t < a.whole ? kBN / 8 : 128 / 8) << 17);
         for (int k0 = 0, k1; ok && k0 < blocks; k0 = k1, ++use) {
           k1 = chunk_end<kSum>(a, k0);
           const int buf = use & 1;
@@ -477,6 +504,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
           if (one) commit_pair(&s_acc_full[buf]);
           __syncwarp();
         }
+      }
     }
   } else {
     wait_for_inputs();
@@ -517,10 +545,11 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       __syncwarp();
     };
     for (int t = first; ok && t < a.items; t += pairs) {
-      const Tile tile = tile_of<kBN, kSymmetric>(a, t);
+      int cols;
+      const Tile tile = item_of<kBN, kSymmetric>(a, t, &cols);
       const int row0 = tile.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, row = row0 + lane, col0 = tile.n0 + own_col;
       // (what lies past the matrix is not there to copy or to store)
-      const bool some = row0 < a.m;
+      const bool some = row0 < a.m && own_col < cols;
       const auto fetch = [&](int col) {
         if (!kAdd || !some || col >= a.pitch) return;
         wait_stored();
@@ -661,6 +690,233 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
 }
 
 // --------------------------------------------------------------------------
+// the products of small matrices
+//
+// Where the tiles above are too few for the device, what takes the time is
+// latency: launch, first copy, each stage in turn, the store.  Here a tile is
+// 128 x 64, and a cluster of `split` CTAs divides the summed axis, so that a
+// CTA has a stage or two.  A stage holds both parts of both operands, 48 KB,
+// for twelve instructions.  The low parts' products and every 256 of high x
+// high have accumulators of their own; a thread adds them up, sends each unit
+// of 8 columns to the CTA that gathers it over distributed shared memory, and
+// that one adds the cluster's parts in the order of the ranks.
+constexpr int kSmallRows = 128, kSmallCols = 64, kSmallStages = 4;
+constexpr int kSmallThreads = 320;  // warp 0 copies, warp 1 issues, eight add up and store
+constexpr int kSmallP = kSmallRows * kBK * 2, kSmallQ = kSmallCols * kBK * 2, kSmallStage = 2 * (kSmallP + kSmallQ);
+constexpr int kSmallSmem = 1024 + kSmallStages * kSmallStage;
+constexpr int kSmallAccs = static_cast<int>(kTmemCols) / kSmallCols - 1;  // of high x high
+constexpr int kMaxSplit = 8;
+constexpr int kUnit = 8, kUnits = kSmallCols / kUnit;  // columns that move together
+static_assert((kUnits + kMaxSplit - 1) * kSmallRows * kUnit * 4 <= kSmallStages * kSmallStage, "the gathered parts take the stages' place");
+
+// Eight neighbouring columns of this thread's row, of both planes.
+struct Pair8 {
+  uint4 h, l;
+};
+
+template <int kMode, int kT, bool kUpdate>
+__global__ void __launch_bounds__(kSmallThreads, 1)
+ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
+  constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
+  constexpr bool kTrans = kMode == kApply || kMode == kFinal;  // q's summed axis is its rows
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  float* const parts = reinterpret_cast<float*>(sm);  // [rank][unit of the share][row][8], once the stages are done with
+  __shared__ __align__(8) uint64_t s_full[kSmallStages], s_empty[kSmallStages], s_done;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_fail;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  uint32_t rank;
+  asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
+  const Tile tile = tile_of<kSmallRows, kSmallCols, kSymmetric>(a, static_cast<int>(blockIdx.x) / a.split);
+  const int kb0 = a.kblocks * static_cast<int>(rank) / a.split, count = a.kblocks * (static_cast<int>(rank) + 1) / a.split - kb0;
+  const int least = (count + kSmallAccs - 1) / kSmallAccs, chunk = least > kChunk ? least : kChunk;
+  const int accs = (count + chunk - 1) / chunk;
+  const bool pairs = a.passes == 3;
+  if (threadIdx.x == 0) {
+    prefetch_map(&a.p);
+    prefetch_map(&a.q);
+    s_fail = 0;
+    for (int i = 0; i < kSmallStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+    mbar_init(&s_done, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  wait_for_inputs();
+  let_next_begin();
+
+  const int quarter = warp & 3, half = (warp - 2) / 4, row = quarter * 32 + lane, r = tile.m0 + row;
+  const uint32_t share = (kUnits + a.split - 1) / a.split;
+  const int64_t plane = static_cast<int64_t>(a.m) * a.pitch;
+  // this thread's units of its CTA's share: the half-th and every second from there
+  constexpr int kMine = kUnits / 2;
+  const auto unit_col = [&](uint32_t u) { return tile.n0 + static_cast<int>(rank * share + u) * kUnit; };
+  const auto unit_in = [&](uint32_t u) { return u < share && rank * share + u < kUnits && r < a.m && unit_col(u) < a.pitch; };
+  Pair8 add[kAdd ? kMine : 1];
+  if (warp == 0) {
+    const bool one = elect_one();
+    Ring<kSmallStages> ring;
+    for (int i = 0; i < count; ++i, ring.next()) {
+      if (!mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail)) break;
+      if (one) {
+        const int k = (kb0 + i) * kBK;
+        uint64_t* const bar = &s_full[ring.s];
+        uint8_t* const p = sm + ring.s * kSmallStage;
+        mbar_expect_tx(bar, pairs ? kSmallStage : kSmallP + kSmallQ);
+        for (int h = 0; h < (pairs ? 2 : 1); ++h) {
+          tma_load3_one(p + h * kSmallP, &a.p, k, tile.m0, 2 * tile.z + h, bar);
+          tma_load3_one(p + 2 * kSmallP + h * kSmallQ, &a.q, kTrans ? tile.n0 : k, kTrans ? k : tile.n0, 2 * tile.z + h, bar);
+        }
+      }
+      __syncwarp();
+    }
+  } else if (warp == 1) {
+    const bool one = elect_one();
+    const uint32_t idesc = (1u << 4) | (kTrans ? 1u << 16 : 0u) | ((kSmallCols / 8) << 17) | ((kSmallRows / 16) << 24);
+    const uint64_t dp0 = smem_desc(smem_u32(sm), 16, 1024, 2), dq0 = smem_desc(smem_u32(sm + 2 * kSmallP), kTrans ? kBK * 128 : 16, 1024, 2);
+    constexpr uint32_t kStepP = 32 / 16, kStepQ = kTrans ? 2048 / 16 : 32 / 16;
+    Ring<kSmallStages> ring;
+    for (int i = 0; i < count; ++i, ring.next()) {
+      if (!mbar_wait(&s_full[ring.s], ring.phase, &s_fail)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (one) {
+        const uint64_t dp = dp0 + static_cast<uint32_t>(ring.s * (kSmallStage / 16)), dq = dq0 + static_cast<uint32_t>(ring.s * (kSmallStage / 16));
+        const auto issue = [&](uint32_t acc, uint64_t p, uint64_t q, bool fresh) {
+#pragma unroll
+          for (uint32_t s = 0; s < 4; ++s)
+            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+                         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
+                         ::"r"(acc), "l"(p + s * kStepP), "l"(q + s * kStepQ), "r"(idesc), "r"(static_cast<uint32_t>(!fresh || s != 0)) : "memory");
+        };
+        if (pairs) {
+          issue(tmem, dp + kSmallP / 16, dq, i == 0);
+          issue(tmem, dp, dq + kSmallQ / 16, false);
+        }
+        issue(tmem + kSmallCols * (1 + i / chunk), dp, dq, i % chunk == 0);
+        commit_one(&s_empty[ring.s]);
+      }
+      __syncwarp();
+    }
+    if (one) commit_one(&s_done);
+  } else if constexpr (kAdd) {
+    // under way while the products are
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const uint32_t u = 2 * i + half;
+      if (!unit_in(u)) continue;
+      const __half* const from = a.add_at + 2 * tile.z * plane + static_cast<int64_t>(r) * a.pitch + unit_col(u);
+      add[i] = Pair8{__ldg(reinterpret_cast<const uint4*>(from)), __ldg(reinterpret_cast<const uint4*>(from + plane))};
+    }
+  }
+  __syncwarp();
+  bool ok = true;
+  if (warp >= 2) {
+    ok = __all_sync(0xffffffffu, mbar_wait(&s_done, 0, &s_fail));
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  }
+  if (s_fail && lane == 0 && warp < 2) let_copies_land();
+  __syncwarp();
+  cluster_sync();  // every CTA is done with its stages: the parts may take their place
+  if (warp >= 2) {
+#pragma unroll
+    for (int c = 0; c < kSmallCols; c += 32) {
+      const int c0 = c + 16 * half;  // the two halves' warps take turns at 16 columns
+      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
+      float sum[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
+      for (int i = pairs ? 0 : 1; i <= accs && count > 0; ++i) {
+        float v[16];
+        tmem_load16(from + i * kSmallCols, v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sum[j] = __fadd_rn(sum[j], v[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; j += kUnit) {
+        const uint32_t unit = (c0 + j) / kUnit, to = unit / share, at = ((rank * share + unit - to * share) * kSmallRows + row) * kUnit;
+        uint32_t dst;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + at)), "r"(to));
+#pragma unroll
+        for (int q = 0; q < kUnit; q += 4)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
+                       ::"r"(dst + 4 * q), "f"(sum[j + q]), "f"(sum[j + q + 1]), "f"(sum[j + q + 2]), "f"(sum[j + q + 3]) : "memory");
+      }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp >= 2 && ok) {
+    bool writes = true;
+    if constexpr (kMode == kFinal && kUpdate) writes = finite(f.grad_scale ? *f.grad_scale : 1.0f);
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const uint32_t u = 2 * i + half;
+      // rows past the matrix hold zeros, which a mirrored tile's pad needs
+      const bool pad = kSymmetric && tile.mirror && u < share && rank * share + u < kUnits && r >= a.m && r < a.pitch && unit_col(u) < a.pitch;
+      if (!unit_in(u) && !pad) continue;
+      const int col = unit_col(u);
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      for (int q = 0; q < a.split; ++q) {
+        const float4* const from = reinterpret_cast<const float4*>(parts + ((q * share + u) * kSmallRows + row) * kUnit);
+        const float4 x = from[0], y = from[1];
+        v[0] = __fadd_rn(v[0], x.x); v[1] = __fadd_rn(v[1], x.y); v[2] = __fadd_rn(v[2], x.z); v[3] = __fadd_rn(v[3], x.w);
+        v[4] = __fadd_rn(v[4], y.x); v[5] = __fadd_rn(v[5], y.y); v[6] = __fadd_rn(v[6], y.z); v[7] = __fadd_rn(v[7], y.w);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = __fmul_rn(a.beta, v[j]);
+        if constexpr (kAdd) v[j] = pad ? 0.0f : __fmaf_rn(a.alpha, __fadd_rn(half_at(add[i].h, j), half_at(add[i].l, j)), v[j]);
+      }
+      if constexpr (kMode != kFinal) {
+        Pair8 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split2(v[2 * j], v[2 * j + 1], (&o.h.x)[j], (&o.l.x)[j]);
+        __half* const base = a.out_at + 2 * tile.z * plane;
+        if (!pad) {
+          __half* const to = base + static_cast<int64_t>(r) * a.pitch + col;
+          *reinterpret_cast<uint4*>(to) = o.h;
+          *reinterpret_cast<uint4*>(to + plane) = o.l;
+        }
+        if (kSymmetric && tile.mirror && r < a.pitch) {
+          uint16_t* to = reinterpret_cast<uint16_t*>(base) + static_cast<int64_t>(col) * a.pitch + r;
+#pragma unroll
+          for (int j = 0; j < 8; ++j, to += a.pitch) {
+            to[0] = static_cast<uint16_t>(j % 2 ? (&o.h.x)[j / 2] >> 16 : (&o.h.x)[j / 2] & 0xffffu);
+            to[plane] = static_cast<uint16_t>(j % 2 ? (&o.l.x)[j / 2] >> 16 : (&o.l.x)[j / 2] & 0xffffu);
+          }
+        }
+      } else if (writes) {
+        const bool tall = f.x.tall[tile.z];
+        const int64_t at = tall ? static_cast<int64_t>(col) * a.m + r : static_cast<int64_t>(r) * a.n + col, step = tall ? a.m : 1;
+        void* const out = f.x.out[tile.z];
+        if constexpr (kUpdate) {
+          float p[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) p[j] = col + j < a.n ? load1<kT>(out, at + j * step) : 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(-f.step, v[j], __fmul_rn(p[j], f.decay));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j < a.n) store1<kT>(out, at + j * step, v[j]);
+      }
+    }
+  }
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// --------------------------------------------------------------------------
 // host side
 
 bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
@@ -692,7 +948,8 @@ constexpr int kMaxDevices = 64;
 struct DeviceState {
   bool ready = false;
   unsigned long long ctx = 0;
-  int pairs = 0;
+  int pairs = 0;  // CTA pairs that are resident at a time
+  int clusters[kMaxSplit + 1] = {};  // clusters of so many CTAs of the small products'
 };
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -715,7 +972,19 @@ cudaError_t opt_in_all() {
   return cudaSuccess;
 }
 
-bwd_status ensure_device(int* pairs) {
+template <int kMode, int kT, bool kUpdate>
+cudaError_t opt_in_small() { return opt_in(ns_small_kernel<kMode, kT, kUpdate>, kSmallSmem); }
+
+cudaError_t opt_in_all_small() {
+  const cudaError_t e[] = {opt_in_small<kGram, kF32, false>(), opt_in_small<kPoly, kF32, false>(), opt_in_small<kApply, kF32, false>(),
+                           opt_in_small<kFinal, kF32, false>(), opt_in_small<kFinal, kBF16, false>(), opt_in_small<kFinal, kF16, false>(),
+                           opt_in_small<kFinal, kF32, true>(), opt_in_small<kFinal, kBF16, true>(), opt_in_small<kFinal, kF16, true>()};
+  for (const cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+bwd_status ensure_device(DeviceState* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -730,6 +999,7 @@ bwd_status ensure_device(int* pairs) {
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess) e = opt_in_all<256>();
     if (e == cudaSuccess) e = opt_in_all<128>();
+    if (e == cudaSuccess) e = opt_in_all_small();
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(sms / 2 * 2));
@@ -743,10 +1013,19 @@ bwd_status ensure_device(int* pairs) {
     e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of<256, kApply, kF16, false>(), &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
     if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
+    cfg.blockDim = dim3(kSmallThreads);
+    cfg.dynamicSmemBytes = kSmallSmem;
+    d.clusters[1] = sms;
+    for (int c = 2; c <= kMaxSplit; ++c) {
+      cfg.gridDim = dim3(static_cast<unsigned>(sms / c * c));
+      attr[0].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[c], ns_small_kernel<kApply, kF32, false>, &cfg);
+      if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+    }
     d.ctx = ctx;
     d.ready = true;
   }
-  *pairs = d.pairs;
+  *out = d;
   return BWD_OK;
 }
 
@@ -774,10 +1053,10 @@ struct Step {
   bwd_dtype g_type, out_type;
 };
 
-// Tiles of a product with kBN columns each.
-int64_t tiles_of(const Shape& result, int bn, bool symmetric) {
-  const int64_t tm = (result.m + kBM - 1) / kBM;
-  return symmetric ? kBM / bn * tm * (tm + 1) / 2 : tm * ((result.n + bn - 1) / bn);
+// Tiles of a product, of so many rows and columns each.
+int64_t tiles_of(const Shape& result, int rows, int cols, bool symmetric) {
+  const int64_t tm = (result.m + rows - 1) / rows;
+  return symmetric ? rows / cols * tm * (tm + 1) / 2 : tm * ((result.n + cols - 1) / cols);
 }
 
 template <int kBN, int kMode>
@@ -797,37 +1076,80 @@ bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& 
   }
 }
 
+template <int kMode>
+bwd_status launch_small(const ProductArgs& a, const FinalArgs* f, const Step& st, cudaStream_t stream) {
+  const auto go = [&](auto kernel, const auto& last) {
+    return launch_ex(kernel, dim3(static_cast<unsigned>(a.items * a.split)), kSmallThreads, a.split, kSmallSmem, stream,
+                     "ns_small_kernel launch", a, last);
+  };
+  if constexpr (kMode != kFinal) {
+    return go(ns_small_kernel<kMode, kF32, false>, 0);
+  } else if (st.update) {
+    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, true>, *f);
+    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, true>, *f) : go(ns_small_kernel<kMode, kF16, true>, *f);
+  } else {
+    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, false>, *f);
+    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, false>, *f) : go(ns_small_kernel<kMode, kF16, false>, *f);
+  }
+}
+
 // result = alpha add + beta P Q^T (or P Q), `count` matrices.
 template <int kMode>
 bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* p, const __half* q, const __half* add, __half* out,
-                   float alpha, float beta, int passes, const FinalArgs* f, const Step& st, int pairs, cudaStream_t stream) {
+                   float alpha, float beta, int passes, const FinalArgs* f, const Step& st, const DeviceState& d, cudaStream_t stream) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
-  const auto waves = [&](int bn) { return (count * tiles_of(result, bn, kSymmetric) + pairs - 1) / pairs; };
+  const auto waves = [&](int bn) { return (count * tiles_of(result, kBM, bn, kSymmetric) + d.pairs - 1) / d.pairs; };
+  const int64_t kblocks = (k + kBK - 1) / kBK, small = count * tiles_of(result, kSmallRows, kSmallCols, kSymmetric);
+  int64_t split = kblocks < kMaxSplit ? kblocks : kMaxSplit;
+  while (split > 1 && small > d.clusters[split]) --split;
+  // Small tiles where they take less time than the large ones.  In us: a stage
+  // of a small tile 0.2, and 0.5 where all SMs read (48 KB each, 14.6 TB/s from
+  // L2); of a large one, a third of that work for four or eight times the tile,
+  // 0.24 with 128 columns and 0.36 with 256; beside its stages a wave of small
+  // tiles takes some 5, a launch of large ones 8.  (777 x 301 and five such:
+  // 159 us with large tiles, 119 with small ones; A of 4096 x 11008, 1,056
+  // small tiles, 600 us against 342 the other way.)
+  const int64_t at_once = d.clusters[split] * split, small_waves = (small * split + at_once - 1) / at_once;
+  const double full = std::min(1.0, static_cast<double>(small * split) / static_cast<double>(at_once));
+  const double stage = (0.2 + 0.3 * full) * (passes == 3 ? 1.0 : 0.5);
+  const double small_time = static_cast<double>(small_waves) * (5.0 + stage * static_cast<double>((kblocks + split - 1) / split));
+  const double large_time = 8.0 + std::min(0.24 * static_cast<double>(waves(128)), 0.36 * static_cast<double>(waves(256))) *
+                                      static_cast<double>(passes * kblocks);
+  const bool is_small = small_time < large_time;
   // a tile of 256 columns takes up to one and a half times as long as one of 128
-  const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
+  const int rows = is_small ? kSmallRows : kBM, bn = is_small ? kSmallCols : 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   ProductArgs a{};
+  a.add_at = add; a.out_at = out;
   a.m = static_cast<int>(result.m); a.n = static_cast<int>(result.n); a.pitch = static_cast<int>(up(result.n, 64));
-  a.kblocks = static_cast<int>((k + kBK - 1) / kBK);
+  a.kblocks = static_cast<int>(kblocks);
   a.passes = passes;
-  a.tiles_m = static_cast<int>((result.m + kBM - 1) / kBM); a.tiles_n = static_cast<int>((result.n + bn - 1) / bn);
-  const int64_t tiles = tiles_of(result, bn, kSymmetric);
+  a.split = static_cast<int>(split);
+  a.tiles_m = static_cast<int>((result.m + rows - 1) / rows); a.tiles_n = static_cast<int>((result.n + bn - 1) / bn);
+  const int64_t tiles = tiles_of(result, rows, bn, kSymmetric);
   if (tiles * count > 0x3fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
   a.tiles = static_cast<int>(tiles); a.items = static_cast<int>(tiles * count);
+  const int64_t last = a.items % d.pairs;
+  const bool halves = !is_small && bn == 256 && 2 * last <= d.pairs;
+  a.whole = static_cast<int>(halves ? a.items - last : a.items);
+  a.items += a.items - a.whole;
   a.alpha = alpha; a.beta = beta;
-  // P: `m` lines along k; Q: its lines along k, or its rows along the result's columns
-  bwd_status s = plane_map(&a.p, p, result.m, up(k, 64), 2 * count, kBK, kBM / 2);
+  // P: `m` lines along k; Q: its lines along k, or its rows along the result's
+  // columns.  Of a pair's tile each CTA copies half of Q's lines.
+  const int lines_p = is_small ? rows : rows / 2, lines_q = is_small ? bn : bn / 2;
+  bwd_status s = plane_map(&a.p, p, result.m, up(k, 64), 2 * count, kBK, lines_p);
   if (s != BWD_OK) return s;
-  s = kSymmetric ? plane_map(&a.q, q, result.m, up(k, 64), 2 * count, kBK, bn / 2) : plane_map(&a.q, q, k, up(result.n, 64), 2 * count, 64, kBK);
-  if (s == BWD_OK && add) s = plane_map(&a.add, add, result.m, a.pitch, 2 * count, 32, 32);
-  if (s == BWD_OK && out) s = plane_map(&a.out, out, result.m, a.pitch, 2 * count, 32, 32);
+  s = kSymmetric ? plane_map(&a.q, q, result.m, up(k, 64), 2 * count, kBK, lines_q) : plane_map(&a.q, q, k, up(result.n, 64), 2 * count, 64, kBK);
+  if (s == BWD_OK && add && !is_small) s = plane_map(&a.add, add, result.m, a.pitch, 2 * count, 32, 32);
+  if (s == BWD_OK && out && !is_small) s = plane_map(&a.out, out, result.m, a.pitch, 2 * count, 32, 32);
   if (s != BWD_OK) return s;
-  return bn == 256 ? launch_product<256, kMode>(a, f, st, pairs, stream) : launch_product<128, kMode>(a, f, st, pairs, stream);
+  if (is_small) return launch_small<kMode>(a, f, st, stream);
+  return bn == 256 ? launch_product<256, kMode>(a, f, st, d.pairs, stream) : launch_product<128, kMode>(a, f, st, d.pairs, stream);
 }
 
 template <bool kMomentum>
 bwd_status prepare(const PrepareArgs& a, int64_t count, int type, cudaStream_t st) {
   const dim3 by_chunk(static_cast<unsigned>(a.chunks), static_cast<unsigned>(count));
-  const dim3 by_tile(static_cast<unsigned>((a.pitch + kSplitCols - 1) / kSplitCols),
+  const dim3 by_tile(static_cast<unsigned>((a.pitch + a.split_cols - 1) / a.split_cols),
                      static_cast<unsigned>((a.m + kSplitRows - 1) / kSplitRows), static_cast<unsigned>(count));
   const auto go = [&](auto norm, auto split) {
     const bwd_status s = launch_ex(norm, by_chunk, kThreads, 0, 0, st, "ns_norm_kernel launch", a);
@@ -839,7 +1161,7 @@ bwd_status prepare(const PrepareArgs& a, int64_t count, int type, cudaStream_t s
 }
 
 // All of one batch: matrices of one shape, in either orientation.
-bwd_status run_batch(const Matrices& x, int64_t count, const Shape& s, const Step& st, uint8_t* work, int pairs, cudaStream_t stream) {
+bwd_status run_batch(const Matrices& x, int64_t count, const Shape& s, const Step& st, uint8_t* work, const DeviceState& d, cudaStream_t stream) {
   Pieces pieces{work};
   double* const slots = reinterpret_cast<double*>(pieces.take(8 * kSlots * count));
   __half* xs[2] = {reinterpret_cast<__half*>(pieces.take(s.x_bytes() * count)), reinterpret_cast<__half*>(pieces.take(s.x_bytes() * count))};
@@ -852,6 +1174,8 @@ bwd_status run_batch(const Matrices& x, int64_t count, const Shape& s, const Ste
   a.chunk = up((a.size + kSlots - 1) / kSlots, 8 * kThreads);
   a.chunks = static_cast<int>((a.size + a.chunk - 1) / a.chunk);
   a.m = static_cast<int>(s.m); a.n = static_cast<int>(s.n); a.pitch = static_cast<int>(up(s.n, 64));
+  // each CTA adds up the norm's parts: four tiles share that where there are many
+  a.split_cols = count * ((s.m + 63) / 64) * ((s.n + 63) / 64) > 2048 ? 256 : 64;
   a.momentum = st.momentum; a.nesterov = st.nesterov;
   bwd_status e = st.has_momentum ? prepare<true>(a, count, st.g_type, stream) : prepare<false>(a, count, st.g_type, stream);
   f.x = x; f.grad_scale = st.grad_scale; f.decay = st.decay;
@@ -861,12 +1185,12 @@ bwd_status run_batch(const Matrices& x, int64_t count, const Shape& s, const Ste
     const bool last = i + 1 == st.steps;
     const int passes = last && st.out_type == BWD_BF16 ? 1 : 3;
     const __half* const from = xs[i % 2];
-    e = product<kGram>(square, s.n, count, from, from, nullptr, gram, 0.0f, 1.0f / kScale, passes, nullptr, st, pairs, stream);
+    e = product<kGram>(square, s.n, count, from, from, nullptr, gram, 0.0f, 1.0f / kScale, passes, nullptr, st, d, stream);
     if (e == BWD_OK)
-      e = product<kPoly>(square, s.m, count, gram, gram, gram, poly, kB, kC / kScale, passes, nullptr, st, pairs, stream);
+      e = product<kPoly>(square, s.m, count, gram, gram, gram, poly, kB, kC / kScale, passes, nullptr, st, d, stream);
     if (e != BWD_OK) break;
-    e = last ? product<kFinal>(s, s.m, count, poly, from, from, nullptr, kA / kScale, 1.0f / (kScale * kScale), passes, &f, st, pairs, stream)
-             : product<kApply>(s, s.m, count, poly, from, from, xs[(i + 1) % 2], kA, 1.0f / kScale, passes, nullptr, st, pairs, stream);
+    e = last ? product<kFinal>(s, s.m, count, poly, from, from, nullptr, kA / kScale, 1.0f / (kScale * kScale), passes, &f, st, d, stream)
+             : product<kApply>(s, s.m, count, poly, from, from, xs[(i + 1) % 2], kA, 1.0f / kScale, passes, nullptr, st, d, stream);
   }
   return e;
 }
@@ -917,8 +1241,8 @@ bwd_status run(int32_t count, const void* const* g, float* const* mom, void* con
       return fail(BWD_ERR_INVALID_ARG, "matrix %d: pointer not aligned to its element size", i);
   }
   if (!work || !aligned_to(work, 256)) return fail(BWD_ERR_INVALID_ARG, "work must be 256-byte aligned");
-  int pairs = 0;
-  if ((s = ensure_device(&pairs)) != BWD_OK) return s;
+  DeviceState d;
+  if ((s = ensure_device(&d)) != BWD_OK) return s;
   static thread_local Matrices x;
   return each_group(at, rows, cols, [&](size_t first, int64_t number, const Shape& shape) {
     const int64_t batch = batch_of(shape, number);
@@ -931,7 +1255,7 @@ bwd_status run(int32_t count, const void* const* g, float* const* mom, void* con
         x.out[z] = out[i];
         x.tall[z] = rows[i] > cols[i];
       }
-      const bwd_status e = run_batch(x, n, shape, st, static_cast<uint8_t*>(work), pairs, static_cast<cudaStream_t>(stream));
+      const bwd_status e = run_batch(x, n, shape, st, static_cast<uint8_t*>(work), d, static_cast<cudaStream_t>(stream));
       if (e != BWD_OK) return e;
     }
     return BWD_OK;

@@ -115,16 +115,18 @@ def test_larger(muon, shape):
 
 
 def test_batches(muon):
-    """More matrices than one launch takes, the same as each by itself."""
+    """More matrices than one launch takes.  (How a sum is divided depends on
+    how many there are, and with it a result's last bits.)"""
     g = torch.stack([draw(40, 70, i, "strong") for i in range(140)]).view(2, 70, 40, 70)
     out = muon.orthogonalize(g)
     assert out.shape == g.shape
     for i, j in [(0, 0), (0, 63), (0, 64), (1, 0), (1, 69)]:
-        assert torch.equal(out[i, j], muon.orthogonalize(g[i, j]))
+        check(out[i, j], g[i, j])
+    assert torch.equal(muon.orthogonalize(g), out)
     # a transposed view, and one that starts off every boundary
     flat = torch.zeros(40 * 70 + 1, device=DEV)
     flat[1:] = g[0, 0].reshape(-1)
-    assert torch.equal(muon.orthogonalize(flat[1:].view(40, 70)), out[0, 0])
+    assert torch.equal(muon.orthogonalize(flat[1:].view(40, 70)), muon.orthogonalize(g[0, 0]))
     check(muon.orthogonalize(g[0, 0].t()), g[0, 0].t())
 
 
