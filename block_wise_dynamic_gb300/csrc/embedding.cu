@@ -816,7 +816,7 @@ bwd_status bwd_check_device(void* stream) {
   if ((e = cudaMemcpyFromSymbol(&fault, g_embed_fault, sizeof fault)) != cudaSuccess)
     return cuda_fail(e, "cudaMemcpyFromSymbol(fault word)");
   unsigned int product_fault = 0;
-  for (const auto take : {bwd::host::take_fp8_fault, bwd::host::take_fp4_fault, bwd::host::take_muon_fault}) {
+  for (const auto take : {bwd::host::take_fp8_fault, bwd::host::take_fp4_fault, bwd::host::take_norm_fault, bwd::host::take_muon_fault}) {
     unsigned int one = 0;
     const bwd_status s = take(&one);
     if (s != BWD_OK) return s;

@@ -43,10 +43,11 @@ bwd_status advance(StepCount* count, const float* grad_scale, const bwd_adamw_hp
 bwd_status check_hparams(const bwd_adam_hparams* hp);
 bwd_status check_hparams(const bwd_adamw_hparams* hp);
 
-// Read and clear the fault words of the 8-bit and 4-bit products and of the
-// orthogonalised updates (see bwd_check_device).
+// Read and clear the fault words of the 8-bit and 4-bit products, the layer
+// norm and the orthogonalised updates (see bwd_check_device).
 bwd_status take_fp8_fault(unsigned int* fault);
 bwd_status take_fp4_fault(unsigned int* fault);
+bwd_status take_norm_fault(unsigned int* fault);
 bwd_status take_muon_fault(unsigned int* fault);
 
 // Unique id of the current CUDA context (the driver's cuCtxGetId, unique for

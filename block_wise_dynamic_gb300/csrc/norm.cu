@@ -17,6 +17,7 @@
 // on the schedule.
 #include "tensor.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace {
@@ -48,14 +49,34 @@ struct Part {
       u[i] = c < width ? __ldcs(reinterpret_cast<const Unit*>(static_cast<const char*>(row) + static_cast<int64_t>(c) * elem_bytes<kT>())) : Unit{};
     }
   }
+  __device__ __forceinline__ void load_shared(const uint8_t* row, int width, int t, int threads) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) {
+      const int c = (i * threads + t) * kVals;
+      u[i] = c < width ? *reinterpret_cast<const Unit*>(row + c * elem_bytes<kT>()) : Unit{};
+    }
+  }
+  // 32-bit word k of unit i
+  __device__ __forceinline__ uint32_t word(int i, int k) const {
+    if constexpr (sizeof(Unit) <= 4) return u[i];
+    else return (&u[i].x)[k];
+  }
   __device__ __forceinline__ float value(int i, int j) const {
-    const char* const at = reinterpret_cast<const char*>(&u[i]);
     if constexpr (kT == kF32) {
-      return reinterpret_cast<const float*>(at)[j];
+      return __uint_as_float(word(i, j));
     } else {
-      const unsigned short h = reinterpret_cast<const unsigned short*>(at)[j];
-      if constexpr (kT == kBF16) return __uint_as_float(static_cast<uint32_t>(h) << 16);
-      else return __half2float(__ushort_as_half(h));
+      const uint32_t w = word(i, j / 2);
+      if constexpr (kT == kBF16) return __uint_as_float(j % 2 ? w & 0xffff0000u : w << 16);
+      else return __half2float(__ushort_as_half(static_cast<unsigned short>(j % 2 ? w >> 16 : w & 0xffffu)));
+    }
+  }
+  // values 2 k and 2 k + 1
+  __device__ __forceinline__ float2 two(int i, int k) const {
+    if constexpr (kT == kF16) {
+      const uint32_t w = word(i, k);
+      return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    } else {
+      return make_float2(value(i, 2 * k), value(i, 2 * k + 1));
     }
   }
 };
@@ -140,10 +161,11 @@ norm_forward_kernel(const ForwardArgs a) {
   const int64_t groups = kWarp ? static_cast<int64_t>(gridDim.x) * kWarps : gridDim.x;
   int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32 : blockIdx.x;
   GroupSum<kWarp, 1> sum{s_red};
+  const auto x_row = [&](int64_t r) { return static_cast<const char*>(a.x) + r * a.ldx * elem_bytes<kT>(); };
   wait_for_inputs();
   let_next_begin();
   Part<kT, kVals> next;
-  if (row < a.rows) next.load(static_cast<const char*>(a.x) + row * a.ldx * elem_bytes<kT>(), a.width, t, threads);
+  if (row < a.rows) next.load(x_row(row), a.width, t, threads);
   float g[kKeep ? kThreadValues : 1], b[kKeep ? kThreadValues : 1];
   if constexpr (kKeep) {
 #pragma unroll
@@ -163,8 +185,7 @@ norm_forward_kernel(const ForwardArgs a) {
     for (int i = 0; i < kUnits; ++i)
 #pragma unroll
       for (int j = 0; j < kVals; ++j) s[0] += v[i * kVals + j] = next.value(i, j);
-    if (row + groups < a.rows)
-      next.load(static_cast<const char*>(a.x) + (row + groups) * a.ldx * elem_bytes<kT>(), a.width, t, threads);
+    if (row + groups < a.rows) next.load(x_row(row + groups), a.width, t, threads);
     sum(s);
     const float mean = __fdiv_rn(s[0], width);
     s[0] = 0.0f;
@@ -221,19 +242,22 @@ __global__ void __launch_bounds__(kMax)
 norm_backward_kernel(const BackwardArgs a) {
   constexpr int kUnits = kThreadValues / kVals;
   constexpr bool kKeep = kMax <= kMaxThreads / 2;
-  extern __shared__ float s_sums[];  // [2][width]: of wide rows, or of a CTA's warps
+  extern __shared__ __align__(128) uint8_t s_raw[];
+  float* const s_sums = reinterpret_cast<float*>(s_raw);  // [2][width]: of wide rows, or of a CTA's warps
   __shared__ float s_red[2][2][32];
   const int threads = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int64_t groups = kWarp ? static_cast<int64_t>(gridDim.x) * kWarps : gridDim.x;
   int64_t row = kWarp ? static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32 : blockIdx.x;
   GroupSum<kWarp, 2> sum{s_red};
+  const auto x_row = [&](int64_t r) { return static_cast<const char*>(a.x) + r * a.ldx * elem_bytes<kT>(); };
+  const auto dy_row = [&](int64_t r) { return static_cast<const char*>(a.dy) + r * a.lddy * elem_bytes<kT>(); };
   wait_for_inputs();
   let_next_begin();
   Part<kT, kVals> next_x, next_dy;
   float next_mean = 0.0f, next_rstd = 0.0f;
   const auto fetch = [&](int64_t r) {
-    next_x.load(static_cast<const char*>(a.x) + r * a.ldx * elem_bytes<kT>(), a.width, t, threads);
-    next_dy.load(static_cast<const char*>(a.dy) + r * a.lddy * elem_bytes<kT>(), a.width, t, threads);
+    next_x.load(x_row(r), a.width, t, threads);
+    next_dy.load(dy_row(r), a.width, t, threads);
     next_mean = a.mean[r];
     next_rstd = a.rstd[r];
   };
@@ -262,31 +286,30 @@ norm_backward_kernel(const BackwardArgs a) {
     const float mean = next_mean, rstd = next_rstd;
     if (row + groups < a.rows) fetch(row + groups);
     float s[2] = {0.0f, 0.0f};
-    float h[kThreadValues], xh[kThreadValues];
+    const auto xh_of = [&](int i, int j) { return __fmul_rn(__fsub_rn(x.value(i, j), mean), rstd); };
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
       const int c = (i * threads + t) * kVals;
-      const bool in = c < a.width;
+      if (c >= a.width) continue;
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
         const int e = i * kVals + j;
-        const float d = dy.value(i, j);
-        xh[e] = in ? __fmul_rn(__fsub_rn(x.value(i, j), mean), rstd) : 0.0f;
-        float gamma = 0.0f;
+        const float d = dy.value(i, j), xh = xh_of(i, j);
+        float gamma;
         if constexpr (kKeep) {
           gamma = g[e];
-          dg[e] = __fmaf_rn(d, xh[e], dg[e]);
+          dg[e] = __fmaf_rn(d, xh, dg[e]);
           db[e] = __fadd_rn(db[e], d);
-        } else if (in) {
+        } else {
           gamma = vector_at<kT>(a.gamma, c + j, 1.0f);
           if (a.partial) {
-            s_sums[c + j] = __fmaf_rn(d, xh[e], s_sums[c + j]);
+            s_sums[c + j] = __fmaf_rn(d, xh, s_sums[c + j]);
             s_sums[a.width + c + j] = __fadd_rn(s_sums[a.width + c + j], d);
           }
         }
-        h[e] = __fmul_rn(d, gamma);
-        s[0] += h[e];
-        s[1] = __fmaf_rn(h[e], xh[e], s[1]);
+        const float h = __fmul_rn(d, gamma);
+        s[0] += h;
+        s[1] = __fmaf_rn(h, xh, s[1]);
       }
     }
     if (!a.dx) continue;
@@ -300,8 +323,8 @@ norm_backward_kernel(const BackwardArgs a) {
       float out[kVals];
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
-        const int e = i * kVals + j;
-        out[j] = __fmul_rn(rstd, __fmaf_rn(-xh[e], mean_hx, __fsub_rn(h[e], mean_h)));
+        const float h = __fmul_rn(dy.value(i, j), kKeep ? g[kKeep ? i * kVals + j : 0] : vector_at<kT>(a.gamma, c + j, 1.0f));
+        out[j] = __fmul_rn(rstd, __fmaf_rn(-xh_of(i, j), mean_hx, __fsub_rn(h, mean_h)));
       }
       store_unit<kT, kVals>(dx, c, out);
     }
@@ -343,9 +366,324 @@ norm_backward_kernel(const BackwardArgs a) {
   }
 }
 
-// Sums of the CTAs' rows: eight warps of a CTA each add every eighth of 32
-// columns' rows, in order, and the first then adds the eight.
-constexpr int kSumWarps = 8;
+// --------------------------------------------------------------------------
+// rows of whole 16-byte pieces, many of them
+
+// Two operations in one instruction, each rounded by itself.
+__device__ __forceinline__ uint64_t bits2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 from2(uint64_t a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return from2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+  return from2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return from2(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+//
+// A CTA takes kR rows at a time: what a row costs beside its bytes is the
+// latency of its sums over the CTA, which kR rows share.  Rows come into
+// shared memory by bulk copies, a set of kR ahead, and are read from there by
+// each pass over them; the registers hold gamma, beta and the columns' sums.
+// (16384 x 4096 bf16, forward and backward, with a row at a time in registers:
+// 58 and 97 us; from shared memory, a row at a time, 56 and 100, and these sets
+// with one operation to an instruction 58 and 89, bound by instructions.)
+
+constexpr int kSets = 2;  // of rows, at most one of them being read
+
+template <int kR, int kArrays>
+struct RowRing {
+  uint64_t* bars;
+  uint8_t* rows;  // [kSets][kR][kArrays][row_bytes]
+  int row_bytes;
+  int s = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ const uint8_t* row(int r, int array) const { return rows + ((s * kR + r) * kArrays + array) * row_bytes; }
+  __device__ __forceinline__ void init() {
+    if (threadIdx.x == 0) {
+      for (int i = 0; i < kSets; ++i) mbar_init(&bars[i], 1);
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+  }
+  // By one thread: rows first .. first + count - 1 of each array, `ld` bytes apart.
+  __device__ __forceinline__ void fill(int set, int count, const char* x, int64_t ldx, const char* y, int64_t ldy) {
+    mbar_expect_tx(&bars[set], count * kArrays * row_bytes);
+    for (int r = 0; r < count; ++r) {
+      uint8_t* const to = rows + (set * kR + r) * kArrays * row_bytes;
+      bulk_load(to, x + r * ldx, row_bytes, &bars[set]);
+      if constexpr (kArrays == 2) bulk_load(to + row_bytes, y + r * ldy, row_bytes, &bars[set]);
+    }
+  }
+  // Waits for the current set.  Where a wait gives up, the CTA goes on over
+  // whatever there is, with no wait any more, so that its barriers still meet.
+  __device__ __forceinline__ void wait(volatile int* fail) { mbar_wait(&bars[s], phase, fail); }
+  __device__ __forceinline__ void next() {
+    if (++s == kSets) { s = 0; phase ^= 1u; }
+  }
+};
+
+// Sums of kN values over a CTA, the same in each of its threads; two buffers
+// in turn, as for GroupSum.
+template <int kN>
+__device__ __forceinline__ void cta_sum(float (&s)[kN], float (*red)[32][kN], int& turn) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
+  const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  if (threadIdx.x % 32 == 0)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) red[turn][warp][n] = s[n];
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < kN; ++n) s[n] = 0.0f;
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w)
+#pragma unroll
+    for (int n = 0; n < kN; ++n) s[n] += red[turn][w][n];
+  turn ^= 1;
+}
+
+template <int kT, int kMax, int kR>
+__global__ void __launch_bounds__(kMax)
+norm_forward_ring_kernel(const ForwardArgs a, int row_bytes) {
+  constexpr int kVals = 16 / elem_bytes<kT>(), kUnits = kThreadValues / kVals;
+  constexpr bool kKeep = kMax <= kMaxThreads / 2;
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  __shared__ __align__(8) uint64_t s_bars[kSets];
+  __shared__ __align__(16) float s_red[2][32][kR];
+  __shared__ int s_fail;
+  const int threads = blockDim.x, t = threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kR, ld = a.ldx * elem_bytes<kT>();
+  RowRing<kR, 1> ring{s_bars, s_rows, row_bytes};
+  const auto fill = [&](int set, int64_t r) {
+    if (t == 0 && r < a.rows)
+      ring.fill(set, a.rows - r < kR ? static_cast<int>(a.rows - r) : kR, static_cast<const char*>(a.x) + r * ld, ld, nullptr, 0);
+  };
+  s_fail = 0;
+  ring.init();
+  wait_for_inputs();
+  let_next_begin();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kR;
+  fill(0, row);
+  const auto gamma_at = [&](int c) { return make_float2(vector_at<kT>(a.gamma, c, 1.0f), vector_at<kT>(a.gamma, c + 1, 1.0f)); };
+  const auto beta_at = [&](int c) { return make_float2(vector_at<kT>(a.beta, c, 0.0f), vector_at<kT>(a.beta, c + 1, 0.0f)); };
+  float2 g[kKeep ? kThreadValues / 2 : 1], b[kKeep ? kThreadValues / 2 : 1];
+  if constexpr (kKeep) {
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+      for (int k = 0; k < kVals / 2; ++k) {
+        const int c = (i * threads + t) * kVals, e = i * kVals / 2 + k;
+        g[e] = c < a.width ? gamma_at(c + 2 * k) : both(0.0f);
+        b[e] = c < a.width ? beta_at(c + 2 * k) : both(0.0f);
+      }
+  }
+  const float width = static_cast<float>(a.width);
+  int turn = 0;
+  for (; row < a.rows; row += step) {
+    ring.wait(&s_fail);
+    float mean[kR], s[kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      Part<kT, kVals> x;
+      x.load_shared(ring.row(r, 0), a.width, t, threads);
+      float2 sum = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+        for (int k = 0; k < kVals / 2; ++k) sum = add2(sum, x.two(i, k));
+      s[r] = __fadd_rn(sum.x, sum.y);
+    }
+    cta_sum<kR>(s, s_red, turn);
+    fill(ring.s ^ 1, row + step);  // behind the barrier all threads are done with the set before
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      mean[r] = __fdiv_rn(s[r], width);
+      const float2 less = both(-mean[r]);
+      float2 sum = both(0.0f);
+      Part<kT, kVals> x;
+      x.load_shared(ring.row(r, 0), a.width, t, threads);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        if ((i * threads + t) * kVals >= a.width) continue;
+#pragma unroll
+        for (int k = 0; k < kVals / 2; ++k) {
+          const float2 d = add2(x.two(i, k), less);
+          sum = fma2(d, d, sum);
+        }
+      }
+      s[r] = __fadd_rn(sum.x, sum.y);
+    }
+    cta_sum<kR>(s, s_red, turn);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (row + r >= a.rows) break;
+      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s[r], width), a.eps)));
+      if (t == 0) {
+        if (a.mean) a.mean[row + r] = mean[r];
+        if (a.rstd) a.rstd[row + r] = rstd;
+      }
+      char* const y = static_cast<char*>(a.y) + (row + r) * row_bytes;
+      Part<kT, kVals> x;
+      x.load_shared(ring.row(r, 0), a.width, t, threads);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int c = (i * threads + t) * kVals;
+        if (c >= a.width) continue;
+        float out[kVals];
+#pragma unroll
+        for (int k = 0; k < kVals / 2; ++k) {
+          const int e = i * kVals / 2 + k;
+          const float2 xh = mul2(add2(x.two(i, k), both(-mean[r])), both(rstd));
+          const float2 o = fma2(xh, kKeep ? g[kKeep ? e : 0] : gamma_at(c + 2 * k), kKeep ? b[kKeep ? e : 0] : beta_at(c + 2 * k));
+          out[2 * k] = o.x;
+          out[2 * k + 1] = o.y;
+        }
+        store_unit<kT, kVals>(y, c, out);
+      }
+    }
+    ring.next();
+  }
+  if (s_fail) let_copies_land();
+}
+
+template <int kT, int kMax, int kR>
+__global__ void __launch_bounds__(kMax)
+norm_backward_ring_kernel(const BackwardArgs a, int row_bytes) {
+  constexpr int kVals = 16 / elem_bytes<kT>(), kUnits = kThreadValues / kVals;
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  __shared__ __align__(8) uint64_t s_bars[kSets];
+  __shared__ __align__(16) float s_red[2][32][2 * kR];
+  __shared__ int s_fail;
+  const int threads = blockDim.x, t = threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kR, ldx = a.ldx * elem_bytes<kT>(), lddy = a.lddy * elem_bytes<kT>();
+  RowRing<kR, 2> ring{s_bars, s_rows, row_bytes};
+  const auto fill = [&](int set, int64_t r) {
+    if (t == 0 && r < a.rows)
+      ring.fill(set, a.rows - r < kR ? static_cast<int>(a.rows - r) : kR, static_cast<const char*>(a.x) + r * ldx, ldx,
+                static_cast<const char*>(a.dy) + r * lddy, lddy);
+  };
+  s_fail = 0;
+  ring.init();
+  wait_for_inputs();
+  let_next_begin();
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kR;
+  fill(0, row);
+  float next_mean[kR], next_rstd[kR];
+  const auto statistics = [&](int64_t first) {
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const bool in = first + r < a.rows;
+      next_mean[r] = in ? a.mean[first + r] : 0.0f;
+      next_rstd[r] = in ? a.rstd[first + r] : 0.0f;
+    }
+  };
+  statistics(row);
+  float2 g[kThreadValues / 2], dg[kThreadValues / 2], db[kThreadValues / 2];
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+    for (int k = 0; k < kVals / 2; ++k) {
+      const int c = (i * threads + t) * kVals + 2 * k, e = i * kVals / 2 + k;
+      g[e] = c < a.width ? make_float2(vector_at<kT>(a.gamma, c, 1.0f), vector_at<kT>(a.gamma, c + 1, 1.0f)) : both(0.0f);
+      dg[e] = db[e] = both(0.0f);
+    }
+  const float width = static_cast<float>(a.width);
+  int turn = 0;
+  for (; row < a.rows; row += step) {
+    float mean[kR], rstd[kR], s[2 * kR];
+#pragma unroll
+    for (int r = 0; r < kR; ++r) { mean[r] = next_mean[r]; rstd[r] = next_rstd[r]; }
+    statistics(row + step);
+    ring.wait(&s_fail);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      s[2 * r] = s[2 * r + 1] = 0.0f;
+      if (row + r >= a.rows) continue;
+      const float2 less = both(-mean[r]), scale = both(rstd[r]);
+      float2 s0 = both(0.0f), s1 = both(0.0f);
+      Part<kT, kVals> x, dy;
+      x.load_shared(ring.row(r, 0), a.width, t, threads);
+      dy.load_shared(ring.row(r, 1), a.width, t, threads);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        if ((i * threads + t) * kVals >= a.width) continue;
+#pragma unroll
+        for (int k = 0; k < kVals / 2; ++k) {
+          const int e = i * kVals / 2 + k;
+          const float2 d = dy.two(i, k), xh = mul2(add2(x.two(i, k), less), scale), h = mul2(d, g[e]);
+          dg[e] = fma2(d, xh, dg[e]);
+          db[e] = add2(db[e], d);
+          s0 = add2(s0, h);
+          s1 = fma2(h, xh, s1);
+        }
+      }
+      s[2 * r] = __fadd_rn(s0.x, s0.y);
+      s[2 * r + 1] = __fadd_rn(s1.x, s1.y);
+    }
+    cta_sum<2 * kR>(s, s_red, turn);
+    fill(ring.s ^ 1, row + step);  // behind the barrier all threads are done with the set before
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      if (!a.dx || row + r >= a.rows) break;
+      const float mean_h = __fdiv_rn(s[2 * r], width), mean_hx = __fdiv_rn(s[2 * r + 1], width);
+      char* const dx = static_cast<char*>(a.dx) + (row + r) * row_bytes;
+      Part<kT, kVals> x, dy;
+      x.load_shared(ring.row(r, 0), a.width, t, threads);
+      dy.load_shared(ring.row(r, 1), a.width, t, threads);
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int c = (i * threads + t) * kVals;
+        if (c >= a.width) continue;
+        float out[kVals];
+#pragma unroll
+        for (int k = 0; k < kVals / 2; ++k) {
+          const float2 xh = mul2(add2(x.two(i, k), both(-mean[r])), both(rstd[r])), h = mul2(dy.two(i, k), g[i * kVals / 2 + k]);
+          const float2 o = mul2(both(rstd[r]), fma2(xh, both(-mean_hx), add2(h, both(-mean_h))));
+          out[2 * k] = o.x;
+          out[2 * k + 1] = o.y;
+        }
+        store_unit<kT, kVals>(dx, c, out);
+      }
+    }
+    ring.next();
+  }
+  if (s_fail) let_copies_land();
+  if (!a.partial) return;
+  float* const to_gamma = a.partial + static_cast<int64_t>(blockIdx.x) * a.width;
+  float* const to_beta = to_gamma + static_cast<int64_t>(gridDim.x) * a.width;
+#pragma unroll
+  for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+    for (int j = 0; j < kVals; j += 4) {
+      const int c = (i * threads + t) * kVals + j, e = (i * kVals + j) / 2;
+      if (c >= a.width) continue;
+      *reinterpret_cast<float4*>(to_gamma + c) = make_float4(dg[e].x, dg[e].y, dg[e + 1].x, dg[e + 1].y);
+      *reinterpret_cast<float4*>(to_beta + c) = make_float4(db[e].x, db[e].y, db[e + 1].x, db[e + 1].y);
+    }
+}
+
+// Sums of the CTAs' rows: sixteen warps of a CTA each add every sixteenth of
+// 32 columns' rows, in order, and the first then adds the sixteen.
+constexpr int kSumWarps = 16;
 
 struct SumArgs {
   const float* partial;
@@ -366,7 +704,7 @@ norm_sums_kernel(const SumArgs a) {
   const float* const from = a.partial + blockIdx.y * a.parts * a.width;
   float s = 0.0f;
   if (c < a.width) {
-#pragma unroll 8
+#pragma unroll 16
     for (int64_t p = warp; p < a.parts; p += kSumWarps) s += from[p * a.width + c];
   }
   s_part[warp][lane] = s;
@@ -386,15 +724,37 @@ norm_sums_kernel(const SumArgs a) {
 bool valid_type(int t) { return t == BWD_F32 || t == BWD_BF16 || t == BWD_F16; }
 int bytes_of(int t) { return t == BWD_F32 ? 4 : 2; }
 
-constexpr int kSms = 160;             // at least as many as the device has
-constexpr int kThreadsPerSm = 1024;
+constexpr int kSms = 160;  // at least as many as the device has
 
-// CTAs of the backward pass, and so rows of its workspace, at most.
+int threads_of(int width) { return (width + 32 * kThreadValues - 1) / (32 * kThreadValues) * 32; }
+
+// CTAs of the backward pass, and so rows of its workspace, at most: as many as
+// are resident (some 100 registers to a thread), each with two rows or more,
+// since every one adds a row of sums.
 int64_t backward_ctas(int64_t rows, int width, int sms) {
-  const int threads = width <= kWarpWidth ? 32 * kWarps : (width + 32 * kThreadValues - 1) / (32 * kThreadValues) * 32;
-  const int64_t most = static_cast<int64_t>(sms) * (threads < kThreadsPerSm ? kThreadsPerSm / threads : 1);
-  const int64_t need = width <= kWarpWidth ? (rows + kWarps - 1) / kWarps : rows;
-  return need < most ? need : most;
+  const bool warp = width <= kWarpWidth;
+  const int threads = warp ? 32 * kWarps : threads_of(width);
+  const int64_t most = static_cast<int64_t>(sms) * std::max(1, std::min(512 / threads, 8));
+  const int64_t each = 2 * (warp ? kWarps : 1), need = (rows + each - 1) / each;
+  return std::min(need, most);
+}
+
+// Rows that a CTA of the ring kernels takes at a time, of so many bytes in
+// all arrays, where `ctas` share an SM's shared memory: at most `most`, no more
+// than gives each CTA several sets; 0 where not even one row fits twice.
+int rows_at_a_time(int64_t row_bytes, int ctas, int64_t rows_each, int most) {
+  for (int r = most; r >= 1; r /= 2)
+    if (kSets * r * row_bytes * ctas <= 200 << 10 && rows_each >= 2 * r) return r;
+  return 0;
+}
+
+template <typename... Params, typename... Args>
+bwd_status launch_ring(void (*kernel)(Params...), int64_t ctas, int threads, int smem, cudaStream_t st, const char* what, const Args&... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e = opt_in(kernel, 200 << 10);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
+  }
+  return launch_ex(kernel, dim3(static_cast<unsigned>(ctas)), threads, 0, smem, st, what, args...);
 }
 
 bwd_status sm_count(int* out) {
@@ -416,18 +776,12 @@ int unit_values(int eb, uintptr_t addresses, int64_t row_bytes) {
   return bytes / eb;
 }
 
-int threads_of(int width, int values) {
-  const int per = 32 * kThreadValues;
-  (void)values;
-  return (width + per - 1) / per * 32;
-}
-
 template <template <int, int, bool, int> class Launch, typename Args, typename... More>
 bwd_status by_type(int type, int values, int width, const Args& a, More... more) {
   const auto sized = [&](auto t, auto v) {
     constexpr int kT = decltype(t)::value, kVals = decltype(v)::value;
     if (width <= kWarpWidth) return Launch<kT, kVals, true, 32 * kWarps>::go(a, more...);
-    const int threads = threads_of(width, kVals);
+    const int threads = threads_of(width);
     if (threads <= kMaxThreads / 4) return Launch<kT, kVals, false, kMaxThreads / 4>::go(a, more...);
     if (threads <= kMaxThreads / 2) return Launch<kT, kVals, false, kMaxThreads / 2>::go(a, more...);
     return Launch<kT, kVals, false, kMaxThreads>::go(a, more...);
@@ -448,9 +802,20 @@ bwd_status by_type(int type, int values, int width, const Args& a, More... more)
 template <int kT, int kVals, bool kWarp, int kMax>
 struct LaunchForward {
   static bwd_status go(const ForwardArgs& a, int sms, cudaStream_t st) {
-    const int threads = kWarp ? 32 * kWarps : threads_of(a.width, kVals);
-    const int64_t most = static_cast<int64_t>(sms) * (2 * kThreadsPerSm / threads), need = kWarp ? (a.rows + kWarps - 1) / kWarps : a.rows;
-    return launch_ex(norm_forward_kernel<kT, kVals, kWarp, kMax>, dim3(static_cast<unsigned>(need < most ? need : most)), threads, 0, 0, st,
+    constexpr bool kPieces = kVals * elem_bytes<kT>() == 16 && !kWarp;
+    const int threads = kWarp ? 32 * kWarps : threads_of(a.width), per_sm = std::max(1, std::min(768 / threads, 8));
+    const int64_t most = static_cast<int64_t>(sms) * per_sm, need = kWarp ? (a.rows + kWarps - 1) / kWarps : a.rows;
+    const int64_t ctas = std::min(need, most);
+    if constexpr (kPieces) {
+      const int row_bytes = a.width * elem_bytes<kT>(), r = rows_at_a_time(row_bytes, per_sm, a.rows / ctas, 4);
+      const auto go = [&](auto* kernel) {
+        return launch_ring(kernel, ctas, threads, kSets * r * row_bytes, st, "norm_forward_ring_kernel launch", a, row_bytes);
+      };
+      if (r == 4) return go(norm_forward_ring_kernel<kT, kMax, 4>);
+      if (r == 2) return go(norm_forward_ring_kernel<kT, kMax, 2>);
+      if (r == 1) return go(norm_forward_ring_kernel<kT, kMax, 1>);
+    }
+    return launch_ex(norm_forward_kernel<kT, kVals, kWarp, kMax>, dim3(static_cast<unsigned>(ctas)), threads, 0, 0, st,
                      "norm_forward_kernel launch", a);
   }
 };
@@ -458,14 +823,19 @@ struct LaunchForward {
 template <int kT, int kVals, bool kWarp, int kMax>
 struct LaunchBackward {
   static bwd_status go(const BackwardArgs& a, int64_t ctas, cudaStream_t st) {
-    const int threads = kWarp ? 32 * kWarps : threads_of(a.width, kVals);
-    const int smem = a.partial && (kWarp || kMax == kMaxThreads) ? 8 * a.width : 0;
-    if (smem > 48 * 1024) {
-      const cudaError_t e = opt_in(norm_backward_kernel<kT, kVals, kWarp, kMax>, 8 * kMaxWidth);
-      if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
+    constexpr bool kKeep = kMax <= kMaxThreads / 2, kPieces = kVals * elem_bytes<kT>() == 16 && !kWarp && kKeep;
+    const int threads = kWarp ? 32 * kWarps : threads_of(a.width), per_sm = std::max(1, std::min(512 / threads, 8));
+    if constexpr (kPieces) {
+      // (the partial sums go out in pieces of 16 bytes too)
+      const int row_bytes = a.width * elem_bytes<kT>(), r = aligned16(a.partial) ? rows_at_a_time(2 * row_bytes, per_sm, a.rows / ctas, 2) : 0;
+      const auto go = [&](auto* kernel) {
+        return launch_ring(kernel, ctas, threads, kSets * r * 2 * row_bytes, st, "norm_backward_ring_kernel launch", a, row_bytes);
+      };
+      if (r == 2) return go(norm_backward_ring_kernel<kT, kMax, 2>);
+      if (r == 1) return go(norm_backward_ring_kernel<kT, kMax, 1>);
     }
-    return launch_ex(norm_backward_kernel<kT, kVals, kWarp, kMax>, dim3(static_cast<unsigned>(ctas)), threads, 0, smem, st,
-                     "norm_backward_kernel launch", a);
+    const int smem = a.partial && (kWarp || !kKeep) ? 8 * a.width : 0;
+    return launch_ring(norm_backward_kernel<kT, kVals, kWarp, kMax>, ctas, threads, smem, st, "norm_backward_kernel launch", a);
   }
 };
 
@@ -480,6 +850,14 @@ bwd_status check_size(int64_t rows, int64_t width, bwd_dtype dtype, bwd_dtype ve
 }
 
 }  // namespace
+
+namespace bwd {
+namespace host {
+
+bwd_status take_norm_fault(unsigned int* fault) { return take_wait_fault(fault); }
+
+}  // namespace host
+}  // namespace bwd
 
 extern "C" {
 

@@ -43,17 +43,19 @@ class Fp4Matrix:
     bytes up to its pitch), and the scales' bytes in tiles (``scales``); both
     lie in ``buffer``."""
 
-    __slots__ = ("shape", "dtype", "device", "buffer")
+    __slots__ = ("shape", "dtype", "device", "buffer", "_pointers")
 
     def __init__(self, rows: int, cols: int, dtype, buffer: torch.Tensor):
         """Over a buffer that was another such matrix's, or will be filled."""
-        end = _layout(rows, cols)[2]
-        _need(buffer, "buffer", torch.uint8, end)
-        if buffer.data_ptr() % 16:
-            buffer = buffer.clone()
+        _need(buffer, "buffer", torch.uint8, _layout(rows, cols)[2])
         if dtype not in _GDT:
             raise TypeError("dtype must be float32, bfloat16 or float16")
-        self.shape, self.dtype, self.device, self.buffer = (int(rows), int(cols)), dtype, buffer.device, buffer
+        self._place(rows, cols, dtype, buffer if buffer.data_ptr() % 16 == 0 else buffer.clone(), buffer.device)
+
+    def _place(self, rows, cols, dtype, buffer, device):
+        self.shape, self.dtype, self.device, self.buffer = (rows, cols), dtype, device, buffer
+        base = buffer.data_ptr()
+        self._pointers = base, base + _layout(rows, cols)[1]  # addresses of codes and scales
 
     @property
     def codes(self) -> torch.Tensor:
@@ -63,10 +65,6 @@ class Fp4Matrix:
     @property
     def scales(self) -> torch.Tensor:
         return self.buffer[_layout(*self.shape)[1]:]
-
-    def _pointers(self):
-        base = self.buffer.data_ptr()
-        return base, base + _layout(*self.shape)[1]
 
     def dequantize(self, dtype=None, stream=None) -> torch.Tensor:
         return dequantize(self, dtype, stream)
@@ -85,8 +83,10 @@ def quantize(x: torch.Tensor, stream=None) -> Fp4Matrix:
             return quantize(x)
     x = _matrix(x, "x")
     rows, cols = x.shape
-    q = Fp4Matrix(rows, cols, x.dtype, _bytes(_layout(rows, cols)[2], x.device))
-    _launch("bwd_fp4_quantize", x.device, None, x.data_ptr(), _GDT[x.dtype], rows, cols, max(x.stride(0), cols), *q._pointers())
+    dev, dtype = x.device, x.dtype
+    q = Fp4Matrix.__new__(Fp4Matrix)
+    q._place(rows, cols, dtype, _bytes(_layout(rows, cols)[2], dev), dev)
+    _launch("bwd_fp4_quantize", dev, None, x.data_ptr(), _GDT[dtype], rows, cols, max(x.stride(0), cols), *q._pointers)
     return q
 
 
@@ -100,7 +100,7 @@ def dequantize(a: Fp4Matrix, dtype=None, stream=None) -> torch.Tensor:
     if dtype not in _GDT:
         raise TypeError("dtype must be float32, bfloat16 or float16")
     out = torch.empty(a.shape, dtype=dtype, device=a.device)
-    _launch("bwd_fp4_dequantize", a.device, None, *a._pointers(), *a.shape, out.data_ptr(), _GDT[dtype])
+    _launch("bwd_fp4_dequantize", a.device, None, *a._pointers, *a.shape, out.data_ptr(), _GDT[dtype])
     return out
 
 
@@ -121,7 +121,7 @@ def matmul(a: Fp4Matrix, b: Fp4Matrix, bias: Optional[torch.Tensor] = None, dtyp
     if bias is not None:
         _need(bias, "bias", dtype, n, a.device)
     out = torch.empty((m, n), dtype=dtype, device=a.device)
-    _launch("bwd_fp4_matmul", a.device, None, m, n, k, *a._pointers(), *b._pointers(), _ptr(bias), out.data_ptr(), n, _GDT[dtype])
+    _launch("bwd_fp4_matmul", a.device, None, m, n, k, *a._pointers, *b._pointers, _ptr(bias), out.data_ptr(), n, _GDT[dtype])
     return out
 
 
@@ -147,9 +147,9 @@ def linear(x: torch.Tensor, w: Fp4Matrix, bias: Optional[torch.Tensor] = None, s
         raise ValueError(f"w is on {w.device}, the call runs on {dev}")
     if bias is not None:
         _need(bias, "bias", m.dtype, n, dev)
-    y = torch.empty((*x.shape[:-1], n), dtype=m.dtype, device=dev)
+    y = torch.empty((rows, n) if m is x else (*x.shape[:-1], n), dtype=m.dtype, device=dev)
     work = _bytes(_work(rows, cols), dev)
-    _launch("bwd_fp4_linear", dev, None, m.data_ptr(), _GDT[m.dtype], rows, cols, max(m.stride(0), cols), *w._pointers(), n, _ptr(bias),
+    _launch("bwd_fp4_linear", dev, None, m.data_ptr(), _GDT[m.dtype], rows, cols, max(m.stride(0), cols), *w._pointers, n, _ptr(bias),
             y.data_ptr(), n, work.data_ptr())
     return y
 

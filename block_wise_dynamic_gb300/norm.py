@@ -38,22 +38,19 @@ def _work(rows: int, width: int) -> int:
     return _abi.load().bwd_norm_backward_work_bytes(rows, width) // 4
 
 
-def _vectors(vectors, x_dtype, width, device):
-    """The ABI's type of gamma and beta (fp32 where there is neither)."""
-    dtype = next((v.dtype for v in vectors.values() if isinstance(v, torch.Tensor)), torch.float32)
-    if dtype not in (torch.float32, x_dtype):
+def _vectors(gamma, beta, x_dtype, width, device):
+    """The type of gamma and beta (float32 where there is neither)."""
+    one = beta if gamma is None else gamma
+    if one is None:
+        return torch.float32
+    dtype = one.dtype if isinstance(one, torch.Tensor) else None
+    if dtype is not torch.float32 and dtype is not x_dtype:
         raise TypeError("gamma and beta must be float32 or of x's dtype")
-    for name, v in vectors.items():
-        if v is not None:
-            _need(v, name, dtype, width, device)
+    if gamma is not None:
+        _need(gamma, "gamma", dtype, width, device)
+    if beta is not None:
+        _need(beta, "beta", dtype, width, device)
     return dtype
-
-
-def _width(m: torch.Tensor) -> int:
-    width = m.shape[1]
-    if not 1 <= width <= MAX_WIDTH:
-        raise ValueError(f"the last dimension must be 1 to {MAX_WIDTH}")
-    return width
 
 
 def forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optional[torch.Tensor] = None, eps: float = EPS,
@@ -65,13 +62,16 @@ def forward(x: torch.Tensor, gamma: Optional[torch.Tensor] = None, beta: Optiona
         with _on(stream, x.device):
             return forward(x, gamma, beta, eps, need_stats)
     m = _matrix(x, "x")
-    width, dev = _width(m), m.device
-    vectors = _vectors({"gamma": gamma, "beta": beta}, m.dtype, width, dev)
-    rows = m.shape[0]
-    y = torch.empty(x.shape, dtype=m.dtype, device=dev)
-    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=dev).unbind() if need_stats else (None, None)
-    _launch("bwd_norm_forward", dev, None, m.data_ptr(), _GDT[m.dtype], rows, width, max(m.stride(0), width), _ptr(gamma), _ptr(beta),
-            _GDT[vectors], float(eps), y.data_ptr(), _ptr(mean), _ptr(rstd))
+    rows, width = m.shape
+    if not 1 <= width <= MAX_WIDTH:
+        raise ValueError(f"the last dimension must be 1 to {MAX_WIDTH}")
+    dev, dtype = m.device, m.dtype
+    vectors = _vectors(gamma, beta, dtype, width, dev)
+    y = torch.empty((rows, width) if m is x else x.shape, dtype=dtype, device=dev)
+    mean = torch.empty(rows, dtype=torch.float32, device=dev) if need_stats else None
+    rstd = torch.empty(rows, dtype=torch.float32, device=dev) if need_stats else None
+    _launch("bwd_norm_forward", dev, None, m.data_ptr(), _GDT[dtype], rows, width, max(m.stride(0), width), _ptr(gamma), _ptr(beta),
+            _GDT[vectors], eps, y.data_ptr(), _ptr(mean), _ptr(rstd))
     return y, mean, rstd
 
 
@@ -83,24 +83,26 @@ def backward(dy: torch.Tensor, x: torch.Tensor, gamma: Optional[torch.Tensor], m
         with _on(stream, x.device):
             return backward(dy, x, gamma, mean, rstd, need_input, need_gamma, need_beta, vector_dtype)
     m, d = _matrix(x, "x"), _matrix(dy, "dy")
-    width, dev = _width(m), m.device
-    if dy.shape != x.shape or d.dtype != m.dtype:
+    rows, width = m.shape
+    if not 1 <= width <= MAX_WIDTH:
+        raise ValueError(f"the last dimension must be 1 to {MAX_WIDTH}")
+    dev, dtype = m.device, m.dtype
+    if dy.shape != x.shape or d.dtype is not dtype:
         raise ValueError(f"dy must have x's shape and dtype, {tuple(x.shape)} {x.dtype}")
     if d.device != dev:
         raise ValueError(f"dy is on {d.device}, the call runs on {dev}")
-    rows = m.shape[0]
-    vectors = _vectors({"gamma": gamma}, m.dtype, width, dev)
+    vectors = _vectors(gamma, None, dtype, width, dev)
     if gamma is None and vector_dtype is not None:
         vectors = vector_dtype
-        if vectors not in (torch.float32, m.dtype):
+        if vectors not in (torch.float32, dtype):
             raise TypeError("vector_dtype must be float32 or x's dtype")
     _need(mean, "mean", torch.float32, rows, dev)
     _need(rstd, "rstd", torch.float32, rows, dev)
-    dx = torch.empty(x.shape, dtype=m.dtype, device=dev) if need_input else None
+    dx = torch.empty((rows, width) if m is x else x.shape, dtype=dtype, device=dev) if need_input else None
     dgamma = torch.empty(width, dtype=vectors, device=dev) if need_gamma else None
     dbeta = torch.empty(width, dtype=vectors, device=dev) if need_beta else None
     work = torch.empty(_work(rows, width), dtype=torch.float32, device=dev) if need_gamma or need_beta else None
-    _launch("bwd_norm_backward", dev, None, d.data_ptr(), m.data_ptr(), _GDT[m.dtype], rows, width, max(d.stride(0), width),
+    _launch("bwd_norm_backward", dev, None, d.data_ptr(), m.data_ptr(), _GDT[dtype], rows, width, max(d.stride(0), width),
             max(m.stride(0), width), _ptr(gamma), _GDT[vectors], mean.data_ptr(), rstd.data_ptr(), _ptr(dx), _ptr(dgamma), _ptr(dbeta),
             _ptr(work))
     return dx, dgamma, dbeta

@@ -172,7 +172,7 @@ def test_outputs_end_where_they_should(fp4):
         xq, wq = fp4.quantize(x), fp4.quantize(w)
         for dtype, code in ((torch.bfloat16, 1), (torch.float32, 0)):
             out = torch.full((m + 2, ldo), 7.0, dtype=dtype, device=DEV)
-            assert lib.bwd_fp4_matmul(m, n, k, *xq._pointers(), *wq._pointers(), None, out[1].data_ptr(), ldo, code, None) == 0
+            assert lib.bwd_fp4_matmul(m, n, k, *xq._pointers, *wq._pointers, None, out[1].data_ptr(), ldo, code, None) == 0
             torch.cuda.synchronize()
             assert (out[0] == 7).all() and (out[m + 1] == 7).all() and (out[1:m + 1, n:] == 7).all()
             check_product(out[1:m + 1, :n].contiguous(), x, w, None)
