@@ -115,6 +115,23 @@ __device__ __forceinline__ void load8(const char* src, int64_t left, float (&v)[
   }
 }
 
+// A lane's eight codes, and the bytes of the four blocks that its half warp
+// holds in one word.
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int lane, uint32_t* word) {
+  // magnitudes order like their bits, infinities and NaN above all numbers
+  uint32_t top = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t b = scale_byte(top);
+  uint32_t w = b << (lane / 4 % 4 * 8);
+  w |= __shfl_xor_sync(0xffffffffu, w, 4);
+  w |= __shfl_xor_sync(0xffffffffu, w, 8);
+  *word = w;
+  return codes8(v, inv_scale(b));
+}
+
 template <int kT, typename Unit>
 __global__ void __launch_bounds__(32 * kWarps)
 fp4_quantize_kernel(const QuantArgs a) {
@@ -133,19 +150,9 @@ fp4_quantize_kernel(const QuantArgs a) {
   for (int i = 0; i < kEach; ++i) {
     const int64_t r = r0 + i * kWarps;
     if (r >= a.rows) break;
-    // magnitudes order like their bits, infinities and NaN above all numbers
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[i][j]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const uint32_t b = scale_byte(top);
-    const uint32_t codes = codes8(v[i], inv_scale(b));
+    uint32_t word;
+    const uint32_t codes = quantize8(v[i], lane, &word);
     if (c / 2 < a.pitch) *reinterpret_cast<uint32_t*>(a.codes + r * a.pitch + c / 2) = codes;
-    // a word of four blocks' bytes, from lanes 0, 4, 8 and 12 of each half warp
-    uint32_t word = b << (lane / 4 % 4 * 8);
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
     if (lane % 16 == 0) *reinterpret_cast<uint32_t*>(a.scales + scale_word(r, 2 * blockIdx.x + lane / 16, a.groups)) = word;
   }
 }
@@ -540,7 +547,13 @@ fp4_matmul_kernel(const __grid_constant__ MmArgs p) {
 // the cluster over distributed shared memory, the r-th share of the columns
 // and adds the parts in the order of the ranks.  Products of more rows that
 // have few tiles and a long sum are split here too, 128 rows to a tile.
+//
+// Up to kFuse rows, A may also come unquantized: the warps that store in the
+// end then quantize each stage's 256 columns on the way into shared memory
+// while the weight's copies are under way, which saves the quantizer's launch
+// and its results' way through memory.
 
+constexpr int kFuse = 16;
 constexpr int kFewThreads = 320;  // warp 0 copies, warp 1 issues, warps 2 to 9 store
 template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 128 ? 3 : kBN >= 32 ? 4 : 5; }
 template <int kBN> __host__ __device__ constexpr int few_stage_bytes() { return kTile * kStageBytes + kBN * kStageBytes; }
@@ -557,6 +570,9 @@ template <int kBN> __host__ __device__ constexpr int few_smem() {
 constexpr uint32_t kFewCols = kTmemCols / 2, kFewSfCol = kFewCols - 32;
 template <int kBN> __host__ __device__ constexpr int few_accs() { return static_cast<int>(kFewSfCol) / kBN; }
 constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
+// Longest row of A that the kernel quantizes for fp32 results: longer ones
+// leave the accumulators of a cluster's CTAs more than kChunk stages each.
+constexpr int64_t kFuseCols = int64_t{kMaxSplit} * few_accs<kFuse>() * kChunk * kStageK;
 
 struct FewArgs {
   CUtensorMap map_w, map_x;  // rows of B in boxes of 128, of A in boxes of kBN
@@ -569,11 +585,27 @@ struct FewArgs {
   int split;             // CTAs of a cluster, along the summed axis
   int tiles_n;           // tiles of 128 rows of B
   int b_ready;           // B is no result of the kernel ahead
+  const void* x;         // A itself, `ldx` elements between rows of k, where the kernel quantizes it
+  int64_t ldx;
+  int k;
+  int unit;              // its rows start on boundaries of so many bytes, and hold whole units
 };
 
-template <int kT, int kBN>
+// Eight values of a row from column c on as they lie in memory, zeros past its end.
+template <int kT>
+__device__ __forceinline__ void few_load(const FewArgs& p, int line, int c, float (&v)[8]) {
+  const char* const src = static_cast<const char*>(p.x) + (line * p.ldx + c) * elem_bytes<kT>();
+  const int64_t left = line < p.m ? p.k - c : 0;
+  if (p.unit == 16) load8<kT, uint4>(src, left, v);
+  else if (p.unit == 8) load8<kT, uint2>(src, left, v);
+  else if (kT == kF32 || p.unit == 4) load8<kT, uint32_t>(src, left, v);
+  else if constexpr (kT != kF32) load8<kT, uint16_t>(src, left, v);
+}
+
+template <int kT, int kBN, bool kFused>
 __global__ void __launch_bounds__(kFewThreads, 2)
 fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
+  static_assert(!kFused || kBN == kFuse, "scales of up to 32 rows lie in one column");
   constexpr int kStages = few_stages<kBN>(), kW = kTile * kStageBytes, kStage = few_stage_bytes<kBN>(), kAccs = few_accs<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -595,7 +627,7 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
 
   const auto weight = [&](int i, int s) {  // stage i of this CTA's, into stage s of the ring
     const int kb = kb0 + i;
-    mbar_expect_tx(&s_full[s], kStage + 2 * kSfTile);
+    mbar_expect_tx(&s_full[s], kFused ? kW + kSfTile : kStage + 2 * kSfTile);
     tma_load_one(sm + s * kStage, &p.map_w, kb * kStageBytes, n0, &s_full[s]);
     bulk_load(sf + s * 2 * kSfTile, p.sfw + (static_cast<int64_t>(n0 / 128) * p.stages + kb) * kSfTile, kSfTile, &s_full[s]);
   };
@@ -603,7 +635,7 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
   if (warp == 0) {
     if (elect_one()) {
       s_fail = 0;
-      for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
+      for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], kFused ? 2 : 1); mbar_init(&s_empty[i], 1); }
       mbar_init(&s_done, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       // the first stages' weights, at once where they do not depend on the kernel ahead
@@ -631,10 +663,12 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
       if (i >= ahead && !mbar_wait(&s_empty[ring.s], ring.phase ^ 1u, &s_fail)) break;
       if (one) {
         if (i >= ahead) weight(i, ring.s);
-        const int kb = kb0 + i;
-        tma_load_one(sm + ring.s * kStage + kW, &p.map_x, kb * kStageBytes, m0, &s_full[ring.s]);
-        bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + (static_cast<int64_t>(m0 / 128) * p.stages + kb) * kSfTile, kSfTile,
-                  &s_full[ring.s]);
+        if constexpr (!kFused) {
+          const int kb = kb0 + i;
+          tma_load_one(sm + ring.s * kStage + kW, &p.map_x, kb * kStageBytes, m0, &s_full[ring.s]);
+          bulk_load(sf + ring.s * 2 * kSfTile + kSfTile, p.sfx + (static_cast<int64_t>(m0 / 128) * p.stages + kb) * kSfTile, kSfTile,
+                    &s_full[ring.s]);
+        }
       }
       __syncwarp();
     }
@@ -671,6 +705,38 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
       if (--left == 0) { left = chunk; acc += kBN; }
     }
     if (one) commit_one(&s_done);
+  } else if constexpr (kFused) {
+    // A warp to each stage of the ring, a row at a time, eight columns to a
+    // lane.  A warp sees every phase of its own stage's barrier.
+    static_assert(kStages <= kFewThreads / 32 - 2, "a warp to each stage");
+    wait_for_inputs();
+    const int s = warp - 2;
+    uint32_t phase = 1;
+    uint8_t* const codes = sm + s * kStage + kW;
+    uint8_t* const scales = sf + s * 2 * kSfTile + kSfTile;
+    for (int i = s < kStages ? s : count; i < count; i += kStages, phase ^= 1u) {
+      const int c = (kb0 + i) * kStageK + 8 * lane;
+      constexpr int kAtOnce = 4;  // rows whose loads are under way together
+      for (int l0 = 0; l0 < p.m; l0 += kAtOnce) {
+        float v[kAtOnce][8];
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) few_load<kT>(p, l0 + h, c, v[h]);
+        if (l0 == 0 && i >= kStages && !__all_sync(0xffffffffu, mbar_wait(&s_empty[s], phase, &s_fail))) break;
+#pragma unroll
+        for (int h = 0; h < kAtOnce; ++h) {
+          const int l = l0 + h;
+          if (l >= p.m) break;
+          uint32_t word;
+          const uint32_t q = quantize8(v[h], lane, &word);
+          // the 128-byte swizzle: 16-byte piece of row l at piece ^ (l mod 8)
+          *reinterpret_cast<uint32_t*>(codes + l * kStageBytes + (((lane >> 2) ^ (l & 7)) << 4) + (lane & 3) * 4) = q;
+          if (lane % 16 == 0) *reinterpret_cast<uint32_t*>(scales + lane / 16 * kSfGroup + l * 16) = word;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_full[s]);
+    }
   }
   __syncwarp();
   // warps w and w + 4 share a quarter of the rows and take turns at the columns
@@ -780,8 +846,9 @@ DeviceState g_dev[kMaxDevices];
 template <int kT>
 cudaError_t opt_in_all() {
   const cudaError_t e[] = {opt_in(fp4_matmul_kernel<kT, 256, kT == kF32>, mm_smem<256>()), opt_in(fp4_matmul_kernel<kT, 128, kT == kF32>, mm_smem<128>()),
-                           opt_in(fp4_matmul_few_kernel<kT, 16>, few_smem<16>()), opt_in(fp4_matmul_few_kernel<kT, 32>, few_smem<32>()),
-                           opt_in(fp4_matmul_few_kernel<kT, 64>, few_smem<64>()), opt_in(fp4_matmul_few_kernel<kT, 128>, few_smem<128>())};
+                           opt_in(fp4_matmul_few_kernel<kT, 16, false>, few_smem<16>()), opt_in(fp4_matmul_few_kernel<kT, 32, false>, few_smem<32>()),
+                           opt_in(fp4_matmul_few_kernel<kT, 64, false>, few_smem<64>()), opt_in(fp4_matmul_few_kernel<kT, 128, false>, few_smem<128>()),
+                           opt_in(fp4_matmul_few_kernel<kT, kFuse, true>, few_smem<kFuse>())};
   for (const cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -808,7 +875,7 @@ bwd_status ensure_device(const DeviceState** out) {
   if (e == cudaSuccess) e = opt_in_all<kF16>();
   // so much shared memory that no SM takes two
   smem = smem / 2 > few_smem<128>() ? smem / 2 : few_smem<128>();
-  if (e == cudaSuccess) e = opt_in(fp4_matmul_few_kernel<kBF16, 128>, smem);
+  if (e == cudaSuccess) e = opt_in(fp4_matmul_few_kernel<kBF16, 128, false>, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
@@ -828,7 +895,7 @@ bwd_status ensure_device(const DeviceState** out) {
   for (int c = 2; c <= kMaxSplit; ++c) {
     cfg.gridDim = dim3(static_cast<unsigned>(d.sms / c * c));
     attr[0].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
-    e = cudaOccupancyMaxActiveClusters(&d.clusters[c], fp4_matmul_few_kernel<kBF16, 128>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&d.clusters[c], fp4_matmul_few_kernel<kBF16, 128, false>, &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
   }
   d.ctx = ctx;
@@ -921,12 +988,20 @@ int64_t few_split(int64_t tiles, int64_t stages, int64_t rows, const DeviceState
   return two > split ? two : split;
 }
 
-template <int kT, int kBN>
-bwd_status launch_few(const Product& q, int b_ready, const DeviceState& d, cudaStream_t st) {
+// A as it is, for the kernel that quantizes it.
+struct Plain {
+  const void* x;
+  int64_t ld;
+  int unit;
+};
+
+template <int kT, int kBN, bool kFused>
+bwd_status launch_few(const Product& q, const Plain& plain, int b_ready, const DeviceState& d, cudaStream_t st) {
   FewArgs p{};
   bwd_status s;
   if ((s = code_map(&p.map_w, q.b, q.k, kTile)) != BWD_OK) return s;
-  if ((s = code_map(&p.map_x, q.a, q.k, kBN)) != BWD_OK) return s;
+  if (!kFused && (s = code_map(&p.map_x, q.a, q.k, kBN)) != BWD_OK) return s;
+  p.x = plain.x; p.ldx = plain.ld; p.unit = plain.unit; p.k = static_cast<int>(q.k);
   p.sfw = q.b.scales; p.sfx = q.a.scales; p.bias = q.bias; p.out = q.out; p.ldo = q.ldo;
   p.m = static_cast<int>(q.a.rows); p.n = static_cast<int>(q.b.rows); p.stages = static_cast<int>(stages_of(q.k));
   const int64_t tiles = tiles_of(p.n) * ((p.m + kBN - 1) / kBN), part = few_accs<kBN>() * kChunk;
@@ -935,16 +1010,22 @@ bwd_status launch_few(const Product& q, int b_ready, const DeviceState& d, cudaS
   p.split = static_cast<int>(kT == kF32 && split * part < p.stages ? (p.stages + part - 1) / part : split);
   p.tiles_n = static_cast<int>(tiles_of(p.n));
   p.b_ready = b_ready;
-  return launch_ex(fp4_matmul_few_kernel<kT, kBN>, dim3(static_cast<unsigned>(tiles * p.split)), kFewThreads, p.split, few_smem<kBN>(), st,
+  return launch_ex(fp4_matmul_few_kernel<kT, kBN, kFused>, dim3(static_cast<unsigned>(tiles * p.split)), kFewThreads, p.split, few_smem<kBN>(), st,
                    "fp4_matmul_few_kernel launch", p);
 }
 
 template <int kT>
-bwd_status few(const Product& q, int b_ready, const DeviceState& d, cudaStream_t st) {
-  if (q.a.rows > 64) return launch_few<kT, 128>(q, b_ready, d, st);
-  if (q.a.rows > 32) return launch_few<kT, 64>(q, b_ready, d, st);
-  if (q.a.rows > 16) return launch_few<kT, 32>(q, b_ready, d, st);
-  return launch_few<kT, 16>(q, b_ready, d, st);
+bwd_status few(const Product& q, const Plain& plain, int b_ready, const DeviceState& d, cudaStream_t st) {
+  if (plain.x) return launch_few<kT, kFuse, true>(q, plain, b_ready, d, st);
+  if (q.a.rows > 64) return launch_few<kT, 128, false>(q, plain, b_ready, d, st);
+  if (q.a.rows > 32) return launch_few<kT, 64, false>(q, plain, b_ready, d, st);
+  if (q.a.rows > 16) return launch_few<kT, 32, false>(q, plain, b_ready, d, st);
+  return launch_few<kT, 16, false>(q, plain, b_ready, d, st);
+}
+
+bwd_status few(const Product& q, const Plain& plain, bwd_dtype dtype, int b_ready, const DeviceState& d, cudaStream_t st) {
+  if (dtype == BWD_F32) return few<kF32>(q, plain, b_ready, d, st);
+  return dtype == BWD_BF16 ? few<kBF16>(q, plain, b_ready, d, st) : few<kF16>(q, plain, b_ready, d, st);
 }
 
 // Whether a product goes to the kernel for few rows of A, or few tiles: for
@@ -976,7 +1057,7 @@ bwd_status product(const Product& q, bwd_dtype dtype, int b_ready, cudaStream_t 
   const bwd_status s = ensure_device(&d);
   if (s != BWD_OK) return s;
   if (!use_few(q, dtype, *d)) return by_pairs(q, dtype, *d, st);
-  return dtype == BWD_F32 ? few<kF32>(q, b_ready, *d, st) : dtype == BWD_BF16 ? few<kBF16>(q, b_ready, *d, st) : few<kF16>(q, b_ready, *d, st);
+  return few(q, Plain{nullptr, 0, 0}, dtype, b_ready, *d, st);
 }
 
 bwd_status check_matrix(const void* x, bwd_dtype dtype, int64_t rows, int64_t cols, int64_t ld) {
@@ -1093,6 +1174,7 @@ bwd_status bwd_fp4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a, con
 
 int64_t bwd_fp4_linear_work_bytes(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || rows > kMaxDim || cols > kMaxDim) return -1;
+  if (rows <= kFuse && cols <= kFuseCols) return 0;
   Pieces w{nullptr};
   w.take(rows * bwd_fp4_pitch(cols));
   w.take(bwd_fp4_scale_bytes(rows, cols));
@@ -1107,10 +1189,17 @@ bwd_status bwd_fp4_linear(const void* x, bwd_dtype dtype, int64_t rows, int64_t 
   if (ldy < n) return fail(BWD_ERR_INVALID_ARG, "ldy is less than n");
   if (rows == 0 || n == 0) return BWD_OK;
   const int eb = bytes_of(dtype);
-  if (!y || (cols > 0 && (!w || !w_scales || !work))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
+  const bool fused = rows <= kFuse && (dtype != BWD_F32 || cols <= kFuseCols);
+  if (!y || (cols > 0 && (!w || !w_scales || (!fused && !work)))) return fail(BWD_ERR_INVALID_ARG, "NULL pointer");
   if (!aligned_to(y, eb) || !aligned_to(bias, eb)) return fail(BWD_ERR_INVALID_ARG, "y and bias must be aligned to their element size");
   if (!aligned16(w) || !aligned16(w_scales) || !aligned16(work)) return fail(BWD_ERR_INVALID_ARG, "codes, scales and work must be 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (fused && cols > 0) {
+    const DeviceState* d = nullptr;
+    if ((s = ensure_device(&d)) != BWD_OK) return s;
+    return few(Product{Operand{nullptr, nullptr, rows}, Operand{w, w_scales, n}, cols, bias, y, ldy}, Plain{x, ld, unit16_of(x, (ld | cols) * eb)},
+               dtype, 0, *d, st);
+  }
   Pieces pieces{static_cast<uint8_t*>(work)};
   uint8_t* const codes = pieces.take(rows * bwd_fp4_pitch(cols));
   uint8_t* const scales = pieces.take(bwd_fp4_scale_bytes(rows, cols));

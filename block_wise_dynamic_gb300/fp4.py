@@ -125,9 +125,14 @@ def matmul(a: Fp4Matrix, b: Fp4Matrix, bias: Optional[torch.Tensor] = None, dtyp
     return out
 
 
+_FUSED_ROWS, _FUSED_COLS = 16, 229_376  # what the library's product quantizes itself, without a workspace
+
+
 @lru_cache(maxsize=1024)
 def _work(rows: int, cols: int) -> int:
     """bwd_fp4_linear_work_bytes."""
+    if rows <= _FUSED_ROWS and cols <= _FUSED_COLS:
+        return 0
     return _round256(_layout(rows, cols)[2])
 
 
@@ -148,9 +153,10 @@ def linear(x: torch.Tensor, w: Fp4Matrix, bias: Optional[torch.Tensor] = None, s
     if bias is not None:
         _need(bias, "bias", m.dtype, n, dev)
     y = torch.empty((rows, n) if m is x else (*x.shape[:-1], n), dtype=m.dtype, device=dev)
-    work = _bytes(_work(rows, cols), dev)
+    size = _work(rows, cols)
+    work = _bytes(size, dev) if size else None
     _launch("bwd_fp4_linear", dev, None, m.data_ptr(), _GDT[m.dtype], rows, cols, max(m.stride(0), cols), *w._pointers, n, _ptr(bias),
-            y.data_ptr(), n, work.data_ptr())
+            y.data_ptr(), n, _ptr(work))
     return y
 
 

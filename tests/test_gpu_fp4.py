@@ -178,6 +178,18 @@ def test_outputs_end_where_they_should(fp4):
             check_product(out[1:m + 1, :n].contiguous(), x, w, None)
 
 
+@pytest.mark.parametrize("kind", list(TYPES))
+@pytest.mark.parametrize("off,pitch", [(0, 8), (1, 0), (1, 3), (2, 2), (4, 4), (8, 1)])
+def test_few_rows_strides_and_alignment(fp4, off, pitch, kind):
+    """Up to 16 rows are quantized by the product's kernel."""
+    for rows, cols in [(16, 2600), (9, 520), (1, 77)]:
+        flat = torch.full((off + rows * (cols + pitch),), 1e4, dtype=TYPES[kind], device=DEV)
+        x = flat[off:].view(rows, cols + pitch)[:, :cols]
+        x.copy_(draw((rows, cols), 2, kind))
+        wq = fp4.quantize(draw((200, cols), 3, kind))
+        assert torch.equal(fp4.linear(x, wq), fp4.matmul(fp4.quantize(x), wq))
+
+
 def test_not_finite_rows(fp4):
     x, w = draw((300, 400), 1, "bf16"), draw((200, 400), 2, "bf16")
     x[7, 350] = float("inf")
