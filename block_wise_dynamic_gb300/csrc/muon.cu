@@ -35,6 +35,7 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f, kEps = 1e-7f;
 constexpr float kScale = 16384.0f;
 
 constexpr int kBatch = 64;      // matrices of one launch
+constexpr int kGroups = 8;      // shapes of one launch
 constexpr int kSlots = 512;     // partial sums of a matrix's norm at most
 constexpr int kThreads = 256;
 
@@ -48,18 +49,26 @@ struct Matrices {
 // --------------------------------------------------------------------------
 // momentum, norm and the first pair of operands
 
-struct PrepareArgs {
-  Matrices x;
-  double* slots;            // [matrix][kSlots]
-  const float* grad_scale;  // or null: 1
+// Matrices of one shape, in either orientation.
+struct PrepareGroup {
   __half* planes;           // [matrix][high, low][m][pitch]
   int64_t size;             // elements of a matrix
   int64_t chunk;            // of one CTA of the first kernel
   int chunks;
   int m, n, pitch;          // of the wide form
   int split_cols;           // columns of one CTA of the second kernel, a multiple of 64
+  int first;                // its first matrix
+  int norm_start, split_start;  // its first CTA of either kernel
+};
+
+struct PrepareArgs {
+  Matrices x;
+  double* slots;            // [matrix][kSlots]
+  const float* grad_scale;  // or null: 1
   float momentum;
   int nesterov;
+  int groups;
+  PrepareGroup g[kGroups];
 };
 
 __device__ __forceinline__ bool finite(float s) { return fabsf(s) <= 3.402823466e38f; }
@@ -131,15 +140,18 @@ ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
   __shared__ double s_red[kThreads / 32];
   wait_for_inputs();
   let_next_begin();
-  const int z = blockIdx.y;
+  int gi = 0;
+  while (gi + 1 < a.groups && static_cast<int>(blockIdx.x) >= a.g[gi + 1].norm_start) ++gi;
+  const PrepareGroup& p = a.g[gi];
+  const int local = static_cast<int>(blockIdx.x) - p.norm_start, z = p.first + local / p.chunks, chunk = local % p.chunks;
   const void* const g = a.x.g[z];
   float* const mom = a.x.mom[z];
   const float s = kMomentum && a.grad_scale ? *a.grad_scale : 1.0f;
   const bool vec = on16(g) && on16(mom);
   double sum = 0.0;
-  const int64_t end = min(a.size, (blockIdx.x + 1) * a.chunk);
+  const int64_t end = min(p.size, (chunk + 1) * p.chunk);
 #pragma unroll 2
-  for (int64_t i = blockIdx.x * a.chunk + 8 * threadIdx.x; i < end; i += 8 * kThreads) {
+  for (int64_t i = chunk * p.chunk + 8 * threadIdx.x; i < end; i += 8 * kThreads) {
     float u[8];
     update8<kT, kMomentum, true>(a, g, mom, s, vec, i, end, u);
     float part = 0.0f;
@@ -162,7 +174,7 @@ ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int w = 1; w < kThreads / 32; ++w) sum += s_red[w];
-  a.slots[z * kSlots + blockIdx.x] = sum;
+  a.slots[z * kSlots + chunk] = sum;
 }
 
 // Two values as packed pairs of high and low parts.
@@ -188,9 +200,13 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
   __shared__ float s_inv[2];
   wait_for_inputs();
   let_next_begin();
-  const int z = blockIdx.z;
+  int gi = 0;
+  while (gi + 1 < a.groups && static_cast<int>(blockIdx.x) >= a.g[gi + 1].split_start) ++gi;
+  const PrepareGroup& p = a.g[gi];
+  const int strips = (p.pitch + p.split_cols - 1) / p.split_cols, per = strips * ((p.m + kSplitRows - 1) / kSplitRows);
+  const int local = static_cast<int>(blockIdx.x) - p.split_start, in_group = local / per, tile = local % per, z = p.first + in_group;
   double sum = 0.0;
-  for (int i = threadIdx.x; i < a.chunks; i += kThreads) sum += a.slots[z * kSlots + i];
+  for (int i = threadIdx.x; i < p.chunks; i += kThreads) sum += a.slots[z * kSlots + i];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = sum;
@@ -209,22 +225,22 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
   float* const mom = a.x.mom[z];
   const float s = kMomentum && a.grad_scale ? *a.grad_scale : 1.0f;
   const bool tall = a.x.tall[z];
-  const int cols = tall ? a.m : a.n;  // as stored
+  const int cols = tall ? p.m : p.n;  // as stored
   const bool vec = on16(g) && on16(mom) && cols % 8 == 0;
-  __half* const high = a.planes + static_cast<int64_t>(z) * 2 * a.m * a.pitch;
-  __half* const low = high + static_cast<int64_t>(a.m) * a.pitch;
-  const int r0 = blockIdx.y * kSplitRows;
+  __half* const high = p.planes + static_cast<int64_t>(in_group) * 2 * p.m * p.pitch;
+  __half* const low = high + static_cast<int64_t>(p.m) * p.pitch;
+  const int r0 = tile / strips * kSplitRows;
   const auto put = [&](int row, int col, const float (&x)[8]) {
-    if (row >= a.m || col >= a.pitch) return;
+    if (row >= p.m || col >= p.pitch) return;
     uint4 h, l;
 #pragma unroll
     for (int j = 0; j < 4; ++j) split2(x[2 * j], x[2 * j + 1], (&h.x)[j], (&l.x)[j]);
-    const int64_t at = static_cast<int64_t>(row) * a.pitch + col;
+    const int64_t at = static_cast<int64_t>(row) * p.pitch + col;
     *reinterpret_cast<uint4*>(high + at) = h;
     *reinterpret_cast<uint4*>(low + at) = l;
   };
-  for (int c0 = blockIdx.x * a.split_cols, c1 = c0 + a.split_cols; c0 < c1; c0 += 64) {
-    const int sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0, rows = tall ? a.n : a.m;
+  for (int c0 = tile % strips * p.split_cols, c1 = c0 + p.split_cols; c0 < c1; c0 += 64) {
+    const int sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0, rows = tall ? p.n : p.m;
 #pragma unroll
     for (int e = threadIdx.x; e < 64 * 8; e += kThreads) {
       const int r = e / 8, c = e % 8 * 8;
@@ -293,14 +309,15 @@ struct ProductArgs {
   int passes;            // 3, or 1: the high parts alone
   int tiles_m, tiles_n, tiles, items;
   int whole;             // the first items; the others are halves of a tile
-  int split;             // CTAs that divide the summed axis, of small products
   float alpha, beta;     // result = alpha add + beta product
 };
 
 struct FinalArgs {
   Matrices x;
   const float* grad_scale;  // or null: 1
-  float decay, step;        // of the parameter and of the update
+  float decay;              // of the parameter
+  float step[kGroups];      // of the update
+  int first[kGroups];       // a group's first matrix
 };
 
 __device__ __forceinline__ void tma_load3(void* dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -648,7 +665,8 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
           // 32 values of a line of the result that are far apart, neighbouring
           // lanes' side by side; several old parameters are read before any of
           // them is written
-          const bool tall = f.x.tall[tile.z];
+          const int z = f.first[0] + tile.z;
+          const bool tall = f.x.tall[z];
           float* const stage = reinterpret_cast<float*>(buf);
           __syncwarp();
           if (!tall) {
@@ -659,7 +677,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
           const int64_t ld = tall ? a.m : a.n;
           int64_t at = tall ? static_cast<int64_t>(col) * ld + row : static_cast<int64_t>(row0) * ld + col + lane;
           const int count = tall ? (row < a.m ? a.n - col : 0) : col + lane < a.n ? a.m - row0 : 0;
-          void* const out = f.x.out[tile.z];
+          void* const out = f.x.out[z];
 #pragma unroll
           for (int j0 = 0; j0 < 32; j0 += 8, at += 8 * ld) {
             float o[8];
@@ -670,7 +688,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
 #pragma unroll
               for (int j = 0; j < 8; ++j) p[j] = j0 + j < count ? load1<kT>(out, at + j * ld) : 0.0f;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(-f.step, o[j], __fmul_rn(p[j], f.decay));
+              for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(-f.step[0], o[j], __fmul_rn(p[j], f.decay));
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -709,6 +727,13 @@ constexpr int kMaxSplit = 8;
 constexpr int kUnit = 8, kUnits = kSmallCols / kUnit;  // columns that move together
 static_assert((kUnits + kMaxSplit - 1) * kSmallRows * kUnit * 4 <= kSmallStages * kSmallStage, "the gathered parts take the stages' place");
 
+// Products of up to kGroups shapes, one CTA cluster for each tile.
+struct SmallCall {
+  int groups, split;
+  int start[kGroups];  // a group's first tile
+  ProductArgs g[kGroups];
+};
+
 // Eight neighbouring columns of this thread's row, of both planes.
 struct Pair8 {
   uint4 h, l;
@@ -716,7 +741,7 @@ struct Pair8 {
 
 template <int kMode, int kT, bool kUpdate>
 __global__ void __launch_bounds__(kSmallThreads, 1)
-ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
+ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
   constexpr bool kTrans = kMode == kApply || kMode == kFinal;  // q's summed axis is its rows
   extern __shared__ uint8_t smem_raw[];
@@ -728,8 +753,12 @@ ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ s
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   uint32_t rank;
   asm("mov.u32 %0, %cluster_ctarank;" : "=r"(rank));
-  const Tile tile = tile_of<kSmallRows, kSmallCols, kSymmetric>(a, static_cast<int>(blockIdx.x) / a.split);
-  const int kb0 = a.kblocks * static_cast<int>(rank) / a.split, count = a.kblocks * (static_cast<int>(rank) + 1) / a.split - kb0;
+  const int item = static_cast<int>(blockIdx.x) / call.split;
+  int gi = 0;
+  while (gi + 1 < call.groups && item >= call.start[gi + 1]) ++gi;
+  const ProductArgs& a = call.g[gi];
+  const Tile tile = tile_of<kSmallRows, kSmallCols, kSymmetric>(a, item - call.start[gi]);
+  const int kb0 = a.kblocks * static_cast<int>(rank) / call.split, count = a.kblocks * (static_cast<int>(rank) + 1) / call.split - kb0;
   const int least = (count + kSmallAccs - 1) / kSmallAccs, chunk = least > kChunk ? least : kChunk;
   const int accs = (count + chunk - 1) / chunk;
   const bool pairs = a.passes == 3;
@@ -754,7 +783,7 @@ ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ s
   let_next_begin();
 
   const int quarter = warp & 3, half = (warp - 2) / 4, row = quarter * 32 + lane, r = tile.m0 + row;
-  const uint32_t share = (kUnits + a.split - 1) / a.split;
+  const uint32_t share = (kUnits + call.split - 1) / call.split;
   const int64_t plane = static_cast<int64_t>(a.m) * a.pitch;
   // this thread's units of its CTA's share: the half-th and every second from there
   constexpr int kMine = kUnits / 2;
@@ -867,7 +896,7 @@ ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ s
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      for (int q = 0; q < a.split; ++q) {
+      for (int q = 0; q < call.split; ++q) {
         const float4* const from = reinterpret_cast<const float4*>(parts + ((q * share + u) * kSmallRows + row) * kUnit);
         const float4 x = from[0], y = from[1];
         v[0] = __fadd_rn(v[0], x.x); v[1] = __fadd_rn(v[1], x.y); v[2] = __fadd_rn(v[2], x.z); v[3] = __fadd_rn(v[3], x.w);
@@ -897,15 +926,16 @@ ns_small_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ s
           }
         }
       } else if (writes) {
-        const bool tall = f.x.tall[tile.z];
+        const int z = f.first[gi] + tile.z;
+        const bool tall = f.x.tall[z];
         const int64_t at = tall ? static_cast<int64_t>(col) * a.m + r : static_cast<int64_t>(r) * a.n + col, step = tall ? a.m : 1;
-        void* const out = f.x.out[tile.z];
+        void* const out = f.x.out[z];
         if constexpr (kUpdate) {
           float p[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) p[j] = col + j < a.n ? load1<kT>(out, at + j * step) : 0.0f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(-f.step, v[j], __fmul_rn(p[j], f.decay));
+          for (int j = 0; j < 8; ++j) v[j] = __fmaf_rn(-f.step[gi], v[j], __fmul_rn(p[j], f.decay));
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -931,18 +961,33 @@ struct Shape {
   int64_t m, n;
   int64_t x_bytes() const { return 4 * m * up(n, 64); }  // a pair of planes
   int64_t a_bytes() const { return 4 * m * up(m, 64); }
-  int64_t bytes() const { return 2 * x_bytes() + 2 * a_bytes() + 8 * kSlots + 256; }
   bool operator<(const Shape& o) const { return m != o.m ? m < o.m : n < o.n; }
 };
 Shape shape_of(int64_t rows, int64_t cols) { return rows > cols ? Shape{cols, rows} : Shape{rows, cols}; }
 
-// Matrices of one shape that are worked on together.
-int64_t batch_of(const Shape& s, int64_t count) {
-  int64_t most = kWorkMost / s.bytes();
-  most = most < 1 ? 1 : most > kBatch ? kBatch : most;
-  const int64_t launches = (count + most - 1) / most;
-  return (count + launches - 1) / launches;
+// Tiles of a product, of so many rows and columns each.
+int64_t tiles_of(const Shape& result, int rows, int cols, bool symmetric) {
+  const int64_t tm = (result.m + rows - 1) / rows;
+  return symmetric ? rows / cols * tm * (tm + 1) / 2 : tm * ((result.n + cols - 1) / cols);
 }
+
+// Matrices that are worked on together: of up to kGroups shapes whose products
+// have few tiles, or of one shape.
+struct Group {
+  Shape s;
+  int64_t first, count;  // in the order of shapes
+};
+struct Set {
+  Group g[kGroups];
+  int groups;
+  bool small;  // few tiles: all groups' products in one launch
+  int64_t count() const { return g[groups - 1].first + g[groups - 1].count - g[0].first; }
+  int64_t bytes() const {
+    int64_t n = 0;
+    for (int i = 0; i < groups; ++i) n += 2 * up(g[i].s.x_bytes() * g[i].count, 256) + 2 * up(g[i].s.a_bytes() * g[i].count, 256);
+    return n + 8 * kSlots * count();
+  }
+};
 
 constexpr int kMaxDevices = 64;
 struct DeviceState {
@@ -1053,12 +1098,6 @@ struct Step {
   bwd_dtype g_type, out_type;
 };
 
-// Tiles of a product, of so many rows and columns each.
-int64_t tiles_of(const Shape& result, int rows, int cols, bool symmetric) {
-  const int64_t tm = (result.m + rows - 1) / rows;
-  return symmetric ? rows / cols * tm * (tm + 1) / 2 : tm * ((result.n + cols - 1) / cols);
-}
-
 template <int kBN, int kMode>
 bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& st, int pairs, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(2 * (a.items < pairs ? a.items : pairs)));
@@ -1077,10 +1116,10 @@ bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& 
 }
 
 template <int kMode>
-bwd_status launch_small(const ProductArgs& a, const FinalArgs* f, const Step& st, cudaStream_t stream) {
+bwd_status launch_small(const SmallCall& c, int tiles, const FinalArgs* f, const Step& st, cudaStream_t stream) {
   const auto go = [&](auto kernel, const auto& last) {
-    return launch_ex(kernel, dim3(static_cast<unsigned>(a.items * a.split)), kSmallThreads, a.split, kSmallSmem, stream,
-                     "ns_small_kernel launch", a, last);
+    return launch_ex(kernel, dim3(static_cast<unsigned>(tiles * c.split)), kSmallThreads, c.split, kSmallSmem, stream, "ns_small_kernel launch",
+                     c, last);
   };
   if constexpr (kMode != kFinal) {
     return go(ns_small_kernel<kMode, kF32, false>, 0);
@@ -1093,15 +1132,67 @@ bwd_status launch_small(const ProductArgs& a, const FinalArgs* f, const Step& st
   }
 }
 
-// result = alpha add + beta P Q^T (or P Q), `count` matrices.
+// A group's product: result = alpha add + beta P Q^T (or P Q).
+struct Operation {
+  Shape result;
+  int64_t k, count;
+  const __half *p, *q, *add;
+  __half* out;
+};
+
+// The kernels' arguments, for tiles of so many rows and columns, of which a
+// CTA copies lines_p of P's lines and lines_q of Q's.
 template <int kMode>
-bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* p, const __half* q, const __half* add, __half* out,
-                   float alpha, float beta, int passes, const FinalArgs* f, const Step& st, const DeviceState& d, cudaStream_t stream) {
+bwd_status fill_args(ProductArgs& a, const Operation& o, int rows, int cols, int lines_p, int lines_q, int passes, float alpha, float beta) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
-  const auto waves = [&](int bn) { return (count * tiles_of(result, kBM, bn, kSymmetric) + d.pairs - 1) / d.pairs; };
-  const int64_t kblocks = (k + kBK - 1) / kBK, small = count * tiles_of(result, kSmallRows, kSmallCols, kSymmetric);
-  int64_t split = kblocks < kMaxSplit ? kblocks : kMaxSplit;
-  while (split > 1 && small > d.clusters[split]) --split;
+  a.add_at = o.add; a.out_at = o.out;
+  a.m = static_cast<int>(o.result.m); a.n = static_cast<int>(o.result.n); a.pitch = static_cast<int>(up(o.result.n, 64));
+  a.kblocks = static_cast<int>((o.k + kBK - 1) / kBK);
+  a.passes = passes;
+  a.tiles_m = static_cast<int>((o.result.m + rows - 1) / rows); a.tiles_n = static_cast<int>((o.result.n + cols - 1) / cols);
+  const int64_t tiles = tiles_of(o.result, rows, cols, kSymmetric);
+  if (tiles * o.count > 0x3fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
+  a.tiles = static_cast<int>(tiles); a.items = a.whole = static_cast<int>(tiles * o.count);
+  a.alpha = alpha; a.beta = beta;
+  // P: lines along k; Q: its lines along k, or its rows along the result's columns
+  const bwd_status s = plane_map(&a.p, o.p, o.result.m, up(o.k, 64), 2 * o.count, kBK, lines_p);
+  if (s != BWD_OK) return s;
+  return kSymmetric ? plane_map(&a.q, o.q, o.result.m, up(o.k, 64), 2 * o.count, kBK, lines_q)
+                    : plane_map(&a.q, o.q, o.k, up(o.result.n, 64), 2 * o.count, 64, kBK);
+}
+
+// CTAs that divide the summed axis of small products: as many as find an SM.
+int small_split(int64_t tiles, int64_t kblocks, const DeviceState& d) {
+  int split = static_cast<int>(kblocks < kMaxSplit ? kblocks : kMaxSplit);
+  while (split > 1 && tiles > d.clusters[split]) --split;
+  return split;
+}
+
+template <int kMode>
+bwd_status products(const Operation* o, int groups, float alpha, float beta, int passes, const FinalArgs* f, const Step& st,
+                    const DeviceState& d, cudaStream_t stream) {
+  static thread_local SmallCall c;
+  c.groups = groups;
+  int64_t tiles = 0, kblocks = 1;
+  for (int i = 0; i < groups; ++i) {
+    const bwd_status s = fill_args<kMode>(c.g[i], o[i], kSmallRows, kSmallCols, kSmallRows, kSmallCols, passes, alpha, beta);
+    if (s != BWD_OK) return s;
+    c.start[i] = static_cast<int>(tiles);
+    tiles += c.g[i].items;
+    kblocks = std::max<int64_t>(kblocks, c.g[i].kblocks);
+  }
+  c.split = small_split(tiles, kblocks, d);
+  return launch_small<kMode>(c, static_cast<int>(tiles), f, st, stream);
+}
+
+// One group's product, by whichever kernel takes less time.
+template <int kMode>
+bwd_status product(const Operation& o, float alpha, float beta, int passes, const FinalArgs* f, const Step& st, const DeviceState& d,
+                   cudaStream_t stream) {
+  constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
+  const auto waves = [&](int bn) { return (o.count * tiles_of(o.result, kBM, bn, kSymmetric) + d.pairs - 1) / d.pairs; };
+  const int64_t kblocks = (o.k + kBK - 1) / kBK, small = o.count * tiles_of(o.result, kSmallRows, kSmallCols, kSymmetric);
+  const int split = small_split(small, kblocks, d);
   // Small tiles where they take less time than the large ones.  In us: a stage
   // of a small tile 0.2, and 0.5 where all SMs read (48 KB each, 14.6 TB/s from
   // L2); of a large one, a third of that work for four or eight times the tile,
@@ -1115,82 +1206,93 @@ bwd_status product(const Shape& result, int64_t k, int64_t count, const __half* 
   const double small_time = static_cast<double>(small_waves) * (5.0 + stage * static_cast<double>((kblocks + split - 1) / split));
   const double large_time = 8.0 + std::min(0.24 * static_cast<double>(waves(128)), 0.36 * static_cast<double>(waves(256))) *
                                       static_cast<double>(passes * kblocks);
-  const bool is_small = small_time < large_time;
+  if (small_time < large_time) return products<kMode>(&o, 1, alpha, beta, passes, f, st, d, stream);
   // a tile of 256 columns takes up to one and a half times as long as one of 128
-  const int rows = is_small ? kSmallRows : kBM, bn = is_small ? kSmallCols : 3 * waves(256) < 2 * waves(128) ? 256 : 128;
+  const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
   ProductArgs a{};
-  a.add_at = add; a.out_at = out;
-  a.m = static_cast<int>(result.m); a.n = static_cast<int>(result.n); a.pitch = static_cast<int>(up(result.n, 64));
-  a.kblocks = static_cast<int>(kblocks);
-  a.passes = passes;
-  a.split = static_cast<int>(split);
-  a.tiles_m = static_cast<int>((result.m + rows - 1) / rows); a.tiles_n = static_cast<int>((result.n + bn - 1) / bn);
-  const int64_t tiles = tiles_of(result, rows, bn, kSymmetric);
-  if (tiles * count > 0x3fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
-  a.tiles = static_cast<int>(tiles); a.items = static_cast<int>(tiles * count);
-  const int64_t last = a.items % d.pairs;
-  const bool halves = !is_small && bn == 256 && 2 * last <= d.pairs;
-  a.whole = static_cast<int>(halves ? a.items - last : a.items);
-  a.items += a.items - a.whole;
-  a.alpha = alpha; a.beta = beta;
-  // P: `m` lines along k; Q: its lines along k, or its rows along the result's
-  // columns.  Of a pair's tile each CTA copies half of Q's lines.
-  const int lines_p = is_small ? rows : rows / 2, lines_q = is_small ? bn : bn / 2;
-  bwd_status s = plane_map(&a.p, p, result.m, up(k, 64), 2 * count, kBK, lines_p);
+  // of a pair's tile each CTA copies half of either operand's lines
+  bwd_status s = fill_args<kMode>(a, o, kBM, bn, kBM / 2, bn / 2, passes, alpha, beta);
+  if (s == BWD_OK && o.add) s = plane_map(&a.add, o.add, o.result.m, a.pitch, 2 * o.count, 32, 32);
+  if (s == BWD_OK && o.out) s = plane_map(&a.out, o.out, o.result.m, a.pitch, 2 * o.count, 32, 32);
   if (s != BWD_OK) return s;
-  s = kSymmetric ? plane_map(&a.q, q, result.m, up(k, 64), 2 * count, kBK, lines_q) : plane_map(&a.q, q, k, up(result.n, 64), 2 * count, 64, kBK);
-  if (s == BWD_OK && add && !is_small) s = plane_map(&a.add, add, result.m, a.pitch, 2 * count, 32, 32);
-  if (s == BWD_OK && out && !is_small) s = plane_map(&a.out, out, result.m, a.pitch, 2 * count, 32, 32);
-  if (s != BWD_OK) return s;
-  if (is_small) return launch_small<kMode>(a, f, st, stream);
+  const int last = a.items % d.pairs;
+  if (bn == 256 && 2 * last <= d.pairs) {
+    a.whole = a.items - last;
+    a.items += last;
+  }
   return bn == 256 ? launch_product<256, kMode>(a, f, st, d.pairs, stream) : launch_product<128, kMode>(a, f, st, d.pairs, stream);
 }
 
 template <bool kMomentum>
-bwd_status prepare(const PrepareArgs& a, int64_t count, int type, cudaStream_t st) {
-  const dim3 by_chunk(static_cast<unsigned>(a.chunks), static_cast<unsigned>(count));
-  const dim3 by_tile(static_cast<unsigned>((a.pitch + a.split_cols - 1) / a.split_cols),
-                     static_cast<unsigned>((a.m + kSplitRows - 1) / kSplitRows), static_cast<unsigned>(count));
+bwd_status prepare(const PrepareArgs& a, int norm_ctas, int split_ctas, int type, cudaStream_t st) {
   const auto go = [&](auto norm, auto split) {
-    const bwd_status s = launch_ex(norm, by_chunk, kThreads, 0, 0, st, "ns_norm_kernel launch", a);
-    return s == BWD_OK ? launch_ex(split, by_tile, kThreads, 0, 0, st, "ns_split_kernel launch", a) : s;
+    const bwd_status s = launch_ex(norm, dim3(static_cast<unsigned>(norm_ctas)), kThreads, 0, 0, st, "ns_norm_kernel launch", a);
+    return s == BWD_OK ? launch_ex(split, dim3(static_cast<unsigned>(split_ctas)), kThreads, 0, 0, st, "ns_split_kernel launch", a) : s;
   };
   if (type == BWD_F32) return go(ns_norm_kernel<kF32, kMomentum>, ns_split_kernel<kF32, kMomentum>);
   if (type == BWD_BF16) return go(ns_norm_kernel<kBF16, kMomentum>, ns_split_kernel<kBF16, kMomentum>);
   return go(ns_norm_kernel<kF16, kMomentum>, ns_split_kernel<kF16, kMomentum>);
 }
 
-// All of one batch: matrices of one shape, in either orientation.
-bwd_status run_batch(const Matrices& x, int64_t count, const Shape& s, const Step& st, uint8_t* work, const DeviceState& d, cudaStream_t stream) {
-  Pieces pieces{work};
-  double* const slots = reinterpret_cast<double*>(pieces.take(8 * kSlots * count));
-  __half* xs[2] = {reinterpret_cast<__half*>(pieces.take(s.x_bytes() * count)), reinterpret_cast<__half*>(pieces.take(s.x_bytes() * count))};
-  __half* const gram = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * count));
-  __half* const poly = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * count));
+bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* work, const DeviceState& d, cudaStream_t stream) {
   static thread_local PrepareArgs a;
   static thread_local FinalArgs f;
-  a.x = x; a.slots = slots; a.grad_scale = st.grad_scale; a.planes = xs[0];
-  a.size = s.m * s.n;
-  a.chunk = up((a.size + kSlots - 1) / kSlots, 8 * kThreads);
-  a.chunks = static_cast<int>((a.size + a.chunk - 1) / a.chunk);
-  a.m = static_cast<int>(s.m); a.n = static_cast<int>(s.n); a.pitch = static_cast<int>(up(s.n, 64));
-  // each CTA adds up the norm's parts: four tiles share that where there are many
-  a.split_cols = count * ((s.m + 63) / 64) * ((s.n + 63) / 64) > 2048 ? 256 : 64;
+  a.x = f.x = x;
+  a.grad_scale = f.grad_scale = st.grad_scale;
   a.momentum = st.momentum; a.nesterov = st.nesterov;
-  bwd_status e = st.has_momentum ? prepare<true>(a, count, st.g_type, stream) : prepare<false>(a, count, st.g_type, stream);
-  f.x = x; f.grad_scale = st.grad_scale; f.decay = st.decay;
-  f.step = static_cast<float>(st.step * std::sqrt(static_cast<double>(s.n)));
-  const Shape square{s.m, s.m};
+  a.groups = set.groups;
+  f.decay = st.decay;
+  Pieces pieces{work};
+  a.slots = reinterpret_cast<double*>(pieces.take(8 * kSlots * set.count()));
+  struct Planes {
+    __half *x[2], *gram, *poly;
+  } planes[kGroups];
+  int64_t norm_ctas = 0, split_ctas = 0;
+  for (int i = 0; i < set.groups; ++i) {
+    const Group& g = set.g[i];
+    const Shape& s = g.s;
+    for (__half** at : {&planes[i].x[0], &planes[i].x[1]}) *at = reinterpret_cast<__half*>(pieces.take(s.x_bytes() * g.count));
+    for (__half** at : {&planes[i].gram, &planes[i].poly}) *at = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * g.count));
+    PrepareGroup& p = a.g[i];
+    p.planes = planes[i].x[0];
+    p.size = s.m * s.n;
+    p.chunk = up((p.size + kSlots - 1) / kSlots, 8 * kThreads);
+    p.chunks = static_cast<int>((p.size + p.chunk - 1) / p.chunk);
+    p.m = static_cast<int>(s.m); p.n = static_cast<int>(s.n); p.pitch = static_cast<int>(up(s.n, 64));
+    // each CTA adds up the norm's parts: four tiles share that where there are many
+    p.split_cols = g.count * ((s.m + 63) / 64) * ((s.n + 63) / 64) > 2048 ? 256 : 64;
+    p.first = f.first[i] = static_cast<int>(g.first - set.g[0].first);
+    p.norm_start = static_cast<int>(norm_ctas); p.split_start = static_cast<int>(split_ctas);
+    norm_ctas += g.count * p.chunks;
+    split_ctas += g.count * ((p.pitch + p.split_cols - 1) / p.split_cols) * ((s.m + kSplitRows - 1) / kSplitRows);
+    f.step[i] = static_cast<float>(st.step * std::sqrt(static_cast<double>(s.n)));
+  }
+  if (split_ctas > 0x7fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
+  bwd_status e = st.has_momentum ? prepare<true>(a, static_cast<int>(norm_ctas), static_cast<int>(split_ctas), st.g_type, stream)
+                                 : prepare<false>(a, static_cast<int>(norm_ctas), static_cast<int>(split_ctas), st.g_type, stream);
   for (int i = 0; e == BWD_OK && i < st.steps; ++i) {
     const bool last = i + 1 == st.steps;
     const int passes = last && st.out_type == BWD_BF16 ? 1 : 3;
-    const __half* const from = xs[i % 2];
-    e = product<kGram>(square, s.n, count, from, from, nullptr, gram, 0.0f, 1.0f / kScale, passes, nullptr, st, d, stream);
-    if (e == BWD_OK)
-      e = product<kPoly>(square, s.m, count, gram, gram, gram, poly, kB, kC / kScale, passes, nullptr, st, d, stream);
-    if (e != BWD_OK) break;
-    e = last ? product<kFinal>(s, s.m, count, poly, from, from, nullptr, kA / kScale, 1.0f / (kScale * kScale), passes, &f, st, d, stream)
-             : product<kApply>(s, s.m, count, poly, from, from, xs[(i + 1) % 2], kA, 1.0f / kScale, passes, nullptr, st, d, stream);
+    Operation gram[kGroups], poly[kGroups], apply[kGroups];
+    for (int j = 0; j < set.groups; ++j) {
+      const Shape& s = set.g[j].s;
+      const Shape square{s.m, s.m};
+      const Planes& p = planes[j];
+      const __half* const from = p.x[i % 2];
+      gram[j] = Operation{square, s.n, set.g[j].count, from, from, nullptr, p.gram};
+      poly[j] = Operation{square, s.m, set.g[j].count, p.gram, p.gram, p.gram, p.poly};
+      apply[j] = Operation{s, s.m, set.g[j].count, p.poly, from, from, last ? nullptr : p.x[(i + 1) % 2]};
+    }
+    const auto run = [&](auto mode, const Operation* o, float alpha, float beta) {
+      constexpr int kMode = decltype(mode)::value;
+      if (e != BWD_OK) return;
+      e = set.small ? products<kMode>(o, set.groups, alpha, beta, passes, &f, st, d, stream)
+                    : product<kMode>(o[0], alpha, beta, passes, &f, st, d, stream);
+    };
+    run(std::integral_constant<int, kGram>{}, gram, 0.0f, 1.0f / kScale);
+    run(std::integral_constant<int, kPoly>{}, poly, kB, kC / kScale);
+    if (last) run(std::integral_constant<int, kFinal>{}, apply, kA / kScale, 1.0f / (kScale * kScale));
+    else run(std::integral_constant<int, kApply>{}, apply, kA, 1.0f / kScale);
   }
   return e;
 }
@@ -1208,18 +1310,44 @@ bwd_status order(int32_t count, const int64_t* rows, const int64_t* cols, std::v
   return BWD_OK;
 }
 
-// Calls f(first, number, shape, matrices of one batch) for each group.
+// Calls f(set) for matrices in that order, set by set.  Shapes with few tiles
+// share sets of up to kBatch matrices and kGroups shapes; the others have sets
+// of their own, of equal numbers and kWorkMost bytes at most.
 template <typename F>
-bwd_status each_group(const std::vector<int32_t>& at, const int64_t* rows, const int64_t* cols, F f) {
-  for (size_t i = 0; i < at.size();) {
+bwd_status each_set(const std::vector<int32_t>& at, const int64_t* rows, const int64_t* cols, F f) {
+  constexpr int64_t kFewTiles = 256;
+  Set few{};
+  few.small = true;
+  const auto flush = [&] {
+    const bwd_status e = few.groups ? f(few) : BWD_OK;
+    few.groups = 0;
+    return e;
+  };
+  const int64_t all = static_cast<int64_t>(at.size());
+  for (int64_t i = 0, j; i < all; i = j) {
     const Shape s = shape_of(rows[at[i]], cols[at[i]]);
-    size_t j = i;
-    while (j < at.size() && !(s < shape_of(rows[at[j]], cols[at[j]]))) ++j;
-    const bwd_status e = f(i, static_cast<int64_t>(j - i), s);
-    if (e != BWD_OK) return e;
-    i = j;
+    for (j = i; j < all && !(s < shape_of(rows[at[j]], cols[at[j]]));) ++j;
+    const int64_t number = j - i;
+    if (number <= kBatch && number * tiles_of(s, kSmallRows, kSmallCols, false) <= kFewTiles) {
+      // a set's matrices follow one another
+      if (few.groups && (few.groups == kGroups || few.count() + number > kBatch || few.g[few.groups - 1].first + few.g[few.groups - 1].count != i))
+        if (const bwd_status e = flush()) return e;
+      few.g[few.groups++] = Group{s, i, number};
+      continue;
+    }
+    Set one{};
+    one.groups = 1;
+    one.g[0] = Group{s, i, 1};
+    int64_t most = kWorkMost / one.bytes();
+    most = most < 1 ? 1 : most > kBatch ? kBatch : most;
+    const int64_t sets = (number + most - 1) / most, each = (number + sets - 1) / sets;
+    for (int64_t b = i; b < j; b += each) {
+      one.g[0].first = b;
+      one.g[0].count = std::min(each, j - b);
+      if (const bwd_status e = f(one)) return e;
+    }
   }
-  return BWD_OK;
+  return flush();
 }
 
 bwd_status run(int32_t count, const void* const* g, float* const* mom, void* const* out, const int64_t* rows, const int64_t* cols,
@@ -1244,21 +1372,15 @@ bwd_status run(int32_t count, const void* const* g, float* const* mom, void* con
   DeviceState d;
   if ((s = ensure_device(&d)) != BWD_OK) return s;
   static thread_local Matrices x;
-  return each_group(at, rows, cols, [&](size_t first, int64_t number, const Shape& shape) {
-    const int64_t batch = batch_of(shape, number);
-    for (int64_t b = 0; b < number; b += batch) {
-      const int64_t n = number - b < batch ? number - b : batch;
-      for (int64_t z = 0; z < n; ++z) {
-        const int32_t i = at[first + b + z];
-        x.g[z] = g[i];
-        x.mom[z] = st.has_momentum ? mom[i] : nullptr;
-        x.out[z] = out[i];
-        x.tall[z] = rows[i] > cols[i];
-      }
-      const bwd_status e = run_batch(x, n, shape, st, static_cast<uint8_t*>(work), d, static_cast<cudaStream_t>(stream));
-      if (e != BWD_OK) return e;
+  return each_set(at, rows, cols, [&](const Set& set) {
+    for (int64_t z = 0; z < set.count(); ++z) {
+      const int32_t i = at[static_cast<size_t>(set.g[0].first + z)];
+      x.g[z] = g[i];
+      x.mom[z] = st.has_momentum ? mom[i] : nullptr;
+      x.out[z] = out[i];
+      x.tall[z] = rows[i] > cols[i];
     }
-    return BWD_OK;
+    return run_set(x, set, st, static_cast<uint8_t*>(work), d, static_cast<cudaStream_t>(stream));
   });
 } catch (const std::bad_alloc&) {
   return fail(BWD_ERR_INVALID_ARG, "out of host memory");
@@ -1280,13 +1402,8 @@ int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows, const i
   std::vector<int32_t> at;
   if (count < 0 || (count > 0 && (!rows || !cols)) || order(count, rows, cols, &at) != BWD_OK) return -1;
   int64_t most = 0;
-  each_group(at, rows, cols, [&](size_t, int64_t number, const Shape& s) {
-    const int64_t batch = batch_of(s, number);
-    Pieces pieces{nullptr};
-    pieces.take(8 * kSlots * batch);
-    for (int i = 0; i < 2; ++i) pieces.take(s.x_bytes() * batch);
-    for (int i = 0; i < 2; ++i) pieces.take(s.a_bytes() * batch);
-    if (pieces.used > most) most = pieces.used;
+  each_set(at, rows, cols, [&](const Set& set) {
+    most = std::max(most, set.bytes());
     return BWD_OK;
   });
   return most;

@@ -64,10 +64,12 @@ def test_work_bytes(abi):
     # two pairs of 100 x 320 and two of 100 x 128 fp16 values, the norms' parts
     assert one == 2 * 4 * 100 * 320 + 2 * 4 * 100 * 128 + 8 * 512
     assert size(2, i64(100, 300), i64(300, 100)) == 2 * one
-    # other shapes take turns
-    assert size(2, i64(100, 10), i64(300, 10)) == one
+    # small matrices of other shapes are worked on together, large ones take turns
+    assert size(2, i64(100, 10), i64(300, 10)) == one + 4 * 2560 + 8 * 512
+    large = size(1, i64(3000), i64(4000))
+    assert size(2, i64(3000, 2000), i64(4000, 3000)) == large == size(3, i64(3000, 100, 2000), i64(4000, 300, 3000))
     # more than a launch takes, in equal parts
-    assert size(65, i64(*[100] * 65), i64(*[300] * 65)) == 33 * one - 32 * 8 * 512 + 32 * 8 * 512
+    assert size(65, i64(*[100] * 65), i64(*[300] * 65)) == 33 * one
 
 
 def test_python_refuses():

@@ -195,6 +195,17 @@ def test_step(muon, p_type, g_type, nesterov):
         assert all(torch.equal(b[1], g) for b, g in zip(before, gs))
 
 
+def test_many_shapes_at_once(muon):
+    """More shapes than one launch takes, more matrices than that, and large ones between them."""
+    shapes = [(20 + 7 * i, 50 + 31 * (i % 5)) for i in range(19)] + [(700, 1900), (40, 30), (1900, 700)] + [(33, 65)] * 50 + [(1, 1)]
+    ps, gs, ms = lists(shapes, torch.float32, torch.float32)
+    before = [(p.clone(), g.clone(), m.clone()) for p, g, m in zip(ps, gs, ms)]
+    hp = dict(lr=0.1, momentum=0.9)
+    muon.MuonArgs(ps, gs, ms).step(**hp)
+    for b, p, m in zip(before, ps, ms):
+        check_step(b, (p, m), **hp)
+
+
 def test_a_factor_that_is_not_finite_writes_nothing(muon):
     ps, gs, ms = lists(SET, torch.float32, torch.float32)
     before = [t.clone() for t in ps + ms]
