@@ -718,11 +718,14 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
 // high have accumulators of their own; a thread adds them up, sends each unit
 // of 8 columns to the CTA that gathers it over distributed shared memory, and
 // that one adds the cluster's parts in the order of the ranks.
-constexpr int kSmallRows = 128, kSmallCols = 64, kSmallStages = 4;
+constexpr int kSmallRows = 128, kSmallCols = 64, kSmallStages = 2;
 constexpr int kSmallThreads = 320;  // warp 0 copies, warp 1 issues, eight add up and store
 constexpr int kSmallP = kSmallRows * kBK * 2, kSmallQ = kSmallCols * kBK * 2, kSmallStage = 2 * (kSmallP + kSmallQ);
 constexpr int kSmallSmem = 1024 + kSmallStages * kSmallStage;
-constexpr int kSmallAccs = static_cast<int>(kTmemCols) / kSmallCols - 1;  // of high x high
+// Two CTAs fit an SM and its tensor memory, so that the next product's begin
+// while this one's still run.
+constexpr uint32_t kSmallTmem = kTmemCols / 2;
+constexpr int kSmallAccs = static_cast<int>(kSmallTmem) / kSmallCols - 1;  // of high x high
 constexpr int kMaxSplit = 8;
 constexpr int kUnit = 8, kUnits = kSmallCols / kUnit;  // columns that move together
 static_assert((kUnits + kMaxSplit - 1) * kSmallRows * kUnit * 4 <= kSmallStages * kSmallStage, "the gathered parts take the stages' place");
@@ -740,13 +743,13 @@ struct Pair8 {
 };
 
 template <int kMode, int kT, bool kUpdate>
-__global__ void __launch_bounds__(kSmallThreads, 1)
+__global__ void __launch_bounds__(kSmallThreads, 2)
 ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
   constexpr bool kTrans = kMode == kApply || kMode == kFinal;  // q's summed axis is its rows
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* const parts = reinterpret_cast<float*>(sm);  // [rank][unit of the share][row][8], once the stages are done with
+  float* const parts = reinterpret_cast<float*>(sm);  // [rank][unit of the share][half][row][4], once the stages are done with
   __shared__ __align__(8) uint64_t s_full[kSmallStages], s_empty[kSmallStages], s_done;
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
@@ -771,7 +774,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(kSmallTmem) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   __syncwarp();
@@ -870,13 +873,13 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
       }
 #pragma unroll
       for (int j = 0; j < 16; j += kUnit) {
-        const uint32_t unit = (c0 + j) / kUnit, to = unit / share, at = ((rank * share + unit - to * share) * kSmallRows + row) * kUnit;
+        const uint32_t unit = (c0 + j) / kUnit, to = unit / share, at = ((rank * share + unit - to * share) * 2 * kSmallRows + row) * 4;
         uint32_t dst;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(dst) : "r"(smem_u32(parts + at)), "r"(to));
 #pragma unroll
         for (int q = 0; q < kUnit; q += 4)
           asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};"
-                       ::"r"(dst + 4 * q), "f"(sum[j + q]), "f"(sum[j + q + 1]), "f"(sum[j + q + 2]), "f"(sum[j + q + 3]) : "memory");
+                       ::"r"(dst + 4 * q * kSmallRows), "f"(sum[j + q]), "f"(sum[j + q + 1]), "f"(sum[j + q + 2]), "f"(sum[j + q + 3]) : "memory");
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -897,8 +900,8 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = 0.0f;
       for (int q = 0; q < call.split; ++q) {
-        const float4* const from = reinterpret_cast<const float4*>(parts + ((q * share + u) * kSmallRows + row) * kUnit);
-        const float4 x = from[0], y = from[1];
+        const float4* const from = reinterpret_cast<const float4*>(parts) + (q * share + u) * 2 * kSmallRows + row;
+        const float4 x = from[0], y = from[kSmallRows];
         v[0] = __fadd_rn(v[0], x.x); v[1] = __fadd_rn(v[1], x.y); v[2] = __fadd_rn(v[2], x.z); v[3] = __fadd_rn(v[3], x.w);
         v[4] = __fadd_rn(v[4], y.x); v[5] = __fadd_rn(v[5], y.y); v[6] = __fadd_rn(v[6], y.z); v[7] = __fadd_rn(v[7], y.w);
       }
@@ -943,7 +946,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
       }
     }
   }
-  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSmallTmem));
 }
 
 // --------------------------------------------------------------------------
@@ -1058,8 +1061,14 @@ bwd_status ensure_device(DeviceState* out) {
     e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of<256, kApply, kF16, false>(), &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
     if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
+    // with so much shared memory that no SM takes two
+    int smem = 0;
+    e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
+    smem = std::max(smem / 2, kSmallSmem);
+    if (e == cudaSuccess) e = opt_in(ns_small_kernel<kApply, kF32, false>, smem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
     cfg.blockDim = dim3(kSmallThreads);
-    cfg.dynamicSmemBytes = kSmallSmem;
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     d.clusters[1] = sms;
     for (int c = 2; c <= kMaxSplit; ++c) {
       cfg.gridDim = dim3(static_cast<unsigned>(sms / c * c));
@@ -1162,6 +1171,9 @@ bwd_status fill_args(ProductArgs& a, const Operation& o, int rows, int cols, int
 }
 
 // CTAs that divide the summed axis of small products: as many as find an SM.
+// (Timestamps in the kernel, 301 x 777: from the inputs to the last product
+// 1.4 us with one or two stages to a CTA and 3.3 with five; the exchange of the
+// parts costs less than that, and divides the storing too.)
 int small_split(int64_t tiles, int64_t kblocks, const DeviceState& d) {
   int split = static_cast<int>(kblocks < kMaxSplit ? kblocks : kMaxSplit);
   while (split > 1 && tiles > d.clusters[split]) --split;
