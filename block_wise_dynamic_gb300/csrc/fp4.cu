@@ -115,6 +115,13 @@ __device__ __forceinline__ void load8(const char* src, int64_t left, float (&v)[
   }
 }
 
+// Bytes of a warp's 256 columns.  Where rows are not made of 16-byte pieces,
+// they pass through shared memory on the way, so that a warp's access to them
+// is one run of units (6391 x 9011 fp16 read back: 151 us with eight values to
+// a lane).
+template <int kT> __host__ __device__ constexpr int strip_bytes() { return kStageK * elem_bytes<kT>(); }
+template <int kT, typename Unit> __host__ __device__ constexpr bool staged() { return sizeof(Unit) < 16; }
+
 // A lane's eight codes, and the bytes of the four blocks that its half warp
 // holds in one word.
 __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int lane, uint32_t* word) {
@@ -135,16 +142,53 @@ __device__ __forceinline__ uint32_t quantize8(const float (&v)[8], int lane, uin
 template <int kT, typename Unit>
 __global__ void __launch_bounds__(32 * kWarps)
 fp4_quantize_kernel(const QuantArgs a) {
+  constexpr bool kStaged = staged<kT, Unit>();
+  constexpr int kLoads = strip_bytes<kT>() / (32 * static_cast<int>(sizeof(Unit)));
+  __shared__ __align__(16) uint8_t s_strip[kStaged ? kWarps : 1][kStaged ? kEach * strip_bytes<kT>() : 16];
   wait_for_inputs();
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kStageK + 8 * lane, left = a.cols - c;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kStageK, c = c0 + 8 * lane, left = a.cols - c;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kRows + warp;
   float v[kEach][8];
+  if constexpr (kStaged) {
+    Unit* const strip = reinterpret_cast<Unit*>(s_strip[warp]);
+    const int64_t here = (a.cols - c0) * elem_bytes<kT>();
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int64_t r = r0 + i * kWarps;
-    load8<kT, Unit>(static_cast<const char*>(a.x) + (r * a.ld + c) * elem_bytes<kT>(), r < a.rows ? left : 0, v[i]);
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t r = r0 + i * kWarps;
+      const Unit* const src = reinterpret_cast<const Unit*>(static_cast<const char*>(a.x) + (r * a.ld + c0) * elem_bytes<kT>());
+      Unit u[kLoads];
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q)
+        u[q] = r < a.rows && (32 * q + lane) * static_cast<int>(sizeof(Unit)) < here ? __ldcs(src + 32 * q + lane) : Unit{};
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) strip[(i * kLoads + q) * 32 + lane] = u[q];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const uint4* const from = reinterpret_cast<const uint4*>(s_strip[warp] + i * strip_bytes<kT>()) + lane * (8 * elem_bytes<kT>() / 16);
+      uint4 w[8 * elem_bytes<kT>() / 16];
+#pragma unroll
+      for (int q = 0; q < 8 * elem_bytes<kT>() / 16; ++q) w[q] = from[q];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (kT == kF32) {
+          v[i][j] = __uint_as_float((&w[j / 4].x)[j % 4]);
+        } else {
+          const uint32_t h = (&w[0].x)[j / 2];
+          v[i][j] = kT == kBF16 ? __uint_as_float(j % 2 ? h & 0xffff0000u : h << 16)
+                                : __half2float(__ushort_as_half(static_cast<unsigned short>(j % 2 ? h >> 16 : h & 0xffffu)));
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t r = r0 + i * kWarps;
+      load8<kT, Unit>(static_cast<const char*>(a.x) + (r * a.ld + c) * elem_bytes<kT>(), r < a.rows ? left : 0, v[i]);
+    }
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -167,20 +211,21 @@ struct DequantArgs {
 template <int kT, typename Unit>
 __global__ void __launch_bounds__(32 * kWarps)
 fp4_dequantize_kernel(const DequantArgs a) {
-  constexpr int kEb = elem_bytes<kT>(), kVals = sizeof(Unit) / kEb;
+  constexpr bool kStaged = staged<kT, Unit>();
+  constexpr int kEb = elem_bytes<kT>(), kPieces = 8 * kEb / 16, kStores = strip_bytes<kT>() / (32 * static_cast<int>(sizeof(Unit)));
+  __shared__ __align__(16) uint8_t s_strip[kStaged ? kWarps : 1][kStaged ? strip_bytes<kT>() : 16];
   wait_for_inputs();
   let_next_begin();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kStageK + 8 * lane;
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kStageK, c = c0 + 8 * lane;
   const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kRows + warp;
-  if (c >= a.cols) return;
   uint32_t codes[kEach], byte[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int64_t r = r0 + i * kWarps;
-    if (r >= a.rows) continue;
-    codes[i] = __ldcs(reinterpret_cast<const uint32_t*>(a.codes + r * a.pitch + c / 2));
-    byte[i] = a.scales[scale_word(r, 2 * blockIdx.x + lane / 16, a.groups) + lane / 4 % 4];
+    const bool in = r < a.rows && c < a.cols;
+    codes[i] = in ? __ldcs(reinterpret_cast<const uint32_t*>(a.codes + r * a.pitch + c / 2)) : 0u;
+    byte[i] = in ? a.scales[scale_word(r, 2 * blockIdx.x + lane / 16, a.groups) + lane / 4 % 4] : 0u;
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -189,21 +234,28 @@ fp4_dequantize_kernel(const DequantArgs a) {
     float v[8];
     values8(codes[i], v);
     const float s = scale_value(byte[i]);
-    Unit* const to = reinterpret_cast<Unit*>(static_cast<char*>(a.out) + (r * a.cols + c) * kEb);
+    uint4 w[kPieces];
 #pragma unroll
-    for (int q = 0; q < 8 / kVals; ++q) {
-      Unit u;
-      if constexpr (kT == kF32) {
+    for (int j = 0; j < 8; j += kEb == 4 ? 1 : 2) {
+      if constexpr (kT == kF32) (&w[j / 4].x)[j % 4] = __float_as_uint(__fmul_rn(v[j], s));
+      else (&w[0].x)[j / 2] = pack16<kT>(__fmul_rn(v[j], s), __fmul_rn(v[j + 1], s));
+    }
+    char* const to = static_cast<char*>(a.out) + (r * a.cols + c0) * kEb;
+    if constexpr (kStaged) {
+      __syncwarp();
 #pragma unroll
-        for (int j = 0; j < kVals; ++j) reinterpret_cast<float*>(&u)[j] = __fmul_rn(v[q * kVals + j], s);
-      } else if constexpr (kVals == 1) {
-        u = static_cast<uint16_t>(pack16<kT>(__fmul_rn(v[q], s), 0.0f));
-      } else {
+      for (int q = 0; q < kPieces; ++q) reinterpret_cast<uint4*>(s_strip[warp])[lane * kPieces + q] = w[q];
+      __syncwarp();
+      const int64_t here = (a.cols - c0) * kEb;
 #pragma unroll
-        for (int j = 0; j < kVals; j += 2)
-          reinterpret_cast<uint32_t*>(&u)[j / 2] = pack16<kT>(__fmul_rn(v[q * kVals + j], s), __fmul_rn(v[q * kVals + j + 1], s));
+      for (int q = 0; q < kStores; ++q) {
+        const int at = (32 * q + lane) * static_cast<int>(sizeof(Unit));
+        if (at < here) *reinterpret_cast<Unit*>(to + at) = *reinterpret_cast<const Unit*>(s_strip[warp] + at);
       }
-      if (c + q * kVals < a.cols) to[q] = u;
+    } else if (c < a.cols) {
+#pragma unroll
+      for (int q = 0; q < kPieces; ++q)
+        if (c + 16 / kEb * q < a.cols) reinterpret_cast<uint4*>(to)[lane * kPieces + q] = w[q];
     }
   }
 }
@@ -511,6 +563,7 @@ fp4_matmul_kernel(const __grid_constant__ MmArgs p) {
           const auto put_rows = [&](auto unit, int rows, int bytes) {
             using Unit = decltype(unit);
             constexpr int kBytes = sizeof(Unit);
+#pragma unroll 16
             for (int at = lane * kBytes; at < rows * 128; at += 32 * kBytes) {
               const int r = at / 128, byte = at % 128;
               if (byte < bytes)
@@ -551,9 +604,13 @@ fp4_matmul_kernel(const __grid_constant__ MmArgs p) {
 // Up to kFuse rows, A may also come unquantized: the warps that store in the
 // end then quantize each stage's 256 columns on the way into shared memory
 // while the weight's copies are under way, which saves the quantizer's launch
-// and its results' way through memory.
+// and its results' way through memory.  Every CTA of a rank quantizes the same
+// part of A again, so this pays for few rows only (4096 x 4096, weight in L2: 1
+// row 4.3 us, 8 rows 6.0 and 16 rows 8.6; 17 rows in two kernels 5.6, with some
+// 4 more on the host).
 
-constexpr int kFuse = 16;
+constexpr int kFuse = 8;
+constexpr int kFewest = 16;  // columns of its products
 constexpr int kFewThreads = 320;  // warp 0 copies, warp 1 issues, warps 2 to 9 store
 template <int kBN> __host__ __device__ constexpr int few_stages() { return kBN == 128 ? 3 : kBN >= 32 ? 4 : 5; }
 template <int kBN> __host__ __device__ constexpr int few_stage_bytes() { return kTile * kStageBytes + kBN * kStageBytes; }
@@ -572,7 +629,7 @@ template <int kBN> __host__ __device__ constexpr int few_accs() { return static_
 constexpr int kMaxSplit = 8;  // CTAs of a portable cluster
 // Longest row of A that the kernel quantizes for fp32 results: longer ones
 // leave the accumulators of a cluster's CTAs more than kChunk stages each.
-constexpr int64_t kFuseCols = int64_t{kMaxSplit} * few_accs<kFuse>() * kChunk * kStageK;
+constexpr int64_t kFuseCols = int64_t{kMaxSplit} * few_accs<kFewest>() * kChunk * kStageK;
 
 struct FewArgs {
   CUtensorMap map_w, map_x;  // rows of B in boxes of 128, of A in boxes of kBN
@@ -605,7 +662,7 @@ __device__ __forceinline__ void few_load(const FewArgs& p, int line, int c, floa
 template <int kT, int kBN, bool kFused>
 __global__ void __launch_bounds__(kFewThreads, 2)
 fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
-  static_assert(!kFused || kBN == kFuse, "scales of up to 32 rows lie in one column");
+  static_assert(!kFused || kBN == kFewest, "scales of up to 32 rows lie in one column");
   constexpr int kStages = few_stages<kBN>(), kW = kTile * kStageBytes, kStage = few_stage_bytes<kBN>(), kAccs = few_accs<kBN>();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -635,7 +692,7 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
   if (warp == 0) {
     if (elect_one()) {
       s_fail = 0;
-      for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], kFused ? 2 : 1); mbar_init(&s_empty[i], 1); }
+      for (int i = 0; i < kStages; ++i) { mbar_init(&s_full[i], kFused ? 1 + p.m : 1); mbar_init(&s_empty[i], 1); }
       mbar_init(&s_done, 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
       // the first stages' weights, at once where they do not depend on the kernel ahead
@@ -706,36 +763,34 @@ fp4_matmul_few_kernel(const __grid_constant__ FewArgs p) {
     }
     if (one) commit_one(&s_done);
   } else if constexpr (kFused) {
-    // A warp to each stage of the ring, a row at a time, eight columns to a
-    // lane.  A warp sees every phase of its own stage's barrier.
-    static_assert(kStages <= kFewThreads / 32 - 2, "a warp to each stage");
+    // The eight warps take turns at units of a row of a stage, eight columns
+    // to a lane, and have kAtOnce units' loads under way.  A unit's wait is for
+    // the phase before its own, which cannot end before the unit does.
     wait_for_inputs();
-    const int s = warp - 2;
-    uint32_t phase = 1;
-    uint8_t* const codes = sm + s * kStage + kW;
-    uint8_t* const scales = sf + s * 2 * kSfTile + kSfTile;
-    for (int i = s < kStages ? s : count; i < count; i += kStages, phase ^= 1u) {
-      const int c = (kb0 + i) * kStageK + 8 * lane;
-      constexpr int kAtOnce = 4;  // rows whose loads are under way together
-      for (int l0 = 0; l0 < p.m; l0 += kAtOnce) {
-        float v[kAtOnce][8];
+    constexpr int kAtOnce = kT == kF32 ? 2 : 4;
+    const int units = count * p.m;
+    for (int u0 = warp - 2; u0 < units; u0 += kAtOnce * 8) {
+      float v[kAtOnce][8];
 #pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) few_load<kT>(p, l0 + h, c, v[h]);
-        if (l0 == 0 && i >= kStages && !__all_sync(0xffffffffu, mbar_wait(&s_empty[s], phase, &s_fail))) break;
-#pragma unroll
-        for (int h = 0; h < kAtOnce; ++h) {
-          const int l = l0 + h;
-          if (l >= p.m) break;
-          uint32_t word;
-          const uint32_t q = quantize8(v[h], lane, &word);
-          // the 128-byte swizzle: 16-byte piece of row l at piece ^ (l mod 8)
-          *reinterpret_cast<uint32_t*>(codes + l * kStageBytes + (((lane >> 2) ^ (l & 7)) << 4) + (lane & 3) * 4) = q;
-          if (lane % 16 == 0) *reinterpret_cast<uint32_t*>(scales + lane / 16 * kSfGroup + l * 16) = word;
-        }
+      for (int h = 0; h < kAtOnce; ++h) {
+        const int u = u0 + 8 * h, i = u / p.m, l = u - i * p.m;
+        if (u < units) few_load<kT>(p, l, (kb0 + i) * kStageK + 8 * lane, v[h]);
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_full[s]);
+#pragma unroll
+      for (int h = 0; h < kAtOnce; ++h) {
+        const int u = u0 + 8 * h, i = u / p.m, l = u - i * p.m, s = i % kStages;
+        if (u >= units) break;
+        if (i >= kStages) mbar_wait(&s_empty[s], (i / kStages - 1) & 1, &s_fail);
+        __syncwarp();
+        uint32_t word;
+        const uint32_t q = quantize8(v[h], lane, &word);
+        // the 128-byte swizzle: 16-byte piece of row l at piece ^ (l mod 8)
+        *reinterpret_cast<uint32_t*>(sm + s * kStage + kW + l * kStageBytes + (((lane >> 2) ^ (l & 7)) << 4) + (lane & 3) * 4) = q;
+        if (lane % 16 == 0) *reinterpret_cast<uint32_t*>(sf + s * 2 * kSfTile + kSfTile + lane / 16 * kSfGroup + l * 16) = word;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_full[s]);
+      }
     }
   }
   __syncwarp();
@@ -848,7 +903,7 @@ cudaError_t opt_in_all() {
   const cudaError_t e[] = {opt_in(fp4_matmul_kernel<kT, 256, kT == kF32>, mm_smem<256>()), opt_in(fp4_matmul_kernel<kT, 128, kT == kF32>, mm_smem<128>()),
                            opt_in(fp4_matmul_few_kernel<kT, 16, false>, few_smem<16>()), opt_in(fp4_matmul_few_kernel<kT, 32, false>, few_smem<32>()),
                            opt_in(fp4_matmul_few_kernel<kT, 64, false>, few_smem<64>()), opt_in(fp4_matmul_few_kernel<kT, 128, false>, few_smem<128>()),
-                           opt_in(fp4_matmul_few_kernel<kT, kFuse, true>, few_smem<kFuse>())};
+                           opt_in(fp4_matmul_few_kernel<kT, kFewest, true>, few_smem<kFewest>())};
   for (const cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -1016,7 +1071,7 @@ bwd_status launch_few(const Product& q, const Plain& plain, int b_ready, const D
 
 template <int kT>
 bwd_status few(const Product& q, const Plain& plain, int b_ready, const DeviceState& d, cudaStream_t st) {
-  if (plain.x) return launch_few<kT, kFuse, true>(q, plain, b_ready, d, st);
+  if (plain.x) return launch_few<kT, kFewest, true>(q, plain, b_ready, d, st);
   if (q.a.rows > 64) return launch_few<kT, 128, false>(q, plain, b_ready, d, st);
   if (q.a.rows > 32) return launch_few<kT, 64, false>(q, plain, b_ready, d, st);
   if (q.a.rows > 16) return launch_few<kT, 32, false>(q, plain, b_ready, d, st);

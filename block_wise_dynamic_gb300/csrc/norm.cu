@@ -6,8 +6,8 @@
 //   h = dy gamma;  dx = rstd (h - sum h / D - xh sum(h xh) / D)
 //   dgamma = sum over rows of dy xh;  dbeta = sum over rows of dy
 //
-// Each row is read once: a group of threads (a warp, or a CTA) holds it in
-// registers as it was stored, forms the sums and writes the result.  The
+// Each row is read once: a group of threads (a warp, or a CTA) holds it, in
+// registers or in shared memory, forms the sums and writes the result.  The
 // variance is summed from the centred values, so a row's offset costs no
 // accuracy.  A group walks rows with a grid stride and has the next row's
 // loads under way while it works on one; a thread's columns are the same in
@@ -25,8 +25,11 @@ namespace {
 constexpr int kMaxWidth = 16384;
 constexpr int kWarpWidth = 512;   // widest row that a warp takes
 constexpr int kWarps = 8;         // rows of such a CTA
-constexpr int kThreadValues = 16; // values of a row that a thread holds
-constexpr int kMaxThreads = kMaxWidth / kThreadValues;
+constexpr int kMaxThreads = 512;
+// Values of a row that a thread holds: 16, and 32 of rows that would need more
+// than kMaxThreads threads so.
+constexpr int kFew = 16, kMany = 32;
+static_assert(kMaxThreads * kMany == kMaxWidth, "a CTA holds a row");
 
 template <int kBytes> struct UnitOf;
 template <> struct UnitOf<16> { using T = uint4; };
@@ -36,9 +39,9 @@ template <> struct UnitOf<2> { using T = uint16_t; };
 
 // A thread's part of a row: units of kVals consecutive values, a group's
 // threads side by side.
-template <int kT, int kVals>
+template <int kT, int kVals, int kValues>
 struct Part {
-  static constexpr int kUnits = kThreadValues / kVals;
+  static constexpr int kUnits = kValues / kVals;
   using Unit = typename UnitOf<kVals * elem_bytes<kT>()>::T;
   Unit u[kUnits];
 
@@ -47,13 +50,6 @@ struct Part {
     for (int i = 0; i < kUnits; ++i) {
       const int c = (i * threads + t) * kVals;
       u[i] = c < width ? __ldcs(reinterpret_cast<const Unit*>(static_cast<const char*>(row) + static_cast<int64_t>(c) * elem_bytes<kT>())) : Unit{};
-    }
-  }
-  __device__ __forceinline__ void load_shared(const uint8_t* row, int width, int t, int threads) {
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int c = (i * threads + t) * kVals;
-      u[i] = c < width ? *reinterpret_cast<const Unit*>(row + c * elem_bytes<kT>()) : Unit{};
     }
   }
   // 32-bit word k of unit i
@@ -149,13 +145,10 @@ struct ForwardArgs {
   float eps;
 };
 
-// kMax: threads of a CTA at most.  Up to half of kMaxThreads gamma and beta
-// stay in registers; wider rows read them again each time.
-template <int kT, int kVals, bool kWarp, int kMax>
-__global__ void __launch_bounds__(kMax)
+template <int kT, int kVals, int kValues, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarps : kMaxThreads)
 norm_forward_kernel(const ForwardArgs a) {
-  constexpr int kUnits = kThreadValues / kVals;
-  constexpr bool kKeep = kMax <= kMaxThreads / 2;
+  constexpr int kUnits = kValues / kVals;
   __shared__ float s_red[2][2][32];
   const int threads = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int64_t groups = kWarp ? static_cast<int64_t>(gridDim.x) * kWarps : gridDim.x;
@@ -164,22 +157,20 @@ norm_forward_kernel(const ForwardArgs a) {
   const auto x_row = [&](int64_t r) { return static_cast<const char*>(a.x) + r * a.ldx * elem_bytes<kT>(); };
   wait_for_inputs();
   let_next_begin();
-  Part<kT, kVals> next;
+  Part<kT, kVals, kValues> next;
   if (row < a.rows) next.load(x_row(row), a.width, t, threads);
-  float g[kKeep ? kThreadValues : 1], b[kKeep ? kThreadValues : 1];
-  if constexpr (kKeep) {
+  float g[kValues], b[kValues];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
+  for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-      for (int j = 0; j < kVals; ++j) {
-        const int c = (i * threads + t) * kVals;
-        g[i * kVals + j] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
-        b[i * kVals + j] = c < a.width ? vector_at<kT>(a.beta, c + j, 0.0f) : 0.0f;
-      }
-  }
+    for (int j = 0; j < kVals; ++j) {
+      const int c = (i * threads + t) * kVals;
+      g[i * kVals + j] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
+      b[i * kVals + j] = c < a.width ? vector_at<kT>(a.beta, c + j, 0.0f) : 0.0f;
+    }
   const float width = static_cast<float>(a.width);
   for (; row < a.rows; row += groups) {
-    float v[kThreadValues];
+    float v[kValues];
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < kUnits; ++i)
@@ -214,8 +205,7 @@ norm_forward_kernel(const ForwardArgs a) {
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
         const int e = i * kVals + j;
-        out[j] = __fmaf_rn(__fmul_rn(v[e], rstd), kKeep ? g[kKeep ? e : 0] : vector_at<kT>(a.gamma, c + j, 1.0f),
-                           kKeep ? b[kKeep ? e : 0] : vector_at<kT>(a.beta, c + j, 0.0f));
+        out[j] = __fmaf_rn(__fmul_rn(v[e], rstd), g[e], b[e]);
       }
       store_unit<kT, kVals>(y, c, out);
     }
@@ -235,15 +225,11 @@ struct BackwardArgs {
   int width;
 };
 
-// The columns' sums are kept in registers for CTAs of up to half of
-// kMaxThreads, in shared memory for wider ones.
-template <int kT, int kVals, bool kWarp, int kMax>
-__global__ void __launch_bounds__(kMax)
+template <int kT, int kVals, int kValues, bool kWarp>
+__global__ void __launch_bounds__(kWarp ? 32 * kWarps : kMaxThreads)
 norm_backward_kernel(const BackwardArgs a) {
-  constexpr int kUnits = kThreadValues / kVals;
-  constexpr bool kKeep = kMax <= kMaxThreads / 2;
-  extern __shared__ __align__(128) uint8_t s_raw[];
-  float* const s_sums = reinterpret_cast<float*>(s_raw);  // [2][width]: of wide rows, or of a CTA's warps
+  constexpr int kUnits = kValues / kVals;
+  __shared__ float s_sums[kWarp ? 2 * kWarpWidth : 1];  // of a CTA's warps
   __shared__ float s_red[2][2][32];
   const int threads = kWarp ? 32 : blockDim.x, t = kWarp ? threadIdx.x % 32 : threadIdx.x;
   const int64_t groups = kWarp ? static_cast<int64_t>(gridDim.x) * kWarps : gridDim.x;
@@ -253,7 +239,7 @@ norm_backward_kernel(const BackwardArgs a) {
   const auto dy_row = [&](int64_t r) { return static_cast<const char*>(a.dy) + r * a.lddy * elem_bytes<kT>(); };
   wait_for_inputs();
   let_next_begin();
-  Part<kT, kVals> next_x, next_dy;
+  Part<kT, kVals, kValues> next_x, next_dy;
   float next_mean = 0.0f, next_rstd = 0.0f;
   const auto fetch = [&](int64_t r) {
     next_x.load(x_row(r), a.width, t, threads);
@@ -262,27 +248,18 @@ norm_backward_kernel(const BackwardArgs a) {
     next_rstd = a.rstd[r];
   };
   if (row < a.rows) fetch(row);
-  float g[kKeep ? kThreadValues : 1], dg[kKeep ? kThreadValues : 1], db[kKeep ? kThreadValues : 1];
-  if constexpr (kKeep) {
+  float g[kValues], dg[kValues], db[kValues];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
+  for (int i = 0; i < kUnits; ++i)
 #pragma unroll
-      for (int j = 0; j < kVals; ++j) {
-        const int c = (i * threads + t) * kVals, e = i * kVals + j;
-        g[e] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
-        dg[e] = db[e] = 0.0f;
-      }
-  } else if (a.partial) {
-    // each thread's own columns: no barrier is needed
-    for (int i = 0; i < kUnits; ++i)
-      for (int j = 0; j < kVals; ++j) {
-        const int c = (i * threads + t) * kVals + j;
-        if (c < a.width) s_sums[c] = s_sums[a.width + c] = 0.0f;
-      }
-  }
+    for (int j = 0; j < kVals; ++j) {
+      const int c = (i * threads + t) * kVals, e = i * kVals + j;
+      g[e] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
+      dg[e] = db[e] = 0.0f;
+    }
   const float width = static_cast<float>(a.width);
   for (; row < a.rows; row += groups) {
-    const Part<kT, kVals> x = next_x, dy = next_dy;
+    const Part<kT, kVals, kValues> x = next_x, dy = next_dy;
     const float mean = next_mean, rstd = next_rstd;
     if (row + groups < a.rows) fetch(row + groups);
     float s[2] = {0.0f, 0.0f};
@@ -295,19 +272,9 @@ norm_backward_kernel(const BackwardArgs a) {
       for (int j = 0; j < kVals; ++j) {
         const int e = i * kVals + j;
         const float d = dy.value(i, j), xh = xh_of(i, j);
-        float gamma;
-        if constexpr (kKeep) {
-          gamma = g[e];
-          dg[e] = __fmaf_rn(d, xh, dg[e]);
-          db[e] = __fadd_rn(db[e], d);
-        } else {
-          gamma = vector_at<kT>(a.gamma, c + j, 1.0f);
-          if (a.partial) {
-            s_sums[c + j] = __fmaf_rn(d, xh, s_sums[c + j]);
-            s_sums[a.width + c + j] = __fadd_rn(s_sums[a.width + c + j], d);
-          }
-        }
-        const float h = __fmul_rn(d, gamma);
+        dg[e] = __fmaf_rn(d, xh, dg[e]);
+        db[e] = __fadd_rn(db[e], d);
+        const float h = __fmul_rn(d, g[e]);
         s[0] += h;
         s[1] = __fmaf_rn(h, xh, s[1]);
       }
@@ -323,7 +290,7 @@ norm_backward_kernel(const BackwardArgs a) {
       float out[kVals];
 #pragma unroll
       for (int j = 0; j < kVals; ++j) {
-        const float h = __fmul_rn(dy.value(i, j), kKeep ? g[kKeep ? i * kVals + j : 0] : vector_at<kT>(a.gamma, c + j, 1.0f));
+        const float h = __fmul_rn(dy.value(i, j), g[i * kVals + j]);
         out[j] = __fmul_rn(rstd, __fmaf_rn(-xh_of(i, j), mean_hx, __fsub_rn(h, mean_h)));
       }
       store_unit<kT, kVals>(dx, c, out);
@@ -342,8 +309,8 @@ norm_backward_kernel(const BackwardArgs a) {
           for (int j = 0; j < kVals; ++j) {
             const int c = (i * 32 + t) * kVals + j, e = i * kVals + j;
             if (c < a.width) {
-              s_sums[c] = w ? __fadd_rn(s_sums[c], dg[kKeep ? e : 0]) : dg[kKeep ? e : 0];
-              s_sums[a.width + c] = w ? __fadd_rn(s_sums[a.width + c], db[kKeep ? e : 0]) : db[kKeep ? e : 0];
+              s_sums[c] = w ? __fadd_rn(s_sums[c], dg[e]) : dg[e];
+              s_sums[kWarpWidth + c] = w ? __fadd_rn(s_sums[kWarpWidth + c], db[e]) : db[e];
             }
           }
       }
@@ -351,7 +318,7 @@ norm_backward_kernel(const BackwardArgs a) {
     }
     for (int c = threadIdx.x; c < a.width; c += 32 * kWarps) {
       to_gamma[c] = s_sums[c];
-      to_beta[c] = s_sums[a.width + c];
+      to_beta[c] = s_sums[kWarpWidth + c];
     }
   } else {
 #pragma unroll
@@ -360,14 +327,27 @@ norm_backward_kernel(const BackwardArgs a) {
       for (int j = 0; j < kVals; ++j) {
         const int c = (i * threads + t) * kVals + j;
         if (c >= a.width) continue;
-        to_gamma[c] = kKeep ? dg[kKeep ? i * kVals + j : 0] : s_sums[c];
-        to_beta[c] = kKeep ? db[kKeep ? i * kVals + j : 0] : s_sums[a.width + c];
+        to_gamma[c] = dg[i * kVals + j];
+        to_beta[c] = db[i * kVals + j];
       }
   }
 }
 
 // --------------------------------------------------------------------------
-// rows of whole 16-byte pieces, many of them
+// many rows
+//
+// A CTA takes kR rows at a time: what a row costs beside its bytes is the
+// latency of its sums over the CTA, which kR rows share.  Rows come into
+// shared memory by bulk copies, up to three sets of kR ahead, and are read by
+// each pass over them from there; the registers hold gamma, beta and the columns' sums.
+// (16384 x 4096 bf16, forward and backward, with a row at a time in registers:
+// 58 and 97 us; from shared memory, a row at a time, 56 and 100, and these sets
+// with one operation to an instruction 58 and 89, bound by instructions.)
+//
+// A copy's pieces have 16 bytes: of rows that start or end inside one, the
+// whole pieces that they touch are copied, and the row starts where it does in
+// the first.  What that reads beside a row belongs to the rows next to it; the
+// first row's start and the last one's end are read by themselves.
 
 // Two operations in one instruction, each rounded by itself.
 __device__ __forceinline__ uint64_t bits2(float2 a) {
@@ -396,197 +376,303 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return from2(r);
 }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-//
-// A CTA takes kR rows at a time: what a row costs beside its bytes is the
-// latency of its sums over the CTA, which kR rows share.  Rows come into
-// shared memory by bulk copies, a set of kR ahead, and are read from there by
-// each pass over them; the registers hold gamma, beta and the columns' sums.
-// (16384 x 4096 bf16, forward and backward, with a row at a time in registers:
-// 58 and 97 us; from shared memory, a row at a time, 56 and 100, and these sets
-// with one operation to an instruction 58 and 89, bound by instructions.)
 
-constexpr int kSets = 2;  // of rows, at most one of them being read
+// A thread's columns, in pairs: of whole pieces neighbours, 16 bytes to a unit;
+// of other rows columns that lie a CTA apart, so that each access is a warp's
+// worth of neighbours.
+template <int kT, bool kPieces, int kValues>
+struct Columns {
+  static constexpr int kPairs = kValues / 2;
+  [[maybe_unused]] static constexpr int kUnitPairs = 8 / elem_bytes<kT>(), kUnits = kPairs / kUnitPairs;
+  int t, threads, width;
+  __device__ __forceinline__ int first(int e) const {
+    if constexpr (kPieces) return ((e / kUnitPairs * threads + t) * kUnitPairs + e % kUnitPairs) * 2;
+    else return 2 * e * threads + t;
+  }
+  __device__ __forceinline__ int second(int e) const { return first(e) + (kPieces ? 1 : threads); }
+  __device__ __forceinline__ float2 vector(const VectorArg& v, int e, float otherwise) const {
+    const int c = first(e), d = second(e);
+    return make_float2(c < width ? vector_at<kT>(v, c, otherwise) : 0.0f, d < width ? vector_at<kT>(v, d, otherwise) : 0.0f);
+  }
+  // Calls f(e, there, values of each row) for this thread's pairs of rows in
+  // shared memory, and writes what it returns to `out`, where that is wanted.
+  // A second value past the row is 0, and not `there`.
+  template <bool kOut, int kN, typename F>
+  __device__ __forceinline__ void over(char* out, const uint8_t* const (&row)[kN], F f) const {
+    if constexpr (kPieces) {
+      // all of a thread's loads before the first use, where registers allow it
+      constexpr int kAtOnce = kValues == kFew ? kUnits : 1;
+#pragma unroll
+      for (int i0 = 0; i0 < kUnits; i0 += kAtOnce) {
+        uint4 w[kAtOnce][kN];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int c = ((i0 + i) * threads + t) * 2 * kUnitPairs;
+#pragma unroll
+          for (int n = 0; n < kN; ++n)
+            w[i][n] = c < width ? *reinterpret_cast<const uint4*>(row[n] + c * elem_bytes<kT>()) : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const int c = ((i0 + i) * threads + t) * 2 * kUnitPairs;
+          if (c >= width) continue;
+          float o[2 * kUnitPairs];
+#pragma unroll
+          for (int k = 0; k < kUnitPairs; ++k) {
+            float2 v[kN];
+#pragma unroll
+            for (int n = 0; n < kN; ++n) {
+              Part<kT, 2 * kUnitPairs, 2 * kUnitPairs> x;
+              x.u[0] = w[i][n];
+              v[n] = x.two(0, k);
+            }
+            const float2 r = f((i0 + i) * kUnitPairs + k, true, v);
+            o[2 * k] = r.x;
+            o[2 * k + 1] = r.y;
+          }
+          if constexpr (kOut) store_unit<kT, 2 * kUnitPairs>(out, c, o);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        const int c = first(e), d = second(e);
+        if (c >= width) continue;
+        const bool there = d < width;
+        float2 v[kN];
+#pragma unroll
+        for (int n = 0; n < kN; ++n) v[n] = make_float2(load1<kT>(row[n], c), there ? load1<kT>(row[n], d) : 0.0f);
+        const float2 r = f(e, there, v);
+        if constexpr (kOut) {
+          store1<kT>(out, c, r.x);
+          if (there) store1<kT>(out, d, r.y);
+        }
+      }
+    }
+  }
+};
 
-template <int kR, int kArrays>
+constexpr int kMaxSets = 4;  // of rows, one of them being read
+
+// One array's rows: where they are, and the whole pieces that they touch.
+struct Rows {
+  const char* base;
+  int64_t ld;       // bytes
+  int row_bytes;
+  int64_t rows;
+};
+
+template <int kT, bool kPieces, int kR, int kArrays>
 struct RowRing {
   uint64_t* bars;
-  uint8_t* rows;  // [kSets][kR][kArrays][row_bytes]
-  int row_bytes;
+  uint8_t* data;  // [sets][kR][kArrays][slot]
+  int sets;
+  int slot;       // bytes of a row's pieces
+  Rows a[kArrays];
   int s = 0;
   uint32_t phase = 0;
-  __device__ __forceinline__ const uint8_t* row(int r, int array) const { return rows + ((s * kR + r) * kArrays + array) * row_bytes; }
+  __device__ __forceinline__ uint8_t* place(int set, int r, int array) const { return data + ((set * kR + r) * kArrays + array) * slot; }
+  // Row r of the set that is being read, which is row `row` of the array.
+  __device__ __forceinline__ const uint8_t* row(int r, int array, int64_t row) const {
+    if constexpr (kPieces) return place(s, r, array);
+    else return place(s, r, array) + (reinterpret_cast<uintptr_t>(a[array].base + row * a[array].ld) & 15u);
+  }
   __device__ __forceinline__ void init() {
     if (threadIdx.x == 0) {
-      for (int i = 0; i < kSets; ++i) mbar_init(&bars[i], 1);
+      for (int i = 0; i < sets; ++i) mbar_init(&bars[i], 1);
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
   }
-  // By one thread: rows first .. first + count - 1 of each array, `ld` bytes apart.
-  __device__ __forceinline__ void fill(int set, int count, const char* x, int64_t ldx, const char* y, int64_t ldy) {
-    mbar_expect_tx(&bars[set], count * kArrays * row_bytes);
-    for (int r = 0; r < count; ++r) {
-      uint8_t* const to = rows + (set * kR + r) * kArrays * row_bytes;
-      bulk_load(to, x + r * ldx, row_bytes, &bars[set]);
-      if constexpr (kArrays == 2) bulk_load(to + row_bytes, y + r * ldy, row_bytes, &bars[set]);
+  // Rows `first` on into a set, by one thread, behind a barrier that all
+  // threads passed when they were done with it.
+  __device__ __forceinline__ void fill(int set, int64_t first) {
+    if (threadIdx.x != 0 || first >= a[0].rows) return;
+    const int count = a[0].rows - first < kR ? static_cast<int>(a[0].rows - first) : kR;
+    uint32_t bytes = 0;
+    for (int r = 0; r < count; ++r)
+#pragma unroll
+      for (int i = 0; i < kArrays; ++i) {
+        const char* const from = a[i].base + (first + r) * a[i].ld;
+        uint8_t* const dst = place(set, r, i);
+        if constexpr (kPieces) {
+          bulk_load(dst, from, a[i].row_bytes, &bars[set]);
+          bytes += a[i].row_bytes;
+        } else {
+          bytes += pieces(dst, reinterpret_cast<uintptr_t>(from), a[i].row_bytes, first + r == 0, first + r + 1 == a[i].rows, &bars[set]);
+        }
+      }
+    mbar_expect_tx(&bars[set], bytes);
+  }
+  static __device__ __forceinline__ uint32_t pieces(uint8_t* dst, uintptr_t from, int row_bytes, bool first, bool last, uint64_t* bar) {
+    const uintptr_t to = from + row_bytes, start = from & ~uintptr_t{15};
+    uintptr_t low = start, high = (to + 15) & ~uintptr_t{15};
+    if (first || last) {
+      // the first row's start and the last one's end, a value at a time
+      using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
+      const auto copy = [&](uintptr_t at, uintptr_t end) {
+        for (; at < end; at += sizeof(Elem)) *reinterpret_cast<Elem*>(dst + (at - start)) = *reinterpret_cast<const Elem*>(at);
+      };
+      if (first && low != from) low += 16;
+      if (last && high != to) high -= 16;
+      if (low >= high) {
+        copy(from, to);
+        return 0;
+      }
+      if (first) copy(from, low);
+      if (last) copy(high, to);
     }
+    bulk_load(dst + (low - start), reinterpret_cast<const void*>(low), static_cast<uint32_t>(high - low), bar);
+    return static_cast<uint32_t>(high - low);
   }
   // Waits for the current set.  Where a wait gives up, the CTA goes on over
   // whatever there is, with no wait any more, so that its barriers still meet.
   __device__ __forceinline__ void wait(volatile int* fail) { mbar_wait(&bars[s], phase, fail); }
+  // The first sets, and later what takes the place of the set before this one.
+  __device__ __forceinline__ void begin(int64_t row, int64_t step) {
+    for (int i = 0; i + 1 < sets; ++i) fill(i, row + i * step);
+  }
+  __device__ __forceinline__ void refill(int64_t row, int64_t step) { fill(s == 0 ? sets - 1 : s - 1, row + (sets - 1) * step); }
   __device__ __forceinline__ void next() {
-    if (++s == kSets) { s = 0; phase ^= 1u; }
+    if (++s == sets) { s = 0; phase ^= 1u; }
   }
 };
 
 // Sums of kN values over a CTA, the same in each of its threads; two buffers
-// in turn, as for GroupSum.
+// in turn, as for GroupSum.  Of several values lanes first divide which ones
+// they go on with, so that four take six shuffles and not twenty.  (With those,
+// and divisions by the width, a row cost a warp more instructions than its 512
+// elements did.)
 template <int kN>
 __device__ __forceinline__ void cta_sum(float (&s)[kN], float (*red)[32][kN], int& turn) {
+  static_assert(kN == 1 || kN == 2 || kN == 4, "values that lanes divide");
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  int mine = 0;  // the value that this lane ends up with
+  float a = s[0];
+  if constexpr (kN == 4) {
+    const bool high = lane & 16, odd = lane & 8;
+    float a0 = high ? s[2] : s[0], a1 = high ? s[3] : s[1];
+    a0 += __shfl_xor_sync(0xffffffffu, high ? s[0] : s[2], 16);
+    a1 += __shfl_xor_sync(0xffffffffu, high ? s[1] : s[3], 16);
+    a = (odd ? a1 : a0) + __shfl_xor_sync(0xffffffffu, odd ? a0 : a1, 8);
+    mine = lane >> 3;
+  } else if constexpr (kN == 2) {
+    const bool high = lane & 16;
+    a = (high ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, high ? s[0] : s[1], 16);
+    a += __shfl_xor_sync(0xffffffffu, a, 8);
+    mine = lane >> 4;
+  } else {
+    a += __shfl_xor_sync(0xffffffffu, a, 16);
+    a += __shfl_xor_sync(0xffffffffu, a, 8);
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) s[n] += __shfl_xor_sync(0xffffffffu, s[n], o);
-  const int warp = threadIdx.x / 32, warps = blockDim.x / 32;
-  if (threadIdx.x % 32 == 0)
-#pragma unroll
-    for (int n = 0; n < kN; ++n) red[turn][warp][n] = s[n];
+  for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if (lane % (32 / kN) == 0) red[turn][warp][mine] = a;
   __syncthreads();
+  const float* const from = red[turn][0];
 #pragma unroll
   for (int n = 0; n < kN; ++n) s[n] = 0.0f;
 #pragma unroll 4
-  for (int w = 0; w < warps; ++w)
+  for (int w = 0; w < warps; ++w) {
+    if constexpr (kN == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(from + 4 * w);
+      s[0] += v.x; s[1] += v.y; s[2] += v.z; s[3] += v.w;
+    } else {
 #pragma unroll
-    for (int n = 0; n < kN; ++n) s[n] += red[turn][w][n];
+      for (int n = 0; n < kN; ++n) s[n] += from[kN * w + n];
+    }
+  }
   turn ^= 1;
 }
 
-template <int kT, int kMax, int kR>
+template <int kT, bool kPieces, int kValues, int kMax, int kR>
 __global__ void __launch_bounds__(kMax)
-norm_forward_ring_kernel(const ForwardArgs a, int row_bytes) {
-  constexpr int kVals = 16 / elem_bytes<kT>(), kUnits = kThreadValues / kVals;
-  constexpr bool kKeep = kMax <= kMaxThreads / 2;
+norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
+  constexpr int kPairs = kValues / 2;
   extern __shared__ __align__(128) uint8_t s_rows[];
-  __shared__ __align__(8) uint64_t s_bars[kSets];
+  __shared__ __align__(8) uint64_t s_bars[kMaxSets];
   __shared__ __align__(16) float s_red[2][32][kR];
   __shared__ int s_fail;
-  const int threads = blockDim.x, t = threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kR, ld = a.ldx * elem_bytes<kT>();
-  RowRing<kR, 1> ring{s_bars, s_rows, row_bytes};
-  const auto fill = [&](int set, int64_t r) {
-    if (t == 0 && r < a.rows)
-      ring.fill(set, a.rows - r < kR ? static_cast<int>(a.rows - r) : kR, static_cast<const char*>(a.x) + r * ld, ld, nullptr, 0);
-  };
+  const Columns<kT, kPieces, kValues> cols{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.width};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kR;
+  const int row_bytes = a.width * elem_bytes<kT>();
+  RowRing<kT, kPieces, kR, 1> ring{s_bars, s_rows, sets, slot, {{static_cast<const char*>(a.x), a.ldx * elem_bytes<kT>(), row_bytes, a.rows}}};
   s_fail = 0;
   ring.init();
   wait_for_inputs();
   let_next_begin();
   int64_t row = static_cast<int64_t>(blockIdx.x) * kR;
-  fill(0, row);
-  const auto gamma_at = [&](int c) { return make_float2(vector_at<kT>(a.gamma, c, 1.0f), vector_at<kT>(a.gamma, c + 1, 1.0f)); };
-  const auto beta_at = [&](int c) { return make_float2(vector_at<kT>(a.beta, c, 0.0f), vector_at<kT>(a.beta, c + 1, 0.0f)); };
-  float2 g[kKeep ? kThreadValues / 2 : 1], b[kKeep ? kThreadValues / 2 : 1];
-  if constexpr (kKeep) {
+  ring.begin(row, step);
+  float2 g[kPairs], b[kPairs];
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-      for (int k = 0; k < kVals / 2; ++k) {
-        const int c = (i * threads + t) * kVals, e = i * kVals / 2 + k;
-        g[e] = c < a.width ? gamma_at(c + 2 * k) : both(0.0f);
-        b[e] = c < a.width ? beta_at(c + 2 * k) : both(0.0f);
-      }
+  for (int e = 0; e < kPairs; ++e) {
+    g[e] = cols.vector(a.gamma, e, 1.0f);
+    b[e] = cols.vector(a.beta, e, 0.0f);
   }
-  const float width = static_cast<float>(a.width);
+  if constexpr (!kPieces) __syncthreads();  // the first row's start, which a thread copied
+  const float inv_width = __fdiv_rn(1.0f, static_cast<float>(a.width));
   int turn = 0;
   for (; row < a.rows; row += step) {
     ring.wait(&s_fail);
     float mean[kR], s[kR];
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      Part<kT, kVals> x;
-      x.load_shared(ring.row(r, 0), a.width, t, threads);
       float2 sum = both(0.0f);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-        for (int k = 0; k < kVals / 2; ++k) sum = add2(sum, x.two(i, k));
+      cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool, const float2 (&v)[1]) { return sum = add2(sum, v[0]); });
       s[r] = __fadd_rn(sum.x, sum.y);
     }
     cta_sum<kR>(s, s_red, turn);
-    fill(ring.s ^ 1, row + step);  // behind the barrier all threads are done with the set before
+    ring.refill(row, step);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      mean[r] = __fdiv_rn(s[r], width);
+      mean[r] = __fmul_rn(s[r], inv_width);
       const float2 less = both(-mean[r]);
       float2 sum = both(0.0f);
-      Part<kT, kVals> x;
-      x.load_shared(ring.row(r, 0), a.width, t, threads);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if ((i * threads + t) * kVals >= a.width) continue;
-#pragma unroll
-        for (int k = 0; k < kVals / 2; ++k) {
-          const float2 d = add2(x.two(i, k), less);
-          sum = fma2(d, d, sum);
-        }
-      }
+      cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool there, const float2 (&v)[1]) {
+        float2 d = add2(v[0], less);
+        if (!there) d.y = 0.0f;
+        return sum = fma2(d, d, sum);
+      });
       s[r] = __fadd_rn(sum.x, sum.y);
     }
     cta_sum<kR>(s, s_red, turn);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       if (row + r >= a.rows) break;
-      const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s[r], width), a.eps)));
-      if (t == 0) {
+      const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
+      if (threadIdx.x == 0) {
         if (a.mean) a.mean[row + r] = mean[r];
         if (a.rstd) a.rstd[row + r] = rstd;
       }
-      char* const y = static_cast<char*>(a.y) + (row + r) * row_bytes;
-      Part<kT, kVals> x;
-      x.load_shared(ring.row(r, 0), a.width, t, threads);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int c = (i * threads + t) * kVals;
-        if (c >= a.width) continue;
-        float out[kVals];
-#pragma unroll
-        for (int k = 0; k < kVals / 2; ++k) {
-          const int e = i * kVals / 2 + k;
-          const float2 xh = mul2(add2(x.two(i, k), both(-mean[r])), both(rstd));
-          const float2 o = fma2(xh, kKeep ? g[kKeep ? e : 0] : gamma_at(c + 2 * k), kKeep ? b[kKeep ? e : 0] : beta_at(c + 2 * k));
-          out[2 * k] = o.x;
-          out[2 * k + 1] = o.y;
-        }
-        store_unit<kT, kVals>(y, c, out);
-      }
+      const float2 less = both(-mean[r]), scale = both(rstd);
+      cols.template over<true, 1>(static_cast<char*>(a.y) + (row + r) * row_bytes, {ring.row(r, 0, row + r)},
+                                  [&](int e, bool, const float2 (&v)[1]) { return fma2(mul2(add2(v[0], less), scale), g[e], b[e]); });
     }
     ring.next();
   }
   if (s_fail) let_copies_land();
 }
 
-template <int kT, int kMax, int kR>
+template <int kT, bool kPieces, int kValues, int kMax, int kR>
 __global__ void __launch_bounds__(kMax)
-norm_backward_ring_kernel(const BackwardArgs a, int row_bytes) {
-  constexpr int kVals = 16 / elem_bytes<kT>(), kUnits = kThreadValues / kVals;
+norm_backward_ring_kernel(const BackwardArgs a, int slot, int sets) {
+  constexpr int kPairs = kValues / 2;
   extern __shared__ __align__(128) uint8_t s_rows[];
-  __shared__ __align__(8) uint64_t s_bars[kSets];
+  __shared__ __align__(8) uint64_t s_bars[kMaxSets];
   __shared__ __align__(16) float s_red[2][32][2 * kR];
   __shared__ int s_fail;
-  const int threads = blockDim.x, t = threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kR, ldx = a.ldx * elem_bytes<kT>(), lddy = a.lddy * elem_bytes<kT>();
-  RowRing<kR, 2> ring{s_bars, s_rows, row_bytes};
-  const auto fill = [&](int set, int64_t r) {
-    if (t == 0 && r < a.rows)
-      ring.fill(set, a.rows - r < kR ? static_cast<int>(a.rows - r) : kR, static_cast<const char*>(a.x) + r * ldx, ldx,
-                static_cast<const char*>(a.dy) + r * lddy, lddy);
-  };
+  const Columns<kT, kPieces, kValues> cols{static_cast<int>(threadIdx.x), static_cast<int>(blockDim.x), a.width};
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kR;
+  const int row_bytes = a.width * elem_bytes<kT>();
+  RowRing<kT, kPieces, kR, 2> ring{s_bars, s_rows, sets, slot,
+                          {{static_cast<const char*>(a.x), a.ldx * elem_bytes<kT>(), row_bytes, a.rows},
+                           {static_cast<const char*>(a.dy), a.lddy * elem_bytes<kT>(), row_bytes, a.rows}}};
   s_fail = 0;
   ring.init();
   wait_for_inputs();
   let_next_begin();
   int64_t row = static_cast<int64_t>(blockIdx.x) * kR;
-  fill(0, row);
+  ring.begin(row, step);
   float next_mean[kR], next_rstd[kR];
   const auto statistics = [&](int64_t first) {
 #pragma unroll
@@ -597,16 +683,14 @@ norm_backward_ring_kernel(const BackwardArgs a, int row_bytes) {
     }
   };
   statistics(row);
-  float2 g[kThreadValues / 2], dg[kThreadValues / 2], db[kThreadValues / 2];
+  float2 g[kPairs], dg[kPairs], db[kPairs];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-    for (int k = 0; k < kVals / 2; ++k) {
-      const int c = (i * threads + t) * kVals + 2 * k, e = i * kVals / 2 + k;
-      g[e] = c < a.width ? make_float2(vector_at<kT>(a.gamma, c, 1.0f), vector_at<kT>(a.gamma, c + 1, 1.0f)) : both(0.0f);
-      dg[e] = db[e] = both(0.0f);
-    }
-  const float width = static_cast<float>(a.width);
+  for (int e = 0; e < kPairs; ++e) {
+    g[e] = cols.vector(a.gamma, e, 1.0f);
+    dg[e] = db[e] = both(0.0f);
+  }
+  if constexpr (!kPieces) __syncthreads();  // the first rows' starts, which a thread copied
+  const float inv_width = __fdiv_rn(1.0f, static_cast<float>(a.width));
   int turn = 0;
   for (; row < a.rows; row += step) {
     float mean[kR], rstd[kR], s[2 * kR];
@@ -620,49 +704,29 @@ norm_backward_ring_kernel(const BackwardArgs a, int row_bytes) {
       if (row + r >= a.rows) continue;
       const float2 less = both(-mean[r]), scale = both(rstd[r]);
       float2 s0 = both(0.0f), s1 = both(0.0f);
-      Part<kT, kVals> x, dy;
-      x.load_shared(ring.row(r, 0), a.width, t, threads);
-      dy.load_shared(ring.row(r, 1), a.width, t, threads);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        if ((i * threads + t) * kVals >= a.width) continue;
-#pragma unroll
-        for (int k = 0; k < kVals / 2; ++k) {
-          const int e = i * kVals / 2 + k;
-          const float2 d = dy.two(i, k), xh = mul2(add2(x.two(i, k), less), scale), h = mul2(d, g[e]);
-          dg[e] = fma2(d, xh, dg[e]);
-          db[e] = add2(db[e], d);
-          s0 = add2(s0, h);
-          s1 = fma2(h, xh, s1);
-        }
-      }
+      // (past the row dy is 0, and with it all that is added)
+      cols.template over<false, 2>(nullptr, {ring.row(r, 0, row + r), ring.row(r, 1, row + r)}, [&](int e, bool, const float2 (&v)[2]) {
+        const float2 xh = mul2(add2(v[0], less), scale), h = mul2(v[1], g[e]);
+        dg[e] = fma2(v[1], xh, dg[e]);
+        db[e] = add2(db[e], v[1]);
+        s0 = add2(s0, h);
+        return s1 = fma2(h, xh, s1);
+      });
       s[2 * r] = __fadd_rn(s0.x, s0.y);
       s[2 * r + 1] = __fadd_rn(s1.x, s1.y);
     }
     cta_sum<2 * kR>(s, s_red, turn);
-    fill(ring.s ^ 1, row + step);  // behind the barrier all threads are done with the set before
+    ring.refill(row, step);
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       if (!a.dx || row + r >= a.rows) break;
-      const float mean_h = __fdiv_rn(s[2 * r], width), mean_hx = __fdiv_rn(s[2 * r + 1], width);
-      char* const dx = static_cast<char*>(a.dx) + (row + r) * row_bytes;
-      Part<kT, kVals> x, dy;
-      x.load_shared(ring.row(r, 0), a.width, t, threads);
-      dy.load_shared(ring.row(r, 1), a.width, t, threads);
-#pragma unroll
-      for (int i = 0; i < kUnits; ++i) {
-        const int c = (i * threads + t) * kVals;
-        if (c >= a.width) continue;
-        float out[kVals];
-#pragma unroll
-        for (int k = 0; k < kVals / 2; ++k) {
-          const float2 xh = mul2(add2(x.two(i, k), both(-mean[r])), both(rstd[r])), h = mul2(dy.two(i, k), g[i * kVals / 2 + k]);
-          const float2 o = mul2(both(rstd[r]), fma2(xh, both(-mean_hx), add2(h, both(-mean_h))));
-          out[2 * k] = o.x;
-          out[2 * k + 1] = o.y;
-        }
-        store_unit<kT, kVals>(dx, c, out);
-      }
+      const float mean_h = __fmul_rn(s[2 * r], inv_width), mean_hx = __fmul_rn(s[2 * r + 1], inv_width);
+      const float2 less = both(-mean[r]), scale = both(rstd[r]), less_h = both(-mean_h), less_hx = both(-mean_hx);
+      cols.template over<true, 2>(static_cast<char*>(a.dx) + (row + r) * row_bytes, {ring.row(r, 0, row + r), ring.row(r, 1, row + r)},
+                                  [&](int e, bool, const float2 (&v)[2]) {
+        const float2 xh = mul2(add2(v[0], less), scale);
+        return mul2(scale, fma2(xh, less_hx, add2(mul2(v[1], g[e]), less_h)));
+      });
     }
     ring.next();
   }
@@ -671,14 +735,16 @@ norm_backward_ring_kernel(const BackwardArgs a, int row_bytes) {
   float* const to_gamma = a.partial + static_cast<int64_t>(blockIdx.x) * a.width;
   float* const to_beta = to_gamma + static_cast<int64_t>(gridDim.x) * a.width;
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i)
-#pragma unroll
-    for (int j = 0; j < kVals; j += 4) {
-      const int c = (i * threads + t) * kVals + j, e = (i * kVals + j) / 2;
-      if (c >= a.width) continue;
-      *reinterpret_cast<float4*>(to_gamma + c) = make_float4(dg[e].x, dg[e].y, dg[e + 1].x, dg[e + 1].y);
-      *reinterpret_cast<float4*>(to_beta + c) = make_float4(db[e].x, db[e].y, db[e + 1].x, db[e + 1].y);
+  for (int e = 0; e < kPairs; ++e) {
+    if (cols.first(e) < a.width) {
+      to_gamma[cols.first(e)] = dg[e].x;
+      to_beta[cols.first(e)] = db[e].x;
     }
+    if (cols.second(e) < a.width) {
+      to_gamma[cols.second(e)] = dg[e].y;
+      to_beta[cols.second(e)] = db[e].y;
+    }
+  }
 }
 
 // Sums of the CTAs' rows: sixteen warps of a CTA each add every sixteenth of
@@ -726,32 +792,45 @@ int bytes_of(int t) { return t == BWD_F32 ? 4 : 2; }
 
 constexpr int kSms = 160;  // at least as many as the device has
 
-int threads_of(int width) { return (width + 32 * kThreadValues - 1) / (32 * kThreadValues) * 32; }
+int values_of(int width) { return width <= kMaxThreads * kFew ? kFew : kMany; }
+int threads_of(int width) { return (width + 32 * values_of(width) - 1) / (32 * values_of(width)) * 32; }
+
+// CTAs to an SM, by the registers that a thread takes: in the forward pass some
+// 75 for four rows of pieces and 64 for one row without, in the backward pass up
+// to 128, and more of rows with many values.
+int per_sm(int width, int threads) { return std::max(1, std::min((values_of(width) == kFew ? threads : 384) / threads_of(width), 16)); }
+int forward_per_sm(int width, bool pieces) { return per_sm(width, pieces ? 768 : 1024); }
+int backward_per_sm(int width) { return per_sm(width, 512); }
 
 // CTAs of the backward pass, and so rows of its workspace, at most: as many as
-// are resident (some 100 registers to a thread), each with two rows or more,
-// since every one adds a row of sums.
+// are resident, each with two rows or more, since every one adds a row of sums.
 int64_t backward_ctas(int64_t rows, int width, int sms) {
   const bool warp = width <= kWarpWidth;
-  const int threads = warp ? 32 * kWarps : threads_of(width);
-  const int64_t most = static_cast<int64_t>(sms) * std::max(1, std::min(512 / threads, 8));
+  const int64_t most = static_cast<int64_t>(sms) * (warp ? 2 : backward_per_sm(width));
   const int64_t each = 2 * (warp ? kWarps : 1), need = (rows + each - 1) / each;
   return std::min(need, most);
 }
 
-// Rows that a CTA of the ring kernels takes at a time, of so many bytes in
-// all arrays, where `ctas` share an SM's shared memory: at most `most`, no more
-// than gives each CTA several sets; 0 where not even one row fits twice.
-int rows_at_a_time(int64_t row_bytes, int ctas, int64_t rows_each, int most) {
-  for (int r = most; r >= 1; r /= 2)
-    if (kSets * r * row_bytes * ctas <= 200 << 10 && rows_each >= 2 * r) return r;
+constexpr int64_t kRingBytes = 200 << 10;  // of an SM's shared memory
+
+// Rows that a CTA of the ring kernels takes at a time, whose slots have so many
+// bytes, where `ctas` share an SM's shared memory: `most`, or one where that
+// does not fit or leaves a CTA less than two sets; 0 where one does not either.
+int rows_at_a_time(int64_t slot, int ctas, int64_t rows_each, int most) {
+  for (const int r : {most, 1})
+    if (2 * r * slot * ctas <= kRingBytes && rows_each >= 2 * r) return r;
   return 0;
 }
+// Sets of so many bytes that a CTA keeps.
+int sets_of(int64_t bytes, int ctas) { return static_cast<int>(std::min<int64_t>(kMaxSets, kRingBytes / ctas / bytes)); }
+
+// Bytes that a row's pieces take.
+int64_t slot_of(int64_t row_bytes, bool pieces) { return pieces ? row_bytes : (row_bytes + 15 + 15) / 16 * 16; }
 
 template <typename... Params, typename... Args>
 bwd_status launch_ring(void (*kernel)(Params...), int64_t ctas, int threads, int smem, cudaStream_t st, const char* what, const Args&... args) {
-  if (smem > 48 * 1024) {
-    const cudaError_t e = opt_in(kernel, 200 << 10);
+  if (smem > 40 * 1024) {  // 48 KB, less the static variables
+    const cudaError_t e = opt_in(kernel, static_cast<int>(kRingBytes));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
   }
   return launch_ex(kernel, dim3(static_cast<unsigned>(ctas)), threads, 0, smem, st, what, args...);
@@ -769,75 +848,80 @@ bwd_status sm_count(int* out) {
   return BWD_OK;
 }
 
-// Values of the largest unit that all of a call's rows consist of and start on.
+// Values of the largest unit that all of a call's rows consist of and start on:
+// a piece of 16 bytes, 4 bytes, or one value.
 int unit_values(int eb, uintptr_t addresses, int64_t row_bytes) {
   const uintptr_t all = addresses | static_cast<uintptr_t>(row_bytes);
-  const int bytes = all % 16 == 0 ? 16 : all % 8 == 0 ? 8 : all % 4 == 0 ? 4 : 2;
-  return bytes / eb;
+  return all % 16 == 0 ? 16 / eb : all % 4 == 0 ? 4 / eb : 1;
 }
 
-template <template <int, int, bool, int> class Launch, typename Args, typename... More>
-bwd_status by_type(int type, int values, int width, const Args& a, More... more) {
-  const auto sized = [&](auto t, auto v) {
-    constexpr int kT = decltype(t)::value, kVals = decltype(v)::value;
-    if (width <= kWarpWidth) return Launch<kT, kVals, true, 32 * kWarps>::go(a, more...);
-    const int threads = threads_of(width);
-    if (threads <= kMaxThreads / 4) return Launch<kT, kVals, false, kMaxThreads / 4>::go(a, more...);
-    if (threads <= kMaxThreads / 2) return Launch<kT, kVals, false, kMaxThreads / 2>::go(a, more...);
-    return Launch<kT, kVals, false, kMaxThreads>::go(a, more...);
-  };
+// Calls f<type, unit>.
+template <typename F>
+bwd_status by_type(int type, int values, F f) {
   const auto typed = [&](auto t) {
-    constexpr int kT = decltype(t)::value;
-    if constexpr (kT != kF32)
-      if (values == 8) return sized(t, std::integral_constant<int, 8>{});
-    if (values == 4) return sized(t, std::integral_constant<int, 4>{});
-    if (values == 2) return sized(t, std::integral_constant<int, 2>{});
-    return sized(t, std::integral_constant<int, 1>{});
+    constexpr int kT = decltype(t)::value, kEb = elem_bytes<kT>();
+    if (values == 16 / kEb) return f(t, std::integral_constant<int, 16 / kEb>{});
+    if constexpr (kEb != 4)
+      if (values == 2) return f(t, std::integral_constant<int, 2>{});
+    return f(t, std::integral_constant<int, 1>{});
   };
   if (type == BWD_F32) return typed(std::integral_constant<int, kF32>{});
   if (type == BWD_BF16) return typed(std::integral_constant<int, kBF16>{});
   return typed(std::integral_constant<int, kF16>{});
 }
 
-template <int kT, int kVals, bool kWarp, int kMax>
-struct LaunchForward {
-  static bwd_status go(const ForwardArgs& a, int sms, cudaStream_t st) {
-    constexpr bool kPieces = kVals * elem_bytes<kT>() == 16 && !kWarp;
-    const int threads = kWarp ? 32 * kWarps : threads_of(a.width), per_sm = std::max(1, std::min(768 / threads, 8));
-    const int64_t most = static_cast<int64_t>(sms) * per_sm, need = kWarp ? (a.rows + kWarps - 1) / kWarps : a.rows;
-    const int64_t ctas = std::min(need, most);
-    if constexpr (kPieces) {
-      const int row_bytes = a.width * elem_bytes<kT>(), r = rows_at_a_time(row_bytes, per_sm, a.rows / ctas, 4);
-      const auto go = [&](auto* kernel) {
-        return launch_ring(kernel, ctas, threads, kSets * r * row_bytes, st, "norm_forward_ring_kernel launch", a, row_bytes);
-      };
-      if (r == 4) return go(norm_forward_ring_kernel<kT, kMax, 4>);
-      if (r == 2) return go(norm_forward_ring_kernel<kT, kMax, 2>);
-      if (r == 1) return go(norm_forward_ring_kernel<kT, kMax, 1>);
-    }
-    return launch_ex(norm_forward_kernel<kT, kVals, kWarp, kMax>, dim3(static_cast<unsigned>(ctas)), threads, 0, 0, st,
-                     "norm_forward_kernel launch", a);
+template <int kT, int kVals>
+bwd_status launch_forward(const ForwardArgs& a, int sms, cudaStream_t st) {
+  constexpr bool kPieces = kVals * elem_bytes<kT>() == 16;
+  const auto plain = [&](auto* kernel, int64_t ctas, int threads) {
+    return launch_ex(kernel, dim3(static_cast<unsigned>(ctas)), threads, 0, 0, st, "norm_forward_kernel launch", a);
+  };
+  if (a.width <= kWarpWidth)
+    return plain(norm_forward_kernel<kT, kVals, kFew, true>, std::min<int64_t>((a.rows + kWarps - 1) / kWarps, 3 * sms), 32 * kWarps);
+  const int threads = threads_of(a.width), per = forward_per_sm(a.width, kPieces);
+  const int64_t ctas = std::min<int64_t>(a.rows, static_cast<int64_t>(sms) * per), slot = slot_of(a.width * elem_bytes<kT>(), kPieces);
+  const int r = rows_at_a_time(slot, per, a.rows / ctas, !kPieces ? 1 : values_of(a.width) == kFew ? 4 : 2);
+  const auto ring = [&](auto* kernel) {
+    const int sets = sets_of(r * slot, per);
+    return launch_ring(kernel, ctas, threads, static_cast<int>(sets * r * slot), st, "norm_forward_ring_kernel launch", a, static_cast<int>(slot), sets);
+  };
+  if (values_of(a.width) == kFew) {
+    if constexpr (kPieces)
+      if (r == 4) return ring(norm_forward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 4>);
+    if (r == 1) return ring(norm_forward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 1>);
+    return plain(norm_forward_kernel<kT, kVals, kFew, false>, ctas, threads);
   }
-};
+  if constexpr (kPieces)
+    if (r == 2) return ring(norm_forward_ring_kernel<kT, kPieces, kMany, kMaxThreads, 2>);
+  if (r == 1) return ring(norm_forward_ring_kernel<kT, kPieces, kMany, kMaxThreads, 1>);
+  return plain(norm_forward_kernel<kT, kVals, kMany, false>, ctas, threads);
+}
 
-template <int kT, int kVals, bool kWarp, int kMax>
-struct LaunchBackward {
-  static bwd_status go(const BackwardArgs& a, int64_t ctas, cudaStream_t st) {
-    constexpr bool kKeep = kMax <= kMaxThreads / 2, kPieces = kVals * elem_bytes<kT>() == 16 && !kWarp && kKeep;
-    const int threads = kWarp ? 32 * kWarps : threads_of(a.width), per_sm = std::max(1, std::min(512 / threads, 8));
-    if constexpr (kPieces) {
-      // (the partial sums go out in pieces of 16 bytes too)
-      const int row_bytes = a.width * elem_bytes<kT>(), r = aligned16(a.partial) ? rows_at_a_time(2 * row_bytes, per_sm, a.rows / ctas, 2) : 0;
-      const auto go = [&](auto* kernel) {
-        return launch_ring(kernel, ctas, threads, kSets * r * 2 * row_bytes, st, "norm_backward_ring_kernel launch", a, row_bytes);
-      };
-      if (r == 2) return go(norm_backward_ring_kernel<kT, kMax, 2>);
-      if (r == 1) return go(norm_backward_ring_kernel<kT, kMax, 1>);
-    }
-    const int smem = a.partial && (kWarp || !kKeep) ? 8 * a.width : 0;
-    return launch_ring(norm_backward_kernel<kT, kVals, kWarp, kMax>, ctas, threads, smem, st, "norm_backward_kernel launch", a);
+template <int kT, int kVals>
+bwd_status launch_backward(const BackwardArgs& a, int64_t ctas, cudaStream_t st) {
+  constexpr bool kPieces = kVals * elem_bytes<kT>() == 16;
+  const auto plain = [&](auto* kernel, int threads) {
+    return launch_ex(kernel, dim3(static_cast<unsigned>(ctas)), threads, 0, 0, st, "norm_backward_kernel launch", a);
+  };
+  if (a.width <= kWarpWidth) return plain(norm_backward_kernel<kT, kVals, kFew, true>, 32 * kWarps);
+  const int threads = threads_of(a.width), per = backward_per_sm(a.width);
+  const int64_t slot = slot_of(a.width * elem_bytes<kT>(), kPieces);
+  const int r = rows_at_a_time(2 * slot, per, a.rows / ctas, kPieces && values_of(a.width) == kFew ? 2 : 1);
+  const auto ring = [&](auto* kernel) {
+    const int sets = sets_of(2 * r * slot, per);
+    return launch_ring(kernel, ctas, threads, static_cast<int>(sets * 2 * r * slot), st, "norm_backward_ring_kernel launch", a, static_cast<int>(slot), sets);
+  };
+  if (values_of(a.width) == kFew) {
+    if constexpr (kPieces)
+      if (r == 2) return ring(norm_backward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 2>);
+    if (r == 1) return ring(norm_backward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 1>);
+    return plain(norm_backward_kernel<kT, kVals, kFew, false>, threads);
   }
-};
+  // (a thread's sums and values fit its registers where a CTA has no more than 384)
+  if (r == 1 && threads <= 384) return ring(norm_backward_ring_kernel<kT, kPieces, kMany, 384, 1>);
+  if (r == 1) return ring(norm_backward_ring_kernel<kT, kPieces, kMany, kMaxThreads, 1>);
+  return plain(norm_backward_kernel<kT, kVals, kMany, false>, threads);
+}
 
 constexpr int64_t kMaxRows = int64_t{1} << 31;
 
@@ -877,7 +961,9 @@ bwd_status bwd_norm_forward(const void* x, bwd_dtype dtype, int64_t rows, int64_
   const int f32 = vector_dtype == BWD_F32;
   const ForwardArgs a{x, ldx, {gamma, f32}, {beta, f32}, y, mean, rstd, rows, static_cast<int>(width), eps};
   const int values = unit_values(eb, reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y), (ldx | width) * eb);
-  return by_type<LaunchForward>(dtype, values, a.width, a, sms, static_cast<cudaStream_t>(stream));
+  return by_type(dtype, values, [&](auto t, auto v) {
+    return launch_forward<decltype(t)::value, decltype(v)::value>(a, sms, static_cast<cudaStream_t>(stream));
+  });
 }
 
 int64_t bwd_norm_backward_work_bytes(int64_t rows, int64_t width) {
@@ -907,7 +993,8 @@ bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype, int
                          static_cast<int>(width)};
     const int values = unit_values(eb, reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(dx),
                                    (ldx | lddy | width) * eb);
-    if ((s = by_type<LaunchBackward>(dtype, values, a.width, a, ctas, st)) != BWD_OK) return s;
+    s = by_type(dtype, values, [&](auto t, auto v) { return launch_backward<decltype(t)::value, decltype(v)::value>(a, ctas, st); });
+    if (s != BWD_OK) return s;
   }
   if (!sums) return BWD_OK;
   const SumArgs a{static_cast<const float*>(work), rows > 0 ? ctas : 0, static_cast<int>(width), {dgamma, dbeta}, {vector_dtype, vector_dtype}};

@@ -125,7 +125,7 @@ def matmul(a: Fp4Matrix, b: Fp4Matrix, bias: Optional[torch.Tensor] = None, dtyp
     return out
 
 
-_FUSED_ROWS, _FUSED_COLS = 16, 229_376  # what the library's product quantizes itself, without a workspace
+_FUSED_ROWS, _FUSED_COLS = 8, 229_376  # what the library's product quantizes itself, without a workspace
 
 
 @lru_cache(maxsize=1024)

@@ -512,7 +512,7 @@ bwd_status bwd_fp4_matmul(int64_t m, int64_t n, int64_t k, const uint8_t* a,
 /* y = Q(x) W^T + bias in one call, x (rows x cols) quantized in the workspace.
  *   w, w_scales : of the n x cols weight.   y : rows x n of x's type.
  *   work : device, 16-byte aligned, bwd_fp4_linear_work_bytes(rows, cols)
- *          bytes; none, and NULL will do, for up to 16 rows of up to 229,376
+ *          bytes; none, and NULL will do, for up to 8 rows of up to 229,376
  *          elements, which the product's kernel quantizes itself. */
 int64_t bwd_fp4_linear_work_bytes(int64_t rows, int64_t cols);
 bwd_status bwd_fp4_linear(const void* x, bwd_dtype dtype, int64_t rows,

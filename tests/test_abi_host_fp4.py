@@ -30,9 +30,9 @@ def test_sizes(lib):
             layout = fp4._layout(rows, cols)
             assert layout[0] == pitch and layout[2] - layout[1] == lib.bwd_fp4_scale_bytes(rows, cols)
             assert fp4._work(rows, cols) == lib.bwd_fp4_linear_work_bytes(rows, cols)
-    for rows, cols in ((16, 229_376), (16, 229_377), (17, 1), (1, 1 << 20)):
+    for rows, cols in ((8, 229_376), (8, 229_377), (9, 1), (1, 1 << 20)):
         assert fp4._work(rows, cols) == lib.bwd_fp4_linear_work_bytes(rows, cols)
-        assert (fp4._work(rows, cols) == 0) == (rows <= 16 and cols <= 229_376)
+        assert (fp4._work(rows, cols) == 0) == (rows <= 8 and cols <= 229_376)
 
 
 def test_quantize_and_dequantize_refuse(lib):
@@ -52,7 +52,7 @@ def test_products_refuse(lib):
         assert lib.bwd_fp4_matmul(*{**good, **b}.values()) in (1, 2), b
     good = dict(x=P, dtype=1, rows=3, cols=10, ld=10, w=P, ws=P, n=4, bias=P, y=P, ldy=4, work=P, stream=None)
     for b in (dict(dtype=5), dict(rows=-1), dict(ld=9), dict(n=-1), dict(ldy=3), dict(x=None), dict(w=None), dict(ws=None), dict(y=None),
-              dict(rows=17, work=None), dict(work=P + 8), dict(w=P + 8), dict(y=P + 1), dict(bias=P + 1)):
+              dict(rows=9, work=None), dict(work=P + 8), dict(w=P + 8), dict(y=P + 1), dict(bias=P + 1)):
         assert lib.bwd_fp4_linear(*{**good, **b}.values()) in (1, 2), b
 
 

@@ -93,7 +93,8 @@ def check_backward(dy, x, gamma, mean, rstd, dx, dgamma, dbeta):
 
 
 SIZES = [(1, 1), (1, 4096), (3, 7), (5, 33), (1, 16384), (300, 64), (77, 512), (77, 513), (129, 1003), (40, 1024), (33, 4096), (9, 8192),
-         (9, 8200), (5, 11008), (3, 16383), (2000, 130), (4000, 1000)]
+         (9, 8200), (5, 11008), (3, 16383), (2000, 130), (4000, 1000), (2500, 1003), (3000, 520), (700, 4100), (700, 4096), (900, 8193),
+         (700, 9001), (700, 6144), (700, 12288), (650, 16384), (640, 13001)]
 
 
 @pytest.mark.parametrize("kind,vectors", [("fp32", "fp32"), ("bf16", "fp32"), ("bf16", "bf16"), ("fp16", "fp32"), ("fp16", "fp16")])
@@ -113,11 +114,11 @@ def test_both_passes(norm, rows, width, kind, vectors):
 
 
 @pytest.mark.parametrize("kind", ["fp32", "bf16"])
-@pytest.mark.parametrize("off,pitch", [(0, 8), (1, 0), (1, 3), (2, 2), (4, 4), (0, 1)])
-@pytest.mark.parametrize("width", [96, 1024, 9000])
-def test_strides_and_alignment(norm, width, off, pitch, kind):
+@pytest.mark.parametrize("off,pitch", [(0, 8), (1, 0), (1, 3), (2, 2), (4, 4), (0, 1), (7, 9)])
+@pytest.mark.parametrize("rows,width", [(37, 96), (37, 1024), (37, 9000), (2000, 1001), (700, 4098), (650, 9003)])
+def test_strides_and_alignment(norm, rows, width, off, pitch, kind):
     """Rows with a pitch, and starts off every boundary; what lies between is left alone."""
-    rows, flat = 37, torch.zeros(60 + 37 * (width + pitch), dtype=TYPES[kind], device=DEV)
+    flat = torch.full((off + rows * (width + pitch),), 1e4, dtype=TYPES[kind], device=DEV)
     x = flat[off:off + rows * (width + pitch)].view(rows, width + pitch)[:, :width]
     x.copy_(draw(rows, width, 5, kind))
     dy_flat = torch.zeros_like(flat)
