@@ -173,6 +173,8 @@ class Muon(torch.optim.Optimizer):
                 raise TypeError("Muon needs fp32, bf16 or fp16 CUDA parameters")
             if g.is_sparse:
                 raise TypeError("sparse gradients are not supported")
+            if not p.is_contiguous():
+                raise ValueError("Muon needs contiguous parameters")
             if "momentum_buffer" not in self.state[p]:
                 self.state[p]["momentum_buffer"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
             buckets.setdefault((p.device, p.dtype, g.dtype), []).append(i)

@@ -243,6 +243,41 @@ def test_a_weight_written_by_the_kernel_ahead(fp4):
     for _ in range(20):
         for w, y in zip(ws, want):
             assert torch.equal(fp4.matmul(xq, fp4.quantize(w)), y)
+    # rows that a launch of their own quantizes between the weight's and the product
+    for rows in (40, 200):
+        x = draw((rows, 2048), 2, "bf16")
+        want = [fp4.linear(x, fp4.quantize(w)) for w in ws]
+        torch.cuda.synchronize()
+        for _ in range(20):
+            got = [fp4.linear(x, fp4.quantize(w)) for w in ws]
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once(fp4):
+    x = [draw((rows, 1500), rows, "bf16") for rows in (3, 40, 300, 1000)]
+    w = draw((900, 1500), 1, "bf16")
+    wq = fp4.quantize(w)
+    want = [fp4.linear(a, wq) for a in x]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in x]
+    for _ in range(20):
+        got = [fp4.linear(a, wq, stream=s) for a, s in zip(x, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_the_largest_pitch(fp4):
+    """Codes and values beyond 2^31 elements."""
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 20 GB")
+    rows, cols = 70000, 32000
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(DEV).manual_seed(0))
+    q = fp4.quantize(x)
+    last = fp4.quantize(x[-3:])
+    assert torch.equal(q.codes[-3:], last.codes)
+    assert torch.equal(q.dequantize()[-3:], last.dequantize())
+    y = fp4.linear(x, fp4.quantize(x[:130]))
+    assert torch.equal(y[-3:], fp4.matmul(last, fp4.quantize(x[:130])))
 
 
 def test_module(fp4):

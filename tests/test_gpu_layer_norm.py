@@ -256,3 +256,16 @@ def test_streams_and_graphs(norm):
     torch.cuda.synchronize()
     check_forward(x, gamma, None, *out[:3], norm.EPS)
     check_backward(dy, x, gamma, out[1], out[2], *out[3:])
+
+
+def test_two_streams_at_once(norm):
+    x = [draw(rows, width, i, "bf16") for i, (rows, width) in enumerate(((900, 4096), (900, 1003), (40, 300)))]
+    want = [norm.forward(a) for a in x]
+    want = [w + norm.backward(a, a, None, *w[1:]) for a, w in zip(x, want)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in x]
+    for _ in range(10):
+        got = [norm.forward(a, stream=s) for a, s in zip(x, streams)]
+        got = [g + norm.backward(a, a, None, *g[1:], stream=s) for a, g, s in zip(x, got, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))

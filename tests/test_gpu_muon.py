@@ -312,3 +312,55 @@ def test_optimizer_groups_and_missing_gradients(muon):
     give_gradients(m, 5)  # another set of gradients than the plan's
     opt.step()
     assert not torch.equal(ps[2], before[2])
+
+
+def test_optimizer_refusals(muon):
+    p = torch.nn.Parameter(torch.zeros(4, 6, device=DEV).t())
+    p.grad = torch.ones(6, 4, device=DEV)
+    with pytest.raises(ValueError, match="contiguous"):
+        muon.Muon([p]).step()
+    p = torch.nn.Parameter(torch.zeros(4, 6, device=DEV))
+    opt = muon.Muon([p])
+    with pytest.raises(ValueError, match="no parameter has a gradient"):
+        opt.clip_scale(1.0)
+    opt.step()  # nothing to do
+    p.grad = torch.ones(4, 6, device=DEV)
+    opt.step()
+    p.grad = torch.ones(4, 6, device=DEV).t().contiguous().t()  # of another layout: copied
+    opt.step()
+    assert torch.isfinite(p).all()
+    opt.param_groups[0]["lr"] = -1.0
+    from block_wise_dynamic_gb300 import BwdError
+
+    before = p.detach().clone()
+    with pytest.raises(BwdError):
+        opt.step()
+    assert torch.equal(p, before)
+
+
+def test_two_streams_at_once(muon):
+    """Lists with workspaces of their own, small and large matrices, side by side."""
+    sets = [lists([(300, 200), (64, 100)], torch.float32, torch.float32, s) for s in (0, 1000)]
+    sets += [lists([(700, 1900)], torch.float32, torch.float32, 2000)]
+    alone = [[[t.clone() for t in l] for l in s] for s in sets]
+    for s in alone:
+        args = muon.MuonArgs(*s)
+        for _ in range(5):
+            args.step()
+    args = [muon.MuonArgs(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        for a, st in zip(args, streams):
+            a.step(stream=st)
+    torch.cuda.synchronize()
+    for s, t in zip(sets, alone):
+        assert all(torch.equal(a, b) for a, b in zip(s[0] + s[2], t[0] + t[2]))
+
+
+def test_fifty_thousand_columns(muon):
+    """A long row: offsets, and sums of many stages."""
+    g = draw(3, 50000, 1)
+    check(muon.orthogonalize(g), g)
+    g = draw(40001, 5, 2)
+    check(muon.orthogonalize(g), g)
