@@ -132,8 +132,10 @@ __device__ __forceinline__ void update8(const PrepareArgs& a, const void* g, flo
 }
 
 // One chunk of one matrix: the new momentum, and the update's sum of squares
-// into its slot (in fp32 for a thread's eight elements, in binary64 beyond
-// them, or from the start where fp32 does not hold the squares).
+// into its slot.  A thread adds in fp32, with what each addition loses carried
+// along, a warp in fp32, and only the warps in binary64, of which the device
+// does few (with all of it in binary64 33.5M bf16 values took 34 us).  Eight
+// values whose squares fp32 does not hold in full are squared in binary64.
 template <int kT, bool kMomentum>
 __global__ void __launch_bounds__(kThreads)
 ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
@@ -148,9 +150,10 @@ ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
   float* const mom = a.x.mom[z];
   const float s = kMomentum && a.grad_scale ? *a.grad_scale : 1.0f;
   const bool vec = on16(g) && on16(mom);
-  double sum = 0.0;
+  float sum = 0.0f, lost = 0.0f;
+  double wide = 0.0;
   const int64_t end = min(p.size, (chunk + 1) * p.chunk);
-#pragma unroll 2
+#pragma unroll 4
   for (int64_t i = chunk * p.chunk + 8 * threadIdx.x; i < end; i += 8 * kThreads) {
     float u[8];
     update8<kT, kMomentum, true>(a, g, mom, s, vec, i, end, u);
@@ -161,20 +164,27 @@ ns_norm_kernel(const __grid_constant__ PrepareArgs a) {
       any |= __float_as_uint(u[j]);
       part = __fmaf_rn(u[j], u[j], part);
     }
-    if ((any & 0x7fffffffu) != 0 && !(part >= 0x1p-120f && part <= 3.402823466e38f)) {
+    if ((any & 0x7fffffffu) != 0 && !(part >= 0x1p-120f && part <= 0x1p100f)) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __fma_rn(static_cast<double>(u[j]), static_cast<double>(u[j]), sum);
+      for (int j = 0; j < 8; ++j) wide = __fma_rn(static_cast<double>(u[j]), static_cast<double>(u[j]), wide);
     } else {
-      sum += static_cast<double>(part);
+      const float next = __fsub_rn(part, lost), all = __fadd_rn(sum, next);
+      lost = __fsub_rn(__fsub_rn(all, sum), next);
+      sum = all;
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = sum;
+  if (__any_sync(0xffffffffu, wide != 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xffffffffu, wide, o);
+  }
+  wide += static_cast<double>(sum);
+  if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = wide;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int w = 1; w < kThreads / 32; ++w) sum += s_red[w];
-  a.slots[z * kSlots + chunk] = sum;
+  for (int w = 1; w < kThreads / 32; ++w) wide += s_red[w];
+  a.slots[z * kSlots + chunk] = wide;
 }
 
 // Two values as packed pairs of high and low parts.
@@ -196,7 +206,6 @@ template <int kT, bool kMomentum>
 __global__ void __launch_bounds__(kThreads)
 ns_split_kernel(const __grid_constant__ PrepareArgs a) {
   __shared__ float s_x[64][65];
-  __shared__ double s_red[kThreads / 32];
   __shared__ float s_inv[2];
   wait_for_inputs();
   let_next_begin();
@@ -205,19 +214,18 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
   const PrepareGroup& p = a.g[gi];
   const int strips = (p.pitch + p.split_cols - 1) / p.split_cols, per = strips * ((p.m + kSplitRows - 1) / kSplitRows);
   const int local = static_cast<int>(blockIdx.x) - p.split_start, in_group = local / per, tile = local % per, z = p.first + in_group;
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < p.chunks; i += kThreads) sum += a.slots[z * kSlots + i];
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < p.chunks; i += 32) sum += a.slots[z * kSlots + i];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (threadIdx.x % 32 == 0) s_red[threadIdx.x / 32] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kThreads / 32; ++w) sum += s_red[w];
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     // the norm may pass fp32's range, and its reciprocal what fp32 holds in full
     const double norm = sqrt(sum) + static_cast<double>(kEps);
     const bool large = norm > 0x1p64;
-    s_inv[0] = large ? 0x1p-64f : 1.0f;
-    s_inv[1] = static_cast<float>((large ? 0x1p64 : 1.0) * static_cast<double>(kScale) / norm);
+    if (threadIdx.x == 0) {
+      s_inv[0] = large ? 0x1p-64f : 1.0f;
+      s_inv[1] = static_cast<float>((large ? 0x1p64 : 1.0) * static_cast<double>(kScale) / norm);
+    }
   }
   __syncthreads();
   const float first = s_inv[0], inv = s_inv[1];
@@ -1202,7 +1210,11 @@ template <int kMode>
 bwd_status product(const Operation& o, float alpha, float beta, int passes, const FinalArgs* f, const Step& st, const DeviceState& d,
                    cudaStream_t stream) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
-  const auto waves = [&](int bn) { return (o.count * tiles_of(o.result, kBM, bn, kSymmetric) + d.pairs - 1) / d.pairs; };
+  // (the last wave of 256 columns counts half where its tiles are cut into halves)
+  const int64_t items = o.count * tiles_of(o.result, kBM, 256, kSymmetric), left = items % d.pairs;
+  const bool halves = 2 * left <= d.pairs;
+  const double waves256 = static_cast<double>(items / d.pairs) + (left == 0 ? 0.0 : halves ? 0.5 : 1.0);
+  const double waves128 = static_cast<double>((o.count * tiles_of(o.result, kBM, 128, kSymmetric) + d.pairs - 1) / d.pairs);
   const int64_t kblocks = (o.k + kBK - 1) / kBK, small = o.count * tiles_of(o.result, kSmallRows, kSmallCols, kSymmetric);
   const int split = small_split(small, kblocks, d);
   // Small tiles where they take less time than the large ones.  In us: a stage
@@ -1216,21 +1228,19 @@ bwd_status product(const Operation& o, float alpha, float beta, int passes, cons
   const double full = std::min(1.0, static_cast<double>(small * split) / static_cast<double>(at_once));
   const double stage = (0.2 + 0.3 * full) * (passes == 3 ? 1.0 : 0.5);
   const double small_time = static_cast<double>(small_waves) * (5.0 + stage * static_cast<double>((kblocks + split - 1) / split));
-  const double large_time = 8.0 + std::min(0.24 * static_cast<double>(waves(128)), 0.36 * static_cast<double>(waves(256))) *
-                                      static_cast<double>(passes * kblocks);
+  const double large_time = 8.0 + std::min(0.24 * waves128, 0.36 * waves256) * static_cast<double>(passes * kblocks);
   if (small_time < large_time) return products<kMode>(&o, 1, alpha, beta, passes, f, st, d, stream);
-  // a tile of 256 columns takes up to one and a half times as long as one of 128
-  const int bn = 3 * waves(256) < 2 * waves(128) ? 256 : 128;
+  // (eight matrices of 1024 x 4096, A: 133 us with 128 columns, three waves, and 120 with 256, one and a half)
+  const int bn = 0.36 * waves256 < 0.24 * waves128 ? 256 : 128;
   ProductArgs a{};
   // of a pair's tile each CTA copies half of either operand's lines
   bwd_status s = fill_args<kMode>(a, o, kBM, bn, kBM / 2, bn / 2, passes, alpha, beta);
   if (s == BWD_OK && o.add) s = plane_map(&a.add, o.add, o.result.m, a.pitch, 2 * o.count, 32, 32);
   if (s == BWD_OK && o.out) s = plane_map(&a.out, o.out, o.result.m, a.pitch, 2 * o.count, 32, 32);
   if (s != BWD_OK) return s;
-  const int last = a.items % d.pairs;
-  if (bn == 256 && 2 * last <= d.pairs) {
-    a.whole = a.items - last;
-    a.items += last;
+  if (bn == 256 && halves) {
+    a.whole = a.items - static_cast<int>(left);
+    a.items += static_cast<int>(left);
   }
   return bn == 256 ? launch_product<256, kMode>(a, f, st, d.pairs, stream) : launch_product<128, kMode>(a, f, st, d.pairs, stream);
 }

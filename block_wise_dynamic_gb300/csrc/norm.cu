@@ -383,7 +383,7 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 template <int kT, bool kPieces, int kValues>
 struct Columns {
   static constexpr int kPairs = kValues / 2;
-  [[maybe_unused]] static constexpr int kUnitPairs = 8 / elem_bytes<kT>(), kUnits = kPairs / kUnitPairs;
+  [[maybe_unused]] static constexpr int kUnitPairs = kPieces ? 8 / elem_bytes<kT>() : kPairs;  // of a unit
   int t, threads, width;
   __device__ __forceinline__ int first(int e) const {
     if constexpr (kPieces) return ((e / kUnitPairs * threads + t) * kUnitPairs + e % kUnitPairs) * 2;
@@ -401,7 +401,7 @@ struct Columns {
   __device__ __forceinline__ void over(char* out, const uint8_t* const (&row)[kN], F f) const {
     if constexpr (kPieces) {
       // all of a thread's loads before the first use, where registers allow it
-      constexpr int kAtOnce = kValues == kFew ? kUnits : 1;
+      constexpr int kUnits = kPairs / kUnitPairs, kAtOnce = kValues == kFew ? kUnits : 1;
 #pragma unroll
       for (int i0 = 0; i0 < kUnits; i0 += kAtOnce) {
         uint4 w[kAtOnce][kN];
