@@ -19,6 +19,19 @@
 // spectrum is level and an operand's rounding counts once: for bf16 results,
 // whose own rounding is 1.7e-3, that step takes the high parts alone (4e-4 to
 // 7e-4 more).
+//
+// The last steps of a wide matrix (n columns, m rows, n > m) stay among m x m
+// matrices, all of them polynomials of A, so that they commute and their
+// products are symmetric:
+//
+//   P = a I + B;  Q = P Q;  A = P A P        and in the end X = Q X
+//
+// A step takes four symmetric products, 4 m m m operations, in place of m m n
+// + m m m + 2 m m n.  What it costs is precision: rounding A moves its small
+// eigenvalues, squares of the singular values, which a step raises by 11.8 as
+// it raises those by 3.4; see squared_steps for how many steps that leaves.
+// Of a bf16 gradient times a power of two X has no low part: its product with
+// itself then takes one pass, and that with Q two.
 #include "tensor.cuh"
 
 #include <algorithm>
@@ -64,6 +77,7 @@ struct PrepareGroup {
 struct PrepareArgs {
   Matrices x;
   double* slots;            // [matrix][kSlots]
+  float* scale;             // [matrix] of exact planes: X = scale planes / kScale; null: pairs
   const float* grad_scale;  // or null: 1
   float momentum;
   int nesterov;
@@ -197,6 +211,8 @@ __device__ __forceinline__ void split2(float v0, float v1, uint32_t& high, uint3
 }
 
 // X's pair from the update, 64 rows and split_cols columns of the wide form to a CTA.
+// Of a 16-bit gradient, whose bits fp16 holds, the high part alone with a
+// power of two for its factor, and what is left of the factor as a.scale.
 // A tall matrix goes through shared memory, 64 x 64 elements at a time, so
 // that both sides' rows are contiguous.  Columns up to the pitch are written,
 // as zeros.
@@ -224,7 +240,10 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
     const bool large = norm > 0x1p64;
     if (threadIdx.x == 0) {
       s_inv[0] = large ? 0x1p-64f : 1.0f;
-      s_inv[1] = static_cast<float>((large ? 0x1p64 : 1.0) * static_cast<double>(kScale) / norm);
+      const float inv = static_cast<float>((large ? 0x1p64 : 1.0) * static_cast<double>(kScale) / norm);
+      const float power = __uint_as_float(__float_as_uint(inv) & 0x7f800000u);
+      s_inv[1] = a.scale ? power : inv;
+      if (a.scale && tile == 0) a.scale[z] = __fdiv_rn(inv, power);
     }
   }
   __syncthreads();
@@ -245,7 +264,7 @@ ns_split_kernel(const __grid_constant__ PrepareArgs a) {
     for (int j = 0; j < 4; ++j) split2(x[2 * j], x[2 * j + 1], (&h.x)[j], (&l.x)[j]);
     const int64_t at = static_cast<int64_t>(row) * p.pitch + col;
     *reinterpret_cast<uint4*>(high + at) = h;
-    *reinterpret_cast<uint4*>(low + at) = l;
+    if (!a.scale) *reinterpret_cast<uint4*>(low + at) = l;
   };
   for (int c0 = tile % strips * p.split_cols, c1 = c0 + p.split_cols; c0 < c1; c0 += 64) {
     const int sr0 = tall ? c0 : r0, sc0 = tall ? r0 : c0, rows = tall ? p.n : p.m;
@@ -310,15 +329,25 @@ enum Mode { kGram, kPoly, kApply, kFinal };
 struct ProductArgs {
   CUtensorMap p, q;      // planes of the two operands
   CUtensorMap add, out;  // planes that alpha multiplies, and the result's, in boxes of 32 x 32
-  const __half* add_at;  // the same planes' addresses
+  const __half* add_at;  // the same planes' addresses; null: nothing is added
   __half* out_at;
   int m, n, pitch;       // the result's
   int kblocks;
-  int passes;            // 3, or 1: the high parts alone
+  int passes;            // 3; 2: q's high part alone; 1: the high parts alone
   int tiles_m, tiles_n, tiles, items;
   int whole;             // the first items; the others are halves of a tile
   float alpha, beta;     // result = alpha add + beta product
+  const float* scale;    // [matrix] of exact planes, or null; a factor of beta, its square for A
+  const float* diagonal; // [matrix][m] of p, which has zeros there, or null: in place of alpha, times beta
 };
+
+// beta of one matrix.
+template <int kMode>
+__device__ __forceinline__ float beta_of(const ProductArgs& a, int z) {
+  if ((kMode != kGram && kMode != kFinal) || !a.scale) return a.beta;
+  const float s = a.scale[z];
+  return __fmul_rn(a.beta, kMode == kGram ? __fmul_rn(s, s) : s);
+}
 
 struct FinalArgs {
   Matrices x;
@@ -395,20 +424,25 @@ __device__ __forceinline__ float half_at(const uint4& w, int j) {
 }
 
 // The matrix instruction adds into its fp32 accumulator with truncation, an
-// error with a sign, which A's diagonal shows in full.  For fp32 results (kSum)
-// the sums leave it every kChunk stages of high x high, 256 products, and are
-// added up in registers, rounded to nearest; what low parts add is 2^-11 of
-// that and stays for all of their products.  (777 x 301: error 5.2e-6 without,
-// and fp32 arithmetic has 1.8e-6.)
-constexpr int kChunk = 4;
+// error with a sign, which A's diagonal shows in full.  So sums leave it every
+// kChunk stages of high x high, 128 products, and are added up in registers,
+// rounded to nearest; what low parts add is 2^-11 of that and stays for all of
+// their products.  (1000 x 1000, fp32: error 1.6e-6, 2.5e-6 with 256 products;
+// 96 x 1024 x 1024 and 48 x 1024 x 4096 9.13 ms, 8.98 with 256.)
+constexpr int kChunk = 2;
 
 // Stages of a tile whose sums leave the accumulator together, from stage k on.
-template <bool kSum>
 __device__ __forceinline__ int chunk_end(const ProductArgs& a, int k) {
   const int all = a.passes * a.kblocks, small = all - a.kblocks;
-  if (!kSum) return all;
   if (k < small) return small;
   return k + kChunk < all ? k + kChunk : all;
+}
+
+// alpha of one row.
+template <int kMode>
+__device__ __forceinline__ float alpha_of(const ProductArgs& a, int z, int row) {
+  if (kMode != kFinal || !a.diagonal) return a.alpha;
+  return row < a.m ? __fmul_rn(a.beta, a.diagonal[static_cast<int64_t>(z) * a.m + row]) : 0.0f;
 }
 
 // What a pair works on: a tile, or half of its columns.  A last wave that less
@@ -425,7 +459,7 @@ __device__ __forceinline__ Tile item_of(const ProductArgs& a, int i, int* cols) 
 
 // kT and kUpdate: of the last product, whose result has type kT, or updates a
 // parameter of that type.
-template <int kBN, int kMode, int kT, bool kUpdate, bool kSum>
+template <int kBN, int kMode, int kT, bool kUpdate>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
@@ -506,7 +540,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       for (int t = first; ok && t < a.items; t += pairs) {
         const uint32_t idesc = idesc_of | ((kBN == 128 || t < a.whole ? kBN / 8 : 128 / 8) << 17);
         for (int k0 = 0, k1; ok && k0 < blocks; k0 = k1, ++use) {
-          k1 = chunk_end<kSum>(a, k0);
+          k1 = chunk_end(a, k0);
           const int buf = use & 1;
           ok = mbar_wait(&s_acc_empty[buf], ((use >> 1) & 1) ^ 1, &s_fail);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -540,6 +574,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
     const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + own_col;
     int use = 0;
     uint32_t adds = 0;  // parity of the next tensor copy
+    const bool adds_some = kAdd && (kMode != kFinal || a.add_at);
     bool ok = true, writes = true;
     if constexpr (kMode == kFinal && kUpdate) writes = finite(f.grad_scale ? *f.grad_scale : 1.0f);
     const int blocks = a.passes * a.kblocks;
@@ -576,7 +611,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       // (what lies past the matrix is not there to copy or to store)
       const bool some = row0 < a.m && own_col < cols;
       const auto fetch = [&](int col) {
-        if (!kAdd || !some || col >= a.pitch) return;
+        if (!adds_some || !some || col >= a.pitch) return;
         wait_stored();
         if (lane == 0) {
           mbar_expect_tx(&s_add[w], 2 * kPlaneBytes);
@@ -585,44 +620,32 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         }
       };
       fetch(col0);
-      float sum[kSum ? kOwn : 1];
+      float sum[kOwn];
 #pragma unroll
-      for (int j = 0; j < (kSum ? kOwn : 1); ++j) sum[j] = 0.0f;
-      if constexpr (kSum) {
+      for (int j = 0; j < kOwn; ++j) sum[j] = 0.0f;
 #pragma unroll 1
-        for (int k0 = 0; k0 < blocks; k0 = chunk_end<kSum>(a, k0)) {
-          if (!wait_full()) break;
+      for (int k0 = 0; k0 < blocks; k0 = chunk_end(a, k0)) {
+        if (!wait_full()) break;
 #pragma unroll
-          for (int c = 0; c < kOwn; c += 16) {
-            float r[16];
-            tmem_load16(own + (use & 1) * 256 + c, r);
+        for (int c = 0; c < kOwn; c += 16) {
+          float r[16];
+          tmem_load16(own + (use & 1) * 256 + c, r);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], r[j]);
-          }
-          done();
+          for (int j = 0; j < 16; ++j) sum[c + j] = __fadd_rn(sum[c + j], r[j]);
         }
-      } else {
-        wait_full();
+        done();
       }
       if (!ok) break;
+      const float beta = beta_of<kMode>(a, tile.z), alpha = alpha_of<kMode>(a, tile.z, row);
 #pragma unroll
       for (int g = 0; g < kGroups; ++g) {
         const int col = col0 + 32 * g;
         if (g > 0) fetch(col);
         float v[32];
-        if constexpr (kSum) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = sum[32 * g + j];
-        } else {
-          uint32_t r[32];
-          tmem_load32(own + (use & 1) * 256 + 32 * g, r);
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          if (g == kGroups - 1) done();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-        }
+        for (int j = 0; j < 32; ++j) v[j] = sum[32 * g + j];
         if (!some || col >= a.pitch) continue;
-        if constexpr (kAdd) {
+        if (adds_some) {
           ok = __all_sync(0xffffffffu, mbar_wait(&s_add[w], adds, &s_fail));
           adds ^= 1u;
           if (!ok) break;
@@ -632,16 +655,16 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
         uint32_t h[16], l[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          uint4 ch, cl;
-          if constexpr (kAdd) {
+          uint4 ch{}, cl{};
+          if (adds_some) {
             ch = shared_load16(my_row + (swizzle ^ (q << 4)));
             cl = shared_load16(my_row + (swizzle ^ (q << 4)) + kPlaneBytes);
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             float& x = v[8 * q + j];
-            x = __fmul_rn(a.beta, x);
-            if constexpr (kAdd) x = __fmaf_rn(a.alpha, __fadd_rn(half_at(ch, j), half_at(cl, j)), x);
+            x = __fmul_rn(beta, x);
+            if constexpr (kAdd) x = __fmaf_rn(alpha, __fadd_rn(half_at(ch, j), half_at(cl, j)), x);
           }
           if constexpr (kMode != kFinal) {
 #pragma unroll
@@ -772,7 +795,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   const int kb0 = a.kblocks * static_cast<int>(rank) / call.split, count = a.kblocks * (static_cast<int>(rank) + 1) / call.split - kb0;
   const int least = (count + kSmallAccs - 1) / kSmallAccs, chunk = least > kChunk ? least : kChunk;
   const int accs = (count + chunk - 1) / chunk;
-  const bool pairs = a.passes == 3;
+  const bool p_low = a.passes >= 2, q_low = a.passes == 3;
   if (threadIdx.x == 0) {
     prefetch_map(&a.p);
     prefetch_map(&a.q);
@@ -810,10 +833,10 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
         const int k = (kb0 + i) * kBK;
         uint64_t* const bar = &s_full[ring.s];
         uint8_t* const p = sm + ring.s * kSmallStage;
-        mbar_expect_tx(bar, pairs ? kSmallStage : kSmallP + kSmallQ);
-        for (int h = 0; h < (pairs ? 2 : 1); ++h) {
+        mbar_expect_tx(bar, (p_low ? 2 : 1) * kSmallP + (q_low ? 2 : 1) * kSmallQ);
+        for (int h = 0; h < (p_low ? 2 : 1); ++h) {
           tma_load3_one(p + h * kSmallP, &a.p, k, tile.m0, 2 * tile.z + h, bar);
-          tma_load3_one(p + 2 * kSmallP + h * kSmallQ, &a.q, kTrans ? tile.n0 : k, kTrans ? k : tile.n0, 2 * tile.z + h, bar);
+          if (h == 0 || q_low) tma_load3_one(p + 2 * kSmallP + h * kSmallQ, &a.q, kTrans ? tile.n0 : k, kTrans ? k : tile.n0, 2 * tile.z + h, bar);
         }
       }
       __syncwarp();
@@ -836,10 +859,8 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
                          "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}"
                          ::"r"(acc), "l"(p + s * kStepP), "l"(q + s * kStepQ), "r"(idesc), "r"(static_cast<uint32_t>(!fresh || s != 0)) : "memory");
         };
-        if (pairs) {
-          issue(tmem, dp + kSmallP / 16, dq, i == 0);
-          issue(tmem, dp, dq + kSmallQ / 16, false);
-        }
+        if (p_low) issue(tmem, dp + kSmallP / 16, dq, i == 0);
+        if (q_low) issue(tmem, dp, dq + kSmallQ / 16, false);
         issue(tmem + kSmallCols * (1 + i / chunk), dp, dq, i % chunk == 0);
         commit_one(&s_empty[ring.s]);
       }
@@ -852,6 +873,10 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
     for (int i = 0; i < kMine; ++i) {
       const uint32_t u = 2 * i + half;
       if (!unit_in(u)) continue;
+      if (kMode == kFinal && !a.add_at) {
+        add[i] = Pair8{};
+        continue;
+      }
       const __half* const from = a.add_at + 2 * tile.z * plane + static_cast<int64_t>(r) * a.pitch + unit_col(u);
       add[i] = Pair8{__ldg(reinterpret_cast<const uint4*>(from)), __ldg(reinterpret_cast<const uint4*>(from + plane))};
     }
@@ -873,7 +898,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
       float sum[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
-      for (int i = pairs ? 0 : 1; i <= accs && count > 0; ++i) {
+      for (int i = p_low ? 0 : 1; i <= accs && count > 0; ++i) {
         float v[16];
         tmem_load16(from + i * kSmallCols, v);
 #pragma unroll
@@ -897,6 +922,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   if (warp >= 2 && ok) {
     bool writes = true;
     if constexpr (kMode == kFinal && kUpdate) writes = finite(f.grad_scale ? *f.grad_scale : 1.0f);
+    const float beta = beta_of<kMode>(a, tile.z), alpha = alpha_of<kMode>(a, tile.z, r);
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const uint32_t u = 2 * i + half;
@@ -915,8 +941,8 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[j] = __fmul_rn(a.beta, v[j]);
-        if constexpr (kAdd) v[j] = pad ? 0.0f : __fmaf_rn(a.alpha, __fadd_rn(half_at(add[i].h, j), half_at(add[i].l, j)), v[j]);
+        v[j] = __fmul_rn(beta, v[j]);
+        if constexpr (kAdd) v[j] = pad ? 0.0f : __fmaf_rn(alpha, __fadd_rn(half_at(add[i].h, j), half_at(add[i].l, j)), v[j]);
       }
       if constexpr (kMode != kFinal) {
         Pair8 o;
@@ -957,6 +983,29 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kSmallTmem));
 }
 
+// Diagonals of `all` rows: P = a I + B, or (with `out`) taken out of Q, which
+// has zeros there from then on.
+__global__ void __launch_bounds__(kThreads)
+ns_diagonal_kernel(__half* planes, int64_t m, int64_t pitch, int64_t all, float* out) {
+  wait_for_inputs();
+  let_next_begin();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= all) return;
+  __half* const high = planes + i / m * 2 * m * pitch + i % m * (pitch + 1);
+  __half* const low = high + m * pitch;
+  float x = __fadd_rn(__half2float(*high), __half2float(*low));
+  if (out) {
+    out[i] = x;
+    x = 0.0f;
+  } else {
+    x = __fmaf_rn(kA, kScale, x);
+  }
+  uint32_t h, l;
+  split2(x, 0.0f, h, l);
+  *high = __ushort_as_half(static_cast<unsigned short>(h & 0xffffu));
+  *low = __ushort_as_half(static_cast<unsigned short>(l & 0xffffu));
+}
+
 // --------------------------------------------------------------------------
 // host side
 
@@ -972,6 +1021,7 @@ struct Shape {
   int64_t m, n;
   int64_t x_bytes() const { return 4 * m * up(n, 64); }  // a pair of planes
   int64_t a_bytes() const { return 4 * m * up(m, 64); }
+  bool wide() const { return 4 * n >= 5 * m; }
   bool operator<(const Shape& o) const { return m != o.m ? m < o.m : n < o.n; }
 };
 Shape shape_of(int64_t rows, int64_t cols) { return rows > cols ? Shape{cols, rows} : Shape{rows, cols}; }
@@ -995,8 +1045,12 @@ struct Set {
   int64_t count() const { return g[groups - 1].first + g[groups - 1].count - g[0].first; }
   int64_t bytes() const {
     int64_t n = 0;
-    for (int i = 0; i < groups; ++i) n += 2 * up(g[i].s.x_bytes() * g[i].count, 256) + 2 * up(g[i].s.a_bytes() * g[i].count, 256);
-    return n + 8 * kSlots * count();
+    for (int i = 0; i < groups; ++i) {
+      const bool squares = !small && g[i].s.wide();
+      n += 2 * up(g[i].s.x_bytes() * g[i].count, 256) + (squares ? 4 : 2) * up(g[i].s.a_bytes() * g[i].count, 256) +
+           (squares ? up(4 * g[i].s.m * g[i].count, 256) : 0);
+    }
+    return n + 8 * kSlots * count() + up(4 * count(), 256);
   }
 };
 
@@ -1010,9 +1064,8 @@ struct DeviceState {
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
 
-// The products of a call whose results have type kT.
 template <int kBN, int kMode, int kT, bool kUpdate>
-constexpr auto kernel_of() { return ns_product_kernel<kBN, kMode, kMode == kFinal ? kT : kF32, kUpdate, kT == kF32>; }
+constexpr auto kernel_of() { return ns_product_kernel<kBN, kMode, kT, kUpdate>; }
 
 template <int kBN, int kMode, int kT, bool kUpdate>
 cudaError_t opt_in_one() { return opt_in(kernel_of<kBN, kMode, kT, kUpdate>(), ns_smem<kBN>()); }
@@ -1020,7 +1073,6 @@ cudaError_t opt_in_one() { return opt_in(kernel_of<kBN, kMode, kT, kUpdate>(), n
 template <int kBN>
 cudaError_t opt_in_all() {
   const cudaError_t e[] = {opt_in_one<kBN, kGram, kF32, false>(), opt_in_one<kBN, kPoly, kF32, false>(), opt_in_one<kBN, kApply, kF32, false>(),
-                           opt_in_one<kBN, kGram, kF16, false>(), opt_in_one<kBN, kPoly, kF16, false>(), opt_in_one<kBN, kApply, kF16, false>(),
                            opt_in_one<kBN, kFinal, kF32, false>(), opt_in_one<kBN, kFinal, kBF16, false>(), opt_in_one<kBN, kFinal, kF16, false>(),
                            opt_in_one<kBN, kFinal, kF32, true>(), opt_in_one<kBN, kFinal, kBF16, true>(), opt_in_one<kBN, kFinal, kF16, true>()};
   for (const cudaError_t x : e)
@@ -1066,7 +1118,7 @@ bwd_status ensure_device(DeviceState* out) {
     attr[0].val.clusterDim = {2, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of<256, kApply, kF16, false>(), &cfg);
+    e = cudaOccupancyMaxActiveClusters(&d.pairs, kernel_of<256, kApply, kF32, false>(), &cfg);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
     if (d.pairs < 1) return fail(BWD_ERR_CUDA, "no room for a CTA pair of the matrix product");
     // with so much shared memory that no SM takes two
@@ -1115,6 +1167,19 @@ struct Step {
   bwd_dtype g_type, out_type;
 };
 
+// How many of the last steps work on the squares (see the top), by what takes
+// fewer passes of the matrix instruction, at n = r m: without them 39 r + 13
+// times m m m for bf16 results and 45 r + 15 for others; five on squares 9 r +
+// 51 (5 r + 51 from exact planes), three 27 r + 33.  An error of A in a weak
+// direction is raised by 11.8 a step, so only bf16 results take five (in
+// simulation at most 4e-4 of the result, whatever the spectrum), and others
+// three where that adds nothing to what the other steps make of the same
+// error, n >= 2 m (1e-5 instead of 2e-6 for a square matrix).
+int squared_steps(const Shape& s, const Step& st) {
+  if (st.out_type == BWD_BF16) return s.wide() ? std::min(st.steps, 5) : 0;
+  return s.n >= 2 * s.m ? std::min(st.steps, 3) : 0;
+}
+
 template <int kBN, int kMode>
 bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& st, int pairs, cudaStream_t stream) {
   const dim3 grid(static_cast<unsigned>(2 * (a.items < pairs ? a.items : pairs)));
@@ -1122,7 +1187,7 @@ bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& 
     return launch_ex(kernel, grid, kMmThreads, 0, ns_smem<kBN>(), stream, "ns_product_kernel launch", a, last);
   };
   if constexpr (kMode != kFinal) {
-    return st.out_type == BWD_F32 ? go(kernel_of<kBN, kMode, kF32, false>(), 0) : go(kernel_of<kBN, kMode, kF16, false>(), 0);
+    return go(kernel_of<kBN, kMode, kF32, false>(), 0);
   } else if (st.update) {
     if (st.out_type == BWD_F32) return go(kernel_of<kBN, kMode, kF32, true>(), *f);
     return st.out_type == BWD_BF16 ? go(kernel_of<kBN, kMode, kBF16, true>(), *f) : go(kernel_of<kBN, kMode, kF16, true>(), *f);
@@ -1155,22 +1220,27 @@ struct Operation {
   int64_t k, count;
   const __half *p, *q, *add;
   __half* out;
+  const float *scale = nullptr, *diagonal = nullptr;
+};
+struct Factors {
+  int passes;
+  float alpha, beta;
 };
 
 // The kernels' arguments, for tiles of so many rows and columns, of which a
 // CTA copies lines_p of P's lines and lines_q of Q's.
 template <int kMode>
-bwd_status fill_args(ProductArgs& a, const Operation& o, int rows, int cols, int lines_p, int lines_q, int passes, float alpha, float beta) {
+bwd_status fill_args(ProductArgs& a, const Operation& o, int rows, int cols, int lines_p, int lines_q, const Factors& x) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
   a.add_at = o.add; a.out_at = o.out;
   a.m = static_cast<int>(o.result.m); a.n = static_cast<int>(o.result.n); a.pitch = static_cast<int>(up(o.result.n, 64));
   a.kblocks = static_cast<int>((o.k + kBK - 1) / kBK);
-  a.passes = passes;
+  a.passes = x.passes; a.scale = o.scale; a.diagonal = o.diagonal;
   a.tiles_m = static_cast<int>((o.result.m + rows - 1) / rows); a.tiles_n = static_cast<int>((o.result.n + cols - 1) / cols);
   const int64_t tiles = tiles_of(o.result, rows, cols, kSymmetric);
   if (tiles * o.count > 0x3fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
   a.tiles = static_cast<int>(tiles); a.items = a.whole = static_cast<int>(tiles * o.count);
-  a.alpha = alpha; a.beta = beta;
+  a.alpha = x.alpha; a.beta = x.beta;
   // P: lines along k; Q: its lines along k, or its rows along the result's columns
   const bwd_status s = plane_map(&a.p, o.p, o.result.m, up(o.k, 64), 2 * o.count, kBK, lines_p);
   if (s != BWD_OK) return s;
@@ -1189,13 +1259,13 @@ int small_split(int64_t tiles, int64_t kblocks, const DeviceState& d) {
 }
 
 template <int kMode>
-bwd_status products(const Operation* o, int groups, float alpha, float beta, int passes, const FinalArgs* f, const Step& st,
+bwd_status products(const Operation* o, int groups, const Factors& x, const FinalArgs* f, const Step& st,
                     const DeviceState& d, cudaStream_t stream) {
   static thread_local SmallCall c;
   c.groups = groups;
   int64_t tiles = 0, kblocks = 1;
   for (int i = 0; i < groups; ++i) {
-    const bwd_status s = fill_args<kMode>(c.g[i], o[i], kSmallRows, kSmallCols, kSmallRows, kSmallCols, passes, alpha, beta);
+    const bwd_status s = fill_args<kMode>(c.g[i], o[i], kSmallRows, kSmallCols, kSmallRows, kSmallCols, x);
     if (s != BWD_OK) return s;
     c.start[i] = static_cast<int>(tiles);
     tiles += c.g[i].items;
@@ -1207,7 +1277,7 @@ bwd_status products(const Operation* o, int groups, float alpha, float beta, int
 
 // One group's product, by whichever kernel takes less time.
 template <int kMode>
-bwd_status product(const Operation& o, float alpha, float beta, int passes, const FinalArgs* f, const Step& st, const DeviceState& d,
+bwd_status product(const Operation& o, const Factors& x, const FinalArgs* f, const Step& st, const DeviceState& d,
                    cudaStream_t stream) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly;
   // (the last wave of 256 columns counts half where its tiles are cut into halves)
@@ -1226,15 +1296,15 @@ bwd_status product(const Operation& o, float alpha, float beta, int passes, cons
   // small tiles, 600 us against 342 the other way.)
   const int64_t at_once = d.clusters[split] * split, small_waves = (small * split + at_once - 1) / at_once;
   const double full = std::min(1.0, static_cast<double>(small * split) / static_cast<double>(at_once));
-  const double stage = (0.2 + 0.3 * full) * (passes == 3 ? 1.0 : 0.5);
+  const double stage = (0.2 + 0.3 * full) * (x.passes > 1 ? 1.0 : 0.5);
   const double small_time = static_cast<double>(small_waves) * (5.0 + stage * static_cast<double>((kblocks + split - 1) / split));
-  const double large_time = 8.0 + std::min(0.24 * waves128, 0.36 * waves256) * static_cast<double>(passes * kblocks);
-  if (small_time < large_time) return products<kMode>(&o, 1, alpha, beta, passes, f, st, d, stream);
+  const double large_time = 8.0 + std::min(0.24 * waves128, 0.36 * waves256) * static_cast<double>(x.passes * kblocks);
+  if (small_time < large_time) return products<kMode>(&o, 1, x, f, st, d, stream);
   // (eight matrices of 1024 x 4096, A: 133 us with 128 columns, three waves, and 120 with 256, one and a half)
   const int bn = 0.36 * waves256 < 0.24 * waves128 ? 256 : 128;
   ProductArgs a{};
   // of a pair's tile each CTA copies half of either operand's lines
-  bwd_status s = fill_args<kMode>(a, o, kBM, bn, kBM / 2, bn / 2, passes, alpha, beta);
+  bwd_status s = fill_args<kMode>(a, o, kBM, bn, kBM / 2, bn / 2, x);
   if (s == BWD_OK && o.add) s = plane_map(&a.add, o.add, o.result.m, a.pitch, 2 * o.count, 32, 32);
   if (s == BWD_OK && o.out) s = plane_map(&a.out, o.out, o.result.m, a.pitch, 2 * o.count, 32, 32);
   if (s != BWD_OK) return s;
@@ -1266,15 +1336,21 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
   f.decay = st.decay;
   Pieces pieces{work};
   a.slots = reinterpret_cast<double*>(pieces.take(8 * kSlots * set.count()));
+  const int squares = set.small ? 0 : squared_steps(set.g[0].s, st);
+  float* const scale = reinterpret_cast<float*>(pieces.take(4 * set.count()));
+  float* const diagonal = reinterpret_cast<float*>(pieces.take(squares > 0 ? 4 * set.g[0].s.m * set.count() : 0));
+  a.scale = squares > 0 && squares == st.steps && !st.has_momentum && st.g_type == BWD_BF16 ? scale : nullptr;
   struct Planes {
-    __half *x[2], *gram, *poly;
+    __half *x[2], *a, *p, *q[2];
   } planes[kGroups];
   int64_t norm_ctas = 0, split_ctas = 0;
   for (int i = 0; i < set.groups; ++i) {
     const Group& g = set.g[i];
     const Shape& s = g.s;
     for (__half** at : {&planes[i].x[0], &planes[i].x[1]}) *at = reinterpret_cast<__half*>(pieces.take(s.x_bytes() * g.count));
-    for (__half** at : {&planes[i].gram, &planes[i].poly}) *at = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * g.count));
+    for (__half** at : {&planes[i].a, &planes[i].p}) *at = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * g.count));
+    if (squares > 0)
+      for (__half*& at : planes[i].q) at = reinterpret_cast<__half*>(pieces.take(s.a_bytes() * g.count));
     PrepareGroup& p = a.g[i];
     p.planes = planes[i].x[0];
     p.size = s.m * s.n;
@@ -1292,7 +1368,17 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
   if (split_ctas > 0x7fffffff) return fail(BWD_ERR_INVALID_ARG, "too many tiles");
   bwd_status e = st.has_momentum ? prepare<true>(a, static_cast<int>(norm_ctas), static_cast<int>(split_ctas), st.g_type, stream)
                                  : prepare<false>(a, static_cast<int>(norm_ctas), static_cast<int>(split_ctas), st.g_type, stream);
-  for (int i = 0; e == BWD_OK && i < st.steps; ++i) {
+  const auto run = [&](auto mode, const Operation* o, const Factors& x) {
+    constexpr int kMode = decltype(mode)::value;
+    if (e != BWD_OK) return;
+    e = set.small ? products<kMode>(o, set.groups, x, &f, st, d, stream) : product<kMode>(o[0], x, &f, st, d, stream);
+  };
+  constexpr std::integral_constant<int, kGram> to_square{};  // a symmetric product, of A or of two that commute
+  constexpr std::integral_constant<int, kPoly> to_poly{};
+  constexpr std::integral_constant<int, kApply> to_x{};
+  constexpr std::integral_constant<int, kFinal> to_result{};
+  const int before = st.steps - squares;
+  for (int i = 0; i < before; ++i) {
     const bool last = i + 1 == st.steps;
     const int passes = last && st.out_type == BWD_BF16 ? 1 : 3;
     Operation gram[kGroups], poly[kGroups], apply[kGroups];
@@ -1301,21 +1387,59 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
       const Shape square{s.m, s.m};
       const Planes& p = planes[j];
       const __half* const from = p.x[i % 2];
-      gram[j] = Operation{square, s.n, set.g[j].count, from, from, nullptr, p.gram};
-      poly[j] = Operation{square, s.m, set.g[j].count, p.gram, p.gram, p.gram, p.poly};
-      apply[j] = Operation{s, s.m, set.g[j].count, p.poly, from, from, last ? nullptr : p.x[(i + 1) % 2]};
+      gram[j] = Operation{square, s.n, set.g[j].count, from, from, nullptr, p.a};
+      poly[j] = Operation{square, s.m, set.g[j].count, p.a, p.a, p.a, p.p};
+      apply[j] = Operation{s, s.m, set.g[j].count, p.p, from, from, last ? nullptr : p.x[(i + 1) % 2]};
     }
-    const auto run = [&](auto mode, const Operation* o, float alpha, float beta) {
-      constexpr int kMode = decltype(mode)::value;
-      if (e != BWD_OK) return;
-      e = set.small ? products<kMode>(o, set.groups, alpha, beta, passes, &f, st, d, stream)
-                    : product<kMode>(o[0], alpha, beta, passes, &f, st, d, stream);
-    };
-    run(std::integral_constant<int, kGram>{}, gram, 0.0f, 1.0f / kScale);
-    run(std::integral_constant<int, kPoly>{}, poly, kB, kC / kScale);
-    if (last) run(std::integral_constant<int, kFinal>{}, apply, kA / kScale, 1.0f / (kScale * kScale));
-    else run(std::integral_constant<int, kApply>{}, apply, kA, 1.0f / kScale);
+    run(to_square, gram, Factors{passes, 0.0f, 1.0f / kScale});
+    run(to_poly, poly, Factors{passes, kB, kC / kScale});
+    if (last) run(to_result, apply, Factors{passes, kA / kScale, 1.0f / (kScale * kScale)});
+    else run(to_x, apply, Factors{passes, kA, 1.0f / kScale});
   }
+  if (squares == 0) return e;
+  const Group& g = set.g[0];
+  const Shape square{g.s.m, g.s.m};
+  const __half* const from = planes[0].x[before % 2];
+  __half *const at_a = planes[0].a, *const at_p = planes[0].p, *q = planes[0].q[0], *c = planes[0].q[1];
+  const auto diagonals = [&](float* out) {
+    const int64_t all = g.count * g.s.m;
+    if (e == BWD_OK)
+      e = launch_ex(ns_diagonal_kernel, dim3(static_cast<unsigned>((all + kThreads - 1) / kThreads)), kThreads, 0, 0, stream,
+                    "ns_diagonal_kernel launch", q, g.s.m, up(g.s.m, 64), all, out);
+  };
+  // a Y + B Y, which is P Y
+  const auto times = [&](const __half* b, const __half* y, __half* out, float factor) {
+    const Operation o{square, g.s.m, g.count, b, y, y, out};
+    run(to_poly, &o, Factors{3, kA * factor, factor / kScale});
+  };
+  const Operation gram{square, g.s.n, g.count, from, from, nullptr, at_a, a.scale};
+  run(to_square, &gram, Factors{a.scale ? 1 : 3, 0.0f, 1.0f / kScale});
+  float level = 1.0f;  // Q is stored divided by this
+  for (int i = 0; i < squares; ++i) {
+    const bool last = i + 1 == squares;
+    __half* const b = i == 0 ? q : at_p;
+    const Operation poly{square, g.s.m, g.count, at_a, at_a, at_a, b};
+    run(to_poly, &poly, Factors{3, kB, kC / kScale});
+    if (i > 0) {
+      times(b, q, c, 0.25f);
+      std::swap(q, c);
+      level *= 4.0f;
+    }
+    if (!last) {
+      times(b, at_a, c, 1.0f);
+      times(b, c, at_a, 1.0f);
+    }
+    if (i == 0) diagonals(nullptr);  // the first P is Q
+  }
+  Operation last{g.s, g.s.m, g.count, q, from, nullptr, nullptr, a.scale};
+  if (st.out_type != BWD_BF16) {
+    // Q's diagonal outweighs its rows; in the sums each addition would be cut
+    // off at its 24th bit (1024 x 4096: 4e-7 of the result)
+    diagonals(diagonal);
+    last.add = from;
+    last.diagonal = diagonal;
+  }
+  run(to_result, &last, Factors{a.scale ? 2 : 3, 0.0f, level / (kScale * kScale)});
   return e;
 }
 

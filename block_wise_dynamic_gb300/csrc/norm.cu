@@ -383,7 +383,8 @@ __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 template <int kT, bool kPieces, int kValues>
 struct Columns {
   static constexpr int kPairs = kValues / 2;
-  [[maybe_unused]] static constexpr int kUnitPairs = kPieces ? 8 / elem_bytes<kT>() : kPairs;  // of a unit
+  static constexpr int kUnitPairs = kPieces ? 8 / elem_bytes<kT>() : kPairs;  // of a unit
+  static_assert(kPairs % kUnitPairs == 0, "a thread holds whole units");
   int t, threads, width;
   __device__ __forceinline__ int first(int e) const {
     if constexpr (kPieces) return ((e / kUnitPairs * threads + t) * kUnitPairs + e % kUnitPairs) * 2;

@@ -364,3 +364,139 @@ def test_fifty_thousand_columns(muon):
     check(muon.orthogonalize(g), g)
     g = draw(40001, 5, 2)
     check(muon.orthogonalize(g), g)
+
+
+def squares_bound(g, steps, squares):
+    """As error_bound, for a result whose last `squares` steps stay among m x m matrices (m rows of the wide form).
+
+    P = a I + B, Q = P Q, A' = P A P, all of them polynomials of A.  An operand
+    is off by d of its value; sums of 128 products leave the accumulator and
+    are added up in fp32, so that a product is off by e = 2.02 d + 128 2e-10 +
+    2^-24 (n / 128 + 4) of the sum of its terms' magnitudes.  With Frobenius
+    norms F = |X|, |A| and |B| <= 4.8 |A|, and spectral norms of at most 1.47 of
+    A, 3.45 of P and 1.5 of P A, what one step adds:
+      the first A    e F^2 + d |A|
+      B              t = 2.04 e |A|^2 + d |B|, and on the first P's diagonal 3.45 d
+      P A            e |B| |A| + 1.5 d |A|, times |P|
+      P (P A)        1.5 e |B| |A| + d |A'|
+      both times B   3 t, and 3 3.45 d |A| for the first
+    these last three times 2^1/2, as one half is the other's mirror image.  An
+    error of A grows by 11.9 a step, the largest slope of s (a + b s + c s^2)^2.
+    What moves X: P_k's error, 4.8 times A_k's and t, times |X_k| <= 1.21; Q's
+    rounding and product, (d |Q| + e 3.45^k |B|) times X's spectral norm with
+    |Q| <= 3.45^(k+1) m^1/2; each raised by 3.45 a step that follows; and Q X,
+    e |Q| F.  X's own error before them is stretched by 4.3 a step.  Stored
+    values (times 2^14, Q's divided by 4^k) are off by 2^-39 besides.  All to
+    first order: a twentieth on top."""
+    xs = ref.iterates(np64(g), steps)
+    m, n = xs[0].shape
+    start, least = steps - squares, 2.0 ** -39
+    d = 2.0 ** -22 + 2.0 ** -30
+    e = 2.02 * d + 2e-10 * 128 + 2.0 ** -24 * (n / 128 + 4)
+    total = 2.0 ** -20 * np.linalg.norm(xs[0]) + least * (m * n) ** 0.5
+    for x in xs[:start]:
+        f = np.linalg.norm(x)
+        total = 4.3 * total + 27 * e * f * f + 29 * d * f + 17.5 * least * (m * n) ** 0.5
+    total *= 4.3 ** squares
+    x0, f = np.linalg.norm(xs[start], 2), np.linalg.norm(xs[start])
+    grams = [np.linalg.norm(x @ x.T) for x in xs[start:]]
+    off = e * f * f + d * grams[0] + least * m
+    for k in range(squares):
+        a, b, first = grams[k], 4.8 * grams[k], 3.45 * d * (k == 0)
+        t = 2.04 * e * a * a + d * b + least * m
+        here = 1.21 * (4.8 * off + t + first * m ** 0.5)
+        here += x0 * (3.45 ** (k + 1) * d * m ** 0.5 + 3.45 ** k * e * b + 4 ** k * least * m)
+        total += 3.45 ** (squares - 1 - k) * here
+        step = 3.45 * (e * b * a + 1.5 * d * a) + 1.5 * e * b * a + d * grams[k + 1] + 3 * (t + first * a) + 5 * least * m
+        off = 11.9 * off + 2 ** 0.5 * step
+    return 1.05 * (total + e * 3.45 ** squares * m ** 0.5 * f)
+
+
+def check_wide(out, g, steps=5):
+    """g: so many columns (or rows) that the last five steps (bf16) or three stay among the squares."""
+    want = ref.orthogonalize(np64(g), steps)
+    off = np.linalg.norm(np64(out) - want)
+    bound = squares_bound(g, steps, min(steps, 5 if g.dtype == torch.bfloat16 else 3))
+    bound += ROUND[g.dtype] * (np.linalg.norm(want) + bound) + TINY[g.dtype] * want.size ** 0.5
+    assert out.shape == g.shape and out.dtype == g.dtype and off <= bound, (off, bound)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("shape", [(1000, 2100), (2303, 1001), (130, 30000)])
+def test_wide(muon, shape, dtype):
+    for kind in ("gauss", "strong"):
+        g = draw(*shape, 21, kind, TYPES[dtype])
+        before = g.clone()
+        out = muon.orthogonalize(g)
+        check_wide(out, g)
+        assert torch.equal(g, before)
+        # what the two forms of the steps are said to leave, whatever the spectrum
+        want = ref.orthogonalize(np64(g))
+        most = {"fp32": 1e-4, "bf16": 2.0 ** -8 + 1e-3, "fp16": 2.0 ** -11 + 1e-4}[dtype]
+        assert np.linalg.norm(np64(out) - want) < most * np.linalg.norm(want)
+
+
+def test_a_little_wide(muon):
+    """bf16 results take the squares from 1.25 columns to a row on."""
+    check_wide(muon.orthogonalize(g := draw(1320, 1650, 22, "strong", torch.bfloat16)), g)
+    check(muon.orthogonalize(g := draw(1320, 1649, 22, "strong", torch.bfloat16)), g)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 9])
+def test_wide_batches(muon, steps, dtype):
+    g = torch.stack([draw(300, 700, 30 + i, "strong" if i % 2 else "gauss", TYPES[dtype]) for i in range(9)])
+    out = muon.orthogonalize(g, steps)
+    for i in (0, 1, 8):
+        check_wide(out[i], g[i], steps)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_special_wide_matrices(muon, dtype):
+    kind = TYPES[dtype]
+    g = torch.stack([draw(300, 700, 40 + i) for i in range(9)])
+    g[4] *= {"fp32": 1e30, "bf16": 1e37, "fp16": 1e6}[dtype]
+    g[5] *= {"fp32": 1e-20, "bf16": 1e-1, "fp16": 1e-1}[dtype]
+    g = g.to(kind)
+    want = muon.orthogonalize(g)
+    g[1] = 0
+    g[2, 3, 4] = float("nan")
+    g[3, 0, 0] = float("inf")
+    out = muon.orthogonalize(g)
+    for i in (0, 4, 5, 6, 7, 8):
+        assert torch.equal(out[i], want[i])
+    assert not out[1].any() and out[2].isnan().all() and out[3].isnan().all()
+    for i in (4, 5):
+        check_wide(out[i], g[i])
+
+
+@pytest.mark.parametrize("p_type,g_type", [("fp32", "fp32"), ("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp16")])
+def test_wide_step(muon, p_type, g_type):
+    """Without momentum and from zeros a step leaves -lr rms n^1/2 times the orthogonalised gradient."""
+    gs = [draw(*((300, 700) if i % 2 else (700, 300)), 50 + i, "strong", TYPES[g_type]) for i in range(10)]
+    ps = [torch.zeros(g.shape, dtype=TYPES[p_type], device=DEV) for g in gs]
+    ms = [torch.zeros(g.shape, device=DEV) for g in gs]
+    args = muon.MuonArgs(ps, gs, ms)
+    args.step(lr=0.5, momentum=0.0, nesterov=False, weight_decay=0.0, rms=0.25)
+    factor = 0.125 * 700 ** 0.5
+    for p, g, m in zip(ps, gs, ms):
+        assert torch.equal(m, g.float())
+        want = ref.orthogonalize(np64(g))
+        off = np.linalg.norm(np64(p) / -factor - want)
+        bound = squares_bound(g, 5, 5 if p_type == "bf16" else 3)
+        bound += (ROUND[TYPES[p_type]] + 4 * U) * (np.linalg.norm(want) + bound) + TINY[TYPES[p_type]] / factor * want.size ** 0.5
+        assert off <= bound, (off, bound)
+
+
+def test_a_wide_graph_replays(muon):
+    """The planes' factors and Q's diagonal are formed anew by each replay."""
+    for dtype in (torch.bfloat16, torch.float32):
+        g = draw(1001, 2303, 60, "strong", dtype)
+        muon.orthogonalize(g)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = muon.orthogonalize(g)
+        for seed, factor in ((61, 1.0), (62, 1e-3), (63, 40.0)):
+            g.copy_((draw(1001, 2303, seed, "strong") * factor).to(dtype))
+            graph.replay()
+            assert torch.equal(out, muon.orthogonalize(g))
