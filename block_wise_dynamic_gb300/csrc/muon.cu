@@ -428,7 +428,7 @@ __device__ __forceinline__ float half_at(const uint4& w, int j) {
 // kChunk stages of high x high, 128 products, and are added up in registers,
 // rounded to nearest; what low parts add is 2^-11 of that and stays for all of
 // their products.  (1000 x 1000, fp32: error 1.6e-6, 2.5e-6 with 256 products;
-// 96 x 1024 x 1024 and 48 x 1024 x 4096 9.13 ms, 8.98 with 256.)
+// 24 matrices of 1024 x 1024 and 48 of 1024 x 4096 9.13 ms, 8.98 with 256.)
 constexpr int kChunk = 2;
 
 // Stages of a tile whose sums leave the accumulator together, from stage k on.
