@@ -1048,9 +1048,9 @@ struct Set {
     for (int i = 0; i < groups; ++i) {
       const bool squares = !small && g[i].s.wide();
       n += 2 * up(g[i].s.x_bytes() * g[i].count, 256) + (squares ? 4 : 2) * up(g[i].s.a_bytes() * g[i].count, 256) +
-           (squares ? up(4 * g[i].s.m * g[i].count, 256) : 0);
+           (squares ? up(4 * g[i].s.m * g[i].count, 256) + up(4 * g[i].count, 256) : 0);
     }
-    return n + 8 * kSlots * count() + up(4 * count(), 256);
+    return n + 8 * kSlots * count();
   }
 };
 
@@ -1337,7 +1337,7 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
   Pieces pieces{work};
   a.slots = reinterpret_cast<double*>(pieces.take(8 * kSlots * set.count()));
   const int squares = set.small ? 0 : squared_steps(set.g[0].s, st);
-  float* const scale = reinterpret_cast<float*>(pieces.take(4 * set.count()));
+  float* const scale = reinterpret_cast<float*>(pieces.take(squares > 0 ? 4 * set.count() : 0));
   float* const diagonal = reinterpret_cast<float*>(pieces.take(squares > 0 ? 4 * set.g[0].s.m * set.count() : 0));
   a.scale = squares > 0 && squares == st.steps && !st.has_momentum && st.g_type == BWD_BF16 ? scale : nullptr;
   struct Planes {

@@ -68,8 +68,8 @@ def test_work_bytes(abi):
     assert size(2, i64(100, 10), i64(300, 10)) == one + 4 * 2560 + 8 * 512
     large = size(1, i64(3000), i64(4000))
     assert size(2, i64(3000, 2000), i64(4000, 3000)) == large == size(3, i64(3000, 100, 2000), i64(4000, 300, 3000))
-    # more than a launch takes, in equal parts
-    assert size(65, i64(*[100] * 65), i64(*[300] * 65)) == 33 * one
+    # more than a launch takes, in equal parts, with two more pairs of squares, their diagonals and the planes' factors
+    assert size(65, i64(*[100] * 65), i64(*[300] * 65)) == 33 * (one + 2 * 4 * 100 * 128) + 13312 + 256
 
 
 def test_python_refuses():
