@@ -184,7 +184,8 @@ class Muon(torch.optim.Optimizer):
             args = MuonArgs(ps, self._matrices(grads, idx), [self.state[params[i]]["momentum_buffer"] for i in idx], self._work.get(device))
             self._work[device] = args.work
             plan.append((idx, args))
-        return {"params": list(params), "has_grad": [g is not None for g in grads], "buckets": plan}
+        return {"params": list(params), "has_grad": [g is not None for g in grads], "at": [p.data_ptr() for p in params],
+                "buckets": plan}
 
     @staticmethod
     def _matrices(grads, idx):
@@ -204,7 +205,7 @@ class Muon(torch.optim.Optimizer):
             grads = [p.grad for p in params]
             plan = self._args_cache.get(gi)
             fresh = (plan is None or len(plan["params"]) != len(params) or not all(a is b for a, b in zip(plan["params"], params))
-                     or plan["has_grad"] != [g is not None for g in grads])
+                     or plan["has_grad"] != [g is not None for g in grads] or plan["at"] != [p.data_ptr() for p in params])
             if fresh:
                 plan = self._args_cache[gi] = self._plan(params, grads)
             for idx, args in plan["buckets"]:

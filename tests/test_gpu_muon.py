@@ -500,3 +500,21 @@ def test_a_wide_graph_replays(muon):
             g.copy_((draw(1001, 2303, seed, "strong") * factor).to(dtype))
             graph.replay()
             assert torch.equal(out, muon.orthogonalize(g))
+
+
+def test_parameters_that_move(muon):
+    """A parameter whose storage is replaced between steps is updated where it lies then."""
+    g = draw(64, 100, 70)
+    a, b = (torch.nn.Parameter(draw(64, 100, 71)) for _ in range(2))
+    one, two = muon.Muon([a], lr=0.1), muon.Muon([b], lr=0.1)
+    for step in range(3):
+        a.grad, b.grad = g * (step + 1), g * (step + 1)
+        one.step()
+        two.step()
+        old = a.data
+        kept = old.clone()
+        a.data = old.clone()
+        a.grad = b.grad = g
+        one.step()
+        two.step()
+        assert torch.equal(old, kept) and torch.equal(a, b)
