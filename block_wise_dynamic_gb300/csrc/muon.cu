@@ -608,8 +608,9 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
       int cols;
       const Tile tile = item_of<kBN, kSymmetric>(a, t, &cols);
       const int row0 = tile.m0 + static_cast<int>(rank) * (kBM / 2) + quarter * 32, row = row0 + lane, col0 = tile.n0 + own_col;
-      // (what lies past the matrix is not there to copy or to store)
-      const bool some = row0 < a.m && own_col < cols;
+      // (what lies past the matrix is not there to copy or to store, but for a
+      // mirrored tile's rows up to the pitch: their zeros are the pad's columns)
+      const bool some = row0 < (kSymmetric && tile.mirror ? a.pitch : a.m) && own_col < cols;
       const auto fetch = [&](int col) {
         if (!adds_some || !some || col >= a.pitch) return;
         wait_stored();
@@ -674,7 +675,7 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
           }
         }
         if constexpr (kMode != kFinal) {
-          store_planes(col, row0, tile.z);
+          if (row0 < a.m) store_planes(col, row0, tile.z);
           // Columns left of the diagonal's tiles are all rows of the matrix.
           if (kSymmetric && tile.mirror) {
             wait_stored();

@@ -518,3 +518,22 @@ def test_parameters_that_move(muon):
         one.step()
         two.step()
         assert torch.equal(old, kept) and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_whatever_the_workspace_held(muon, dtype):
+    """Sides that end 1 to 64 short of a stage of 64, with every bit of the workspace set before (NaNs in all of its types)."""
+    for count, shape in ((1, (910, 993)), (3, (1050, 1060)), (8, (290, 700)), (1, (961, 2500)), (2, (520, 1300)), (3, (40, 70)), (2, (289, 300))):
+        gs = [draw(*shape, 80 + i, "strong", TYPES[dtype]) for i in range(count)]
+        want = muon.orthogonalize(torch.stack(gs))
+        ps = [torch.zeros(shape, dtype=TYPES[dtype], device=DEV) for _ in gs]
+        ms = [torch.zeros(shape, device=DEV) for _ in gs]
+        args = muon.MuonArgs(ps, gs, ms)
+        args.work.fill_(255)
+        args.step(lr=1.0, momentum=0.0, nesterov=False, rms=0.125)
+        factor = 0.125 * max(shape) ** 0.5
+        for p, o in zip(ps, want):
+            assert p.isfinite().all()
+            # two roundings and two ways to the same result
+            off = np.linalg.norm(np64(p) / -factor - np64(o))
+            assert off <= (2 * ROUND[TYPES[dtype]] + 1e-3 * (dtype == "bf16") + 2e-4) * np.linalg.norm(np64(o))
