@@ -338,8 +338,9 @@ norm_backward_kernel(const BackwardArgs a) {
 //
 // A CTA takes kR rows at a time: what a row costs beside its bytes is the
 // latency of its sums over the CTA, which kR rows share.  Rows come into
-// shared memory by bulk copies, up to three sets of kR ahead, and are read by
-// each pass over them from there; the registers hold gamma, beta and the columns' sums.
+// shared memory by bulk copies, up to three sets of kR ahead.  Each pass reads
+// them from there, or (forward, up to 8192 columns in whole pieces) the first
+// one alone; the registers hold gamma, beta and the columns' sums.
 // (16384 x 4096 bf16, forward and backward, with a row at a time in registers:
 // 58 and 97 us; from shared memory, a row at a time, 56 and 100, and these sets
 // with one operation to an instruction 58 and 89, bound by instructions.)
@@ -590,6 +591,7 @@ template <int kT, bool kPieces, int kValues, int kMax, int kR>
 __global__ void __launch_bounds__(kMax)
 norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
   constexpr int kPairs = kValues / 2;
+  constexpr bool kKeep = kPieces && kValues == kFew;
   extern __shared__ __align__(128) uint8_t s_rows[];
   __shared__ __align__(8) uint64_t s_bars[kMaxSets];
   __shared__ __align__(16) float s_red[2][32][kR];
@@ -616,38 +618,99 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
   for (; row < a.rows; row += step) {
     ring.wait(&s_fail);
     float mean[kR], s[kR];
+    if constexpr (kKeep) {
+      // A row's values stay in registers, widened once.  (16384 x 4096 bf16 44.7
+      // us, 49.4 with four rows read anew and widened by each pass, 56 with one
+      // row in registers; 8192 x 8192 bf16 50.3 and 60.1; 16384 x 768 fp32 15.9
+      // and 23.9.  The backward pass, which would hold twice as much, gains
+      // nothing: 75.8 and 75.1.)
+      constexpr int kUnitPairs = Columns<kT, kPieces, kValues>::kUnitPairs;
+      float2 v[kR][kPairs];
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      float2 sum = both(0.0f);
-      cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool, const float2 (&v)[1]) { return sum = add2(sum, v[0]); });
-      s[r] = __fadd_rn(sum.x, sum.y);
-    }
-    cta_sum<kR>(s, s_red, turn);
-    ring.refill(row, step);
+      for (int r = 0; r < kR; ++r) {
+        float2 sum = both(0.0f);
 #pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      mean[r] = __fmul_rn(s[r], inv_width);
-      const float2 less = both(-mean[r]);
-      float2 sum = both(0.0f);
-      cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool there, const float2 (&v)[1]) {
-        float2 d = add2(v[0], less);
-        if (!there) d.y = 0.0f;
-        return sum = fma2(d, d, sum);
-      });
-      s[r] = __fadd_rn(sum.x, sum.y);
-    }
-    cta_sum<kR>(s, s_red, turn);
-#pragma unroll
-    for (int r = 0; r < kR; ++r) {
-      if (row + r >= a.rows) break;
-      const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
-      if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row + r] = mean[r];
-        if (a.rstd) a.rstd[row + r] = rstd;
+        for (int e = 0; e < kPairs; ++e) v[r][e] = both(0.0f);
+        cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int e, bool, const float2 (&x)[1]) {
+          v[r][e] = x[0];
+          return sum = add2(sum, x[0]);
+        });
+        s[r] = __fadd_rn(sum.x, sum.y);
       }
-      const float2 less = both(-mean[r]), scale = both(rstd);
-      cols.template over<true, 1>(static_cast<char*>(a.y) + (row + r) * row_bytes, {ring.row(r, 0, row + r)},
-                                  [&](int e, bool, const float2 (&v)[1]) { return fma2(mul2(add2(v[0], less), scale), g[e], b[e]); });
+      cta_sum<kR>(s, s_red, turn);
+      ring.refill(row, step);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        mean[r] = __fmul_rn(s[r], inv_width);
+        const float2 less = both(-mean[r]);
+        float2 sum = both(0.0f);
+#pragma unroll
+        for (int e = 0; e < kPairs; ++e) {
+          if (cols.first(e) < a.width) {
+            v[r][e] = add2(v[r][e], less);
+            sum = fma2(v[r][e], v[r][e], sum);
+          }
+        }
+        s[r] = __fadd_rn(sum.x, sum.y);
+      }
+      cta_sum<kR>(s, s_red, turn);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (row + r >= a.rows) break;
+        const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
+        if (threadIdx.x == 0) {
+          if (a.mean) a.mean[row + r] = mean[r];
+          if (a.rstd) a.rstd[row + r] = rstd;
+        }
+        const float2 scale = both(rstd);
+        char* const y = static_cast<char*>(a.y) + (row + r) * row_bytes;
+#pragma unroll
+        for (int u = 0; u < kPairs; u += kUnitPairs) {
+          if (cols.first(u) >= a.width) continue;
+          float o[2 * kUnitPairs];
+#pragma unroll
+          for (int k = 0; k < kUnitPairs; ++k) {
+            const float2 z = fma2(mul2(v[r][u + k], scale), g[u + k], b[u + k]);
+            o[2 * k] = z.x;
+            o[2 * k + 1] = z.y;
+          }
+          store_unit<kT, 2 * kUnitPairs>(y, cols.first(u), o);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        float2 sum = both(0.0f);
+        cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool, const float2 (&v)[1]) { return sum = add2(sum, v[0]); });
+        s[r] = __fadd_rn(sum.x, sum.y);
+      }
+      cta_sum<kR>(s, s_red, turn);
+      ring.refill(row, step);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        mean[r] = __fmul_rn(s[r], inv_width);
+        const float2 less = both(-mean[r]);
+        float2 sum = both(0.0f);
+        cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool there, const float2 (&v)[1]) {
+          float2 d = add2(v[0], less);
+          if (!there) d.y = 0.0f;
+          return sum = fma2(d, d, sum);
+        });
+        s[r] = __fadd_rn(sum.x, sum.y);
+      }
+      cta_sum<kR>(s, s_red, turn);
+#pragma unroll
+      for (int r = 0; r < kR; ++r) {
+        if (row + r >= a.rows) break;
+        const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
+        if (threadIdx.x == 0) {
+          if (a.mean) a.mean[row + r] = mean[r];
+          if (a.rstd) a.rstd[row + r] = rstd;
+        }
+        const float2 less = both(-mean[r]), scale = both(rstd);
+        cols.template over<true, 1>(static_cast<char*>(a.y) + (row + r) * row_bytes, {ring.row(r, 0, row + r)},
+                                    [&](int e, bool, const float2 (&v)[1]) { return fma2(mul2(add2(v[0], less), scale), g[e], b[e]); });
+      }
     }
     ring.next();
   }
@@ -797,10 +860,10 @@ int values_of(int width) { return width <= kMaxThreads * kFew ? kFew : kMany; }
 int threads_of(int width) { return (width + 32 * values_of(width) - 1) / (32 * values_of(width)) * 32; }
 
 // CTAs to an SM, by the registers that a thread takes: in the forward pass some
-// 75 for four rows of pieces and 64 for one row without, in the backward pass up
+// 100 for two rows of pieces and 64 for one row without, in the backward pass up
 // to 128, and more of rows with many values.
 int per_sm(int width, int threads) { return std::max(1, std::min((values_of(width) == kFew ? threads : 384) / threads_of(width), 16)); }
-int forward_per_sm(int width, bool pieces) { return per_sm(width, pieces ? 768 : 1024); }
+int forward_per_sm(int width, bool pieces) { return per_sm(width, pieces ? 512 : 1024); }
 int backward_per_sm(int width) { return per_sm(width, 512); }
 
 // CTAs of the backward pass, and so rows of its workspace, at most: as many as
@@ -881,14 +944,14 @@ bwd_status launch_forward(const ForwardArgs& a, int sms, cudaStream_t st) {
     return plain(norm_forward_kernel<kT, kVals, kFew, true>, std::min<int64_t>((a.rows + kWarps - 1) / kWarps, 3 * sms), 32 * kWarps);
   const int threads = threads_of(a.width), per = forward_per_sm(a.width, kPieces);
   const int64_t ctas = std::min<int64_t>(a.rows, static_cast<int64_t>(sms) * per), slot = slot_of(a.width * elem_bytes<kT>(), kPieces);
-  const int r = rows_at_a_time(slot, per, a.rows / ctas, !kPieces ? 1 : values_of(a.width) == kFew ? 4 : 2);
+  const int r = rows_at_a_time(slot, per, a.rows / ctas, !kPieces ? 1 : 2);
   const auto ring = [&](auto* kernel) {
     const int sets = sets_of(r * slot, per);
     return launch_ring(kernel, ctas, threads, static_cast<int>(sets * r * slot), st, "norm_forward_ring_kernel launch", a, static_cast<int>(slot), sets);
   };
   if (values_of(a.width) == kFew) {
     if constexpr (kPieces)
-      if (r == 4) return ring(norm_forward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 4>);
+      if (r == 2) return ring(norm_forward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 2>);
     if (r == 1) return ring(norm_forward_ring_kernel<kT, kPieces, kFew, kMaxThreads, 1>);
     return plain(norm_forward_kernel<kT, kVals, kFew, false>, ctas, threads);
   }
