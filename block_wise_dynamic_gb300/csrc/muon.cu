@@ -15,10 +15,10 @@
 // strong directions, the steps raise the weak ones by up to 3.4 each, and with
 // them the strong ones' roundings (measured in simulation, error of the result
 // relative to its norm for rank 8 plus noise of 1/140: bf16 operands 0.23,
-// fp16 0.028, pairs 5e-6; fp32 arithmetic has 2e-5).  By the last step the
-// spectrum is level and an operand's rounding counts once: for bf16 results,
-// whose own rounding is 1.7e-3, that step takes the high parts alone (4e-4 to
-// 7e-4 more).
+// fp16 0.028, pairs 5e-6; fp32 arithmetic has 2e-5).  The last step takes pairs
+// too, whatever the result's type: high parts alone would save two of its three
+// passes, and leave a bf16 result 2.0e-3 off in place of the 1.66e-3 that its
+// rounding leaves (1024 x 1024).
 //
 // The last steps of a wide matrix (n columns, m rows, n > m) stay among m x m
 // matrices, all of them polynomials of A, so that they commute and their
@@ -1171,13 +1171,13 @@ struct Step {
 };
 
 // How many of the last steps work on the squares (see the top), by what takes
-// fewer passes of the matrix instruction, at n = r m: without them 39 r + 13
-// times m m m for bf16 results and 45 r + 15 for others; five on squares 9 r +
-// 51 (5 r + 51 from exact planes), three 27 r + 33.  An error of A in a weak
-// direction is raised by 11.8 a step, so only bf16 results take five (in
-// simulation at most 4e-4 of the result, whatever the spectrum), and others
-// three where that adds nothing to what the other steps make of the same
-// error, n >= 2 m (1e-5 instead of 2e-6 for a square matrix).
+// fewer passes of the matrix instruction, at n = r m: without them 45 r + 15
+// times m m m; five on squares 9 r + 51 (5 r + 51 from exact planes), three 27
+// r + 33.  An error of A in a weak direction is raised by 11.8 a step, so only
+// bf16 results take five (in simulation at most 4e-4 of the result, whatever
+// the spectrum), and others three where that adds nothing to what the other
+// steps make of the same error, n >= 2 m (1e-5 instead of 2e-6 for a square
+// matrix).
 int squared_steps(const Shape& s, const Step& st) {
   if (st.out_type == BWD_BF16) return s.wide() ? std::min(st.steps, 5) : 0;
   return s.n >= 2 * s.m ? std::min(st.steps, 3) : 0;
@@ -1383,7 +1383,6 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
   const int before = st.steps - squares;
   for (int i = 0; i < before; ++i) {
     const bool last = i + 1 == st.steps;
-    const int passes = last && st.out_type == BWD_BF16 ? 1 : 3;
     Operation gram[kGroups], poly[kGroups], apply[kGroups];
     for (int j = 0; j < set.groups; ++j) {
       const Shape& s = set.g[j].s;
@@ -1394,10 +1393,10 @@ bwd_status run_set(const Matrices& x, const Set& set, const Step& st, uint8_t* w
       poly[j] = Operation{square, s.m, set.g[j].count, p.a, p.a, p.a, p.p};
       apply[j] = Operation{s, s.m, set.g[j].count, p.p, from, from, last ? nullptr : p.x[(i + 1) % 2]};
     }
-    run(to_square, gram, Factors{passes, 0.0f, 1.0f / kScale});
-    run(to_poly, poly, Factors{passes, kB, kC / kScale});
-    if (last) run(to_result, apply, Factors{passes, kA / kScale, 1.0f / (kScale * kScale)});
-    else run(to_x, apply, Factors{passes, kA, 1.0f / kScale});
+    run(to_square, gram, Factors{3, 0.0f, 1.0f / kScale});
+    run(to_poly, poly, Factors{3, kB, kC / kScale});
+    if (last) run(to_result, apply, Factors{3, kA / kScale, 1.0f / (kScale * kScale)});
+    else run(to_x, apply, Factors{3, kA, 1.0f / kScale});
   }
   if (squares == 0) return e;
   const Group& g = set.g[0];

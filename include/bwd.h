@@ -566,9 +566,8 @@ bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype,
  *          (-1 for a bad argument); calls that share it are ordered by the
  *          caller.
  * Products are of pairs of fp16 values (22 bits), added in fp32 by the matrix
- * instruction, which truncates; for bf16 results the last step takes the
- * values' 11 leading bits.  A matrix with a NaN or an infinity comes out NaN,
- * the others are not touched by it. */
+ * instruction, which truncates.  A matrix with a NaN or an infinity comes out
+ * NaN, the others are not touched by it. */
 int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows,
                                      const int64_t* cols);
 bwd_status bwd_orthogonalize(int32_t count, const void* const* g,

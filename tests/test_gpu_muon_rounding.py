@@ -1,0 +1,53 @@
+"""16-bit results of the orthogonalised updates: what fp32 results are, rounded once."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def muon():
+    from block_wise_dynamic_gb300 import build
+
+    build.build()
+    from block_wise_dynamic_gb300 import muon as m
+
+    return m
+
+
+def draw(rows, cols, seed, kind):
+    rng = np.random.default_rng(seed)
+    g = rng.standard_normal((rows, cols))
+    if kind == "strong":  # a few directions far above the rest
+        r = max(1, min(rows, cols) // 32)
+        g = 0.02 * g + rng.standard_normal((rows, r)) @ rng.standard_normal((r, cols))
+    return torch.from_numpy(1e-3 * g).to(DEV)
+
+
+# few tiles, whose steps all run on the matrix itself; and more, of sides too near each other for steps among the squares
+SHAPES = [(40, 70), (300, 300), (301, 777), (64, 1000), (1000, 1000), (1500, 1600), (1100, 900)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_direct_steps_round_once(muon, shape, dtype):
+    """The same 16-bit values in fp32 take the same products, so that the results are the same before they are rounded."""
+    for kind in ("gauss", "strong"):
+        for steps in (1, 5):
+            g = draw(*shape, 1, kind).to(dtype)
+            assert torch.equal(muon.orthogonalize(g, steps), muon.orthogonalize(g.float(), steps).to(dtype))
+
+
+def test_steps_round_once(muon):
+    """The step too: from zeros and without momentum a parameter becomes the update."""
+    for shape in ((300, 200), (64, 1000), (900, 1000)):
+        g = draw(*shape, 2, "strong").to(torch.bfloat16)
+        got = []
+        for kind in (torch.bfloat16, torch.float32):
+            p, m = torch.zeros(shape, dtype=kind, device=DEV), torch.zeros(shape, device=DEV)
+            muon.MuonArgs([p], [g], [m]).step(lr=1.0, momentum=0.0, nesterov=False)
+            got.append(p)
+        assert torch.equal(got[0], got[1].to(torch.bfloat16))
