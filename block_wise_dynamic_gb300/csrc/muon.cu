@@ -1024,7 +1024,7 @@ struct Shape {
   int64_t m, n;
   int64_t x_bytes() const { return 4 * m * up(n, 64); }  // a pair of planes
   int64_t a_bytes() const { return 4 * m * up(m, 64); }
-  bool wide() const { return 4 * n >= 5 * m; }
+  bool wide() const { return n >= 2 * m; }  // steps among the squares
   bool operator<(const Shape& o) const { return m != o.m ? m < o.m : n < o.n; }
 };
 Shape shape_of(int64_t rows, int64_t cols) { return rows > cols ? Shape{cols, rows} : Shape{rows, cols}; }
@@ -1170,17 +1170,18 @@ struct Step {
   bwd_dtype g_type, out_type;
 };
 
-// How many of the last steps work on the squares (see the top), by what takes
-// fewer passes of the matrix instruction, at n = r m: without them 45 r + 15
-// times m m m; five on squares 9 r + 51 (5 r + 51 from exact planes), three 27
-// r + 33.  An error of A in a weak direction is raised by 11.8 a step, so only
-// bf16 results take five (in simulation at most 4e-4 of the result, whatever
-// the spectrum), and others three where that adds nothing to what the other
-// steps make of the same error, n >= 2 m (1e-5 instead of 2e-6 for a square
-// matrix).
+// How many of the last steps work on the squares (see the top), at n = r m.  In
+// passes of the matrix instruction, times m m m, a result takes 45 r + 15
+// without them, 9 r + 51 with five (5 r + 51 from exact planes) and 27 r + 33
+// with three.  An error of A in a weak direction is raised by 11.8 a step, so
+// only bf16 results take five, which leave 3e-5 to 9e-5 of the result beside
+// the rounding's 1.66e-3 (at most 4e-4 in simulation, whatever the spectrum);
+// the direct steps, and three, leave 2e-6 to 2e-5.  Below two columns to a row
+// that buys nothing or little: in ms, bf16, with five and without, 1600 x 2048
+// 0.48 and 0.44, 1320 x 1650 0.37 and 0.39, 1100 x 2100 0.34 and 0.36; 2048 x
+// 5632 0.65 and 1.01, 11008 x 4096 2.98 and 6.45 (three: 5.11).
 int squared_steps(const Shape& s, const Step& st) {
-  if (st.out_type == BWD_BF16) return s.wide() ? std::min(st.steps, 5) : 0;
-  return s.n >= 2 * s.m ? std::min(st.steps, 3) : 0;
+  return s.wide() ? std::min(st.steps, st.out_type == BWD_BF16 ? 5 : 3) : 0;
 }
 
 template <int kBN, int kMode>

@@ -51,3 +51,20 @@ def test_steps_round_once(muon):
             muon.MuonArgs([p], [g], [m]).step(lr=1.0, momentum=0.0, nesterov=False)
             got.append(p)
         assert torch.equal(got[0], got[1].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("shape", [(1320, 1650), (1600, 2048), (1100, 2100)])
+def test_up_to_two_columns_to_a_row_round_once(muon, shape):
+    """The steps run on the matrix itself up to there."""
+    g = draw(*shape, 3, "strong").to(torch.bfloat16)
+    assert torch.equal(muon.orthogonalize(g), muon.orthogonalize(g.float()).to(torch.bfloat16))
+
+
+def test_results_repeat(muon):
+    """The same bits each time, whatever ran before in the same memory."""
+    for shape, dtype in (((2816, 1024), torch.bfloat16), ((1000, 2100), torch.float32), ((1500, 1600), torch.bfloat16), ((301, 777), torch.float32)):
+        g, other = draw(*shape, 4, "strong").to(dtype), draw(*shape, 5, "gauss").to(dtype)
+        first = muon.orthogonalize(g)
+        for _ in range(5):
+            muon.orthogonalize(other)
+            assert torch.equal(muon.orthogonalize(g), first)
