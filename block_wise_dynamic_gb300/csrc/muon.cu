@@ -746,12 +746,18 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
 // latency: launch, first copy, each stage in turn, the store.  Here a tile is
 // 128 x 64, and a cluster of `split` CTAs divides the summed axis, so that a
 // CTA has a stage or two.  A stage holds both parts of both operands, 48 KB,
-// for twelve instructions.  The low parts' products and every 256 of high x
-// high have accumulators of their own; a thread adds them up, sends each unit
-// of 8 columns to the CTA that gathers it over distributed shared memory, and
-// that one adds the cluster's parts in the order of the ranks.
+// for twelve instructions.  The low parts' products and every kChunk stages of
+// high x high, 128 products, have accumulators of their own, three of which
+// take turns: where a CTA has more stages than they hold, its storing warps add
+// up one while the next two fill.  (One 1408 x 16384, fp32, whose sums of 5,504
+// products stayed in one accumulator: error 1.6e-5 of the result, 1.9e-6 so;
+// 1408 x 5632, 1,920 products, 1.0e-5 and 3.2e-6.)  A thread adds its accumulators,
+// sends each unit of 8 columns to the CTA that gathers it over distributed
+// shared memory, and that one adds the cluster's parts in the order of the
+// ranks.
 constexpr int kSmallRows = 128, kSmallCols = 64, kSmallStages = 2;
-constexpr int kSmallThreads = 320;  // warp 0 copies, warp 1 issues, eight add up and store
+constexpr int kSmallStoreWarps = 8;
+constexpr int kSmallThreads = 32 * (2 + kSmallStoreWarps);  // warp 0 copies, warp 1 issues, the others add up and store
 constexpr int kSmallP = kSmallRows * kBK * 2, kSmallQ = kSmallCols * kBK * 2, kSmallStage = 2 * (kSmallP + kSmallQ);
 constexpr int kSmallSmem = 1024 + kSmallStages * kSmallStage;
 // Two CTAs fit an SM and its tensor memory, so that the next product's begin
@@ -774,7 +780,9 @@ struct Pair8 {
   uint4 h, l;
 };
 
-template <int kMode, int kT, bool kUpdate>
+// kLong: a CTA has more stages than the accumulators hold (without it, which
+// takes fewer registers, 777 x 301 99 us, 108 with it).
+template <int kMode, int kT, bool kUpdate, bool kLong>
 __global__ void __launch_bounds__(kSmallThreads, 2)
 ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ std::conditional_t<kMode == kFinal, FinalArgs, int> f) {
   constexpr bool kSymmetric = kMode == kGram || kMode == kPoly, kAdd = kMode != kGram;
@@ -782,7 +790,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   float* const parts = reinterpret_cast<float*>(sm);  // [rank][unit of the share][half][row][4], once the stages are done with
-  __shared__ __align__(8) uint64_t s_full[kSmallStages], s_empty[kSmallStages], s_done;
+  __shared__ __align__(8) uint64_t s_full[kSmallStages], s_empty[kSmallStages], s_done, s_acc_full[kSmallAccs], s_acc_empty[kSmallAccs];
   __shared__ uint32_t s_tmem;
   __shared__ int s_fail;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -794,8 +802,8 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   const ProductArgs& a = call.g[gi];
   const Tile tile = tile_of<kSmallRows, kSmallCols, kSymmetric>(a, item - call.start[gi]);
   const int kb0 = a.kblocks * static_cast<int>(rank) / call.split, count = a.kblocks * (static_cast<int>(rank) + 1) / call.split - kb0;
-  const int least = (count + kSmallAccs - 1) / kSmallAccs, chunk = least > kChunk ? least : kChunk;
-  const int accs = (count + chunk - 1) / chunk;
+  // sums of high x high that leave an accumulator; all but the last kSmallAccs of them while the products go on
+  const int chunks = (count + kChunk - 1) / kChunk, early = kLong && chunks > kSmallAccs ? chunks - kSmallAccs : 0;
   const bool p_low = a.passes >= 2, q_low = a.passes == 3;
   if (threadIdx.x == 0) {
     prefetch_map(&a.p);
@@ -803,6 +811,7 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
     s_fail = 0;
     for (int i = 0; i < kSmallStages; ++i) { mbar_init(&s_full[i], 1); mbar_init(&s_empty[i], 1); }
     mbar_init(&s_done, 1);
+    for (int i = 0; kLong && i < kSmallAccs; ++i) { mbar_init(&s_acc_full[i], 1); mbar_init(&s_acc_empty[i], kSmallStoreWarps); }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -848,7 +857,9 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
     const uint64_t dp0 = smem_desc(smem_u32(sm), 16, 1024, 2), dq0 = smem_desc(smem_u32(sm + 2 * kSmallP), kTrans ? kBK * 128 : 16, 1024, 2);
     constexpr uint32_t kStepP = 32 / 16, kStepQ = kTrans ? 2048 / 16 : 32 / 16;
     Ring<kSmallStages> ring;
+    Ring<kSmallAccs> acc;
     for (int i = 0; i < count; ++i, ring.next()) {
+      if (kLong && i % kChunk == 0 && !mbar_wait(&s_acc_empty[acc.s], acc.phase ^ 1u, &s_fail)) break;
       if (!mbar_wait(&s_full[ring.s], ring.phase, &s_fail)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       if (one) {
@@ -862,10 +873,12 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
         };
         if (p_low) issue(tmem, dp + kSmallP / 16, dq, i == 0);
         if (q_low) issue(tmem, dp, dq + kSmallQ / 16, false);
-        issue(tmem + kSmallCols * (1 + i / chunk), dp, dq, i % chunk == 0);
+        issue(tmem + kSmallCols * (1 + (kLong ? acc.s : i / kChunk)), dp, dq, i % kChunk == 0);
         commit_one(&s_empty[ring.s]);
+        if (kLong && i % kChunk == kChunk - 1) commit_one(&s_acc_full[acc.s]);
       }
       __syncwarp();
+      if (kLong && i % kChunk == kChunk - 1) acc.next();
     }
     if (one) commit_one(&s_done);
   } else if constexpr (kAdd) {
@@ -884,8 +897,29 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
   }
   __syncwarp();
   bool ok = true;
+  const uint32_t own = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + 16 * half;
+  const auto add_up = [&](float (&sum)[16], uint32_t column) {
+    float v[16];
+    tmem_load16(own + column, v);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) sum[j] = __fadd_rn(sum[j], v[j]);
+  };
+  float sums[kLong ? kSmallCols / 32 : 1][16] = {};
+  Ring<kSmallAccs> acc;
   if (warp >= 2) {
-    ok = __all_sync(0xffffffffu, mbar_wait(&s_done, 0, &s_fail));
+    if constexpr (kLong) {
+#pragma unroll 1
+      for (int i = 0; ok && i < early; ++i, acc.next()) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_acc_full[acc.s], acc.phase, &s_fail));
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll
+        for (int c = 0; c < kSmallCols; c += 32) add_up(sums[c / 32], (1 + acc.s) * kSmallCols + c);
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_acc_empty[acc.s]);
+      }
+    }
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(&s_done, 0, &s_fail));
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   }
   if (s_fail && lane == 0 && warp < 2) let_copies_land();
@@ -895,15 +929,15 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
 #pragma unroll
     for (int c = 0; c < kSmallCols; c += 32) {
       const int c0 = c + 16 * half;  // the two halves' warps take turns at 16 columns
-      const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c0;
-      float sum[16];
+      float (&sum)[16] = sums[kLong ? c / 32 : 0];
+      if constexpr (kLong) {
+        if (p_low && count > 0) add_up(sum, c);
+        Ring<kSmallAccs> from = acc;
+        for (int i = early; i < chunks; ++i, from.next()) add_up(sum, (1 + from.s) * kSmallCols + c);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
-      for (int i = p_low ? 0 : 1; i <= accs && count > 0; ++i) {
-        float v[16];
-        tmem_load16(from + i * kSmallCols, v);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sum[j] = __fadd_rn(sum[j], v[j]);
+        for (int j = 0; j < 16; ++j) sum[j] = 0.0f;
+        for (int i = p_low ? 0 : 1; i <= chunks && count > 0; ++i) add_up(sum, i * kSmallCols + c);
       }
 #pragma unroll
       for (int j = 0; j < 16; j += kUnit) {
@@ -1084,7 +1118,10 @@ cudaError_t opt_in_all() {
 }
 
 template <int kMode, int kT, bool kUpdate>
-cudaError_t opt_in_small() { return opt_in(ns_small_kernel<kMode, kT, kUpdate>, kSmallSmem); }
+cudaError_t opt_in_small() {
+  const cudaError_t e = opt_in(ns_small_kernel<kMode, kT, kUpdate, false>, kSmallSmem);
+  return e == cudaSuccess ? opt_in(ns_small_kernel<kMode, kT, kUpdate, true>, kSmallSmem) : e;
+}
 
 cudaError_t opt_in_all_small() {
   const cudaError_t e[] = {opt_in_small<kGram, kF32, false>(), opt_in_small<kPoly, kF32, false>(), opt_in_small<kApply, kF32, false>(),
@@ -1128,7 +1165,7 @@ bwd_status ensure_device(DeviceState* out) {
     int smem = 0;
     e = cudaDeviceGetAttribute(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor, dev);
     smem = std::max(smem / 2, kSmallSmem);
-    if (e == cudaSuccess) e = opt_in(ns_small_kernel<kApply, kF32, false>, smem);
+    if (e == cudaSuccess) e = opt_in(ns_small_kernel<kApply, kF32, false, false>, smem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(MaxDynamicSharedMemorySize)");
     cfg.blockDim = dim3(kSmallThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
@@ -1136,7 +1173,7 @@ bwd_status ensure_device(DeviceState* out) {
     for (int c = 2; c <= kMaxSplit; ++c) {
       cfg.gridDim = dim3(static_cast<unsigned>(sms / c * c));
       attr[0].val.clusterDim = {static_cast<unsigned>(c), 1, 1};
-      e = cudaOccupancyMaxActiveClusters(&d.clusters[c], ns_small_kernel<kApply, kF32, false>, &cfg);
+      e = cudaOccupancyMaxActiveClusters(&d.clusters[c], ns_small_kernel<kApply, kF32, false, false>, &cfg);
       if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
     }
     d.ctx = ctx;
@@ -1201,20 +1238,20 @@ bwd_status launch_product(const ProductArgs& a, const FinalArgs* f, const Step& 
   }
 }
 
-template <int kMode>
+template <int kMode, bool kLong>
 bwd_status launch_small(const SmallCall& c, int tiles, const FinalArgs* f, const Step& st, cudaStream_t stream) {
   const auto go = [&](auto kernel, const auto& last) {
     return launch_ex(kernel, dim3(static_cast<unsigned>(tiles * c.split)), kSmallThreads, c.split, kSmallSmem, stream, "ns_small_kernel launch",
                      c, last);
   };
   if constexpr (kMode != kFinal) {
-    return go(ns_small_kernel<kMode, kF32, false>, 0);
+    return go(ns_small_kernel<kMode, kF32, false, kLong>, 0);
   } else if (st.update) {
-    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, true>, *f);
-    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, true>, *f) : go(ns_small_kernel<kMode, kF16, true>, *f);
+    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, true, kLong>, *f);
+    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, true, kLong>, *f) : go(ns_small_kernel<kMode, kF16, true, kLong>, *f);
   } else {
-    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, false>, *f);
-    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, false>, *f) : go(ns_small_kernel<kMode, kF16, false>, *f);
+    if (st.out_type == BWD_F32) return go(ns_small_kernel<kMode, kF32, false, kLong>, *f);
+    return st.out_type == BWD_BF16 ? go(ns_small_kernel<kMode, kBF16, false, kLong>, *f) : go(ns_small_kernel<kMode, kF16, false, kLong>, *f);
   }
 }
 
@@ -1276,7 +1313,9 @@ bwd_status products(const Operation* o, int groups, const Factors& x, const Fina
     kblocks = std::max<int64_t>(kblocks, c.g[i].kblocks);
   }
   c.split = small_split(tiles, kblocks, d);
-  return launch_small<kMode>(c, static_cast<int>(tiles), f, st, stream);
+  const bool longer = (kblocks + c.split - 1) / c.split > kSmallAccs * kChunk;
+  return longer ? launch_small<kMode, true>(c, static_cast<int>(tiles), f, st, stream)
+                : launch_small<kMode, false>(c, static_cast<int>(tiles), f, st, stream);
 }
 
 // One group's product, by whichever kernel takes less time.
