@@ -20,7 +20,7 @@
 // passes, and leave a bf16 result 2.0e-3 off in place of the 1.66e-3 that its
 // rounding leaves (1024 x 1024).
 //
-// The last steps of a wide matrix (n columns, m rows, n > m) stay among m x m
+// The last steps of a wide matrix (n columns, m rows, 2 m to 16 m) stay among m x m
 // matrices, all of them polynomials of A, so that they commute and their
 // products are symmetric:
 //
@@ -1058,7 +1058,7 @@ struct Shape {
   int64_t m, n;
   int64_t x_bytes() const { return 4 * m * up(n, 64); }  // a pair of planes
   int64_t a_bytes() const { return 4 * m * up(m, 64); }
-  bool wide() const { return n >= 2 * m; }  // steps among the squares
+  bool wide() const { return n >= 2 * m && n <= 16 * m; }  // steps among the squares
   bool operator<(const Shape& o) const { return m != o.m ? m < o.m : n < o.n; }
 };
 Shape shape_of(int64_t rows, int64_t cols) { return rows > cols ? Shape{cols, rows} : Shape{rows, cols}; }
@@ -1216,7 +1216,11 @@ struct Step {
 // the direct steps, and three, leave 2e-6 to 2e-5.  Below two columns to a row
 // that buys nothing or little: in ms, bf16, with five and without, 1600 x 2048
 // 0.48 and 0.44, 1320 x 1650 0.37 and 0.39, 1100 x 2100 0.34 and 0.36; 2048 x
-// 5632 0.65 and 1.01, 11008 x 4096 2.98 and 6.45 (three: 5.11).
+// 5632 0.65 and 1.01, 11008 x 4096 2.98 and 6.45 (three: 5.11).  Above sixteen
+// a row of X is known far better than A, whose error the steps raise: fp32,
+// error against 64 bits with three, without, and in fp32 arithmetic, 64 x 65536
+// 1.2e-5, 1.7e-6 and 1.0e-6 (0.37 and 0.51 ms), 512 x 16384 3.7e-6, 0.9e-6 and
+// 1.9e-6 (0.31 and 0.40 ms); 512 x 8192 3.6e-6, 0.8e-6 and 3.1e-6.
 int squared_steps(const Shape& s, const Step& st) {
   return s.wide() ? std::min(st.steps, st.out_type == BWD_BF16 ? 5 : 3) : 0;
 }

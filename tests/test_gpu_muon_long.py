@@ -61,3 +61,35 @@ def test_long_and_short_rows_together(muon):
         want = -max(shape) ** 0.5 * ref.orthogonalize(np64(g))
         # beside an error of some 20 bits, what 300 times the truth's rounding in fp32 leaves
         assert np.linalg.norm(np64(p) - want) <= 300 * 2.0 ** -24 * np.linalg.norm(want)
+
+
+def steps_in_fp32(g):
+    a, b, c = 3.4445, -4.7750, 2.0315
+    x = g.t() if g.shape[0] > g.shape[1] else g
+    x = x / (x.square().sum().sqrt() + 1e-7)
+    for _ in range(5):
+        gram = x @ x.t()
+        x = a * x + (b * gram + c * gram @ gram) @ x
+    return x.t() if g.shape[0] > g.shape[1] else x
+
+
+@pytest.mark.parametrize("shape", [(64, 65536), (30000, 130), (16, 65536), (300, 30000)])
+def test_error_of_long_rows(muon, shape):
+    """No more than four times that of the same steps in fp32: operands have 22 bits instead of 24."""
+    rng = np.random.default_rng(3)
+    for strong in (False, True):
+        g = rng.standard_normal(shape)
+        if strong:
+            r = max(1, min(shape) // 4)
+            g += (rng.standard_normal((shape[0], r)) * np.exp(-3 * np.arange(r) / r)) @ rng.standard_normal((r, shape[1]))
+        g = torch.from_numpy(1e-3 * g).to(DEV, torch.float32)
+        want = ref.orthogonalize(np64(g))
+        off, plain = (np.linalg.norm(np64(o) - want) / np.linalg.norm(want) for o in (muon.orthogonalize(g), steps_in_fp32(g)))
+        assert off <= 4 * plain, (strong, off, plain)
+
+
+def test_more_than_sixteen_columns_to_a_row_round_once(muon):
+    """The steps run on the matrix itself from there on."""
+    for shape in ((130, 30000), (17000, 1024)):
+        g = torch.from_numpy(np.random.default_rng(4).standard_normal(shape)).to(DEV, torch.bfloat16)
+        assert torch.equal(muon.orthogonalize(g), muon.orthogonalize(g.float()).to(torch.bfloat16))
