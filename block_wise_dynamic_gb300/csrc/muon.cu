@@ -20,8 +20,8 @@
 // passes, and leave a bf16 result 2.0e-3 off in place of the 1.66e-3 that its
 // rounding leaves (1024 x 1024).
 //
-// The last steps of a wide matrix (n columns, m rows, 2 m to 16 m) stay among m x m
-// matrices, all of them polynomials of A, so that they commute and their
+// The last steps of a wide matrix (m rows, n = 2 m to 16 m columns) stay among
+// m x m matrices, all of them polynomials of A, so that they commute and their
 // products are symmetric:
 //
 //   P = a I + B;  Q = P Q;  A = P A P        and in the end X = Q X
@@ -726,6 +726,8 @@ ns_product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__
             for (int j = 0; j < 8; ++j)
               if (j0 + j < count) store1<kT>(out, at + j * ld, o[j]);
           }
+          // the next tensor copy writes where `stage` was written
+          if (adds_some) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
       }

@@ -68,3 +68,12 @@ def test_results_repeat(muon):
         for _ in range(5):
             muon.orthogonalize(other)
             assert torch.equal(muon.orthogonalize(g), first)
+
+
+def test_last_products_with_an_added_matrix_repeat(muon):
+    """Large tiles whose last product adds the matrix that it multiplies, in both orientations: the same bits each time."""
+    for shape in ((1500, 2300), (2300, 1500)):
+        for dtype in (torch.float32, torch.bfloat16, torch.float16):
+            g = draw(*shape, 6, "strong").to(dtype)
+            first = muon.orthogonalize(g)
+            assert all(torch.equal(muon.orthogonalize(g), first) for _ in range(20))
