@@ -919,7 +919,8 @@ __device__ __forceinline__ void few_load(const FewArgs& p, int line, int e, uint
     w[q] = make_uint4(0u, 0u, 0u, 0u);
     if (line >= p.m) continue;
     if (p.vec) {
-      if (e + q * kVals < p.k) w[q] = __ldg(reinterpret_cast<const uint4*>(src) + q);
+      // (not a load for constant data: the kernel ahead may have written x after this one began)
+      if (e + q * kVals < p.k) w[q] = *(reinterpret_cast<const uint4*>(src) + q);
     } else {
 #pragma unroll
       for (int j = 0; j < kVals; ++j)

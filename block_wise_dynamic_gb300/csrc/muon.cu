@@ -894,7 +894,8 @@ ns_small_kernel(const __grid_constant__ SmallCall call, const __grid_constant__ 
         continue;
       }
       const __half* const from = a.add_at + 2 * tile.z * plane + static_cast<int64_t>(r) * a.pitch + unit_col(u);
-      add[i] = Pair8{__ldg(reinterpret_cast<const uint4*>(from)), __ldg(reinterpret_cast<const uint4*>(from + plane))};
+      // (not loads for constant data: the kernel ahead may have written these after this one began)
+      add[i] = Pair8{*reinterpret_cast<const uint4*>(from), *reinterpret_cast<const uint4*>(from + plane)};
     }
   }
   __syncwarp();
