@@ -133,6 +133,26 @@ struct GroupSum {
   }
 };
 
+// What the kernels for few rows and those for many make of a row's sums, so that
+// they make the same of the same sums.
+//
+// s / width, rounded to nearest, for inv = RN(1 / width): the quotient's
+// remainder is exact in one fused multiply-add, and one step with it rounds
+// correctly (Markstein 1990) where nothing underflows, for sums above 2^-100.
+// (A product with 1 / width alone is a unit, 2^-14, off for a thousand 1000.0,
+// and y 0.019, as rstd is 316.)
+__device__ __forceinline__ float per_width(float s, float width, float inv) {
+  const float q = __fmul_rn(s, inv), r = __fmaf_rn(__fmaf_rn(-width, q, s), inv, q);
+  return fabsf(q) <= 3.402823466e38f ? r : q;
+}
+// (var + eps)^-1/2: rsqrtf is up to two units off, one step of Newton's method
+// leaves less than one.  (A correctly rounded root and quotient, 16384 x 4096
+// bf16: 51.4 us forward, 47.2 so; 45.7 with rsqrtf alone and the product above.)
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  const float x = __fadd_rn(var, eps), y = rsqrtf(x), e = __fmaf_rn(-__fmul_rn(x, y), y, 1.0f);
+  return fabsf(e) <= 1.0f ? __fmaf_rn(__fmul_rn(0.5f, y), e, y) : y;
+}
+
 struct ForwardArgs {
   const void* x;
   int64_t ldx;  // elements between rows
@@ -168,7 +188,7 @@ norm_forward_kernel(const ForwardArgs a) {
       g[i * kVals + j] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
       b[i * kVals + j] = c < a.width ? vector_at<kT>(a.beta, c + j, 0.0f) : 0.0f;
     }
-  const float width = static_cast<float>(a.width);
+  const float width = static_cast<float>(a.width), inv_width = __fdiv_rn(1.0f, width);
   for (; row < a.rows; row += groups) {
     float v[kValues];
     float s[1] = {0.0f};
@@ -178,7 +198,7 @@ norm_forward_kernel(const ForwardArgs a) {
       for (int j = 0; j < kVals; ++j) s[0] += v[i * kVals + j] = next.value(i, j);
     if (row + groups < a.rows) next.load(x_row(row + groups), a.width, t, threads);
     sum(s);
-    const float mean = __fdiv_rn(s[0], width);
+    const float mean = per_width(s[0], width, inv_width);
     s[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -191,7 +211,7 @@ norm_forward_kernel(const ForwardArgs a) {
       }
     }
     sum(s);
-    const float rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(s[0], width), a.eps)));
+    const float rstd = rstd_of(per_width(s[0], width, inv_width), a.eps);
     if (t == 0) {
       if (a.mean) a.mean[row] = mean;
       if (a.rstd) a.rstd[row] = rstd;
@@ -257,7 +277,7 @@ norm_backward_kernel(const BackwardArgs a) {
       g[e] = c < a.width ? vector_at<kT>(a.gamma, c + j, 1.0f) : 0.0f;
       dg[e] = db[e] = 0.0f;
     }
-  const float width = static_cast<float>(a.width);
+  const float width = static_cast<float>(a.width), inv_width = __fdiv_rn(1.0f, width);
   for (; row < a.rows; row += groups) {
     const Part<kT, kVals, kValues> x = next_x, dy = next_dy;
     const float mean = next_mean, rstd = next_rstd;
@@ -281,7 +301,7 @@ norm_backward_kernel(const BackwardArgs a) {
     }
     if (!a.dx) continue;
     sum(s);
-    const float mean_h = __fdiv_rn(s[0], width), mean_hx = __fdiv_rn(s[1], width);
+    const float mean_h = per_width(s[0], width, inv_width), mean_hx = per_width(s[1], width, inv_width);
     char* const dx = static_cast<char*>(a.dx) + row * a.width * elem_bytes<kT>();
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -613,13 +633,13 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
     b[e] = cols.vector(a.beta, e, 0.0f);
   }
   if constexpr (!kPieces) __syncthreads();  // the first row's start, which a thread copied
-  const float inv_width = __fdiv_rn(1.0f, static_cast<float>(a.width));
+  const float width = static_cast<float>(a.width), inv_width = __fdiv_rn(1.0f, width);
   int turn = 0;
   for (; row < a.rows; row += step) {
     ring.wait(&s_fail);
     float mean[kR], s[kR];
     if constexpr (kKeep) {
-      // A row's values stay in registers, widened once.  (16384 x 4096 bf16 44.7
+      // A row's values stay in registers, widened once.  (16384 x 4096 bf16 45
       // us, 49.4 with four rows read anew and widened by each pass, 56 with one
       // row in registers; 8192 x 8192 bf16 50.3 and 60.1; 16384 x 768 fp32 15.9
       // and 23.9.  The backward pass, which would hold twice as much, gains
@@ -641,7 +661,7 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
       ring.refill(row, step);
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
-        mean[r] = __fmul_rn(s[r], inv_width);
+        mean[r] = per_width(s[r], width, inv_width);
         const float2 less = both(-mean[r]);
         float2 sum = both(0.0f);
 #pragma unroll
@@ -657,7 +677,7 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         if (row + r >= a.rows) break;
-        const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
+        const float rstd = rstd_of(per_width(s[r], width, inv_width), a.eps);
         if (threadIdx.x == 0) {
           if (a.mean) a.mean[row + r] = mean[r];
           if (a.rstd) a.rstd[row + r] = rstd;
@@ -688,7 +708,7 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
       ring.refill(row, step);
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
-        mean[r] = __fmul_rn(s[r], inv_width);
+        mean[r] = per_width(s[r], width, inv_width);
         const float2 less = both(-mean[r]);
         float2 sum = both(0.0f);
         cols.template over<false, 1>(nullptr, {ring.row(r, 0, row + r)}, [&](int, bool there, const float2 (&v)[1]) {
@@ -702,7 +722,7 @@ norm_forward_ring_kernel(const ForwardArgs a, int slot, int sets) {
 #pragma unroll
       for (int r = 0; r < kR; ++r) {
         if (row + r >= a.rows) break;
-        const float rstd = rsqrtf(__fadd_rn(__fmul_rn(s[r], inv_width), a.eps));
+        const float rstd = rstd_of(per_width(s[r], width, inv_width), a.eps);
         if (threadIdx.x == 0) {
           if (a.mean) a.mean[row + r] = mean[r];
           if (a.rstd) a.rstd[row + r] = rstd;
@@ -754,7 +774,7 @@ norm_backward_ring_kernel(const BackwardArgs a, int slot, int sets) {
     dg[e] = db[e] = both(0.0f);
   }
   if constexpr (!kPieces) __syncthreads();  // the first rows' starts, which a thread copied
-  const float inv_width = __fdiv_rn(1.0f, static_cast<float>(a.width));
+  const float width = static_cast<float>(a.width), inv_width = __fdiv_rn(1.0f, width);
   int turn = 0;
   for (; row < a.rows; row += step) {
     float mean[kR], rstd[kR], s[2 * kR];
@@ -784,7 +804,7 @@ norm_backward_ring_kernel(const BackwardArgs a, int slot, int sets) {
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       if (!a.dx || row + r >= a.rows) break;
-      const float mean_h = __fmul_rn(s[2 * r], inv_width), mean_hx = __fmul_rn(s[2 * r + 1], inv_width);
+      const float mean_h = per_width(s[2 * r], width, inv_width), mean_hx = per_width(s[2 * r + 1], width, inv_width);
       const float2 less = both(-mean[r]), scale = both(rstd[r]), less_h = both(-mean_h), less_hx = both(-mean_hx);
       cols.template over<true, 2>(static_cast<char*>(a.dx) + (row + r) * row_bytes, {ring.row(r, 0, row + r), ring.row(r, 1, row + r)},
                                   [&](int e, bool, const float2 (&v)[2]) {
