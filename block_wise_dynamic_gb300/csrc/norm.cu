@@ -534,6 +534,7 @@ struct RowRing {
       using Elem = std::conditional_t<kT == kF32, uint32_t, uint16_t>;
       const auto copy = [&](uintptr_t at, uintptr_t end) {
         for (; at < end; at += sizeof(Elem)) *reinterpret_cast<Elem*>(dst + (at - start)) = *reinterpret_cast<const Elem*>(at);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // a later row's copy writes here too
       };
       if (first && low != from) low += 16;
       if (last && high != to) high -= 16;
