@@ -27,7 +27,7 @@ from typing import Sequence
 import torch
 
 from . import _abi
-from . import _GDT, _launch, _lib, _need
+from . import _GDT, _launch, _lib, _need, _stream_handle
 from .adam32 import _check_scale, _GradList, _one_dtype, _pointers
 from .fp8 import _on
 from .optim import Adam8bit
@@ -40,11 +40,11 @@ def _sides(shapes):
     return kind(*[r for r, _ in shapes]), kind(*[c for _, c in shapes])
 
 
-def _workspace(count, rows, cols, device):
+def _work_bytes(count, rows, cols):
     size = _lib.bwd_orthogonalize_work_bytes(count, rows, cols)
     if size < 0:
         raise ValueError("a matrix has at most 65536 rows and columns")
-    return torch.empty(size, dtype=torch.uint8, device=device)
+    return size
 
 
 def orthogonalize(g: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
@@ -69,7 +69,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
     if count == 0:
         return out
     rows, cols = _sides([(r, c)] * count)
-    work = _workspace(count, rows, cols, g.device)
+    work = torch.empty(_work_bytes(count, rows, cols), dtype=torch.uint8, device=g.device)
     size = r * c * g.element_size()
     table = ctypes.c_void_p * count
     _launch("bwd_orthogonalize", g.device, None, count, table(*[g.data_ptr() + i * size for i in range(count)]), _GDT[g.dtype], rows, cols,
@@ -79,9 +79,10 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
 
 class MuonArgs(_GradList):
     """Host pointer arrays for ``bwd_muon_step``, built once for a fixed list
-    of matrices and reused by every step.  Its workspace belongs to it (or is
-    ``work``, another list's, that is as large): steps that share one are made
-    on one stream, or ordered by the caller."""
+    of matrices and reused by every step.  Its workspace belongs to it and to
+    the stream that was current when it was made (or is ``work``, that of
+    another list made on the same stream, if it is as large); a step on another
+    stream, or in a graph that is captured, takes one of its own."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor], work=None):
         if not (len(grads) == len(momenta) == len(params)):
@@ -100,15 +101,28 @@ class MuonArgs(_GradList):
         self.p, self.m = _pointers(params), _pointers(momenta)
         self._shapes = [p.shape for p in params]
         self.rows, self.cols = _sides(self._shapes)
-        size = _lib.bwd_orthogonalize_work_bytes(self.T, self.rows, self.cols) if work is not None else 0
-        if work is None or not 0 <= size <= work.numel() or work.device != self.device:
-            work = _workspace(self.T, self.rows, self.cols, self.device) if self.T else None
-        self.work = work
+        self.work = None
+        if self.T:
+            self._size = _work_bytes(self.T, self.rows, self.cols)
+            self._stream = _stream_handle(self.device, None)
+            fits = work is not None and work.device == self.device and work.is_contiguous() and work.nbytes >= self._size
+            self.work = work if fits else torch.empty(self._size, dtype=torch.uint8, device=self.device)
 
     def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
         if [g.shape for g in grads] != self._shapes:
             raise ValueError("gradient shapes differ from the parameters'")
         super().set_grads(grads)
+
+    def _workspace(self, stream):
+        """The list's workspace, or one for a single call: the memory of the
+        list's follows the order of the stream that it was made on alone, and a
+        graph may outlive it."""
+        if stream is not None:
+            with _on(stream, self.device):
+                return self._workspace(None)
+        if _stream_handle(self.device, None) == self._stream and not torch.cuda.is_current_stream_capturing():
+            return self.work
+        return torch.empty(self._size, dtype=torch.uint8, device=self.device)
 
     def step(self, *, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, rms=0.2, steps=5, grad_scale=None, stream=None) -> None:
         """One step in place:
@@ -122,8 +136,9 @@ class MuonArgs(_GradList):
         if self.T == 0:
             return
         hp = _abi.MuonHParams(lr, momentum, weight_decay, rms, int(bool(nesterov)), int(steps))
+        scale, work = _check_scale(grad_scale, self.device), self._workspace(stream)
         _launch("bwd_muon_step", self.device, stream, self.T, self.p, self.p_dtype, self.g, self.g_dtype, self.m, self.rows, self.cols,
-                _check_scale(grad_scale, self.device), ctypes.byref(hp), self.work.data_ptr())
+                scale, ctypes.byref(hp), work.data_ptr())
 
 
 class Muon(torch.optim.Optimizer):
@@ -132,8 +147,8 @@ class Muon(torch.optim.Optimizer):
     gradients are float32, bfloat16 or float16 CUDA tensors, momentum float32;
     bfloat16 parameters take an update of that precision, the others one of
     some 20 bits.  ``clip_scale`` and ``step(grad_scale=factor)`` are as
-    :class:`Adam8bit`'s.  All of an optimizer's steps share a workspace for
-    each device: they are made on one stream, or ordered by the caller."""
+    :class:`Adam8bit`'s.  The steps of all groups share a workspace for each
+    device and stream; one that is captured in a graph takes one of its own."""
 
     def __init__(self, params, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, rms=0.2, steps=5):
         if not 0.0 <= lr < float("inf"):
@@ -181,8 +196,9 @@ class Muon(torch.optim.Optimizer):
         plan = []
         for (device, _, _), idx in buckets.items():
             ps = [params[i].view(params[i].shape[0], -1) for i in idx]
-            args = MuonArgs(ps, self._matrices(grads, idx), [self.state[params[i]]["momentum_buffer"] for i in idx], self._work.get(device))
-            self._work[device] = args.work
+            place = device, _stream_handle(device, None)
+            args = MuonArgs(ps, self._matrices(grads, idx), [self.state[params[i]]["momentum_buffer"] for i in idx], self._work.get(place))
+            self._work[place] = args.work
             plan.append((idx, args))
         return {"params": list(params), "has_grad": [g is not None for g in grads], "at": [p.data_ptr() for p in params],
                 "buckets": plan}

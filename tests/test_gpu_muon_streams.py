@@ -1,0 +1,119 @@
+"""Workspaces of the optimizer step on other streams than the one they were made on, and in graphs."""
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def muon():
+    from block_wise_dynamic_gb300 import build
+
+    build.build()
+    from block_wise_dynamic_gb300 import muon as m
+
+    return m
+
+
+def draw(shape, seed):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape).astype(np.float32)).to(DEV)
+
+
+def lists(seed):
+    shapes = [(300, 500), (500, 300)]
+    return [draw(s, seed + i) for i, s in enumerate(shapes)], [draw(s, seed + 10 + i) for i, s in enumerate(shapes)], [torch.zeros(s, device=DEV) for s in shapes]
+
+
+def busy(stream):
+    """Some milliseconds of work on a stream."""
+    with torch.cuda.stream(stream):
+        a = torch.ones(6000, 6000, device=DEV)
+        for _ in range(3):
+            a = a @ a * 1e-4
+    return a
+
+
+@pytest.mark.parametrize("how", ["argument", "current", "handle"])
+def test_a_dropped_list_keeps_its_workspace_until_the_step_has_run(muon, how):
+    """The step waits behind other work on a side stream while the list's memory is handed out and written."""
+    busy(torch.cuda.current_stream())  # libraries set up
+    ps, gs, ms = lists(1)
+    twin = [[t.clone() for t in l] for l in (ps, gs, ms)]
+    muon.MuonArgs(*twin).step()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    args = muon.MuonArgs(ps, gs, ms)
+    size = args.work.numel()
+    torch.cuda.synchronize()
+    kept = busy(side)
+    if how == "argument":
+        args.step(stream=side)
+    elif how == "handle":
+        args.step(stream=side.cuda_stream)
+    else:
+        with torch.cuda.stream(side):
+            args.step()
+    running = not side.query()
+    del args
+    others = [torch.full((size,), 255, dtype=torch.uint8, device=DEV) for _ in range(4)]
+    assert running
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(ps + ms, twin[0] + twin[2]))
+    del kept, others
+
+
+def test_a_graph_keeps_its_workspace(muon):
+    """Replayed after the optimizer's plan, and with it the list's workspace, was replaced, and that memory written."""
+    ps, gs, _ = lists(3)
+    params = [[torch.nn.Parameter(ps[0].clone()), torch.nn.Parameter(draw((700, 900), 30))] for _ in range(2)]
+    grads = [gs[0], draw((700, 900), 31)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        one, two = (muon.Muon(p) for p in params)
+        params[0][0].grad = grads[0]
+        one.step()
+        graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        one.step()
+    with torch.cuda.stream(side):
+        params[0][1].grad = grads[1]
+        one.step()  # a new plan, whose workspace is larger
+        others = [torch.full((1 << 20,), 255, dtype=torch.uint8, device=DEV) for _ in range(40)]
+        graph.replay()
+        # the same three steps: of one matrix, of both (which divides the sums in another way), and of one
+        for both in (False, True, False):
+            params[1][0].grad, params[1][1].grad = grads[0], grads[1] if both else None
+            two.step()
+    torch.cuda.synchronize()
+    assert torch.equal(params[0][0], params[1][0]) and torch.equal(params[0][1], params[1][1])
+    del others
+
+
+def test_an_optimizer_on_a_side_stream(muon):
+    """Steps on another stream than the first one's, whose plan and workspace are replaced while they wait."""
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    ps, gs, _ = lists(2)
+    a, b = ([torch.nn.Parameter(p.clone()) for p in ps] for _ in range(2))
+    one, two = muon.Muon(a), muon.Muon(b)
+    for opt, params, stream in ((one, a, side), (two, b, torch.cuda.current_stream())):
+        params[0].grad = gs[0]
+        opt.step()  # one matrix, on the current stream
+        torch.cuda.synchronize()
+        params[1].grad = gs[1]
+        with torch.cuda.stream(stream):
+            kept = busy(stream)
+            opt.step()  # both: a new plan
+            opt.step()
+            params[1].grad = None
+            opt.step()  # another
+        torch.empty(1 << 24, dtype=torch.uint8, device=DEV).fill_(255)
+        torch.cuda.synchronize()
+        del kept
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
