@@ -69,6 +69,7 @@ class MuonHParams(ctypes.Structure):
         ("rms", ctypes.c_double),
         ("nesterov", ctypes.c_int32),
         ("steps", ctypes.c_int32),
+        ("work_most", ctypes.c_int64),
     ]
 
 
@@ -142,6 +143,7 @@ _SIGNATURES = {
         _int, [_vp, _vp, _int, _i64, _i64, _i64, _i64, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     "bwd_orthogonalize_work_bytes": (_i64, [_i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
     "bwd_orthogonalize": (_int, [_i32, _pp, _int, ctypes.POINTER(_i64), ctypes.POINTER(_i64), _i32, _pp, _vp, _vp]),
+    "bwd_muon_work_bytes": (_i64, [_i32, ctypes.POINTER(_i64), ctypes.POINTER(_i64), _i64]),
     "bwd_muon_step": (
         _int, [_i32, _pp, _int, _pp, _int, _pp, ctypes.POINTER(_i64), ctypes.POINTER(_i64), _vp, ctypes.POINTER(MuonHParams), _vp, _vp]),
     "bwd_check_device": (_int, [_vp]),

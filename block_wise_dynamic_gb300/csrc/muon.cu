@@ -1053,8 +1053,9 @@ int64_t up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 constexpr int64_t kMaxSide = 65536;
 constexpr int kMaxSteps = 100;
-// Bytes of a batch of more than one matrix.  (48 matrices of 1024 x 4096 and 24
-// of 1024 x 1024: 9.50 ms with 1 GB, 9.19 with 2, 8.84 with 4, which is one batch.)
+// Bytes of a batch of more than one matrix, where the caller names no other
+// number.  (48 matrices of 1024 x 4096, 50 MB each, and 24 of 1024 x 1024: 9.45
+// ms with 1 GB, 9.20 with 2, 8.88 with 4, of which they take 2.4.)
 constexpr int64_t kWorkMost = int64_t{4} << 30;
 
 struct Shape {
@@ -1208,6 +1209,7 @@ struct Step {
   int nesterov, steps;
   bool has_momentum, update;
   bwd_dtype g_type, out_type;
+  int64_t work_most;  // bytes of a batch of more than one matrix
 };
 
 // How many of the last steps work on the squares (see the top), at n = r m.  In
@@ -1507,9 +1509,10 @@ bwd_status order(int32_t count, const int64_t* rows, const int64_t* cols, std::v
 
 // Calls f(set) for matrices in that order, set by set.  Shapes with few tiles
 // share sets of up to kBatch matrices and kGroups shapes; the others have sets
-// of their own, of equal numbers and kWorkMost bytes at most.
+// of their own, of equal numbers.  A set of more than one matrix has `work_most`
+// bytes at most.
 template <typename F>
-bwd_status each_set(const std::vector<int32_t>& at, const int64_t* rows, const int64_t* cols, F f) {
+bwd_status each_set(const std::vector<int32_t>& at, const int64_t* rows, const int64_t* cols, int64_t work_most, F f) {
   constexpr int64_t kFewTiles = 256;
   Set few{};
   few.small = true;
@@ -1523,17 +1526,21 @@ bwd_status each_set(const std::vector<int32_t>& at, const int64_t* rows, const i
     const Shape s = shape_of(rows[at[i]], cols[at[i]]);
     for (j = i; j < all && !(s < shape_of(rows[at[j]], cols[at[j]]));) ++j;
     const int64_t number = j - i;
-    if (number <= kBatch && number * tiles_of(s, kSmallRows, kSmallCols, false) <= kFewTiles) {
-      // a set's matrices follow one another
-      if (few.groups && (few.groups == kGroups || few.count() + number > kBatch || few.g[few.groups - 1].first + few.g[few.groups - 1].count != i))
-        if (const bwd_status e = flush()) return e;
-      few.g[few.groups++] = Group{s, i, number};
-      continue;
-    }
     Set one{};
     one.groups = 1;
-    one.g[0] = Group{s, i, 1};
-    int64_t most = kWorkMost / one.bytes();
+    one.g[0] = Group{s, i, number};
+    one.small = number <= kBatch && number * tiles_of(s, kSmallRows, kSmallCols, false) <= kFewTiles;
+    if (one.small && (number == 1 || one.bytes() <= work_most)) {
+      // a set's matrices follow one another
+      if (few.groups && (few.groups == kGroups || few.count() + number > kBatch || few.bytes() + one.bytes() > work_most ||
+                         few.g[few.groups - 1].first + few.g[few.groups - 1].count != i))
+        if (const bwd_status e = flush()) return e;
+      few.g[few.groups++] = one.g[0];
+      continue;
+    }
+    one.small = false;
+    one.g[0].count = 1;
+    int64_t most = work_most / one.bytes();
     most = most < 1 ? 1 : most > kBatch ? kBatch : most;
     const int64_t sets = (number + most - 1) / most, each = (number + sets - 1) / sets;
     for (int64_t b = i; b < j; b += each) {
@@ -1567,7 +1574,7 @@ bwd_status run(int32_t count, const void* const* g, float* const* mom, void* con
   DeviceState d;
   if ((s = ensure_device(&d)) != BWD_OK) return s;
   static thread_local Matrices x;
-  return each_set(at, rows, cols, [&](const Set& set) {
+  return each_set(at, rows, cols, st.work_most, [&](const Set& set) {
     for (int64_t z = 0; z < set.count(); ++z) {
       const int32_t i = at[static_cast<size_t>(set.g[0].first + z)];
       x.g[z] = g[i];
@@ -1593,11 +1600,15 @@ bwd_status take_muon_fault(unsigned int* fault) { return take_wait_fault(fault);
 
 extern "C" {
 
-int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows, const int64_t* cols) try {
+int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows, const int64_t* cols) {
+  return bwd_muon_work_bytes(count, rows, cols, 0);
+}
+
+int64_t bwd_muon_work_bytes(int32_t count, const int64_t* rows, const int64_t* cols, int64_t work_most) try {
   std::vector<int32_t> at;
-  if (count < 0 || (count > 0 && (!rows || !cols)) || order(count, rows, cols, &at) != BWD_OK) return -1;
+  if (count < 0 || work_most < 0 || (count > 0 && (!rows || !cols)) || order(count, rows, cols, &at) != BWD_OK) return -1;
   int64_t most = 0;
-  each_set(at, rows, cols, [&](const Set& set) {
+  each_set(at, rows, cols, work_most > 0 ? work_most : kWorkMost, [&](const Set& set) {
     most = std::max(most, set.bytes());
     return BWD_OK;
   });
@@ -1608,7 +1619,7 @@ int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows, const i
 
 bwd_status bwd_orthogonalize(int32_t count, const void* const* g, bwd_dtype dtype, const int64_t* rows, const int64_t* cols, int32_t steps,
                              void* const* out, void* work, void* stream) {
-  return run(count, g, nullptr, out, rows, cols, Step{nullptr, 0.0f, 1.0f, 0.0, 0, steps, false, false, dtype, dtype}, work, stream);
+  return run(count, g, nullptr, out, rows, cols, Step{nullptr, 0.0f, 1.0f, 0.0, 0, steps, false, false, dtype, dtype, kWorkMost}, work, stream);
 }
 
 bwd_status bwd_muon_step(int32_t count, void* const* p, bwd_dtype p_dtype, const void* const* g, bwd_dtype g_dtype, float* const* mom,
@@ -1619,8 +1630,9 @@ bwd_status bwd_muon_step(int32_t count, void* const* p, bwd_dtype p_dtype, const
       !std::isfinite(hp->weight_decay))
     return fail(BWD_ERR_INVALID_ARG, "lr and weight_decay must be finite and >= 0, momentum in [0, 1)");
   if (!(hp->rms >= 0.0) || !std::isfinite(hp->rms)) return fail(BWD_ERR_INVALID_ARG, "rms must be finite and >= 0");
+  if (hp->work_most < 0) return fail(BWD_ERR_INVALID_ARG, "work_most must be >= 0");
   const Step st{grad_scale, static_cast<float>(hp->momentum), static_cast<float>(1.0 - hp->lr * hp->weight_decay), hp->lr * hp->rms,
-                hp->nesterov != 0, hp->steps, true, true, g_dtype, p_dtype};
+                hp->nesterov != 0, hp->steps, true, true, g_dtype, p_dtype, hp->work_most > 0 ? hp->work_most : kWorkMost};
   return run(count, g, mom, reinterpret_cast<void* const*>(p), rows, cols, st, work, stream);
 }
 

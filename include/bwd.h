@@ -564,7 +564,10 @@ bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype,
  *   rows, cols : HOST arrays, at most 65536 each; an empty matrix is left out.
  *   work : device, 256-byte aligned, bwd_orthogonalize_work_bytes(...) bytes
  *          (-1 for a bad argument); calls that share it are ordered by the
- *          caller.
+ *          caller.  A matrix of m x n, m <= n, takes 8 m (n + m) bytes, with
+ *          n and m in the sums rounded up to 64, and 8 m m more where 2 m <= n
+ *          <= 16 m; up to 64 matrices are worked on together, of those that
+ *          are not small as many as 4 GB hold.
  * Products are of pairs of fp16 values (22 bits), added in fp32 by the matrix
  * instruction, which truncates.  A matrix with a NaN or an infinity comes out
  * NaN, the others are not touched by it. */
@@ -584,6 +587,8 @@ typedef struct {
   double rms;
   int32_t nesterov;
   int32_t steps;
+  int64_t work_most; /* bytes that matrices worked on together may take of
+                        work, a single one aside; 0 for 4 GB */
 } bwd_muon_hparams;
 
 /* One step over a list of matrices, in place:
@@ -594,7 +599,10 @@ typedef struct {
  *             values of p_dtype, g_dtype and float; p and m are updated.
  *   grad_scale : device float[1], s, read by the kernels, or NULL for 1.
  *             Where it is infinite or NaN the call writes nothing but work.
- *   work : as for bwd_orthogonalize. */
+ *   work : as for bwd_orthogonalize, bwd_muon_work_bytes(...) bytes for the
+ *          hyper-parameters' work_most. */
+int64_t bwd_muon_work_bytes(int32_t count, const int64_t* rows,
+                            const int64_t* cols, int64_t work_most);
 bwd_status bwd_muon_step(int32_t count, void* const* p, bwd_dtype p_dtype,
                          const void* const* g, bwd_dtype g_dtype,
                          float* const* m, const int64_t* rows,

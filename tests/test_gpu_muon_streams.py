@@ -117,3 +117,45 @@ def test_an_optimizer_on_a_side_stream(muon):
         torch.cuda.synchronize()
         del kept
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_a_limited_workspace(muon):
+    """Fewer matrices at a time; a copied optimizer and one that resumes keep the limit, and it can be changed between steps."""
+    import copy
+
+    from oracle import muon as ref
+
+    shapes = [(300, 700)] * 9 + [(40, 60), (30, 90)]
+    gs = [draw(s, 50 + i) for i, s in enumerate(shapes)]
+    want = [-0.1 * 0.2 * max(s) ** 0.5 * ref.orthogonalize(g.double().cpu().numpy()) for s, g in zip(shapes, gs)]
+
+    def near(params):
+        for p, w in zip(params, want):
+            # beside an error of some 20 bits, what 300 times the truth's rounding in fp32 leaves
+            assert np.linalg.norm(p.detach().double().cpu().numpy() - w) <= 300 * 2.0 ** -24 * np.linalg.norm(w)
+
+    sizes = []
+    for limit in (None, 8 << 20, 1):
+        ps, ms = [torch.zeros(s, device=DEV) for s in shapes], [torch.zeros(s, device=DEV) for s in shapes]
+        args = muon.MuonArgs(ps, gs, ms, work_bytes=limit)
+        args.step(lr=0.1)
+        near(ps)
+        sizes.append(args.work.numel())
+    assert sizes[0] > 8 << 20 >= sizes[1] > sizes[2]
+
+    params = [torch.nn.Parameter(torch.zeros(s, device=DEV)) for s in shapes]
+    opt = muon.Muon(params, lr=0.1, work_bytes=8 << 20)
+    for p, g in zip(params, gs):
+        p.grad = g
+    opt.step()
+    near(params)
+    assert [w.numel() for w in opt._work.values()] == [sizes[1]]
+    assert copy.deepcopy(opt).param_groups[0]["work_bytes"] == 8 << 20
+    state = opt.state_dict()
+    del state["param_groups"][0]["work_bytes"]  # as an earlier version saved it
+    opt.load_state_dict(state)
+    opt.step()
+    assert sizes[0] in [w.numel() for w in opt._work.values()]
+    opt.param_groups[0]["work_bytes"] = 1
+    opt.step()
+    assert all(p.isfinite().all() for p in params)
