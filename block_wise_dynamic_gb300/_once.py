@@ -1,11 +1,23 @@
-"""First derivatives only: autograd Functions whose backward pass computes
-through addresses."""
+"""First derivatives only, and none in forward mode: autograd Functions whose
+passes compute through addresses."""
 
 from __future__ import annotations
 
 from functools import wraps
 
 import torch
+from torch.autograd import forward_ad
+
+
+def without_autograd() -> bool:
+    """Whether a module may leave its Function out.  ``no_grad`` does not
+    switch forward mode off: inside a ``dual_level`` the Function is called,
+    which refuses an input with a tangent."""
+    return not torch.is_grad_enabled() and forward_ad._current_level < 0
+
+
+def has_tangent(x: torch.Tensor) -> bool:
+    return forward_ad._current_level >= 0 and forward_ad.unpack_dual(x).tangent is not None
 
 
 class _NoSecondDerivative(torch.autograd.Function):

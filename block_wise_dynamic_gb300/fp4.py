@@ -23,6 +23,7 @@ from typing import Optional
 import torch
 
 from . import _GDT, _launch, _need
+from ._once import has_tangent
 from .fp8 import _bytes, _matrix, _on, _ptr, _round256
 
 __all__ = ["Fp4Matrix", "quantize", "dequantize", "matmul", "linear", "Fp4Linear"]
@@ -183,7 +184,7 @@ class Fp4Linear(torch.nn.Module):
         return Fp4Matrix(self.out_features, self.in_features, self.dtype, self.quantized)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if torch.is_grad_enabled() and x.requires_grad:
+        if has_tangent(x) or torch.is_grad_enabled() and x.requires_grad:
             raise RuntimeError("Fp4Linear has no gradients: use it under torch.no_grad()")
         bias = self.bias if self.bias is None or self.bias.dtype == x.dtype else self.bias.to(x.dtype)
         return linear(x, self.weight, bias)

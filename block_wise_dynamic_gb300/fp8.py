@@ -28,7 +28,7 @@ import torch
 
 from . import _abi
 from . import _GDT, _launch, _need
-from ._once import first_order
+from ._once import first_order, without_autograd
 
 __all__ = ["Fp8Matrix", "quantize", "dequantize", "matmul", "linear", "forward", "backward", "Fp8Linear"]
 
@@ -361,8 +361,9 @@ class Fp8Linear(torch.nn.Module):
     """Linear layer whose three products take 8-bit operands.  ``weight``
     (outputs x inputs, Xavier-uniform) and ``bias`` (zeros) are ordinary
     parameters of ``dtype`` for any optimizer; each call quantizes the weight
-    as it is then.  It has first derivatives only: differentiating through
-    gradients made with ``create_graph`` raises.  :func:`linear` takes a weight quantized once."""
+    as it is then.  It has first derivatives in backward mode only:
+    differentiating through gradients made with ``create_graph`` raises, and so
+    do inputs with a forward-mode tangent.  :func:`linear` takes a weight quantized once."""
 
     def __init__(self, in_features: int, out_features: int, bias: bool = True, device=None, dtype=torch.bfloat16):
         super().__init__()
@@ -376,6 +377,6 @@ class Fp8Linear(torch.nn.Module):
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         wq = quantize(self.weight.detach(), "tiles")
-        if not torch.is_grad_enabled():
+        if without_autograd():
             return linear(x, wq, self.bias)
         return _Fp8LinearFn.apply(x, self.weight, self.bias, wq)

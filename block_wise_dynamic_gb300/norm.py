@@ -24,7 +24,7 @@ import torch
 
 from . import _abi
 from . import _GDT, _launch, _need
-from ._once import first_order
+from ._once import first_order, without_autograd
 from .fp8 import _matrix, _on, _ptr
 
 EPS = 1e-5
@@ -127,8 +127,9 @@ class LayerNorm(torch.nn.Module):
     """Layer normalisation over the last dimension of ``dim`` elements.
     ``weight`` (ones) and, with ``bias``, ``bias`` (zeros) are float32 unless
     ``dtype`` says otherwise, for activations of any of the types.  It has
-    first derivatives only: differentiating through gradients made with
-    ``create_graph`` raises."""
+    first derivatives in backward mode only: differentiating through gradients
+    made with ``create_graph`` raises, and so do inputs with a forward-mode
+    tangent."""
 
     def __init__(self, dim: int, eps: float = EPS, bias: bool = True, device=None, dtype=torch.float32):
         super().__init__()
@@ -140,6 +141,6 @@ class LayerNorm(torch.nn.Module):
         self.bias = torch.nn.Parameter(torch.zeros(dim, dtype=dtype, device=device)) if bias else None
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        if not torch.is_grad_enabled():
+        if without_autograd():
             return forward(x, self.weight, self.bias, self.eps, need_stats=False)[0]
         return _LayerNormFn.apply(x, self.weight, self.bias, self.eps)
