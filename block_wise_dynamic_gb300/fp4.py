@@ -3,7 +3,8 @@ power-of-two scale for each block of 32 along a row, sm_103a).
 
 A block's scale is 2^e with the smallest e >= -127 for which no magnitude in
 it exceeds 6 * 2^e; codes are rounded to nearest, ties to even.  For serving
-what was trained at more bits: a weight takes 17/32 of a byte an element.
+what was trained at more bits: a weight takes 17/32 of a byte an element.  A
+matrix that is quantized, or read back, has at most 2,097,120 rows.
 
   quantize(x) -> Fp4Matrix          blocks of 1 x 32 along the rows
   dequantize(q)                     the values that the codes stand for

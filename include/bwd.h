@@ -487,7 +487,8 @@ bwd_status bwd_fp8_linear_backward(const void* dy, bwd_dtype dtype,
 int64_t bwd_fp4_pitch(int64_t cols);
 int64_t bwd_fp4_scale_bytes(int64_t rows, int64_t cols);
 
-/* x: device, rows x cols values of `dtype`, `ld` elements between rows. */
+/* x: device, rows x cols values of `dtype`, `ld` elements between rows; at most
+ * 65535 * 32 = 2,097,120 rows here, to read back and for bwd_fp4_linear. */
 bwd_status bwd_fp4_quantize(const void* x, bwd_dtype dtype, int64_t rows,
                             int64_t cols, int64_t ld, uint8_t* codes,
                             uint8_t* scales, void* stream);
