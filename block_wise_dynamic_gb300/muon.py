@@ -50,9 +50,10 @@ def _work_bytes(count, rows, cols, most=0):
 def orthogonalize(g: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
     """``g`` (..., rows, columns; float32, bfloat16 or float16), each matrix
     orthogonalised, in its type.  A matrix of zeros stays one; one with a NaN
-    or an infinity comes out NaN.  bfloat16 matrices with two to sixteen times as
-    many columns as rows, or the other way round, take a faster form that is up to 1e-4 off beside
-    their rounding's 1.7e-3; ``g.float()`` takes the more exact one."""
+    or an infinity comes out NaN.  bfloat16 matrices with two to sixteen times
+    as many columns as rows, or the other way round, take a faster form that is
+    up to 1e-4 off beside their rounding's 1.7e-3; ``g.float()`` takes the more
+    exact one."""
     if not isinstance(g, torch.Tensor):
         raise TypeError("g must be a torch.Tensor")
     if not g.is_cuda:
@@ -82,12 +83,13 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, stream=None) -> torch.Tensor:
 class MuonArgs(_GradList):
     """Host pointer arrays for ``bwd_muon_step``, built once for a fixed list
     of matrices and reused by every step.  Its workspace belongs to it and to
-    the stream that was current when it was made (or is ``work``, that of
-    another list made on the same stream, if it is as large); a step on another
+    the stream of its first step (or is ``work``, that of another list made on
+    the stream that is current now, if it is as large); a step on another
     stream, or in a graph that is captured, takes one of its own.  Matrices
     are worked on together, up to 64 at a time and as far as ``work_bytes`` of
     workspace hold them, 4 GB by default (a matrix of m x n takes 8 m (m + n)
-    to 8 m (2 m + n) bytes, m its shorter side): less memory in more, smaller launches."""
+    to 8 m (2 m + n) bytes, m its shorter side): less memory in more, smaller
+    launches."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor], work=None, work_bytes=None):
         if work_bytes is not None and not 0 < work_bytes < 1 << 63:
@@ -108,13 +110,22 @@ class MuonArgs(_GradList):
         self.p, self.m = _pointers(params), _pointers(momenta)
         self._shapes = [p.shape for p in params]
         self.rows, self.cols = _sides(self._shapes)
-        self.work = None
+        self._held = self._stream = None
         if self.T:
             self._most = int(work_bytes or 0)
             self._size = _work_bytes(self.T, self.rows, self.cols, self._most)
-            self._stream = _stream_handle(self.device, None)
-            fits = work is not None and work.device == self.device and work.is_contiguous() and work.nbytes >= self._size
-            self.work = work if fits else torch.empty(self._size, dtype=torch.uint8, device=self.device)
+            if work is not None and work.device == self.device and work.is_contiguous() and work.nbytes >= self._size:
+                self._held, self._stream = work, _stream_handle(self.device, None)
+
+    @property
+    def work(self):
+        """The list's workspace; the first access makes it, on the stream that is current."""
+        if self._held is None and self.T:
+            self._held, self._stream = self._new_work(), _stream_handle(self.device, None)
+        return self._held
+
+    def _new_work(self):
+        return torch.empty(self._size, dtype=torch.uint8, device=self.device)
 
     def set_grads(self, grads: Sequence[torch.Tensor]) -> None:
         if [g.shape for g in grads] != self._shapes:
@@ -128,9 +139,9 @@ class MuonArgs(_GradList):
         if stream is not None:
             with _on(stream, self.device):
                 return self._workspace(None)
-        if _stream_handle(self.device, None) == self._stream and not torch.cuda.is_current_stream_capturing():
-            return self.work
-        return torch.empty(self._size, dtype=torch.uint8, device=self.device)
+        if torch.cuda.is_current_stream_capturing() or self._held is not None and self._stream != _stream_handle(self.device, None):
+            return self._new_work()
+        return self.work
 
     def step(self, *, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, rms=0.2, steps=5, grad_scale=None, stream=None) -> None:
         """One step in place:
@@ -154,12 +165,13 @@ class Muon(torch.optim.Optimizer):
     dimensions (those after the first are taken together).  Parameters and
     gradients are float32, bfloat16 or float16 CUDA tensors, momentum float32;
     the update is formed to some 18 bits, to some 13 of bfloat16 parameters
-    with two to sixteen times as many columns as rows, or the other way round.  ``clip_scale`` and ``step(grad_scale=factor)`` are as
-    :class:`Adam8bit`'s.  The steps of all groups share a workspace for each
-    device and stream; one that is captured in a graph takes one of its own.
-    It lives as long as the optimizer; ``work_bytes`` limits it, to 4 GB by
-    default (see :class:`MuonArgs`): 48 matrices of 1024 x 4096 take 2.4 GB, or
-    1.2 with 2 GB for a limit, and 4% more time."""
+    with two to sixteen times as many columns as rows, or the other way round.
+    ``clip_scale`` and ``step(grad_scale=factor)`` are as :class:`Adam8bit`'s.
+    The steps of all groups share a workspace for each device and stream; one
+    that is captured in a graph takes one of its own.  It lives as long as the
+    optimizer; ``work_bytes`` limits it, to 4 GB by default (see
+    :class:`MuonArgs`): 48 matrices of 1024 x 4096 take 2.4 GB, or 1.2 with 2 GB
+    for a limit, and 4% more time."""
 
     def __init__(self, params, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, rms=0.2, steps=5, work_bytes=None):
         if not 0.0 <= lr < float("inf"):
@@ -213,7 +225,8 @@ class Muon(torch.optim.Optimizer):
             place = device, _stream_handle(device, None)
             args = MuonArgs(ps, self._matrices(grads, idx), [self.state[params[i]]["momentum_buffer"] for i in idx], self._work.get(place),
                             work_bytes)
-            self._work[place] = args.work
+            if not torch.cuda.is_current_stream_capturing():
+                self._work[place] = args.work
             plan.append((idx, args))
         return {"params": list(params), "has_grad": [g is not None for g in grads], "at": [p.data_ptr() for p in params],
                 "work_bytes": work_bytes, "buckets": plan}

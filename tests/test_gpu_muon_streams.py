@@ -159,3 +159,54 @@ def test_a_limited_workspace(muon):
     opt.param_groups[0]["work_bytes"] = 1
     opt.step()
     assert all(p.isfinite().all() for p in params)
+
+
+def test_a_list_has_one_workspace(muon):
+    """Made by its first step, on that one's stream: a list made elsewhere holds no second one."""
+    ps, gs, ms = lists(4)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    before = torch.cuda.memory_allocated()
+    side = torch.cuda.Stream()
+    args = muon.MuonArgs(ps, gs, ms)
+    assert torch.cuda.memory_allocated() == before
+    for _ in range(3):
+        args.step(stream=side)
+        assert torch.cuda.memory_allocated() - before == (args.work.numel() + 511) // 512 * 512
+    # captured first: the graph's own, and then one for the list
+    other = muon.MuonArgs(*[[t.clone() for t in l] for l in (ps, gs, ms)])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.step()
+    twin = [[t.clone() for t in l] for l in (ps, gs, ms)]
+    graph.replay()
+    other.step()
+    again = muon.MuonArgs(*twin)
+    again.step()
+    again.step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(twin[0], other._keep[0]))
+
+
+def test_an_optimizer_whose_first_step_is_captured(muon):
+    ps, gs, _ = lists(5)
+    a, b = ([torch.nn.Parameter(p.clone()) for p in ps] for _ in range(2))
+    for params in (a, b):
+        for p, g in zip(params, gs):
+            p.grad = g
+    muon.orthogonalize(gs[0])
+    one, two = muon.Muon(a), muon.Muon(b)
+    for p in a:  # state that outlives the graph's memory
+        one.state[p]["momentum_buffer"] = torch.zeros_like(p)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one.step()
+    graph.replay()
+    one.step()
+    graph.replay()
+    for _ in range(3):
+        two.step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
