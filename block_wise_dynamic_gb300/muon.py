@@ -217,6 +217,8 @@ class Muon(torch.optim.Optimizer):
             if not p.is_contiguous():
                 raise ValueError("Muon needs contiguous parameters")
             if "momentum_buffer" not in self.state[p]:
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError("a parameter's first step makes its momentum and cannot be captured: each replay would make it again")
                 self.state[p]["momentum_buffer"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
             buckets.setdefault((p.device, p.dtype, g.dtype), []).append(i)
         plan = []

@@ -210,3 +210,25 @@ def test_an_optimizer_whose_first_step_is_captured(muon):
         two.step()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_a_first_step_that_is_captured_is_refused(muon):
+    """Each replay would start from no momentum."""
+    ps, gs, _ = lists(6)
+    params = [torch.nn.Parameter(p) for p in ps]
+    params[0].grad = gs[0]
+    opt = muon.Muon(params)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="first step"):
+        with torch.cuda.graph(graph):
+            opt.step()
+    before = [p.detach().clone() for p in params]
+    opt.step()
+    params[1].grad = gs[1]  # another parameter's first one
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="first step"):
+        with torch.cuda.graph(graph):
+            opt.step()
+    opt.step()
+    torch.cuda.synchronize()
+    assert all(p.isfinite().all() and not torch.equal(p, b) for p, b in zip(params, before))
