@@ -164,7 +164,7 @@ class Muon(torch.optim.Optimizer):
     """Momentum and orthogonalised updates for parameters of two or more
     dimensions (those after the first are taken together).  Parameters and
     gradients are float32, bfloat16 or float16 CUDA tensors, momentum float32;
-    the update is formed to some 18 bits, to some 13 of bfloat16 parameters
+    the update is formed to some 17 to 20 bits, to 13 of bfloat16 parameters
     with two to sixteen times as many columns as rows, or the other way round.
     ``clip_scale`` and ``step(grad_scale=factor)`` are as :class:`Adam8bit`'s.
     The steps of all groups share a workspace for each device and stream; one

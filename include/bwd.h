@@ -571,8 +571,8 @@ bwd_status bwd_norm_backward(const void* dy, const void* x, bwd_dtype dtype,
  *          are not small as many as 4 GB hold.
  * Products are of pairs of fp16 values (22 bits), added in fp32 by the matrix
  * instruction, which truncates; sums leave it every 128 products and are then
- * added up to nearest.  A result is off by 1e-6 to 5e-6 of its norm before it
- * is rounded, a bf16 one with 2 <= n / m <= 16 by up to 1e-4.  A matrix with a
+ * added up to nearest.  A result is off by 1e-6 to 8e-6 of its norm before it
+ * is rounded, as in fp32, a bf16 one with 2 <= n / m <= 16 by up to 1e-4.  A matrix with a
  * NaN or an infinity comes out NaN, the others are not touched by it. */
 int64_t bwd_orthogonalize_work_bytes(int32_t count, const int64_t* rows,
                                      const int64_t* cols);

@@ -93,3 +93,15 @@ def test_more_than_sixteen_columns_to_a_row_round_once(muon):
     for shape in ((130, 30000), (17000, 1024)):
         g = torch.from_numpy(np.random.default_rng(4).standard_normal(shape)).to(DEV, torch.bfloat16)
         assert torch.equal(muon.orthogonalize(g), muon.orthogonalize(g.float()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("shape", [(1024, 4096), (1408, 5632), (16384, 1408), (1000, 1000), (301, 777)])
+def test_documented_error(muon, shape):
+    """8e-6 of a result's norm at most, alone (small tiles for all or some of the products) and four together (large ones for most)."""
+    rng = np.random.default_rng(5)
+    r = min(shape) // 64
+    gs = rng.standard_normal((4, *shape)) + 2 * rng.standard_normal((4, shape[0], r)) @ rng.standard_normal((4, r, shape[1]))
+    gs = torch.from_numpy(1e-3 * gs).to(DEV, torch.float32)
+    want = ref.orthogonalize(np64(gs[0]))
+    for got in (muon.orthogonalize(gs[0]), muon.orthogonalize(gs)[0]):
+        assert np.linalg.norm(np64(got) - want) <= 8e-6 * np.linalg.norm(want)
